@@ -270,6 +270,145 @@ size_t dilution_attn_decode_noalloc_scratch_bytes(void);
 int dilution_attn_decode_noalloc_get_error(void *stream);
 
 /* ------------------------------------------------------------------------
+ * Rotary positions of queries and keys, with one to four position axes.
+ *
+ * A token at position n_a on axis a turns pair j of a head's elements by the
+ * angle theta_j = n_{axis(j)} * inv_freq_j (radians):
+ *     (x, y) -> (x cos theta_j - y sin theta_j,  y cos theta_j + x sin theta_j).
+ * Pair j is the elements (j, n_pairs + j), or (2j, 2j + 1) if `adjacent` is
+ * set; elements from 2 n_pairs on pass unchanged.  Text has one axis; images
+ * and video give each pair the axis (time, height, width) that pair_axis
+ * names.  The angle is taken modulo one turn in 64-bit fixed point, so far
+ * positions lose nothing; the products run in fp32 and are rounded once.
+ * ---------------------------------------------------------------------- */
+#define DA_MAX_ROPE_PAIRS 64
+#define DA_MAX_ROPE_AXES  4
+
+typedef struct dilution_attn_rope_spec {
+  const float *inv_freq;                 /* DEVICE [n_pairs] fp32, |inv_freq| < 2^24 (others give NaN) */
+  int32_t n_pairs;                       /* 0 .. d/2 (0: every element passes unchanged) */
+  int32_t n_axes;                        /* 1 .. DA_MAX_ROPE_AXES */
+  int32_t adjacent;                      /* 0: pairs (j, n_pairs + j), 1: pairs (2j, 2j + 1) */
+  uint8_t pair_axis[DA_MAX_ROPE_PAIRS];  /* axis of each pair, < n_axes */
+} dilution_attn_rope_spec;
+
+/* q_out, k_out [B,H,T,d] = q, k turned by +theta (k and k_out may both be NULL
+ * with Hk = 0).  The four *_strides are HOST arrays of three element strides
+ * (b, h, t), or NULL for contiguous [B,H,T,d]; d is always contiguous, so the
+ * inputs may be views of a fused projection [B,T,(Hq + 2 Hk) d].  Input
+ * strides may be 0 (a head or batch entry read several times).  Outputs must
+ * not address an element twice (their strides, sorted, must each step over
+ * the extent below; else DA_ERR_INVALID).  An output may be its own input
+ * (same pointer and strides); other overlaps are not allowed.
+ * positions: DEVICE int32 [n_axes][pos_batch][T], pos_batch 1 (every batch
+ * entry alike) or B; negative positions are valid.
+ * spec is a HOST struct, read during the call.  No workspace.  Errors as for
+ * dilution_attn_fwd, without a workspace; any 2-byte (bf16) or 4-byte (fp32)
+ * aligned pointer is accepted, rows whose pointers and strides are all
+ * multiples of 16 bytes take the fast path. */
+int dilution_attn_rope(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                       void *q_out, const int64_t *q_out_strides, void *k_out, const int64_t *k_out_strides,
+                       const int32_t *positions, int pos_batch, const dilution_attn_rope_spec *spec,
+                       int B, int Hq, int Hk, int T, int d, int dtype, void *stream);
+
+/* Backward of dilution_attn_rope: dq, dk = the upstream gradients dq_out,
+ * dk_out turned by -theta (positions and frequencies take no gradient).  Same
+ * arguments and errors; the gradients' strides let them be written straight
+ * into a fused projection's gradient. */
+int dilution_attn_rope_bwd(const void *dq_out, const int64_t *dq_out_strides, const void *dk_out,
+                           const int64_t *dk_out_strides, void *dq, const int64_t *dq_strides, void *dk,
+                           const int64_t *dk_strides, const int32_t *positions, int pos_batch,
+                           const dilution_attn_rope_spec *spec, int B, int Hq, int Hk, int T, int d, int dtype,
+                           void *stream);
+
+/* ------------------------------------------------------------------------
+ * Paged cache of S sequences of different lengths.
+ *
+ * Keys and values live in pages of page_size tokens, the demand totals (one
+ * per key and QUERY head) in pages of their own:
+ *   k_pages, v_pages [num_pages, Hkv, page_size, d],
+ *   demand_pages     [num_demand_pages, Hq, page_size] fp32.
+ * Token t of sequence s has its key and value in row t % page_size of page
+ * page_table[s][t / page_size], its demand in that row of page
+ * demand_table[s][t / page_size].  Sequences that share a prefix may name the
+ * same key/value pages; the demand differs between them, so a demand page
+ * belongs to one sequence (two sequences naming one demand page, or appending
+ * to one key/value page, race with each other).  Query head h reads key head
+ * h / (Hq / Hkv).  Rows past a sequence's length are never used, whatever
+ * they hold, nor are table entries past its last page.
+ *
+ * The tables and seq_lens are device data that the kernels check: a length
+ * that is negative or longer than the table (or max_len), or a page id outside
+ * the pool, records DA_ERR_INVALID in the workspace's status word; nothing
+ * outside the pools is read or written, an append skips that token, and a
+ * decode step's results for that sequence are unspecified.  page_size is 16, 32,
+ * 64, 128 or 256; Hq is a multiple of Hkv; d 64 or 128; pools and out 16-byte
+ * aligned.
+ *
+ * Unlike the calls above, the paged calls leave the status word alone unless
+ * they record an error: the caller zeroes the first 256 bytes of a workspace
+ * once before its first use, and dilution_attn_get_error reads and clears
+ * the first error recorded since.
+ * ---------------------------------------------------------------------- */
+typedef struct dilution_attn_paged_cache {
+  void *k_pages, *v_pages;               /* DEVICE, dtype */
+  float *demand_pages;                   /* DEVICE */
+  const int32_t *page_table;             /* DEVICE [S][max_pages] */
+  const int32_t *demand_table;           /* DEVICE [S][max_pages] */
+  const int32_t *seq_lens;               /* DEVICE [S] */
+  int32_t S, Hq, Hkv, d, page_size, num_pages, num_demand_pages, max_pages, dtype;
+} dilution_attn_paged_cache;
+
+/* Appends new tokens: sequence s receives tokens cu_tokens[s] ..
+ * cu_tokens[s+1] - 1 of the N given, as its LAST tokens; cache->seq_lens
+ * already counts them.  For each token
+ *   - its key, turned by its position, goes to its row of k_pages, its value
+ *     unchanged to v_pages;
+ *   - its demand becomes demand[n][h] (a prompt's demand_out after prefill),
+ *     or 0 where demand is NULL (a token about to be decoded);
+ *   - q (nullable), turned likewise, goes to q_out [N,Hq,d] contiguous.
+ * q [N,Hq,d], k, v [N,Hkv,d]: *_strides are HOST arrays of two element strides
+ * (token, head) or NULL for contiguous; demand fp32 [N,Hq] likewise.
+ * cu_tokens: DEVICE [S+1] int32, starting at 0 and not decreasing; tokens from
+ * cu_tokens[S] on are padding, neither read nor written.
+ * spec: NULL appends k and q unrotated.  positions: DEVICE [n_axes][N], or NULL
+ * for the token's place in its sequence on every axis.
+ * workspace: 256 bytes (dilution_attn_paged_append_workspace_size()). */
+size_t dilution_attn_paged_append_workspace_size(void);
+
+int dilution_attn_paged_append(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                               const void *v, const int64_t *v_strides, const float *demand,
+                               const int64_t *demand_strides, void *q_out, const int32_t *cu_tokens, int N,
+                               const dilution_attn_paged_cache *cache, const dilution_attn_rope_spec *spec,
+                               const int32_t *positions, void *workspace, size_t workspace_bytes, void *stream);
+
+/* One decode step of every sequence over the paged cache (the operator of
+ * dilution_attn_decode_step; the new token has been appended, with demand 0):
+ * q, out [S,Hq,d]; sequence s sees its seq_lens[s] keys, out is formed as in
+ * steps 2-4 there and the demand of every key it sees grows by its bid.  A
+ * sequence of length 0 (an idle slot) gets zeros and changes nothing.
+ *
+ * prefix_table (nullable): DEVICE [n_prefix_pages] page ids.  The first
+ * n_prefix_pages * page_size tokens of EVERY sequence then live in those
+ * pages, whose keys and values are read once for the whole batch (the first
+ * n_prefix_pages entries of each page_table row are not read); each sequence
+ * keeps its own demand over them.  A length below the prefix's, other than 0,
+ * records DA_ERR_INVALID.  The result is that of the same call with the
+ * prefix's pages in every page_table row.
+ *
+ * max_len: host upper bound of seq_lens (at most max_pages * page_size); sizes
+ * the workspace and the launch.  tau_bh: nullable device [S*Hq], index
+ * s*Hq + h.  tau, eps, flags (DA_FLAG_EARLIER_DEMAND_ONLY) as for
+ * dilution_attn_decode_step_ex; DA_BF16 needs eps >= 1e-18 as the forward.
+ * Repeated calls give equal bits.  Errors as for dilution_attn_decode_step_ex. */
+size_t dilution_attn_paged_decode_workspace_size(int S, int Hq, int Hkv, int d, int max_len, int n_prefix_pages,
+                                                 int page_size, int dtype);
+
+int dilution_attn_paged_decode(const void *q, const dilution_attn_paged_cache *cache, const int32_t *prefix_table,
+                               int n_prefix_pages, int max_len, void *out, float tau, const float *tau_bh,
+                               float eps, int flags, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
  * Synchronises `stream`, reads the status word that kernels of the last call
  * on `workspace` may have set, clears it and returns it (DA_OK if none).
  * Returns DA_ERR_CUDA if the synchronisation or the copy fails.

@@ -60,6 +60,13 @@ _SIGNATURES = {
     "dilution_attn_debug_decode_stall": (_c_int, [_c_void_p] * 6 + [_c_int, _c_int, _c_void_p] + [_c_int] * 3 +
                                          [_c_float, _c_float, _c_int, _c_void_p, _c_size_t, _c_void_p, _c_int, _c_int,
                                           ctypes.c_longlong]),
+    "dilution_attn_rope": (_c_int, [_c_void_p] * 9 + [_c_int, _c_void_p] + [_c_int] * 6 + [_c_void_p]),
+    "dilution_attn_rope_bwd": (_c_int, [_c_void_p] * 9 + [_c_int, _c_void_p] + [_c_int] * 6 + [_c_void_p]),
+    "dilution_attn_paged_append_workspace_size": (_c_size_t, []),
+    "dilution_attn_paged_append": (_c_int, [_c_void_p] * 10 + [_c_int] + [_c_void_p] * 4 + [_c_size_t, _c_void_p]),
+    "dilution_attn_paged_decode_workspace_size": (_c_size_t, [_c_int] * 8),
+    "dilution_attn_paged_decode": (_c_int, [_c_void_p] * 3 + [_c_int, _c_int, _c_void_p, _c_float, _c_void_p, _c_float,
+                                                             _c_int, _c_void_p, _c_size_t, _c_void_p]),
     "dilution_attn_get_error": (_c_int, [_c_void_p, _c_void_p]),
     "dilution_attn_debug_last_timeout": (_c_int, [_c_void_p, _c_void_p]),
     "dilution_attn_debug_tile_schedule": (_c_int, [_c_int, _c_int, _c_int, _c_void_p, _c_size_t]),
@@ -404,6 +411,269 @@ def dilution_attn_debug_decode_stall(q_new, k_new, v_new, k_cache, v_cache, dema
                                               _stream_handle(stream), int(stall_chunk), int(stall_bh),
                                               int(wait_limit_ns))
     return int(st), out
+
+
+# --------------------------------------------------------------------- rotary positions
+DA_MAX_ROPE_PAIRS, DA_MAX_ROPE_AXES = 64, 4
+
+
+class _CRopeSpec(ctypes.Structure):
+    _fields_ = [("inv_freq", _c_void_p), ("n_pairs", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("adjacent", ctypes.c_int32), ("pair_axis", ctypes.c_uint8 * DA_MAX_ROPE_PAIRS)]
+
+
+class RopeSpec:
+    """What ``rope_spec`` returns: the C struct, the frequencies it points to and its sizes."""
+
+    __slots__ = ("inv_freq", "n_pairs", "n_axes", "adjacent", "_c", "_ref")
+
+    def __init__(self, inv_freq, pair_axis, n_axes, adjacent):
+        self.inv_freq, self.n_pairs, self.n_axes, self.adjacent = inv_freq, len(pair_axis), n_axes, adjacent
+        self._c = _CRopeSpec(inv_freq.data_ptr(), self.n_pairs, n_axes, int(adjacent),
+                             (ctypes.c_uint8 * DA_MAX_ROPE_PAIRS)(*pair_axis))
+        self._ref = ctypes.byref(self._c)
+
+
+def rope_spec(inv_freq, pair_axis=None, n_axes: int = 1, adjacent: bool = False) -> RopeSpec:
+    """Rotation of ``inv_freq.numel()`` pairs of a head's elements (fp32 CUDA
+    frequencies, radians per position).  ``pair_axis``: the position axis of
+    each pair (axis 0 when omitted).  Pairs are (j, n_pairs + j), or
+    (2j, 2j + 1) with ``adjacent``.  The tensor is read by every call that
+    gets the spec: new frequencies written into it take effect."""
+    _need(inv_freq, "inv_freq", None, torch.float32)
+    n = inv_freq.numel()
+    if inv_freq.dim() != 1 or n > DA_MAX_ROPE_PAIRS:
+        raise ValueError(f"inv_freq must be one-dimensional with at most {DA_MAX_ROPE_PAIRS} entries")
+    if not 1 <= n_axes <= DA_MAX_ROPE_AXES:
+        raise ValueError(f"n_axes must be 1 .. {DA_MAX_ROPE_AXES}, got {n_axes}")
+    pair_axis = [0] * n if pair_axis is None else [int(a) for a in pair_axis]
+    if len(pair_axis) != n or any(not 0 <= a < n_axes for a in pair_axis):
+        raise ValueError(f"pair_axis must hold {n} axes in 0 .. {n_axes - 1}")
+    return RopeSpec(inv_freq, pair_axis, int(n_axes), bool(adjacent))
+
+
+def _need_rows(t, name, shape, dtype):
+    """A CUDA tensor whose last dimension is contiguous; other strides are free."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device} but the current device is cuda:{torch.cuda.current_device()}; "
+                         f"call inside torch.cuda.device({t.device})")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def _strides(t, n):
+    """The first n strides as a C array."""
+    return None if t is None else (ctypes.c_int64 * n)(*t.stride()[:n])
+
+
+def _rope_call(name, q, k, positions, rope, q_out, k_out, stream, check):
+    lib = load()
+    if not isinstance(rope, RopeSpec):
+        raise TypeError("rope must be a RopeSpec (see rope_spec)")
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a [B, H, T, d] tensor")
+    B, Hq, T, d = q.shape
+    _need_rows(q, "q", q.shape, q.dtype)
+    dt, Hk = _dtype_code(q), 0
+    if k is not None:
+        Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
+        _need_rows(k, "k", (B, Hk, T, d), q.dtype)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _need(positions, "positions", None, torch.int32)
+    if positions.dim() == 2:
+        positions = positions.unsqueeze(1)
+    if positions.dim() != 3 or positions.shape[0] != rope.n_axes or positions.shape[1] not in (1, B) or \
+            positions.shape[2] != T:
+        raise ValueError(f"positions has shape {tuple(positions.shape)}, expected ({rope.n_axes}, [1 or {B},] {T})")
+    _need(rope.inv_freq, "inv_freq")
+    q_out = torch.empty((B, Hq, T, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
+    _need_rows(q_out, "q_out", q.shape, q.dtype)
+    if k is not None:
+        k_out = torch.empty((B, Hk, T, d), dtype=q.dtype, device=q.device) if k_out is None else k_out
+        _need_rows(k_out, "k_out", k.shape, q.dtype)
+    st = getattr(lib, name)(_ptr(q), _strides(q, 3), _ptr(k), _strides(k, 3), _ptr(q_out), _strides(q_out, 3),
+                            _ptr(k_out), _strides(k_out, 3), _ptr(positions), positions.shape[1], rope._ref, B, Hq, Hk,
+                            T, d, dt, _stream_handle(stream))
+    if check:
+        _check(st, name)
+    return q_out, k_out
+
+
+def dilution_attn_rope(q, k, positions, rope, q_out=None, k_out=None, *, stream=None, check: bool = True):
+    """Queries and keys turned by their positions: q [B, Hq, T, d], k [B, Hk, T, d]
+    (views of a fused projection are fine; k may be None) -> (q_out, k_out),
+    contiguous [B, H, T, d] when not given.  positions: int32 [n_axes, T] or
+    [n_axes, B, T]; ``rope``: see rope_spec."""
+    return _rope_call("dilution_attn_rope", q, k, positions, rope, q_out, k_out, stream, check)
+
+
+def dilution_attn_rope_bwd(dq_out, dk_out, positions, rope, dq=None, dk=None, *, stream=None, check: bool = True):
+    """Gradients (dq, dk) of dilution_attn_rope's inputs from those of its
+    outputs; dq and dk may be views of a fused projection's gradient."""
+    return _rope_call("dilution_attn_rope_bwd", dq_out, dk_out, positions, rope, dq, dk, stream, check)
+
+
+# ---------------------------------------------------------------------------- paged cache
+class _CPagedCache(ctypes.Structure):
+    _fields_ = [(n, _c_void_p) for n in ("k_pages", "v_pages", "demand_pages", "page_table", "demand_table", "seq_lens")] \
+        + [(n, ctypes.c_int32) for n in ("S", "Hq", "Hkv", "d", "page_size", "num_pages", "num_demand_pages",
+                                         "max_pages", "dtype")]
+
+
+class PagedCache:
+    """The tensors of a paged cache (see the header): k_pages, v_pages
+    [num_pages, Hkv, page_size, d], demand_pages [num_demand_pages, Hq,
+    page_size] fp32, page_table and demand_table [S, max_pages] int32, seq_lens
+    [S] int32.  Checked once here; the tables and lengths are the caller's to
+    update in place between calls."""
+
+    __slots__ = ("k_pages", "v_pages", "demand_pages", "page_table", "demand_table", "seq_lens", "S", "Hq", "Hkv", "d",
+                 "page_size", "max_pages", "dtype", "device", "_code", "_c", "_ref")
+
+    def __init__(self, k_pages, v_pages, demand_pages, page_table, demand_table, seq_lens):
+        _need(k_pages, "k_pages")
+        if k_pages.dim() != 4:
+            raise ValueError("k_pages must be [num_pages, Hkv, page_size, d]")
+        num_pages, Hkv, page_size, d = k_pages.shape
+        _need(v_pages, "v_pages", k_pages.shape, k_pages.dtype)
+        _need(demand_pages, "demand_pages", None, torch.float32)
+        if demand_pages.dim() != 3 or demand_pages.shape[2] != page_size:
+            raise ValueError(f"demand_pages must be [num_demand_pages, Hq, {page_size}]")
+        num_demand_pages, Hq, _ = demand_pages.shape
+        if Hkv < 1 or Hq < 1 or Hq % Hkv != 0:
+            raise ValueError(f"{Hq} query heads over {Hkv} key heads: not a multiple")
+        _need(page_table, "page_table", None, torch.int32)
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [S, max_pages]")
+        S, max_pages = page_table.shape
+        _need(demand_table, "demand_table", page_table.shape, torch.int32)
+        _need(seq_lens, "seq_lens", (S,), torch.int32)
+        self._code = _dtype_code(k_pages)
+        self.k_pages, self.v_pages, self.demand_pages = k_pages, v_pages, demand_pages
+        self.page_table, self.demand_table, self.seq_lens = page_table, demand_table, seq_lens
+        self.S, self.Hq, self.Hkv, self.d, self.page_size, self.max_pages = S, Hq, Hkv, d, page_size, max_pages
+        self.dtype, self.device = k_pages.dtype, k_pages.device
+        self._c = _CPagedCache(*(t.data_ptr() for t in (k_pages, v_pages, demand_pages, page_table, demand_table,
+                                                        seq_lens)), S, Hq, Hkv, d, page_size, num_pages,
+                               num_demand_pages, max_pages, self._code)
+        self._ref = ctypes.byref(self._c)
+
+
+def _need_cache(cache):
+    if not isinstance(cache, PagedCache):
+        raise TypeError("cache must be a PagedCache")
+    if cache.device.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {cache.device} but the current device is "
+                         f"cuda:{torch.cuda.current_device()}; call inside torch.cuda.device({cache.device})")
+
+
+def dilution_attn_paged_append_workspace_size() -> int:
+    return int(load().dilution_attn_paged_append_workspace_size())
+
+
+def dilution_attn_paged_append_workspace(cache):
+    """A workspace for dilution_attn_paged_append, its status block zeroed."""
+    return torch.zeros(dilution_attn_paged_append_workspace_size(), dtype=torch.uint8, device=cache.device)
+
+
+def dilution_attn_paged_append(q, k, v, cache, cu_tokens, q_out=None, *, rope=None, positions=None, demand=None,
+                               workspace=None, stream=None, check: bool = True):
+    """Append k, v [N, Hkv, d] (rows may be strided) as the last tokens of the
+    cache's sequences: sequence s takes tokens cu_tokens[s] .. cu_tokens[s+1]-1
+    (int32 [S+1]; seq_lens already counts them).  With ``rope`` the keys turn
+    on the way, by ``positions`` (int32 [n_axes, N]) or by their place in the
+    sequence.  ``demand`` [N, Hq] fp32: the keys' totals (a prompt's
+    demand_out after prefill), 0 when omitted.  q [N, Hq, d] (or None) turns
+    likewise into ``q_out`` (contiguous), which is returned."""
+    lib = load()
+    _need_cache(cache)
+    Hq, Hkv, d = cache.Hq, cache.Hkv, cache.d
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be [N, Hkv, d]")
+    N = k.shape[0]
+    _need_rows(k, "k", (N, Hkv, d), cache.dtype)
+    _need_rows(v, "v", (N, Hkv, d), cache.dtype)
+    _need(cu_tokens, "cu_tokens", (cache.S + 1,), torch.int32)
+    if q is not None:
+        _need_rows(q, "q", (N, Hq, d), cache.dtype)
+        q_out = torch.empty((N, Hq, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
+        _need(q_out, "q_out", (N, Hq, d), q.dtype)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if rope is not None and not isinstance(rope, RopeSpec):
+        raise TypeError("rope must be a RopeSpec (see rope_spec)")
+    if rope is not None:
+        _need(rope.inv_freq, "inv_freq")
+    if positions is not None:
+        _need(positions, "positions", (1 if rope is None else rope.n_axes, N), torch.int32)
+    if demand is not None:
+        _need_rows(demand.unsqueeze(-1), "demand", (N, Hq, 1), torch.float32)
+    if workspace is None:
+        workspace = dilution_attn_paged_append_workspace(cache)
+    _need(workspace, "workspace", None, torch.uint8)
+    st = lib.dilution_attn_paged_append(_ptr(q), _strides(q, 2), _ptr(k), _strides(k, 2), _ptr(v), _strides(v, 2),
+                                        _ptr(demand), _strides(demand, 2), _ptr(q_out), _ptr(cu_tokens), N, cache._ref,
+                                        None if rope is None else rope._ref, _ptr(positions), _ptr(workspace),
+                                        workspace.numel(), _stream_handle(stream))
+    if check:
+        _check(st, "dilution_attn_paged_append")
+    return q_out
+
+
+def dilution_attn_paged_decode_workspace_size(S: int, Hq: int, Hkv: int, d: int, max_len: int, n_prefix_pages: int,
+                                              page_size: int, dtype: int) -> int:
+    return int(load().dilution_attn_paged_decode_workspace_size(S, Hq, Hkv, d, max_len, n_prefix_pages, page_size,
+                                                                dtype))
+
+
+def dilution_attn_paged_decode_workspace(cache, max_len: int, n_prefix_pages=None):
+    """A workspace for dilution_attn_paged_decode over ``cache`` up to
+    ``max_len`` tokens, its status block zeroed.  n_prefix_pages: the prefix
+    it will serve (omitted: large enough for any)."""
+    args = (cache.S, cache.Hq, cache.Hkv, cache.d, int(max_len))
+    need = max(dilution_attn_paged_decode_workspace_size(*args, n, cache.page_size, cache._code)
+               for n in ((0, int(max_len) // cache.page_size) if n_prefix_pages is None else (int(n_prefix_pages),)))
+    ws = torch.empty(max(need + (4096 if n_prefix_pages is None else 0), 256), dtype=torch.uint8, device=cache.device)
+    ws[:256].zero_()
+    return ws
+
+
+def dilution_attn_paged_decode(q, cache, max_len: int, out=None, *, prefix_table=None, tau: float = 1.0, tau_bh=None,
+                               eps: float = 1e-6, flags: int = 0, workspace=None, stream=None, check: bool = True):
+    """One decode step of every sequence of ``cache`` (the new tokens are
+    already appended): q [S, Hq, d] -> ``out`` [S, Hq, d]; each key's demand
+    grows by its bid.  ``max_len``: upper bound of cache.seq_lens.
+    ``prefix_table`` (int32 [n]): pages of the tokens that every sequence
+    shares, read once for the batch.  Bad lengths or page ids are found on the
+    device: read them with dilution_attn_get_error on ``workspace``."""
+    lib = load()
+    _need_cache(cache)
+    _need(q, "q", (cache.S, cache.Hq, cache.d), cache.dtype)
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", q.shape, q.dtype)
+    n_prefix = 0
+    if prefix_table is not None:
+        _need(prefix_table, "prefix_table", None, torch.int32)
+        n_prefix = prefix_table.numel()
+    if workspace is None:
+        workspace = dilution_attn_paged_decode_workspace(cache, max_len, n_prefix)
+    _need(workspace, "workspace", None, torch.uint8)
+    st = lib.dilution_attn_paged_decode(_ptr(q), cache._ref, _ptr(prefix_table), n_prefix, int(max_len), _ptr(out),
+                                        float(tau), _tau_bh_ptr(tau_bh, cache.S, cache.Hq), float(eps), int(flags),
+                                        _ptr(workspace), workspace.numel(), _stream_handle(stream))
+    if check:
+        _check(st, "dilution_attn_paged_decode")
+    return out
 
 
 # ----------------------------------------------------------------------------- misc

@@ -1,0 +1,48 @@
+// Paged decode: the host-side problem description and workspace layouts that
+// the C ABI and the kernels share.
+#pragma once
+
+#include "da_internal.h"
+
+namespace da {
+
+// One paged decode call.
+struct PagedDecode {
+  dilution_attn_paged_cache c;
+  const void *q;
+  void *out;
+  const int32_t *prefix_table;   // null without a prefix
+  int prefix_len;                // tokens of the shared prefix, a multiple of page_size
+  int prefix_pages;
+  int max_len;                   // host bound of seq_lens
+  HeadScale hs;
+  float eps;
+  bool earlier;
+  int *status;
+  uint8_t *ws;
+};
+
+#if defined(__CUDACC__)
+// Length of sequence s, 0 where it is not valid (then recorded once by the
+// caller that passes `status`).
+__device__ __forceinline__ int paged_len(const PagedDecode &p, int s, int *status) {
+  const int len = __ldg(p.c.seq_lens + s);
+  if (len == 0) return 0;
+  if (len < 0 || len > p.max_len || len < p.prefix_len) {
+    if (status != nullptr) atomicCAS(status, DA_OK, DA_ERR_INVALID);
+    return 0;
+  }
+  return len;
+}
+// Page id from a table, -1 (recorded) where it is outside the pool.
+__device__ __forceinline__ int checked_page(const int32_t *entry, int num_pages, int *status) {
+  const int pg = __ldg(entry);
+  if (pg < 0 || pg >= num_pages) {
+    atomicCAS(status, DA_OK, DA_ERR_INVALID);
+    return -1;
+  }
+  return pg;
+}
+#endif
+
+}  // namespace da

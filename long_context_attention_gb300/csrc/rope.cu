@@ -1,0 +1,418 @@
+// Rotary positions: the rotation of queries and keys on their way into
+// attention (and of their gradients on the way back), and the append to a
+// paged cache, which rotates on the way.
+//
+// Mathematics.  Pair j of a head at position n (of the pair's axis) turns by
+// theta = n * inv_freq_j radians.  Only theta modulo one turn matters, so the
+// frequency is held in turns per position as a 64-bit fixed-point fraction
+//     F = inv_freq_j / (2 pi) * 2^64  mod 2^64
+// and n * F mod 2^64 is the angle, exact in its products: the 24-bit mantissa
+// of inv_freq_j times the first 64 bits of 1 / (2 pi), shifted by the exponent,
+// leaves F within one unit and the angle within n 2^-64 turns (n = 2^31: 7e-10
+// radians, below fp32's rounding of the cosine).  No fp64 (GB300 has few fp64
+// units) and no long fp32 products.  The products x cos - y sin run in fp32
+// and round once to the output's type.
+//
+// What bounds it: bytes.  Each element is read once and written once; sin and
+// cos are computed in registers for one token and 16 bytes of a head's row and
+// serve `hpt` heads in turn, so they are a small part of the instructions.
+#include "da_rope.h"
+#include "da_ptx.cuh"
+
+#include <cuda_bf16.h>
+
+namespace da {
+
+// inv_freq in turns per position, times 2^64 modulo 2^64.  Frequencies of
+// magnitude 2^24 and above, infinities and NaN give ok = false.
+__device__ __forceinline__ unsigned long long turns_fixed(float f, bool &ok) {
+  constexpr unsigned long long kInvTwoPi = 0x28BE60DB9391054Aull;   // floor(2^64 / (2 pi))
+  const uint32_t u = __float_as_uint(f);
+  int e = (int)((u >> 23) & 0xffu);
+  unsigned long long m = u & 0x7fffffu;
+  if (e == 0)
+    e = 1;
+  else
+    m |= 0x800000u;
+  const int shift = 150 - e;   // |f| = m 2^-shift
+  ok = shift > 0;
+  unsigned long long r = 0;
+  if (ok && shift < 128) {
+    const unsigned long long lo = m * kInvTwoPi, hi = __umul64hi(m, kInvTwoPi);
+    r = shift < 64 ? (lo >> shift) | (hi << (64 - shift)) : hi >> (shift - 64);
+  }
+  return (u >> 31) ? 0ull - r : r;
+}
+
+// cos and sin of position * inv_freq.
+__device__ __forceinline__ void rope_sincos(float inv_freq, int pos, float sign, float &c, float &s) {
+  bool ok;
+  const unsigned long long F = turns_fixed(inv_freq, ok);
+  const long long a = (long long)((unsigned long long)(long long)pos * F);   // the angle as a signed 0.64 turn
+  sincospif((float)a * 0x1p-63f, &s, &c);
+  s *= sign;
+  if (!ok) c = s = __int_as_float(0x7fc00000);
+}
+
+template <typename E>
+struct RopeVec;   // 16 bytes of a row
+template <>
+struct RopeVec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+  }
+};
+template <>
+struct RopeVec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[4]) {
+    f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y), f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f32(float x, float &y) { y = x; }
+__device__ __forceinline__ void from_f32(float x, __nv_bfloat16 &y) { y = __float2bfloat16_rn(x); }
+
+// The two 16-byte vectors of a row that unit u of a token handles, and the
+// angles of the N pairs they hold.  Units cover a row of d elements in d / 2N
+// steps.  Half-split pairs: a rotated unit holds elements [N u, N u + N) and
+// their partners n_pairs further on.  Adjacent pairs: vectors 2u and 2u + 1.
+template <typename E, bool ADJ>
+struct RopeUnit {
+  static constexpr int N = RopeVec<E>::N;
+  int va, vb;                 // element offsets of the two vectors
+  bool rot_a, rot_b;          // whether they rotate (half-split: both or none)
+  float c[N], s[N];           // half-split: N pairs; adjacent: N / 2 of each vector
+
+  // `angle(j, c, s)` gives the cosine and sine of pair j.
+  template <typename F>
+  __device__ __forceinline__ void init(int u, int n_pairs, F &&angle) {
+    if constexpr (ADJ) {
+      va = 2 * u * N;
+      vb = va + N;
+      rot_a = va < 2 * n_pairs;
+      rot_b = vb < 2 * n_pairs;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        c[i] = 1.f, s[i] = 0.f;
+        if (i < N / 2 ? rot_a : rot_b) angle(va / 2 + i, c[i], s[i]);
+      }
+    } else {
+      const int rot_units = n_pairs / N;
+      rot_a = rot_b = u < rot_units;
+      va = rot_a ? u * N : 2 * n_pairs + 2 * (u - rot_units) * N;
+      vb = rot_a ? va + n_pairs : va + N;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        c[i] = 1.f, s[i] = 0.f;
+        if (rot_a) angle(va + i, c[i], s[i]);
+      }
+    }
+  }
+  __device__ __forceinline__ void apply(uint4 &a, uint4 &b) const {
+    using V = RopeVec<E>;
+    if (!rot_a) return;       // passes bit for bit (rot_b implies rot_a)
+    float x[N], y[N];
+    V::unpack(a, x);
+    V::unpack(b, y);
+    if constexpr (ADJ) {
+      float ra[N], rb[N];
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        ra[2 * i] = fmaf(x[2 * i], c[i], -x[2 * i + 1] * s[i]);
+        ra[2 * i + 1] = fmaf(x[2 * i + 1], c[i], x[2 * i] * s[i]);
+        rb[2 * i] = fmaf(y[2 * i], c[N / 2 + i], -y[2 * i + 1] * s[N / 2 + i]);
+        rb[2 * i + 1] = fmaf(y[2 * i + 1], c[N / 2 + i], y[2 * i] * s[N / 2 + i]);
+      }
+      a = V::pack(ra);
+      if (rot_b) b = V::pack(rb);
+    } else {
+      float ra[N], rb[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        ra[i] = fmaf(x[i], c[i], -y[i] * s[i]);
+        rb[i] = fmaf(y[i], c[i], x[i] * s[i]);
+      }
+      a = V::pack(ra);
+      b = V::pack(rb);
+    }
+  }
+};
+
+__device__ __forceinline__ int rope_position(const RopeParams &rp, int axis, long long b, long long t, int fallback) {
+  return rp.positions == nullptr ? fallback : __ldg(rp.positions + axis * rp.pos_stride_axis + b * rp.pos_stride_b + t);
+}
+
+constexpr int kRopeThreads = 128;
+
+// grid.x: (token, unit) pairs, grid.y: groups of hpt heads of q followed by k.
+template <typename E, bool ADJ>
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_kernel(RopeTensor q, RopeTensor k, RopeParams rp, int Hq, int Hk, int T, long long n_units, int units, int hpt) {
+  const long long i = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
+  if (i >= n_units) return;
+  const long long tok = i / units;
+  const int u = (int)(i - tok * units);
+  const long long b = tok / T, t = tok - b * T;
+  RopeUnit<E, ADJ> ru;
+  ru.init(u, rp.n_pairs, [&](int j, float &c, float &s) {
+    rope_sincos(__ldg(rp.inv_freq + j), rope_position(rp, rp.pair_axis[j], b, t, 0), rp.sign, c, s);
+  });
+  const int h0 = blockIdx.y * hpt, h1 = min(h0 + hpt, Hq + Hk);
+#pragma unroll 4
+  for (int h = h0; h < h1; ++h) {
+    const bool isq = h < Hq;
+    const RopeTensor &x = isq ? q : k;
+    const int hh = isq ? h : h - Hq;
+    const E *src = static_cast<const E *>(x.in) + b * x.in_b + hh * x.in_h + t * x.in_t;
+    E *dst = static_cast<E *>(x.out) + b * x.out_b + hh * x.out_h + t * x.out_t;
+    uint4 va = *reinterpret_cast<const uint4 *>(src + ru.va), vb = *reinterpret_cast<const uint4 *>(src + ru.vb);
+    ru.apply(va, vb);
+    *reinterpret_cast<uint4 *>(dst + ru.va) = va;
+    *reinterpret_cast<uint4 *>(dst + ru.vb) = vb;
+  }
+}
+
+// Two elements of a row, of any alignment: pair j < n_pairs, or two elements
+// past the rotated part.
+template <typename E, typename F>
+__device__ __forceinline__ void rope_pair(const E *src, E *dst, int j, int n_pairs, bool adjacent, F &&angle) {
+  const bool rot = j < n_pairs;
+  const int a = rot ? (adjacent ? 2 * j : j) : 2 * j;
+  const int b = rot && !adjacent ? j + n_pairs : a + 1;
+  const E ea = src[a], eb = src[b];
+  if (!rot) {
+    dst[a] = ea;
+    dst[b] = eb;
+    return;
+  }
+  float c, s;
+  angle(j, c, s);
+  const float x = to_f32(ea), y = to_f32(eb);
+  from_f32(fmaf(x, c, -y * s), dst[a]);
+  from_f32(fmaf(y, c, x * s), dst[b]);
+}
+
+// Any alignment: one thread per pair of elements (d / 2 of them a row).
+template <typename E>
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_scalar_kernel(RopeTensor q, RopeTensor k, RopeParams rp, int adjacent, int Hq, int Hk, int T,
+                       long long n_units, int units, int hpt) {
+  const long long i = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
+  if (i >= n_units) return;
+  const long long tok = i / units;
+  const int j = (int)(i - tok * units);
+  const long long b = tok / T, t = tok - b * T;
+  float c = 1.f, s = 0.f;
+  if (j < rp.n_pairs)
+    rope_sincos(__ldg(rp.inv_freq + j), rope_position(rp, rp.pair_axis[j], b, t, 0), rp.sign, c, s);
+  const int h0 = blockIdx.y * hpt, h1 = min(h0 + hpt, Hq + Hk);
+  for (int h = h0; h < h1; ++h) {
+    const bool isq = h < Hq;
+    const RopeTensor &x = isq ? q : k;
+    const int hh = isq ? h : h - Hq;
+    rope_pair(static_cast<const E *>(x.in) + b * x.in_b + hh * x.in_h + t * x.in_t,
+              static_cast<E *>(x.out) + b * x.out_b + hh * x.out_h + t * x.out_t, j, rp.n_pairs, adjacent != 0,
+              [&](int, float &cc, float &ss) { cc = c, ss = s; });
+  }
+}
+
+// Heads per thread: sin and cos are shared by the heads a thread visits, but a
+// short input needs the heads spread over threads to fill the GPU.
+static int heads_per_thread(long long n_units, int heads) {
+  const long long threads = n_units * heads, want = 152ll * 1024;
+  const long long h = threads / want;
+  return (int)(h < 1 ? 1 : h > 8 ? 8 : h);
+}
+
+cudaError_t launch_rope(const RopeTensor &q, const RopeTensor &k, const RopeParams &rp, bool adjacent, bool vec, int B,
+                        int Hq, int Hk, int T, int d, int dtype, cudaStream_t stream) {
+  const int n = dtype == DA_BF16 ? 8 : 4;
+  const int units = vec ? d / (2 * n) : d / 2;
+  const long long n_units = (long long)B * T * units;
+  const int hpt = heads_per_thread(n_units, Hq + Hk);
+  const dim3 grid((unsigned)((n_units + kRopeThreads - 1) / kRopeThreads), (unsigned)((Hq + Hk + hpt - 1) / hpt));
+#define DA_ROPE_ARGS q, k, rp, Hq, Hk, T, n_units, units, hpt
+  if (!vec) {
+    if (dtype == DA_BF16)
+      rope_scalar_kernel<__nv_bfloat16>
+          <<<grid, kRopeThreads, 0, stream>>>(q, k, rp, adjacent, Hq, Hk, T, n_units, units, hpt);
+    else
+      rope_scalar_kernel<float><<<grid, kRopeThreads, 0, stream>>>(q, k, rp, adjacent, Hq, Hk, T, n_units, units, hpt);
+  } else if (dtype == DA_BF16) {
+    if (adjacent)
+      rope_kernel<__nv_bfloat16, true><<<grid, kRopeThreads, 0, stream>>>(DA_ROPE_ARGS);
+    else
+      rope_kernel<__nv_bfloat16, false><<<grid, kRopeThreads, 0, stream>>>(DA_ROPE_ARGS);
+  } else {
+    if (adjacent)
+      rope_kernel<float, true><<<grid, kRopeThreads, 0, stream>>>(DA_ROPE_ARGS);
+    else
+      rope_kernel<float, false><<<grid, kRopeThreads, 0, stream>>>(DA_ROPE_ARGS);
+  }
+#undef DA_ROPE_ARGS
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Append to the paged cache.
+//
+// A block takes a run of tokens.  Its first threads place the tokens: the
+// sequence by a binary search of cu_tokens (held in shared memory up to
+// kAppendSearch sequences, so one global read serves the search), the place in
+// the cache from the sequence's length, the pages from the tables.  Then every
+// thread rotates or copies 16-byte pieces of `hpt` heads of q, k and v, and the
+// demand goes out with neighbouring threads on neighbouring tokens.
+// ---------------------------------------------------------------------------
+constexpr int kAppendSearch = 1024;
+
+struct TokenPlace {
+  int pos;            // place in its sequence; -1: skip this token
+  int page, dpage;
+};
+
+__device__ __forceinline__ TokenPlace place_token(int n, const int32_t *cu, const AppendArgs &a,
+                                                  const dilution_attn_paged_cache &c) {
+  TokenPlace p{-1, 0, 0};
+  if (n >= a.N || n >= cu[c.S]) return p;   // padding
+  int lo = 0, hi = c.S - 1;                 // the last sequence that starts at or before n
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (cu[mid] <= n)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int first = cu[lo], end = cu[lo + 1];
+  const int len = __ldg(c.seq_lens + lo);
+  const long long pos = (long long)len - end + n;
+  const long long pg = pos / c.page_size;
+  bool ok = first >= 0 && first <= n && n < end && end <= a.N && pos >= 0 && end - first <= len && pg < c.max_pages;
+  if (ok) {
+    p.page = __ldg(c.page_table + (size_t)lo * c.max_pages + pg);
+    p.dpage = __ldg(c.demand_table + (size_t)lo * c.max_pages + pg);
+    ok = p.page >= 0 && p.page < c.num_pages && p.dpage >= 0 && p.dpage < c.num_demand_pages;
+  }
+  if (ok)
+    p.pos = (int)pos;
+  else
+    atomicCAS(a.status, DA_OK, DA_ERR_INVALID);
+  return p;
+}
+
+// grid.x: runs of tokens; grid.y: groups of heads of [q | k | v], then the
+// demand.  VEC: 16-byte pieces (units of RopeUnit); else pairs of elements.
+template <typename E, bool ADJ, bool VEC>
+__global__ void __launch_bounds__(kRopeThreads)
+    append_kernel(AppendArgs a, dilution_attn_paged_cache c, RopeParams rp) {
+  __shared__ int32_t s_cu[kAppendSearch];
+  __shared__ TokenPlace s_place[kRopeThreads];
+  const int32_t *cu = a.cu_tokens;
+  if (c.S + 1 <= kAppendSearch) {
+    for (int i = threadIdx.x; i <= c.S; i += kRopeThreads) s_cu[i] = __ldg(a.cu_tokens + i);
+    cu = s_cu;
+    __syncthreads();
+  }
+  const int n0 = blockIdx.x * a.tokens;
+  if (threadIdx.x < a.tokens) s_place[threadIdx.x] = place_token(n0 + threadIdx.x, cu, a, c);
+  __syncthreads();
+  const int Hq = a.q != nullptr ? c.Hq : 0;
+  const int rows = Hq + 2 * c.Hkv;
+  const int groups = (rows + a.hpt - 1) / a.hpt;
+  if ((int)blockIdx.y == groups) {   // demand: [page][head][row]
+    for (int i = threadIdx.x; i < a.tokens * c.Hq; i += kRopeThreads) {
+      const int tt = i % a.tokens, h = i / a.tokens;
+      const TokenPlace p = s_place[tt];
+      if (p.pos < 0) continue;
+      const float x = a.demand != nullptr ? a.demand[(long long)(n0 + tt) * a.dem_t + (long long)h * a.dem_h] : 0.f;
+      c.demand_pages[((size_t)p.dpage * c.Hq + h) * c.page_size + p.pos % c.page_size] = x;
+    }
+    return;
+  }
+  const int h0 = blockIdx.y * a.hpt, h1 = min(h0 + a.hpt, rows);
+  for (int i = threadIdx.x; i < a.tokens * a.units; i += kRopeThreads) {
+    const int tt = i / a.units, u = i - tt * a.units;
+    const TokenPlace p = s_place[tt];
+    if (p.pos < 0) continue;
+    const long long n = n0 + tt;
+    auto angle = [&](int j, float &cc, float &ss) {
+      rope_sincos(__ldg(rp.inv_freq + j), rope_position(rp, rp.pair_axis[j], 0, n, p.pos), 1.f, cc, ss);
+    };
+    auto source = [&](int h) -> const E * {
+      if (h < Hq) return static_cast<const E *>(a.q) + n * a.q_t + h * a.q_h;
+      if (h < Hq + c.Hkv) return static_cast<const E *>(a.k) + n * a.k_t + (h - Hq) * a.k_h;
+      return static_cast<const E *>(a.v) + n * a.v_t + (h - Hq - c.Hkv) * a.v_h;
+    };
+    auto target = [&](int h) -> E * {
+      if (h < Hq) return static_cast<E *>(a.q_out) + ((size_t)n * c.Hq + h) * c.d;
+      const bool is_k = h < Hq + c.Hkv;
+      const size_t row =
+          ((size_t)p.page * c.Hkv + (h - Hq - (is_k ? 0 : c.Hkv))) * c.page_size + p.pos % c.page_size;
+      return static_cast<E *>(is_k ? c.k_pages : c.v_pages) + row * c.d;
+    };
+    const int h_turn = Hq + c.Hkv;                 // heads below turn, the values pass
+    if constexpr (VEC) {
+      RopeUnit<E, ADJ> ru;
+      ru.init(u, h0 < h_turn ? rp.n_pairs : 0, angle);
+#pragma unroll 4
+      for (int h = h0; h < h1; ++h) {
+        const E *src = source(h);
+        E *dst = target(h);
+        uint4 va = *reinterpret_cast<const uint4 *>(src + ru.va), vb = *reinterpret_cast<const uint4 *>(src + ru.vb);
+        if (h < h_turn) ru.apply(va, vb);
+        *reinterpret_cast<uint4 *>(dst + ru.va) = va;
+        *reinterpret_cast<uint4 *>(dst + ru.vb) = vb;
+      }
+    } else {
+      float c1 = 1.f, s1 = 0.f;
+      if (u < rp.n_pairs && h0 < h_turn) angle(u, c1, s1);
+      for (int h = h0; h < h1; ++h)
+        rope_pair(source(h), target(h), u, h < h_turn ? rp.n_pairs : 0, ADJ,
+                  [&](int, float &cc, float &ss) { cc = c1, ss = s1; });
+    }
+  }
+}
+
+cudaError_t launch_append(const AppendArgs &args, const dilution_attn_paged_cache &c, const RopeParams &rp, bool vec,
+                          cudaStream_t stream) {
+  AppendArgs a = args;
+  const int nv = c.dtype == DA_BF16 ? 8 : 4;
+  a.units = vec ? c.d / (2 * nv) : c.d / 2;
+  const int rows = (a.q != nullptr ? c.Hq : 0) + 2 * c.Hkv;
+  a.hpt = heads_per_thread((long long)a.N * a.units, rows);
+  // a run of tokens: as many as give every thread one unit, fewer when the
+  // call is too short to fill the GPU
+  a.tokens = kRopeThreads / a.units < 1 ? 1 : kRopeThreads / a.units;
+  const dim3 grid((unsigned)((a.N + a.tokens - 1) / a.tokens), (unsigned)((rows + a.hpt - 1) / a.hpt + 1));
+#define DA_APPEND(E, ADJ, VEC) append_kernel<E, ADJ, VEC><<<grid, kRopeThreads, 0, stream>>>(a, c, rp)
+  if (c.dtype == DA_BF16) {
+    if (vec)
+      a.adjacent ? DA_APPEND(__nv_bfloat16, true, true) : DA_APPEND(__nv_bfloat16, false, true);
+    else
+      a.adjacent ? DA_APPEND(__nv_bfloat16, true, false) : DA_APPEND(__nv_bfloat16, false, false);
+  } else {
+    if (vec)
+      a.adjacent ? DA_APPEND(float, true, true) : DA_APPEND(float, false, true);
+    else
+      a.adjacent ? DA_APPEND(float, true, false) : DA_APPEND(float, false, false);
+  }
+#undef DA_APPEND
+  return cudaGetLastError();
+}
+
+}  // namespace da

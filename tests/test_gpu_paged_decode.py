@@ -1,0 +1,215 @@
+"""GPU parity of dilution_attn_paged_decode against the float64 oracle: ragged
+lengths, page sizes, shared heads, shared prefixes, options, masked rows full
+of NaN, bad tables, graphs and streams."""
+import numpy as np
+import pytest
+import torch
+
+from long_context_attention_gb300 import binding as b
+from tests._paged import DEV, check_step, make_cache, oracle_step, step_and_check
+from tests._parity import host64
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("S,lens,Hq,Hkv,d,page", [
+    (1, [1], 1, 1, 64, 16),
+    (1, [500], 12, 12, 64, 16),
+    (3, [1, 0, 129], 4, 2, 64, 16),
+    (4, [127, 128, 129, 257], 6, 2, 128, 32),
+    (5, [16, 17, 1000, 64, 63], 8, 1, 64, 64),
+    (2, [700, 3], 16, 1, 128, 128),
+    (2, [300, 2], 34, 2, 64, 32),          # 17 query heads a key head: more than one 16-row tile
+    (2, [2049, 1025], 3, 3, 128, 256),
+    (9, [0, 0, 5, 0, 1, 33, 0, 400, 0], 2, 2, 64, 16),
+])
+def test_ragged_decode_matches_oracle(dtype, S, lens, Hq, Hkv, d, page):
+    cache, q, _ = make_cache(S, lens, Hq, Hkv, d, page, dtype, seed=sum(lens) + Hq)
+    step_and_check(cache, q, max(lens))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_all_idle(dtype):
+    cache, q, _ = make_cache(3, [0, 0, 0], 4, 2, 64, 16, dtype)
+    before = cache.demand_pages.clone()
+    out = torch.full_like(q, 7.0)
+    for max_len in (0, 16):
+        b.dilution_attn_paged_decode(q, cache, max_len, out)
+        assert not out.any() and torch.equal(cache.demand_pages, before)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("junk", [float("nan"), float("inf"), -3.0e38])
+def test_rows_past_the_end_are_never_used(dtype, junk):
+    cache, q, _ = make_cache(4, [1, 15, 130, 333], 4, 2, 64, 32, dtype, seed=5, junk=junk)
+    step_and_check(cache, q, 352)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("S,own,Hq,Hkv,d,page,prefix", [
+    (2, [1, 2], 1, 1, 64, 16, 16),
+    (5, [1, 40, 130, 7, 300], 4, 2, 64, 16, 272),
+    (17, [1 + 13 * i for i in range(17)], 2, 2, 128, 64, 448),
+    (3, [5, 1, 129], 8, 1, 128, 128, 128),
+    (40, [1 + i % 5 for i in range(40)], 6, 2, 64, 32, 160),
+    (70, [1 + i % 3 for i in range(70)], 4, 1, 64, 16, 144),     # 280 rows of one key head
+    (36, [2 + i % 7 for i in range(36)], 8, 2, 128, 16, 400),
+])
+def test_shared_prefix_matches_oracle(dtype, S, own, Hq, Hkv, d, page, prefix):
+    lens = [prefix + n for n in own]
+    cache, q, pt = make_cache(S, lens, Hq, Hkv, d, page, dtype, seed=S + prefix, prefix=prefix)
+    step_and_check(cache, q, max(lens), prefix_table=pt)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_shared_prefix_with_idle_slots_and_nothing_of_their_own(dtype):
+    # idle slots among the sequences, and sequences that end with the prefix
+    lens = [0, 160, 165, 0, 160, 300, 0]
+    cache, q, pt = make_cache(7, lens, 4, 2, 64, 32, dtype, seed=9, prefix=160, junk=float("nan"))
+    step_and_check(cache, q, 300, prefix_table=pt)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefix_equals_the_same_pages_in_the_tables(dtype):
+    lens = [512 + n for n in (3, 70, 200, 1)]
+    cache, q, pt = make_cache(4, lens, 4, 2, 64, 64, dtype, seed=21, prefix=512)
+    old = cache.demand_pages.clone()
+    a = step_and_check(cache, q, 800, prefix_table=pt)
+    da = cache.demand_pages.clone()
+    cache.demand_pages.copy_(old)
+    step_and_check(cache, q, 800)
+    # two roundings of bids that differ by the order of their sums (see tests/_paged.py)
+    assert torch.allclose(da, cache.demand_pages, rtol=1e-5, atol=1e-6)
+    assert a.isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_options(dtype):
+    lens = [40, 0, 300]
+    for flags, tau, per_head, prefix in ((b.DA_FLAG_EARLIER_DEMAND_ONLY, 1.3, False, 0), (0, 1.0, True, 0),
+                                         (0, 0.0, False, 0), (b.DA_FLAG_EARLIER_DEMAND_ONLY, 1.0, True, 32),
+                                         (0, 2.0, False, 32)):
+        cache, q, pt = make_cache(3, lens, 4, 2, 64, 16, dtype, seed=31, prefix=prefix)
+        tau_bh = torch.linspace(0.0, 2.0, 12, device=DEV) if per_head else None
+        step_and_check(cache, q, 300, tau=tau, tau_bh=tau_bh, flags=flags, eps=1e-3, prefix_table=pt)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sharp_logits(dtype):
+    # one key takes nearly the whole bid of its row; another row is uniform
+    cache, q, _ = make_cache(2, [200, 90], 2, 2, 64, 16, dtype, seed=41)
+    q[0, 0] = cache.k_pages[int(cache.page_table[0, 3]), 0, 5] * 4
+    q[1, 1] = 0
+    step_and_check(cache, q, 200)
+
+
+def test_max_len_beyond_every_sequence_and_repeats():
+    cache, q, pt = make_cache(3, [70, 200, 64], 4, 2, 64, 32, "bf16", seed=51, prefix=64, extra_width=300)
+    old = cache.demand_pages.clone()
+    outs = []
+    for max_len, table in ((200, None), (9000, None), (200, pt), (200, pt), (9000, pt)):
+        cache.demand_pages.copy_(old)
+        outs.append((step_and_check(cache, q, max_len, prefix_table=table), cache.demand_pages.clone()))
+    assert torch.equal(outs[2][0], outs[3][0]) and torch.equal(outs[2][1], outs[3][1])   # equal bits
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_bad_device_data_is_reported(dtype):
+    good, q, pt = make_cache(3, [70, 200, 64], 4, 2, 64, 32, dtype, seed=61, prefix=64)
+    ws = b.dilution_attn_paged_decode_workspace(good, 224)
+
+    def after(change, prefix=None):
+        cache, qq, _ = make_cache(3, [70, 200, 64], 4, 2, 64, 32, dtype, seed=61, prefix=64)
+        change(cache)
+        p = None if prefix is None else prefix.clone()
+        b.dilution_attn_paged_decode(qq, cache, 224, prefix_table=p, workspace=ws)
+        first = b.dilution_attn_get_error(ws)
+        assert b.dilution_attn_get_error(ws) == b.DA_OK      # read once
+        return first
+
+    assert after(lambda c: None) == b.DA_OK
+    assert after(lambda c: c.seq_lens.__setitem__(1, 225)) == b.DA_ERR_INVALID
+    assert after(lambda c: c.seq_lens.__setitem__(1, -1)) == b.DA_ERR_INVALID
+    assert after(lambda c: c.seq_lens.__setitem__(1, 63), pt) == b.DA_ERR_INVALID     # shorter than the prefix
+    assert after(lambda c: c.page_table.__setitem__((1, 3), -5)) == b.DA_ERR_INVALID
+    assert after(lambda c: c.page_table.__setitem__((1, 3), 10 ** 6)) == b.DA_ERR_INVALID
+    assert after(lambda c: c.demand_table.__setitem__((0, 0), 10 ** 6)) == b.DA_ERR_INVALID
+    assert after(lambda c: c.page_table.__setitem__((1, 0), -5), pt) == b.DA_OK       # not read behind a prefix
+    bad = pt.clone()
+    bad[1] = 10 ** 6
+    assert after(lambda c: None, bad) == b.DA_ERR_INVALID
+    # the other sequences of a call with one bad length are right
+    cache, qq, _ = make_cache(3, [70, 200, 64], 4, 2, 64, 32, dtype, seed=61)
+    cache.seq_lens[1] = 0
+    ref = oracle_step(cache, qq)
+    cache.seq_lens[1] = 300
+    out = b.dilution_attn_paged_decode(qq, cache, 224, workspace=ws)
+    assert b.dilution_attn_get_error(ws) == b.DA_ERR_INVALID
+    keep = [0, 2]
+    assert np.abs(host64(out)[keep] - ref[0][keep]).max() <= 2e-2
+
+
+def test_graph_replay_with_growing_sequences():
+    # one captured step replays over lengths and tables that change on the device
+    cache, q, pt = make_cache(3, [64 + 100, 64 + 200, 64 + 30], 4, 2, 64, 32, "bf16", seed=71, prefix=64)
+    cache.seq_lens.copy_(torch.tensor([70, 64, 65], dtype=torch.int32))
+    ws = b.dilution_attn_paged_decode_workspace(cache, 264)
+    out = torch.empty_like(q)
+    old = cache.demand_pages.clone()
+    b.dilution_attn_paged_decode(q, cache, 264, out, prefix_table=pt, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b.dilution_attn_paged_decode(q, cache, 264, out, prefix_table=pt, workspace=ws)
+    cache.demand_pages.copy_(old)
+    for lens in ([70, 64, 65], [100, 0, 94], [164, 264, 94]):
+        cache.seq_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        before = cache.demand_pages.clone()
+        ref = oracle_step(cache, q, prefix_table=pt)
+        g.replay()
+        assert b.dilution_attn_get_error(ws) == b.DA_OK
+        check_step(cache, q, before, out, ref)
+
+
+def test_two_streams_with_their_own_workspaces():
+    made = [make_cache(4, [900, 1, 333, 64], 4, 4, 64, 32, "bf16", seed=80 + i) for i in range(2)]
+    refs = [oracle_step(c, q) for c, q, _ in made]
+    before = [c.demand_pages.clone() for c, _, _ in made]
+    wss = [b.dilution_attn_paged_decode_workspace(c, 900) for c, _, _ in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.empty_like(q) for _, q, _ in made]
+    for (c, q, _), ws, st, out in zip(made, wss, streams, outs):
+        b.dilution_attn_paged_decode(q, c, 900, out, workspace=ws, stream=st)
+    torch.cuda.synchronize()
+    for (c, q, _), o, r, old in zip(made, outs, refs, before):
+        check_step(c, q, old, o, r)
+
+
+def test_pool_past_32_bit_offsets():
+    # pools of more than 2^32 bytes and 2^31 elements: the sequence's pages lie at the end
+    page, d, Hkv = 256, 128, 4
+    n = (1 << 31) // (Hkv * page * d) + 40
+    k = torch.empty(n, Hkv, page, d, dtype=torch.bfloat16, device=DEV)
+    v = torch.empty_like(k)
+    lens = [700, 300]
+    ids = torch.tensor([[n - 1, n - 5, n - 3], [n - 9, n - 7, -1]], dtype=torch.int32)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    for i in ids.flatten().tolist():
+        if i >= 0:
+            k[i] = torch.randn(Hkv, page, d, generator=g, device=DEV)
+            v[i] = torch.randn(Hkv, page, d, generator=g, device=DEV)
+    small = {int(i): j for j, i in enumerate(x for x in ids.flatten().tolist() if x >= 0)}
+    order = list(small)
+    dem = torch.rand(6, Hkv, page, generator=g, device=DEV)
+    dt = torch.tensor([[0, 1, 2], [3, 4, -1]], dtype=torch.int32, device=DEV)
+    sl = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    cache = b.PagedCache(k, v, dem, ids.to(DEV), dt, sl)
+    local = torch.tensor([[small.get(int(i), -1) for i in row] for row in ids], dtype=torch.int32, device=DEV)
+    mirror = b.PagedCache(k[order].contiguous(), v[order].contiguous(), dem.clone(), local, dt, sl)
+    q = torch.randn(2, Hkv, d, generator=g, device=DEV).bfloat16()
+    ref = oracle_step(mirror, q)
+    before = cache.demand_pages.clone()
+    out = b.dilution_attn_paged_decode(q, cache, 700)
+    check_step(cache, q, before, out, ref)
