@@ -640,9 +640,10 @@ def dilution_attn_paged_decode_workspace(cache, max_len: int, n_prefix_pages=Non
     ``max_len`` tokens, its status block zeroed.  n_prefix_pages: the prefix
     it will serve (omitted: large enough for any)."""
     args = (cache.S, cache.Hq, cache.Hkv, cache.d, int(max_len))
-    need = max(dilution_attn_paged_decode_workspace_size(*args, n, cache.page_size, cache._code)
-               for n in ((0, int(max_len) // cache.page_size) if n_prefix_pages is None else (int(n_prefix_pages),)))
-    ws = torch.empty(max(need + (4096 if n_prefix_pages is None else 0), 256), dtype=torch.uint8, device=cache.device)
+    # the size depends on whether there is a prefix, not on its length
+    counts = (0, min(1, int(max_len) // cache.page_size)) if n_prefix_pages is None else (int(n_prefix_pages),)
+    need = max(dilution_attn_paged_decode_workspace_size(*args, n, cache.page_size, cache._code) for n in counts)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=cache.device)
     ws[:256].zero_()
     return ws
 

@@ -8,6 +8,9 @@
 namespace da {
 size_t pgs_workspace(int64_t rows, int max_len, int prefix_len, int d);
 cudaError_t launch_paged_decode_simt(const PagedDecode &p, cudaStream_t stream);
+size_t pgt_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len);
+bool pgt_serves(int S, int dtype);
+int launch_paged_decode_bf16(const PagedDecode &p, cudaStream_t stream);
 }  // namespace da
 
 using namespace da;
@@ -144,6 +147,11 @@ int check_cache(const dilution_attn_paged_cache *c) {
   return DA_OK;
 }
 
+size_t decode_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int dtype) {
+  return pgt_serves(S, dtype) ? pgt_workspace(S, Hq, Hkv, d, max_len, prefix_len)
+                              : pgs_workspace((int64_t)S * Hq, max_len, prefix_len, d);
+}
+
 int check_workspace(const void *ws, size_t bytes, size_t need) {
   if (ws == nullptr || bytes < need) return DA_ERR_WORKSPACE;
   return aligned(ws, 256) ? DA_OK : DA_ERR_INVALID;
@@ -223,11 +231,11 @@ int dilution_attn_paged_append(const void *q, const int64_t *q_strides, const vo
 
 size_t dilution_attn_paged_decode_workspace_size(int S, int Hq, int Hkv, int d, int max_len, int n_prefix_pages,
                                                  int page_size, int dtype) {
-  (void)dtype;
-  if (S < 0 || Hq < 1 || Hkv < 1 || max_len < 0 || n_prefix_pages < 0 || page_size < 1 || !head_dim_supported(d))
+  if (dtype != DA_F32 && dtype != DA_BF16) return 0;
+  if (S < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_len < 0 || n_prefix_pages < 0 || page_size < 1 || !head_dim_supported(d))
     return 0;
   if ((int64_t)n_prefix_pages * page_size > max_len) return 0;
-  return pgs_workspace((int64_t)S * Hq, max_len, n_prefix_pages * page_size, d);
+  return decode_workspace(S, Hq, Hkv, d, max_len, n_prefix_pages * page_size, dtype);
 }
 
 int dilution_attn_paged_decode(const void *q, const dilution_attn_paged_cache *cache, const int32_t *prefix_table,
@@ -245,8 +253,9 @@ int dilution_attn_paged_decode(const void *q, const dilution_attn_paged_cache *c
   if (c.S == 0) return DA_OK;
   if (q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 16)) return DA_ERR_INVALID;
   const int prefix_len = n_prefix_pages * c.page_size;
-  st = check_workspace(workspace, workspace_bytes, pgs_workspace((int64_t)c.S * c.Hq, max_len, prefix_len, c.d));
+  st = check_workspace(workspace, workspace_bytes, decode_workspace(c.S, c.Hq, c.Hkv, c.d, max_len, prefix_len, c.dtype));
   if (st != DA_OK) return st;
+  if ((int64_t)c.num_pages * c.Hkv > 0x7FFFFFFF) return DA_ERR_UNSUPPORTED;   // a copy's coordinate
   // the launch grids' third dimension counts 16-row groups
   const int64_t G = c.Hq / c.Hkv;
   if (c.S * ((G + 15) / 16) + (c.S * G + 15) / 16 > 65535 || c.Hkv > 65535) return DA_ERR_UNSUPPORTED;
@@ -264,6 +273,7 @@ int dilution_attn_paged_decode(const void *q, const dilution_attn_paged_cache *c
   p.earlier = (flags & DA_FLAG_EARLIER_DEMAND_ONLY) != 0;
   p.status = reinterpret_cast<int *>(workspace);
   p.ws = reinterpret_cast<uint8_t *>(workspace);
+  if (pgt_serves(c.S, c.dtype)) return launch_paged_decode_bf16(p, reinterpret_cast<cudaStream_t>(stream));
   return launch_paged_decode_simt(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 

@@ -36,7 +36,8 @@ DA_HD PgsLayout pgs_layout(int64_t rows, int max_len, int prefix_len, int d) {
   w.Lp = (int)round_up(max_len, 16);
   w.prefix_chunks = (prefix_len + kPgsChunk - 1) / kPgsChunk;
   w.own_chunks = (max_len - prefix_len + kPgsChunk - 1) / kPgsChunk;
-  w.nchunk = w.prefix_chunks + w.own_chunks;
+  w.nchunk = (max_len + kPgsChunk - 1) / kPgsChunk + 1;   // for any prefix
+
   w.logit_off = kStatusBytes;
   w.ml_off = (size_t)round_up((int64_t)w.logit_off + rows * w.Lp * 4, 256);
   w.acc_off = (size_t)round_up((int64_t)w.ml_off + rows * w.nchunk * 8, 256);
@@ -222,10 +223,10 @@ __global__ void __launch_bounds__(kPgsThreads) pgs_update(PagedDecode p, PgsLayo
     b.row(p, G, r, s, hq);
     const float2 *ml = reinterpret_cast<const float2 *>(p.ws + L.ml_off) + ((size_t)s * p.c.Hq + hq) * L.nchunk;
     float m = -INFINITY, l = 0.f;
-    for (int c = lane; c < L.nchunk; c += 32) m = fmaxf(m, ml[c].x);
+    for (int c = lane; c < L.prefix_chunks + L.own_chunks; c += 32) m = fmaxf(m, ml[c].x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    for (int c = lane; c < L.nchunk; c += 32)
+    for (int c = lane; c < L.prefix_chunks + L.own_chunks; c += 32)
       if (ml[c].y != 0.f) l += ml[c].y * exp2f(ml[c].x - m);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);

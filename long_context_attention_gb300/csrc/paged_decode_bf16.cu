@@ -1,0 +1,812 @@
+// Decode step over the paged cache in bf16: streaming tensor-core kernels.
+//
+// Mathematics: as paged_decode.cu.  Two passes over the keys, joined by the
+// softmax normaliser that a share needs:
+//   pgt_keys    x = q . k (tau / sqrt(d) log2 e) of every key into a scratch of
+//               4 bytes per (row, key), and each piece's (max, sum 2^(x - max));
+//   pgt_values  lse2 from the pieces, p = 2^(x - lse2), share = p / (D + p +
+//               eps), D += p, and each piece's sum share v and sum share;
+//   pgt_combine out = sum of the pieces' numerators / sum of their share sums,
+//               in a fixed order (equal bits from equal calls).
+//
+// What bounds it: HBM.  K and V are read once, D is read and written once, the
+// logits stay mostly in L2.  So the layout serves the copies: whole pages (or
+// a tile's rows of one) arrive by TMA with a 128-byte swizzle into a ring of stages
+// of 16 KB (128 keys at d = 64, 64 at d = 128) that one producer warp fills; in pgt_values the same warp brings
+// the logits and the demand by 16-byte asynchronous copies, so that everything
+// a stage needs is in flight together.
+//
+// Tensor cores: m16n8k16 (bf16, fp32 sums).  A decode step has few query rows
+// per key head, so the tensor rate is not what bounds it; the M = 16 rows are
+// the query heads that share a key head (padded), and one 16-key group costs a
+// warp 8 + 16 instructions at d = 64.  Keys are taken in an order in which each
+// thread holds 4 consecutive keys of a row: logits, demand and shares then move
+// in 16-byte pieces, and the share of a key is already where the A operand of
+// the value product wants it (no shuffles).  Shares enter that product as two
+// bf16 terms (share rounded, and what rounding left), so they keep 2^-16
+// relative; one term alone would double the output's rounding error.
+//
+// Work split: the (segment, key tile) pairs of the call are numbered, a
+// segment being one sequence's own part or the shared prefix for one key head
+// and up to 16 rows; every CTA takes an equal run of numbers, so ragged
+// lengths balance to one tile.  A run crosses segments; the stretch inside one
+// is a piece and leaves one partial result, in slot (CTA + segment), which grows
+// along the numbering and is therefore unique.
+#include "da_paged.h"
+#include "da_ptx.cuh"
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+namespace da {
+
+constexpr int kPgtWarps = 4;                      // consumer warps
+constexpr int kPgtThreads = kPgtWarps * 32 + 32;  // and the producer warp
+constexpr int kPgtMaxSeqs = 1024;                 // lengths kept in shared memory
+DA_HD constexpr int pgt_tile(int d) { return d == 64 ? 128 : 64; }   // keys per stage (16 KB of K or V)
+DA_HD constexpr int pgt_pitch(int d) { return pgt_tile(d) + 4; }     // floats per staged row (no bank conflicts)
+constexpr int kPgtMaxCtas = 2 * 152;              // two resident CTAs on each SM
+
+// Host plan of a call; slots and scratch offsets.
+struct PgtPlan {
+  int ctas, tile, G, own_rows, own_groups, prefix_groups, prefix_tiles, own_segs, prefix_segs, Lp;
+  size_t logit_off, own_ml_off, own_acc_off, pre_ml_off, pre_acc_off, total;
+};
+
+static PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_len) {
+  PgtPlan w;
+  w.G = Hq / Hkv;
+  w.own_rows = w.G < 16 ? w.G : 16;
+  w.own_groups = (w.G + 15) / 16;
+  w.tile = pgt_tile(d);
+  w.prefix_tiles = (prefix_len + w.tile - 1) / w.tile;
+  w.prefix_groups = prefix_len > 0 ? (S * w.G + 15) / 16 : 0;
+  w.own_segs = S * Hkv * w.own_groups;
+  w.prefix_segs = Hkv * w.prefix_groups;
+  const int64_t own_tiles = (max_len - prefix_len + w.tile - 1) / w.tile;
+  const int64_t most = (int64_t)w.own_segs * own_tiles + (int64_t)w.prefix_segs * w.prefix_tiles;
+  w.ctas = (int)(most < 1 ? 1 : most > kPgtMaxCtas ? kPgtMaxCtas : most);
+  w.Lp = (int)round_up(max_len, 16);
+  // slots for the most CTAs, so that the size depends on the prefix's presence alone
+  const int64_t own_slots = kPgtMaxCtas + w.own_segs;
+  const int64_t pre_slots = w.prefix_segs > 0 ? kPgtMaxCtas + w.prefix_segs : 0;
+  auto next = [](size_t off, int64_t bytes) { return (size_t)round_up((int64_t)off + bytes, 256); };
+  w.logit_off = kStatusBytes;
+  w.own_ml_off = next(w.logit_off, (int64_t)S * Hq * w.Lp * 4);
+  w.own_acc_off = next(w.own_ml_off, own_slots * w.own_rows * 8);
+  w.pre_ml_off = next(w.own_acc_off, own_slots * w.own_rows * acc_stride(d) * 4);
+  w.pre_acc_off = next(w.pre_ml_off, pre_slots * 16 * 8);
+  w.total = next(w.pre_acc_off, pre_slots * 16 * acc_stride(d) * 4);
+  return w;
+}
+size_t pgt_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len) {
+  return pgt_plan(S, Hq, Hkv, d, max_len, prefix_len).total;
+}
+bool pgt_serves(int S, int dtype) { return dtype == DA_BF16 && S <= kPgtMaxSeqs; }
+
+// ------------------------------------------------------------------ device plan
+// Lengths and running tile counts of the sequences, in shared memory.
+struct PgtLens {
+  int len[kPgtMaxSeqs];
+  int cum[kPgtMaxSeqs + 1];   // own tiles of the sequences before
+  int warp_sum[32];
+};
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// All threads of the block: fills L; ends with a block barrier.
+template <int THREADS>
+__device__ void pgt_load_lens(const PagedDecode &p, const PgtPlan &w, PgtLens &L, int *status) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, S = p.c.S;
+  const int per = (S + THREADS - 1) / THREADS;
+  const int s0 = min(tid * per, S), s1 = min(s0 + per, S);
+  int sum = 0;
+  for (int s = s0; s < s1; ++s) {
+    const int n = paged_len(p, s, status);
+    L.len[s] = n;
+    L.cum[s] = sum;
+    if (n > 0) sum += (n - p.prefix_len + w.tile - 1) / w.tile;
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) L.warp_sum[warp] = inc;
+  __syncthreads();
+  int base = inc - sum;
+  for (int i = 0; i < warp; ++i) base += L.warp_sum[i];
+  for (int s = s0; s < s1; ++s) L.cum[s] += base;
+  if (tid == THREADS - 1) L.cum[S] = base + sum;
+  __syncthreads();
+}
+
+// Tile numbers: the prefix's segments first, then each sequence's.
+struct PgtTiles {
+  long long total, prefix;   // all tiles; the prefix's
+  int per_own;               // segments of one sequence
+  int ctas;                  // CTAs that take tiles: no more than tiles, so that each has one
+};
+__device__ __forceinline__ PgtTiles pgt_tiles(const PagedDecode &p, const PgtPlan &w, const PgtLens &L) {
+  PgtTiles t;
+  t.per_own = p.c.Hkv * w.own_groups;
+  t.prefix = (long long)w.prefix_segs * w.prefix_tiles;
+  t.total = t.prefix + (long long)L.cum[p.c.S] * t.per_own;
+  t.ctas = (int)min((long long)w.ctas, t.total);
+  return t;
+}
+__device__ __forceinline__ long long pgt_first(const PgtTiles &t, int cta) {
+  return cta < t.ctas ? (long long)cta * t.total / t.ctas : t.total;
+}
+__device__ __forceinline__ int pgt_cta_of(const PgtTiles &t, long long tile) {   // t.total > 0
+  return (int)(((tile + 1) * t.ctas + t.total - 1) / t.total) - 1;
+}
+
+// One segment, seen from a tile of it.
+struct PgtSeg {
+  int s;                     // its sequence; -1: the prefix
+  int hkv, row0, nrows;      // rows row0 .. of the sequence's group / of the batch
+  int key0, end;             // keys of the tile and the segment's end
+  int left;                  // tiles from here to the segment's end
+  int seg;                   // its number among the prefix's or the sequences' segments
+  __device__ __forceinline__ void row(int G, int r, int &seq, int &hq) const {
+    if (s >= 0) {
+      seq = s;
+      hq = hkv * G + row0 + r;
+    } else {
+      seq = (row0 + r) / G;
+      hq = hkv * G + (row0 + r) % G;
+    }
+  }
+};
+
+__device__ __forceinline__ PgtSeg pgt_seg(const PagedDecode &p, const PgtPlan &w, const PgtTiles &t, const PgtLens &L,
+                                          long long tile) {
+  PgtSeg g;
+  int at;
+  if (tile < t.prefix) {
+    g.s = -1;
+    g.seg = (int)(tile / w.prefix_tiles);
+    at = (int)(tile - (long long)g.seg * w.prefix_tiles);
+    g.hkv = g.seg / w.prefix_groups;
+    g.row0 = g.seg % w.prefix_groups * 16;
+    g.nrows = min(16, p.c.S * w.G - g.row0);
+    g.key0 = at * w.tile;
+    g.end = p.prefix_len;
+    g.left = w.prefix_tiles - at;
+  } else {
+    const long long j = tile - t.prefix;
+    const int q = (int)(j / t.per_own);          // tiles of one segment column
+    int lo = 0, hi = p.c.S - 1;                  // the last sequence with cum <= q (and tiles of its own)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (L.cum[mid] <= q)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const int n = L.cum[lo + 1] - L.cum[lo];
+    const int r = (int)(j - (long long)L.cum[lo] * t.per_own);
+    const int h = r / n;
+    at = r - h * n;
+    g.s = lo;
+    g.hkv = h / w.own_groups;
+    g.row0 = h % w.own_groups * 16;
+    g.nrows = min(16, w.G - g.row0);
+    g.key0 = p.prefix_len + at * w.tile;
+    g.end = L.len[lo];
+    g.left = n - at;
+    g.seg = lo * t.per_own + h;
+  }
+  return g;
+}
+
+// Slots of the pieces of row (s, hq): the prefix's and its own.
+struct PgtPieces {
+  int pre0, npre, pre_row;   // first slot, count, row inside the slot
+  int own0, nown, own_row;
+};
+__device__ __forceinline__ PgtPieces pgt_pieces(const PagedDecode &p, const PgtPlan &w, const PgtTiles &t,
+                                                const PgtLens &L, int s, int hq) {
+  PgtPieces r{0, 0, 0, 0, 0, 0};
+  if (L.len[s] == 0) return r;
+  const int hkv = hq / w.G, g = hq % w.G;
+  if (w.prefix_tiles > 0) {
+    const int R = s * w.G + g, seg = hkv * w.prefix_groups + R / 16;
+    const long long a = (long long)seg * w.prefix_tiles;
+    const int c0 = pgt_cta_of(t, a), c1 = pgt_cta_of(t, a + w.prefix_tiles - 1);
+    r.pre0 = c0 + seg;
+    r.npre = c1 - c0 + 1;
+    r.pre_row = R % 16;
+  }
+  const int n = L.cum[s + 1] - L.cum[s];
+  if (n > 0) {
+    const int h = hkv * w.own_groups + g / 16;
+    const long long a = t.prefix + (long long)L.cum[s] * t.per_own + (long long)h * n;
+    const int c0 = pgt_cta_of(t, a), c1 = pgt_cta_of(t, a + n - 1);
+    r.own0 = c0 + s * t.per_own + h;
+    r.nown = c1 - c0 + 1;
+    r.own_row = g % 16;
+  }
+  return r;
+}
+
+// ------------------------------------------------------------------ tensor pieces
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte piece `piece` of row `row` in a staged tile: boxes of
+// 64 elements (128 bytes) by a tile's rows, pieces swizzled by the row.
+template <int D>
+__device__ __forceinline__ uint32_t tile_off(int row, int piece) {
+  return (uint32_t)((piece >> 3) * pgt_tile(D) * 128 + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
+}
+// The order of a 16-key group: column c of the first 8 (half 0) and the last 8
+// (half 1) columns is key 4 (c / 2) + 2 half + c % 2, so that a thread's four
+// columns (2t, 2t + 1 of both halves) are keys 4t .. 4t + 3.
+__device__ __forceinline__ int group_key(int c, int half) { return 4 * (c >> 1) + 2 * half + (c & 1); }
+
+template <int D>
+struct PgtRing {
+  static constexpr int kTile = pgt_tile(D);
+  static constexpr int kTileBytes = kTile * D * 2;
+  uint64_t full[8], empty[8];
+  int abort_word;
+  __device__ __forceinline__ void init(int stages, int full_count) {
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(&full[i], full_count);
+      mbar_init(&empty[i], kPgtWarps);
+    }
+    abort_word = 0;
+    fence_mbar_init();
+  }
+};
+
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z) {
+  asm volatile(
+      "{\n\t.reg .b64 pol;\n\t"
+      "createpolicy.fractional.L2::evict_first.b64 pol, 1.0;\n\t"
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], pol;\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// Producer warp: the pages behind keys [key0, min(key0 + tile, end)) of one
+// segment into a stage; lane i brings page piece i.  `arrive` adds the stage's
+// expected bytes (lane 0 arrives once).
+template <int D>
+__device__ __forceinline__ void load_tile(const PagedDecode &p, const PgtSeg &g, const CUtensorMap *map, uint32_t dst,
+                                          uint64_t *full, int lane) {
+  constexpr int TILE = pgt_tile(D);
+  const int ps = p.c.page_size, rows = min(ps, TILE);
+  const int pieces = (min(TILE, g.end - g.key0) + rows - 1) / rows;
+  int page = -1, key = g.key0 + lane * rows;
+  if (lane < pieces) {
+    const int32_t *e = g.s >= 0 ? p.c.page_table + (size_t)g.s * p.c.max_pages + key / ps : p.prefix_table + key / ps;
+    page = checked_page(e, p.c.num_pages, p.status);
+  }
+  const int n = __popc(__ballot_sync(0xffffffffu, page >= 0));
+  if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(n * rows * D * 2));
+  __syncwarp();
+  if (page >= 0) {
+#pragma unroll
+    for (int x = 0; x < D; x += 64)
+      tma_page(dst + (x / 64) * TILE * 128 + lane * rows * 128, map, full, x, key % ps, page * p.c.Hkv + g.hkv);
+  }
+}
+
+// Let the copies in flight land before the CTA exits after a timeout.
+__device__ __forceinline__ void drain(uint64_t *full, int stages, long long issued) {
+  for (long long st = issued > stages ? issued - stages : 0; st < issued; ++st) {
+    const unsigned long long t0 = globaltimer();
+    while (!mbar_try_wait(&full[st % stages], (uint32_t)((st / stages) & 1)))
+      if (globaltimer() - t0 > 100ull * 1000ull * 1000ull) break;
+  }
+}
+
+extern __shared__ __align__(1024) uint8_t pgt_smem_raw[];
+__device__ __forceinline__ uint8_t *pgt_smem_base() {   // the swizzle counts from 1024-byte boundaries
+  return pgt_smem_raw + ((1024u - (smem_u32(pgt_smem_raw) & 1023u)) & 1023u);
+}
+
+// ------------------------------------------------------------------ pass 1: logits
+template <int D>
+__global__ void __launch_bounds__(kPgtThreads, 2)
+    pgt_keys(PagedDecode p, PgtPlan w, const __grid_constant__ CUtensorMap kmap, int stages) {
+  constexpr int KS = D / 16;   // k-steps
+  constexpr int TILE = pgt_tile(D), WK = TILE / kPgtWarps;   // a warp's keys of a tile
+  __shared__ PgtLens L;
+  __shared__ PgtRing<D> ring;
+  __shared__ float2 s_ml[kPgtWarps][16];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  pdl_launch_dependents();
+  if (tid == 0) ring.init(stages, 1);
+  pgt_load_lens<kPgtThreads>(p, w, L, blockIdx.x == 0 ? p.status : nullptr);
+  const PgtTiles tt = pgt_tiles(p, w, L);
+  const long long i0 = pgt_first(tt, blockIdx.x), i1 = pgt_first(tt, blockIdx.x + 1);
+  const WaitCtx wc{reinterpret_cast<volatile int *>(&ring.abort_word), p.status};
+  const uint32_t base = smem_u32(pgt_smem_base());
+  if (warp == kPgtWarps) {   // producer
+    PgtSeg g{};
+    int left = 0;
+    long long st = 0;
+    for (long long i = i0; i < i1; ++i, ++st) {
+      if (left == 0) {
+        g = pgt_seg(p, w, tt, L, i);
+        left = g.left;
+      }
+      const int slot = (int)(st % stages);
+      if (!warp_wait(&ring.empty[slot], (uint32_t)(((st / stages) & 1) ^ 1), wc)) break;
+      load_tile<D>(p, g, &kmap, base + slot * PgtRing<D>::kTileBytes, &ring.full[slot], lane);
+      g.key0 += TILE;
+      --left;
+    }
+    if (ring.abort_word && lane == 0) drain(ring.full, stages, st);
+    return;
+  }
+  const int gid = lane / 4, t = lane % 4;
+  for (long long i = i0; i < i1;) {
+    PgtSeg g = pgt_seg(p, w, tt, L, i);
+    const int n = (int)min((long long)g.left, i1 - i);
+    // Q rows as the A operand; rows past the segment's are 0
+    uint32_t qa[KS][4];
+    float c2[2] = {0.f, 0.f};
+    float *xrow[2] = {nullptr, nullptr};
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const int r = gid + 8 * hh;
+      const bool ok = r < g.nrows;
+      int s = 0, hq = 0;
+      if (ok) {
+        g.row(w.G, r, s, hq);
+        c2[hh] = head_c2(p.hs, s * p.c.Hq + hq, (t == 0 && warp == 0) ? p.status : nullptr);
+        xrow[hh] = reinterpret_cast<float *>(p.ws + w.logit_off) + ((size_t)s * p.c.Hq + hq) * w.Lp;
+      }
+      const uint32_t *qr =
+          reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)s * p.c.Hq + hq) * D);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        qa[ks][hh] = ok ? __ldg(qr + ks * 8 + t) : 0u;
+        qa[ks][2 + hh] = ok ? __ldg(qr + ks * 8 + 4 + t) : 0u;
+      }
+    }
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // A wait that gave up ends the piece's loop but not the warp, which still
+    // meets the others at the barriers below (its later waits fail at once).
+    for (int k = 0; k < n; ++k) {
+      const long long st = i - i0 + k;
+      const int slot = (int)(st % stages);
+      if (!warp_wait(&ring.full[slot], (uint32_t)((st / stages) & 1), wc)) break;
+      const uint32_t tile = base + slot * PgtRing<D>::kTileBytes;
+      const int key_tile = g.key0 + k * TILE;
+#pragma unroll
+      for (int gg = 0; gg < WK / 16; ++gg) {
+        const int kl = warp * WK + gg * 16;          // the group's first key in the tile
+        if (key_tile + kl >= g.end) break;
+        float acc[2][4] = {};
+        // lane -> the row it addresses: matrices (half 0, k 0-7), (half 0, k 8-15), (half 1, ..), (half 1, ..)
+        const int row = kl + group_key(lane & 7, lane >> 4);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t bfr[4];
+          ldsm_x4(tile + tile_off<D>(row, 2 * ks + ((lane >> 3) & 1)), bfr);
+          mma16816(acc[0], qa[ks], bfr[0], bfr[1]);
+          mma16816(acc[1], qa[ks], bfr[2], bfr[3]);
+        }
+        const int key = key_tile + kl + 4 * t;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          if (gid + 8 * hh >= g.nrows) continue;
+          float x[4] = {acc[0][2 * hh] * c2[hh], acc[0][2 * hh + 1] * c2[hh], acc[1][2 * hh] * c2[hh],
+                        acc[1][2 * hh + 1] * c2[hh]};
+          *reinterpret_cast<float4 *>(xrow[hh] + key) = make_float4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (key + e >= g.end) x[e] = -INFINITY;
+          const float mn = fmaxf(m[hh], fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+          const float ms = mn == -INFINITY ? 0.f : mn;
+          l[hh] = l[hh] * ex2_approx(m[hh] - ms) + (ex2_approx(x[0] - ms) + ex2_approx(x[1] - ms)) +
+                  (ex2_approx(x[2] - ms) + ex2_approx(x[3] - ms));
+          m[hh] = mn;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring.empty[slot]);
+    }
+    // the piece's (max, sum) of each row: over the quad, then over the warps
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m[hh], o), l2 = __shfl_xor_sync(0xffffffffu, l[hh], o);
+        const float mn = fmaxf(m[hh], m2), ms = mn == -INFINITY ? 0.f : mn;
+        l[hh] = l[hh] * ex2_approx(m[hh] - ms) + l2 * ex2_approx(m2 - ms);
+        m[hh] = mn;
+      }
+      if (t == 0) s_ml[warp][gid + 8 * hh] = make_float2(m[hh], l[hh]);
+    }
+    named_bar_sync(1, kPgtWarps * 32);
+    if (tid < g.nrows) {
+      float M = -INFINITY, S = 0.f;
+#pragma unroll
+      for (int v = 0; v < kPgtWarps; ++v) M = fmaxf(M, s_ml[v][tid].x);
+      const float ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int v = 0; v < kPgtWarps; ++v) S += s_ml[v][tid].y * ex2_approx(s_ml[v][tid].x - ms);
+      const size_t slot = (size_t)blockIdx.x + g.seg;
+      float2 *ml = g.s >= 0 ? reinterpret_cast<float2 *>(p.ws + w.own_ml_off) + slot * w.own_rows
+                            : reinterpret_cast<float2 *>(p.ws + w.pre_ml_off) + slot * 16;
+      ml[tid] = make_float2(M, S);
+    }
+    named_bar_sync(1, kPgtWarps * 32);
+    i += n;
+  }
+}
+
+// ------------------------------------------------------------------ pass 2: shares
+template <int D>
+__global__ void __launch_bounds__(kPgtThreads, 2)
+    pgt_values(PagedDecode p, PgtPlan w, const __grid_constant__ CUtensorMap vmap, int stages, int stage_rows) {
+  constexpr int NT = D / 8;    // n-tiles of the value product
+  constexpr int TILE = pgt_tile(D), WK = TILE / kPgtWarps, PITCH = pgt_pitch(D);
+  constexpr int LPR = TILE / 4, RPI = 32 / LPR;   // producer lanes per staged row, rows side by side
+  __shared__ PgtLens L;
+  __shared__ PgtRing<D> ring;
+  __shared__ float s_lse[16];
+  __shared__ float s_sum[kPgtWarps][16];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  pdl_launch_dependents();
+  if (tid == 0) ring.init(stages, 33);
+  pgt_load_lens<kPgtThreads>(p, w, L, nullptr);
+  const PgtTiles tt = pgt_tiles(p, w, L);
+  const long long i0 = pgt_first(tt, blockIdx.x), i1 = pgt_first(tt, blockIdx.x + 1);
+  const WaitCtx wc{reinterpret_cast<volatile int *>(&ring.abort_word), p.status};
+  // a stage: the tile, then the logits and the demand of its rows
+  uint8_t *const smem = pgt_smem_base();
+  const uint32_t base = smem_u32(smem);
+  const int side = stage_rows * PITCH;                       // floats
+  const int stage_bytes = (int)round_up(PgtRing<D>::kTileBytes + 2 * side * 4, 1024);
+  float *red = reinterpret_cast<float *>(smem + stages * stage_bytes);   // [stage_rows][D]
+  const float *logits = reinterpret_cast<const float *>(p.ws + w.logit_off);
+  if (warp == kPgtWarps) {   // producer
+    PgtSeg g{};
+    int left = 0;
+    bool waited = false;
+    long long st = 0;
+    for (long long i = i0; i < i1; ++i, ++st) {
+      if (left == 0) {
+        g = pgt_seg(p, w, tt, L, i);
+        left = g.left;
+      }
+      const int slot = (int)(st % stages);
+      if (!warp_wait(&ring.empty[slot], (uint32_t)(((st / stages) & 1) ^ 1), wc)) break;
+      load_tile<D>(p, g, &vmap, base + slot * stage_bytes, &ring.full[slot], lane);
+      if (!waited) {   // the values do not depend on the first pass, the logits do
+        pdl_wait();
+        waited = true;
+      }
+      float *xs = reinterpret_cast<float *>(smem + slot * stage_bytes + PgtRing<D>::kTileBytes), *ds = xs + side;
+      // lane -> 4 keys of row r0, r0 + RPI, ..
+      const int kl = 4 * (lane % LPR), key = g.key0 + kl, r0 = lane / LPR;
+      if (key < g.end) {
+        const int col = key / p.c.page_size, off = key % p.c.page_size;
+        int dpg[16 / RPI];   // the rows' demand pages (one page for all rows of a sequence)
+#pragma unroll
+        for (int i = 0; i < 16 / RPI; ++i) {
+          const int r = r0 + i * RPI;
+          dpg[i] = i > 0 && g.s >= 0 ? dpg[0] : -1;
+          if (r < g.nrows && (i == 0 || g.s < 0)) {
+            int s, hq;
+            g.row(w.G, r, s, hq);
+            if (L.len[s] > 0)
+              dpg[i] = checked_page(p.c.demand_table + (size_t)s * p.c.max_pages + col, p.c.num_demand_pages, p.status);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16 / RPI; ++i) {
+          const int r = r0 + i * RPI;
+          if (r >= g.nrows) break;
+          int s, hq;
+          g.row(w.G, r, s, hq);
+          cp_async16(xs + r * PITCH + kl, logits + ((size_t)s * p.c.Hq + hq) * w.Lp + key);
+          if (dpg[i] >= 0)
+            cp_async16(ds + r * PITCH + kl, p.c.demand_pages + ((size_t)dpg[i] * p.c.Hq + hq) * p.c.page_size + off);
+        }
+      }
+      cp_async_arrive_noinc(&ring.full[slot]);
+      g.key0 += TILE;
+      --left;
+    }
+    if (!waited) pdl_wait();
+    cp_async_wait_all();
+    if (ring.abort_word && lane == 0) drain(ring.full, stages, st);
+    return;
+  }
+  pdl_wait();
+  const int gid = lane / 4, t = lane % 4;
+  for (long long i = i0; i < i1;) {
+    PgtSeg g = pgt_seg(p, w, tt, L, i);
+    const int n = (int)min((long long)g.left, i1 - i);
+    // lse2 of the rows: a warp joins a row's pieces
+    for (int r = warp; r < g.nrows; r += kPgtWarps) {
+      int s, hq;
+      g.row(w.G, r, s, hq);
+      const PgtPieces pc = pgt_pieces(p, w, tt, L, s, hq);
+      const float2 *pre = reinterpret_cast<const float2 *>(p.ws + w.pre_ml_off);
+      const float2 *own = reinterpret_cast<const float2 *>(p.ws + w.own_ml_off);
+      float m = -INFINITY, l = 0.f;
+      for (int c = lane; c < pc.npre + pc.nown; c += 32) {
+        const float2 ml = c < pc.npre ? pre[(size_t)(pc.pre0 + c) * 16 + pc.pre_row]
+                                      : own[(size_t)(pc.own0 + c - pc.npre) * w.own_rows + pc.own_row];
+        const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
+        l = l * ex2_approx(m - ms) + ml.y * ex2_approx(ml.x - ms);
+        m = mn;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+        const float mn = fmaxf(m, m2), ms = mn == -INFINITY ? 0.f : mn;
+        l = l * ex2_approx(m - ms) + l2 * ex2_approx(m2 - ms);
+        m = mn;
+      }
+      if (lane == 0) s_lse[r] = L.len[s] > 0 ? m + log2f(l) : INFINITY;   // an idle slot bids nothing
+    }
+    named_bar_sync(1, kPgtWarps * 32);
+    float lse[2];
+    int rs[2], rh[2];
+    bool on[2];
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const int r = gid + 8 * hh;
+      lse[hh] = r < g.nrows ? s_lse[r] : INFINITY;
+      on[hh] = lse[hh] != INFINITY;
+      rs[hh] = rh[hh] = 0;
+      if (r < g.nrows) g.row(w.G, r, rs[hh], rh[hh]);
+    }
+    float acc[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+    float sum[2] = {0.f, 0.f};
+    // A wait that gave up ends the piece's loop but not the warp, which still
+    // meets the others at the barriers below (its later waits fail at once).
+    for (int k = 0; k < n; ++k) {
+      const long long st = i - i0 + k;
+      const int slot = (int)(st % stages);
+      if (!warp_wait(&ring.full[slot], (uint32_t)((st / stages) & 1), wc)) break;
+      const uint32_t tile = base + slot * stage_bytes;
+      const float *xs = reinterpret_cast<const float *>(smem + slot * stage_bytes + PgtRing<D>::kTileBytes);
+      const float *ds = xs + side;
+      const int key_tile = g.key0 + k * TILE;
+#pragma unroll
+      for (int gg = 0; gg < WK / 16; ++gg) {
+        const int kl = warp * WK + gg * 16;
+        const int valid = g.end - (key_tile + kl);   // keys of the group before the end
+        if (valid <= 0) break;
+        if (valid < 16) {   // rows past the end may hold anything: 0 times NaN is NaN
+          for (int j = lane; j < (16 - valid) * (D / 8); j += 32) {
+            const int row = kl + valid + j / (D / 8);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(tile + tile_off<D>(row, j % (D / 8))), "r"(0u)
+                         : "memory");
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float sh[4] = {0.f, 0.f, 0.f, 0.f};
+          if (on[hh] && 4 * t < valid) {
+            const float4 x = *reinterpret_cast<const float4 *>(xs + (gid + 8 * hh) * PITCH + kl + 4 * t);
+            const float4 d = *reinterpret_cast<const float4 *>(ds + (gid + 8 * hh) * PITCH + kl + 4 * t);
+            const float xe[4] = {x.x, x.y, x.z, x.w}, de[4] = {d.x, d.y, d.z, d.w};
+            float nd[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float bid = ex2_approx(xe[e] - lse[hh]);
+              nd[e] = de[e] + bid;
+              const float den = (p.earlier ? de[e] : nd[e]) + p.eps;
+              sh[e] = 4 * t + e < valid ? bid * rcp_approx(den) : 0.f;
+              sum[hh] += sh[e];
+            }
+            const int key = key_tile + kl + 4 * t;
+            const int dpg =
+                __ldg(p.c.demand_table + (size_t)rs[hh] * p.c.max_pages + key / p.c.page_size);
+            if (dpg >= 0 && dpg < p.c.num_demand_pages) {
+              float *dst = p.c.demand_pages + ((size_t)dpg * p.c.Hq + rh[hh]) * p.c.page_size + key % p.c.page_size;
+              if (4 * t + 4 <= valid) {
+                *reinterpret_cast<float4 *>(dst) = make_float4(nd[0], nd[1], nd[2], nd[3]);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (4 * t + e < valid) dst[e] = nd[e];
+              }
+            }
+          }
+          // columns 2t, 2t + 1 of the first 8 are keys 4t, 4t + 1, of the last 8 keys 4t + 2, 4t + 3
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const float s0 = sh[2 * half], s1 = sh[2 * half + 1];
+            const uint32_t h2 = pack_bf16x2(s0, s1);
+            hi[hh + 2 * half] = h2;
+            lo[hh + 2 * half] =
+                pack_bf16x2(s0 - __uint_as_float(h2 << 16), s1 - __uint_as_float(h2 & 0xffff0000u));
+          }
+        }
+        // lane -> row: matrices (k half 0, n 0-7), (k half 1, n 0-7), (k half 0, n 8-15), (k half 1, n 8-15)
+        const int row = kl + group_key(lane & 7, (lane >> 3) & 1);
+#pragma unroll
+        for (int j = 0; j < NT; j += 2) {
+          uint32_t bfr[4];
+          ldsm_x4_t(tile + tile_off<D>(row, j + (lane >> 4)), bfr);
+          mma16816(acc[j], hi, bfr[0], bfr[1]);
+          mma16816(acc[j + 1], hi, bfr[2], bfr[3]);
+          mma16816(acc[j], lo, bfr[0], bfr[1]);
+          mma16816(acc[j + 1], lo, bfr[2], bfr[3]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring.empty[slot]);
+    }
+    // the piece's numerators and share sums: the warps' parts, added in warp order
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) sum[hh] += __shfl_xor_sync(0xffffffffu, sum[hh], o);
+      if (t == 0) s_sum[warp][gid + 8 * hh] = sum[hh];
+    }
+#pragma unroll 1
+    for (int v = 0; v < kPgtWarps; ++v) {
+      if (warp == v) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          if (gid + 8 * hh >= g.nrows) continue;
+          float *to = red + (gid + 8 * hh) * D + 2 * t;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            float2 a = make_float2(acc[j][2 * hh], acc[j][2 * hh + 1]);
+            if (v > 0) {
+              const float2 b = *reinterpret_cast<const float2 *>(to + 8 * j);
+              a.x += b.x, a.y += b.y;
+            }
+            *reinterpret_cast<float2 *>(to + 8 * j) = a;
+          }
+        }
+      }
+      named_bar_sync(1, kPgtWarps * 32);
+    }
+    const size_t slot = (size_t)blockIdx.x + g.seg;
+    float *part = g.s >= 0 ? reinterpret_cast<float *>(p.ws + w.own_acc_off) + slot * w.own_rows * acc_stride(D)
+                           : reinterpret_cast<float *>(p.ws + w.pre_acc_off) + slot * 16 * acc_stride(D);
+    for (int j = tid; j < g.nrows * D; j += kPgtWarps * 32) {
+      part[j / D * acc_stride(D) + j % D] = red[j];
+    }
+    if (tid < g.nrows) {
+      float a = 0.f;
+#pragma unroll
+      for (int v = 0; v < kPgtWarps; ++v) a += s_sum[v][tid];
+      part[tid * acc_stride(D) + D] = a;
+    }
+    named_bar_sync(1, kPgtWarps * 32);
+    i += n;
+  }
+}
+
+// ------------------------------------------------------------------ join
+constexpr int kPgtCombThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kPgtCombThreads) pgt_combine(PagedDecode p, PgtPlan w) {
+  constexpr int WAYS = kPgtCombThreads / D;
+  __shared__ PgtLens L;
+  __shared__ float s_a[WAYS][D], s_r[WAYS];
+  const int tid = threadIdx.x, e = tid % D, way = tid / D;
+  pgt_load_lens<kPgtCombThreads>(p, w, L, nullptr);
+  const PgtTiles tt = pgt_tiles(p, w, L);
+  pdl_wait();
+  const int s = blockIdx.x / p.c.Hq, hq = blockIdx.x % p.c.Hq;
+  const PgtPieces pc = pgt_pieces(p, w, tt, L, s, hq);
+  const float *pre = reinterpret_cast<const float *>(p.ws + w.pre_acc_off) + pc.pre_row * acc_stride(D);
+  const float *own = reinterpret_cast<const float *>(p.ws + w.own_acc_off) + pc.own_row * acc_stride(D);
+  float a = 0.f, rs = 0.f;
+  for (int c = way; c < pc.npre + pc.nown; c += WAYS) {
+    const float *pa = c < pc.npre ? pre + (size_t)(pc.pre0 + c) * 16 * acc_stride(D)
+                                  : own + (size_t)(pc.own0 + c - pc.npre) * w.own_rows * acc_stride(D);
+    a += pa[e];
+    rs += pa[D];
+  }
+  s_a[way][e] = a;
+  if (e == 0) s_r[way] = rs;
+  __syncthreads();
+  if (way == 0) {
+    for (int v = 1; v < WAYS; ++v) {
+      a += s_a[v][e];
+      rs += s_r[v];
+    }
+    static_cast<__nv_bfloat16 *>(p.out)[(size_t)blockIdx.x * D + e] =
+        __float2bfloat16_rn(L.len[s] > 0 ? a / rs : 0.f);
+  }
+}
+
+// ------------------------------------------------------------------ host
+bool make_page_map(CUtensorMap *m, const void *base, int64_t num, int page_size, int rows, int d);   // fwd_bf16.cu
+
+template <typename... KArgs, typename... Args>
+static cudaError_t launch_after(void (*kernel)(KArgs...), int grid, int threads, int smem, cudaStream_t stream,
+                                Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+constexpr int kPgtSmemPerCta = 100 * 1024;   // two CTAs an SM beside their static shared memory
+
+template <int D>
+static int launch_pgt_t(const PagedDecode &p, cudaStream_t stream) {
+  using R = PgtRing<D>;
+  static PerDeviceOnce once;
+  const int prep = once.run([] {
+    return (cudaFuncSetAttribute(pgt_keys<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgtSmemPerCta) !=
+                cudaSuccess ||
+            cudaFuncSetAttribute(pgt_values<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgtSmemPerCta) !=
+                cudaSuccess)
+               ? DA_ERR_CUDA
+               : DA_OK;
+  });
+  if (prep != DA_OK) return prep;
+  const PgtPlan w = pgt_plan(p.c.S, p.c.Hq, p.c.Hkv, D, p.max_len, p.prefix_len);
+  CUtensorMap km, vm;
+  const int64_t num = (int64_t)p.c.num_pages * p.c.Hkv;
+  // an empty pool has no pages to map; every page id then fails its check, and no copy is issued
+  if (!make_page_map(&km, p.c.k_pages, num > 0 ? num : 1, p.c.page_size, R::kTile, D) ||
+      !make_page_map(&vm, p.c.v_pages, num > 0 ? num : 1, p.c.page_size, R::kTile, D))
+    return DA_ERR_CUDA;
+  constexpr int k_stages = (kPgtSmemPerCta - 1024) / R::kTileBytes;
+  static_assert(k_stages <= 8, "the ring's barriers");
+  pgt_keys<D><<<w.ctas, kPgtThreads, 1024 + k_stages * R::kTileBytes, stream>>>(p, w, km, k_stages);
+  const int rows = w.prefix_segs > 0 ? 16 : w.own_rows;
+  const int stage = (int)round_up(R::kTileBytes + 2 * rows * pgt_pitch(D) * 4, 1024);
+  const int red = rows * D * 4;
+  int v_stages = (kPgtSmemPerCta - 1024 - red) / stage;
+  if (v_stages > 8) v_stages = 8;
+  if (launch_after(pgt_values<D>, w.ctas, kPgtThreads, 1024 + v_stages * stage + red, stream, p, w, vm, v_stages, rows) !=
+      cudaSuccess)
+    return DA_ERR_CUDA;
+  if (launch_after(pgt_combine<D>, p.c.S * p.c.Hq, kPgtCombThreads, 0, stream, p, w) != cudaSuccess)
+    return DA_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+int launch_paged_decode_bf16(const PagedDecode &p, cudaStream_t stream) {
+  return p.c.d == 128 ? launch_pgt_t<128>(p, stream) : launch_pgt_t<64>(p, stream);
+}
+
+}  // namespace da
