@@ -452,58 +452,98 @@ def rope_spec(inv_freq, pair_axis=None, n_axes: int = 1, adjacent: bool = False)
     return RopeSpec(inv_freq, pair_axis, int(n_axes), bool(adjacent))
 
 
-def _need_rows(t, name, shape, dtype):
-    """A CUDA tensor whose last dimension is contiguous; other strides are free."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device} but the current device is cuda:{torch.cuda.current_device()}; "
-                         f"call inside torch.cuda.device({t.device})")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if shape[-1] > 1 and t.stride(-1) != 1:
+# The calls of a serving loop are short (a few microseconds on the GPU), so their
+# checks are written for the case that passes: one condition per tensor, the
+# device and the stream read once, strides kept as C arrays by their values.
+def _fit(t, name, shape, dtype, dev):
+    """_need for a contiguous tensor on device ``dev`` (the current one)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape
+            and t.is_contiguous()):
+        _need(t, name, tuple(shape), dtype)
+
+
+def _fit_rows(t, name, shape, dtype, dev):
+    """The same for a tensor whose last dimension alone is contiguous; returns its strides."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape):
+        _need_any_strides(t, name, tuple(shape), dtype)
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
+    return st
 
 
-def _strides(t, n):
-    """The first n strides as a C array."""
-    return None if t is None else (ctypes.c_int64 * n)(*t.stride()[:n])
+def _need_any_strides(t, name, shape, dtype):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index == torch.cuda.current_device():
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    _need(t, name)
+
+
+_stride_arrays: dict = {}
+
+
+def _c_strides(st, n):
+    """The first n of a tensor's strides as a C array."""
+    key = st[:n]
+    got = _stride_arrays.get(key)
+    if got is None:
+        if len(_stride_arrays) >= 4096:
+            _stride_arrays.clear()
+        got = _stride_arrays[key] = (ctypes.c_int64 * n)(*key)
+    return got
+
+
+def _current_device() -> int:
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
+
+
+def _stream_id(stream, dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+_CODES = {torch.float32: DA_F32, torch.bfloat16: DA_BF16}
 
 
 def _rope_call(name, q, k, positions, rope, q_out, k_out, stream, check):
-    lib = load()
+    lib = _lib or load()
     if not isinstance(rope, RopeSpec):
         raise TypeError("rope must be a RopeSpec (see rope_spec)")
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a [B, H, T, d] tensor")
-    B, Hq, T, d = q.shape
-    _need_rows(q, "q", q.shape, q.dtype)
-    dt, Hk = _dtype_code(q), 0
+    shape, dtype = q.shape, q.dtype
+    B, Hq, T, d = shape
+    dt = _CODES[dtype] if dtype in _CODES else _dtype_code(q)
+    dev = _current_device()
+    sq = _c_strides(_fit_rows(q, "q", shape, dtype, dev), 3)
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=dtype, device=q.device)
+        so = None
+    else:
+        so = _c_strides(_fit_rows(q_out, "q_out", shape, dtype, dev), 3)
     if k is not None:
         Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
-        _need_rows(k, "k", (B, Hk, T, d), q.dtype)
+        kshape = (B, Hk, T, d)
+        sk, kp = _c_strides(_fit_rows(k, "k", kshape, dtype, dev), 3), k.data_ptr()
+        if k_out is None:
+            k_out = torch.empty(kshape, dtype=dtype, device=q.device)
+            sko = None
+        else:
+            sko = _c_strides(_fit_rows(k_out, "k_out", kshape, dtype, dev), 3)
+        kop = k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _need(positions, "positions", None, torch.int32)
-    if positions.dim() == 2:
-        positions = positions.unsqueeze(1)
-    if positions.dim() != 3 or positions.shape[0] != rope.n_axes or positions.shape[1] not in (1, B) or \
-            positions.shape[2] != T:
-        raise ValueError(f"positions has shape {tuple(positions.shape)}, expected ({rope.n_axes}, [1 or {B},] {T})")
-    _need(rope.inv_freq, "inv_freq")
-    q_out = torch.empty((B, Hq, T, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
-    _need_rows(q_out, "q_out", q.shape, q.dtype)
-    if k is not None:
-        k_out = torch.empty((B, Hk, T, d), dtype=q.dtype, device=q.device) if k_out is None else k_out
-        _need_rows(k_out, "k_out", k.shape, q.dtype)
-    st = getattr(lib, name)(_ptr(q), _strides(q, 3), _ptr(k), _strides(k, 3), _ptr(q_out), _strides(q_out, 3),
-                            _ptr(k_out), _strides(k_out, 3), _ptr(positions), positions.shape[1], rope._ref, B, Hq, Hk,
-                            T, d, dt, _stream_handle(stream))
-    if check:
+    else:
+        Hk, sk, kp, sko, kop = 0, None, None, None, None
+    _fit(positions, "positions", positions.shape if isinstance(positions, torch.Tensor) else (), torch.int32, dev)
+    ps = positions.shape
+    pb = 1 if len(ps) == 2 else ps[1] if len(ps) == 3 else -1
+    if pb not in (1, B) or ps[0] != rope.n_axes or ps[-1] != T:
+        raise ValueError(f"positions has shape {tuple(ps)}, expected ({rope.n_axes}, [1 or {B},] {T})")
+    _fit(rope.inv_freq, "inv_freq", (rope.n_pairs,), torch.float32, dev)
+    st = getattr(lib, name)(q.data_ptr(), sq, kp, sk, q_out.data_ptr(), so, kop, sko, positions.data_ptr(), pb,
+                            rope._ref, B, Hq, Hk, T, d, dt, _stream_id(stream, dev))
+    if check and st != DA_OK:
         _check(st, name)
     return q_out, k_out
 
@@ -568,12 +608,15 @@ class PagedCache:
         self._ref = ctypes.byref(self._c)
 
 
-def _need_cache(cache):
+def _need_cache(cache) -> int:
+    """The cache's device, which has to be the current one."""
     if not isinstance(cache, PagedCache):
         raise TypeError("cache must be a PagedCache")
-    if cache.device.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {cache.device} but the current device is "
-                         f"cuda:{torch.cuda.current_device()}; call inside torch.cuda.device({cache.device})")
+    dev = _current_device()
+    if cache.device.index != dev:
+        raise ValueError(f"the cache is on {cache.device} but the current device is cuda:{dev}; "
+                         f"call inside torch.cuda.device({cache.device})")
+    return dev
 
 
 def dilution_attn_paged_append_workspace_size() -> int:
@@ -594,37 +637,46 @@ def dilution_attn_paged_append(q, k, v, cache, cu_tokens, q_out=None, *, rope=No
     sequence.  ``demand`` [N, Hq] fp32: the keys' totals (a prompt's
     demand_out after prefill), 0 when omitted.  q [N, Hq, d] (or None) turns
     likewise into ``q_out`` (contiguous), which is returned."""
-    lib = load()
-    _need_cache(cache)
-    Hq, Hkv, d = cache.Hq, cache.Hkv, cache.d
+    lib = _lib or load()
+    dev = _need_cache(cache)
+    Hq, Hkv, d, dtype = cache.Hq, cache.Hkv, cache.d, cache.dtype
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be [N, Hkv, d]")
     N = k.shape[0]
-    _need_rows(k, "k", (N, Hkv, d), cache.dtype)
-    _need_rows(v, "v", (N, Hkv, d), cache.dtype)
-    _need(cu_tokens, "cu_tokens", (cache.S + 1,), torch.int32)
+    kvshape = (N, Hkv, d)
+    sk = _c_strides(_fit_rows(k, "k", kvshape, dtype, dev), 2)
+    sv = _c_strides(_fit_rows(v, "v", kvshape, dtype, dev), 2)
+    _fit(cu_tokens, "cu_tokens", (cache.S + 1,), torch.int32, dev)
+    qp = sq = qop = dp = sd = None
     if q is not None:
-        _need_rows(q, "q", (N, Hq, d), cache.dtype)
-        q_out = torch.empty((N, Hq, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
-        _need(q_out, "q_out", (N, Hq, d), q.dtype)
+        qshape = (N, Hq, d)
+        sq, qp = _c_strides(_fit_rows(q, "q", qshape, dtype, dev), 2), q.data_ptr()
+        if q_out is None:
+            q_out = torch.empty(qshape, dtype=dtype, device=cache.device)
+        else:
+            _fit(q_out, "q_out", qshape, dtype, dev)
+        qop = q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if rope is not None and not isinstance(rope, RopeSpec):
-        raise TypeError("rope must be a RopeSpec (see rope_spec)")
     if rope is not None:
-        _need(rope.inv_freq, "inv_freq")
+        if not isinstance(rope, RopeSpec):
+            raise TypeError("rope must be a RopeSpec (see rope_spec)")
+        _fit(rope.inv_freq, "inv_freq", (rope.n_pairs,), torch.float32, dev)
     if positions is not None:
-        _need(positions, "positions", (1 if rope is None else rope.n_axes, N), torch.int32)
+        _fit(positions, "positions", (1 if rope is None else rope.n_axes, N), torch.int32, dev)
     if demand is not None:
-        _need_rows(demand.unsqueeze(-1), "demand", (N, Hq, 1), torch.float32)
+        if not (isinstance(demand, torch.Tensor) and demand.dtype is torch.float32 and demand.get_device() == dev
+                and demand.shape == (N, Hq)):
+            _need_any_strides(demand, "demand", (N, Hq), torch.float32)
+        dp, sd = demand.data_ptr(), _c_strides(demand.stride(), 2)
     if workspace is None:
         workspace = dilution_attn_paged_append_workspace(cache)
-    _need(workspace, "workspace", None, torch.uint8)
-    st = lib.dilution_attn_paged_append(_ptr(q), _strides(q, 2), _ptr(k), _strides(k, 2), _ptr(v), _strides(v, 2),
-                                        _ptr(demand), _strides(demand, 2), _ptr(q_out), _ptr(cu_tokens), N, cache._ref,
-                                        None if rope is None else rope._ref, _ptr(positions), _ptr(workspace),
-                                        workspace.numel(), _stream_handle(stream))
-    if check:
+    _fit(workspace, "workspace", workspace.shape if isinstance(workspace, torch.Tensor) else (), torch.uint8, dev)
+    st = lib.dilution_attn_paged_append(qp, sq, k.data_ptr(), sk, v.data_ptr(), sv, dp, sd, qop, cu_tokens.data_ptr(), N,
+                                        cache._ref, None if rope is None else rope._ref,
+                                        None if positions is None else positions.data_ptr(), workspace.data_ptr(),
+                                        workspace.numel(), _stream_id(stream, dev))
+    if check and st != DA_OK:
         _check(st, "dilution_attn_paged_append")
     return q_out
 
@@ -656,23 +708,26 @@ def dilution_attn_paged_decode(q, cache, max_len: int, out=None, *, prefix_table
     ``prefix_table`` (int32 [n]): pages of the tokens that every sequence
     shares, read once for the batch.  Bad lengths or page ids are found on the
     device: read them with dilution_attn_get_error on ``workspace``."""
-    lib = load()
-    _need_cache(cache)
-    _need(q, "q", (cache.S, cache.Hq, cache.d), cache.dtype)
+    lib = _lib or load()
+    dev = _need_cache(cache)
+    shape, dtype = (cache.S, cache.Hq, cache.d), cache.dtype
+    _fit(q, "q", shape, dtype, dev)
     if out is None:
-        out = torch.empty_like(q)
-    _need(out, "out", q.shape, q.dtype)
-    n_prefix = 0
+        out = torch.empty(shape, dtype=dtype, device=cache.device)
+    else:
+        _fit(out, "out", shape, dtype, dev)
+    n_prefix, pt = 0, None
     if prefix_table is not None:
-        _need(prefix_table, "prefix_table", None, torch.int32)
-        n_prefix = prefix_table.numel()
+        n_prefix = prefix_table.numel() if isinstance(prefix_table, torch.Tensor) else 0
+        _fit(prefix_table, "prefix_table", (n_prefix,), torch.int32, dev)
+        pt = prefix_table.data_ptr()
     if workspace is None:
         workspace = dilution_attn_paged_decode_workspace(cache, max_len, n_prefix)
-    _need(workspace, "workspace", None, torch.uint8)
-    st = lib.dilution_attn_paged_decode(_ptr(q), cache._ref, _ptr(prefix_table), n_prefix, int(max_len), _ptr(out),
+    _fit(workspace, "workspace", workspace.shape if isinstance(workspace, torch.Tensor) else (), torch.uint8, dev)
+    st = lib.dilution_attn_paged_decode(q.data_ptr(), cache._ref, pt, n_prefix, int(max_len), out.data_ptr(),
                                         float(tau), _tau_bh_ptr(tau_bh, cache.S, cache.Hq), float(eps), int(flags),
-                                        _ptr(workspace), workspace.numel(), _stream_handle(stream))
-    if check:
+                                        workspace.data_ptr(), workspace.numel(), _stream_id(stream, dev))
+    if check and st != DA_OK:
         _check(st, "dilution_attn_paged_decode")
     return out
 

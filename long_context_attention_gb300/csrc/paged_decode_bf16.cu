@@ -12,9 +12,8 @@
 // What bounds it: HBM.  K and V are read once, D is read and written once, the
 // logits stay mostly in L2.  So the layout serves the copies: whole pages (or
 // a tile's rows of one) arrive by TMA with a 128-byte swizzle into a ring of stages
-// of 16 KB (128 keys at d = 64, 64 at d = 128) that one producer warp fills; in pgt_values the same warp brings
-// the logits and the demand by 16-byte asynchronous copies, so that everything
-// a stage needs is in flight together.
+// of 16 KB (128 keys at d = 64, 64 at d = 128) that one producer warp fills, and
+// in pgt_values every thread keeps its logits and demand in flight two tiles ahead.
 //
 // Tensor cores: m16n8k16 (bf16, fp32 sums).  A decode step has few query rows
 // per key head, so the tensor rate is not what bounds it; the M = 16 rows are
@@ -40,21 +39,26 @@
 
 namespace da {
 
-constexpr int kPgtWarps = 4;                      // consumer warps
-constexpr int kPgtThreads = kPgtWarps * 32 + 32;  // and the producer warp
 constexpr int kPgtMaxSeqs = 1024;                 // lengths kept in shared memory
 DA_HD constexpr int pgt_tile(int d) { return d == 64 ? 128 : 64; }   // keys per stage (16 KB of K or V)
-DA_HD constexpr int pgt_pitch(int d) { return pgt_tile(d) + 4; }     // floats per staged row (no bank conflicts)
+DA_HD constexpr int pgt_warps(int d) { return pgt_tile(d) / 16; }    // consumer warps: 16 keys of a stage each
+DA_HD constexpr int pgt_threads(int d) { return 32 * pgt_warps(d) + 32; }   // and the producer warp
+constexpr int kPgtAhead = 3;                      // tiles whose logits and demand are in flight or in use
 constexpr int kPgtMaxCtas = 2 * 152;              // two resident CTAs on each SM
+
+// pgt_values: bytes of the logits and demand in flight for `rows` rows.
+DA_HD int pgt_side_bytes(int d, int rows) { return kPgtAhead * pgt_warps(d) * rows * 128; }
 
 // Host plan of a call; slots and scratch offsets.
 struct PgtPlan {
-  int ctas, tile, G, own_rows, own_groups, prefix_groups, prefix_tiles, own_segs, prefix_segs, Lp;
+  int ctas, tile, page_shift, G, own_rows, own_groups, prefix_groups, prefix_tiles, own_segs, prefix_segs, Lp;
   size_t logit_off, own_ml_off, own_acc_off, pre_ml_off, pre_acc_off, total;
 };
 
-static PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_len) {
+static PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int page_size = 16) {
   PgtPlan w;
+  w.page_shift = 0;
+  while ((1 << w.page_shift) < page_size) ++w.page_shift;
   w.G = Hq / Hkv;
   w.own_rows = w.G < 16 ? w.G : 16;
   w.own_groups = (w.G + 15) / 16;
@@ -270,10 +274,10 @@ struct PgtRing {
   static constexpr int kTileBytes = kTile * D * 2;
   uint64_t full[8], empty[8];
   int abort_word;
-  __device__ __forceinline__ void init(int stages, int full_count) {
+  __device__ __forceinline__ void init(int stages) {
     for (int i = 0; i < stages; ++i) {
-      mbar_init(&full[i], full_count);
-      mbar_init(&empty[i], kPgtWarps);
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], pgt_warps(D));
     }
     abort_word = 0;
     fence_mbar_init();
@@ -290,30 +294,6 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, u
       : "memory");
 }
 
-// Producer warp: the pages behind keys [key0, min(key0 + tile, end)) of one
-// segment into a stage; lane i brings page piece i.  `arrive` adds the stage's
-// expected bytes (lane 0 arrives once).
-template <int D>
-__device__ __forceinline__ void load_tile(const PagedDecode &p, const PgtSeg &g, const CUtensorMap *map, uint32_t dst,
-                                          uint64_t *full, int lane) {
-  constexpr int TILE = pgt_tile(D);
-  const int ps = p.c.page_size, rows = min(ps, TILE);
-  const int pieces = (min(TILE, g.end - g.key0) + rows - 1) / rows;
-  int page = -1, key = g.key0 + lane * rows;
-  if (lane < pieces) {
-    const int32_t *e = g.s >= 0 ? p.c.page_table + (size_t)g.s * p.c.max_pages + key / ps : p.prefix_table + key / ps;
-    page = checked_page(e, p.c.num_pages, p.status);
-  }
-  const int n = __popc(__ballot_sync(0xffffffffu, page >= 0));
-  if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)(n * rows * D * 2));
-  __syncwarp();
-  if (page >= 0) {
-#pragma unroll
-    for (int x = 0; x < D; x += 64)
-      tma_page(dst + (x / 64) * TILE * 128 + lane * rows * 128, map, full, x, key % ps, page * p.c.Hkv + g.hkv);
-  }
-}
-
 // Let the copies in flight land before the CTA exits after a timeout.
 __device__ __forceinline__ void drain(uint64_t *full, int stages, long long issued) {
   for (long long st = issued > stages ? issued - stages : 0; st < issued; ++st) {
@@ -323,56 +303,95 @@ __device__ __forceinline__ void drain(uint64_t *full, int stages, long long issu
   }
 }
 
+// Producer warp: fills the ring with the CTA's tiles i0 .. i1 - 1 of K or V.
+// Lane i brings page piece i of a tile.  One warp issues about one dependent
+// instruction every 5 cycles, and a tile has 0.7 us at HBM rate, so the loop is
+// short: no divisions, one table entry per lane, fetched a tile ahead.
+template <int D>
+__device__ void produce(const PagedDecode &p, const PgtPlan &w, const PgtTiles &tt, const PgtLens &L, PgtRing<D> &ring,
+                        const CUtensorMap *map, uint32_t base, int stages, long long i0, long long i1,
+                        const WaitCtx &wc) {
+  constexpr int TILE = pgt_tile(D);
+  const int lane = threadIdx.x % 32, sh = w.page_shift, ps = 1 << sh;
+  const int rows = min(ps, TILE), rsh = min(sh, D == 64 ? 7 : 6);
+  int slot = 0;
+  uint32_t parity = 1;
+  long long st = 0;
+  for (long long i = i0; i < i1;) {
+    const PgtSeg g = pgt_seg(p, w, tt, L, i);
+    const int n = (int)min((long long)g.left, i1 - i);
+    const int32_t *table = g.s >= 0 ? p.c.page_table + (size_t)g.s * p.c.max_pages : p.prefix_table;
+    int key = g.key0 + lane * rows;                                   // this lane's piece
+    const int limit = lane * rows < TILE ? g.end : 0;                 // lanes past the tile bring nothing
+    int page = key < limit ? __ldg(table + (key >> sh)) : -1;
+    for (int k = 0; k < n; ++k, ++st) {
+      const int ahead = k + 1 < n && key + TILE < limit ? __ldg(table + ((key + TILE) >> sh)) : -1;
+      if (!warp_wait(&ring.empty[slot], parity, wc)) goto out;
+      const bool ok = (unsigned)page < (unsigned)p.c.num_pages;
+      const uint32_t have = __ballot_sync(0xffffffffu, ok);
+      if (!ok && key < limit) atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
+      if (lane == 0) mbar_arrive_expect_tx(&ring.full[slot], (uint32_t)(__popc(have) << rsh) * (D * 2));
+      __syncwarp();
+      if (ok) {
+        const uint32_t dst = base + slot * PgtRing<D>::kTileBytes + lane * rows * 128;
+#pragma unroll
+        for (int x = 0; x < D; x += 64)
+          tma_page(dst + (x / 64) * TILE * 128, map, &ring.full[slot], x, key & (ps - 1), page * p.c.Hkv + g.hkv);
+      }
+      page = ahead;
+      key += TILE;
+      if (++slot == stages) {
+        slot = 0;
+        parity ^= 1;
+      }
+    }
+    i += n;
+  }
+out:
+  if (ring.abort_word && lane == 0) drain(ring.full, stages, st);
+}
+
 extern __shared__ __align__(1024) uint8_t pgt_smem_raw[];
 __device__ __forceinline__ uint8_t *pgt_smem_base() {   // the swizzle counts from 1024-byte boundaries
   return pgt_smem_raw + ((1024u - (smem_u32(pgt_smem_raw) & 1023u)) & 1023u);
 }
 
 // ------------------------------------------------------------------ pass 1: logits
-template <int D>
-__global__ void __launch_bounds__(kPgtThreads, 2)
+// HH: halves of 8 rows in use (1 for up to 8 rows).
+template <int D, int HH>
+__global__ void __launch_bounds__(pgt_threads(D), 2)
     pgt_keys(PagedDecode p, PgtPlan w, const __grid_constant__ CUtensorMap kmap, int stages) {
   constexpr int KS = D / 16;   // k-steps
-  constexpr int TILE = pgt_tile(D), WK = TILE / kPgtWarps;   // a warp's keys of a tile
+  constexpr int TILE = pgt_tile(D), WARPS = pgt_warps(D);
   __shared__ PgtLens L;
   __shared__ PgtRing<D> ring;
-  __shared__ float2 s_ml[kPgtWarps][16];
+  __shared__ float2 s_ml[WARPS][16];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   pdl_launch_dependents();
-  if (tid == 0) ring.init(stages, 1);
-  pgt_load_lens<kPgtThreads>(p, w, L, blockIdx.x == 0 ? p.status : nullptr);
+  if (tid == 0) ring.init(stages);
+  pgt_load_lens<pgt_threads(D)>(p, w, L, blockIdx.x == 0 ? p.status : nullptr);
   const PgtTiles tt = pgt_tiles(p, w, L);
   const long long i0 = pgt_first(tt, blockIdx.x), i1 = pgt_first(tt, blockIdx.x + 1);
   const WaitCtx wc{reinterpret_cast<volatile int *>(&ring.abort_word), p.status};
   const uint32_t base = smem_u32(pgt_smem_base());
-  if (warp == kPgtWarps) {   // producer
-    PgtSeg g{};
-    int left = 0;
-    long long st = 0;
-    for (long long i = i0; i < i1; ++i, ++st) {
-      if (left == 0) {
-        g = pgt_seg(p, w, tt, L, i);
-        left = g.left;
-      }
-      const int slot = (int)(st % stages);
-      if (!warp_wait(&ring.empty[slot], (uint32_t)(((st / stages) & 1) ^ 1), wc)) break;
-      load_tile<D>(p, g, &kmap, base + slot * PgtRing<D>::kTileBytes, &ring.full[slot], lane);
-      g.key0 += TILE;
-      --left;
-    }
-    if (ring.abort_word && lane == 0) drain(ring.full, stages, st);
+  if (warp == WARPS) {
+    produce<D>(p, w, tt, L, ring, &kmap, base, stages, i0, i1, wc);
     return;
   }
   const int gid = lane / 4, t = lane % 4;
+  // lane -> the row it addresses: matrices (half 0, k 0-7), (half 0, k 8-15), (half 1, ..), (half 1, ..)
+  const int row = warp * 16 + group_key(lane & 7, lane >> 4);
+  int slot = 0;
+  uint32_t parity = 0;
   for (long long i = i0; i < i1;) {
     PgtSeg g = pgt_seg(p, w, tt, L, i);
     const int n = (int)min((long long)g.left, i1 - i);
     // Q rows as the A operand; rows past the segment's are 0
-    uint32_t qa[KS][4];
-    float c2[2] = {0.f, 0.f};
-    float *xrow[2] = {nullptr, nullptr};
+    uint32_t qa[KS][4] = {};
+    float c2[HH] = {};
+    float *xrow[HH] = {};
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
+    for (int hh = 0; hh < HH; ++hh) {
       const int r = gid + 8 * hh;
       const bool ok = r < g.nrows;
       int s = 0, hq = 0;
@@ -389,22 +408,18 @@ __global__ void __launch_bounds__(kPgtThreads, 2)
         qa[ks][2 + hh] = ok ? __ldg(qr + ks * 8 + 4 + t) : 0u;
       }
     }
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float m[HH], l[HH];
+#pragma unroll
+    for (int hh = 0; hh < HH; ++hh) m[hh] = -INFINITY, l[hh] = 0.f;
+    const int first = g.key0 + warp * 16;   // this warp's 16 keys of the first tile
     // A wait that gave up ends the piece's loop but not the warp, which still
     // meets the others at the barriers below (its later waits fail at once).
     for (int k = 0; k < n; ++k) {
-      const long long st = i - i0 + k;
-      const int slot = (int)(st % stages);
-      if (!warp_wait(&ring.full[slot], (uint32_t)((st / stages) & 1), wc)) break;
+      if (!warp_wait(&ring.full[slot], parity, wc)) break;
       const uint32_t tile = base + slot * PgtRing<D>::kTileBytes;
-      const int key_tile = g.key0 + k * TILE;
-#pragma unroll
-      for (int gg = 0; gg < WK / 16; ++gg) {
-        const int kl = warp * WK + gg * 16;          // the group's first key in the tile
-        if (key_tile + kl >= g.end) break;
+      const int kg = first + k * TILE;
+      if (kg < g.end) {
         float acc[2][4] = {};
-        // lane -> the row it addresses: matrices (half 0, k 0-7), (half 0, k 8-15), (half 1, ..), (half 1, ..)
-        const int row = kl + group_key(lane & 7, lane >> 4);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           uint32_t bfr[4];
@@ -412,16 +427,18 @@ __global__ void __launch_bounds__(kPgtThreads, 2)
           mma16816(acc[0], qa[ks], bfr[0], bfr[1]);
           mma16816(acc[1], qa[ks], bfr[2], bfr[3]);
         }
-        const int key = key_tile + kl + 4 * t;
+        const int key = kg + 4 * t;
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
+        for (int hh = 0; hh < HH; ++hh) {
           if (gid + 8 * hh >= g.nrows) continue;
           float x[4] = {acc[0][2 * hh] * c2[hh], acc[0][2 * hh + 1] * c2[hh], acc[1][2 * hh] * c2[hh],
                         acc[1][2 * hh + 1] * c2[hh]};
           *reinterpret_cast<float4 *>(xrow[hh] + key) = make_float4(x[0], x[1], x[2], x[3]);
+          if (kg + 16 > g.end) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (key + e >= g.end) x[e] = -INFINITY;
+            for (int e = 0; e < 4; ++e)
+              if (key + e >= g.end) x[e] = -INFINITY;
+          }
           const float mn = fmaxf(m[hh], fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
           const float ms = mn == -INFINITY ? 0.f : mn;
           l[hh] = l[hh] * ex2_approx(m[hh] - ms) + (ex2_approx(x[0] - ms) + ex2_approx(x[1] - ms)) +
@@ -431,10 +448,14 @@ __global__ void __launch_bounds__(kPgtThreads, 2)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.empty[slot]);
+      if (++slot == stages) {
+        slot = 0;
+        parity ^= 1;
+      }
     }
     // the piece's (max, sum) of each row: over the quad, then over the warps
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
+    for (int hh = 0; hh < HH; ++hh) {
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) {
         const float m2 = __shfl_xor_sync(0xffffffffu, m[hh], o), l2 = __shfl_xor_sync(0xffffffffu, l[hh], o);
@@ -444,110 +465,116 @@ __global__ void __launch_bounds__(kPgtThreads, 2)
       }
       if (t == 0) s_ml[warp][gid + 8 * hh] = make_float2(m[hh], l[hh]);
     }
-    named_bar_sync(1, kPgtWarps * 32);
+    named_bar_sync(1, WARPS * 32);
     if (tid < g.nrows) {
       float M = -INFINITY, S = 0.f;
 #pragma unroll
-      for (int v = 0; v < kPgtWarps; ++v) M = fmaxf(M, s_ml[v][tid].x);
+      for (int v = 0; v < WARPS; ++v) M = fmaxf(M, s_ml[v][tid].x);
       const float ms = M == -INFINITY ? 0.f : M;
 #pragma unroll
-      for (int v = 0; v < kPgtWarps; ++v) S += s_ml[v][tid].y * ex2_approx(s_ml[v][tid].x - ms);
-      const size_t slot = (size_t)blockIdx.x + g.seg;
-      float2 *ml = g.s >= 0 ? reinterpret_cast<float2 *>(p.ws + w.own_ml_off) + slot * w.own_rows
-                            : reinterpret_cast<float2 *>(p.ws + w.pre_ml_off) + slot * 16;
+      for (int v = 0; v < WARPS; ++v) S += s_ml[v][tid].y * ex2_approx(s_ml[v][tid].x - ms);
+      const size_t at = (size_t)blockIdx.x + g.seg;
+      float2 *ml = g.s >= 0 ? reinterpret_cast<float2 *>(p.ws + w.own_ml_off) + at * w.own_rows
+                            : reinterpret_cast<float2 *>(p.ws + w.pre_ml_off) + at * 16;
       ml[tid] = make_float2(M, S);
     }
-    named_bar_sync(1, kPgtWarps * 32);
+    named_bar_sync(1, WARPS * 32);
     i += n;
   }
 }
 
 // ------------------------------------------------------------------ pass 2: shares
-template <int D>
-__global__ void __launch_bounds__(kPgtThreads, 2)
-    pgt_values(PagedDecode p, PgtPlan w, const __grid_constant__ CUtensorMap vmap, int stages, int stage_rows) {
+// Each thread brings the logits and demand of its own (row, 4 keys) itself, by
+// 16-byte asynchronous copies kPgtAhead - 1 tiles ahead into its own place in
+// shared memory: nothing to hand over between warps, and no registers held by
+// bytes in flight.
+template <int D, int HH>
+__global__ void __launch_bounds__(pgt_threads(D), 2)
+    pgt_values(PagedDecode p, PgtPlan w, const __grid_constant__ CUtensorMap vmap, int stages, int max_rows) {
   constexpr int NT = D / 8;    // n-tiles of the value product
-  constexpr int TILE = pgt_tile(D), WK = TILE / kPgtWarps, PITCH = pgt_pitch(D);
-  constexpr int LPR = TILE / 4, RPI = 32 / LPR;   // producer lanes per staged row, rows side by side
+  constexpr int TILE = pgt_tile(D), WARPS = pgt_warps(D);
   __shared__ PgtLens L;
   __shared__ PgtRing<D> ring;
   __shared__ float s_lse[16];
-  __shared__ float s_sum[kPgtWarps][16];
+  __shared__ float s_sum[WARPS][16];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   pdl_launch_dependents();
-  if (tid == 0) ring.init(stages, 33);
-  pgt_load_lens<kPgtThreads>(p, w, L, nullptr);
+  if (tid == 0) ring.init(stages);
+  pgt_load_lens<pgt_threads(D)>(p, w, L, nullptr);
   const PgtTiles tt = pgt_tiles(p, w, L);
   const long long i0 = pgt_first(tt, blockIdx.x), i1 = pgt_first(tt, blockIdx.x + 1);
   const WaitCtx wc{reinterpret_cast<volatile int *>(&ring.abort_word), p.status};
-  // a stage: the tile, then the logits and the demand of its rows
   uint8_t *const smem = pgt_smem_base();
   const uint32_t base = smem_u32(smem);
-  const int side = stage_rows * PITCH;                       // floats
-  const int stage_bytes = (int)round_up(PgtRing<D>::kTileBytes + 2 * side * 4, 1024);
-  float *red = reinterpret_cast<float *>(smem + stages * stage_bytes);   // [stage_rows][D]
-  const float *logits = reinterpret_cast<const float *>(p.ws + w.logit_off);
-  if (warp == kPgtWarps) {   // producer
-    PgtSeg g{};
-    int left = 0;
-    bool waited = false;
-    long long st = 0;
-    for (long long i = i0; i < i1; ++i, ++st) {
-      if (left == 0) {
-        g = pgt_seg(p, w, tt, L, i);
-        left = g.left;
-      }
-      const int slot = (int)(st % stages);
-      if (!warp_wait(&ring.empty[slot], (uint32_t)(((st / stages) & 1) ^ 1), wc)) break;
-      load_tile<D>(p, g, &vmap, base + slot * stage_bytes, &ring.full[slot], lane);
-      if (!waited) {   // the values do not depend on the first pass, the logits do
-        pdl_wait();
-        waited = true;
-      }
-      float *xs = reinterpret_cast<float *>(smem + slot * stage_bytes + PgtRing<D>::kTileBytes), *ds = xs + side;
-      // lane -> 4 keys of row r0, r0 + RPI, ..
-      const int kl = 4 * (lane % LPR), key = g.key0 + kl, r0 = lane / LPR;
-      if (key < g.end) {
-        const int col = key / p.c.page_size, off = key % p.c.page_size;
-        int dpg[16 / RPI];   // the rows' demand pages (one page for all rows of a sequence)
-#pragma unroll
-        for (int i = 0; i < 16 / RPI; ++i) {
-          const int r = r0 + i * RPI;
-          dpg[i] = i > 0 && g.s >= 0 ? dpg[0] : -1;
-          if (r < g.nrows && (i == 0 || g.s < 0)) {
-            int s, hq;
-            g.row(w.G, r, s, hq);
-            if (L.len[s] > 0)
-              dpg[i] = checked_page(p.c.demand_table + (size_t)s * p.c.max_pages + col, p.c.num_demand_pages, p.status);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 16 / RPI; ++i) {
-          const int r = r0 + i * RPI;
-          if (r >= g.nrows) break;
-          int s, hq;
-          g.row(w.G, r, s, hq);
-          cp_async16(xs + r * PITCH + kl, logits + ((size_t)s * p.c.Hq + hq) * w.Lp + key);
-          if (dpg[i] >= 0)
-            cp_async16(ds + r * PITCH + kl, p.c.demand_pages + ((size_t)dpg[i] * p.c.Hq + hq) * p.c.page_size + off);
-        }
-      }
-      cp_async_arrive_noinc(&ring.full[slot]);
-      g.key0 += TILE;
-      --left;
-    }
-    if (!waited) pdl_wait();
-    cp_async_wait_all();
-    if (ring.abort_word && lane == 0) drain(ring.full, stages, st);
+  if (warp == WARPS) {   // the values do not depend on the first pass
+    produce<D>(p, w, tt, L, ring, &vmap, base, stages, i0, i1, wc);
     return;
   }
+  float *const side = reinterpret_cast<float *>(smem + stages * PgtRing<D>::kTileBytes);
+  float *const red = reinterpret_cast<float *>(smem + stages * PgtRing<D>::kTileBytes + pgt_side_bytes(D, max_rows));
+  const float *const logits = reinterpret_cast<const float *>(p.ws + w.logit_off);
+  const int gid = lane / 4, t = lane % 4, sh = w.page_shift, ps = 1 << sh;
+  // lane -> row: matrices (k half 0, n 0-7), (k half 1, n 0-7), (k half 0, n 8-15), (k half 1, n 8-15)
+  const int row = warp * 16 + group_key(lane & 7, (lane >> 3) & 1);
+  int slot = 0;
+  uint32_t parity = 0;
   pdl_wait();
-  const int gid = lane / 4, t = lane % 4;
   for (long long i = i0; i < i1;) {
     PgtSeg g = pgt_seg(p, w, tt, L, i);
     const int n = (int)min((long long)g.left, i1 - i);
+    const int first = g.key0 + warp * 16;   // this warp's 16 keys of the first tile
+    // the thread's rows: logits, demand table, demand pool of its query head, its place in shared memory
+    const float *xrow[HH];
+    const int32_t *dtab[HH];
+    float *dpool[HH], *stash[HH];
+    bool on[HH];
+    const size_t page_floats = (size_t)p.c.Hq << sh;
+#pragma unroll
+    for (int hh = 0; hh < HH; ++hh) {
+      const int r = gid + 8 * hh;
+      int s = 0, hq = 0;
+      on[hh] = r < g.nrows;
+      if (on[hh]) g.row(w.G, r, s, hq);
+      on[hh] = on[hh] && L.len[s] > 0;                 // an idle slot bids nothing
+      xrow[hh] = logits + ((size_t)s * p.c.Hq + hq) * w.Lp + first + 4 * t;
+      dtab[hh] = p.c.demand_table + (size_t)s * p.c.max_pages;
+      dpool[hh] = p.c.demand_pages + ((size_t)hq << sh) + ((first + 4 * t) & (ps - 1));
+      stash[hh] = side + (((size_t)warp * max_rows + r) * 4 + t) * 8;
+    }
+    const int stash_step = WARPS * max_rows * 32;       // floats between tiles in flight
+    // demand page of this warp's group of tile k, per row half
+    auto demand_page = [&](int k, int hh) -> int {
+      const int key = first + k * TILE;
+      return on[hh] && k < n && key < g.end ? __ldg(dtab[hh] + (key >> sh)) : -1;
+    };
+    // where the demand of tile k lies: the place inside a page moves by TILE
+    auto demand_at = [&](int k, int hh, int pg) -> float * {
+      const int move = ((first + 4 * t + k * TILE) & (ps - 1)) - ((first + 4 * t) & (ps - 1));
+      return dpool[hh] + (size_t)pg * page_floats + move;
+    };
+    auto bring = [&](int k, const int (&pg)[HH]) {
+#pragma unroll
+      for (int hh = 0; hh < HH; ++hh) {
+        if (on[hh] && k < n && first + k * TILE + 4 * t < g.end) {
+          float *to = stash[hh] + (k % kPgtAhead) * stash_step;
+          cp_async16(to, xrow[hh] + k * TILE);
+          if ((unsigned)pg[hh] < (unsigned)p.c.num_demand_pages)
+            cp_async16(to + 4, demand_at(k, hh, pg[hh]));
+          else
+            atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int pages[kPgtAhead + 1][HH];   // demand pages of tiles k .. k + kPgtAhead
+#pragma unroll
+    for (int a = 0; a < kPgtAhead; ++a)
+#pragma unroll
+      for (int hh = 0; hh < HH; ++hh) pages[a][hh] = demand_page(a, hh);
+#pragma unroll
+    for (int a = 0; a < kPgtAhead - 1; ++a) bring(a, pages[a]);
     // lse2 of the rows: a warp joins a row's pieces
-    for (int r = warp; r < g.nrows; r += kPgtWarps) {
+    for (int r = warp; r < g.nrows; r += WARPS) {
       int s, hq;
       g.row(w.G, r, s, hq);
       const PgtPieces pc = pgt_pieces(p, w, tt, L, s, hq);
@@ -568,93 +595,84 @@ __global__ void __launch_bounds__(kPgtThreads, 2)
         l = l * ex2_approx(m - ms) + l2 * ex2_approx(m2 - ms);
         m = mn;
       }
-      if (lane == 0) s_lse[r] = L.len[s] > 0 ? m + log2f(l) : INFINITY;   // an idle slot bids nothing
+      if (lane == 0) s_lse[r] = m + log2f(l);
     }
-    named_bar_sync(1, kPgtWarps * 32);
-    float lse[2];
-    int rs[2], rh[2];
-    bool on[2];
+    named_bar_sync(1, WARPS * 32);
+    float lse[HH];
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const int r = gid + 8 * hh;
-      lse[hh] = r < g.nrows ? s_lse[r] : INFINITY;
-      on[hh] = lse[hh] != INFINITY;
-      rs[hh] = rh[hh] = 0;
-      if (r < g.nrows) g.row(w.G, r, rs[hh], rh[hh]);
-    }
+    for (int hh = 0; hh < HH; ++hh) lse[hh] = on[hh] ? s_lse[gid + 8 * hh] : 0.f;
     float acc[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-    float sum[2] = {0.f, 0.f};
-    // A wait that gave up ends the piece's loop but not the warp, which still
-    // meets the others at the barriers below (its later waits fail at once).
+    float sum[HH] = {};
+    // A wait that gave up ends the piece's loop but not the warp (see pgt_keys).
     for (int k = 0; k < n; ++k) {
-      const long long st = i - i0 + k;
-      const int slot = (int)(st % stages);
-      if (!warp_wait(&ring.full[slot], (uint32_t)((st / stages) & 1), wc)) break;
-      const uint32_t tile = base + slot * stage_bytes;
-      const float *xs = reinterpret_cast<const float *>(smem + slot * stage_bytes + PgtRing<D>::kTileBytes);
-      const float *ds = xs + side;
-      const int key_tile = g.key0 + k * TILE;
+      bring(k + kPgtAhead - 1, pages[kPgtAhead - 1]);
 #pragma unroll
-      for (int gg = 0; gg < WK / 16; ++gg) {
-        const int kl = warp * WK + gg * 16;
-        const int valid = g.end - (key_tile + kl);   // keys of the group before the end
-        if (valid <= 0) break;
-        if (valid < 16) {   // rows past the end may hold anything: 0 times NaN is NaN
-          for (int j = lane; j < (16 - valid) * (D / 8); j += 32) {
-            const int row = kl + valid + j / (D / 8);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(tile + tile_off<D>(row, j % (D / 8))), "r"(0u)
-                         : "memory");
+      for (int hh = 0; hh < HH; ++hh) pages[kPgtAhead][hh] = demand_page(k + kPgtAhead, hh);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kPgtAhead - 1) : "memory");   // tile k's have landed
+      const int kg = first + k * TILE;
+      const int valid = g.end - kg;     // keys of the group before the end
+      uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int hh = 0; hh < HH; ++hh) {
+        if (on[hh] && 4 * t < valid) {
+          const float *from = stash[hh] + (k % kPgtAhead) * stash_step;
+          const float4 x = *reinterpret_cast<const float4 *>(from);
+          const float4 d = *reinterpret_cast<const float4 *>(from + 4);
+          const float xe[4] = {x.x, x.y, x.z, x.w}, de[4] = {d.x, d.y, d.z, d.w};
+          float nd[4], sh4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float bid = ex2_approx(xe[e] - lse[hh]);
+            nd[e] = de[e] + bid;
+            const float den = (p.earlier ? de[e] : nd[e]) + p.eps;
+            sh4[e] = bid * rcp_approx(den);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        uint32_t hi[4], lo[4];
+          if (valid < 16) {
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          float sh[4] = {0.f, 0.f, 0.f, 0.f};
-          if (on[hh] && 4 * t < valid) {
-            const float4 x = *reinterpret_cast<const float4 *>(xs + (gid + 8 * hh) * PITCH + kl + 4 * t);
-            const float4 d = *reinterpret_cast<const float4 *>(ds + (gid + 8 * hh) * PITCH + kl + 4 * t);
-            const float xe[4] = {x.x, x.y, x.z, x.w}, de[4] = {d.x, d.y, d.z, d.w};
-            float nd[4];
+            for (int e = 0; e < 4; ++e)
+              if (4 * t + e >= valid) sh4[e] = 0.f;
+          }
+          sum[hh] += (sh4[0] + sh4[1]) + (sh4[2] + sh4[3]);
+          if ((unsigned)pages[0][hh] < (unsigned)p.c.num_demand_pages) {
+            float *dst = demand_at(k, hh, pages[0][hh]);
+            if (4 * t + 4 <= valid) {
+              *reinterpret_cast<float4 *>(dst) = make_float4(nd[0], nd[1], nd[2], nd[3]);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float bid = ex2_approx(xe[e] - lse[hh]);
-              nd[e] = de[e] + bid;
-              const float den = (p.earlier ? de[e] : nd[e]) + p.eps;
-              sh[e] = 4 * t + e < valid ? bid * rcp_approx(den) : 0.f;
-              sum[hh] += sh[e];
-            }
-            const int key = key_tile + kl + 4 * t;
-            const int dpg =
-                __ldg(p.c.demand_table + (size_t)rs[hh] * p.c.max_pages + key / p.c.page_size);
-            if (dpg >= 0 && dpg < p.c.num_demand_pages) {
-              float *dst = p.c.demand_pages + ((size_t)dpg * p.c.Hq + rh[hh]) * p.c.page_size + key % p.c.page_size;
-              if (4 * t + 4 <= valid) {
-                *reinterpret_cast<float4 *>(dst) = make_float4(nd[0], nd[1], nd[2], nd[3]);
-              } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (4 * t + e < valid) dst[e] = nd[e];
-              }
+              for (int e = 0; e < 4; ++e)
+                if (4 * t + e < valid) dst[e] = nd[e];
             }
           }
           // columns 2t, 2t + 1 of the first 8 are keys 4t, 4t + 1, of the last 8 keys 4t + 2, 4t + 3
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const float s0 = sh[2 * half], s1 = sh[2 * half + 1];
+            const float s0 = sh4[2 * half], s1 = sh4[2 * half + 1];
             const uint32_t h2 = pack_bf16x2(s0, s1);
             hi[hh + 2 * half] = h2;
-            lo[hh + 2 * half] =
-                pack_bf16x2(s0 - __uint_as_float(h2 << 16), s1 - __uint_as_float(h2 & 0xffff0000u));
+            lo[hh + 2 * half] = pack_bf16x2(s0 - __uint_as_float(h2 << 16), s1 - __uint_as_float(h2 & 0xffff0000u));
           }
         }
-        // lane -> row: matrices (k half 0, n 0-7), (k half 1, n 0-7), (k half 0, n 8-15), (k half 1, n 8-15)
-        const int row = kl + group_key(lane & 7, (lane >> 3) & 1);
+      }
+#pragma unroll
+      for (int a = 0; a < kPgtAhead; ++a)
+#pragma unroll
+        for (int hh = 0; hh < HH; ++hh) pages[a][hh] = pages[a + 1][hh];
+      if (!warp_wait(&ring.full[slot], parity, wc)) break;
+      if (valid > 0) {
+        const uint32_t tile = base + slot * PgtRing<D>::kTileBytes;
+        if (valid < 16) {   // rows past the end may hold anything: 0 times NaN is NaN
+          for (int j = lane; j < (16 - valid) * (D / 8); j += 32) {
+            const int r = warp * 16 + valid + j / (D / 8);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(tile + tile_off<D>(r, j % (D / 8))), "r"(0u)
+                         : "memory");
+          }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
 #pragma unroll
         for (int j = 0; j < NT; j += 2) {
           uint32_t bfr[4];
@@ -667,19 +685,24 @@ __global__ void __launch_bounds__(kPgtThreads, 2)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.empty[slot]);
+      if (++slot == stages) {
+        slot = 0;
+        parity ^= 1;
+      }
     }
+    cp_async_wait_all();
     // the piece's numerators and share sums: the warps' parts, added in warp order
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
+    for (int hh = 0; hh < HH; ++hh) {
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) sum[hh] += __shfl_xor_sync(0xffffffffu, sum[hh], o);
       if (t == 0) s_sum[warp][gid + 8 * hh] = sum[hh];
     }
 #pragma unroll 1
-    for (int v = 0; v < kPgtWarps; ++v) {
+    for (int v = 0; v < WARPS; ++v) {
       if (warp == v) {
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
+        for (int hh = 0; hh < HH; ++hh) {
           if (gid + 8 * hh >= g.nrows) continue;
           float *to = red + (gid + 8 * hh) * D + 2 * t;
 #pragma unroll
@@ -693,21 +716,19 @@ __global__ void __launch_bounds__(kPgtThreads, 2)
           }
         }
       }
-      named_bar_sync(1, kPgtWarps * 32);
+      named_bar_sync(1, WARPS * 32);
     }
-    const size_t slot = (size_t)blockIdx.x + g.seg;
-    float *part = g.s >= 0 ? reinterpret_cast<float *>(p.ws + w.own_acc_off) + slot * w.own_rows * acc_stride(D)
-                           : reinterpret_cast<float *>(p.ws + w.pre_acc_off) + slot * 16 * acc_stride(D);
-    for (int j = tid; j < g.nrows * D; j += kPgtWarps * 32) {
-      part[j / D * acc_stride(D) + j % D] = red[j];
-    }
+    const size_t at = (size_t)blockIdx.x + g.seg;
+    float *part = g.s >= 0 ? reinterpret_cast<float *>(p.ws + w.own_acc_off) + at * w.own_rows * acc_stride(D)
+                           : reinterpret_cast<float *>(p.ws + w.pre_acc_off) + at * 16 * acc_stride(D);
+    for (int j = tid; j < g.nrows * D; j += WARPS * 32) part[j / D * acc_stride(D) + j % D] = red[j];
     if (tid < g.nrows) {
       float a = 0.f;
 #pragma unroll
-      for (int v = 0; v < kPgtWarps; ++v) a += s_sum[v][tid];
+      for (int v = 0; v < WARPS; ++v) a += s_sum[v][tid];
       part[tid * acc_stride(D) + D] = a;
     }
-    named_bar_sync(1, kPgtWarps * 32);
+    named_bar_sync(1, WARPS * 32);
     i += n;
   }
 }
@@ -769,20 +790,19 @@ static cudaError_t launch_after(void (*kernel)(KArgs...), int grid, int threads,
 
 constexpr int kPgtSmemPerCta = 100 * 1024;   // two CTAs an SM beside their static shared memory
 
-template <int D>
-static int launch_pgt_t(const PagedDecode &p, cudaStream_t stream) {
+template <int D, int HH>
+static int launch_pgt_t(const PagedDecode &p, const PgtPlan &w, int rows, cudaStream_t stream) {
   using R = PgtRing<D>;
   static PerDeviceOnce once;
   const int prep = once.run([] {
-    return (cudaFuncSetAttribute(pgt_keys<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgtSmemPerCta) !=
+    return (cudaFuncSetAttribute(pgt_keys<D, HH>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgtSmemPerCta) !=
                 cudaSuccess ||
-            cudaFuncSetAttribute(pgt_values<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgtSmemPerCta) !=
+            cudaFuncSetAttribute(pgt_values<D, HH>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgtSmemPerCta) !=
                 cudaSuccess)
                ? DA_ERR_CUDA
                : DA_OK;
   });
   if (prep != DA_OK) return prep;
-  const PgtPlan w = pgt_plan(p.c.S, p.c.Hq, p.c.Hkv, D, p.max_len, p.prefix_len);
   CUtensorMap km, vm;
   const int64_t num = (int64_t)p.c.num_pages * p.c.Hkv;
   // an empty pool has no pages to map; every page id then fails its check, and no copy is issued
@@ -791,14 +811,12 @@ static int launch_pgt_t(const PagedDecode &p, cudaStream_t stream) {
     return DA_ERR_CUDA;
   constexpr int k_stages = (kPgtSmemPerCta - 1024) / R::kTileBytes;
   static_assert(k_stages <= 8, "the ring's barriers");
-  pgt_keys<D><<<w.ctas, kPgtThreads, 1024 + k_stages * R::kTileBytes, stream>>>(p, w, km, k_stages);
-  const int rows = w.prefix_segs > 0 ? 16 : w.own_rows;
-  const int stage = (int)round_up(R::kTileBytes + 2 * rows * pgt_pitch(D) * 4, 1024);
-  const int red = rows * D * 4;
-  int v_stages = (kPgtSmemPerCta - 1024 - red) / stage;
+  pgt_keys<D, HH><<<w.ctas, pgt_threads(D), 1024 + k_stages * R::kTileBytes, stream>>>(p, w, km, k_stages);
+  const int rest = pgt_side_bytes(D, rows) + rows * D * 4;
+  int v_stages = (kPgtSmemPerCta - 1024 - rest) / R::kTileBytes;
   if (v_stages > 8) v_stages = 8;
-  if (launch_after(pgt_values<D>, w.ctas, kPgtThreads, 1024 + v_stages * stage + red, stream, p, w, vm, v_stages, rows) !=
-      cudaSuccess)
+  if (launch_after(pgt_values<D, HH>, w.ctas, pgt_threads(D), 1024 + v_stages * R::kTileBytes + rest, stream, p, w, vm,
+                   v_stages, rows) != cudaSuccess)
     return DA_ERR_CUDA;
   if (launch_after(pgt_combine<D>, p.c.S * p.c.Hq, kPgtCombThreads, 0, stream, p, w) != cudaSuccess)
     return DA_ERR_CUDA;
@@ -806,7 +824,11 @@ static int launch_pgt_t(const PagedDecode &p, cudaStream_t stream) {
 }
 
 int launch_paged_decode_bf16(const PagedDecode &p, cudaStream_t stream) {
-  return p.c.d == 128 ? launch_pgt_t<128>(p, stream) : launch_pgt_t<64>(p, stream);
+  const PgtPlan w = pgt_plan(p.c.S, p.c.Hq, p.c.Hkv, p.c.d, p.max_len, p.prefix_len, p.c.page_size);
+  const int rows = w.prefix_segs > 0 ? 16 : w.own_rows;   // the most rows of a segment
+  if (p.c.d == 128)
+    return rows > 8 ? launch_pgt_t<128, 2>(p, w, rows, stream) : launch_pgt_t<128, 1>(p, w, rows, stream);
+  return rows > 8 ? launch_pgt_t<64, 2>(p, w, rows, stream) : launch_pgt_t<64, 1>(p, w, rows, stream);
 }
 
 }  // namespace da
