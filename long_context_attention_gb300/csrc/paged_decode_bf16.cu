@@ -41,13 +41,37 @@ namespace da {
 
 constexpr int kPgtMaxSeqs = 1024;                 // lengths kept in shared memory
 DA_HD constexpr int pgt_tile(int d) { return d == 64 ? 128 : 64; }   // keys per stage (16 KB of K or V)
-DA_HD constexpr int pgt_warps(int d) { return pgt_tile(d) / 16; }    // consumer warps: 16 keys of a stage each
+DA_HD constexpr int pgt_warps(int d) { return pgt_tile(d) / 16; }    // pgt_keys: consumer warps, 16 keys of a stage each
 DA_HD constexpr int pgt_threads(int d) { return 32 * pgt_warps(d) + 32; }   // and the producer warp
-constexpr int kPgtAhead = 3;                      // tiles whose logits and demand are in flight or in use
+constexpr int kPgtSmemPerCta = 100 * 1024;        // two CTAs an SM beside their static shared memory
 constexpr int kPgtMaxCtas = 2 * 152;              // two resident CTAs on each SM
 
-// pgt_values: bytes of the logits and demand in flight for `rows` rows.
-DA_HD int pgt_side_bytes(int d, int rows) { return kPgtAhead * pgt_warps(d) * rows * 128; }
+// pgt_values for up to GE rows of a segment (1, 2, 4, 8 or 16).
+template <int D, int GE>
+struct PgtVal {
+  static constexpr bool kWide = GE == 16;             // rows fill the M = 16 of the product
+  static constexpr int kTile = pgt_tile(D);
+  static constexpr int kGroups = kWide ? 1 : (8 / GE < kTile / 16 ? 8 / GE : kTile / 16);   // 16-key groups a step
+  static constexpr int kStep = 16 * kGroups;          // keys a warp takes at a time
+  static constexpr int kStepsPerTile = kTile / kStep;
+  // Enough warps that the shares of a 16 KB tile take less than its 0.7 us at HBM rate.
+  static constexpr int kWarps = D == 64 && GE >= 8 ? 8 : 4;
+  static constexpr int kThreads = 32 * kWarps + 32;
+  static constexpr int kTileStride = kWarps / kStepsPerTile;   // tiles between a warp's steps
+  static_assert(kWarps % kStepsPerTile == 0, "whole tiles");
+  static constexpr int kAhead = kTileStride >= 2 ? 2 : 3;      // steps whose logits and demand are in flight or in use
+  static constexpr int kHalves = kWide ? 2 : 1;
+  static constexpr int kSideBytes = kAhead * kHalves * 1024;   // a warp's logits and demand
+  static constexpr int kRedBytes = (kWide ? 16 : 8) * D * 4;   // a warp's numerators, in the same place afterwards
+  static constexpr int kWarpBytes = kSideBytes > kRedBytes ? kSideBytes : kRedBytes;
+  static constexpr int kRoom = (kPgtSmemPerCta - 1024 - kWarps * kWarpBytes) / 16384;
+  // A multiple of the stride: every tile that passes through a slot then goes
+  // to the same warps, which therefore see each phase of its barrier (a wait
+  // that skips a phase cannot tell it from the one before it).
+  static constexpr int kStages = (kRoom < 8 ? kRoom : 8) / kTileStride * kTileStride;
+  static_assert(kStages >= 2 && kStages >= kTileStride, "a slot for every warp");
+  static constexpr int kSmemBytes = 1024 + kStages * 16384 + kWarps * kWarpBytes;
+};
 
 // Host plan of a call; slots and scratch offsets.
 struct PgtPlan {
@@ -273,11 +297,11 @@ struct PgtRing {
   static constexpr int kTile = pgt_tile(D);
   static constexpr int kTileBytes = kTile * D * 2;
   uint64_t full[8], empty[8];
-  int abort_word;
-  __device__ __forceinline__ void init(int stages) {
+  volatile int abort_word;
+  __device__ __forceinline__ void init(int stages, int arrivals) {
     for (int i = 0; i < stages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], pgt_warps(D));
+      mbar_init(&empty[i], arrivals);   // one per consumer of a tile
     }
     abort_word = 0;
     fence_mbar_init();
@@ -368,11 +392,11 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
   __shared__ float2 s_ml[WARPS][16];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   pdl_launch_dependents();
-  if (tid == 0) ring.init(stages);
+  if (tid == 0) ring.init(stages, WARPS);
   pgt_load_lens<pgt_threads(D)>(p, w, L, blockIdx.x == 0 ? p.status : nullptr);
   const PgtTiles tt = pgt_tiles(p, w, L);
   const long long i0 = pgt_first(tt, blockIdx.x), i1 = pgt_first(tt, blockIdx.x + 1);
-  const WaitCtx wc{reinterpret_cast<volatile int *>(&ring.abort_word), p.status};
+  const WaitCtx wc{&ring.abort_word, p.status};
   const uint32_t base = smem_u32(pgt_smem_base());
   if (warp == WARPS) {
     produce<D>(p, w, tt, L, ring, &kmap, base, stages, i0, i1, wc);
@@ -386,6 +410,7 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
   for (long long i = i0; i < i1;) {
     PgtSeg g = pgt_seg(p, w, tt, L, i);
     const int n = (int)min((long long)g.left, i1 - i);
+    const int tiles = __any_sync(0xffffffffu, ring.abort_word != 0) ? 0 : n;   // a wait gave up: touch no barrier again
     // Q rows as the A operand; rows past the segment's are 0
     uint32_t qa[KS][4] = {};
     float c2[HH] = {};
@@ -413,8 +438,8 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
     for (int hh = 0; hh < HH; ++hh) m[hh] = -INFINITY, l[hh] = 0.f;
     const int first = g.key0 + warp * 16;   // this warp's 16 keys of the first tile
     // A wait that gave up ends the piece's loop but not the warp, which still
-    // meets the others at the barriers below (its later waits fail at once).
-    for (int k = 0; k < n; ++k) {
+    // meets the others at the barriers below.
+    for (int k = 0; k < tiles; ++k) {
       if (!warp_wait(&ring.full[slot], parity, wc)) break;
       const uint32_t tile = base + slot * PgtRing<D>::kTileBytes;
       const int kg = first + k * TILE;
@@ -484,80 +509,93 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
 }
 
 // ------------------------------------------------------------------ pass 2: shares
-// Each thread brings the logits and demand of its own (row, 4 keys) itself, by
-// 16-byte asynchronous copies kPgtAhead - 1 tiles ahead into its own place in
-// shared memory: nothing to hand over between warps, and no registers held by
-// bytes in flight.
-template <int D, int HH>
-__global__ void __launch_bounds__(pgt_threads(D), 2)
-    pgt_values(PagedDecode p, PgtPlan w, const __grid_constant__ CUtensorMap vmap, int stages, int max_rows) {
+// Lane (g, t) of a warp holds 4 consecutive keys of one row.  With GE rows the
+// 8 values of g are GE rows x kGroups groups of 16 keys, so that few query heads
+// per key head still use every lane for the exponentials and reciprocals: group
+// q's shares sit in rows q GE .. of the A operand, the other rows are 0 for its
+// product, and the rows of equal query head are added once per piece.  Rows
+// 8-15 of the operand take what rounding the shares to bf16 left (the second
+// term costs no instructions).  With 9 to 16 rows (GE = 16) the second term is
+// a product of its own.
+//
+// Each thread brings the logits and demand of its own keys itself, by 16-byte
+// asynchronous copies into its own place in shared memory one or two steps
+// ahead: nothing to hand over between warps, and no registers held by bytes in
+// flight.  A warp takes every kTileStride-th tile's step (8 x 12 x 131072 keys,
+// d = 64: 4 of 32 lanes at work and 250 instructions per 16 keys took 365 us).
+template <int D, int GE>
+__global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
+    pgt_values(PagedDecode p, PgtPlan w, const __grid_constant__ CUtensorMap vmap) {
+  using V = PgtVal<D, GE>;
   constexpr int NT = D / 8;    // n-tiles of the value product
-  constexpr int TILE = pgt_tile(D), WARPS = pgt_warps(D);
+  constexpr int TILE = V::kTile, WARPS = V::kWarps, HH = V::kHalves, AHEAD = V::kAhead;
+  constexpr int STRIDE = V::kTileStride * TILE;   // keys between a warp's steps
   __shared__ PgtLens L;
   __shared__ PgtRing<D> ring;
   __shared__ float s_lse[16];
   __shared__ float s_sum[WARPS][16];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   pdl_launch_dependents();
-  if (tid == 0) ring.init(stages);
-  pgt_load_lens<pgt_threads(D)>(p, w, L, nullptr);
+  if (tid == 0) ring.init(V::kStages, V::kStepsPerTile);
+  pgt_load_lens<V::kThreads>(p, w, L, nullptr);
   const PgtTiles tt = pgt_tiles(p, w, L);
   const long long i0 = pgt_first(tt, blockIdx.x), i1 = pgt_first(tt, blockIdx.x + 1);
-  const WaitCtx wc{reinterpret_cast<volatile int *>(&ring.abort_word), p.status};
+  const WaitCtx wc{&ring.abort_word, p.status};
   uint8_t *const smem = pgt_smem_base();
   const uint32_t base = smem_u32(smem);
   if (warp == WARPS) {   // the values do not depend on the first pass
-    produce<D>(p, w, tt, L, ring, &vmap, base, stages, i0, i1, wc);
+    produce<D>(p, w, tt, L, ring, &vmap, base, V::kStages, i0, i1, wc);
     return;
   }
-  float *const side = reinterpret_cast<float *>(smem + stages * PgtRing<D>::kTileBytes);
-  float *const red = reinterpret_cast<float *>(smem + stages * PgtRing<D>::kTileBytes + pgt_side_bytes(D, max_rows));
+  uint8_t *const mine = smem + V::kStages * 16384 + warp * V::kWarpBytes;
+  float *const stash = reinterpret_cast<float *>(mine) + lane * 8;   // this thread's logits and demand: [AHEAD][HH]
   const float *const logits = reinterpret_cast<const float *>(p.ws + w.logit_off);
   const int gid = lane / 4, t = lane % 4, sh = w.page_shift, ps = 1 << sh;
+  const int q = V::kWide ? 0 : gid / GE, r0 = V::kWide ? gid : gid % GE;   // the lane's group and row
+  const int sub = warp % V::kStepsPerTile * V::kStep;    // the warp's keys inside a tile
   // lane -> row: matrices (k half 0, n 0-7), (k half 1, n 0-7), (k half 0, n 8-15), (k half 1, n 8-15)
-  const int row = warp * 16 + group_key(lane & 7, (lane >> 3) & 1);
-  int slot = 0;
-  uint32_t parity = 0;
+  const int vrow = sub + group_key(lane & 7, (lane >> 3) & 1);
   pdl_wait();
   for (long long i = i0; i < i1;) {
     PgtSeg g = pgt_seg(p, w, tt, L, i);
     const int n = (int)min((long long)g.left, i1 - i);
-    const int first = g.key0 + warp * 16;   // this warp's 16 keys of the first tile
-    // the thread's rows: logits, demand table, demand pool of its query head, its place in shared memory
+    // the warp's first tile of the piece: tile x of the CTA's run goes to the
+    // warps x % kTileStride, whatever the pieces
+    const int tile0 = (warp / V::kStepsPerTile + V::kTileStride - (int)((i - i0) % V::kTileStride)) % V::kTileStride;
+    int steps = n > tile0 ? (n - tile0 + V::kTileStride - 1) / V::kTileStride : 0;
+    if (__any_sync(0xffffffffu, ring.abort_word != 0)) steps = 0;    // a wait gave up: touch no barrier again
+    const int step0 = g.key0 + tile0 * TILE + sub;                   // its first key
+    const int key0 = step0 + 16 * q + 4 * t;                         // the lane's first key
+    // the lane's rows: logits, demand table, demand pool of its query head
     const float *xrow[HH];
     const int32_t *dtab[HH];
-    float *dpool[HH], *stash[HH];
+    float *dpool[HH];
     bool on[HH];
     const size_t page_floats = (size_t)p.c.Hq << sh;
 #pragma unroll
     for (int hh = 0; hh < HH; ++hh) {
-      const int r = gid + 8 * hh;
+      const int r = r0 + 8 * hh;
       int s = 0, hq = 0;
-      on[hh] = r < g.nrows;
+      on[hh] = r < g.nrows && q < V::kGroups;
       if (on[hh]) g.row(w.G, r, s, hq);
       on[hh] = on[hh] && L.len[s] > 0;                 // an idle slot bids nothing
-      xrow[hh] = logits + ((size_t)s * p.c.Hq + hq) * w.Lp + first + 4 * t;
+      xrow[hh] = logits + ((size_t)s * p.c.Hq + hq) * w.Lp + key0;
       dtab[hh] = p.c.demand_table + (size_t)s * p.c.max_pages;
-      dpool[hh] = p.c.demand_pages + ((size_t)hq << sh) + ((first + 4 * t) & (ps - 1));
-      stash[hh] = side + (((size_t)warp * max_rows + r) * 4 + t) * 8;
+      dpool[hh] = p.c.demand_pages + ((size_t)hq << sh);
     }
-    const int stash_step = WARPS * max_rows * 32;       // floats between tiles in flight
-    // demand page of this warp's group of tile k, per row half
-    auto demand_page = [&](int k, int hh) -> int {
-      const int key = first + k * TILE;
-      return on[hh] && k < n && key < g.end ? __ldg(dtab[hh] + (key >> sh)) : -1;
+    auto demand_page = [&](int k, int hh) -> int {     // of the lane's keys of step k
+      const int key = key0 + k * STRIDE;
+      return on[hh] && k < steps && key < g.end ? __ldg(dtab[hh] + (key >> sh)) : -1;
     };
-    // where the demand of tile k lies: the place inside a page moves by TILE
     auto demand_at = [&](int k, int hh, int pg) -> float * {
-      const int move = ((first + 4 * t + k * TILE) & (ps - 1)) - ((first + 4 * t) & (ps - 1));
-      return dpool[hh] + (size_t)pg * page_floats + move;
+      return dpool[hh] + (size_t)pg * page_floats + ((key0 + k * STRIDE) & (ps - 1));
     };
     auto bring = [&](int k, const int (&pg)[HH]) {
 #pragma unroll
       for (int hh = 0; hh < HH; ++hh) {
-        if (on[hh] && k < n && first + k * TILE + 4 * t < g.end) {
-          float *to = stash[hh] + (k % kPgtAhead) * stash_step;
-          cp_async16(to, xrow[hh] + k * TILE);
+        if (on[hh] && k < steps && key0 + k * STRIDE < g.end) {
+          float *to = stash + ((k % AHEAD) * HH + hh) * 256;
+          cp_async16(to, xrow[hh] + k * STRIDE);
           if ((unsigned)pg[hh] < (unsigned)p.c.num_demand_pages)
             cp_async16(to + 4, demand_at(k, hh, pg[hh]));
           else
@@ -566,13 +604,13 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    int pages[kPgtAhead + 1][HH];   // demand pages of tiles k .. k + kPgtAhead
+    int pages[AHEAD + 1][HH];   // demand pages of steps k .. k + AHEAD
 #pragma unroll
-    for (int a = 0; a < kPgtAhead; ++a)
+    for (int a = 0; a < AHEAD; ++a)
 #pragma unroll
       for (int hh = 0; hh < HH; ++hh) pages[a][hh] = demand_page(a, hh);
 #pragma unroll
-    for (int a = 0; a < kPgtAhead - 1; ++a) bring(a, pages[a]);
+    for (int a = 0; a < AHEAD - 1; ++a) bring(a, pages[a]);
     // lse2 of the rows: a warp joins a row's pieces
     for (int r = warp; r < g.nrows; r += WARPS) {
       int s, hq;
@@ -598,134 +636,151 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
       if (lane == 0) s_lse[r] = m + log2f(l);
     }
     named_bar_sync(1, WARPS * 32);
-    float lse[HH];
+    float lse[HH], sum[HH] = {};
 #pragma unroll
-    for (int hh = 0; hh < HH; ++hh) lse[hh] = on[hh] ? s_lse[gid + 8 * hh] : 0.f;
+    for (int hh = 0; hh < HH; ++hh) lse[hh] = on[hh] ? s_lse[r0 + 8 * hh] : 0.f;
     float acc[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-    float sum[HH] = {};
     // A wait that gave up ends the piece's loop but not the warp (see pgt_keys).
-    for (int k = 0; k < n; ++k) {
-      bring(k + kPgtAhead - 1, pages[kPgtAhead - 1]);
+    for (int k = 0; k < steps; ++k) {
+      bring(k + AHEAD - 1, pages[AHEAD - 1]);
 #pragma unroll
-      for (int hh = 0; hh < HH; ++hh) pages[kPgtAhead][hh] = demand_page(k + kPgtAhead, hh);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kPgtAhead - 1) : "memory");   // tile k's have landed
-      const int kg = first + k * TILE;
-      const int valid = g.end - kg;     // keys of the group before the end
-      uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+      for (int hh = 0; hh < HH; ++hh) pages[AHEAD][hh] = demand_page(k + AHEAD, hh);
+      asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");   // step k's have landed
+      const int left = g.end - (step0 + k * STRIDE);     // keys of the step before the end
+      const int valid = left - 16 * q - 4 * t;           // of the lane's four
+      uint32_t hi[HH][2], lo[HH][2];
 #pragma unroll
       for (int hh = 0; hh < HH; ++hh) {
-        if (on[hh] && 4 * t < valid) {
-          const float *from = stash[hh] + (k % kPgtAhead) * stash_step;
+        hi[hh][0] = hi[hh][1] = lo[hh][0] = lo[hh][1] = 0u;
+        if (on[hh] && valid > 0) {
+          const float *from = stash + ((k % AHEAD) * HH + hh) * 256;
           const float4 x = *reinterpret_cast<const float4 *>(from);
           const float4 d = *reinterpret_cast<const float4 *>(from + 4);
           const float xe[4] = {x.x, x.y, x.z, x.w}, de[4] = {d.x, d.y, d.z, d.w};
-          float nd[4], sh4[4];
+          float nd[4], share[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float bid = ex2_approx(xe[e] - lse[hh]);
             nd[e] = de[e] + bid;
             const float den = (p.earlier ? de[e] : nd[e]) + p.eps;
-            sh4[e] = bid * rcp_approx(den);
+            share[e] = bid * rcp_approx(den);
           }
-          if (valid < 16) {
+          if (valid < 4) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (4 * t + e >= valid) sh4[e] = 0.f;
+            for (int e = 1; e < 4; ++e)
+              if (e >= valid) share[e] = 0.f;
           }
-          sum[hh] += (sh4[0] + sh4[1]) + (sh4[2] + sh4[3]);
+          sum[hh] += (share[0] + share[1]) + (share[2] + share[3]);
           if ((unsigned)pages[0][hh] < (unsigned)p.c.num_demand_pages) {
             float *dst = demand_at(k, hh, pages[0][hh]);
-            if (4 * t + 4 <= valid) {
+            if (valid >= 4) {
               *reinterpret_cast<float4 *>(dst) = make_float4(nd[0], nd[1], nd[2], nd[3]);
             } else {
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                if (4 * t + e < valid) dst[e] = nd[e];
+              for (int e = 0; e < 3; ++e)
+                if (e < valid) dst[e] = nd[e];
             }
           }
           // columns 2t, 2t + 1 of the first 8 are keys 4t, 4t + 1, of the last 8 keys 4t + 2, 4t + 3
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const float s0 = sh4[2 * half], s1 = sh4[2 * half + 1];
+            const float s0 = share[2 * half], s1 = share[2 * half + 1];
             const uint32_t h2 = pack_bf16x2(s0, s1);
-            hi[hh + 2 * half] = h2;
-            lo[hh + 2 * half] = pack_bf16x2(s0 - __uint_as_float(h2 << 16), s1 - __uint_as_float(h2 & 0xffff0000u));
+            hi[hh][half] = h2;
+            lo[hh][half] = pack_bf16x2(s0 - __uint_as_float(h2 << 16), s1 - __uint_as_float(h2 & 0xffff0000u));
           }
         }
       }
 #pragma unroll
-      for (int a = 0; a < kPgtAhead; ++a)
+      for (int a = 0; a < AHEAD; ++a)
 #pragma unroll
         for (int hh = 0; hh < HH; ++hh) pages[a][hh] = pages[a + 1][hh];
-      if (!warp_wait(&ring.full[slot], parity, wc)) break;
-      if (valid > 0) {
-        const uint32_t tile = base + slot * PgtRing<D>::kTileBytes;
-        if (valid < 16) {   // rows past the end may hold anything: 0 times NaN is NaN
-          for (int j = lane; j < (16 - valid) * (D / 8); j += 32) {
-            const int r = warp * 16 + valid + j / (D / 8);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(tile + tile_off<D>(r, j % (D / 8))), "r"(0u)
-                         : "memory");
-          }
-          fence_proxy_async_smem();
+      const int st = (int)(i - i0) + tile0 + k * V::kTileStride;       // the tile's place in the ring
+      const int slot = st % V::kStages;
+      if (!warp_wait(&ring.full[slot], (uint32_t)((st / V::kStages) & 1), wc)) break;
+      const uint32_t tile = base + slot * 16384;
+      if (left > 0 && left < V::kStep) {   // rows past the end may hold anything: 0 times NaN is NaN
+        const int fill = (-left) & 15;     // up to the end of their group; later groups are left out
+        for (int j = lane; j < fill * (D / 8); j += 32) {
+          const int r = sub + left + j / (D / 8);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(tile + tile_off<D>(r, j % (D / 8))), "r"(0u)
+                       : "memory");
         }
-        __syncwarp();
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+#pragma unroll
+      for (int gg = 0; gg < V::kGroups; ++gg) {
+        if (16 * gg >= left) break;
+        uint32_t a1[4], a2[4];
+        if constexpr (V::kWide) {
+          a1[0] = hi[0][0], a1[1] = hi[HH - 1][0], a1[2] = hi[0][1], a1[3] = hi[HH - 1][1];
+          a2[0] = lo[0][0], a2[1] = lo[HH - 1][0], a2[2] = lo[0][1], a2[3] = lo[HH - 1][1];
+        } else {
+          const bool here = V::kGroups == 1 || q == gg;
+          a1[0] = here ? hi[0][0] : 0u, a1[1] = here ? lo[0][0] : 0u;
+          a1[2] = here ? hi[0][1] : 0u, a1[3] = here ? lo[0][1] : 0u;
+        }
 #pragma unroll
         for (int j = 0; j < NT; j += 2) {
           uint32_t bfr[4];
-          ldsm_x4_t(tile + tile_off<D>(row, j + (lane >> 4)), bfr);
-          mma16816(acc[j], hi, bfr[0], bfr[1]);
-          mma16816(acc[j + 1], hi, bfr[2], bfr[3]);
-          mma16816(acc[j], lo, bfr[0], bfr[1]);
-          mma16816(acc[j + 1], lo, bfr[2], bfr[3]);
+          ldsm_x4_t(tile + tile_off<D>(vrow + 16 * gg, j + (lane >> 4)), bfr);
+          mma16816(acc[j], a1, bfr[0], bfr[1]);
+          mma16816(acc[j + 1], a1, bfr[2], bfr[3]);
+          if constexpr (V::kWide) {
+            mma16816(acc[j], a2, bfr[0], bfr[1]);
+            mma16816(acc[j + 1], a2, bfr[2], bfr[3]);
+          }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.empty[slot]);
-      if (++slot == stages) {
-        slot = 0;
-        parity ^= 1;
-      }
     }
     cp_async_wait_all();
-    // the piece's numerators and share sums: the warps' parts, added in warp order
+    __syncwarp();
+    // the piece's numerators and share sums: each warp's rows into its own
+    // place, then the parts of a query head added in a fixed order
+    float *const red = reinterpret_cast<float *>(mine);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      float *to = red + gid * D + 8 * j + 2 * t;
+      if constexpr (V::kWide) {
+        *reinterpret_cast<float2 *>(to) = make_float2(acc[j][0], acc[j][1]);
+        *reinterpret_cast<float2 *>(to + 8 * D) = make_float2(acc[j][2], acc[j][3]);
+      } else {
+        *reinterpret_cast<float2 *>(to) = make_float2(acc[j][0] + acc[j][2], acc[j][1] + acc[j][3]);
+      }
+    }
 #pragma unroll
     for (int hh = 0; hh < HH; ++hh) {
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) sum[hh] += __shfl_xor_sync(0xffffffffu, sum[hh], o);
       if (t == 0) s_sum[warp][gid + 8 * hh] = sum[hh];
     }
-#pragma unroll 1
-    for (int v = 0; v < WARPS; ++v) {
-      if (warp == v) {
-#pragma unroll
-        for (int hh = 0; hh < HH; ++hh) {
-          if (gid + 8 * hh >= g.nrows) continue;
-          float *to = red + (gid + 8 * hh) * D + 2 * t;
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            float2 a = make_float2(acc[j][2 * hh], acc[j][2 * hh + 1]);
-            if (v > 0) {
-              const float2 b = *reinterpret_cast<const float2 *>(to + 8 * j);
-              a.x += b.x, a.y += b.y;
-            }
-            *reinterpret_cast<float2 *>(to + 8 * j) = a;
-          }
-        }
-      }
-      named_bar_sync(1, WARPS * 32);
-    }
+    named_bar_sync(1, WARPS * 32);
     const size_t at = (size_t)blockIdx.x + g.seg;
     float *part = g.s >= 0 ? reinterpret_cast<float *>(p.ws + w.own_acc_off) + at * w.own_rows * acc_stride(D)
                            : reinterpret_cast<float *>(p.ws + w.pre_acc_off) + at * 16 * acc_stride(D);
-    for (int j = tid; j < g.nrows * D; j += WARPS * 32) part[j / D * acc_stride(D) + j % D] = red[j];
+    for (int j = tid; j < g.nrows * D; j += WARPS * 32) {
+      const int r = j / D, e = j % D;
+      float a = 0.f;
+#pragma unroll
+      for (int v = 0; v < WARPS; ++v)
+#pragma unroll
+        for (int gg = 0; gg < V::kGroups; ++gg)
+          a += reinterpret_cast<const float *>(smem + V::kStages * 16384 + v * V::kWarpBytes)[(gg * GE + r) * D + e];
+      part[r * acc_stride(D) + e] = a;
+    }
     if (tid < g.nrows) {
       float a = 0.f;
 #pragma unroll
-      for (int v = 0; v < WARPS; ++v) a += s_sum[v][tid];
+      for (int v = 0; v < WARPS; ++v)
+#pragma unroll
+        for (int gg = 0; gg < V::kGroups; ++gg) a += s_sum[v][gg * GE + tid];
       part[tid * acc_stride(D) + D] = a;
     }
     named_bar_sync(1, WARPS * 32);
@@ -788,16 +843,16 @@ static cudaError_t launch_after(void (*kernel)(KArgs...), int grid, int threads,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-constexpr int kPgtSmemPerCta = 100 * 1024;   // two CTAs an SM beside their static shared memory
-
-template <int D, int HH>
-static int launch_pgt_t(const PagedDecode &p, const PgtPlan &w, int rows, cudaStream_t stream) {
+template <int D, int GE>
+static int launch_pgt_t(const PagedDecode &p, const PgtPlan &w, cudaStream_t stream) {
   using R = PgtRing<D>;
+  using V = PgtVal<D, GE>;
+  constexpr int HH = GE > 8 ? 2 : 1;
   static PerDeviceOnce once;
   const int prep = once.run([] {
     return (cudaFuncSetAttribute(pgt_keys<D, HH>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgtSmemPerCta) !=
                 cudaSuccess ||
-            cudaFuncSetAttribute(pgt_values<D, HH>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPgtSmemPerCta) !=
+            cudaFuncSetAttribute(pgt_values<D, GE>, cudaFuncAttributeMaxDynamicSharedMemorySize, V::kSmemBytes) !=
                 cudaSuccess)
                ? DA_ERR_CUDA
                : DA_OK;
@@ -812,23 +867,27 @@ static int launch_pgt_t(const PagedDecode &p, const PgtPlan &w, int rows, cudaSt
   constexpr int k_stages = (kPgtSmemPerCta - 1024) / R::kTileBytes;
   static_assert(k_stages <= 8, "the ring's barriers");
   pgt_keys<D, HH><<<w.ctas, pgt_threads(D), 1024 + k_stages * R::kTileBytes, stream>>>(p, w, km, k_stages);
-  const int rest = pgt_side_bytes(D, rows) + rows * D * 4;
-  int v_stages = (kPgtSmemPerCta - 1024 - rest) / R::kTileBytes;
-  if (v_stages > 8) v_stages = 8;
-  if (launch_after(pgt_values<D, HH>, w.ctas, pgt_threads(D), 1024 + v_stages * R::kTileBytes + rest, stream, p, w, vm,
-                   v_stages, rows) != cudaSuccess)
+  if (launch_after(pgt_values<D, GE>, w.ctas, V::kThreads, V::kSmemBytes, stream, p, w, vm) != cudaSuccess)
     return DA_ERR_CUDA;
   if (launch_after(pgt_combine<D>, p.c.S * p.c.Hq, kPgtCombThreads, 0, stream, p, w) != cudaSuccess)
     return DA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
+template <int D>
+static int launch_pgt_d(const PagedDecode &p, cudaStream_t stream) {
+  const PgtPlan w = pgt_plan(p.c.S, p.c.Hq, p.c.Hkv, D, p.max_len, p.prefix_len, p.c.page_size);
+  int rows = w.own_rows;                                 // the most rows of a segment
+  if (w.prefix_segs > 0) rows = p.c.S * w.G < 16 ? p.c.S * w.G : 16;
+  if (rows <= 1) return launch_pgt_t<D, 1>(p, w, stream);
+  if (rows <= 2) return launch_pgt_t<D, 2>(p, w, stream);
+  if (rows <= 4) return launch_pgt_t<D, 4>(p, w, stream);
+  if (rows <= 8) return launch_pgt_t<D, 8>(p, w, stream);
+  return launch_pgt_t<D, 16>(p, w, stream);
+}
+
 int launch_paged_decode_bf16(const PagedDecode &p, cudaStream_t stream) {
-  const PgtPlan w = pgt_plan(p.c.S, p.c.Hq, p.c.Hkv, p.c.d, p.max_len, p.prefix_len, p.c.page_size);
-  const int rows = w.prefix_segs > 0 ? 16 : w.own_rows;   // the most rows of a segment
-  if (p.c.d == 128)
-    return rows > 8 ? launch_pgt_t<128, 2>(p, w, rows, stream) : launch_pgt_t<128, 1>(p, w, rows, stream);
-  return rows > 8 ? launch_pgt_t<64, 2>(p, w, rows, stream) : launch_pgt_t<64, 1>(p, w, rows, stream);
+  return p.c.d == 128 ? launch_pgt_d<128>(p, stream) : launch_pgt_d<64>(p, stream);
 }
 
 }  // namespace da

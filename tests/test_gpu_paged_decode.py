@@ -29,6 +29,24 @@ def test_ragged_decode_matches_oracle(dtype, S, lens, Hq, Hkv, d, page):
     step_and_check(cache, q, max(lens))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 2, 3, 8, 12])
+def test_long_runs_of_tiles(G, d):
+    # every CTA takes many tiles in a row, across sequences: 2 CTAs on 152 SMs share 2 x 40000 keys of 4 heads
+    cache, q, _ = make_cache(3, [40000, 20001, 30], 4 * G, 4, d, 64, "bf16", seed=90 + G)
+    before = cache.demand_pages.clone()
+    out = b.dilution_attn_paged_decode(q, cache, 40000)
+    # the oracle on one query head of every sequence
+    for h in (G - 1, 4 * G - 1):
+        one = b.PagedCache(cache.k_pages[:, h // G:h // G + 1].contiguous(), cache.v_pages[:, h // G:h // G + 1].contiguous(),
+                           before[:, h:h + 1].contiguous(), cache.page_table, cache.demand_table, cache.seq_lens)
+        qh = q[:, h:h + 1].contiguous()
+        ref = oracle_step(one, qh)
+        old = one.demand_pages.clone()
+        one.demand_pages.copy_(cache.demand_pages[:, h:h + 1])
+        check_step(one, qh, old, out[:, h:h + 1], ref)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_all_idle(dtype):
     cache, q, _ = make_cache(3, [0, 0, 0], 4, 2, 64, 16, dtype)
