@@ -10,6 +10,7 @@ size_t pgs_workspace(int64_t rows, int max_len, int prefix_len, int d);
 cudaError_t launch_paged_decode_simt(const PagedDecode &p, cudaStream_t stream);
 size_t pgt_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len);
 bool pgt_serves(int S, int dtype);
+bool pgt_fits(int S, int Hq, int Hkv, int d, int max_len, int prefix_len);
 int launch_paged_decode_bf16(const PagedDecode &p, cudaStream_t stream);
 }  // namespace da
 
@@ -259,6 +260,7 @@ int dilution_attn_paged_decode(const void *q, const dilution_attn_paged_cache *c
   // the launch grids' third dimension counts 16-row groups
   const int64_t G = c.Hq / c.Hkv;
   if (c.S * ((G + 15) / 16) + (c.S * G + 15) / 16 > 65535 || c.Hkv > 65535) return DA_ERR_UNSUPPORTED;
+  if (pgt_serves(c.S, c.dtype) && !pgt_fits(c.S, c.Hq, c.Hkv, c.d, max_len, prefix_len)) return DA_ERR_UNSUPPORTED;
   PagedDecode p{};
   p.c = c;
   p.q = q;

@@ -25,12 +25,15 @@
 // bf16 terms (share rounded, and what rounding left), so they keep 2^-16
 // relative; one term alone would double the output's rounding error.
 //
-// Work split: the (segment, key tile) pairs of the call are numbered, a
-// segment being one sequence's own part or the shared prefix for one key head
-// and up to 16 rows; every CTA takes an equal run of numbers, so ragged
-// lengths balance to one tile.  A run crosses segments; the stretch inside one
-// is a piece and leaves one partial result, in slot (CTA + segment), which grows
-// along the numbering and is therefore unique.
+// Work split: a segment is one sequence's own part or the shared prefix for one
+// key head and up to 16 rows.  All segments lie on one line, each as kPgtHead
+// units (what beginning a segment costs, in tiles) followed by its key tiles;
+// every CTA takes an equal stretch of the line, so ragged lengths balance to a
+// tile and many short sequences do not gather in one CTA (48 sequences of 1 ..
+// 16384 tokens, d = 128: without the head units the SMs were busy 43 % of
+// pgt_keys).  The part of a segment inside one stretch is a piece and leaves
+// one partial result, in slot (CTA + segment), which grows along the line and
+// is therefore unique.
 #include "da_paged.h"
 #include "da_ptx.cuh"
 
@@ -45,6 +48,8 @@ DA_HD constexpr int pgt_warps(int d) { return pgt_tile(d) / 16; }    // pgt_keys
 DA_HD constexpr int pgt_threads(int d) { return 32 * pgt_warps(d) + 32; }   // and the producer warp
 constexpr int kPgtSmemPerCta = 100 * 1024;        // two CTAs an SM beside their static shared memory
 constexpr int kPgtMaxCtas = 2 * 152;              // two resident CTAs on each SM
+
+constexpr int kPgtHead = 4;   // units of a segment before its first tile (a piece costs ~2 us beside its tiles' 0.5 us)
 
 // pgt_values for up to GE rows of a segment (1, 2, 4, 8 or 16).
 template <int D, int GE>
@@ -79,6 +84,13 @@ struct PgtPlan {
   size_t logit_off, own_ml_off, own_acc_off, pre_ml_off, pre_acc_off, total;
 };
 
+// Units on the line at most (int arithmetic on the device).
+bool pgt_fits(int S, int Hq, int Hkv, int d, int max_len, int prefix_len) {
+  const int64_t G = Hq / Hkv, tile = pgt_tile(d), rows = (S * G + 15) / 16;
+  const int64_t own = (max_len - prefix_len + tile - 1) / tile + kPgtHead, pre = (prefix_len + tile - 1) / tile + kPgtHead;
+  return S * (int64_t)Hkv * ((G + 15) / 16) * own + (prefix_len > 0 ? Hkv * rows * pre : 0) < 0x7FFF0000ll;
+}
+
 static PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int page_size = 16) {
   PgtPlan w;
   w.page_shift = 0;
@@ -92,7 +104,8 @@ static PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_l
   w.own_segs = S * Hkv * w.own_groups;
   w.prefix_segs = Hkv * w.prefix_groups;
   const int64_t own_tiles = (max_len - prefix_len + w.tile - 1) / w.tile;
-  const int64_t most = (int64_t)w.own_segs * own_tiles + (int64_t)w.prefix_segs * w.prefix_tiles;
+  const int64_t most = w.own_segs * (own_tiles > 0 ? own_tiles + kPgtHead : 0) +
+                       (int64_t)w.prefix_segs * (w.prefix_tiles + kPgtHead);   // units of the line
   w.ctas = (int)(most < 1 ? 1 : most > kPgtMaxCtas ? kPgtMaxCtas : most);
   w.Lp = (int)round_up(max_len, 16);
   // slots for the most CTAs, so that the size depends on the prefix's presence alone
@@ -113,10 +126,11 @@ size_t pgt_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len)
 bool pgt_serves(int S, int dtype) { return dtype == DA_BF16 && S <= kPgtMaxSeqs; }
 
 // ------------------------------------------------------------------ device plan
-// Lengths and running tile counts of the sequences, in shared memory.
+// Lengths of the sequences and the units of one of their segments, summed, in
+// shared memory.
 struct PgtLens {
   int len[kPgtMaxSeqs];
-  int cum[kPgtMaxSeqs + 1];   // own tiles of the sequences before
+  int cum[kPgtMaxSeqs + 1];   // of the sequences before
   int warp_sum[32];
 };
 
@@ -134,7 +148,7 @@ __device__ void pgt_load_lens(const PagedDecode &p, const PgtPlan &w, PgtLens &L
     const int n = paged_len(p, s, status);
     L.len[s] = n;
     L.cum[s] = sum;
-    if (n > 0) sum += (n - p.prefix_len + w.tile - 1) / w.tile;
+    if (n > p.prefix_len) sum += kPgtHead + (n - p.prefix_len + w.tile - 1) / w.tile;
   }
   int inc = sum;
 #pragma unroll
@@ -151,34 +165,38 @@ __device__ void pgt_load_lens(const PagedDecode &p, const PgtPlan &w, PgtLens &L
   __syncthreads();
 }
 
-// Tile numbers: the prefix's segments first, then each sequence's.
-struct PgtTiles {
-  long long total, prefix;   // all tiles; the prefix's
-  int per_own;               // segments of one sequence
-  int ctas;                  // CTAs that take tiles: no more than tiles, so that each has one
+// The line: the prefix's segments first, then each sequence's; and its cut into
+// stretches of base or base + 1 units.
+struct PgtLine {
+  int total, prefix;   // units; the prefix's
+  int per_own;         // segments of one sequence
+  int ctas, base, rem;
+  __device__ __forceinline__ int first(int cta) const { return cta < ctas ? cta * base + min(cta, rem) : total; }
+  __device__ __forceinline__ int cta_of(int unit) const {   // total > 0
+    const int cut = rem * (base + 1);
+    return unit < cut ? unit / (base + 1) : rem + (unit - cut) / base;
+  }
 };
-__device__ __forceinline__ PgtTiles pgt_tiles(const PagedDecode &p, const PgtPlan &w, const PgtLens &L) {
-  PgtTiles t;
+__device__ __forceinline__ PgtLine pgt_line(const PagedDecode &p, const PgtPlan &w, const PgtLens &L) {
+  PgtLine t;
   t.per_own = p.c.Hkv * w.own_groups;
-  t.prefix = (long long)w.prefix_segs * w.prefix_tiles;
-  t.total = t.prefix + (long long)L.cum[p.c.S] * t.per_own;
-  t.ctas = (int)min((long long)w.ctas, t.total);
+  t.prefix = w.prefix_segs > 0 ? w.prefix_segs * (w.prefix_tiles + kPgtHead) : 0;
+  t.total = t.prefix + L.cum[p.c.S] * t.per_own;
+  t.ctas = max(1, min(w.ctas, t.total));   // no stretch without a unit
+  t.base = t.total / t.ctas;
+  t.rem = t.total - t.base * t.ctas;
   return t;
 }
-__device__ __forceinline__ long long pgt_first(const PgtTiles &t, int cta) {
-  return cta < t.ctas ? (long long)cta * t.total / t.ctas : t.total;
-}
-__device__ __forceinline__ int pgt_cta_of(const PgtTiles &t, long long tile) {   // t.total > 0
-  return (int)(((tile + 1) * t.ctas + t.total - 1) / t.total) - 1;
-}
 
-// One segment, seen from a tile of it.
+// One piece of a segment.
 struct PgtSeg {
   int s;                     // its sequence; -1: the prefix
   int hkv, row0, nrows;      // rows row0 .. of the sequence's group / of the batch
-  int key0, end;             // keys of the tile and the segment's end
-  int left;                  // tiles from here to the segment's end
+  int key0, end;             // the piece's first key and the segment's end
+  int n;                     // tiles of the piece (0: none left)
   int seg;                   // its number among the prefix's or the sequences' segments
+  int run;                   // tiles of the CTA's pieces before this one
+  int unit, tiles, stop;     // place of its first tile, tiles of the segment, the stretch's end
   __device__ __forceinline__ void row(int G, int r, int &seq, int &hq) const {
     if (s >= 0) {
       seq = s;
@@ -188,72 +206,101 @@ struct PgtSeg {
       hq = hkv * G + (row0 + r) % G;
     }
   }
-};
-
-__device__ __forceinline__ PgtSeg pgt_seg(const PagedDecode &p, const PgtPlan &w, const PgtTiles &t, const PgtLens &L,
-                                          long long tile) {
-  PgtSeg g;
-  int at;
-  if (tile < t.prefix) {
-    g.s = -1;
-    g.seg = (int)(tile / w.prefix_tiles);
-    at = (int)(tile - (long long)g.seg * w.prefix_tiles);
-    g.hkv = g.seg / w.prefix_groups;
-    g.row0 = g.seg % w.prefix_groups * 16;
-    g.nrows = min(16, p.c.S * w.G - g.row0);
-    g.key0 = at * w.tile;
-    g.end = p.prefix_len;
-    g.left = w.prefix_tiles - at;
-  } else {
-    const long long j = tile - t.prefix;
-    const int q = (int)(j / t.per_own);          // tiles of one segment column
-    int lo = 0, hi = p.c.S - 1;                  // the last sequence with cum <= q (and tiles of its own)
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (L.cum[mid] <= q)
-        lo = mid;
-      else
-        hi = mid - 1;
+  // Rows, keys and piece from s, seg, unit and the piece's first tile.
+  __device__ __forceinline__ void fill(const PagedDecode &p, const PgtPlan &w, const PgtLine &t, const PgtLens &L,
+                                       int tile) {
+    const int left = tiles - tile;
+    n = min(left, stop - unit);
+    if (s < 0) {
+      hkv = seg / w.prefix_groups;
+      row0 = seg % w.prefix_groups * 16;
+      nrows = min(16, p.c.S * w.G - row0);
+      key0 = tile * w.tile;
+      end = p.prefix_len;
+    } else {
+      const int h = seg - s * t.per_own;
+      hkv = h / w.own_groups;
+      row0 = h % w.own_groups * 16;
+      nrows = min(16, w.G - row0);
+      key0 = p.prefix_len + tile * w.tile;
+      end = L.len[s];
     }
-    const int n = L.cum[lo + 1] - L.cum[lo];
-    const int r = (int)(j - (long long)L.cum[lo] * t.per_own);
-    const int h = r / n;
-    at = r - h * n;
-    g.s = lo;
-    g.hkv = h / w.own_groups;
-    g.row0 = h % w.own_groups * 16;
-    g.nrows = min(16, w.G - g.row0);
-    g.key0 = p.prefix_len + at * w.tile;
-    g.end = L.len[lo];
-    g.left = n - at;
-    g.seg = lo * t.per_own + h;
   }
-  return g;
-}
+  // The first piece of the stretch [from, to).
+  __device__ void start(const PagedDecode &p, const PgtPlan &w, const PgtLine &t, const PgtLens &L, int from, int to) {
+    stop = to;
+    run = 0;
+    n = 0;
+    if (from >= to) return;
+    int u;   // place inside the segment
+    if (from < t.prefix) {
+      s = -1;
+      tiles = w.prefix_tiles;
+      seg = from / (tiles + kPgtHead);
+      u = from - seg * (tiles + kPgtHead);
+    } else {
+      const int x = from - t.prefix, q = x / t.per_own;
+      int lo = 0, hi = p.c.S - 1;   // the last sequence with cum <= q: one with units of its own
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (L.cum[mid] <= q)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      const int units = L.cum[lo + 1] - L.cum[lo], r = x - L.cum[lo] * t.per_own, h = r / units;
+      s = lo;
+      tiles = units - kPgtHead;
+      seg = lo * t.per_own + h;
+      u = r - h * units;
+    }
+    const int tile = max(0, u - kPgtHead);
+    unit = from + (tile + kPgtHead - u);
+    fill(p, w, t, L, tile);
+  }
+  // The piece after this one.
+  __device__ void next(const PagedDecode &p, const PgtPlan &w, const PgtLine &t, const PgtLens &L) {
+    run += n;
+    unit += n + kPgtHead;   // the next segment's first tile, if this piece ends its segment
+    if (unit >= stop) {
+      n = 0;
+      return;
+    }
+    ++seg;
+    if (s < 0 ? seg == w.prefix_segs : seg == (s + 1) * t.per_own) {   // on to the next sequence with keys of its own
+      int k = s + 1;
+      while (L.cum[k + 1] == L.cum[k]) ++k;   // there is one: the line goes on
+      s = k;
+      seg = k * t.per_own;
+      tiles = L.cum[k + 1] - L.cum[k] - kPgtHead;
+    }
+    fill(p, w, t, L, 0);
+  }
+};
 
 // Slots of the pieces of row (s, hq): the prefix's and its own.
 struct PgtPieces {
   int pre0, npre, pre_row;   // first slot, count, row inside the slot
   int own0, nown, own_row;
 };
-__device__ __forceinline__ PgtPieces pgt_pieces(const PagedDecode &p, const PgtPlan &w, const PgtTiles &t,
+__device__ __forceinline__ PgtPieces pgt_pieces(const PagedDecode &p, const PgtPlan &w, const PgtLine &t,
                                                 const PgtLens &L, int s, int hq) {
   PgtPieces r{0, 0, 0, 0, 0, 0};
   if (L.len[s] == 0) return r;
   const int hkv = hq / w.G, g = hq % w.G;
   if (w.prefix_tiles > 0) {
     const int R = s * w.G + g, seg = hkv * w.prefix_groups + R / 16;
-    const long long a = (long long)seg * w.prefix_tiles;
-    const int c0 = pgt_cta_of(t, a), c1 = pgt_cta_of(t, a + w.prefix_tiles - 1);
+    const int a = seg * (w.prefix_tiles + kPgtHead) + kPgtHead;
+    const int c0 = t.cta_of(a), c1 = t.cta_of(a + w.prefix_tiles - 1);
     r.pre0 = c0 + seg;
     r.npre = c1 - c0 + 1;
     r.pre_row = R % 16;
   }
-  const int n = L.cum[s + 1] - L.cum[s];
-  if (n > 0) {
+  const int units = L.cum[s + 1] - L.cum[s];
+  if (units > 0) {
     const int h = hkv * w.own_groups + g / 16;
-    const long long a = t.prefix + (long long)L.cum[s] * t.per_own + (long long)h * n;
-    const int c0 = pgt_cta_of(t, a), c1 = pgt_cta_of(t, a + n - 1);
+    const int a = t.prefix + L.cum[s] * t.per_own + h * units + kPgtHead;
+    const int c0 = t.cta_of(a), c1 = t.cta_of(a + units - kPgtHead - 1);
     r.own0 = c0 + s * t.per_own + h;
     r.nown = c1 - c0 + 1;
     r.own_row = g % 16;
@@ -319,38 +366,41 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, u
 }
 
 // Let the copies in flight land before the CTA exits after a timeout.
-__device__ __forceinline__ void drain(uint64_t *full, int stages, long long issued) {
-  for (long long st = issued > stages ? issued - stages : 0; st < issued; ++st) {
+__device__ __forceinline__ void drain(uint64_t *full, int stages, int issued) {
+  for (int st = issued > stages ? issued - stages : 0; st < issued; ++st) {
     const unsigned long long t0 = globaltimer();
     while (!mbar_try_wait(&full[st % stages], (uint32_t)((st / stages) & 1)))
       if (globaltimer() - t0 > 100ull * 1000ull * 1000ull) break;
   }
 }
 
-// Producer warp: fills the ring with the CTA's tiles i0 .. i1 - 1 of K or V.
-// Lane i brings page piece i of a tile.  One warp issues about one dependent
-// instruction every 5 cycles, and a tile has 0.7 us at HBM rate, so the loop is
-// short: no divisions, one table entry per lane, fetched a tile ahead.
+// Producer warp: fills the ring with the tiles of the stretch [from, to) of K or
+// V.  Lane i brings page piece i of a tile.  One warp issues about one
+// dependent instruction every 5 cycles, and a tile has 0.7 us at HBM rate, so
+// the loop is short: no divisions, one table entry per lane, fetched a tile
+// ahead.
 template <int D>
-__device__ void produce(const PagedDecode &p, const PgtPlan &w, const PgtTiles &tt, const PgtLens &L, PgtRing<D> &ring,
-                        const CUtensorMap *map, uint32_t base, int stages, long long i0, long long i1,
+__device__ void produce(const PagedDecode &p, const PgtPlan &w, const PgtLine &line, const PgtLens &L,
+                        PgtRing<D> &ring, const CUtensorMap *map, uint32_t base, int stages, int from, int to,
                         const WaitCtx &wc) {
   constexpr int TILE = pgt_tile(D);
   const int lane = threadIdx.x % 32, sh = w.page_shift, ps = 1 << sh;
   const int rows = min(ps, TILE), rsh = min(sh, D == 64 ? 7 : 6);
   int slot = 0;
   uint32_t parity = 1;
-  long long st = 0;
-  for (long long i = i0; i < i1;) {
-    const PgtSeg g = pgt_seg(p, w, tt, L, i);
-    const int n = (int)min((long long)g.left, i1 - i);
+  PgtSeg g;
+  int issued = 0;
+  for (g.start(p, w, line, L, from, to); g.n > 0; g.next(p, w, line, L)) {
     const int32_t *table = g.s >= 0 ? p.c.page_table + (size_t)g.s * p.c.max_pages : p.prefix_table;
     int key = g.key0 + lane * rows;                                   // this lane's piece
     const int limit = lane * rows < TILE ? g.end : 0;                 // lanes past the tile bring nothing
     int page = key < limit ? __ldg(table + (key >> sh)) : -1;
-    for (int k = 0; k < n; ++k, ++st) {
-      const int ahead = k + 1 < n && key + TILE < limit ? __ldg(table + ((key + TILE) >> sh)) : -1;
-      if (!warp_wait(&ring.empty[slot], parity, wc)) goto out;
+    for (int k = 0; k < g.n; ++k, ++issued) {
+      const int ahead = k + 1 < g.n && key + TILE < limit ? __ldg(table + ((key + TILE) >> sh)) : -1;
+      if (!warp_wait(&ring.empty[slot], parity, wc)) {
+        if (lane == 0) drain(ring.full, stages, issued);
+        return;
+      }
       const bool ok = (unsigned)page < (unsigned)p.c.num_pages;
       const uint32_t have = __ballot_sync(0xffffffffu, ok);
       if (!ok && key < limit) atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
@@ -369,10 +419,8 @@ __device__ void produce(const PagedDecode &p, const PgtPlan &w, const PgtTiles &
         parity ^= 1;
       }
     }
-    i += n;
   }
-out:
-  if (ring.abort_word && lane == 0) drain(ring.full, stages, st);
+  if (ring.abort_word && lane == 0) drain(ring.full, stages, issued);
 }
 
 extern __shared__ __align__(1024) uint8_t pgt_smem_raw[];
@@ -394,12 +442,12 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
   pdl_launch_dependents();
   if (tid == 0) ring.init(stages, WARPS);
   pgt_load_lens<pgt_threads(D)>(p, w, L, blockIdx.x == 0 ? p.status : nullptr);
-  const PgtTiles tt = pgt_tiles(p, w, L);
-  const long long i0 = pgt_first(tt, blockIdx.x), i1 = pgt_first(tt, blockIdx.x + 1);
+  const PgtLine line = pgt_line(p, w, L);
+  const int from = line.first(blockIdx.x), to = line.first(blockIdx.x + 1);
   const WaitCtx wc{&ring.abort_word, p.status};
   const uint32_t base = smem_u32(pgt_smem_base());
   if (warp == WARPS) {
-    produce<D>(p, w, tt, L, ring, &kmap, base, stages, i0, i1, wc);
+    produce<D>(p, w, line, L, ring, &kmap, base, stages, from, to, wc);
     return;
   }
   const int gid = lane / 4, t = lane % 4;
@@ -407,9 +455,9 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
   const int row = warp * 16 + group_key(lane & 7, lane >> 4);
   int slot = 0;
   uint32_t parity = 0;
-  for (long long i = i0; i < i1;) {
-    PgtSeg g = pgt_seg(p, w, tt, L, i);
-    const int n = (int)min((long long)g.left, i1 - i);
+  PgtSeg g;
+  for (g.start(p, w, line, L, from, to); g.n > 0; g.next(p, w, line, L)) {
+    const int n = g.n;
     const int tiles = __any_sync(0xffffffffu, ring.abort_word != 0) ? 0 : n;   // a wait gave up: touch no barrier again
     // Q rows as the A operand; rows past the segment's are 0
     uint32_t qa[KS][4] = {};
@@ -504,7 +552,6 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
       ml[tid] = make_float2(M, S);
     }
     named_bar_sync(1, WARPS * 32);
-    i += n;
   }
 }
 
@@ -538,13 +585,13 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
   pdl_launch_dependents();
   if (tid == 0) ring.init(V::kStages, V::kStepsPerTile);
   pgt_load_lens<V::kThreads>(p, w, L, nullptr);
-  const PgtTiles tt = pgt_tiles(p, w, L);
-  const long long i0 = pgt_first(tt, blockIdx.x), i1 = pgt_first(tt, blockIdx.x + 1);
+  const PgtLine line = pgt_line(p, w, L);
+  const int from = line.first(blockIdx.x), to = line.first(blockIdx.x + 1);
   const WaitCtx wc{&ring.abort_word, p.status};
   uint8_t *const smem = pgt_smem_base();
   const uint32_t base = smem_u32(smem);
   if (warp == WARPS) {   // the values do not depend on the first pass
-    produce<D>(p, w, tt, L, ring, &vmap, base, V::kStages, i0, i1, wc);
+    produce<D>(p, w, line, L, ring, &vmap, base, V::kStages, from, to, wc);
     return;
   }
   uint8_t *const mine = smem + V::kStages * 16384 + warp * V::kWarpBytes;
@@ -556,12 +603,12 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
   // lane -> row: matrices (k half 0, n 0-7), (k half 1, n 0-7), (k half 0, n 8-15), (k half 1, n 8-15)
   const int vrow = sub + group_key(lane & 7, (lane >> 3) & 1);
   pdl_wait();
-  for (long long i = i0; i < i1;) {
-    PgtSeg g = pgt_seg(p, w, tt, L, i);
-    const int n = (int)min((long long)g.left, i1 - i);
+  PgtSeg g;
+  for (g.start(p, w, line, L, from, to); g.n > 0; g.next(p, w, line, L)) {
+    const int n = g.n;
     // the warp's first tile of the piece: tile x of the CTA's run goes to the
     // warps x % kTileStride, whatever the pieces
-    const int tile0 = (warp / V::kStepsPerTile + V::kTileStride - (int)((i - i0) % V::kTileStride)) % V::kTileStride;
+    const int tile0 = (warp / V::kStepsPerTile + V::kTileStride - g.run % V::kTileStride) % V::kTileStride;
     int steps = n > tile0 ? (n - tile0 + V::kTileStride - 1) / V::kTileStride : 0;
     if (__any_sync(0xffffffffu, ring.abort_word != 0)) steps = 0;    // a wait gave up: touch no barrier again
     const int step0 = g.key0 + tile0 * TILE + sub;                   // its first key
@@ -615,7 +662,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
     for (int r = warp; r < g.nrows; r += WARPS) {
       int s, hq;
       g.row(w.G, r, s, hq);
-      const PgtPieces pc = pgt_pieces(p, w, tt, L, s, hq);
+      const PgtPieces pc = pgt_pieces(p, w, line, L, s, hq);
       const float2 *pre = reinterpret_cast<const float2 *>(p.ws + w.pre_ml_off);
       const float2 *own = reinterpret_cast<const float2 *>(p.ws + w.own_ml_off);
       float m = -INFINITY, l = 0.f;
@@ -699,7 +746,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
       for (int a = 0; a < AHEAD; ++a)
 #pragma unroll
         for (int hh = 0; hh < HH; ++hh) pages[a][hh] = pages[a + 1][hh];
-      const int st = (int)(i - i0) + tile0 + k * V::kTileStride;       // the tile's place in the ring
+      const int st = g.run + tile0 + k * V::kTileStride;       // the tile's place in the ring
       const int slot = st % V::kStages;
       if (!warp_wait(&ring.full[slot], (uint32_t)((st / V::kStages) & 1), wc)) break;
       const uint32_t tile = base + slot * 16384;
@@ -784,7 +831,6 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
       part[tid * acc_stride(D) + D] = a;
     }
     named_bar_sync(1, WARPS * 32);
-    i += n;
   }
 }
 
@@ -798,10 +844,10 @@ __global__ void __launch_bounds__(kPgtCombThreads) pgt_combine(PagedDecode p, Pg
   __shared__ float s_a[WAYS][D], s_r[WAYS];
   const int tid = threadIdx.x, e = tid % D, way = tid / D;
   pgt_load_lens<kPgtCombThreads>(p, w, L, nullptr);
-  const PgtTiles tt = pgt_tiles(p, w, L);
+  const PgtLine line = pgt_line(p, w, L);
   pdl_wait();
   const int s = blockIdx.x / p.c.Hq, hq = blockIdx.x % p.c.Hq;
-  const PgtPieces pc = pgt_pieces(p, w, tt, L, s, hq);
+  const PgtPieces pc = pgt_pieces(p, w, line, L, s, hq);
   const float *pre = reinterpret_cast<const float *>(p.ws + w.pre_acc_off) + pc.pre_row * acc_stride(D);
   const float *own = reinterpret_cast<const float *>(p.ws + w.own_acc_off) + pc.own_row * acc_stride(D);
   float a = 0.f, rs = 0.f;
