@@ -9,7 +9,6 @@ namespace da {
 size_t pgs_workspace(int64_t rows, int max_len, int prefix_len, int d);
 cudaError_t launch_paged_decode_simt(const PagedDecode &p, cudaStream_t stream);
 size_t pgt_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len);
-bool pgt_serves(int S, int dtype);
 bool pgt_fits(int S, int Hq, int Hkv, int d, int max_len, int prefix_len);
 int launch_paged_decode_bf16(const PagedDecode &p, cudaStream_t stream);
 }  // namespace da
@@ -149,8 +148,8 @@ int check_cache(const dilution_attn_paged_cache *c) {
 }
 
 size_t decode_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int dtype) {
-  return pgt_serves(S, dtype) ? pgt_workspace(S, Hq, Hkv, d, max_len, prefix_len)
-                              : pgs_workspace((int64_t)S * Hq, max_len, prefix_len, d);
+  return dtype == DA_BF16 ? pgt_workspace(S, Hq, Hkv, d, max_len, prefix_len)
+                          : pgs_workspace((int64_t)S * Hq, max_len, prefix_len, d);
 }
 
 int check_workspace(const void *ws, size_t bytes, size_t need) {
@@ -257,10 +256,13 @@ int dilution_attn_paged_decode(const void *q, const dilution_attn_paged_cache *c
   st = check_workspace(workspace, workspace_bytes, decode_workspace(c.S, c.Hq, c.Hkv, c.d, max_len, prefix_len, c.dtype));
   if (st != DA_OK) return st;
   if ((int64_t)c.num_pages * c.Hkv > 0x7FFFFFFF) return DA_ERR_UNSUPPORTED;   // a copy's coordinate
-  // the launch grids' third dimension counts 16-row groups
+  // what the kernels count in 32 bits: places in the demand pool (16 floats
+  // each), work units (bf16), 16-row groups of a launch grid (fp32)
+  if ((int64_t)c.num_demand_pages * c.Hq * (c.page_size / 16) >= 0xFFFFFFFFll) return DA_ERR_UNSUPPORTED;
   const int64_t G = c.Hq / c.Hkv;
-  if (c.S * ((G + 15) / 16) + (c.S * G + 15) / 16 > 65535 || c.Hkv > 65535) return DA_ERR_UNSUPPORTED;
-  if (pgt_serves(c.S, c.dtype) && !pgt_fits(c.S, c.Hq, c.Hkv, c.d, max_len, prefix_len)) return DA_ERR_UNSUPPORTED;
+  if (c.dtype == DA_BF16 ? !pgt_fits(c.S, c.Hq, c.Hkv, c.d, max_len, prefix_len)
+                         : c.S * ((G + 15) / 16) + (c.S * G + 15) / 16 > 65535)
+    return DA_ERR_UNSUPPORTED;
   PagedDecode p{};
   p.c = c;
   p.q = q;
@@ -275,7 +277,7 @@ int dilution_attn_paged_decode(const void *q, const dilution_attn_paged_cache *c
   p.earlier = (flags & DA_FLAG_EARLIER_DEMAND_ONLY) != 0;
   p.status = reinterpret_cast<int *>(workspace);
   p.ws = reinterpret_cast<uint8_t *>(workspace);
-  if (pgt_serves(c.S, c.dtype)) return launch_paged_decode_bf16(p, reinterpret_cast<cudaStream_t>(stream));
+  if (c.dtype == DA_BF16) return launch_paged_decode_bf16(p, reinterpret_cast<cudaStream_t>(stream));
   return launch_paged_decode_simt(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 

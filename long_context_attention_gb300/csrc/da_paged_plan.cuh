@@ -1,0 +1,326 @@
+// The bf16 paged decode step's plan: workspace layout, the line of work units
+// that the CTAs share, and where each row's partial results lie.  Shared by the
+// streaming kernels (paged_decode_bf16.cu) and those of a prefix with many rows
+// (paged_prefix_bf16.cu).
+#pragma once
+
+#include "da_paged.h"
+#include "da_ptx.cuh"
+
+namespace da {
+
+constexpr int kPgtMaxSeqs = 832;                  // lengths kept in shared memory (a larger batch goes in parts)
+DA_HD constexpr int pgt_tile(int d) { return d == 64 ? 128 : 64; }   // keys per stage (16 KB of K or V)
+DA_HD constexpr int pgt_warps(int d) { return pgt_tile(d) / 16; }    // pgt_keys: consumer warps, 16 keys of a stage each
+DA_HD constexpr int pgt_threads(int d) { return 32 * pgt_warps(d) + 32; }   // and the producer warp
+constexpr int kPgtMaxCtas = 2 * 152;              // two resident CTAs on each SM
+
+constexpr int kPgtHead = 4;   // units of a segment before its first tile (a piece costs ~2 us beside its tiles' 0.5 us)
+
+// Rows of the batch at the prefix (sequences x query heads of one key head)
+// from which the tcgen05 kernels take it: they work on 64 rows at a time, the
+// streaming kernels on 16 and read the prefix's keys from L2 once per 16 rows.
+constexpr int kPgxMinRows = 17;
+constexpr int kPgxRows = 64;      // rows of a segment there
+constexpr int kPgxTile = 128;     // keys of a tile
+constexpr int kPgxCtas = 152;     // pgx_values: one CTA an SM
+constexpr int kPgxKeyCtas = 304;  // pgx_keys: two
+
+// Equal cut of `total` units into stretches of base or base + 1.
+struct PgtCut {
+  int total, ctas, base, rem;
+  DA_HD int first(int cta) const { return cta < ctas ? cta * base + (cta < rem ? cta : rem) : total; }
+  DA_HD int cta_of(int unit) const {   // total > 0
+    const int cut = rem * (base + 1);
+    return unit < cut ? unit / (base + 1) : rem + (unit - cut) / base;
+  }
+};
+DA_HD PgtCut pgt_cut(int total, int ctas) {   // no stretch without a unit
+  PgtCut c;
+  c.total = total;
+  c.ctas = ctas < total ? ctas : total;
+  if (c.ctas < 1) c.ctas = 1;
+  c.base = total / c.ctas;
+  c.rem = total - c.base * c.ctas;
+  return c;
+}
+
+// Host plan of a call; slots and scratch offsets.
+struct PgtPlan {
+  int ctas, tile, page_shift, G, own_rows, own_groups, prefix_groups, prefix_tiles, own_segs, prefix_segs, Lp;
+  int logit_key0;                    // key of the logits' first column
+  int wide;                          // the prefix goes to the tcgen05 kernels: 64-row segments, their own cuts
+  int pre_rows;                      // rows of a prefix slot
+  int x_groups, x_tiles, x_segs;     // segments of the tcgen05 kernels
+  PgtCut x_keys, x_values;
+  size_t logit_off, own_ml_off, own_acc_off, pre_ml_off, pre_acc_off, total;
+};
+
+inline PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int page_size) {
+  PgtPlan w;
+  w.page_shift = 0;
+  while ((1 << w.page_shift) < page_size) ++w.page_shift;
+  w.G = Hq / Hkv;
+  w.own_rows = w.G < 16 ? w.G : 16;
+  w.own_groups = (w.G + 15) / 16;
+  w.tile = pgt_tile(d);
+  w.own_segs = S * Hkv * w.own_groups;
+  const int rows = S * w.G;
+  w.wide = prefix_len > 0 && rows >= kPgxMinRows;
+  const bool narrow = prefix_len > 0 && !w.wide;
+  w.prefix_tiles = narrow ? (prefix_len + w.tile - 1) / w.tile : 0;
+  w.prefix_groups = narrow ? (rows + 15) / 16 : 0;
+  w.prefix_segs = Hkv * w.prefix_groups;
+  w.x_tiles = w.wide ? (prefix_len + kPgxTile - 1) / kPgxTile : 0;
+  w.x_groups = w.wide ? (rows + kPgxRows - 1) / kPgxRows : 0;
+  w.x_segs = Hkv * w.x_groups;
+  w.x_keys = pgt_cut(w.x_segs * w.x_tiles, kPgxKeyCtas);
+  w.x_values = pgt_cut(w.x_segs * w.x_tiles, kPgxCtas);
+  w.pre_rows = w.wide ? kPgxRows : 16;
+  w.logit_key0 = w.wide ? prefix_len : 0;
+  const int64_t own_tiles = (max_len - prefix_len + w.tile - 1) / w.tile;
+  const int64_t most = w.own_segs * (own_tiles > 0 ? own_tiles + kPgtHead : 0) +
+                       (int64_t)w.prefix_segs * (w.prefix_tiles + kPgtHead);   // units of the line
+  w.ctas = (int)(most < 1 ? 1 : most > kPgtMaxCtas ? kPgtMaxCtas : most);
+  w.Lp = (int)round_up(max_len - w.logit_key0, 16);
+  // slots for the most CTAs: their size depends on the prefix's presence alone
+  const int64_t own_slots = kPgtMaxCtas + w.own_segs;
+  const int64_t pre_slots = prefix_len > 0 ? kPgtMaxCtas + w.prefix_segs + w.x_segs : 0;
+  auto next = [](size_t off, int64_t bytes) { return (size_t)round_up((int64_t)off + bytes, 256); };
+  w.logit_off = kStatusBytes;
+  w.own_ml_off = next(w.logit_off, (int64_t)S * Hq * w.Lp * 4);
+  w.own_acc_off = next(w.own_ml_off, own_slots * w.own_rows * 8);
+  w.pre_ml_off = next(w.own_acc_off, own_slots * w.own_rows * acc_stride(d) * 4);
+  w.pre_acc_off = next(w.pre_ml_off, pre_slots * w.pre_rows * 8);
+  w.total = next(w.pre_acc_off, pre_slots * w.pre_rows * acc_stride(d) * 4);
+  return w;
+}
+
+#if defined(__CUDACC__)
+// ------------------------------------------------------------------ device plan
+// Lengths of the sequences and the units of one of their segments, summed, in
+// shared memory.
+struct PgtLens {
+  int len[kPgtMaxSeqs];
+  int cum[kPgtMaxSeqs + 1];   // of the sequences before
+  int warp_sum[32];
+};
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// All threads of the block: fills L; ends with a block barrier.
+template <int THREADS>
+__device__ void pgt_load_lens(const PagedDecode &p, const PgtPlan &w, PgtLens &L, int *status) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, S = p.c.S;
+  const int per = (S + THREADS - 1) / THREADS;
+  const int s0 = min(tid * per, S), s1 = min(s0 + per, S);
+  int sum = 0;
+  for (int s = s0; s < s1; ++s) {
+    const int n = paged_len(p, s, status);
+    L.len[s] = n;
+    L.cum[s] = sum;
+    if (n > p.prefix_len) sum += kPgtHead + (n - p.prefix_len + w.tile - 1) / w.tile;
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) L.warp_sum[warp] = inc;
+  __syncthreads();
+  int base = inc - sum;
+  for (int i = 0; i < warp; ++i) base += L.warp_sum[i];
+  for (int s = s0; s < s1; ++s) L.cum[s] += base;
+  if (tid == THREADS - 1) L.cum[S] = base + sum;
+  __syncthreads();
+}
+
+// The line: the prefix's segments first, then each sequence's; and its cut.
+struct PgtLine {
+  int prefix;          // units of the prefix
+  int per_own;         // segments of one sequence
+  PgtCut cut;
+};
+__device__ __forceinline__ PgtLine pgt_line(const PagedDecode &p, const PgtPlan &w, const PgtLens &L) {
+  PgtLine t;
+  t.per_own = p.c.Hkv * w.own_groups;
+  t.prefix = w.prefix_segs > 0 ? w.prefix_segs * (w.prefix_tiles + kPgtHead) : 0;
+  t.cut = pgt_cut(t.prefix + L.cum[p.c.S] * t.per_own, w.ctas);
+  return t;
+}
+
+// One piece of a segment.
+struct PgtSeg {
+  int s;                     // its sequence; -1: the prefix
+  int hkv, row0, nrows;      // rows row0 .. of the sequence's group / of the batch
+  int key0, end;             // the piece's first key and the segment's end
+  int n;                     // tiles of the piece (0: none left)
+  int seg;                   // its number among the prefix's or the sequences' segments
+  int run;                   // tiles of the CTA's pieces before this one
+  int unit, tiles, stop;     // place of its first tile, tiles of the segment, the stretch's end
+  __device__ __forceinline__ void row(int G, int r, int &seq, int &hq) const {
+    if (s >= 0) {
+      seq = s;
+      hq = hkv * G + row0 + r;
+    } else {
+      seq = (row0 + r) / G;
+      hq = hkv * G + (row0 + r) % G;
+    }
+  }
+  // Rows, keys and piece from s, seg, unit and the piece's first tile.
+  __device__ __forceinline__ void fill(const PagedDecode &p, const PgtPlan &w, const PgtLine &t, const PgtLens &L,
+                                       int tile) {
+    const int left = tiles - tile;
+    n = min(left, stop - unit);
+    if (s < 0) {
+      hkv = seg / w.prefix_groups;
+      row0 = seg % w.prefix_groups * 16;
+      nrows = min(16, p.c.S * w.G - row0);
+      key0 = tile * w.tile;
+      end = p.prefix_len;
+    } else {
+      const int h = seg - s * t.per_own;
+      hkv = h / w.own_groups;
+      row0 = h % w.own_groups * 16;
+      nrows = min(16, w.G - row0);
+      key0 = p.prefix_len + tile * w.tile;
+      end = L.len[s];
+    }
+  }
+  // The first piece of the stretch [from, to).
+  __device__ void start(const PagedDecode &p, const PgtPlan &w, const PgtLine &t, const PgtLens &L, int from, int to) {
+    stop = to;
+    run = 0;
+    n = 0;
+    if (from >= to) return;
+    int u;   // place inside the segment
+    if (from < t.prefix) {
+      s = -1;
+      tiles = w.prefix_tiles;
+      seg = from / (tiles + kPgtHead);
+      u = from - seg * (tiles + kPgtHead);
+    } else {
+      const int x = from - t.prefix, q = x / t.per_own;
+      int lo = 0, hi = p.c.S - 1;   // the last sequence with cum <= q: one with units of its own
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (L.cum[mid] <= q)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      const int units = L.cum[lo + 1] - L.cum[lo], r = x - L.cum[lo] * t.per_own, h = r / units;
+      s = lo;
+      tiles = units - kPgtHead;
+      seg = lo * t.per_own + h;
+      u = r - h * units;
+    }
+    const int tile = max(0, u - kPgtHead);
+    unit = from + (tile + kPgtHead - u);
+    fill(p, w, t, L, tile);
+  }
+  // The piece after this one.
+  __device__ void next(const PagedDecode &p, const PgtPlan &w, const PgtLine &t, const PgtLens &L) {
+    run += n;
+    unit += n + kPgtHead;   // the next segment's first tile, if this piece ends its segment
+    if (unit >= stop) {
+      n = 0;
+      return;
+    }
+    ++seg;
+    if (s < 0 ? seg == w.prefix_segs : seg == (s + 1) * t.per_own) {   // on to the next sequence with keys of its own
+      int k = s + 1;
+      while (L.cum[k + 1] == L.cum[k]) ++k;   // there is one: the line goes on
+      s = k;
+      seg = k * t.per_own;
+      tiles = L.cum[k + 1] - L.cum[k] - kPgtHead;
+    }
+    fill(p, w, t, L, 0);
+  }
+};
+
+// Slots of the pieces of row (s, hq): the prefix's and its own.
+struct PgtPieces {
+  int pre0, npre, pre_row;   // first slot, count, row inside the slot
+  int own0, nown, own_row;
+};
+// `values`: of the second pass (the tcgen05 kernels cut the two passes differently).
+__device__ __forceinline__ PgtPieces pgt_pieces(const PagedDecode &p, const PgtPlan &w, const PgtLine &t,
+                                                const PgtLens &L, int s, int hq, bool values) {
+  PgtPieces r{0, 0, 0, 0, 0, 0};
+  if (L.len[s] == 0) return r;
+  const int hkv = hq / w.G, g = hq % w.G;
+  if (w.wide) {
+    const int R = s * w.G + g, seg = hkv * w.x_groups + R / kPgxRows;
+    const PgtCut &c = values ? w.x_values : w.x_keys;
+    const int c0 = c.cta_of(seg * w.x_tiles), c1 = c.cta_of(seg * w.x_tiles + w.x_tiles - 1);
+    r.pre0 = c0 + seg;
+    r.npre = c1 - c0 + 1;
+    r.pre_row = R % kPgxRows;
+  } else if (w.prefix_tiles > 0) {
+    const int R = s * w.G + g, seg = hkv * w.prefix_groups + R / 16;
+    const int a = seg * (w.prefix_tiles + kPgtHead) + kPgtHead;
+    const int c0 = t.cut.cta_of(a), c1 = t.cut.cta_of(a + w.prefix_tiles - 1);
+    r.pre0 = c0 + seg;
+    r.npre = c1 - c0 + 1;
+    r.pre_row = R % 16;
+  }
+  const int units = L.cum[s + 1] - L.cum[s];
+  if (units > 0) {
+    const int h = hkv * w.own_groups + g / 16;
+    const int a = t.prefix + L.cum[s] * t.per_own + h * units + kPgtHead;
+    const int c0 = t.cut.cta_of(a), c1 = t.cut.cta_of(a + units - kPgtHead - 1);
+    r.own0 = c0 + s * t.per_own + h;
+    r.nown = c1 - c0 + 1;
+    r.own_row = g % 16;
+  }
+  return r;
+}
+
+// lse2 of row (s, hq), by one warp (the same value in every lane): its pieces'
+// (max, sum) joined.
+__device__ __forceinline__ float pgt_row_lse(const PagedDecode &p, const PgtPlan &w, const PgtLine &t,
+                                             const PgtLens &L, int s, int hq, int lane) {
+  const PgtPieces pc = pgt_pieces(p, w, t, L, s, hq, false);
+  const float2 *pre = reinterpret_cast<const float2 *>(p.ws + w.pre_ml_off);
+  const float2 *own = reinterpret_cast<const float2 *>(p.ws + w.own_ml_off);
+  float m = -INFINITY, l = 0.f;
+  for (int c = lane; c < pc.npre + pc.nown; c += 32) {
+    const float2 ml = c < pc.npre ? pre[(size_t)(pc.pre0 + c) * w.pre_rows + pc.pre_row]
+                                  : own[(size_t)(pc.own0 + c - pc.npre) * w.own_rows + pc.own_row];
+    const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
+    l = l * ex2_approx(m - ms) + ml.y * ex2_approx(ml.x - ms);
+    m = mn;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+    const float mn = fmaxf(m, m2), ms = mn == -INFINITY ? 0.f : mn;
+    l = l * ex2_approx(m - ms) + l2 * ex2_approx(m2 - ms);
+    m = mn;
+  }
+  return m + log2f(l);
+}
+
+// Launch that may begin before its predecessor in the stream has finished (the
+// kernel waits with pdl_wait where it needs the predecessor's results).
+template <typename... KArgs, typename... Args>
+static cudaError_t launch_after(void (*kernel)(KArgs...), int grid, int threads, int smem, cudaStream_t stream,
+                                Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#endif  // __CUDACC__
+
+}  // namespace da

@@ -347,8 +347,6 @@ static cudaError_t launch_pgs_t(const PagedDecode &p, cudaStream_t stream) {
 }
 
 cudaError_t launch_paged_decode_simt(const PagedDecode &p, cudaStream_t stream) {
-  if (p.c.dtype == DA_BF16)
-    return p.c.d == 128 ? launch_pgs_t<__nv_bfloat16, 128>(p, stream) : launch_pgs_t<__nv_bfloat16, 64>(p, stream);
   return p.c.d == 128 ? launch_pgs_t<float, 128>(p, stream) : launch_pgs_t<float, 64>(p, stream);
 }
 

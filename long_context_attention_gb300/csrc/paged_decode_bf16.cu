@@ -34,22 +34,14 @@
 // pgt_keys).  The part of a segment inside one stretch is a piece and leaves
 // one partial result, in slot (CTA + segment), which grows along the line and
 // is therefore unique.
-#include "da_paged.h"
-#include "da_ptx.cuh"
+#include "da_paged_plan.cuh"
 
 #include <cuda.h>
 #include <cuda_bf16.h>
 
 namespace da {
 
-constexpr int kPgtMaxSeqs = 1024;                 // lengths kept in shared memory
-DA_HD constexpr int pgt_tile(int d) { return d == 64 ? 128 : 64; }   // keys per stage (16 KB of K or V)
-DA_HD constexpr int pgt_warps(int d) { return pgt_tile(d) / 16; }    // pgt_keys: consumer warps, 16 keys of a stage each
-DA_HD constexpr int pgt_threads(int d) { return 32 * pgt_warps(d) + 32; }   // and the producer warp
 constexpr int kPgtSmemPerCta = 100 * 1024;        // two CTAs an SM beside their static shared memory
-constexpr int kPgtMaxCtas = 2 * 152;              // two resident CTAs on each SM
-
-constexpr int kPgtHead = 4;   // units of a segment before its first tile (a piece costs ~2 us beside its tiles' 0.5 us)
 
 // pgt_values for up to GE rows of a segment (1, 2, 4, 8 or 16).
 template <int D, int GE>
@@ -77,236 +69,6 @@ struct PgtVal {
   static_assert(kStages >= 2 && kStages >= kTileStride, "a slot for every warp");
   static constexpr int kSmemBytes = 1024 + kStages * 16384 + kWarps * kWarpBytes;
 };
-
-// Host plan of a call; slots and scratch offsets.
-struct PgtPlan {
-  int ctas, tile, page_shift, G, own_rows, own_groups, prefix_groups, prefix_tiles, own_segs, prefix_segs, Lp;
-  size_t logit_off, own_ml_off, own_acc_off, pre_ml_off, pre_acc_off, total;
-};
-
-// Units on the line at most (int arithmetic on the device).
-bool pgt_fits(int S, int Hq, int Hkv, int d, int max_len, int prefix_len) {
-  const int64_t G = Hq / Hkv, tile = pgt_tile(d), rows = (S * G + 15) / 16;
-  const int64_t own = (max_len - prefix_len + tile - 1) / tile + kPgtHead, pre = (prefix_len + tile - 1) / tile + kPgtHead;
-  return S * (int64_t)Hkv * ((G + 15) / 16) * own + (prefix_len > 0 ? Hkv * rows * pre : 0) < 0x7FFF0000ll;
-}
-
-static PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int page_size = 16) {
-  PgtPlan w;
-  w.page_shift = 0;
-  while ((1 << w.page_shift) < page_size) ++w.page_shift;
-  w.G = Hq / Hkv;
-  w.own_rows = w.G < 16 ? w.G : 16;
-  w.own_groups = (w.G + 15) / 16;
-  w.tile = pgt_tile(d);
-  w.prefix_tiles = (prefix_len + w.tile - 1) / w.tile;
-  w.prefix_groups = prefix_len > 0 ? (S * w.G + 15) / 16 : 0;
-  w.own_segs = S * Hkv * w.own_groups;
-  w.prefix_segs = Hkv * w.prefix_groups;
-  const int64_t own_tiles = (max_len - prefix_len + w.tile - 1) / w.tile;
-  const int64_t most = w.own_segs * (own_tiles > 0 ? own_tiles + kPgtHead : 0) +
-                       (int64_t)w.prefix_segs * (w.prefix_tiles + kPgtHead);   // units of the line
-  w.ctas = (int)(most < 1 ? 1 : most > kPgtMaxCtas ? kPgtMaxCtas : most);
-  w.Lp = (int)round_up(max_len, 16);
-  // slots for the most CTAs, so that the size depends on the prefix's presence alone
-  const int64_t own_slots = kPgtMaxCtas + w.own_segs;
-  const int64_t pre_slots = w.prefix_segs > 0 ? kPgtMaxCtas + w.prefix_segs : 0;
-  auto next = [](size_t off, int64_t bytes) { return (size_t)round_up((int64_t)off + bytes, 256); };
-  w.logit_off = kStatusBytes;
-  w.own_ml_off = next(w.logit_off, (int64_t)S * Hq * w.Lp * 4);
-  w.own_acc_off = next(w.own_ml_off, own_slots * w.own_rows * 8);
-  w.pre_ml_off = next(w.own_acc_off, own_slots * w.own_rows * acc_stride(d) * 4);
-  w.pre_acc_off = next(w.pre_ml_off, pre_slots * 16 * 8);
-  w.total = next(w.pre_acc_off, pre_slots * 16 * acc_stride(d) * 4);
-  return w;
-}
-size_t pgt_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len) {
-  return pgt_plan(S, Hq, Hkv, d, max_len, prefix_len).total;
-}
-bool pgt_serves(int S, int dtype) { return dtype == DA_BF16 && S <= kPgtMaxSeqs; }
-
-// ------------------------------------------------------------------ device plan
-// Lengths of the sequences and the units of one of their segments, summed, in
-// shared memory.
-struct PgtLens {
-  int len[kPgtMaxSeqs];
-  int cum[kPgtMaxSeqs + 1];   // of the sequences before
-  int warp_sum[32];
-};
-
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-// All threads of the block: fills L; ends with a block barrier.
-template <int THREADS>
-__device__ void pgt_load_lens(const PagedDecode &p, const PgtPlan &w, PgtLens &L, int *status) {
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, S = p.c.S;
-  const int per = (S + THREADS - 1) / THREADS;
-  const int s0 = min(tid * per, S), s1 = min(s0 + per, S);
-  int sum = 0;
-  for (int s = s0; s < s1; ++s) {
-    const int n = paged_len(p, s, status);
-    L.len[s] = n;
-    L.cum[s] = sum;
-    if (n > p.prefix_len) sum += kPgtHead + (n - p.prefix_len + w.tile - 1) / w.tile;
-  }
-  int inc = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
-  }
-  if (lane == 31) L.warp_sum[warp] = inc;
-  __syncthreads();
-  int base = inc - sum;
-  for (int i = 0; i < warp; ++i) base += L.warp_sum[i];
-  for (int s = s0; s < s1; ++s) L.cum[s] += base;
-  if (tid == THREADS - 1) L.cum[S] = base + sum;
-  __syncthreads();
-}
-
-// The line: the prefix's segments first, then each sequence's; and its cut into
-// stretches of base or base + 1 units.
-struct PgtLine {
-  int total, prefix;   // units; the prefix's
-  int per_own;         // segments of one sequence
-  int ctas, base, rem;
-  __device__ __forceinline__ int first(int cta) const { return cta < ctas ? cta * base + min(cta, rem) : total; }
-  __device__ __forceinline__ int cta_of(int unit) const {   // total > 0
-    const int cut = rem * (base + 1);
-    return unit < cut ? unit / (base + 1) : rem + (unit - cut) / base;
-  }
-};
-__device__ __forceinline__ PgtLine pgt_line(const PagedDecode &p, const PgtPlan &w, const PgtLens &L) {
-  PgtLine t;
-  t.per_own = p.c.Hkv * w.own_groups;
-  t.prefix = w.prefix_segs > 0 ? w.prefix_segs * (w.prefix_tiles + kPgtHead) : 0;
-  t.total = t.prefix + L.cum[p.c.S] * t.per_own;
-  t.ctas = max(1, min(w.ctas, t.total));   // no stretch without a unit
-  t.base = t.total / t.ctas;
-  t.rem = t.total - t.base * t.ctas;
-  return t;
-}
-
-// One piece of a segment.
-struct PgtSeg {
-  int s;                     // its sequence; -1: the prefix
-  int hkv, row0, nrows;      // rows row0 .. of the sequence's group / of the batch
-  int key0, end;             // the piece's first key and the segment's end
-  int n;                     // tiles of the piece (0: none left)
-  int seg;                   // its number among the prefix's or the sequences' segments
-  int run;                   // tiles of the CTA's pieces before this one
-  int unit, tiles, stop;     // place of its first tile, tiles of the segment, the stretch's end
-  __device__ __forceinline__ void row(int G, int r, int &seq, int &hq) const {
-    if (s >= 0) {
-      seq = s;
-      hq = hkv * G + row0 + r;
-    } else {
-      seq = (row0 + r) / G;
-      hq = hkv * G + (row0 + r) % G;
-    }
-  }
-  // Rows, keys and piece from s, seg, unit and the piece's first tile.
-  __device__ __forceinline__ void fill(const PagedDecode &p, const PgtPlan &w, const PgtLine &t, const PgtLens &L,
-                                       int tile) {
-    const int left = tiles - tile;
-    n = min(left, stop - unit);
-    if (s < 0) {
-      hkv = seg / w.prefix_groups;
-      row0 = seg % w.prefix_groups * 16;
-      nrows = min(16, p.c.S * w.G - row0);
-      key0 = tile * w.tile;
-      end = p.prefix_len;
-    } else {
-      const int h = seg - s * t.per_own;
-      hkv = h / w.own_groups;
-      row0 = h % w.own_groups * 16;
-      nrows = min(16, w.G - row0);
-      key0 = p.prefix_len + tile * w.tile;
-      end = L.len[s];
-    }
-  }
-  // The first piece of the stretch [from, to).
-  __device__ void start(const PagedDecode &p, const PgtPlan &w, const PgtLine &t, const PgtLens &L, int from, int to) {
-    stop = to;
-    run = 0;
-    n = 0;
-    if (from >= to) return;
-    int u;   // place inside the segment
-    if (from < t.prefix) {
-      s = -1;
-      tiles = w.prefix_tiles;
-      seg = from / (tiles + kPgtHead);
-      u = from - seg * (tiles + kPgtHead);
-    } else {
-      const int x = from - t.prefix, q = x / t.per_own;
-      int lo = 0, hi = p.c.S - 1;   // the last sequence with cum <= q: one with units of its own
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (L.cum[mid] <= q)
-          lo = mid;
-        else
-          hi = mid - 1;
-      }
-      const int units = L.cum[lo + 1] - L.cum[lo], r = x - L.cum[lo] * t.per_own, h = r / units;
-      s = lo;
-      tiles = units - kPgtHead;
-      seg = lo * t.per_own + h;
-      u = r - h * units;
-    }
-    const int tile = max(0, u - kPgtHead);
-    unit = from + (tile + kPgtHead - u);
-    fill(p, w, t, L, tile);
-  }
-  // The piece after this one.
-  __device__ void next(const PagedDecode &p, const PgtPlan &w, const PgtLine &t, const PgtLens &L) {
-    run += n;
-    unit += n + kPgtHead;   // the next segment's first tile, if this piece ends its segment
-    if (unit >= stop) {
-      n = 0;
-      return;
-    }
-    ++seg;
-    if (s < 0 ? seg == w.prefix_segs : seg == (s + 1) * t.per_own) {   // on to the next sequence with keys of its own
-      int k = s + 1;
-      while (L.cum[k + 1] == L.cum[k]) ++k;   // there is one: the line goes on
-      s = k;
-      seg = k * t.per_own;
-      tiles = L.cum[k + 1] - L.cum[k] - kPgtHead;
-    }
-    fill(p, w, t, L, 0);
-  }
-};
-
-// Slots of the pieces of row (s, hq): the prefix's and its own.
-struct PgtPieces {
-  int pre0, npre, pre_row;   // first slot, count, row inside the slot
-  int own0, nown, own_row;
-};
-__device__ __forceinline__ PgtPieces pgt_pieces(const PagedDecode &p, const PgtPlan &w, const PgtLine &t,
-                                                const PgtLens &L, int s, int hq) {
-  PgtPieces r{0, 0, 0, 0, 0, 0};
-  if (L.len[s] == 0) return r;
-  const int hkv = hq / w.G, g = hq % w.G;
-  if (w.prefix_tiles > 0) {
-    const int R = s * w.G + g, seg = hkv * w.prefix_groups + R / 16;
-    const int a = seg * (w.prefix_tiles + kPgtHead) + kPgtHead;
-    const int c0 = t.cta_of(a), c1 = t.cta_of(a + w.prefix_tiles - 1);
-    r.pre0 = c0 + seg;
-    r.npre = c1 - c0 + 1;
-    r.pre_row = R % 16;
-  }
-  const int units = L.cum[s + 1] - L.cum[s];
-  if (units > 0) {
-    const int h = hkv * w.own_groups + g / 16;
-    const int a = t.prefix + L.cum[s] * t.per_own + h * units + kPgtHead;
-    const int c0 = t.cta_of(a), c1 = t.cta_of(a + units - kPgtHead - 1);
-    r.own0 = c0 + s * t.per_own + h;
-    r.nown = c1 - c0 + 1;
-    r.own_row = g % 16;
-  }
-  return r;
-}
 
 // ------------------------------------------------------------------ tensor pieces
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -443,7 +205,7 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
   if (tid == 0) ring.init(stages, WARPS);
   pgt_load_lens<pgt_threads(D)>(p, w, L, blockIdx.x == 0 ? p.status : nullptr);
   const PgtLine line = pgt_line(p, w, L);
-  const int from = line.first(blockIdx.x), to = line.first(blockIdx.x + 1);
+  const int from = line.cut.first(blockIdx.x), to = line.cut.first(blockIdx.x + 1);
   const WaitCtx wc{&ring.abort_word, p.status};
   const uint32_t base = smem_u32(pgt_smem_base());
   if (warp == WARPS) {
@@ -471,7 +233,7 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
       if (ok) {
         g.row(w.G, r, s, hq);
         c2[hh] = head_c2(p.hs, s * p.c.Hq + hq, (t == 0 && warp == 0) ? p.status : nullptr);
-        xrow[hh] = reinterpret_cast<float *>(p.ws + w.logit_off) + ((size_t)s * p.c.Hq + hq) * w.Lp;
+        xrow[hh] = reinterpret_cast<float *>(p.ws + w.logit_off) + ((size_t)s * p.c.Hq + hq) * w.Lp - w.logit_key0;
       }
       const uint32_t *qr =
           reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)s * p.c.Hq + hq) * D);
@@ -548,7 +310,7 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
       for (int v = 0; v < WARPS; ++v) S += s_ml[v][tid].y * ex2_approx(s_ml[v][tid].x - ms);
       const size_t at = (size_t)blockIdx.x + g.seg;
       float2 *ml = g.s >= 0 ? reinterpret_cast<float2 *>(p.ws + w.own_ml_off) + at * w.own_rows
-                            : reinterpret_cast<float2 *>(p.ws + w.pre_ml_off) + at * 16;
+                            : reinterpret_cast<float2 *>(p.ws + w.pre_ml_off) + at * w.pre_rows;
       ml[tid] = make_float2(M, S);
     }
     named_bar_sync(1, WARPS * 32);
@@ -586,7 +348,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
   if (tid == 0) ring.init(V::kStages, V::kStepsPerTile);
   pgt_load_lens<V::kThreads>(p, w, L, nullptr);
   const PgtLine line = pgt_line(p, w, L);
-  const int from = line.first(blockIdx.x), to = line.first(blockIdx.x + 1);
+  const int from = line.cut.first(blockIdx.x), to = line.cut.first(blockIdx.x + 1);
   const WaitCtx wc{&ring.abort_word, p.status};
   uint8_t *const smem = pgt_smem_base();
   const uint32_t base = smem_u32(smem);
@@ -626,7 +388,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
       on[hh] = r < g.nrows && q < V::kGroups;
       if (on[hh]) g.row(w.G, r, s, hq);
       on[hh] = on[hh] && L.len[s] > 0;                 // an idle slot bids nothing
-      xrow[hh] = logits + ((size_t)s * p.c.Hq + hq) * w.Lp + key0;
+      xrow[hh] = logits + ((size_t)s * p.c.Hq + hq) * w.Lp + (key0 - w.logit_key0);
       dtab[hh] = p.c.demand_table + (size_t)s * p.c.max_pages;
       dpool[hh] = p.c.demand_pages + ((size_t)hq << sh);
     }
@@ -662,25 +424,8 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
     for (int r = warp; r < g.nrows; r += WARPS) {
       int s, hq;
       g.row(w.G, r, s, hq);
-      const PgtPieces pc = pgt_pieces(p, w, line, L, s, hq);
-      const float2 *pre = reinterpret_cast<const float2 *>(p.ws + w.pre_ml_off);
-      const float2 *own = reinterpret_cast<const float2 *>(p.ws + w.own_ml_off);
-      float m = -INFINITY, l = 0.f;
-      for (int c = lane; c < pc.npre + pc.nown; c += 32) {
-        const float2 ml = c < pc.npre ? pre[(size_t)(pc.pre0 + c) * 16 + pc.pre_row]
-                                      : own[(size_t)(pc.own0 + c - pc.npre) * w.own_rows + pc.own_row];
-        const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
-        l = l * ex2_approx(m - ms) + ml.y * ex2_approx(ml.x - ms);
-        m = mn;
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
-        const float mn = fmaxf(m, m2), ms = mn == -INFINITY ? 0.f : mn;
-        l = l * ex2_approx(m - ms) + l2 * ex2_approx(m2 - ms);
-        m = mn;
-      }
-      if (lane == 0) s_lse[r] = m + log2f(l);
+      const float v = pgt_row_lse(p, w, line, L, s, hq, lane);
+      if (lane == 0) s_lse[r] = v;
     }
     named_bar_sync(1, WARPS * 32);
     float lse[HH], sum[HH] = {};
@@ -811,7 +556,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
     named_bar_sync(1, WARPS * 32);
     const size_t at = (size_t)blockIdx.x + g.seg;
     float *part = g.s >= 0 ? reinterpret_cast<float *>(p.ws + w.own_acc_off) + at * w.own_rows * acc_stride(D)
-                           : reinterpret_cast<float *>(p.ws + w.pre_acc_off) + at * 16 * acc_stride(D);
+                           : reinterpret_cast<float *>(p.ws + w.pre_acc_off) + at * w.pre_rows * acc_stride(D);
     for (int j = tid; j < g.nrows * D; j += WARPS * 32) {
       const int r = j / D, e = j % D;
       float a = 0.f;
@@ -847,12 +592,12 @@ __global__ void __launch_bounds__(kPgtCombThreads) pgt_combine(PagedDecode p, Pg
   const PgtLine line = pgt_line(p, w, L);
   pdl_wait();
   const int s = blockIdx.x / p.c.Hq, hq = blockIdx.x % p.c.Hq;
-  const PgtPieces pc = pgt_pieces(p, w, line, L, s, hq);
+  const PgtPieces pc = pgt_pieces(p, w, line, L, s, hq, true);
   const float *pre = reinterpret_cast<const float *>(p.ws + w.pre_acc_off) + pc.pre_row * acc_stride(D);
   const float *own = reinterpret_cast<const float *>(p.ws + w.own_acc_off) + pc.own_row * acc_stride(D);
   float a = 0.f, rs = 0.f;
   for (int c = way; c < pc.npre + pc.nown; c += WAYS) {
-    const float *pa = c < pc.npre ? pre + (size_t)(pc.pre0 + c) * 16 * acc_stride(D)
+    const float *pa = c < pc.npre ? pre + (size_t)(pc.pre0 + c) * w.pre_rows * acc_stride(D)
                                   : own + (size_t)(pc.own0 + c - pc.npre) * w.own_rows * acc_stride(D);
     a += pa[e];
     rs += pa[D];
@@ -872,21 +617,20 @@ __global__ void __launch_bounds__(kPgtCombThreads) pgt_combine(PagedDecode p, Pg
 
 // ------------------------------------------------------------------ host
 bool make_page_map(CUtensorMap *m, const void *base, int64_t num, int page_size, int rows, int d);   // fwd_bf16.cu
+// paged_prefix_bf16.cu: the two passes over a prefix with many rows.
+int launch_pgx_keys(const PagedDecode &p, const PgtPlan &w, cudaStream_t stream);
+int launch_pgx_values(const PagedDecode &p, const PgtPlan &w, cudaStream_t stream);
 
-template <typename... KArgs, typename... Args>
-static cudaError_t launch_after(void (*kernel)(KArgs...), int grid, int threads, int smem, cudaStream_t stream,
-                                Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+size_t pgt_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len) {
+  return pgt_plan(S < kPgtMaxSeqs ? S : kPgtMaxSeqs, Hq, Hkv, d, max_len, prefix_len, 16).total;
+}
+// Units on the line at most (int arithmetic on the device).
+bool pgt_fits(int S, int Hq, int Hkv, int d, int max_len, int prefix_len) {
+  if (S > kPgtMaxSeqs) S = kPgtMaxSeqs;
+  const int64_t G = Hq / Hkv, tile = pgt_tile(d), rows = (S * G + 15) / 16;
+  const int64_t own = (max_len - prefix_len + tile - 1) / tile + kPgtHead;
+  const int64_t pre = (prefix_len + tile - 1) / tile + kPgtHead;
+  return S * (int64_t)Hkv * ((G + 15) / 16) * own + (prefix_len > 0 ? Hkv * rows * pre : 0) < 0x7FFF0000ll;
 }
 
 template <int D, int GE>
@@ -913,8 +657,16 @@ static int launch_pgt_t(const PagedDecode &p, const PgtPlan &w, cudaStream_t str
   constexpr int k_stages = (kPgtSmemPerCta - 1024) / R::kTileBytes;
   static_assert(k_stages <= 8, "the ring's barriers");
   pgt_keys<D, HH><<<w.ctas, pgt_threads(D), 1024 + k_stages * R::kTileBytes, stream>>>(p, w, km, k_stages);
+  if (w.wide) {
+    const int st = launch_pgx_keys(p, w, stream);
+    if (st != DA_OK) return st;
+  }
   if (launch_after(pgt_values<D, GE>, w.ctas, V::kThreads, V::kSmemBytes, stream, p, w, vm) != cudaSuccess)
     return DA_ERR_CUDA;
+  if (w.wide) {
+    const int st = launch_pgx_values(p, w, stream);
+    if (st != DA_OK) return st;
+  }
   if (launch_after(pgt_combine<D>, p.c.S * p.c.Hq, kPgtCombThreads, 0, stream, p, w) != cudaSuccess)
     return DA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
@@ -932,8 +684,21 @@ static int launch_pgt_d(const PagedDecode &p, cudaStream_t stream) {
   return launch_pgt_t<D, 16>(p, w, stream);
 }
 
-int launch_paged_decode_bf16(const PagedDecode &p, cudaStream_t stream) {
-  return p.c.d == 128 ? launch_pgt_d<128>(p, stream) : launch_pgt_d<64>(p, stream);
+int launch_paged_decode_bf16(const PagedDecode &a, cudaStream_t stream) {
+  for (int s0 = 0; s0 < a.c.S; s0 += kPgtMaxSeqs) {   // the kernels keep the lengths of one part in shared memory
+    PagedDecode p = a;
+    const size_t rows = (size_t)s0 * a.c.Hq;
+    p.c.S = a.c.S - s0 < kPgtMaxSeqs ? a.c.S - s0 : kPgtMaxSeqs;
+    p.c.page_table += (size_t)s0 * a.c.max_pages;
+    p.c.demand_table += (size_t)s0 * a.c.max_pages;
+    p.c.seq_lens += s0;
+    p.q = static_cast<const __nv_bfloat16 *>(a.q) + rows * a.c.d;
+    p.out = static_cast<__nv_bfloat16 *>(a.out) + rows * a.c.d;
+    if (a.hs.tau_bh != nullptr) p.hs.tau_bh = a.hs.tau_bh + rows;
+    const int st = a.c.d == 128 ? launch_pgt_d<128>(p, stream) : launch_pgt_d<64>(p, stream);
+    if (st != DA_OK) return st;
+  }
+  return DA_OK;
 }
 
 }  // namespace da

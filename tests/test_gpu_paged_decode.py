@@ -73,11 +73,44 @@ def test_rows_past_the_end_are_never_used(dtype, junk):
     (40, [1 + i % 5 for i in range(40)], 6, 2, 64, 32, 160),
     (70, [1 + i % 3 for i in range(70)], 4, 1, 64, 16, 144),     # 280 rows of one key head
     (36, [2 + i % 7 for i in range(36)], 8, 2, 128, 16, 400),
+    (17, [1 + i for i in range(17)], 1, 1, 64, 256, 1024),        # one row past 16; pages of two tiles
+    (33, [3] * 33, 4, 2, 128, 32, 32),                            # a prefix shorter than a tile
+    (20, [1 + i for i in range(20)], 14, 2, 64, 64, 4096),        # 140 rows in three 64-row segments
 ])
 def test_shared_prefix_matches_oracle(dtype, S, own, Hq, Hkv, d, page, prefix):
     lens = [prefix + n for n in own]
     cache, q, pt = make_cache(S, lens, Hq, Hkv, d, page, dtype, seed=S + prefix, prefix=prefix)
     step_and_check(cache, q, max(lens), prefix_table=pt)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefix_rows_beyond_one_segment_over_many_tiles(d):
+    # 20 sequences x 4 heads a key head: two 64-row segments of 157 tiles each, cut over all CTAs; idle slots inside
+    prefix = 20000 // 32 * 32
+    lens = [0 if i % 7 == 2 else prefix + 1 + i for i in range(20)]
+    cache, q, pt = make_cache(20, lens, 8, 2, d, 32, "bf16", seed=97 + d, prefix=prefix)
+    before = cache.demand_pages.clone()
+    for flags in (0, b.DA_FLAG_EARLIER_DEMAND_ONLY):
+        cache.demand_pages.copy_(before)
+        out = b.dilution_attn_paged_decode(q, cache, max(lens), prefix_table=pt, flags=flags, eps=1e-4)
+        h, rows = 5, [0, 1, 2, 19]                  # the oracle on one query head of four sequences
+        one = b.PagedCache(cache.k_pages[:, 1:2].contiguous(), cache.v_pages[:, 1:2].contiguous(),
+                           before[:, h:h + 1].contiguous(), cache.page_table[rows].contiguous(),
+                           cache.demand_table[rows].contiguous(), cache.seq_lens[rows].contiguous())
+        ref = oracle_step(one, q[rows, h:h + 1], eps=1e-4, earlier=bool(flags))
+        mine = torch.zeros(one.demand_pages.shape[0], dtype=torch.bool, device=DEV)
+        mine[one.demand_table[one.demand_table >= 0].long()] = True
+        old = one.demand_pages.clone()
+        one.demand_pages[mine] = cache.demand_pages[mine, h:h + 1]
+        check_step(one, q[rows, h:h + 1], old, out[rows, h:h + 1], ref)
+
+
+def test_more_sequences_than_one_part():
+    lens = [64 + i % 3 for i in range(900)]
+    cache, q, pt = make_cache(900, lens, 1, 1, 64, 16, "bf16", seed=98, prefix=64)
+    tau = torch.linspace(0.5, 1.5, 900, device=DEV)
+    step_and_check(cache, q, 66, tau_bh=tau)
+    step_and_check(cache, q, 66, tau_bh=tau, prefix_table=pt)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
