@@ -15,20 +15,24 @@
 // pgx_keys: S[row, key] = Q K^T with M = 128, N = 128.  The 64 rows stand twice
 // in the M dimension; TMEM lanes 0-63 reduce keys 0-63 of a tile and lanes
 // 64-127 keys 64-127, so that all threads work.  One thread per lane keeps a
-// running maximum and sum.
+// running maximum and sum; two warpgroups take alternate tiles.
 //
 // pgx_values: S^T[key, row] = K Q^T (M = 128 keys, N = 64 rows), one thread per
-// key: the threads of a warp hold neighbouring keys, so the demand moves in
-// whole 128-byte lines.  Each thread has its 64 demand values in registers and
-// refills them for its next tile as it uses them up: 64 KB an SM are in flight.
-// The shares go to shared memory as the MN-major A operand of D[row, :] +=
-// share^T [V | 1]: rows 0-63 of M = 128 hold the shares rounded to bf16, rows
-// 64-127 what the rounding left (2^-16 relative in all; the second term costs
-// no instruction).  Two warpgroups take alternate tiles.
+// key.  The demand of a tile lies in shared memory, [row][key]; every warp
+// brings that of its own 32 keys by 16-byte asynchronous copies, 16 rows at a
+// time into the place of rows it has just written back, so that 64 KB an SM are
+// always in flight or waiting.  The shares go to shared memory as the MN-major A
+// operand of D[row, :] += share^T [V | 1]: rows 0-63 of M = 128 hold the shares
+// rounded to bf16, rows 64-127 what the rounding left (2^-16 relative in all;
+// the second term costs no instruction).  Two warpgroups take alternate tiles.
+// (With the demand in registers, 4-byte loads and stores and fully unrolled
+// rows, a pair took 30 instructions, the instruction cache missed, and 64 rows x
+// 12 heads x 131072 keys took 269 us.)
 //
 // Roles: warps 0-7 demand, then a warp each for K copies, V copies, MMA issue
 // and the demand-page table of the next tiles.  Waits are bounded; rows of
-// missing or invalid pages are filled with zeros by reading past the pool's end.
+// missing or invalid pages are filled with zeros by reading past the pool's end;
+// a key past the prefix's end has eps = infinity and so no share.
 #include "da_paged_plan.cuh"
 
 #include <cuda.h>
@@ -124,7 +128,7 @@ __device__ __forceinline__ uint4 x_query(const PagedDecode &p, const PgtPlan &w,
 // ============================================================================ pass 1
 template <int D>
 struct XKeys {
-  static constexpr int kThreads = 192;                 // 4 reduction warps, copies, MMA
+  static constexpr int kThreads = 320;                 // 2 x 4 reduction warps (alternate tiles), copies, MMA
   static constexpr int kTB = kPgxTile * D * 2;
   static constexpr int kStages = D == 64 ? 4 : 2;
   static constexpr int kSmemBytes = 1024 + kTB + kStages * kTB + 256;
@@ -143,11 +147,11 @@ __global__ void __launch_bounds__(XKeys<D>::kThreads, 2)
   uint64_t *done = s_free + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  __shared__ float2 s_ml[kPgxRows];
+  __shared__ float2 s_ml[3][kPgxRows];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   pdl_launch_dependents();
   if (tid == 0) {
-    mbar_init(q_full, 4);
+    mbar_init(q_full, 1);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
@@ -160,7 +164,7 @@ __global__ void __launch_bounds__(XKeys<D>::kThreads, 2)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc(tmem_slot, C::kTmemCols);
     tmem_relinquish();
   }
@@ -170,7 +174,7 @@ __global__ void __launch_bounds__(XKeys<D>::kThreads, 2)
   const WaitCtx wc{abort_flag, p.status};
   XWalk it;
   it.start(p, w, w.x_keys);
-  if (warp == 4) {
+  if (warp == 8) {
     int issued = 0;
     for (; it.c.n > 0; it.next(p, w)) {
       int page = x_page<D>(p, w, it.c.tile, lane);
@@ -188,7 +192,7 @@ __global__ void __launch_bounds__(XKeys<D>::kThreads, 2)
     if (*abort_flag && lane == 0)
       for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
         x_drain(&k_full[i % C::kStages], (i / C::kStages) & 1);
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16(128, kPgxTile, false, false);
       const uint64_t dQ = x_kmajor(sQ), dK = x_kmajor(sK);
@@ -213,21 +217,22 @@ __global__ void __launch_bounds__(XKeys<D>::kThreads, 2)
       x_drain(done, 0);
     }
   } else {
-    const int row = tid, r = row % kPgxRows, half = row / kPgxRows;   // TMEM lane; query row; keys 64 half ..
+    const int g = warp / 4, row = tid % 128, r = row % kPgxRows, half = row / kPgxRows;   // TMEM lane; query row; keys 64 half ..
     for (; it.c.n > 0; it.next(p, w)) {
-      // the rows, twice, as the K-major A operand (every MMA of the piece
-      // before has completed: this warp saw its last tile's)
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        *reinterpret_cast<uint4 *>(sQ + (i >> 3) * kXHalf + row * 128 + (((i & 7) ^ (row & 7)) << 4)) =
-            x_query<D>(p, w, it.c, r, i);
+      // the rows, twice, as the K-major A operand (every product of the piece
+      // before has completed: the warpgroups saw their last tiles and met)
+      for (int e = tid; e < 128 * (D / 8); e += 256) {
+        const int rr = e / (D / 8), i = e % (D / 8);
+        *reinterpret_cast<uint4 *>(sQ + (i >> 3) * kXHalf + rr * 128 + (((i & 7) ^ (rr & 7)) << 4)) =
+            x_query<D>(p, w, it.c, rr % kPgxRows, i);
+      }
       fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
+      named_bar_sync(1, 256);
+      if (tid == 0) mbar_arrive(q_full);
       float c2 = 1e-30f;
       if (r < it.c.nrows) {
         const int R = it.c.row0 + r, s = R / w.G;
-        c2 = fmaxf(head_c2(p.hs, s * p.c.Hq + it.c.hkv * w.G + R % w.G, half == 0 ? p.status : nullptr), 1e-30f);
+        c2 = fmaxf(head_c2(p.hs, s * p.c.Hq + it.c.hkv * w.G + R % w.G, tid < 64 ? p.status : nullptr), 1e-30f);
       }
       const bool work = (row & 32) < it.c.nrows;   // uniform over the warp: its 32 rows hold at least one
       float m = -INFINITY;
@@ -261,42 +266,48 @@ __global__ void __launch_bounds__(XKeys<D>::kThreads, 2)
         }
       };
       const int tiles = __any_sync(0xffffffffu, *abort_flag != 0) ? 0 : it.c.n;
-      for (int k = 0; k < tiles; ++k) {
-        const int t = it.c.run + k, b = t & 1;
+      for (int k = g ^ (it.c.run & 1); k < tiles; k += 2) {   // the warpgroup's tiles: alternate over the whole run
+        const int t = it.c.run + k, b = g;
         if (!warp_wait(&s_full[b], (t >> 1) & 1, wc)) break;
         tc_fence_after();
         if (work) {
-          const uint32_t ta = tmem + b * 128 + half * 64 + ((uint32_t)(warp * 32) << 16);
+          const uint32_t ta = tmem + b * 128 + half * 64 + ((uint32_t)(warp % 4 * 32) << 16);
           const int left = p.prefix_len - (it.c.tile + k) * kPgxTile - half * 64;
-          float A[32], B[32];
-          tmem_ld32(ta, A);
-          tmem_wait_ld_r(A);
-          tmem_ld32(ta + 32, B);
-          take(A, left);
-          tmem_wait_ld_r(B);
+          float x[32];
+          tmem_ld32(ta, x);
+          tmem_wait_ld_r(x);
+          take(x, left);
+          tmem_ld32(ta + 32, x);
+          tmem_wait_ld_r(x);
           x_release(&s_free[b], lane);
-          take(B, left - 32);
+          take(x, left - 32);
         } else {
           x_release(&s_free[b], lane);
         }
       }
-      // the two halves of a row's keys
+      // a row's four parts: two halves of the keys, two warpgroups
       const float l = (l0.x + l0.y) + (l1.x + l1.y);
-      if (half == 1) s_ml[r] = make_float2(m, l);
-      named_bar_sync(1, 128);
-      if (half == 0 && r < it.c.nrows) {
-        const float2 o = s_ml[r];
-        const float mn = fmaxf(m, o.x), ms = mn == -INFINITY ? 0.f : mn;
+      const int part = 2 * g + half;
+      if (part > 0) s_ml[part - 1][r] = make_float2(m, l);
+      named_bar_sync(1, 256);
+      if (part == 0 && r < it.c.nrows) {
+        float M = m;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) M = fmaxf(M, s_ml[i][r].x);
+        const float ms = M == -INFINITY ? 0.f : M;
+        float sum = l * ex2_approx(m - ms);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) sum += s_ml[i][r].y * ex2_approx(s_ml[i][r].x - ms);
         reinterpret_cast<float2 *>(p.ws + w.pre_ml_off)[(size_t)(blockIdx.x + it.c.seg) * w.pre_rows + r] =
-            make_float2(mn, l * ex2_approx(m - ms) + o.y * ex2_approx(o.x - ms));
+            make_float2(M, sum);
       }
-      named_bar_sync(1, 128);
+      named_bar_sync(1, 256);
     }
     if (tid == 0) pdl_wait();   // this kernel ends after its predecessor: whoever waits for it waits for both
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == 9) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
@@ -308,15 +319,16 @@ template <int D>
 struct XVal {
   static constexpr int kThreads = 384;                 // 8 demand warps; K, V copies, MMA, table
   static constexpr int kTB = kPgxTile * D * 2;
-  static constexpr int kStages = D == 64 ? 3 : 2;
+  static constexpr int kStages = D == 64 ? 2 : 1;      // what the demand leaves room for
   static constexpr uint32_t kShBytes = 32 * 1024;      // a warpgroup's shares: 2 x 64 rows x 128 keys
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffK = kPgxRows * D * 2;
   static constexpr uint32_t kOffV = kOffK + kStages * kTB;
   static constexpr uint32_t kOffSh = kOffV + kStages * kTB;
   static constexpr uint32_t kOffOnes = kOffSh + 2 * kShBytes;   // above every V tile (positive offset)
-  static constexpr uint32_t kOffTab = kOffOnes + 2048;          // 4 tables [8 groups of 16 keys][64 rows]
-  static constexpr uint32_t kOffRow = kOffTab + 4 * 2048;       // (c2, -lse2) of the rows
+  static constexpr uint32_t kOffDem = kOffOnes + 2048;          // demand: 8 warps x [64 rows][32 keys]
+  static constexpr uint32_t kOffTab = kOffDem + 8 * 8192;       // 4 tables [8 groups of 16 keys][64 rows]
+  static constexpr uint32_t kOffRow = kOffTab + 4 * 2048;       // c2, then -lse2, of the rows
   static constexpr uint32_t kOffBar = kOffRow + kPgxRows * 8;
   static constexpr int kSmemBytes = 1024 + kOffBar + 512;
   // TMEM: S^T of warpgroup g at 64 g; D at 128 (80 columns: values 0-63, share
@@ -324,12 +336,6 @@ struct XVal {
   static constexpr uint32_t kTmemD = 128, kTmemDHi = 208;
   static constexpr int kLd = D + 5;                    // floats per row of the low terms' stage
 };
-
-__device__ __forceinline__ float x_ld(const float *p) {
-  float v;
-  asm volatile("ld.global.L1::no_allocate.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
-  return v;
-}
 
 template <int D, bool EARLIER>
 __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
@@ -340,7 +346,7 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
   uint8_t *smem = x_smem_raw + ((1024u - (smem_u32(x_smem_raw) & 1023u)) & 1023u);
   uint8_t *sQ = smem + C::kOffQ, *sK = smem + C::kOffK, *sV = smem + C::kOffV, *sSh = smem + C::kOffSh;
   uint32_t *sTab = reinterpret_cast<uint32_t *>(smem + C::kOffTab);
-  float2 *sRow = reinterpret_cast<float2 *>(smem + C::kOffRow);
+  float *sC2 = reinterpret_cast<float *>(smem + C::kOffRow), *sNl = sC2 + kPgxRows;
   uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
   uint64_t *k_full = q_full + 1, *k_empty = k_full + C::kStages, *v_full = k_empty + C::kStages,
            *v_empty = v_full + C::kStages, *s_full = v_empty + C::kStages, *s_free = s_full + 2, *sh_full = s_free + 2,
@@ -514,8 +520,13 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
     const PgtLine line = pgt_line(p, w, L);
     const uint32_t ts = tmem + g * 64 + ((uint32_t)(quarter * 32) << 16);
     uint8_t *sh_row = sSh + g * C::kShBytes + (key_l / 8) * 1024 + (key_l % 8) * 128;
-    const uint32_t *tab_mine = sTab + (key_l >> 4) * kPgxRows;
-    float *const pool = p.c.demand_pages + (key_l & 15);
+    // the warp's demand: lane -> row 4 j + lane / 8, keys 4 (lane % 8) .. of the warp's 32
+    float *const dem = reinterpret_cast<float *>(smem + C::kOffDem + warp * 8192);
+    const int dr = lane / 8, dk = 4 * (lane % 8);
+    const uint32_t *tab_lane = sTab + ((quarter * 32 + dk) >> 4) * kPgxRows + dr;
+    float *const pool = p.c.demand_pages + (dk & 15);
+    float *const slot = dem + dr * 32 + dk;
+    const float *const mine = dem + lane;            // this thread's key: row r at 32 r
     int piece = 0;
     pdl_wait();
     for (; it.c.n > 0; it.next(p, w), ++piece) {
@@ -528,7 +539,10 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
           if (L.len[s] > 0)
             v = make_float2(fmaxf(head_c2(p.hs, s * p.c.Hq + hq, nullptr), 1e-30f), -pgt_row_lse(p, w, line, L, s, hq, lane));
         }
-        if (lane == 0) sRow[r] = v;
+        if (lane == 0) {
+          sC2[r] = v.x;
+          sNl[r] = v.y;
+        }
       }
       for (int e = tid; e < kPgxRows * (D / 8); e += 256) {   // Q: the K-major B operand
         const int r = e / (D / 8), i = e % (D / 8);
@@ -540,78 +554,101 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
       if (tid == 0) mbar_arrive(q_full);
       const bool dead = __any_sync(0xffffffffu, *abort_flag != 0);
       const int k0 = (g ^ (it.c.run & 1));           // the warpgroup's first tile: alternate over the whole run
-      float d[2][32];                                // demand of the tile at hand, refilled for the next
-      auto load = [&](float (&x)[32], const uint32_t *tab, int c) {
+      const int groups = (it.c.nrows + 15) / 16;     // 16-row groups with rows
+      for (int i = 2 * groups; i < 8; ++i) {         // rows past them: no share (the products before are done)
+        const int at = (i ^ (key_l & 7)) << 4;
+        *reinterpret_cast<uint4 *>(sh_row + at) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(sh_row + 16384 + at) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      // rows 16 c .. 16 c + 15 of a tile's demand, one group of copies
+      auto bring = [&](const uint32_t *tab, int c) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint4 at = *reinterpret_cast<const uint4 *>(tab + 32 * c + 4 * q);
-          const uint32_t a4[4] = {at.x, at.y, at.z, at.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[4 * q + e] = a4[e] != kNoDemand ? x_ld(pool + (size_t)a4[e] * 16) : 0.f;
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t at = tab[16 * c + 4 * j];
+          float *to = slot + (16 * c + 4 * j) * 32;
+          if (at != kNoDemand)
+            cp_async16(to, pool + (size_t)at * 16);
+          else
+            *reinterpret_cast<float4 *>(to) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
       };
-      if (!dead && k0 < n) {
+      auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+      bool ok = !dead;
+      if (ok && k0 < n) {
         const int t = it.c.run + k0;
-        if (warp_wait(&tab_full[t & 3], (t >> 2) & 1, wc)) {
-          load(d[0], tab_mine + (t & 3) * 512, 0);
-          load(d[1], tab_mine + (t & 3) * 512, 1);
+        ok = warp_wait(&tab_full[t & 3], (t >> 2) & 1, wc);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          if (ok && c < groups) bring(tab_lane + (t & 3) * 512, c);
+          commit();
         }
       }
-      bool ok = !dead;
       for (int k = k0; ok && k < n; k += 2) {
         const int t = it.c.run + k;
-        const uint32_t *tab = tab_mine + (t & 3) * 512, *tab_next = tab_mine + ((t + 2) & 3) * 512;
+        const uint32_t *tab = tab_lane + (t & 3) * 512, *tab_next = tab_lane + ((t + 2) & 3) * 512;
         const bool more = k + 2 < n;
-        ok = warp_wait(&s_full[g], (t >> 1) & 1, wc);
+        // a key past the prefix's end gets no share
+        const float eps = (it.c.tile + k) * kPgxTile + key_l < p.prefix_len ? p.eps : INFINITY;
+        const float2 eps2 = make_float2(eps, eps);
+        ok = warp_wait(&s_full[g], (t >> 1) & 1, wc) &&
+             (!more || warp_wait(&tab_full[(t + 2) & 3], ((t + 2) >> 2) & 1, wc)) &&
+             // the product of this warpgroup's previous tile has read the shares
+             warp_wait(&sh_free[g], ((t >> 1) & 1) ^ 1, wc);
         if (!ok) break;
         tc_fence_after();
-        const bool in = (it.c.tile + k) * kPgxTile + key_l < p.prefix_len;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          asm volatile("cp.async.wait_group 3;" ::: "memory");   // this group's copies have landed
+          if (c < groups) {
+            float x[16];
+            tmem_ld16(ts + 16 * c, x);
+            __syncwarp();                                        // .. those of every lane
+            tmem_wait_ld_r16(x);
+            if (c == groups - 1) x_release(&s_free[g], lane);    // the next tile's S may be formed
+            uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float x[32];
-          tmem_ld32(ts + 32 * c, x);
-          tmem_wait_ld_r(x);
-          if (c == 1) x_release(&s_free[g], lane);
-          uint32_t hi[16], lo[16];
+            for (int q = 0; q < 4; ++q) {
+              const float4 sc = *reinterpret_cast<const float4 *>(sC2 + 16 * c + 4 * q);
+              const float4 nl = *reinterpret_cast<const float4 *>(sNl + 16 * c + 4 * q);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint4 at = *reinterpret_cast<const uint4 *>(tab + 32 * c + 4 * q);
-            const uint32_t a4[4] = {at.x, at.y, at.z, at.w};
-            float sh4[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int r = 4 * q + e;
-              const float2 cl = sRow[32 * c + r];
-              const float bid = ex2_approx(fmaf(x[r], cl.x, cl.y));
-              const float nd = d[c][r] + bid;
-              const float den = (EARLIER ? d[c][r] : nd) + p.eps;
-              sh4[e] = in ? bid * rcp_approx(den) : 0.f;
-              if (a4[e] != kNoDemand) pool[(size_t)a4[e] * 16] = nd;
+              for (int e = 0; e < 2; ++e) {
+                const int r = 4 * q + 2 * e;
+                float *m0 = const_cast<float *>(mine) + (16 * c + r) * 32;
+                const float2 y = ffma2(make_float2(x[r], x[r + 1]), e ? make_float2(sc.z, sc.w) : make_float2(sc.x, sc.y),
+                                       e ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y));
+                const float2 bid = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                const float2 d = make_float2(m0[0], m0[32]);
+                const float2 nd = fadd2(d, bid);
+                m0[0] = nd.x;
+                m0[32] = nd.y;
+                const float2 den = fadd2(EARLIER ? d : nd, eps2);
+                const float2 sh = fmul2(bid, make_float2(rcp_approx(den.x), rcp_approx(den.y)));
+                const uint32_t h2 = pack_bf16x2(sh.x, sh.y);
+                const float2 rest = ffma2(make_float2(__uint_as_float(h2 << 16), __uint_as_float(h2 & 0xffff0000u)),
+                                          make_float2(-1.f, -1.f), sh);
+                hi[2 * q + e] = h2;
+                lo[2 * q + e] = pack_bf16x2(rest.x, rest.y);
+              }
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t h2 = pack_bf16x2(sh4[2 * e], sh4[2 * e + 1]);
-              hi[2 * q + e] = h2;
-              lo[2 * q + e] = pack_bf16x2(sh4[2 * e] - __uint_as_float(h2 << 16),
-                                          sh4[2 * e + 1] - __uint_as_float(h2 & 0xffff0000u));
+            for (int i = 0; i < 2; ++i) {   // rows 16 c + 8 i ..: a 16-byte piece of each block
+              const int at = ((2 * c + i) ^ (key_l & 7)) << 4;
+              *reinterpret_cast<uint4 *>(sh_row + at) =
+                  make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+              *reinterpret_cast<uint4 *>(sh_row + 16384 + at) =
+                  make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
             }
-          }
-          if (more) {
-            if (c == 0) ok = warp_wait(&tab_full[(t + 2) & 3], ((t + 2) >> 2) & 1, wc);
-            if (ok) load(d[c], tab_next, c);
-          }
-          // the product of this warpgroup's previous tile has read the shares
-          if (c == 0) ok = warp_wait(&sh_free[g], ((t >> 1) & 1) ^ 1, wc) && ok;
-          if (!ok) break;
+            __syncwarp();                                        // the new demand of every lane's key
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {   // rows 32 c + 8 i ..: a 16-byte piece of each block
-            const int at = ((4 * c + i) ^ (key_l & 7)) << 4;
-            *reinterpret_cast<uint4 *>(sh_row + at) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-            *reinterpret_cast<uint4 *>(sh_row + 16384 + at) =
-                make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t at = tab[16 * c + 4 * j];
+              const float4 v = *reinterpret_cast<const float4 *>(slot + (16 * c + 4 * j) * 32);
+              if (at != kNoDemand) *reinterpret_cast<float4 *>(pool + (size_t)at * 16) = v;
+            }
+            if (more) bring(tab_next, c);                        // over what this lane has just written back
           }
+          commit();
         }
-        if (!ok) break;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -619,6 +656,7 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
           mbar_arrive(&tab_free[t & 3]);
         }
       }
+      cp_async_wait_all();
       // the piece's sums: TMEM lanes 0-63 hold the rounded shares' products, 64-127 the remainders'
       named_bar_sync(1, 256);
       if (g == 0) {
