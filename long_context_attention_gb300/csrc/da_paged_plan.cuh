@@ -9,7 +9,7 @@
 
 namespace da {
 
-constexpr int kPgtMaxSeqs = 832;                  // lengths kept in shared memory (a larger batch goes in parts)
+constexpr int kPgtMaxSeqs = 704;                  // lengths kept in shared memory (a larger batch goes in parts)
 DA_HD constexpr int pgt_tile(int d) { return d == 64 ? 128 : 64; }   // keys per stage (16 KB of K or V)
 DA_HD constexpr int pgt_warps(int d) { return pgt_tile(d) / 16; }    // pgt_keys: consumer warps, 16 keys of a stage each
 DA_HD constexpr int pgt_threads(int d) { return 32 * pgt_warps(d) + 32; }   // and the producer warp
@@ -279,23 +279,26 @@ __device__ __forceinline__ PgtPieces pgt_pieces(const PagedDecode &p, const PgtP
   return r;
 }
 
-// lse2 of row (s, hq), by one warp (the same value in every lane): its pieces'
-// (max, sum) joined.
+// lse2 of row (s, hq), by WIDTH neighbouring lanes (the same value in each): its
+// pieces' (max, sum) joined.  All lanes of the warp call it.
+template <int WIDTH>
 __device__ __forceinline__ float pgt_row_lse(const PagedDecode &p, const PgtPlan &w, const PgtLine &t,
                                              const PgtLens &L, int s, int hq, int lane) {
   const PgtPieces pc = pgt_pieces(p, w, t, L, s, hq, false);
   const float2 *pre = reinterpret_cast<const float2 *>(p.ws + w.pre_ml_off);
   const float2 *own = reinterpret_cast<const float2 *>(p.ws + w.own_ml_off);
   float m = -INFINITY, l = 0.f;
-  for (int c = lane; c < pc.npre + pc.nown; c += 32) {
+#pragma unroll 4
+  for (int c = lane % WIDTH; c < pc.npre + pc.nown; c += WIDTH) {
     const float2 ml = c < pc.npre ? pre[(size_t)(pc.pre0 + c) * w.pre_rows + pc.pre_row]
                                   : own[(size_t)(pc.own0 + c - pc.npre) * w.own_rows + pc.own_row];
     const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
     l = l * ex2_approx(m - ms) + ml.y * ex2_approx(ml.x - ms);
     m = mn;
   }
+  __syncwarp();
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = WIDTH / 2; o > 0; o >>= 1) {
     const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
     const float mn = fmaxf(m, m2), ms = mn == -INFINITY ? 0.f : mn;
     l = l * ex2_approx(m - ms) + l2 * ex2_approx(m2 - ms);
@@ -304,8 +307,14 @@ __device__ __forceinline__ float pgt_row_lse(const PagedDecode &p, const PgtPlan
   return m + log2f(l);
 }
 
-// Launch that may begin before its predecessor in the stream has finished (the
-// kernel waits with pdl_wait where it needs the predecessor's results).
+// Launch that may begin before its predecessor in the stream has finished: as
+// soon as the predecessor's CTAs have called pdl_launch_dependents.  Kernels of
+// one decode step, in launch order:
+//   pgt_keys    waits for everything before it (an ordinary launch);
+//   pgx_keys    needs nothing of pgt_keys; it waits for it before it ends;
+//   pgt_values  waits for the keys' kernels, then lets its successor begin;
+//   pgx_values  so begins after the keys' kernels; waits for pgt_values before it ends;
+//   pgt_combine waits for its predecessor, and with it for all of them.
 template <typename... KArgs, typename... Args>
 static cudaError_t launch_after(void (*kernel)(KArgs...), int grid, int threads, int smem, cudaStream_t stream,
                                 Args... args) {

@@ -344,7 +344,6 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
   __shared__ float s_lse[16];
   __shared__ float s_sum[WARPS][16];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  pdl_launch_dependents();
   if (tid == 0) ring.init(V::kStages, V::kStepsPerTile);
   pgt_load_lens<V::kThreads>(p, w, L, nullptr);
   const PgtLine line = pgt_line(p, w, L);
@@ -365,6 +364,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
   // lane -> row: matrices (k half 0, n 0-7), (k half 1, n 0-7), (k half 0, n 8-15), (k half 1, n 8-15)
   const int vrow = sub + group_key(lane & 7, (lane >> 3) & 1);
   pdl_wait();
+  pdl_launch_dependents();
   PgtSeg g;
   for (g.start(p, w, line, L, from, to); g.n > 0; g.next(p, w, line, L)) {
     const int n = g.n;
@@ -420,12 +420,13 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
       for (int hh = 0; hh < HH; ++hh) pages[a][hh] = demand_page(a, hh);
 #pragma unroll
     for (int a = 0; a < AHEAD - 1; ++a) bring(a, pages[a]);
-    // lse2 of the rows: a warp joins a row's pieces
-    for (int r = warp; r < g.nrows; r += WARPS) {
-      int s, hq;
-      g.row(w.G, r, s, hq);
-      const float v = pgt_row_lse(p, w, line, L, s, hq, lane);
-      if (lane == 0) s_lse[r] = v;
+    // lse2 of the rows: 8 lanes join a row's pieces
+    for (int r4 = warp * 4; r4 < g.nrows; r4 += WARPS * 4) {
+      const int r = r4 + lane / 8;
+      int s = 0, hq = 0;
+      g.row(w.G, min(r, g.nrows - 1), s, hq);
+      const float v = pgt_row_lse<8>(p, w, line, L, s, hq, lane);
+      if (lane % 8 == 0 && r < g.nrows) s_lse[r] = v;
     }
     named_bar_sync(1, WARPS * 32);
     float lse[HH], sum[HH] = {};

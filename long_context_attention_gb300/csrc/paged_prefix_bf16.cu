@@ -24,12 +24,14 @@
 // always in flight or waiting.  The shares go to shared memory as the MN-major A
 // operand of D[row, :] += share^T [V | 1]: rows 0-63 of M = 128 hold the shares
 // rounded to bf16, rows 64-127 what the rounding left (2^-16 relative in all;
-// the second term costs no instruction).  Two warpgroups take alternate tiles.
+// the second term costs no instruction).  Two pairs of warpgroups take alternate
+// tiles, the warpgroups of a pair 32 rows each: four warps a scheduler hide the
+// latency of each other's exponentials and shared-memory reads.
 // (With the demand in registers, 4-byte loads and stores and fully unrolled
-// rows, a pair took 30 instructions, the instruction cache missed, and 64 rows x
-// 12 heads x 131072 keys took 269 us.)
+// rows, a (row, key) pair took 30 instructions, the instruction cache missed, and
+// 64 rows x 12 heads x 131072 keys took 269 us; with one warpgroup a tile 237 us.)
 //
-// Roles: warps 0-7 demand, then a warp each for K copies, V copies, MMA issue
+// Roles: warps 0-15 demand, then a warp each for K copies, V copies, MMA issue
 // and the demand-page table of the next tiles.  Waits are bounded; rows of
 // missing or invalid pages are filled with zeros by reading past the pool's end;
 // a key past the prefix's end has eps = infinity and so no share.
@@ -45,6 +47,7 @@ bool make_page_map(CUtensorMap *m, const void *base, int64_t num, int page_size,
 constexpr uint32_t kXHalf = 128 * 128;        // 128 rows x 64 bf16
 constexpr uint32_t kXQHalf = kPgxRows * 128;  // 64 rows x 64 bf16
 constexpr uint32_t kNoDemand = 0xFFFFFFFFu;
+constexpr int kTabPitch = 72, kTabWords = 8 * kTabPitch;   // a demand-page table (no bank conflicts between groups)
 
 __device__ __forceinline__ uint64_t x_kmajor(const uint8_t *tile) { return smem_desc(smem_u32(tile), 16, 1024); }
 
@@ -317,7 +320,8 @@ __global__ void __launch_bounds__(XKeys<D>::kThreads, 2)
 // ============================================================================ pass 2
 template <int D>
 struct XVal {
-  static constexpr int kThreads = 384;                 // 8 demand warps; K, V copies, MMA, table
+  static constexpr int kDemandWarps = 16;              // warpgroup x: tiles of parity x & 1, rows 32 (x >> 1) ..
+  static constexpr int kThreads = 640;                 // and a warp each for K, V, MMA and the table
   static constexpr int kTB = kPgxTile * D * 2;
   static constexpr int kStages = D == 64 ? 2 : 1;      // what the demand leaves room for
   static constexpr uint32_t kShBytes = 32 * 1024;      // a warpgroup's shares: 2 x 64 rows x 128 keys
@@ -326,9 +330,9 @@ struct XVal {
   static constexpr uint32_t kOffV = kOffK + kStages * kTB;
   static constexpr uint32_t kOffSh = kOffV + kStages * kTB;
   static constexpr uint32_t kOffOnes = kOffSh + 2 * kShBytes;   // above every V tile (positive offset)
-  static constexpr uint32_t kOffDem = kOffOnes + 2048;          // demand: 8 warps x [64 rows][32 keys]
-  static constexpr uint32_t kOffTab = kOffDem + 8 * 8192;       // 4 tables [8 groups of 16 keys][64 rows]
-  static constexpr uint32_t kOffRow = kOffTab + 4 * 2048;       // c2, then -lse2, of the rows
+  static constexpr uint32_t kOffDem = kOffOnes + 2048;          // demand: 16 warps x [32 rows][32 keys]
+  static constexpr uint32_t kOffTab = kOffDem + 16 * 4096;      // 4 tables [8 groups of 16 keys][64 rows, padded]
+  static constexpr uint32_t kOffRow = kOffTab + 4 * kTabWords * 4;       // c2, then -lse2, of the rows
   static constexpr uint32_t kOffBar = kOffRow + kPgxRows * 8;
   static constexpr int kSmemBytes = 1024 + kOffBar + 512;
   // TMEM: S^T of warpgroup g at 64 g; D at 128 (80 columns: values 0-63, share
@@ -367,13 +371,13 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], 4);
-      mbar_init(&sh_full[i], 4);
+      mbar_init(&s_free[i], 8);
+      mbar_init(&sh_full[i], 8);
       mbar_init(&sh_free[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(&tab_full[i], 1);
-      mbar_init(&tab_free[i], 4);
+      mbar_init(&tab_free[i], 8);
     }
     mbar_init(d_full, 1);
     mbar_init(d_free, 4);
@@ -384,7 +388,7 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
   for (int e = tid; e < 2048 / 4; e += C::kThreads)   // the ones beside V: bf16 1.0
     reinterpret_cast<uint32_t *>(smem + C::kOffOnes)[e] = 0x3F803F80u;
   fence_proxy_async_smem();
-  if (warp == 10) {
+  if (warp == C::kDemandWarps + 2) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -394,9 +398,9 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
   const WaitCtx wc{abort_flag, p.status};
   XWalk it;
   it.start(p, w, w.x_values);
-  if (warp == 8 || warp == 9) {
+  if (warp == C::kDemandWarps || warp == C::kDemandWarps + 1) {
     // ------------------------------------------------------------ K and V copies
-    const bool isk = warp == 8;
+    const bool isk = warp == C::kDemandWarps;
     const CUtensorMap *map = isk ? &kmap : &vmap;
     uint8_t *ring = isk ? sK : sV;
     uint64_t *full = isk ? k_full : v_full, *empty = isk ? k_empty : v_empty;
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
     if (*abort_flag && lane == 0)
       for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
         x_drain(&full[i % C::kStages], (i / C::kStages) & 1);
-  } else if (warp == 10) {
+  } else if (warp == C::kDemandWarps + 2) {
     // ------------------------------------------------------------ MMA issue
     // S(0), S(1), then S(k + 2) before PV(k): the buffer of S(k) is free once
     // its warpgroup has read it, before it has written the shares of k.
@@ -471,7 +475,7 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
       mma_commit(done);
       x_drain(done, 0);
     }
-  } else if (warp == 11) {
+  } else if (warp == C::kDemandWarps + 3) {
     // ------------------------------------------------------------ demand pages
     // Table of a tile: for every 16-key group and row, the group's place in the
     // demand pool in units of 16 floats.
@@ -508,7 +512,7 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
               at = (((uint32_t)id[h][j] * p.c.Hq + head[h]) << (sh - 4)) + (((key0 + 16 * j) & (ps - 1)) >> 4);
             else if (on[h] && key0 + 16 * j < p.prefix_len)
               atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
-            sTab[b * 512 + j * kPgxRows + lane + 32 * h] = at;
+            sTab[b * kTabWords + j * kTabPitch + lane + 32 * h] = at;
           }
         __syncwarp();
         if (lane == 0) mbar_arrive(&tab_full[b]);
@@ -516,89 +520,90 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ demand warpgroups
-    const int g = warp / 4, quarter = warp % 4, key_l = quarter * 32 + lane;   // key inside the tile
+    const int g = warp / 4 & 1, rh = warp / 8, quarter = warp % 4;   // tile parity, row half, TMEM quarter
+    const int key_l = quarter * 32 + lane;                           // key inside the tile
     const PgtLine line = pgt_line(p, w, L);
-    const uint32_t ts = tmem + g * 64 + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t ts = tmem + g * 64 + 32 * rh + ((uint32_t)(quarter * 32) << 16);
     uint8_t *sh_row = sSh + g * C::kShBytes + (key_l / 8) * 1024 + (key_l % 8) * 128;
     // the warp's demand: lane -> row 4 j + lane / 8, keys 4 (lane % 8) .. of the warp's 32
-    float *const dem = reinterpret_cast<float *>(smem + C::kOffDem + warp * 8192);
+    float *const dem = reinterpret_cast<float *>(smem + C::kOffDem + warp * 4096);
     const int dr = lane / 8, dk = 4 * (lane % 8);
-    const uint32_t *tab_lane = sTab + ((quarter * 32 + dk) >> 4) * kPgxRows + dr;
+    const uint32_t *tab_lane = sTab + ((quarter * 32 + dk) >> 4) * kTabPitch + 32 * rh + dr;
     float *const pool = p.c.demand_pages + (dk & 15);
     float *const slot = dem + dr * 32 + dk;
-    const float *const mine = dem + lane;            // this thread's key: row r at 32 r
+    float *const mine = dem + lane;                  // this thread's key: row r at 32 r
     int piece = 0;
-    pdl_wait();
     for (; it.c.n > 0; it.next(p, w), ++piece) {
       const int n = it.c.n;
       // rows: scale and normaliser (a row without a sequence bids nothing)
-      for (int r = warp; r < kPgxRows; r += 8) {
-        float2 v = make_float2(1e-30f, -INFINITY);
-        if (r < it.c.nrows) {
-          const int R = it.c.row0 + r, s = R / w.G, hq = it.c.hkv * w.G + R % w.G;
-          if (L.len[s] > 0)
-            v = make_float2(fmaxf(head_c2(p.hs, s * p.c.Hq + hq, nullptr), 1e-30f), -pgt_row_lse(p, w, line, L, s, hq, lane));
-        }
-        if (lane == 0) {
-          sC2[r] = v.x;
-          sNl[r] = v.y;
+      {
+        static_assert(4 * C::kDemandWarps == kPgxRows, "8 lanes a row");
+        const int r = warp * 4 + lane / 8, R = it.c.row0 + min(r, it.c.nrows - 1), s = R / w.G;
+        const int hq = it.c.hkv * w.G + R % w.G;
+        const float lse = pgt_row_lse<8>(p, w, line, L, s, hq, lane);
+        const bool on = r < it.c.nrows && L.len[s] > 0;
+        if (lane % 8 == 0) {
+          sC2[r] = on ? fmaxf(head_c2(p.hs, s * p.c.Hq + hq, nullptr), 1e-30f) : 1e-30f;
+          sNl[r] = on ? -lse : -INFINITY;
         }
       }
-      for (int e = tid; e < kPgxRows * (D / 8); e += 256) {   // Q: the K-major B operand
+      for (int e = tid; e < kPgxRows * (D / 8); e += 512) {   // Q: the K-major B operand
         const int r = e / (D / 8), i = e % (D / 8);
         *reinterpret_cast<uint4 *>(sQ + (i >> 3) * kXQHalf + r * 128 + (((i & 7) ^ (r & 7)) << 4)) =
             x_query<D>(p, w, it.c, r, i);
       }
       fence_proxy_async_smem();
-      named_bar_sync(1, 256);
+      named_bar_sync(1, 512);
       if (tid == 0) mbar_arrive(q_full);
       const bool dead = __any_sync(0xffffffffu, *abort_flag != 0);
       const int k0 = (g ^ (it.c.run & 1));           // the warpgroup's first tile: alternate over the whole run
-      const int groups = (it.c.nrows + 15) / 16;     // 16-row groups with rows
-      for (int i = 2 * groups; i < 8; ++i) {         // rows past them: no share (the products before are done)
-        const int at = (i ^ (key_l & 7)) << 4;
+      const int groups = min(2, (it.c.nrows - 32 * rh + 15) / 16);   // 16-row groups of the half with rows (or < 1)
+      for (int i = 2 * max(groups, 0); i < 4; ++i) {   // rows past them: no share (the products before are done)
+        const int at = ((4 * rh + i) ^ (key_l & 7)) << 4;
         *reinterpret_cast<uint4 *>(sh_row + at) = make_uint4(0u, 0u, 0u, 0u);
         *reinterpret_cast<uint4 *>(sh_row + 16384 + at) = make_uint4(0u, 0u, 0u, 0u);
       }
-      // rows 16 c .. 16 c + 15 of a tile's demand, one group of copies
-      auto bring = [&](const uint32_t *tab, int c) {
+      // The places of the lane's demand, for the tile at hand and the next.
+      uint32_t at[8], at_next[8];
+      auto places = [&](uint32_t (&a)[8], const uint32_t *tab, bool valid) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t at = tab[16 * c + 4 * j];
-          float *to = slot + (16 * c + 4 * j) * 32;
-          if (at != kNoDemand)
-            cp_async16(to, pool + (size_t)at * 16);
-          else
-            *reinterpret_cast<float4 *>(to) = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+        for (int j = 0; j < 8; ++j) a[j] = valid ? tab[4 * j] : kNoDemand;
       };
-      auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+      // 16 rows of a tile's demand: one group of copies.  A place without demand
+      // keeps what it held: zero, or the demand of an earlier key (both finite).
+      auto bring = [&](const uint32_t (&a)[8], int c) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (a[4 * c + j] != kNoDemand) cp_async16(slot + (16 * c + 4 * j) * 32, pool + (size_t)a[4 * c + j] * 16);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+#pragma unroll
+      for (int j = 0; j < 8; ++j) *reinterpret_cast<float4 *>(slot + 4 * j * 32) = make_float4(0.f, 0.f, 0.f, 0.f);
       bool ok = !dead;
       if (ok && k0 < n) {
         const int t = it.c.run + k0;
         ok = warp_wait(&tab_full[t & 3], (t >> 2) & 1, wc);
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          if (ok && c < groups) bring(tab_lane + (t & 3) * 512, c);
-          commit();
-        }
+        places(at, tab_lane + (t & 3) * kTabWords, ok);
+        bring(at, 0);
+        bring(at, 1);
       }
       for (int k = k0; ok && k < n; k += 2) {
         const int t = it.c.run + k;
-        const uint32_t *tab = tab_lane + (t & 3) * 512, *tab_next = tab_lane + ((t + 2) & 3) * 512;
         const bool more = k + 2 < n;
         // a key past the prefix's end gets no share
         const float eps = (it.c.tile + k) * kPgxTile + key_l < p.prefix_len ? p.eps : INFINITY;
         const float2 eps2 = make_float2(eps, eps);
-        ok = warp_wait(&s_full[g], (t >> 1) & 1, wc) &&
-             (!more || warp_wait(&tab_full[(t + 2) & 3], ((t + 2) >> 2) & 1, wc)) &&
-             // the product of this warpgroup's previous tile has read the shares
+        ok = !more || warp_wait(&tab_full[(t + 2) & 3], ((t + 2) >> 2) & 1, wc);
+        places(at_next, tab_lane + ((t + 2) & 3) * kTabWords, more && ok);
+        ok = ok && warp_wait(&s_full[g], (t >> 1) & 1, wc) &&
+             // the product of this pair's previous tile has read the shares
              warp_wait(&sh_free[g], ((t >> 1) & 1) ^ 1, wc);
         if (!ok) break;
         tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          asm volatile("cp.async.wait_group 3;" ::: "memory");   // this group's copies have landed
+        if (groups < 1) x_release(&s_free[g], lane);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          asm volatile("cp.async.wait_group 1;" ::: "memory");   // this group's copies have landed
           if (c < groups) {
             float x[16];
             tmem_ld16(ts + 16 * c, x);
@@ -608,12 +613,12 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
             uint32_t hi[8], lo[8];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const float4 sc = *reinterpret_cast<const float4 *>(sC2 + 16 * c + 4 * q);
-              const float4 nl = *reinterpret_cast<const float4 *>(sNl + 16 * c + 4 * q);
+              const float4 sc = *reinterpret_cast<const float4 *>(sC2 + 32 * rh + 16 * c + 4 * q);
+              const float4 nl = *reinterpret_cast<const float4 *>(sNl + 32 * rh + 16 * c + 4 * q);
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int r = 4 * q + 2 * e;
-                float *m0 = const_cast<float *>(mine) + (16 * c + r) * 32;
+                float *m0 = mine + (16 * c + r) * 32;
                 const float2 y = ffma2(make_float2(x[r], x[r + 1]), e ? make_float2(sc.z, sc.w) : make_float2(sc.x, sc.y),
                                        e ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y));
                 const float2 bid = make_float2(ex2_approx(y.x), ex2_approx(y.y));
@@ -631,23 +636,21 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
               }
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {   // rows 16 c + 8 i ..: a 16-byte piece of each block
-              const int at = ((2 * c + i) ^ (key_l & 7)) << 4;
-              *reinterpret_cast<uint4 *>(sh_row + at) =
+            for (int i = 0; i < 2; ++i) {   // rows 32 rh + 16 c + 8 i ..: a 16-byte piece of each block
+              const int to = ((4 * rh + 2 * c + i) ^ (key_l & 7)) << 4;
+              *reinterpret_cast<uint4 *>(sh_row + to) =
                   make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-              *reinterpret_cast<uint4 *>(sh_row + 16384 + at) =
+              *reinterpret_cast<uint4 *>(sh_row + 16384 + to) =
                   make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
             }
             __syncwarp();                                        // the new demand of every lane's key
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const uint32_t at = tab[16 * c + 4 * j];
-              const float4 v = *reinterpret_cast<const float4 *>(slot + (16 * c + 4 * j) * 32);
-              if (at != kNoDemand) *reinterpret_cast<float4 *>(pool + (size_t)at * 16) = v;
+              const float4 d4 = *reinterpret_cast<const float4 *>(slot + (16 * c + 4 * j) * 32);
+              if (at[4 * c + j] != kNoDemand) *reinterpret_cast<float4 *>(pool + (size_t)at[4 * c + j] * 16) = d4;
             }
-            if (more) bring(tab_next, c);                        // over what this lane has just written back
           }
-          commit();
+          bring(at_next, c);                                     // over what this lane has just written back
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -655,11 +658,13 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
           mbar_arrive(&sh_full[g]);
           mbar_arrive(&tab_free[t & 3]);
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) at[j] = at_next[j];
       }
       cp_async_wait_all();
       // the piece's sums: TMEM lanes 0-63 hold the rounded shares' products, 64-127 the remainders'
-      named_bar_sync(1, 256);
-      if (g == 0) {
+      named_bar_sync(1, 512);
+      if (warp < 4) {
         float *stage = reinterpret_cast<float *>(sSh);
         const bool have = warp_wait(d_full, piece & 1, wc);
         tc_fence_after();
@@ -706,12 +711,13 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
         }
         x_release(d_free, lane);
       }
-      named_bar_sync(1, 256);
+      named_bar_sync(1, 512);
     }
+    if (tid == 0) pdl_wait();   // (see launch_after) this kernel ends after its predecessor
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 10) {
+  if (warp == C::kDemandWarps + 2) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
