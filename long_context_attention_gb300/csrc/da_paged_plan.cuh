@@ -307,6 +307,31 @@ __device__ __forceinline__ float pgt_row_lse(const PagedDecode &p, const PgtPlan
   return m + log2f(l);
 }
 
+// ------------------------------------------------------------------ tensor pieces
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The order of a 16-key group: column c of the first 8 (half 0) and the last 8
+// (half 1) columns is key 4 (c / 2) + 2 half + c % 2, so that a thread's four
+// columns (2t, 2t + 1 of both halves) are keys 4t .. 4t + 3.
+__device__ __forceinline__ int group_key(int c, int half) { return 4 * (c >> 1) + 2 * half + (c & 1); }
+
 // Launch that may begin before its predecessor in the stream has finished: as
 // soon as the predecessor's CTAs have called pdl_launch_dependents.  Kernels of
 // one decode step, in launch order:

@@ -70,37 +70,12 @@ struct PgtVal {
   static constexpr int kSmemBytes = 1024 + kStages * 16384 + kWarps * kWarpBytes;
 };
 
-// ------------------------------------------------------------------ tensor pieces
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
 // Byte offset of 16-byte piece `piece` of row `row` in a staged tile: boxes of
 // 64 elements (128 bytes) by a tile's rows, pieces swizzled by the row.
 template <int D>
 __device__ __forceinline__ uint32_t tile_off(int row, int piece) {
   return (uint32_t)((piece >> 3) * pgt_tile(D) * 128 + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
 }
-// The order of a 16-key group: column c of the first 8 (half 0) and the last 8
-// (half 1) columns is key 4 (c / 2) + 2 half + c % 2, so that a thread's four
-// columns (2t, 2t + 1 of both halves) are keys 4t .. 4t + 3.
-__device__ __forceinline__ int group_key(int c, int half) { return 4 * (c >> 1) + 2 * half + (c & 1); }
-
 template <int D>
 struct PgtRing {
   static constexpr int kTile = pgt_tile(D);
@@ -583,36 +558,45 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
 // ------------------------------------------------------------------ join
 constexpr int kPgtCombThreads = 256;
 
+// One block a row: thread (way, e) adds 4 columns of every WAYS-th piece, then
+// the ways are added in order.
 template <int D>
 __global__ void __launch_bounds__(kPgtCombThreads) pgt_combine(PagedDecode p, PgtPlan w) {
-  constexpr int WAYS = kPgtCombThreads / D;
+  constexpr int COLS = D / 4, WAYS = kPgtCombThreads / COLS;
   __shared__ PgtLens L;
-  __shared__ float s_a[WAYS][D], s_r[WAYS];
-  const int tid = threadIdx.x, e = tid % D, way = tid / D;
+  __shared__ float4 s_a[WAYS][COLS];
+  __shared__ float s_r[WAYS];
+  const int tid = threadIdx.x, e = tid % COLS, way = tid / COLS;
   pgt_load_lens<kPgtCombThreads>(p, w, L, nullptr);
   const PgtLine line = pgt_line(p, w, L);
-  pdl_wait();
   const int s = blockIdx.x / p.c.Hq, hq = blockIdx.x % p.c.Hq;
   const PgtPieces pc = pgt_pieces(p, w, line, L, s, hq, true);
   const float *pre = reinterpret_cast<const float *>(p.ws + w.pre_acc_off) + pc.pre_row * acc_stride(D);
   const float *own = reinterpret_cast<const float *>(p.ws + w.own_acc_off) + pc.own_row * acc_stride(D);
-  float a = 0.f, rs = 0.f;
+  pdl_wait();
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  float rs = 0.f;
+#pragma unroll 2
   for (int c = way; c < pc.npre + pc.nown; c += WAYS) {
     const float *pa = c < pc.npre ? pre + (size_t)(pc.pre0 + c) * w.pre_rows * acc_stride(D)
                                   : own + (size_t)(pc.own0 + c - pc.npre) * w.own_rows * acc_stride(D);
-    a += pa[e];
+    const float4 v = *reinterpret_cast<const float4 *>(pa + 4 * e);
+    a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
     rs += pa[D];
   }
   s_a[way][e] = a;
   if (e == 0) s_r[way] = rs;
   __syncthreads();
-  if (way == 0) {
-    for (int v = 1; v < WAYS; ++v) {
-      a += s_a[v][e];
-      rs += s_r[v];
+  if (tid < D) {
+    const float *col = reinterpret_cast<const float *>(&s_a[0][0]) + tid;
+    float sum = 0.f, tot = 0.f;
+#pragma unroll
+    for (int v = 0; v < WAYS; ++v) {
+      sum += col[v * D];
+      tot += s_r[v];
     }
-    static_cast<__nv_bfloat16 *>(p.out)[(size_t)blockIdx.x * D + e] =
-        __float2bfloat16_rn(L.len[s] > 0 ? a / rs : 0.f);
+    static_cast<__nv_bfloat16 *>(p.out)[(size_t)blockIdx.x * D + tid] =
+        __float2bfloat16_rn(L.len[s] > 0 ? sum / tot : 0.f);
   }
 }
 
@@ -685,7 +669,13 @@ static int launch_pgt_d(const PagedDecode &p, cudaStream_t stream) {
   return launch_pgt_t<D, 16>(p, w, stream);
 }
 
+// paged_small_bf16.cu: short calls in one launch.
+int small_cluster(int S, int Hq, int Hkv, int d, int max_len);
+int launch_paged_small_bf16(const PagedDecode &p, int csize, cudaStream_t stream);
+
 int launch_paged_decode_bf16(const PagedDecode &a, cudaStream_t stream) {
+  const int cluster = small_cluster(a.c.S, a.c.Hq, a.c.Hkv, a.c.d, a.max_len);
+  if (cluster > 0) return launch_paged_small_bf16(a, cluster, stream);
   for (int s0 = 0; s0 < a.c.S; s0 += kPgtMaxSeqs) {   // the kernels keep the lengths of one part in shared memory
     PagedDecode p = a;
     const size_t rows = (size_t)s0 * a.c.Hq;

@@ -20,18 +20,20 @@ from oracle import paged as op
 from tests._parity import host64
 
 DEV = "cuda"
+LONG = 2600     # a max_len past what the one-launch kernel for short bf16 calls takes
 TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
 
 
-def make_cache(S, lens, Hq, Hkv, d, page, dtype, seed=0, prefix=0, spare=2, extra_width=1, junk=None):
+def make_cache(S, lens, Hq, Hkv, d, page, dtype, seed=0, prefix=0, spare=2, extra_width=None, junk=None):
     """A random paged cache; pages in shuffled order, unused table entries -1.
+    The tables are wide enough for LONG tokens unless extra_width is given.
     ``prefix`` tokens (whole pages) are shared by every sequence.  ``junk``
     fills the rows past each sequence's end (keys, values and demand)."""
     g = torch.Generator().manual_seed(seed)
     lens = list(lens)
     pp = prefix // page
     need = [-(-n // page) for n in lens]
-    width = max(need + [pp]) + extra_width
+    width = max(need + [pp]) + (-(-LONG // page) if extra_width is None else extra_width)
     n_kv = pp + sum(max(0, n - pp) for n in need) + spare
     n_dem = sum(need) + spare
     order = torch.randperm(n_kv, generator=g).to(torch.int32)
@@ -93,6 +95,14 @@ def check_step(cache, q, before, out, ref):
         assert (np.abs(D[at] - rD[at]) <= bound).all(), (s, h, float((np.abs(D[at] - rD[at]) - bound).max()))
     old = host64(before)
     assert np.array_equal(D[~seen], old[~seen], equal_nan=True)
+
+
+def both_sizes(cache, q, max_len, **kw):
+    """The step with max_len and with a max_len that takes the kernels for long caches."""
+    old = cache.demand_pages.clone()
+    step_and_check(cache, q, max_len, **kw)
+    cache.demand_pages.copy_(old)
+    return step_and_check(cache, q, max(max_len, LONG), **kw)
 
 
 def step_and_check(cache, q, max_len, **kw):

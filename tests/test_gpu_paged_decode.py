@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from long_context_attention_gb300 import binding as b
-from tests._paged import DEV, check_step, make_cache, oracle_step, step_and_check
+from tests._paged import DEV, LONG, both_sizes, check_step, make_cache, oracle_step, step_and_check
 from tests._parity import host64
 
 pytestmark = pytest.mark.gpu
@@ -26,7 +26,7 @@ pytestmark = pytest.mark.gpu
 ])
 def test_ragged_decode_matches_oracle(dtype, S, lens, Hq, Hkv, d, page):
     cache, q, _ = make_cache(S, lens, Hq, Hkv, d, page, dtype, seed=sum(lens) + Hq)
-    step_and_check(cache, q, max(lens))
+    both_sizes(cache, q, max(lens))
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -61,7 +61,7 @@ def test_all_idle(dtype):
 @pytest.mark.parametrize("junk", [float("nan"), float("inf"), -3.0e38])
 def test_rows_past_the_end_are_never_used(dtype, junk):
     cache, q, _ = make_cache(4, [1, 15, 130, 333], 4, 2, 64, 32, dtype, seed=5, junk=junk)
-    step_and_check(cache, q, 352)
+    both_sizes(cache, q, 352)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -80,7 +80,7 @@ def test_rows_past_the_end_are_never_used(dtype, junk):
 def test_shared_prefix_matches_oracle(dtype, S, own, Hq, Hkv, d, page, prefix):
     lens = [prefix + n for n in own]
     cache, q, pt = make_cache(S, lens, Hq, Hkv, d, page, dtype, seed=S + prefix, prefix=prefix)
-    step_and_check(cache, q, max(lens), prefix_table=pt)
+    both_sizes(cache, q, max(lens), prefix_table=pt)
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -118,7 +118,7 @@ def test_shared_prefix_with_idle_slots_and_nothing_of_their_own(dtype):
     # idle slots among the sequences, and sequences that end with the prefix
     lens = [0, 160, 165, 0, 160, 300, 0]
     cache, q, pt = make_cache(7, lens, 4, 2, 64, 32, dtype, seed=9, prefix=160, junk=float("nan"))
-    step_and_check(cache, q, 300, prefix_table=pt)
+    both_sizes(cache, q, 300, prefix_table=pt)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -143,7 +143,7 @@ def test_options(dtype):
                                          (0, 2.0, False, 32)):
         cache, q, pt = make_cache(3, lens, 4, 2, 64, 16, dtype, seed=31, prefix=prefix)
         tau_bh = torch.linspace(0.0, 2.0, 12, device=DEV) if per_head else None
-        step_and_check(cache, q, 300, tau=tau, tau_bh=tau_bh, flags=flags, eps=1e-3, prefix_table=pt)
+        both_sizes(cache, q, 300, tau=tau, tau_bh=tau_bh, flags=flags, eps=1e-3, prefix_table=pt)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -152,35 +152,45 @@ def test_sharp_logits(dtype):
     cache, q, _ = make_cache(2, [200, 90], 2, 2, 64, 16, dtype, seed=41)
     q[0, 0] = cache.k_pages[int(cache.page_table[0, 3]), 0, 5] * 4
     q[1, 1] = 0
-    step_and_check(cache, q, 200)
+    both_sizes(cache, q, 200)
 
 
 def test_max_len_beyond_every_sequence_and_repeats():
     cache, q, pt = make_cache(3, [70, 200, 64], 4, 2, 64, 32, "bf16", seed=51, prefix=64, extra_width=300)
+    b.dilution_attn_paged_decode(q, cache, 200)         # whatever ran before
     old = cache.demand_pages.clone()
     outs = []
     for max_len, table in ((200, None), (9000, None), (200, pt), (200, pt), (9000, pt)):
         cache.demand_pages.copy_(old)
         outs.append((step_and_check(cache, q, max_len, prefix_table=table), cache.demand_pages.clone()))
-    assert torch.equal(outs[2][0], outs[3][0]) and torch.equal(outs[2][1], outs[3][1])   # equal bits
+    for _ in range(3):                                  # equal bits from equal calls, on every path
+        for max_len, table in ((200, None), (200, pt), (9000, None), (9000, pt)):
+            got = []
+            for _ in range(2):
+                cache.demand_pages.copy_(old)
+                got.append((b.dilution_attn_paged_decode(q, cache, max_len, prefix_table=table),
+                            cache.demand_pages.clone()))
+            assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_bad_device_data_is_reported(dtype):
-    good, q, pt = make_cache(3, [70, 200, 64], 4, 2, 64, 32, dtype, seed=61, prefix=64)
-    ws = b.dilution_attn_paged_decode_workspace(good, 224)
+@pytest.mark.parametrize("dtype,max_len", [("bf16", 224), ("bf16", LONG), ("f32", 224)])
+@pytest.mark.parametrize("S", [3, 12])          # 12: 24 rows a key head at the prefix
+def test_bad_device_data_is_reported(dtype, max_len, S):
+    lens = [70, 200] + [64] * (S - 2)
+    good, q, pt = make_cache(S, lens, 4, 2, 64, 32, dtype, seed=61, prefix=64)
+    ws = b.dilution_attn_paged_decode_workspace(good, max_len)
 
     def after(change, prefix=None):
-        cache, qq, _ = make_cache(3, [70, 200, 64], 4, 2, 64, 32, dtype, seed=61, prefix=64)
+        cache, qq, _ = make_cache(S, lens, 4, 2, 64, 32, dtype, seed=61, prefix=64)
         change(cache)
         p = None if prefix is None else prefix.clone()
-        b.dilution_attn_paged_decode(qq, cache, 224, prefix_table=p, workspace=ws)
+        b.dilution_attn_paged_decode(qq, cache, max_len, prefix_table=p, workspace=ws)
         first = b.dilution_attn_get_error(ws)
         assert b.dilution_attn_get_error(ws) == b.DA_OK      # read once
         return first
 
     assert after(lambda c: None) == b.DA_OK
-    assert after(lambda c: c.seq_lens.__setitem__(1, 225)) == b.DA_ERR_INVALID
+    assert after(lambda c: c.seq_lens.__setitem__(1, max_len + 1)) == b.DA_ERR_INVALID
     assert after(lambda c: c.seq_lens.__setitem__(1, -1)) == b.DA_ERR_INVALID
     assert after(lambda c: c.seq_lens.__setitem__(1, 63), pt) == b.DA_ERR_INVALID     # shorter than the prefix
     assert after(lambda c: c.page_table.__setitem__((1, 3), -5)) == b.DA_ERR_INVALID
@@ -191,28 +201,29 @@ def test_bad_device_data_is_reported(dtype):
     bad[1] = 10 ** 6
     assert after(lambda c: None, bad) == b.DA_ERR_INVALID
     # the other sequences of a call with one bad length are right
-    cache, qq, _ = make_cache(3, [70, 200, 64], 4, 2, 64, 32, dtype, seed=61)
+    cache, qq, _ = make_cache(S, lens, 4, 2, 64, 32, dtype, seed=61)
     cache.seq_lens[1] = 0
     ref = oracle_step(cache, qq)
-    cache.seq_lens[1] = 300
-    out = b.dilution_attn_paged_decode(qq, cache, 224, workspace=ws)
+    cache.seq_lens[1] = max_len + 5
+    out = b.dilution_attn_paged_decode(qq, cache, max_len, workspace=ws)
     assert b.dilution_attn_get_error(ws) == b.DA_ERR_INVALID
-    keep = [0, 2]
+    keep = [0] + list(range(2, S))
     assert np.abs(host64(out)[keep] - ref[0][keep]).max() <= 2e-2
 
 
-def test_graph_replay_with_growing_sequences():
+@pytest.mark.parametrize("max_len,dtype", [(264, "bf16"), (LONG, "bf16"), (264, "f32")])
+def test_graph_replay_with_growing_sequences(max_len, dtype):
     # one captured step replays over lengths and tables that change on the device
-    cache, q, pt = make_cache(3, [64 + 100, 64 + 200, 64 + 30], 4, 2, 64, 32, "bf16", seed=71, prefix=64)
+    cache, q, pt = make_cache(3, [64 + 100, 64 + 200, 64 + 30], 4, 2, 64, 32, dtype, seed=71, prefix=64)
     cache.seq_lens.copy_(torch.tensor([70, 64, 65], dtype=torch.int32))
-    ws = b.dilution_attn_paged_decode_workspace(cache, 264)
+    ws = b.dilution_attn_paged_decode_workspace(cache, max_len)
     out = torch.empty_like(q)
     old = cache.demand_pages.clone()
-    b.dilution_attn_paged_decode(q, cache, 264, out, prefix_table=pt, workspace=ws)
+    b.dilution_attn_paged_decode(q, cache, max_len, out, prefix_table=pt, workspace=ws)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
-        b.dilution_attn_paged_decode(q, cache, 264, out, prefix_table=pt, workspace=ws)
+        b.dilution_attn_paged_decode(q, cache, max_len, out, prefix_table=pt, workspace=ws)
     cache.demand_pages.copy_(old)
     for lens in ([70, 64, 65], [100, 0, 94], [164, 264, 94]):
         cache.seq_lens.copy_(torch.tensor(lens, dtype=torch.int32))
@@ -223,16 +234,17 @@ def test_graph_replay_with_growing_sequences():
         check_step(cache, q, before, out, ref)
 
 
-def test_two_streams_with_their_own_workspaces():
+@pytest.mark.parametrize("max_len", [900, LONG])
+def test_two_streams_with_their_own_workspaces(max_len):
     made = [make_cache(4, [900, 1, 333, 64], 4, 4, 64, 32, "bf16", seed=80 + i) for i in range(2)]
     refs = [oracle_step(c, q) for c, q, _ in made]
     before = [c.demand_pages.clone() for c, _, _ in made]
-    wss = [b.dilution_attn_paged_decode_workspace(c, 900) for c, _, _ in made]
+    wss = [b.dilution_attn_paged_decode_workspace(c, max_len) for c, _, _ in made]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(2)]
     outs = [torch.empty_like(q) for _, q, _ in made]
     for (c, q, _), ws, st, out in zip(made, wss, streams, outs):
-        b.dilution_attn_paged_decode(q, c, 900, out, workspace=ws, stream=st)
+        b.dilution_attn_paged_decode(q, c, max_len, out, workspace=ws, stream=st)
     torch.cuda.synchronize()
     for (c, q, _), o, r, old in zip(made, outs, refs, before):
         check_step(c, q, old, o, r)
@@ -260,7 +272,16 @@ def test_pool_past_32_bit_offsets():
     local = torch.tensor([[small.get(int(i), -1) for i in row] for row in ids], dtype=torch.int32, device=DEV)
     mirror = b.PagedCache(k[order].contiguous(), v[order].contiguous(), dem.clone(), local, dt, sl)
     q = torch.randn(2, Hkv, d, generator=g, device=DEV).bfloat16()
+    for cap in (700, 768):                                # 1024 keys and more: the kernels for long caches, below
+        ref = oracle_step(mirror, q)
+        before = cache.demand_pages.clone()
+        out = b.dilution_attn_paged_decode(q, cache, cap)
+        check_step(cache, q, before, out, ref)
+        mirror.demand_pages.copy_(cache.demand_pages)
+    wide = torch.cat([ids.to(DEV), torch.full((2, 20), -1, dtype=torch.int32, device=DEV)], 1)
+    wdt = torch.cat([dt, torch.full((2, 20), -1, dtype=torch.int32, device=DEV)], 1)
+    long = b.PagedCache(k, v, cache.demand_pages, wide, wdt, sl)
     ref = oracle_step(mirror, q)
-    before = cache.demand_pages.clone()
-    out = b.dilution_attn_paged_decode(q, cache, 700)
-    check_step(cache, q, before, out, ref)
+    before = long.demand_pages.clone()
+    out = b.dilution_attn_paged_decode(q, long, LONG)
+    check_step(long, q, before, out, ref)
