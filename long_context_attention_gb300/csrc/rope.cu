@@ -5,17 +5,23 @@
 // Mathematics.  Pair j of a head at position n (of the pair's axis) turns by
 // theta = n * inv_freq_j radians.  Only theta modulo one turn matters, so the
 // frequency is held in turns per position as a 64-bit fixed-point fraction
-//     F = inv_freq_j / (2 pi) * 2^64  mod 2^64
-// and n * F mod 2^64 is the angle, exact in its products: the 24-bit mantissa
-// of inv_freq_j times the first 64 bits of 1 / (2 pi), shifted by the exponent,
-// leaves F within one unit and the angle within n 2^-64 turns (n = 2^31: 7e-10
-// radians, below fp32's rounding of the cosine).  No fp64 (GB300 has few fp64
-// units) and no long fp32 products.  The products x cos - y sin run in fp32
-// and round once to the output's type.
+//     F = inv_freq_j / (2 pi) * 2^64  mod 2^64:
+// the 24-bit mantissa of inv_freq_j times the first 64 bits of 1 / (2 pi),
+// shifted by the exponent, within one unit.  n * F mod 2^64 is then the angle to
+// n 2^-64 turns, of which the upper 32 bits (2^-33 turns, 7e-10 radians, below
+// fp32's rounding of the cosine) go to sine and cosine, formed from their series.  No fp64 (GB300 has few
+// fp64 units), no long fp32 products; 32-bit multiplies and funnel shifts (a
+// version in 64-bit operations cost 140 instructions a pair and bounded the
+// append).  The products x cos - y sin run in fp32 and round once to the output's
+// type.
 //
 // What bounds it: bytes.  Each element is read once and written once; sin and
 // cos are computed in registers for one token and 16 bytes of a head's row and
-// serve `hpt` heads in turn, so they are a small part of the instructions.
+// serve `hpt` heads in turn, so they are a small part of the instructions.  The
+// loads of kRopeBatch heads are issued together before the first store: an output
+// may be its input, so the compiler cannot move a load over a store by itself
+// (one head at a time kept 32 bytes a thread in flight: 4.9 TB/s at 4 x 24 x
+// 16384 x 64 bf16).
 #include "da_rope.h"
 #include "da_ptx.cuh"
 
@@ -23,35 +29,66 @@
 
 namespace da {
 
-// inv_freq in turns per position, times 2^64 modulo 2^64.  Frequencies of
-// magnitude 2^24 and above, infinities and NaN give ok = false.
-__device__ __forceinline__ unsigned long long turns_fixed(float f, bool &ok) {
-  constexpr unsigned long long kInvTwoPi = 0x28BE60DB9391054Aull;   // floor(2^64 / (2 pi))
+// inv_freq in turns per position, times 2^64 modulo 2^64 (hi, lo).  Frequencies
+// of magnitude 2^24 and above, infinities and NaN give ok = false.
+__device__ __forceinline__ uint2 turns_fixed(float f, bool &ok) {
+  constexpr uint32_t kHi = 0x28BE60DBu, kLo = 0x9391054Au;   // floor(2^64 / (2 pi))
   const uint32_t u = __float_as_uint(f);
   int e = (int)((u >> 23) & 0xffu);
-  unsigned long long m = u & 0x7fffffu;
+  uint32_t m = u & 0x7fffffu;
   if (e == 0)
     e = 1;
   else
     m |= 0x800000u;
   const int shift = 150 - e;   // |f| = m 2^-shift
-  ok = shift > 0;
-  unsigned long long r = 0;
-  if (ok && shift < 128) {
-    const unsigned long long lo = m * kInvTwoPi, hi = __umul64hi(m, kInvTwoPi);
-    r = shift < 64 ? (lo >> shift) | (hi << (64 - shift)) : hi >> (shift - 64);
+  ok = shift >= 0;
+  // the 86-bit product, least word first
+  const unsigned long long p0 = (unsigned long long)m * kLo, p1 = (unsigned long long)m * kHi + (p0 >> 32);
+  const uint32_t w0 = (uint32_t)p0, w1 = (uint32_t)p1, w2 = (uint32_t)(p1 >> 32);
+  // bits shift .. shift + 63 of it
+  const int words = shift >> 5;
+  const uint32_t a = words == 0 ? w0 : words == 1 ? w1 : words == 2 ? w2 : 0u;
+  const uint32_t b = words == 0 ? w1 : words == 1 ? w2 : 0u;
+  const uint32_t c = words == 0 ? w2 : 0u;
+  uint32_t lo = __funnelshift_r(a, b, shift), hi = __funnelshift_r(b, c, shift);   // (by shift mod 32)
+  if (u >> 31) {
+    lo = 0u - lo;
+    hi = ~hi + (lo == 0u);
   }
-  return (u >> 31) ? 0ull - r : r;
+  return make_uint2(hi, lo);
 }
 
-// cos and sin of position * inv_freq.
-__device__ __forceinline__ void rope_sincos(float inv_freq, int pos, float sign, float &c, float &s) {
-  bool ok;
-  const unsigned long long F = turns_fixed(inv_freq, ok);
-  const long long a = (long long)((unsigned long long)(long long)pos * F);   // the angle as a signed 0.64 turn
-  sincospif((float)a * 0x1p-63f, &s, &c);
+// cos and sin of position * inv_freq, from the frequency in turns (F).  The
+// angle's top bits give the nearest quarter turn, the rest an angle of at most
+// pi / 4, whose Taylor series to the 9th and 8th power are within 2e-9 and 3e-8
+// (half an fp32 step of 1); a quarter turn swaps the two and sets the signs.
+__device__ __forceinline__ void rope_sincos(uint2 F, bool ok, int pos, float sign, float &c, float &s) {
+  // the upper word of pos F mod 2^64: the angle as a signed 0.32 turn
+  uint32_t a = F.x * (uint32_t)pos + __umulhi(F.y, (uint32_t)pos);
+  if (pos < 0) a -= F.y;
+  const uint32_t quarter = (a + 0x20000000u) >> 30;
+  const float x = (float)(int)(a - (quarter << 30)) * 1.4629180792671596e-9f;   // 2 pi 2^-32: radians
+  const float x2 = x * x;
+  float sn = fmaf(x2, 2.7557319e-6f, -1.9841270e-4f);                           // 1 / 9!, -1 / 7!
+  sn = fmaf(x2, sn, 8.3333333e-3f);
+  sn = fmaf(x2, sn, -1.6666667e-1f);
+  sn = fmaf(x2 * x, sn, x);
+  float cs = fmaf(x2, 2.4801587e-5f, -1.3888889e-3f);                           // 1 / 8!, -1 / 6!
+  cs = fmaf(x2, cs, 4.1666667e-2f);
+  cs = fmaf(x2, cs, -0.5f);
+  cs = fmaf(x2, cs, 1.f);
+  const bool swap = quarter & 1u;
+  c = swap ? sn : cs;
+  s = swap ? cs : sn;
+  if ((quarter + 1u) & 2u) c = -c;   // quarters 1, 2
+  if (quarter & 2u) s = -s;          // quarters 2, 3
   s *= sign;
   if (!ok) c = s = __int_as_float(0x7fc00000);
+}
+__device__ __forceinline__ void rope_sincos(float inv_freq, int pos, float sign, float &c, float &s) {
+  bool ok;
+  const uint2 F = turns_fixed(inv_freq, ok);
+  rope_sincos(F, ok, pos, sign, c, s);
 }
 
 template <typename E>
@@ -99,27 +136,28 @@ struct RopeUnit {
   bool rot_a, rot_b;          // whether they rotate (half-split: both or none)
   float c[N], s[N];           // half-split: N pairs; adjacent: N / 2 of each vector
 
-  // `angle(j, c, s)` gives the cosine and sine of pair j.
-  template <typename F>
-  __device__ __forceinline__ void init(int u, int n_pairs, F &&angle) {
+  __device__ __forceinline__ void place(int u, int n_pairs) {
     if constexpr (ADJ) {
       va = 2 * u * N;
       vb = va + N;
       rot_a = va < 2 * n_pairs;
       rot_b = vb < 2 * n_pairs;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        c[i] = 1.f, s[i] = 0.f;
-        if (i < N / 2 ? rot_a : rot_b) angle(va / 2 + i, c[i], s[i]);
-      }
     } else {
       const int rot_units = n_pairs / N;
       rot_a = rot_b = u < rot_units;
       va = rot_a ? u * N : 2 * n_pairs + 2 * (u - rot_units) * N;
       vb = rot_a ? va + n_pairs : va + N;
+    }
+  }
+  // `angle(j, c, s)` gives the cosine and sine of pair j.
+  template <typename F>
+  __device__ __forceinline__ void turn(F &&angle) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        c[i] = 1.f, s[i] = 0.f;
+    for (int i = 0; i < N; ++i) {
+      c[i] = 1.f, s[i] = 0.f;
+      if constexpr (ADJ) {
+        if (i < N / 2 ? rot_a : rot_b) angle(va / 2 + i, c[i], s[i]);
+      } else {
         if (rot_a) angle(va + i, c[i], s[i]);
       }
     }
@@ -154,37 +192,82 @@ struct RopeUnit {
   }
 };
 
-__device__ __forceinline__ int rope_position(const RopeParams &rp, int axis, long long b, long long t, int fallback) {
-  return rp.positions == nullptr ? fallback : __ldg(rp.positions + axis * rp.pos_stride_axis + b * rp.pos_stride_b + t);
-}
+// A token's positions on every axis, read once.
+struct RopePlace {
+  int v[DA_MAX_ROPE_AXES];
+  __device__ __forceinline__ RopePlace(const RopeParams &rp, long long b, long long t, int fallback) {
+#pragma unroll
+    for (int a = 0; a < DA_MAX_ROPE_AXES; ++a) {
+      v[a] = fallback;
+      if (rp.positions != nullptr && a < rp.n_axes)
+        v[a] = __ldg(rp.positions + a * rp.pos_stride_axis + b * rp.pos_stride_b + t);
+    }
+  }
+  __device__ __forceinline__ int on(int axis) const {
+    return axis == 0 ? v[0] : axis == 1 ? v[1] : axis == 2 ? v[2] : v[3];
+  }
+};
 
 constexpr int kRopeThreads = 128;
+constexpr int kRopeBatch = 4;   // heads loaded together
+
+// 16 bytes that are read once or written once: kept out of L1.
+__device__ __forceinline__ uint4 ld_once(const void *p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
 
 // grid.x: (token, unit) pairs, grid.y: groups of hpt heads of q followed by k.
 template <typename E, bool ADJ>
 __global__ void __launch_bounds__(kRopeThreads)
-    rope_kernel(RopeTensor q, RopeTensor k, RopeParams rp, int Hq, int Hk, int T, long long n_units, int units, int hpt) {
+    rope_kernel(RopeTensor q, RopeTensor k, const __grid_constant__ RopeParams rp, int Hq, int Hk, int T, long long n_units, int units, int hpt) {
   const long long i = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
   if (i >= n_units) return;
   const long long tok = i / units;
   const int u = (int)(i - tok * units);
   const long long b = tok / T, t = tok - b * T;
-  RopeUnit<E, ADJ> ru;
-  ru.init(u, rp.n_pairs, [&](int j, float &c, float &s) {
-    rope_sincos(__ldg(rp.inv_freq + j), rope_position(rp, rp.pair_axis[j], b, t, 0), rp.sign, c, s);
-  });
   const int h0 = blockIdx.y * hpt, h1 = min(h0 + hpt, Hq + Hk);
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
+  RopeUnit<E, ADJ> ru;
+  ru.place(u, rp.n_pairs);
+  auto source = [&](int h) -> const E * {
     const bool isq = h < Hq;
     const RopeTensor &x = isq ? q : k;
-    const int hh = isq ? h : h - Hq;
-    const E *src = static_cast<const E *>(x.in) + b * x.in_b + hh * x.in_h + t * x.in_t;
-    E *dst = static_cast<E *>(x.out) + b * x.out_b + hh * x.out_h + t * x.out_t;
-    uint4 va = *reinterpret_cast<const uint4 *>(src + ru.va), vb = *reinterpret_cast<const uint4 *>(src + ru.vb);
-    ru.apply(va, vb);
-    *reinterpret_cast<uint4 *>(dst + ru.va) = va;
-    *reinterpret_cast<uint4 *>(dst + ru.vb) = vb;
+    return static_cast<const E *>(x.in) + b * x.in_b + (isq ? h : h - Hq) * x.in_h + t * x.in_t;
+  };
+  auto target = [&](int h) -> E * {
+    const bool isq = h < Hq;
+    const RopeTensor &x = isq ? q : k;
+    return static_cast<E *>(x.out) + b * x.out_b + (isq ? h : h - Hq) * x.out_h + t * x.out_t;
+  };
+  bool first = true;
+  for (int hb = h0; hb < h1; hb += kRopeBatch) {
+    uint4 va[kRopeBatch], vb[kRopeBatch];
+#pragma unroll
+    for (int j = 0; j < kRopeBatch; ++j)
+      if (hb + j < h1) {
+        const E *src = source(hb + j);
+        va[j] = ld_once(src + ru.va);
+        vb[j] = ld_once(src + ru.vb);
+      }
+    if (first) {   // the angles while the first loads are on their way
+      const RopePlace at(rp, b, t, 0);
+      ru.turn([&](int j, float &c, float &s) {
+        rope_sincos(__ldg(rp.inv_freq + j), at.on(rp.pair_axis[j]), rp.sign, c, s);
+      });
+      first = false;
+    }
+#pragma unroll
+    for (int j = 0; j < kRopeBatch; ++j)
+      if (hb + j < h1) {
+        E *dst = target(hb + j);
+        ru.apply(va[j], vb[j]);
+        __stcs(reinterpret_cast<uint4 *>(dst + ru.va), va[j]);
+        __stcs(reinterpret_cast<uint4 *>(dst + ru.vb), vb[j]);
+      }
   }
 }
 
@@ -211,7 +294,7 @@ __device__ __forceinline__ void rope_pair(const E *src, E *dst, int j, int n_pai
 // Any alignment: one thread per pair of elements (d / 2 of them a row).
 template <typename E>
 __global__ void __launch_bounds__(kRopeThreads)
-    rope_scalar_kernel(RopeTensor q, RopeTensor k, RopeParams rp, int adjacent, int Hq, int Hk, int T,
+    rope_scalar_kernel(RopeTensor q, RopeTensor k, const __grid_constant__ RopeParams rp, int adjacent, int Hq, int Hk, int T,
                        long long n_units, int units, int hpt) {
   const long long i = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
   if (i >= n_units) return;
@@ -220,7 +303,7 @@ __global__ void __launch_bounds__(kRopeThreads)
   const long long b = tok / T, t = tok - b * T;
   float c = 1.f, s = 0.f;
   if (j < rp.n_pairs)
-    rope_sincos(__ldg(rp.inv_freq + j), rope_position(rp, rp.pair_axis[j], b, t, 0), rp.sign, c, s);
+    rope_sincos(__ldg(rp.inv_freq + j), RopePlace(rp, b, t, 0).on(rp.pair_axis[j]), rp.sign, c, s);
   const int h0 = blockIdx.y * hpt, h1 = min(h0 + hpt, Hq + Hk);
   for (int h = h0; h < h1; ++h) {
     const bool isq = h < Hq;
@@ -272,12 +355,15 @@ cudaError_t launch_rope(const RopeTensor &q, const RopeTensor &k, const RopePara
 // ---------------------------------------------------------------------------
 // Append to the paged cache.
 //
-// A block takes a run of tokens.  Its first threads place the tokens: the
-// sequence by a binary search of cu_tokens (held in shared memory up to
-// kAppendSearch sequences, so one global read serves the search), the place in
-// the cache from the sequence's length, the pages from the tables.  Then every
-// thread rotates or copies 16-byte pieces of `hpt` heads of q, k and v, and the
-// demand goes out with neighbouring threads on neighbouring tokens.
+// A block takes a run of up to 128 tokens and up to kRopeBatch heads.  Every
+// thread first issues the loads of its first 16-byte pieces (they do not depend
+// on where the token goes); meanwhile the block's threads place all the tokens,
+// one each: the sequence by a binary search of cu_tokens (held in shared memory
+// with the lengths up to kAppendSearch sequences, so one global read serves
+// both), the pages from the tables.  Then it walks the run.  Placing takes three dependent
+// reads (~3 us): blocks of 16 tokens spent most of their time on it (26600
+// tokens, d = 128: 31 us against 17 of copies).  The demand goes out with
+// neighbouring threads on neighbouring tokens.
 // ---------------------------------------------------------------------------
 constexpr int kAppendSearch = 1024;
 
@@ -286,7 +372,7 @@ struct TokenPlace {
   int page, dpage;
 };
 
-__device__ __forceinline__ TokenPlace place_token(int n, const int32_t *cu, const AppendArgs &a,
+__device__ __forceinline__ TokenPlace place_token(int n, const int32_t *cu, const int32_t *lens, const AppendArgs &a,
                                                   const dilution_attn_paged_cache &c) {
   TokenPlace p{-1, 0, 0};
   if (n >= a.N || n >= cu[c.S]) return p;   // padding
@@ -299,7 +385,7 @@ __device__ __forceinline__ TokenPlace place_token(int n, const int32_t *cu, cons
       hi = mid - 1;
   }
   const int first = cu[lo], end = cu[lo + 1];
-  const int len = __ldg(c.seq_lens + lo);
+  const int len = lens[lo];
   const long long pos = (long long)len - end + n;
   const long long pg = pos / c.page_size;
   bool ok = first >= 0 && first <= n && n < end && end <= a.N && pos >= 0 && end - first <= len && pg < c.max_pages;
@@ -319,71 +405,98 @@ __device__ __forceinline__ TokenPlace place_token(int n, const int32_t *cu, cons
 // demand.  VEC: 16-byte pieces (units of RopeUnit); else pairs of elements.
 template <typename E, bool ADJ, bool VEC>
 __global__ void __launch_bounds__(kRopeThreads)
-    append_kernel(AppendArgs a, dilution_attn_paged_cache c, RopeParams rp) {
-  __shared__ int32_t s_cu[kAppendSearch];
+    append_kernel(const __grid_constant__ AppendArgs a, const __grid_constant__ dilution_attn_paged_cache c,
+                  const __grid_constant__ RopeParams rp) {
+  __shared__ int32_t s_cu[kAppendSearch], s_len[kAppendSearch];
   __shared__ TokenPlace s_place[kRopeThreads];
-  const int32_t *cu = a.cu_tokens;
-  if (c.S + 1 <= kAppendSearch) {
-    for (int i = threadIdx.x; i <= c.S; i += kRopeThreads) s_cu[i] = __ldg(a.cu_tokens + i);
-    cu = s_cu;
-    __syncthreads();
-  }
-  const int n0 = blockIdx.x * a.tokens;
-  if (threadIdx.x < a.tokens) s_place[threadIdx.x] = place_token(n0 + threadIdx.x, cu, a, c);
-  __syncthreads();
   const int Hq = a.q != nullptr ? c.Hq : 0;
   const int rows = Hq + 2 * c.Hkv;
   const int groups = (rows + a.hpt - 1) / a.hpt;
-  if ((int)blockIdx.y == groups) {   // demand: [page][head][row]
+  const bool is_demand = (int)blockIdx.y == groups;
+  const int n0 = blockIdx.x * a.tokens;
+  const int h0 = blockIdx.y * a.hpt, h1 = min(h0 + a.hpt, rows);
+  const int h_turn = Hq + c.Hkv;                 // heads below turn, the values pass
+  // this thread's piece, and its first token of the block's run
+  const int tt0 = threadIdx.x / a.units, u = threadIdx.x - tt0 * a.units, step = kRopeThreads / a.units;
+  const bool mine = !is_demand && tt0 < step;
+  const int last = min(a.tokens, a.N - n0);
+  auto source = [&](long long n, int h) -> const E * {
+    if (h < Hq) return static_cast<const E *>(a.q) + n * a.q_t + h * a.q_h;
+    if (h < h_turn) return static_cast<const E *>(a.k) + n * a.k_t + (h - Hq) * a.k_h;
+    return static_cast<const E *>(a.v) + n * a.v_t + (h - h_turn) * a.v_h;
+  };
+  RopeUnit<E, ADJ> ru;
+  uint4 va[kRopeBatch], vb[kRopeBatch];
+  auto load = [&](int tt) {
+#pragma unroll
+    for (int j = 0; j < kRopeBatch; ++j)
+      if (h0 + j < h1) {
+        const E *src = source(n0 + tt, h0 + j);
+        va[j] = ld_once(src + ru.va);
+        vb[j] = ld_once(src + ru.vb);
+      }
+  };
+  if constexpr (VEC) {
+    ru.place(u, h0 < h_turn ? rp.n_pairs : 0);
+    if (mine && tt0 < last) load(tt0);
+  }
+  const int32_t *cu = a.cu_tokens, *lens = c.seq_lens;
+  if (c.S + 1 <= kAppendSearch) {
+    for (int i = threadIdx.x; i <= c.S; i += kRopeThreads) {
+      s_cu[i] = __ldg(a.cu_tokens + i);
+      if (i < c.S) s_len[i] = __ldg(c.seq_lens + i);
+    }
+    cu = s_cu;
+    lens = s_len;
+    __syncthreads();
+  }
+  if (threadIdx.x < a.tokens) s_place[threadIdx.x] = place_token(n0 + threadIdx.x, cu, lens, a, c);
+  __syncthreads();
+  if (is_demand) {   // [page][head][row]
     for (int i = threadIdx.x; i < a.tokens * c.Hq; i += kRopeThreads) {
-      const int tt = i % a.tokens, h = i / a.tokens;
-      const TokenPlace p = s_place[tt];
+      const int t = i % a.tokens, h = i / a.tokens;
+      const TokenPlace p = s_place[t];
       if (p.pos < 0) continue;
-      const float x = a.demand != nullptr ? a.demand[(long long)(n0 + tt) * a.dem_t + (long long)h * a.dem_h] : 0.f;
+      const float x = a.demand != nullptr ? a.demand[(long long)(n0 + t) * a.dem_t + (long long)h * a.dem_h] : 0.f;
       c.demand_pages[((size_t)p.dpage * c.Hq + h) * c.page_size + p.pos % c.page_size] = x;
     }
     return;
   }
-  const int h0 = blockIdx.y * a.hpt, h1 = min(h0 + a.hpt, rows);
-  for (int i = threadIdx.x; i < a.tokens * a.units; i += kRopeThreads) {
-    const int tt = i / a.units, u = i - tt * a.units;
-    const TokenPlace p = s_place[tt];
-    if (p.pos < 0) continue;
-    const long long n = n0 + tt;
-    auto angle = [&](int j, float &cc, float &ss) {
-      rope_sincos(__ldg(rp.inv_freq + j), rope_position(rp, rp.pair_axis[j], 0, n, p.pos), 1.f, cc, ss);
-    };
-    auto source = [&](int h) -> const E * {
-      if (h < Hq) return static_cast<const E *>(a.q) + n * a.q_t + h * a.q_h;
-      if (h < Hq + c.Hkv) return static_cast<const E *>(a.k) + n * a.k_t + (h - Hq) * a.k_h;
-      return static_cast<const E *>(a.v) + n * a.v_t + (h - Hq - c.Hkv) * a.v_h;
-    };
-    auto target = [&](int h) -> E * {
-      if (h < Hq) return static_cast<E *>(a.q_out) + ((size_t)n * c.Hq + h) * c.d;
-      const bool is_k = h < Hq + c.Hkv;
-      const size_t row =
-          ((size_t)p.page * c.Hkv + (h - Hq - (is_k ? 0 : c.Hkv))) * c.page_size + p.pos % c.page_size;
-      return static_cast<E *>(is_k ? c.k_pages : c.v_pages) + row * c.d;
-    };
-    const int h_turn = Hq + c.Hkv;                 // heads below turn, the values pass
+  if (!mine) return;
+  for (int tt = tt0; tt < last; tt += step) {
     if constexpr (VEC) {
-      RopeUnit<E, ADJ> ru;
-      ru.init(u, h0 < h_turn ? rp.n_pairs : 0, angle);
-#pragma unroll 4
-      for (int h = h0; h < h1; ++h) {
-        const E *src = source(h);
-        E *dst = target(h);
-        uint4 va = *reinterpret_cast<const uint4 *>(src + ru.va), vb = *reinterpret_cast<const uint4 *>(src + ru.vb);
-        if (h < h_turn) ru.apply(va, vb);
-        *reinterpret_cast<uint4 *>(dst + ru.va) = va;
-        *reinterpret_cast<uint4 *>(dst + ru.vb) = vb;
+      if (tt > tt0) load(tt);
+    }
+    const TokenPlace p = s_place[tt];
+    const long long n = n0 + tt;
+    if (p.pos >= 0) {
+      const RopePlace where(rp, 0, n, p.pos);
+      auto angle = [&](int j, float &cc, float &ss) {
+        rope_sincos(__ldg(rp.inv_freq + j), where.on(rp.pair_axis[j]), 1.f, cc, ss);
+      };
+      auto target = [&](int h) -> E * {
+        if (h < Hq) return static_cast<E *>(a.q_out) + ((size_t)n * c.Hq + h) * c.d;
+        const bool is_k = h < h_turn;
+        const size_t row = ((size_t)p.page * c.Hkv + (h - (is_k ? Hq : h_turn))) * c.page_size + p.pos % c.page_size;
+        return static_cast<E *>(is_k ? c.k_pages : c.v_pages) + row * c.d;
+      };
+      if constexpr (VEC) {
+        if (h0 < h_turn) ru.turn(angle);
+#pragma unroll
+        for (int j = 0; j < kRopeBatch; ++j)
+          if (h0 + j < h1) {
+            E *dst = target(h0 + j);
+            if (h0 + j < h_turn) ru.apply(va[j], vb[j]);
+            *reinterpret_cast<uint4 *>(dst + ru.va) = va[j];
+            *reinterpret_cast<uint4 *>(dst + ru.vb) = vb[j];
+          }
+      } else {
+        float c1 = 1.f, s1 = 0.f;
+        if (u < rp.n_pairs && h0 < h_turn) angle(u, c1, s1);
+        for (int h = h0; h < h1; ++h)
+          rope_pair(source(n, h), target(h), u, h < h_turn ? rp.n_pairs : 0, ADJ,
+                    [&](int, float &cc, float &ss) { cc = c1, ss = s1; });
       }
-    } else {
-      float c1 = 1.f, s1 = 0.f;
-      if (u < rp.n_pairs && h0 < h_turn) angle(u, c1, s1);
-      for (int h = h0; h < h1; ++h)
-        rope_pair(source(h), target(h), u, h < h_turn ? rp.n_pairs : 0, ADJ,
-                  [&](int, float &cc, float &ss) { cc = c1, ss = s1; });
     }
   }
 }
@@ -395,10 +508,14 @@ cudaError_t launch_append(const AppendArgs &args, const dilution_attn_paged_cach
   a.units = vec ? c.d / (2 * nv) : c.d / 2;
   const int rows = (a.q != nullptr ? c.Hq : 0) + 2 * c.Hkv;
   a.hpt = heads_per_thread((long long)a.N * a.units, rows);
-  // a run of tokens: as many as give every thread one unit, fewer when the
-  // call is too short to fill the GPU
-  a.tokens = kRopeThreads / a.units < 1 ? 1 : kRopeThreads / a.units;
-  const dim3 grid((unsigned)((a.N + a.tokens - 1) / a.tokens), (unsigned)((rows + a.hpt - 1) / a.hpt + 1));
+  if (a.hpt > kRopeBatch) a.hpt = kRopeBatch;
+  // a block's run: longer ones share the placing, as long as the blocks still
+  // fill the GPU (about 7 on each SM)
+  const int step = kRopeThreads / a.units, heads = (rows + a.hpt - 1) / a.hpt + 1;
+  int64_t turns = ((int64_t)a.N + step - 1) / step * heads / (7 * 152);
+  if (turns > kRopeThreads / step) turns = kRopeThreads / step;
+  a.tokens = step * (int)(turns < 1 ? 1 : turns);
+  const dim3 grid((unsigned)((a.N + a.tokens - 1) / a.tokens), (unsigned)heads);
 #define DA_APPEND(E, ADJ, VEC) append_kernel<E, ADJ, VEC><<<grid, kRopeThreads, 0, stream>>>(a, c, rp)
   if (c.dtype == DA_BF16) {
     if (vec)

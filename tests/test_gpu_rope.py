@@ -153,6 +153,13 @@ def test_rope_frequencies_that_are_no_numbers():
     assert y[..., bad].isnan().all()
     good = [i for i in range(64) if i not in bad]
     assert y[..., good].isfinite().all()
+    # the largest frequencies that are taken: 3 (2^24 - 1) radians, in exact arithmetic
+    from fractions import Fraction
+    pi2 = Fraction(31415926535897932384626433832795028841971693993751, 5 * 10 ** 48)
+    inv = torch.tensor([2.0 ** 24 - 1, -(2.0 ** 23), 2.0 ** -40], device=DEV)
+    y, _ = b.dilution_attn_rope(x, None, pos, b.rope_spec(inv))
+    ang = np.array([[float(Fraction(p) * Fraction(float(f)) % pi2) for f in inv.tolist()] for p in (3, 4)])
+    close(y, x, ang, False)
 
 
 # ------------------------------------------------------------------------------- append
@@ -222,6 +229,31 @@ def test_append_matches_oracle(dtype, S, lens, counts, Hq, Hkv, d, page, n, axes
         assert (got[N - extra:] == 5.0).all()                   # rows behind the last sequence stay
     else:
         assert got is None
+
+
+def test_append_long_runs_of_tokens():
+    # blocks of many tokens: prompts of different lengths in the same block, padding at the end, all types of rows
+    lens = [5000, 1, 0, 777, 3000]
+    cache, _, _ = make_cache(5, lens, 4, 2, 64, 64, "bf16", seed=14)
+    N = sum(lens) + 3
+    spec, inv, pa = spec_of(32, 3, True)
+    g = torch.Generator().manual_seed(1)
+    rows = torch.randn(N, 8, 64, generator=g).bfloat16().to(DEV)
+    ps = positions(3, 1, N, seed=6)[:, 0].contiguous()
+    demand = torch.rand(N, 4, generator=g).to(DEV)
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device=DEV)
+    ws = b.dilution_attn_paged_append_workspace(cache)
+    q = b.dilution_attn_paged_append(rows[:, :4], rows[:, 4:6], rows[:, 6:], cache, cu, rope=spec, positions=ps,
+                                     demand=demand, workspace=ws)
+    assert b.dilution_attn_get_error(ws) == b.DA_OK
+    seq = torch.repeat_interleave(torch.arange(5), torch.tensor(lens)).to(DEV)
+    at = torch.arange(N - 3, device=DEV) - cu.long()[seq]
+    pg, dpg = cache.page_table[seq, at // 64].long(), cache.demand_table[seq, at // 64].long()
+    ang = op.rope_angles(ps.cpu().numpy(), inv.cpu().numpy(), pa)[:N - 3, None]
+    close(q[:N - 3], rows[:N - 3, :4], ang, True)
+    close(cache.k_pages[pg, :, at % 64], rows[:N - 3, 4:6], ang, True)
+    assert torch.equal(cache.v_pages[pg, :, at % 64], rows[:N - 3, 6:])
+    assert torch.equal(cache.demand_pages[dpg, :, at % 64], demand[:N - 3])
 
 
 def test_append_many_sequences():
