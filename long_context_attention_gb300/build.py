@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdilution_attn.so")
 
-SOURCES = ["capi.cu", "capi_paged.cu", "rope.cu", "paged_decode.cu", "paged_decode_bf16.cu",
+SOURCES = ["capi.cu", "capi_paged.cu", "rope.cu", "paged_decode_f32.cu", "paged_decode_bf16.cu",
            "paged_prefix_bf16.cu", "paged_small_bf16.cu", "fwd_f32.cu", "fwd_bf16.cu", "decode.cu", "bwd.cu", "bwd_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -6,11 +6,9 @@
 #include "da_rope.h"
 
 namespace da {
-size_t pgs_workspace(int64_t rows, int max_len, int prefix_len, int d);
-cudaError_t launch_paged_decode_simt(const PagedDecode &p, cudaStream_t stream);
-size_t pgt_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len);
-bool pgt_fits(int S, int Hq, int Hkv, int d, int max_len, int prefix_len);
-int launch_paged_decode_bf16(const PagedDecode &p, cudaStream_t stream);
+size_t pgt_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int dtype);
+bool pgt_fits(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int dtype);
+int launch_paged_decode(const PagedDecode &p, cudaStream_t stream);
 }  // namespace da
 
 using namespace da;
@@ -147,11 +145,6 @@ int check_cache(const dilution_attn_paged_cache *c) {
   return DA_OK;
 }
 
-size_t decode_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int dtype) {
-  return dtype == DA_BF16 ? pgt_workspace(S, Hq, Hkv, d, max_len, prefix_len)
-                          : pgs_workspace((int64_t)S * Hq, max_len, prefix_len, d);
-}
-
 int check_workspace(const void *ws, size_t bytes, size_t need) {
   if (ws == nullptr || bytes < need) return DA_ERR_WORKSPACE;
   return aligned(ws, 256) ? DA_OK : DA_ERR_INVALID;
@@ -235,7 +228,7 @@ size_t dilution_attn_paged_decode_workspace_size(int S, int Hq, int Hkv, int d, 
   if (S < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_len < 0 || n_prefix_pages < 0 || page_size < 1 || !head_dim_supported(d))
     return 0;
   if ((int64_t)n_prefix_pages * page_size > max_len) return 0;
-  return decode_workspace(S, Hq, Hkv, d, max_len, n_prefix_pages * page_size, dtype);
+  return pgt_workspace(S, Hq, Hkv, d, max_len, n_prefix_pages * page_size, dtype);
 }
 
 int dilution_attn_paged_decode(const void *q, const dilution_attn_paged_cache *cache, const int32_t *prefix_table,
@@ -253,16 +246,12 @@ int dilution_attn_paged_decode(const void *q, const dilution_attn_paged_cache *c
   if (c.S == 0) return DA_OK;
   if (q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 16)) return DA_ERR_INVALID;
   const int prefix_len = n_prefix_pages * c.page_size;
-  st = check_workspace(workspace, workspace_bytes, decode_workspace(c.S, c.Hq, c.Hkv, c.d, max_len, prefix_len, c.dtype));
+  st = check_workspace(workspace, workspace_bytes, pgt_workspace(c.S, c.Hq, c.Hkv, c.d, max_len, prefix_len, c.dtype));
   if (st != DA_OK) return st;
   if ((int64_t)c.num_pages * c.Hkv > 0x7FFFFFFF) return DA_ERR_UNSUPPORTED;   // a copy's coordinate
-  // what the kernels count in 32 bits: places in the demand pool (16 floats
-  // each), work units (bf16), 16-row groups of a launch grid (fp32)
+  // what the kernels count in 32 bits: places in the demand pool (16 floats each), work units
   if ((int64_t)c.num_demand_pages * c.Hq * (c.page_size / 16) >= 0xFFFFFFFFll) return DA_ERR_UNSUPPORTED;
-  const int64_t G = c.Hq / c.Hkv;
-  if (c.dtype == DA_BF16 ? !pgt_fits(c.S, c.Hq, c.Hkv, c.d, max_len, prefix_len)
-                         : c.S * ((G + 15) / 16) + (c.S * G + 15) / 16 > 65535)
-    return DA_ERR_UNSUPPORTED;
+  if (!pgt_fits(c.S, c.Hq, c.Hkv, c.d, max_len, prefix_len, c.dtype)) return DA_ERR_UNSUPPORTED;
   PagedDecode p{};
   p.c = c;
   p.q = q;
@@ -277,8 +266,7 @@ int dilution_attn_paged_decode(const void *q, const dilution_attn_paged_cache *c
   p.earlier = (flags & DA_FLAG_EARLIER_DEMAND_ONLY) != 0;
   p.status = reinterpret_cast<int *>(workspace);
   p.ws = reinterpret_cast<uint8_t *>(workspace);
-  if (c.dtype == DA_BF16) return launch_paged_decode_bf16(p, reinterpret_cast<cudaStream_t>(stream));
-  return launch_paged_decode_simt(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  return launch_paged_decode(p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

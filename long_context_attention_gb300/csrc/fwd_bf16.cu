@@ -1036,16 +1036,18 @@ bool make_bf16_tile_map(CUtensorMap *m, const void *base, int BH, int T, int d, 
 }
 
 // For the paged decode step: a pool of `num` pages (per key head) of page_size
-// rows, copied a page (at most `rows` rows) at a time.
-bool make_page_map(CUtensorMap *m, const void *base, int64_t num, int page_size, int rows, int d) {
+// rows, copied a page (at most `rows` rows) by 128 bytes at a time.
+bool make_page_map(CUtensorMap *m, const void *base, int64_t num, int page_size, int rows, int d, int dtype) {
   EncodeTiledFn enc = get_encode_fn();
   if (enc == nullptr) return false;
+  const int eb = dtype == DA_BF16 ? 2 : 4;
   const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)page_size, (cuuint64_t)num};
-  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)page_size * d * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)(page_size < rows ? page_size : rows), 1};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * eb, (cuuint64_t)page_size * d * eb};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / eb), (cuuint32_t)(page_size < rows ? page_size : rows), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return enc(m, dtype == DA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+             const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

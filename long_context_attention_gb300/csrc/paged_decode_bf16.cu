@@ -34,9 +34,8 @@
 // pgt_keys).  The part of a segment inside one stretch is a piece and leaves
 // one partial result, in slot (CTA + segment), which grows along the line and
 // is therefore unique.
-#include "da_paged_plan.cuh"
+#include "da_paged_ring.cuh"
 
-#include <cuda.h>
 #include <cuda_bf16.h>
 
 namespace da {
@@ -70,101 +69,6 @@ struct PgtVal {
   static constexpr int kSmemBytes = 1024 + kStages * 16384 + kWarps * kWarpBytes;
 };
 
-// Byte offset of 16-byte piece `piece` of row `row` in a staged tile: boxes of
-// 64 elements (128 bytes) by a tile's rows, pieces swizzled by the row.
-template <int D>
-__device__ __forceinline__ uint32_t tile_off(int row, int piece) {
-  return (uint32_t)((piece >> 3) * pgt_tile(D) * 128 + row * 128 + (((piece & 7) ^ (row & 7)) << 4));
-}
-template <int D>
-struct PgtRing {
-  static constexpr int kTile = pgt_tile(D);
-  static constexpr int kTileBytes = kTile * D * 2;
-  uint64_t full[8], empty[8];
-  volatile int abort_word;
-  __device__ __forceinline__ void init(int stages, int arrivals) {
-    for (int i = 0; i < stages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], arrivals);   // one per consumer of a tile
-    }
-    abort_word = 0;
-    fence_mbar_init();
-  }
-};
-
-__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z) {
-  asm volatile(
-      "{\n\t.reg .b64 pol;\n\t"
-      "createpolicy.fractional.L2::evict_first.b64 pol, 1.0;\n\t"
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5}], [%2], pol;\n\t}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
-// Let the copies in flight land before the CTA exits after a timeout.
-__device__ __forceinline__ void drain(uint64_t *full, int stages, int issued) {
-  for (int st = issued > stages ? issued - stages : 0; st < issued; ++st) {
-    const unsigned long long t0 = globaltimer();
-    while (!mbar_try_wait(&full[st % stages], (uint32_t)((st / stages) & 1)))
-      if (globaltimer() - t0 > 100ull * 1000ull * 1000ull) break;
-  }
-}
-
-// Producer warp: fills the ring with the tiles of the stretch [from, to) of K or
-// V.  Lane i brings page piece i of a tile.  One warp issues about one
-// dependent instruction every 5 cycles, and a tile has 0.7 us at HBM rate, so
-// the loop is short: no divisions, one table entry per lane, fetched a tile
-// ahead.
-template <int D>
-__device__ void produce(const PagedDecode &p, const PgtPlan &w, const PgtLine &line, const PgtLens &L,
-                        PgtRing<D> &ring, const CUtensorMap *map, uint32_t base, int stages, int from, int to,
-                        const WaitCtx &wc) {
-  constexpr int TILE = pgt_tile(D);
-  const int lane = threadIdx.x % 32, sh = w.page_shift, ps = 1 << sh;
-  const int rows = min(ps, TILE), rsh = min(sh, D == 64 ? 7 : 6);
-  int slot = 0;
-  uint32_t parity = 1;
-  PgtSeg g;
-  int issued = 0;
-  for (g.start(p, w, line, L, from, to); g.n > 0; g.next(p, w, line, L)) {
-    const int32_t *table = g.s >= 0 ? p.c.page_table + (size_t)g.s * p.c.max_pages : p.prefix_table;
-    int key = g.key0 + lane * rows;                                   // this lane's piece
-    const int limit = lane * rows < TILE ? g.end : 0;                 // lanes past the tile bring nothing
-    int page = key < limit ? __ldg(table + (key >> sh)) : -1;
-    for (int k = 0; k < g.n; ++k, ++issued) {
-      const int ahead = k + 1 < g.n && key + TILE < limit ? __ldg(table + ((key + TILE) >> sh)) : -1;
-      if (!warp_wait(&ring.empty[slot], parity, wc)) {
-        if (lane == 0) drain(ring.full, stages, issued);
-        return;
-      }
-      const bool ok = (unsigned)page < (unsigned)p.c.num_pages;
-      const uint32_t have = __ballot_sync(0xffffffffu, ok);
-      if (!ok && key < limit) atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
-      if (lane == 0) mbar_arrive_expect_tx(&ring.full[slot], (uint32_t)(__popc(have) << rsh) * (D * 2));
-      __syncwarp();
-      if (ok) {
-        const uint32_t dst = base + slot * PgtRing<D>::kTileBytes + lane * rows * 128;
-#pragma unroll
-        for (int x = 0; x < D; x += 64)
-          tma_page(dst + (x / 64) * TILE * 128, map, &ring.full[slot], x, key & (ps - 1), page * p.c.Hkv + g.hkv);
-      }
-      page = ahead;
-      key += TILE;
-      if (++slot == stages) {
-        slot = 0;
-        parity ^= 1;
-      }
-    }
-  }
-  if (ring.abort_word && lane == 0) drain(ring.full, stages, issued);
-}
-
-extern __shared__ __align__(1024) uint8_t pgt_smem_raw[];
-__device__ __forceinline__ uint8_t *pgt_smem_base() {   // the swizzle counts from 1024-byte boundaries
-  return pgt_smem_raw + ((1024u - (smem_u32(pgt_smem_raw) & 1023u)) & 1023u);
-}
-
 // ------------------------------------------------------------------ pass 1: logits
 // HH: halves of 8 rows in use (1 for up to 8 rows).
 template <int D, int HH>
@@ -173,7 +77,7 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
   constexpr int KS = D / 16;   // k-steps
   constexpr int TILE = pgt_tile(D), WARPS = pgt_warps(D);
   __shared__ PgtLens L;
-  __shared__ PgtRing<D> ring;
+  __shared__ PgtRing ring;
   __shared__ float2 s_ml[WARPS][16];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   pdl_launch_dependents();
@@ -184,7 +88,7 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
   const WaitCtx wc{&ring.abort_word, p.status};
   const uint32_t base = smem_u32(pgt_smem_base());
   if (warp == WARPS) {
-    produce<D>(p, w, line, L, ring, &kmap, base, stages, from, to, wc);
+    produce<pgt_tile(D), 64>(p, w, line, L, ring, &kmap, base, stages, from, to, wc);
     return;
   }
   const int gid = lane / 4, t = lane % 4;
@@ -226,14 +130,14 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
     // meets the others at the barriers below.
     for (int k = 0; k < tiles; ++k) {
       if (!warp_wait(&ring.full[slot], parity, wc)) break;
-      const uint32_t tile = base + slot * PgtRing<D>::kTileBytes;
+      const uint32_t tile = base + slot * kStageBytes;
       const int kg = first + k * TILE;
       if (kg < g.end) {
         float acc[2][4] = {};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           uint32_t bfr[4];
-          ldsm_x4(tile + tile_off<D>(row, 2 * ks + ((lane >> 3) & 1)), bfr);
+          ldsm_x4(tile + tile_off<pgt_tile(D)>(row, 2 * ks + ((lane >> 3) & 1)), bfr);
           mma16816(acc[0], qa[ks], bfr[0], bfr[1]);
           mma16816(acc[1], qa[ks], bfr[2], bfr[3]);
         }
@@ -315,7 +219,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
   constexpr int TILE = V::kTile, WARPS = V::kWarps, HH = V::kHalves, AHEAD = V::kAhead;
   constexpr int STRIDE = V::kTileStride * TILE;   // keys between a warp's steps
   __shared__ PgtLens L;
-  __shared__ PgtRing<D> ring;
+  __shared__ PgtRing ring;
   __shared__ float s_lse[16];
   __shared__ float s_sum[WARPS][16];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -327,7 +231,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
   uint8_t *const smem = pgt_smem_base();
   const uint32_t base = smem_u32(smem);
   if (warp == WARPS) {   // the values do not depend on the first pass
-    produce<D>(p, w, line, L, ring, &vmap, base, V::kStages, from, to, wc);
+    produce<pgt_tile(D), 64>(p, w, line, L, ring, &vmap, base, V::kStages, from, to, wc);
     return;
   }
   uint8_t *const mine = smem + V::kStages * 16384 + warp * V::kWarpBytes;
@@ -475,7 +379,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
         const int fill = (-left) & 15;     // up to the end of their group; later groups are left out
         for (int j = lane; j < fill * (D / 8); j += 32) {
           const int r = sub + left + j / (D / 8);
-          asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(tile + tile_off<D>(r, j % (D / 8))), "r"(0u)
+          asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(tile + tile_off<pgt_tile(D)>(r, j % (D / 8))), "r"(0u)
                        : "memory");
         }
         fence_proxy_async_smem();
@@ -496,7 +400,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
 #pragma unroll
         for (int j = 0; j < NT; j += 2) {
           uint32_t bfr[4];
-          ldsm_x4_t(tile + tile_off<D>(vrow + 16 * gg, j + (lane >> 4)), bfr);
+          ldsm_x4_t(tile + tile_off<pgt_tile(D)>(vrow + 16 * gg, j + (lane >> 4)), bfr);
           mma16816(acc[j], a1, bfr[0], bfr[1]);
           mma16816(acc[j + 1], a1, bfr[2], bfr[3]);
           if constexpr (V::kWide) {
@@ -560,7 +464,7 @@ constexpr int kPgtCombThreads = 256;
 
 // One block a row: thread (way, e) adds 4 columns of every WAYS-th piece, then
 // the ways are added in order.
-template <int D>
+template <typename E, int D>
 __global__ void __launch_bounds__(kPgtCombThreads) pgt_combine(PagedDecode p, PgtPlan w) {
   constexpr int COLS = D / 4, WAYS = kPgtCombThreads / COLS;
   __shared__ PgtLens L;
@@ -595,32 +499,38 @@ __global__ void __launch_bounds__(kPgtCombThreads) pgt_combine(PagedDecode p, Pg
       sum += col[v * D];
       tot += s_r[v];
     }
-    static_cast<__nv_bfloat16 *>(p.out)[(size_t)blockIdx.x * D + tid] =
-        __float2bfloat16_rn(L.len[s] > 0 ? sum / tot : 0.f);
+    static_cast<E *>(p.out)[(size_t)blockIdx.x * D + tid] = (E)(L.len[s] > 0 ? sum / tot : 0.f);   // rounds to nearest
   }
 }
 
+cudaError_t launch_combine(const PagedDecode &p, const PgtPlan &w, cudaStream_t stream) {
+  const int grid = p.c.S * p.c.Hq;
+  if (p.c.dtype == DA_BF16)
+    return p.c.d == 128 ? launch_after(pgt_combine<__nv_bfloat16, 128>, grid, kPgtCombThreads, 0, stream, p, w)
+                        : launch_after(pgt_combine<__nv_bfloat16, 64>, grid, kPgtCombThreads, 0, stream, p, w);
+  return p.c.d == 128 ? launch_after(pgt_combine<float, 128>, grid, kPgtCombThreads, 0, stream, p, w)
+                      : launch_after(pgt_combine<float, 64>, grid, kPgtCombThreads, 0, stream, p, w);
+}
+
 // ------------------------------------------------------------------ host
-bool make_page_map(CUtensorMap *m, const void *base, int64_t num, int page_size, int rows, int d);   // fwd_bf16.cu
 // paged_prefix_bf16.cu: the two passes over a prefix with many rows.
 int launch_pgx_keys(const PagedDecode &p, const PgtPlan &w, cudaStream_t stream);
 int launch_pgx_values(const PagedDecode &p, const PgtPlan &w, cudaStream_t stream);
 
-size_t pgt_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len) {
-  return pgt_plan(S < kPgtMaxSeqs ? S : kPgtMaxSeqs, Hq, Hkv, d, max_len, prefix_len, 16).total;
+size_t pgt_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int dtype) {
+  return pgt_plan(S < kPgtMaxSeqs ? S : kPgtMaxSeqs, Hq, Hkv, d, max_len, prefix_len, 16, dtype).total;
 }
 // Units on the line at most (int arithmetic on the device).
-bool pgt_fits(int S, int Hq, int Hkv, int d, int max_len, int prefix_len) {
+bool pgt_fits(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int dtype) {
   if (S > kPgtMaxSeqs) S = kPgtMaxSeqs;
-  const int64_t G = Hq / Hkv, tile = pgt_tile(d), rows = (S * G + 15) / 16;
+  const int64_t G = Hq / Hkv, tile = pgt_tile(d, dtype), rt = pgt_row_tile(dtype), rows = (S * G + rt - 1) / rt;
   const int64_t own = (max_len - prefix_len + tile - 1) / tile + kPgtHead;
   const int64_t pre = (prefix_len + tile - 1) / tile + kPgtHead;
-  return S * (int64_t)Hkv * ((G + 15) / 16) * own + (prefix_len > 0 ? Hkv * rows * pre : 0) < 0x7FFF0000ll;
+  return S * (int64_t)Hkv * ((G + rt - 1) / rt) * own + (prefix_len > 0 ? Hkv * rows * pre : 0) < 0x7FFF0000ll;
 }
 
 template <int D, int GE>
 static int launch_pgt_t(const PagedDecode &p, const PgtPlan &w, cudaStream_t stream) {
-  using R = PgtRing<D>;
   using V = PgtVal<D, GE>;
   constexpr int HH = GE > 8 ? 2 : 1;
   static PerDeviceOnce once;
@@ -636,12 +546,12 @@ static int launch_pgt_t(const PagedDecode &p, const PgtPlan &w, cudaStream_t str
   CUtensorMap km, vm;
   const int64_t num = (int64_t)p.c.num_pages * p.c.Hkv;
   // an empty pool has no pages to map; every page id then fails its check, and no copy is issued
-  if (!make_page_map(&km, p.c.k_pages, num > 0 ? num : 1, p.c.page_size, R::kTile, D) ||
-      !make_page_map(&vm, p.c.v_pages, num > 0 ? num : 1, p.c.page_size, R::kTile, D))
+  if (!make_page_map(&km, p.c.k_pages, num > 0 ? num : 1, p.c.page_size, pgt_tile(D), D, DA_BF16) ||
+      !make_page_map(&vm, p.c.v_pages, num > 0 ? num : 1, p.c.page_size, pgt_tile(D), D, DA_BF16))
     return DA_ERR_CUDA;
-  constexpr int k_stages = (kPgtSmemPerCta - 1024) / R::kTileBytes;
+  constexpr int k_stages = (kPgtSmemPerCta - 1024) / kStageBytes;
   static_assert(k_stages <= 8, "the ring's barriers");
-  pgt_keys<D, HH><<<w.ctas, pgt_threads(D), 1024 + k_stages * R::kTileBytes, stream>>>(p, w, km, k_stages);
+  pgt_keys<D, HH><<<w.ctas, pgt_threads(D), 1024 + k_stages * kStageBytes, stream>>>(p, w, km, k_stages);
   if (w.wide) {
     const int st = launch_pgx_keys(p, w, stream);
     if (st != DA_OK) return st;
@@ -652,14 +562,14 @@ static int launch_pgt_t(const PagedDecode &p, const PgtPlan &w, cudaStream_t str
     const int st = launch_pgx_values(p, w, stream);
     if (st != DA_OK) return st;
   }
-  if (launch_after(pgt_combine<D>, p.c.S * p.c.Hq, kPgtCombThreads, 0, stream, p, w) != cudaSuccess)
+  if (launch_combine(p, w, stream) != cudaSuccess)
     return DA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 template <int D>
 static int launch_pgt_d(const PagedDecode &p, cudaStream_t stream) {
-  const PgtPlan w = pgt_plan(p.c.S, p.c.Hq, p.c.Hkv, D, p.max_len, p.prefix_len, p.c.page_size);
+  const PgtPlan w = pgt_plan(p.c.S, p.c.Hq, p.c.Hkv, D, p.max_len, p.prefix_len, p.c.page_size, DA_BF16);
   int rows = w.own_rows;                                 // the most rows of a segment
   if (w.prefix_segs > 0) rows = p.c.S * w.G < 16 ? p.c.S * w.G : 16;
   if (rows <= 1) return launch_pgt_t<D, 1>(p, w, stream);
@@ -672,21 +582,26 @@ static int launch_pgt_d(const PagedDecode &p, cudaStream_t stream) {
 // paged_small_bf16.cu: short calls in one launch.
 int small_cluster(int S, int Hq, int Hkv, int d, int max_len);
 int launch_paged_small_bf16(const PagedDecode &p, int csize, cudaStream_t stream);
+// paged_decode_f32.cu
+int launch_paged_f32(const PagedDecode &p, cudaStream_t stream);
 
-int launch_paged_decode_bf16(const PagedDecode &a, cudaStream_t stream) {
-  const int cluster = small_cluster(a.c.S, a.c.Hq, a.c.Hkv, a.c.d, a.max_len);
+int launch_paged_decode(const PagedDecode &a, cudaStream_t stream) {
+  const bool bf16 = a.c.dtype == DA_BF16;
+  const int cluster = bf16 ? small_cluster(a.c.S, a.c.Hq, a.c.Hkv, a.c.d, a.max_len) : 0;
   if (cluster > 0) return launch_paged_small_bf16(a, cluster, stream);
   for (int s0 = 0; s0 < a.c.S; s0 += kPgtMaxSeqs) {   // the kernels keep the lengths of one part in shared memory
     PagedDecode p = a;
-    const size_t rows = (size_t)s0 * a.c.Hq;
+    const size_t rows = (size_t)s0 * a.c.Hq, skip = rows * a.c.d * (bf16 ? 2 : 4);
     p.c.S = a.c.S - s0 < kPgtMaxSeqs ? a.c.S - s0 : kPgtMaxSeqs;
     p.c.page_table += (size_t)s0 * a.c.max_pages;
     p.c.demand_table += (size_t)s0 * a.c.max_pages;
     p.c.seq_lens += s0;
-    p.q = static_cast<const __nv_bfloat16 *>(a.q) + rows * a.c.d;
-    p.out = static_cast<__nv_bfloat16 *>(a.out) + rows * a.c.d;
+    p.q = static_cast<const uint8_t *>(a.q) + skip;
+    p.out = static_cast<uint8_t *>(a.out) + skip;
     if (a.hs.tau_bh != nullptr) p.hs.tau_bh = a.hs.tau_bh + rows;
-    const int st = a.c.d == 128 ? launch_pgt_d<128>(p, stream) : launch_pgt_d<64>(p, stream);
+    const int st = !bf16           ? launch_paged_f32(p, stream)
+                   : a.c.d == 128 ? launch_pgt_d<128>(p, stream)
+                                  : launch_pgt_d<64>(p, stream);
     if (st != DA_OK) return st;
   }
   return DA_OK;

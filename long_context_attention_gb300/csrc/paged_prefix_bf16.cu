@@ -42,7 +42,8 @@
 
 namespace da {
 
-bool make_page_map(CUtensorMap *m, const void *base, int64_t num, int page_size, int rows, int d);   // fwd_bf16.cu
+bool make_page_map(CUtensorMap *m, const void *base, int64_t num, int page_size, int rows, int d,
+                   int dtype);   // fwd_bf16.cu
 
 constexpr uint32_t kXHalf = 128 * 128;        // 128 rows x 64 bf16
 constexpr uint32_t kXQHalf = kPgxRows * 128;  // 64 rows x 64 bf16
@@ -728,8 +729,8 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
 template <int D>
 static bool x_maps(const PagedDecode &p, CUtensorMap *km, CUtensorMap *vm) {
   const int64_t num = (int64_t)p.c.num_pages * p.c.Hkv;
-  return make_page_map(km, p.c.k_pages, num > 0 ? num : 1, p.c.page_size, kPgxTile, D) &&
-         make_page_map(vm, p.c.v_pages, num > 0 ? num : 1, p.c.page_size, kPgxTile, D);
+  return make_page_map(km, p.c.k_pages, num > 0 ? num : 1, p.c.page_size, kPgxTile, D, DA_BF16) &&
+         make_page_map(vm, p.c.v_pages, num > 0 ? num : 1, p.c.page_size, kPgxTile, D, DA_BF16);
 }
 
 template <int D>

@@ -29,11 +29,12 @@ def test_ragged_decode_matches_oracle(dtype, S, lens, Hq, Hkv, d, page):
     both_sizes(cache, q, max(lens))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("G", [1, 2, 3, 8, 12])
-def test_long_runs_of_tiles(G, d):
+def test_long_runs_of_tiles(G, d, dtype):
     # every CTA takes many tiles in a row, across sequences: 2 CTAs on 152 SMs share 2 x 40000 keys of 4 heads
-    cache, q, _ = make_cache(3, [40000, 20001, 30], 4 * G, 4, d, 64, "bf16", seed=90 + G)
+    cache, q, _ = make_cache(3, [40000, 20001, 30], 4 * G, 4, d, 64, dtype, seed=90 + G)
     before = cache.demand_pages.clone()
     out = b.dilution_attn_paged_decode(q, cache, 40000)
     # the oracle on one query head of every sequence
