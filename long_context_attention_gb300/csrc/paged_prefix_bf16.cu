@@ -19,9 +19,10 @@
 //
 // pgx_values: S^T[key, row] = K Q^T (M = 128 keys, N = 64 rows), one thread per
 // key.  The demand of a tile lies in shared memory, [row][key]; every warp
-// brings that of its own 32 keys by 16-byte asynchronous copies, 16 rows at a
-// time into the place of rows it has just written back, so that 64 KB an SM are
-// always in flight or waiting.  The shares go to shared memory as the MN-major A
+// brings that of its own 32 keys by 16-byte asynchronous copies, 8 rows at a
+// time, two groups ahead, into the place of rows it has just written back (32 KB
+// an SM; 64 KB left the values one stage at d = 128, which then came too late:
+// 95 us for 32 x 16 heads x 32768).  The shares go to shared memory as the MN-major A
 // operand of D[row, :] += share^T [V | 1]: rows 0-63 of M = 128 hold the shares
 // rounded to bf16, rows 64-127 what the rounding left (2^-16 relative in all;
 // the second term costs no instruction).  Two pairs of warpgroups take alternate
@@ -324,15 +325,16 @@ struct XVal {
   static constexpr int kDemandWarps = 16;              // warpgroup x: tiles of parity x & 1, rows 32 (x >> 1) ..
   static constexpr int kThreads = 640;                 // and a warp each for K, V, MMA and the table
   static constexpr int kTB = kPgxTile * D * 2;
-  static constexpr int kStages = D == 64 ? 2 : 1;      // what the demand leaves room for
+  static constexpr int kKStages = D == 64 ? 3 : 1;     // K: each stage is free as soon as its S is formed
+  static constexpr int kVStages = D == 64 ? 3 : 2;
   static constexpr uint32_t kShBytes = 32 * 1024;      // a warpgroup's shares: 2 x 64 rows x 128 keys
   static constexpr uint32_t kOffQ = 0;
   static constexpr uint32_t kOffK = kPgxRows * D * 2;
-  static constexpr uint32_t kOffV = kOffK + kStages * kTB;
-  static constexpr uint32_t kOffSh = kOffV + kStages * kTB;
+  static constexpr uint32_t kOffV = kOffK + kKStages * kTB;
+  static constexpr uint32_t kOffSh = kOffV + kVStages * kTB;
   static constexpr uint32_t kOffOnes = kOffSh + 2 * kShBytes;   // above every V tile (positive offset)
-  static constexpr uint32_t kOffDem = kOffOnes + 2048;          // demand: 16 warps x [32 rows][32 keys]
-  static constexpr uint32_t kOffTab = kOffDem + 16 * 4096;      // 4 tables [8 groups of 16 keys][64 rows, padded]
+  static constexpr uint32_t kOffDem = kOffOnes + 2048;          // demand: 16 warps x 2 x [8 rows][32 keys]
+  static constexpr uint32_t kOffTab = kOffDem + 16 * 2048;      // 4 tables [8 groups of 16 keys][64 rows, padded]
   static constexpr uint32_t kOffRow = kOffTab + 4 * kTabWords * 4;       // c2, then -lse2, of the rows
   static constexpr uint32_t kOffBar = kOffRow + kPgxRows * 8;
   static constexpr int kSmemBytes = 1024 + kOffBar + 512;
@@ -353,8 +355,8 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
   uint32_t *sTab = reinterpret_cast<uint32_t *>(smem + C::kOffTab);
   float *sC2 = reinterpret_cast<float *>(smem + C::kOffRow), *sNl = sC2 + kPgxRows;
   uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + C::kOffBar);
-  uint64_t *k_full = q_full + 1, *k_empty = k_full + C::kStages, *v_full = k_empty + C::kStages,
-           *v_empty = v_full + C::kStages, *s_full = v_empty + C::kStages, *s_free = s_full + 2, *sh_full = s_free + 2,
+  uint64_t *k_full = q_full + 1, *k_empty = k_full + C::kKStages, *v_full = k_empty + C::kKStages,
+           *v_empty = v_full + C::kVStages, *s_full = v_empty + C::kVStages, *s_free = s_full + 2, *sh_full = s_free + 2,
            *sh_free = sh_full + 2, *tab_full = sh_free + 2, *tab_free = tab_full + 4, *d_full = tab_free + 4,
            *d_free = d_full + 1, *done = d_free + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
@@ -364,9 +366,11 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
   pdl_launch_dependents();
   if (tid == 0) {
     mbar_init(q_full, 1);
-    for (int i = 0; i < C::kStages; ++i) {
+    for (int i = 0; i < C::kKStages; ++i) {
       mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < C::kVStages; ++i) {
       mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
     }
@@ -405,14 +409,15 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
     const CUtensorMap *map = isk ? &kmap : &vmap;
     uint8_t *ring = isk ? sK : sV;
     uint64_t *full = isk ? k_full : v_full, *empty = isk ? k_empty : v_empty;
+    const int stages = isk ? C::kKStages : C::kVStages;
     int issued = 0;
     for (; it.c.n > 0; it.next(p, w)) {
       int page = x_page<D>(p, w, it.c.tile, lane);
       bool ok = true;
       for (int k = 0; k < it.c.n; ++k, ++issued) {
         const int ahead = k + 1 < it.c.n ? x_page<D>(p, w, it.c.tile + k + 1, lane) : -1;
-        const int s = issued % C::kStages;
-        ok = warp_wait(&empty[s], ((issued / C::kStages) & 1) ^ 1, wc);
+        const int s = issued % stages;
+        ok = warp_wait(&empty[s], ((issued / stages) & 1) ^ 1, wc);
         if (!ok) break;
         x_load<D>(p, w, map, ring + s * C::kTB, &full[s], it.c.tile + k, it.c.hkv, page, lane);
         page = ahead;
@@ -420,8 +425,8 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
       if (!ok) break;
     }
     if (*abort_flag && lane == 0)
-      for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
-        x_drain(&full[i % C::kStages], (i / C::kStages) & 1);
+      for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+        x_drain(&full[i % stages], (i / stages) & 1);
   } else if (warp == C::kDemandWarps + 2) {
     // ------------------------------------------------------------ MMA issue
     // S(0), S(1), then S(k + 2) before PV(k): the buffer of S(k) is free once
@@ -436,8 +441,8 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
       for (; ok && it.c.n > 0; it.next(p, w), ++piece) {
         const int n = it.c.n, run = it.c.run;
         auto scores = [&](int k) {
-          const int t = run + k, s = t % C::kStages, g = t & 1;
-          if (!mbar_wait(&k_full[s], (t / C::kStages) & 1, wc) || !mbar_wait(&s_free[g], ((t >> 1) & 1) ^ 1, wc))
+          const int t = run + k, s = t % C::kKStages, g = t & 1;
+          if (!mbar_wait(&k_full[s], (t / C::kKStages) & 1, wc) || !mbar_wait(&s_free[g], ((t >> 1) & 1) ^ 1, wc))
             return false;
           tc_fence_after();
           const uint64_t dKs = dK + (uint64_t)s * (C::kTB >> 4);
@@ -454,8 +459,8 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
             ok = false;
             break;
           }
-          const int t = run + k, s = t % C::kStages, g = t & 1;
-          ok = mbar_wait(&v_full[s], (t / C::kStages) & 1, wc) && mbar_wait(&sh_full[g], (t >> 1) & 1, wc) &&
+          const int t = run + k, s = t % C::kVStages, g = t & 1;
+          ok = mbar_wait(&v_full[s], (t / C::kVStages) & 1, wc) && mbar_wait(&sh_full[g], (t >> 1) & 1, wc) &&
                (k > 0 || mbar_wait(d_free, (piece & 1) ^ 1, wc));
           if (!ok) break;
           tc_fence_after();
@@ -527,12 +532,12 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
     const uint32_t ts = tmem + g * 64 + 32 * rh + ((uint32_t)(quarter * 32) << 16);
     uint8_t *sh_row = sSh + g * C::kShBytes + (key_l / 8) * 1024 + (key_l % 8) * 128;
     // the warp's demand: lane -> row 4 j + lane / 8, keys 4 (lane % 8) .. of the warp's 32
-    float *const dem = reinterpret_cast<float *>(smem + C::kOffDem + warp * 4096);
+    float *const dem = reinterpret_cast<float *>(smem + C::kOffDem + warp * 2048);
     const int dr = lane / 8, dk = 4 * (lane % 8);
     const uint32_t *tab_lane = sTab + ((quarter * 32 + dk) >> 4) * kTabPitch + 32 * rh + dr;
     float *const pool = p.c.demand_pages + (dk & 15);
     float *const slot = dem + dr * 32 + dk;
-    float *const mine = dem + lane;                  // this thread's key: row r at 32 r
+    float *const mine = dem + lane;                  // this thread's key: row r of a group at 32 r
     int piece = 0;
     for (; it.c.n > 0; it.next(p, w), ++piece) {
       const int n = it.c.n;
@@ -558,11 +563,11 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
       if (tid == 0) mbar_arrive(q_full);
       const bool dead = __any_sync(0xffffffffu, *abort_flag != 0);
       const int k0 = (g ^ (it.c.run & 1));           // the warpgroup's first tile: alternate over the whole run
-      const int groups = min(2, (it.c.nrows - 32 * rh + 15) / 16);   // 16-row groups of the half with rows (or < 1)
-      for (int i = 2 * max(groups, 0); i < 4; ++i) {   // rows past them: no share (the products before are done)
-        const int at = ((4 * rh + i) ^ (key_l & 7)) << 4;
-        *reinterpret_cast<uint4 *>(sh_row + at) = make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4 *>(sh_row + 16384 + at) = make_uint4(0u, 0u, 0u, 0u);
+      const int groups = min(4, (it.c.nrows - 32 * rh + 7) / 8);   // 8-row groups of the half with rows (or < 1)
+      for (int i = max(groups, 0); i < 4; ++i) {   // rows past them: no share (the products before are done)
+        const int to = ((4 * rh + i) ^ (key_l & 7)) << 4;
+        *reinterpret_cast<uint4 *>(sh_row + to) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(sh_row + 16384 + to) = make_uint4(0u, 0u, 0u, 0u);
       }
       // The places of the lane's demand, for the tile at hand and the next.
       uint32_t at[8], at_next[8];
@@ -570,16 +575,19 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] = valid ? tab[4 * j] : kNoDemand;
       };
-      // 16 rows of a tile's demand: one group of copies.  A place without demand
-      // keeps what it held: zero, or the demand of an earlier key (both finite).
+      // 8 rows of a tile's demand: one group of copies, into place c & 1; zeros
+      // where there is none.
       auto bring = [&](const uint32_t (&a)[8], int c) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (a[4 * c + j] != kNoDemand) cp_async16(slot + (16 * c + 4 * j) * 32, pool + (size_t)a[4 * c + j] * 16);
+        for (int j = 0; j < 2; ++j) {
+          float *to = slot + (8 * (c & 1) + 4 * j) * 32;
+          if (a[2 * c + j] != kNoDemand)
+            cp_async16(to, pool + (size_t)a[2 * c + j] * 16);
+          else
+            *reinterpret_cast<float4 *>(to) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
-#pragma unroll
-      for (int j = 0; j < 8; ++j) *reinterpret_cast<float4 *>(slot + 4 * j * 32) = make_float4(0.f, 0.f, 0.f, 0.f);
       bool ok = !dead;
       if (ok && k0 < n) {
         const int t = it.c.run + k0;
@@ -603,23 +611,23 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
         tc_fence_after();
         if (groups < 1) x_release(&s_free[g], lane);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < 4; ++c) {
           asm volatile("cp.async.wait_group 1;" ::: "memory");   // this group's copies have landed
           if (c < groups) {
-            float x[16];
-            tmem_ld16(ts + 16 * c, x);
+            float x[8];
+            tmem_ld8(ts + 8 * c, x);
             __syncwarp();                                        // .. those of every lane
-            tmem_wait_ld_r16(x);
+            tmem_wait_ld_r8(x);
             if (c == groups - 1) x_release(&s_free[g], lane);    // the next tile's S may be formed
-            uint32_t hi[8], lo[8];
+            uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float4 sc = *reinterpret_cast<const float4 *>(sC2 + 32 * rh + 16 * c + 4 * q);
-              const float4 nl = *reinterpret_cast<const float4 *>(sNl + 32 * rh + 16 * c + 4 * q);
+            for (int q = 0; q < 2; ++q) {
+              const float4 sc = *reinterpret_cast<const float4 *>(sC2 + 32 * rh + 8 * c + 4 * q);
+              const float4 nl = *reinterpret_cast<const float4 *>(sNl + 32 * rh + 8 * c + 4 * q);
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const int r = 4 * q + 2 * e;
-                float *m0 = mine + (16 * c + r) * 32;
+                float *m0 = mine + (8 * (c & 1) + r) * 32;
                 const float2 y = ffma2(make_float2(x[r], x[r + 1]), e ? make_float2(sc.z, sc.w) : make_float2(sc.x, sc.y),
                                        e ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y));
                 const float2 bid = make_float2(ex2_approx(y.x), ex2_approx(y.y));
@@ -636,22 +644,21 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
                 lo[2 * q + e] = pack_bf16x2(rest.x, rest.y);
               }
             }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {   // rows 32 rh + 16 c + 8 i ..: a 16-byte piece of each block
-              const int to = ((4 * rh + 2 * c + i) ^ (key_l & 7)) << 4;
-              *reinterpret_cast<uint4 *>(sh_row + to) =
-                  make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-              *reinterpret_cast<uint4 *>(sh_row + 16384 + to) =
-                  make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-            }
+            const int to = ((4 * rh + c) ^ (key_l & 7)) << 4;    // rows 32 rh + 8 c ..: a 16-byte piece of each block
+            *reinterpret_cast<uint4 *>(sh_row + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(sh_row + 16384 + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             __syncwarp();                                        // the new demand of every lane's key
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float4 d4 = *reinterpret_cast<const float4 *>(slot + (16 * c + 4 * j) * 32);
-              if (at[4 * c + j] != kNoDemand) *reinterpret_cast<float4 *>(pool + (size_t)at[4 * c + j] * 16) = d4;
+            for (int j = 0; j < 2; ++j) {
+              const float4 d4 = *reinterpret_cast<const float4 *>(slot + (8 * (c & 1) + 4 * j) * 32);
+              if (at[2 * c + j] != kNoDemand) *reinterpret_cast<float4 *>(pool + (size_t)at[2 * c + j] * 16) = d4;
             }
           }
-          bring(at_next, c);                                     // over what this lane has just written back
+          // two groups on, over what this lane has just written back
+          if (c < 2)
+            bring(at, c + 2);
+          else
+            bring(at_next, c - 2);
         }
         fence_proxy_async_smem();
         __syncwarp();
