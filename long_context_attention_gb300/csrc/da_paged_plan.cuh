@@ -27,6 +27,11 @@ constexpr int kPgxRows = 64;      // rows of a segment there
 constexpr int kPgxTile = 128;     // keys of a tile
 constexpr int kPgxCtas = 152;     // pgx_values: one CTA an SM
 constexpr int kPgxKeyCtas = 304;  // pgx_keys: two
+// Beginning and ending a piece there costs about as much as this many tiles (8 us
+// of normalisers, queries and first copies, 3 us of sums; a tile 2.5 us; pgx_keys
+// 3 us and 1 us): a segment takes as many units before its first tile, so that a
+// CTA with two pieces gets fewer tiles.
+constexpr int kPgxHead = 4;
 
 // Equal cut of `total` units into stretches of base or base + 1.
 struct PgtCut {
@@ -77,8 +82,8 @@ inline PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_l
   w.x_tiles = w.wide ? (prefix_len + kPgxTile - 1) / kPgxTile : 0;
   w.x_groups = w.wide ? (rows + kPgxRows - 1) / kPgxRows : 0;
   w.x_segs = Hkv * w.x_groups;
-  w.x_keys = pgt_cut(w.x_segs * w.x_tiles, kPgxKeyCtas);
-  w.x_values = pgt_cut(w.x_segs * w.x_tiles, kPgxCtas);
+  w.x_keys = pgt_cut(w.x_segs * (w.x_tiles + kPgxHead), kPgxKeyCtas);
+  w.x_values = pgt_cut(w.x_segs * (w.x_tiles + kPgxHead), kPgxCtas);
   w.pre_rows = w.wide ? kPgxRows : w.row_tile;
   w.logit_key0 = w.wide ? prefix_len : 0;
   const int64_t own_tiles = (max_len - prefix_len + w.tile - 1) / w.tile;
@@ -258,7 +263,8 @@ __device__ __forceinline__ PgtPieces pgt_pieces(const PagedDecode &p, const PgtP
   if (w.wide) {
     const int R = s * w.G + g, seg = hkv * w.x_groups + R / kPgxRows;
     const PgtCut &c = values ? w.x_values : w.x_keys;
-    const int c0 = c.cta_of(seg * w.x_tiles), c1 = c.cta_of(seg * w.x_tiles + w.x_tiles - 1);
+    const int first = seg * (w.x_tiles + kPgxHead) + kPgxHead;
+    const int c0 = c.cta_of(first), c1 = c.cta_of(first + w.x_tiles - 1);
     r.pre0 = c0 + seg;
     r.npre = c1 - c0 + 1;
     r.pre_row = R % kPgxRows;

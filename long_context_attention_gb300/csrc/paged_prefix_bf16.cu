@@ -64,7 +64,7 @@ __device__ __forceinline__ void x_release(uint64_t *bar, int lane) {   // after 
   if (lane == 0) mbar_arrive(bar);
 }
 
-// Pieces of a CTA's stretch of (segment, key tile) pairs.
+// Pieces of a CTA's stretch of the segments' units.
 struct XPiece {
   int hkv, row0, nrows;   // rows of the batch
   int seg, tile, n;       // segment, first key tile, tiles
@@ -76,9 +76,11 @@ struct XWalk {
   __device__ __forceinline__ void set(const PagedDecode &p, const PgtPlan &w) {
     c.n = 0;
     if (at >= to) return;
-    c.seg = at / w.x_tiles;
-    c.tile = at - c.seg * w.x_tiles;
-    c.n = min(w.x_tiles - c.tile, to - at);
+    const int units = w.x_tiles + kPgxHead;   // a segment: its head, then its tiles
+    c.seg = at / units;
+    c.tile = max(at - c.seg * units - kPgxHead, 0);
+    at = c.seg * units + kPgxHead + c.tile;   // the piece's first tile
+    c.n = max(min(w.x_tiles - c.tile, to - at), 0);
     c.hkv = c.seg / w.x_groups;
     c.row0 = c.seg % w.x_groups * kPgxRows;
     c.nrows = min(kPgxRows, p.c.S * w.G - c.row0);
