@@ -50,10 +50,7 @@ bool pieces_ok(const void *p, const long long *strides, const long long *extents
     if (extents[i] > 1 && strides[i] % nv != 0) return false;
   return true;
 }
-bool pairs_ok(int n_pairs, int adjacent, int dtype) {
-  const int nv = 16 / elem_bytes(dtype);
-  return (adjacent ? 2 * n_pairs : n_pairs) % nv == 0;
-}
+bool pairs_ok(int n_pairs, int adjacent, int dtype) { return adjacent || n_pairs % (16 / elem_bytes(dtype)) == 0; }
 
 // An output must not address an element twice: its strides, sorted, each step
 // over the extent below (rows of d elements at the bottom).
@@ -97,7 +94,7 @@ int rope_call(const void *q, const int64_t *q_strides, const void *k, const int6
   rp.pos_stride_axis = (long long)pos_batch * T;
   rp.pos_stride_b = pos_batch == 1 ? 0 : T;
   rp.sign = sign;
-  bool vec = pairs_ok(rp.n_pairs, spec->adjacent, dtype);
+  bool vec = true;
   RopeTensor t[2] = {};
   const void *in[2] = {q, k};
   void *out[2] = {q_out, k_out};
@@ -117,7 +114,8 @@ int rope_call(const void *q, const int64_t *q_strides, const void *k, const int6
     vec = vec && pieces_ok(in[i], si, ext, 3, dtype) && pieces_ok(out[i], so, ext, 3, dtype);
     t[i] = RopeTensor{in[i], out[i], si[0], si[1], si[2], so[0], so[1], so[2]};
   }
-  return launch_rope(t[0], t[1], rp, spec->adjacent != 0, vec, B, Hq, Hk, T, d, dtype,
+  const RopePath path = !vec ? kRopeScalar : pairs_ok(rp.n_pairs, spec->adjacent, dtype) ? kRopeUnits : kRopeAny;
+  return launch_rope(t[0], t[1], rp, spec->adjacent != 0, path, B, Hq, Hk, T, d, dtype,
                      reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? DA_OK
              : DA_ERR_CUDA;

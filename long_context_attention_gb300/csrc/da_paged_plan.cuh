@@ -19,10 +19,16 @@ constexpr int kPgtMaxCtas = 2 * 152;              // two resident CTAs on each S
 
 constexpr int kPgtHead = 4;   // units of a segment before its first tile (a piece costs ~2 us beside its tiles' 0.5 us)
 
-// Rows of the batch at the prefix (sequences x query heads of one key head)
-// from which the tcgen05 kernels take it: they work on 64 rows at a time, the
-// streaming kernels on 16 and read the prefix's keys from L2 once per 16 rows.
+// Which kernels take a shared prefix.  The streaming kernels work on 16 rows (of
+// the batch's sequences x query heads of one key head) at a time and read the
+// prefix's keys from L2 once per 16 rows; the tcgen05 kernels take 64 rows, but
+// are two launches more.  Device time of a step, tcgen05 against streaming, in us:
+// 96 rows x 12 key heads x 16384 keys (19 M pairs) 77 against 111, 24 x 12 x 16384
+// (4.7 M) 44.6 against 44.5, 44 x 2 x 37808 (3.3 M) 37 against 30, 80 x 8 x 4096
+// (2.6 M) 38 against 33.
 constexpr int kPgxMinRows = 17;
+constexpr int64_t kPgxMinPairs = 4ll << 20;
+enum PgxUse { kPgxAuto, kPgxNever, kPgxAlways };
 constexpr int kPgxRows = 64;      // rows of a segment there
 constexpr int kPgxTile = 128;     // keys of a tile
 constexpr int kPgxCtas = 152;     // pgx_values: one CTA an SM
@@ -63,7 +69,8 @@ struct PgtPlan {
   size_t logit_off, own_ml_off, own_acc_off, pre_ml_off, pre_acc_off, total;
 };
 
-inline PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int page_size, int dtype) {
+inline PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int page_size, int dtype,
+                        PgxUse use = kPgxAuto) {
   PgtPlan w;
   w.row_tile = pgt_row_tile(dtype);
   w.page_shift = 0;
@@ -74,7 +81,8 @@ inline PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_l
   w.tile = pgt_tile(d, dtype);
   w.own_segs = S * Hkv * w.own_groups;
   const int rows = S * w.G;
-  w.wide = dtype == DA_BF16 && prefix_len > 0 && rows >= kPgxMinRows;
+  w.wide = dtype == DA_BF16 && prefix_len > 0 && rows >= kPgxMinRows && use != kPgxNever &&
+           (use == kPgxAlways || (int64_t)rows * Hkv * prefix_len >= kPgxMinPairs);
   const bool narrow = prefix_len > 0 && !w.wide;
   w.prefix_tiles = narrow ? (prefix_len + w.tile - 1) / w.tile : 0;
   w.prefix_groups = narrow ? (rows + w.row_tile - 1) / w.row_tile : 0;

@@ -32,8 +32,11 @@ struct AppendArgs {
   int *status;
 };
 
-cudaError_t launch_rope(const RopeTensor &q, const RopeTensor &k, const RopeParams &rp, bool adjacent, bool vec, int B,
-                        int Hq, int Hk, int T, int d, int dtype, cudaStream_t stream);
+// Rows in 16-byte pieces that hold whole pairs (or their halves), in 16-byte
+// pieces otherwise, or of any alignment.
+enum RopePath { kRopeUnits, kRopeAny, kRopeScalar };
+cudaError_t launch_rope(const RopeTensor &q, const RopeTensor &k, const RopeParams &rp, bool adjacent, RopePath path,
+                        int B, int Hq, int Hk, int T, int d, int dtype, cudaStream_t stream);
 cudaError_t launch_append(const AppendArgs &args, const dilution_attn_paged_cache &c, const RopeParams &rp, bool vec,
                           cudaStream_t stream);
 

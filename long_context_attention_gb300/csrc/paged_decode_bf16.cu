@@ -518,7 +518,11 @@ int launch_pgx_keys(const PagedDecode &p, const PgtPlan &w, cudaStream_t stream)
 int launch_pgx_values(const PagedDecode &p, const PgtPlan &w, cudaStream_t stream);
 
 size_t pgt_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int dtype) {
-  return pgt_plan(S < kPgtMaxSeqs ? S : kPgtMaxSeqs, Hq, Hkv, d, max_len, prefix_len, 16, dtype).total;
+  if (S > kPgtMaxSeqs) S = kPgtMaxSeqs;
+  // enough for either way of taking a prefix, so that the size depends on the prefix's presence alone
+  const size_t a = pgt_plan(S, Hq, Hkv, d, max_len, prefix_len, 16, dtype, kPgxNever).total;
+  const size_t b = pgt_plan(S, Hq, Hkv, d, max_len, prefix_len, 16, dtype, kPgxAlways).total;
+  return a > b ? a : b;
 }
 // Units on the line at most (int arithmetic on the device).
 bool pgt_fits(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int dtype) {

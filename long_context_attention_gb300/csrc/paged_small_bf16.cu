@@ -24,14 +24,18 @@ DA_HD constexpr int small_keys(int d) { return d == 64 ? 256 : 128; }   // keys 
 constexpr int kSmallMaxCluster = 8;
 constexpr int kSmallMaxCtas = 3 * 152;   // one wave: 3 CTAs on each SM
 
-// CTAs per (sequence, key head), 0 where the call is not short enough: its
-// CTAs must all be resident at once.
+// CTAs per (sequence, key head), 0 where the call is not short enough.  One wave
+// of CTAs, or two where one or two CTAs hold a sequence.  Device time of this
+// kernel and of the three streaming ones, in us: 64 x 8 x 100 keys (512 CTAs of
+// one) 13.7 against 16.5, 64 x 12 x 250 (768 of one) 17.3 against 23.6, 8 x 12 x
+// 1000 (384 of four) 9.8 against 13.0; past the bound 8 x 12 x 2000 (768 of
+// eight) 18.0 against 16.0, 16 x 8 x 2000 (1024 of eight) 25.8 against 18.7.
 int small_cluster(int S, int Hq, int Hkv, int d, int max_len) {
   const int64_t pairs = (int64_t)S * Hkv;
   if (Hq / Hkv > 16 || max_len < 1 || max_len > kSmallMaxCluster * small_keys(d)) return 0;
   int c = 1;
   while (c * small_keys(d) < max_len) c *= 2;
-  if (pairs * c > kSmallMaxCtas) return 0;
+  if (pairs * c > (c <= 2 ? 2 : 1) * kSmallMaxCtas) return 0;
   // more CTAs shorten each one's copies and products, down to 32 keys
   while (c < kSmallMaxCluster && pairs * c * 2 <= kSmallMaxCtas && max_len > c * 32) c *= 2;
   return c;

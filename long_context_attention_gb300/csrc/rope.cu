@@ -133,10 +133,12 @@ template <typename E, bool ADJ>
 struct RopeUnit {
   static constexpr int N = RopeVec<E>::N;
   int va, vb;                 // element offsets of the two vectors
-  bool rot_a, rot_b;          // whether they rotate (half-split: both or none)
+  bool rot_a, rot_b;          // whether they rotate (half-split: both or none; adjacent: in part)
+  int pairs;
   float c[N], s[N];           // half-split: N pairs; adjacent: N / 2 of each vector
 
   __device__ __forceinline__ void place(int u, int n_pairs) {
+    pairs = n_pairs;
     if constexpr (ADJ) {
       va = 2 * u * N;
       vb = va + N;
@@ -156,11 +158,19 @@ struct RopeUnit {
     for (int i = 0; i < N; ++i) {
       c[i] = 1.f, s[i] = 0.f;
       if constexpr (ADJ) {
-        if (i < N / 2 ? rot_a : rot_b) angle(va / 2 + i, c[i], s[i]);
+        if (va / 2 + i < pairs) angle(va / 2 + i, c[i], s[i]);
       } else {
         if (rot_a) angle(va + i, c[i], s[i]);
       }
     }
+  }
+  // Pairs from n on of a piece as they were.
+  static __device__ __forceinline__ void keep(uint4 &a, const uint4 &was, int n) {
+    constexpr int W = N == 8 ? 1 : 2;   // 32-bit words of a pair
+    if (n <= 0) a.x = was.x;
+    if (n <= 1 / W) a.y = was.y;
+    if (n <= 2 / W) a.z = was.z;
+    if (n <= 3 / W) a.w = was.w;
   }
   __device__ __forceinline__ void apply(uint4 &a, uint4 &b) const {
     using V = RopeVec<E>;
@@ -169,6 +179,7 @@ struct RopeUnit {
     V::unpack(a, x);
     V::unpack(b, y);
     if constexpr (ADJ) {
+      const uint4 a0 = a, b0 = b;
       float ra[N], rb[N];
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) {
@@ -178,7 +189,11 @@ struct RopeUnit {
         rb[2 * i + 1] = fmaf(y[2 * i + 1], c[N / 2 + i], y[2 * i] * s[N / 2 + i]);
       }
       a = V::pack(ra);
-      if (rot_b) b = V::pack(rb);
+      b = V::pack(rb);
+      if (va / 2 + N > pairs) {   // pairs past the rotated part pass bit for bit
+        keep(a, a0, pairs - va / 2);
+        keep(b, b0, pairs - vb / 2);
+      }
     } else {
       float ra[N], rb[N];
 #pragma unroll
@@ -271,6 +286,76 @@ __global__ void __launch_bounds__(kRopeThreads)
   }
 }
 
+// The same for rows in 16-byte pieces whose rotated part is not made of whole
+// pieces (half-split pairs, n_pairs of any size: the partner of an element lies
+// anywhere in the row).  The lanes of a row exchange it through shared memory.
+// (One thread per pair with 2-byte accesses took 539 us for 2 x 48 x 51971 x 64
+// bf16 with 3 pairs, whose copies take 188.)
+template <typename E>
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_any_kernel(RopeTensor q, RopeTensor k, const __grid_constant__ RopeParams rp, int Hq, int Hk, int T,
+                    long long n_units, int d, int hpt) {
+  constexpr int N = RopeVec<E>::N, B = kRopeBatch;
+  __shared__ __align__(16) E s_rows[B][kRopeThreads * N];   // the block's rows, one after another
+  const long long i = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
+  const int units = d / N, n = rp.n_pairs;   // lanes of a row: 8 to 32, so a row is one warp's
+  const long long tok = min(i, n_units - 1) / units;
+  const bool live = i < n_units;
+  const int u = threadIdx.x % units, base = (threadIdx.x - u) * N;
+  const long long b = tok / T, t = tok - b * T;
+  // the turn of each element: x cos + partner sin (the sine negative for the first of a pair)
+  float c[N], s[N];
+  int other[N];
+  {
+    const RopePlace at(rp, b, t, 0);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const int x = u * N + e;
+      other[e] = -1;
+      if (x < 2 * n) {
+        const int j = x < n ? x : x - n;
+        rope_sincos(__ldg(rp.inv_freq + j), at.on(rp.pair_axis[j]), rp.sign, c[e], s[e]);
+        other[e] = base + (x < n ? x + n : x - n);
+        if (x < n) s[e] = -s[e];
+      }
+    }
+  }
+  const int h0 = blockIdx.y * hpt, h1 = min(h0 + hpt, Hq + Hk);
+  auto row = [&](int h, bool out) -> const E * {
+    const bool isq = h < Hq;
+    const RopeTensor &x = isq ? q : k;
+    const int hh = isq ? h : h - Hq;
+    return out ? static_cast<const E *>(x.out) + b * x.out_b + hh * x.out_h + t * x.out_t + u * N
+               : static_cast<const E *>(x.in) + b * x.in_b + hh * x.in_h + t * x.in_t + u * N;
+  };
+  for (int hb = h0; hb < h1; hb += B) {
+    uint4 v[B];
+#pragma unroll
+    for (int j = 0; j < B; ++j)
+      if (live && hb + j < h1) v[j] = ld_once(row(hb + j, false));
+#pragma unroll
+    for (int j = 0; j < B; ++j)
+      if (live && hb + j < h1) *reinterpret_cast<uint4 *>(&s_rows[j][threadIdx.x * N]) = v[j];
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+      if (!live || hb + j >= h1) continue;
+      if (u * N < 2 * n) {   // pieces past the rotated part pass bit for bit
+        float x[N];
+        RopeVec<E>::unpack(v[j], x);
+        alignas(16) E y[N];
+        *reinterpret_cast<uint4 *>(y) = v[j];
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (other[e] >= 0) from_f32(fmaf(x[e], c[e], to_f32(s_rows[j][other[e]]) * s[e]), y[e]);
+        v[j] = *reinterpret_cast<uint4 *>(y);
+      }
+      __stcs(reinterpret_cast<uint4 *>(const_cast<E *>(row(hb + j, true))), v[j]);
+    }
+    __syncwarp();
+  }
+}
+
 // Two elements of a row, of any alignment: pair j < n_pairs, or two elements
 // past the rotated part.
 template <typename E, typename F>
@@ -317,21 +402,26 @@ __global__ void __launch_bounds__(kRopeThreads)
 
 // Heads per thread: sin and cos are shared by the heads a thread visits, but a
 // short input needs the heads spread over threads to fill the GPU.
-static int heads_per_thread(long long n_units, int heads) {
+static int heads_per_thread(long long n_units, int heads, int most) {
   const long long threads = n_units * heads, want = 152ll * 1024;
   const long long h = threads / want;
-  return (int)(h < 1 ? 1 : h > 8 ? 8 : h);
+  return (int)(h < 1 ? 1 : h > most ? most : h);
 }
 
-cudaError_t launch_rope(const RopeTensor &q, const RopeTensor &k, const RopeParams &rp, bool adjacent, bool vec, int B,
-                        int Hq, int Hk, int T, int d, int dtype, cudaStream_t stream) {
+cudaError_t launch_rope(const RopeTensor &q, const RopeTensor &k, const RopeParams &rp, bool adjacent, RopePath path,
+                        int B, int Hq, int Hk, int T, int d, int dtype, cudaStream_t stream) {
   const int n = dtype == DA_BF16 ? 8 : 4;
-  const int units = vec ? d / (2 * n) : d / 2;
+  const int units = path == kRopeUnits ? d / (2 * n) : path == kRopeAny ? d / n : d / 2;
   const long long n_units = (long long)B * T * units;
-  const int hpt = heads_per_thread(n_units, Hq + Hk);
+  const int hpt = heads_per_thread(n_units, Hq + Hk, 8);
   const dim3 grid((unsigned)((n_units + kRopeThreads - 1) / kRopeThreads), (unsigned)((Hq + Hk + hpt - 1) / hpt));
 #define DA_ROPE_ARGS q, k, rp, Hq, Hk, T, n_units, units, hpt
-  if (!vec) {
+  if (path == kRopeAny) {
+    if (dtype == DA_BF16)
+      rope_any_kernel<__nv_bfloat16><<<grid, kRopeThreads, 0, stream>>>(q, k, rp, Hq, Hk, T, n_units, d, hpt);
+    else
+      rope_any_kernel<float><<<grid, kRopeThreads, 0, stream>>>(q, k, rp, Hq, Hk, T, n_units, d, hpt);
+  } else if (path == kRopeScalar) {
     if (dtype == DA_BF16)
       rope_scalar_kernel<__nv_bfloat16>
           <<<grid, kRopeThreads, 0, stream>>>(q, k, rp, adjacent, Hq, Hk, T, n_units, units, hpt);
@@ -355,17 +445,17 @@ cudaError_t launch_rope(const RopeTensor &q, const RopeTensor &k, const RopePara
 // ---------------------------------------------------------------------------
 // Append to the paged cache.
 //
-// A block takes a run of up to 128 tokens and up to kRopeBatch heads.  Every
+// A block takes a run of up to 128 tokens and up to kAppendHeads heads.  Every
 // thread first issues the loads of its first 16-byte pieces (they do not depend
 // on where the token goes); meanwhile the block's threads place all the tokens,
 // one each: the sequence by a binary search of cu_tokens (held in shared memory
 // with the lengths up to kAppendSearch sequences, so one global read serves
 // both), the pages from the tables.  Then it walks the run.  Placing takes three dependent
-// reads (~3 us): blocks of 16 tokens spent most of their time on it (26600
-// tokens, d = 128: 31 us against 17 of copies).  The demand goes out with
+// reads (~3 us), on which blocks of 16 tokens spent most of their time.  The demand goes out with
 // neighbouring threads on neighbouring tokens.
 // ---------------------------------------------------------------------------
 constexpr int kAppendSearch = 1024;
+constexpr int kAppendHeads = 16;   // that share a thread's sines and cosines (48 rows of 64: 228 us, 8 heads 259, 4 heads 323)
 
 struct TokenPlace {
   int pos;            // place in its sequence; -1: skip this token
@@ -427,18 +517,18 @@ __global__ void __launch_bounds__(kRopeThreads)
   };
   RopeUnit<E, ADJ> ru;
   uint4 va[kRopeBatch], vb[kRopeBatch];
-  auto load = [&](int tt) {
+  auto load = [&](int tt, int hb) {
 #pragma unroll
     for (int j = 0; j < kRopeBatch; ++j)
-      if (h0 + j < h1) {
-        const E *src = source(n0 + tt, h0 + j);
+      if (hb + j < h1) {
+        const E *src = source(n0 + tt, hb + j);
         va[j] = ld_once(src + ru.va);
         vb[j] = ld_once(src + ru.vb);
       }
   };
   if constexpr (VEC) {
     ru.place(u, h0 < h_turn ? rp.n_pairs : 0);
-    if (mine && tt0 < last) load(tt0);
+    if (mine && tt0 < last) load(tt0, h0);
   }
   const int32_t *cu = a.cu_tokens, *lens = c.seq_lens;
   if (c.S + 1 <= kAppendSearch) {
@@ -465,7 +555,7 @@ __global__ void __launch_bounds__(kRopeThreads)
   if (!mine) return;
   for (int tt = tt0; tt < last; tt += step) {
     if constexpr (VEC) {
-      if (tt > tt0) load(tt);
+      if (tt > tt0) load(tt, h0);
     }
     const TokenPlace p = s_place[tt];
     const long long n = n0 + tt;
@@ -482,14 +572,17 @@ __global__ void __launch_bounds__(kRopeThreads)
       };
       if constexpr (VEC) {
         if (h0 < h_turn) ru.turn(angle);
+        for (int hb = h0; hb < h1; hb += kRopeBatch) {
+          if (hb > h0) load(tt, hb);
 #pragma unroll
-        for (int j = 0; j < kRopeBatch; ++j)
-          if (h0 + j < h1) {
-            E *dst = target(h0 + j);
-            if (h0 + j < h_turn) ru.apply(va[j], vb[j]);
-            *reinterpret_cast<uint4 *>(dst + ru.va) = va[j];
-            *reinterpret_cast<uint4 *>(dst + ru.vb) = vb[j];
-          }
+          for (int j = 0; j < kRopeBatch; ++j)
+            if (hb + j < h1) {
+              E *dst = target(hb + j);
+              if (hb + j < h_turn) ru.apply(va[j], vb[j]);
+              *reinterpret_cast<uint4 *>(dst + ru.va) = va[j];
+              *reinterpret_cast<uint4 *>(dst + ru.vb) = vb[j];
+            }
+        }
       } else {
         float c1 = 1.f, s1 = 0.f;
         if (u < rp.n_pairs && h0 < h_turn) angle(u, c1, s1);
@@ -507,12 +600,12 @@ cudaError_t launch_append(const AppendArgs &args, const dilution_attn_paged_cach
   const int nv = c.dtype == DA_BF16 ? 8 : 4;
   a.units = vec ? c.d / (2 * nv) : c.d / 2;
   const int rows = (a.q != nullptr ? c.Hq : 0) + 2 * c.Hkv;
-  a.hpt = heads_per_thread((long long)a.N * a.units, rows);
-  if (a.hpt > kRopeBatch) a.hpt = kRopeBatch;
-  // a block's run: longer ones share the placing, as long as the blocks still
-  // fill the GPU (about 7 on each SM)
+  a.hpt = heads_per_thread((long long)a.N * a.units, rows, kAppendHeads);
+  // a block's run: longer ones share the placing, as long as there are 10 blocks
+  // for each SM, more than are resident (27100 tokens of 4 heads, d = 128: 27 us
+  // with 10, 33 with 7, 44 with 4, 29 with 20)
   const int step = kRopeThreads / a.units, heads = (rows + a.hpt - 1) / a.hpt + 1;
-  int64_t turns = ((int64_t)a.N + step - 1) / step * heads / (7 * 152);
+  int64_t turns = ((int64_t)a.N + step - 1) / step * heads / (10 * 152);
   if (turns > kRopeThreads / step) turns = kRopeThreads / step;
   a.tokens = step * (int)(turns < 1 ? 1 : turns);
   const dim3 grid((unsigned)((a.N + a.tokens - 1) / a.tokens), (unsigned)heads);

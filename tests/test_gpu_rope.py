@@ -55,6 +55,9 @@ def positions(axes, B, T, seed=0, span=4096):
     (2, 2, 1, 65, 128, 11, 4, False, False),        # odd number of pairs: no whole 16-byte pieces
     (1, 5, 0, 40, 64, 7, 2, True, False),           # queries only
     (1, 2, 2, 9, 64, 0, 1, False, False),           # nothing rotates: a copy
+    (3, 5, 2, 301, 128, 63, 2, False, True),        # all but two elements, rows of odd halves
+    (2, 3, 1, 77, 64, 1, 1, False, False),          # one pair
+    (2, 3, 1, 77, 128, 61, 3, True, False),         # adjacent, cut inside a 16-byte piece
 ])
 def test_rope_matches_oracle_both_ways(dtype, B, Hq, Hk, T, d, n, axes, adjacent, interleaved):
     t = TYPES[dtype]
@@ -193,6 +196,7 @@ def append_oracle(cache, k, v, cu, spec_pa, pos, demand, adjacent):
     (2, [33, 90], [33, 20], 2, 2, 64, 16, 16, 2, True, True, True, True, 0),
     (2, [33, 90], [33, 20], 2, 1, 64, 64, 9, 1, False, False, True, True, 1),     # unaligned rows, odd pairs
     (1, [300], [300], 8, 1, 128, 256, 0, 1, False, False, False, True, 0),        # no rotation
+    (2, [33, 90], [33, 20], 2, 1, 64, 64, 9, 1, True, False, True, True, 0),      # adjacent, cut inside a piece
     (5, [1, 2, 3, 0, 4], [1, 0, 2, 0, 4], 1, 1, 64, 16, 32, 1, True, False, False, False, 2),
 ])
 def test_append_matches_oracle(dtype, S, lens, counts, Hq, Hkv, d, page, n, axes, adjacent, pos, dem, withq, pad):
