@@ -349,6 +349,8 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // columns (2t, 2t + 1 of both halves) are keys 4t .. 4t + 3.
 __device__ __forceinline__ int group_key(int c, int half) { return 4 * (c >> 1) + 2 * half + (c & 1); }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Launch that may begin before its predecessor in the stream has finished: as
 // soon as the predecessor's CTAs have called pdl_launch_dependents.  Kernels of
 // one decode step, in launch order:

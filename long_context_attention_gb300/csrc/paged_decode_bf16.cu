@@ -242,8 +242,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
   const int sub = warp % V::kStepsPerTile * V::kStep;    // the warp's keys inside a tile
   // lane -> row: matrices (k half 0, n 0-7), (k half 1, n 0-7), (k half 0, n 8-15), (k half 1, n 8-15)
   const int vrow = sub + group_key(lane & 7, (lane >> 3) & 1);
-  pdl_wait();
-  pdl_launch_dependents();
+  bool waited = false;
   PgtSeg g;
   for (g.start(p, w, line, L, from, to); g.n > 0; g.next(p, w, line, L)) {
     const int n = g.n;
@@ -297,6 +296,16 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
     for (int a = 0; a < AHEAD; ++a)
 #pragma unroll
       for (int hh = 0; hh < HH; ++hh) pages[a][hh] = demand_page(a, hh);
+    if (!waited) {   // the demand does not depend on the first pass: to L2 meanwhile
+#pragma unroll
+      for (int a = 0; a < AHEAD - 1; ++a)
+#pragma unroll
+        for (int hh = 0; hh < HH; ++hh)
+          if ((unsigned)pages[a][hh] < (unsigned)p.c.num_demand_pages) prefetch_l2(demand_at(a, hh, pages[a][hh]));
+      pdl_wait();
+      pdl_launch_dependents();
+      waited = true;
+    }
 #pragma unroll
     for (int a = 0; a < AHEAD - 1; ++a) bring(a, pages[a]);
     // lse2 of the rows: 8 lanes join a row's pieces
@@ -456,6 +465,10 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
       part[tid * acc_stride(D) + D] = a;
     }
     named_bar_sync(1, WARPS * 32);
+  }
+  if (!waited) {
+    pdl_wait();
+    pdl_launch_dependents();
   }
 }
 

@@ -193,8 +193,7 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
     const int c = lane * NC * 4 / 16;   // its 16-byte piece
     col[j] = (uint32_t)((c >> 3) * TILE * 128 + (((c & 7) ^ j) << 4) + (NC == 2 ? (lane & 1) * 8 : 0));
   }
-  pdl_wait();
-  pdl_launch_dependents();
+  bool waited = false;
   PgtSeg g;
   for (g.start(p, w, line, L, from, to); g.n > 0; g.next(p, w, line, L)) {
     const int tile0 = (warp / T::kPerTile + T::kStride - g.run % T::kStride) % T::kStride;
@@ -242,6 +241,15 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
     for (int a = 0; a < 2; ++a)
 #pragma unroll
       for (int i = 0; i < PIECES; ++i) pages[a][i] = demand_page(a, i);
+    if (!waited) {   // the demand does not depend on the first pass: to L2 meanwhile
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i)
+        if ((unsigned)pages[0][i] < (unsigned)p.c.num_demand_pages)
+          prefetch_l2(dpool[i] + (((size_t)pages[0][i] * p.c.Hq) << sh) + ((step0 + pk) & (ps - 1)));
+      pdl_wait();
+      pdl_launch_dependents();
+      waited = true;
+    }
     bring(0, pages[0]);
     // lse2 of the rows: 8 lanes join a row's pieces
     for (int r4 = warp * 4; r4 < g.nrows; r4 += kPgfWarps * 4) {
@@ -379,6 +387,10 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
       part[tid * acc_stride(D) + D] = a;
     }
     named_bar_sync(1, 32 * kPgfWarps);
+  }
+  if (!waited) {
+    pdl_wait();
+    pdl_launch_dependents();
   }
 }
 
