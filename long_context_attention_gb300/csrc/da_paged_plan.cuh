@@ -36,8 +36,9 @@ constexpr int kPgxKeyCtas = 304;  // pgx_keys: two
 // Beginning and ending a piece there costs about as much as this many tiles (8 us
 // of normalisers, queries and first copies, 3 us of sums; a tile 2.5 us; pgx_keys
 // 3 us and 1 us): a segment takes as many units before its first tile, so that a
-// CTA with two pieces gets fewer tiles.
-constexpr int kPgxHead = 4;
+// CTA with two pieces gets fewer tiles (a step with 32 x 16 heads x 32768: 71.1
+// us, 72.3 with 4, 74.3 with 3).
+constexpr int kPgxHead = 6;
 
 // Equal cut of `total` units into stretches of base or base + 1.
 struct PgtCut {
