@@ -332,8 +332,8 @@ int dilution_attn_rope_bwd(const void *dq_out, const int64_t *dq_out_strides, co
  * page_table[s][t / page_size], its demand in that row of page
  * demand_table[s][t / page_size].  Sequences that share a prefix may name the
  * same key/value pages; the demand differs between them, so a demand page
- * belongs to one sequence (two sequences naming one demand page, or appending
- * to one key/value page, race with each other).  Query head h reads key head
+ * belongs to one place of one table row (two places naming one demand page, or
+ * two sequences appending to one key/value page, race with each other).  Query head h reads key head
  * h / (Hq / Hkv).  Rows past a sequence's length are never used, whatever
  * they hold, nor are table entries past its last page.
  *
@@ -347,8 +347,12 @@ int dilution_attn_rope_bwd(const void *dq_out, const int64_t *dq_out_strides, co
  *
  * Unlike the calls above, the paged calls leave the status word alone unless
  * they record an error: the caller zeroes the first 256 bytes of a workspace
- * once before its first use, and dilution_attn_get_error reads and clears
- * the first error recorded since.
+ * once before its first use (and again after DA_ERR_TIMEOUT), and
+ * dilution_attn_get_error reads and clears the first error recorded since.  A
+ * decode step overwrites the rest of its workspace: calls that may overlap on
+ * the GPU need workspaces of their own.  At most 2^14 heads, 2^31 - 1 pages x
+ * key heads and 2^32 - 1 runs of 16 rows in the demand pool
+ * (DA_ERR_UNSUPPORTED beyond).
  * ---------------------------------------------------------------------- */
 typedef struct dilution_attn_paged_cache {
   void *k_pages, *v_pages;               /* DEVICE, dtype */
@@ -397,7 +401,9 @@ int dilution_attn_paged_append(const void *q, const int64_t *q_strides, const vo
  * prefix's pages in every page_table row.
  *
  * max_len: host upper bound of seq_lens (at most max_pages * page_size); sizes
- * the workspace and the launch.  tau_bh: nullable device [S*Hq], index
+ * the workspace and the launch, and short bf16 calls (max_len up to 2048 at
+ * d = 64, 1024 at d = 128, few sequences) run as one kernel.  The workspace's
+ * size depends on whether there is a prefix, not on its length.  tau_bh: nullable device [S*Hq], index
  * s*Hq + h.  tau, eps, flags (DA_FLAG_EARLIER_DEMAND_ONLY) as for
  * dilution_attn_decode_step_ex; DA_BF16 needs eps >= 1e-18 as the forward.
  * Repeated calls give equal bits.  Errors as for dilution_attn_decode_step_ex. */

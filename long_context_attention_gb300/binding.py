@@ -425,13 +425,14 @@ class _CRopeSpec(ctypes.Structure):
 class RopeSpec:
     """What ``rope_spec`` returns: the C struct, the frequencies it points to and its sizes."""
 
-    __slots__ = ("inv_freq", "n_pairs", "n_axes", "adjacent", "_c", "_ref")
+    __slots__ = ("inv_freq", "n_pairs", "n_axes", "adjacent", "_c", "_ref", "_dev")
 
     def __init__(self, inv_freq, pair_axis, n_axes, adjacent):
         self.inv_freq, self.n_pairs, self.n_axes, self.adjacent = inv_freq, len(pair_axis), n_axes, adjacent
         self._c = _CRopeSpec(inv_freq.data_ptr(), self.n_pairs, n_axes, int(adjacent),
                              (ctypes.c_uint8 * DA_MAX_ROPE_PAIRS)(*pair_axis))
         self._ref = ctypes.byref(self._c)
+        self._dev = inv_freq.get_device()
 
 
 def rope_spec(inv_freq, pair_axis=None, n_axes: int = 1, adjacent: bool = False) -> RopeSpec:
@@ -495,11 +496,42 @@ def _c_strides(st, n):
 
 
 def _current_device() -> int:
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
+    return _get_device() if torch.cuda.is_initialized() else torch.cuda.current_device()
+
+
+# absent in a torch without CUDA, where every call fails its tensor checks before
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream_id(stream, dev) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _need_bytes(workspace, dev):
+    if not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and workspace.get_device() == dev
+            and workspace.is_contiguous()):
+        _need(workspace, "workspace", None, torch.uint8)
+
+
+def _need_table(table, dev):
+    if not (isinstance(table, torch.Tensor) and table.dtype is torch.int32 and table.get_device() == dev
+            and table.dim() == 1 and table.is_contiguous()):
+        _need(table, "prefix_table", None, torch.int32)
+        raise ValueError("prefix_table must be one-dimensional")
+
+
+def _new(shape, dtype, device, stream, zero_head=0):
+    """A tensor for a call on ``stream`` (None: the current one), allocated, and
+    its first bytes zeroed, on that stream: its memory is then not handed on
+    before the call has used it."""
+    if stream is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        if zero_head:
+            t[:zero_head].zero_()
+        return t
+    with torch.cuda.stream(stream):
+        return _new(shape, dtype, device, None, zero_head)
 
 
 _CODES = {torch.float32: DA_F32, torch.bfloat16: DA_BF16}
@@ -507,7 +539,7 @@ _CODES = {torch.float32: DA_F32, torch.bfloat16: DA_BF16}
 
 def _rope_call(name, q, k, positions, rope, q_out, k_out, stream, check):
     lib = _lib or load()
-    if not isinstance(rope, RopeSpec):
+    if type(rope) is not RopeSpec:
         raise TypeError("rope must be a RopeSpec (see rope_spec)")
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a [B, H, T, d] tensor")
@@ -517,7 +549,7 @@ def _rope_call(name, q, k, positions, rope, q_out, k_out, stream, check):
     dev = _current_device()
     sq = _c_strides(_fit_rows(q, "q", shape, dtype, dev), 3)
     if q_out is None:
-        q_out = torch.empty(shape, dtype=dtype, device=q.device)
+        q_out = _new(shape, dtype, q.device, stream)
         so = None
     else:
         so = _c_strides(_fit_rows(q_out, "q_out", shape, dtype, dev), 3)
@@ -526,7 +558,7 @@ def _rope_call(name, q, k, positions, rope, q_out, k_out, stream, check):
         kshape = (B, Hk, T, d)
         sk, kp = _c_strides(_fit_rows(k, "k", kshape, dtype, dev), 3), k.data_ptr()
         if k_out is None:
-            k_out = torch.empty(kshape, dtype=dtype, device=q.device)
+            k_out = _new(kshape, dtype, q.device, stream)
             sko = None
         else:
             sko = _c_strides(_fit_rows(k_out, "k_out", kshape, dtype, dev), 3)
@@ -535,12 +567,15 @@ def _rope_call(name, q, k, positions, rope, q_out, k_out, stream, check):
         raise ValueError("k_out without k")
     else:
         Hk, sk, kp, sko, kop = 0, None, None, None, None
-    _fit(positions, "positions", positions.shape if isinstance(positions, torch.Tensor) else (), torch.int32, dev)
+    if not (isinstance(positions, torch.Tensor) and positions.dtype is torch.int32 and positions.get_device() == dev
+            and positions.is_contiguous()):
+        _need(positions, "positions", None, torch.int32)
     ps = positions.shape
     pb = 1 if len(ps) == 2 else ps[1] if len(ps) == 3 else -1
     if pb not in (1, B) or ps[0] != rope.n_axes or ps[-1] != T:
         raise ValueError(f"positions has shape {tuple(ps)}, expected ({rope.n_axes}, [1 or {B},] {T})")
-    _fit(rope.inv_freq, "inv_freq", (rope.n_pairs,), torch.float32, dev)
+    if rope._dev != dev:
+        _need(rope.inv_freq, "inv_freq")
     st = getattr(lib, name)(q.data_ptr(), sq, kp, sk, q_out.data_ptr(), so, kop, sko, positions.data_ptr(), pb,
                             rope._ref, B, Hq, Hk, T, d, dt, _stream_id(stream, dev))
     if check and st != DA_OK:
@@ -577,7 +612,7 @@ class PagedCache:
     update in place between calls."""
 
     __slots__ = ("k_pages", "v_pages", "demand_pages", "page_table", "demand_table", "seq_lens", "S", "Hq", "Hkv", "d",
-                 "page_size", "max_pages", "dtype", "device", "_code", "_c", "_ref")
+                 "page_size", "max_pages", "dtype", "device", "_code", "_c", "_ref", "_dev", "_q_shape", "_cu_shape")
 
     def __init__(self, k_pages, v_pages, demand_pages, page_table, demand_table, seq_lens):
         _need(k_pages, "k_pages")
@@ -606,14 +641,15 @@ class PagedCache:
                                                         seq_lens)), S, Hq, Hkv, d, page_size, num_pages,
                                num_demand_pages, max_pages, self._code)
         self._ref = ctypes.byref(self._c)
+        self._dev, self._q_shape, self._cu_shape = k_pages.get_device(), torch.Size((S, Hq, d)), torch.Size((S + 1,))
 
 
 def _need_cache(cache) -> int:
     """The cache's device, which has to be the current one."""
-    if not isinstance(cache, PagedCache):
+    if type(cache) is not PagedCache:
         raise TypeError("cache must be a PagedCache")
     dev = _current_device()
-    if cache.device.index != dev:
+    if cache._dev != dev:
         raise ValueError(f"the cache is on {cache.device} but the current device is cuda:{dev}; "
                          f"call inside torch.cuda.device({cache.device})")
     return dev
@@ -646,22 +682,23 @@ def dilution_attn_paged_append(q, k, v, cache, cu_tokens, q_out=None, *, rope=No
     kvshape = (N, Hkv, d)
     sk = _c_strides(_fit_rows(k, "k", kvshape, dtype, dev), 2)
     sv = _c_strides(_fit_rows(v, "v", kvshape, dtype, dev), 2)
-    _fit(cu_tokens, "cu_tokens", (cache.S + 1,), torch.int32, dev)
+    _fit(cu_tokens, "cu_tokens", cache._cu_shape, torch.int32, dev)
     qp = sq = qop = dp = sd = None
     if q is not None:
         qshape = (N, Hq, d)
         sq, qp = _c_strides(_fit_rows(q, "q", qshape, dtype, dev), 2), q.data_ptr()
         if q_out is None:
-            q_out = torch.empty(qshape, dtype=dtype, device=cache.device)
+            q_out = _new(qshape, dtype, cache.device, stream)
         else:
             _fit(q_out, "q_out", qshape, dtype, dev)
         qop = q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     if rope is not None:
-        if not isinstance(rope, RopeSpec):
+        if type(rope) is not RopeSpec:
             raise TypeError("rope must be a RopeSpec (see rope_spec)")
-        _fit(rope.inv_freq, "inv_freq", (rope.n_pairs,), torch.float32, dev)
+        if rope._dev != dev:
+            _need(rope.inv_freq, "inv_freq")
     if positions is not None:
         _fit(positions, "positions", (1 if rope is None else rope.n_axes, N), torch.int32, dev)
     if demand is not None:
@@ -670,8 +707,9 @@ def dilution_attn_paged_append(q, k, v, cache, cu_tokens, q_out=None, *, rope=No
             _need_any_strides(demand, "demand", (N, Hq), torch.float32)
         dp, sd = demand.data_ptr(), _c_strides(demand.stride(), 2)
     if workspace is None:
-        workspace = dilution_attn_paged_append_workspace(cache)
-    _fit(workspace, "workspace", workspace.shape if isinstance(workspace, torch.Tensor) else (), torch.uint8, dev)
+        workspace = _new(dilution_attn_paged_append_workspace_size(), torch.uint8, cache.device, stream, 256)
+    else:
+        _need_bytes(workspace, dev)
     st = lib.dilution_attn_paged_append(qp, sq, k.data_ptr(), sk, v.data_ptr(), sv, dp, sd, qop, cu_tokens.data_ptr(), N,
                                         cache._ref, None if rope is None else rope._ref,
                                         None if positions is None else positions.data_ptr(), workspace.data_ptr(),
@@ -710,23 +748,27 @@ def dilution_attn_paged_decode(q, cache, max_len: int, out=None, *, prefix_table
     device: read them with dilution_attn_get_error on ``workspace``."""
     lib = _lib or load()
     dev = _need_cache(cache)
-    shape, dtype = (cache.S, cache.Hq, cache.d), cache.dtype
+    shape, dtype = cache._q_shape, cache.dtype
     _fit(q, "q", shape, dtype, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=cache.device)
+        out = torch.empty(shape, dtype=dtype, device=cache.device) if stream is None else \
+            _new(shape, dtype, cache.device, stream)
     else:
         _fit(out, "out", shape, dtype, dev)
     n_prefix, pt = 0, None
     if prefix_table is not None:
-        n_prefix = prefix_table.numel() if isinstance(prefix_table, torch.Tensor) else 0
-        _fit(prefix_table, "prefix_table", (n_prefix,), torch.int32, dev)
-        pt = prefix_table.data_ptr()
+        _need_table(prefix_table, dev)
+        n_prefix, pt = prefix_table.numel(), prefix_table.data_ptr()
     if workspace is None:
-        workspace = dilution_attn_paged_decode_workspace(cache, max_len, n_prefix)
-    _fit(workspace, "workspace", workspace.shape if isinstance(workspace, torch.Tensor) else (), torch.uint8, dev)
-    st = lib.dilution_attn_paged_decode(q.data_ptr(), cache._ref, pt, n_prefix, int(max_len), out.data_ptr(),
-                                        float(tau), _tau_bh_ptr(tau_bh, cache.S, cache.Hq), float(eps), int(flags),
-                                        workspace.data_ptr(), workspace.numel(), _stream_id(stream, dev))
+        need = dilution_attn_paged_decode_workspace_size(cache.S, cache.Hq, cache.Hkv, cache.d, int(max_len), n_prefix,
+                                                         cache.page_size, cache._code)
+        workspace = _new(max(need, 256), torch.uint8, cache.device, stream, 256)
+    else:
+        _need_bytes(workspace, dev)
+    st = lib.dilution_attn_paged_decode(q.data_ptr(), cache._ref, pt, n_prefix, int(max_len), out.data_ptr(), float(tau),
+                                        None if tau_bh is None else _tau_bh_ptr(tau_bh, cache.S, cache.Hq), float(eps),
+                                        int(flags), workspace.data_ptr(), workspace.numel(),
+                                        _raw_stream(dev) if stream is None else stream.cuda_stream)
     if check and st != DA_OK:
         _check(st, "dilution_attn_paged_decode")
     return out

@@ -15,7 +15,7 @@ using namespace da;
 
 namespace {
 
-constexpr int kMaxHeads = 1 << 15;
+constexpr int kMaxHeads = 1 << 14;   // a launch grid's second dimension counts rows of q, k and v
 constexpr int kMaxTokens = 1 << 30;
 
 int elem_bytes(int dtype) { return dtype == DA_BF16 ? 2 : 4; }

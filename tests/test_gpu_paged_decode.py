@@ -251,6 +251,25 @@ def test_two_streams_with_their_own_workspaces(max_len):
         check_step(c, q, old, o, r)
 
 
+@pytest.mark.parametrize("max_len", [300, LONG])
+def test_call_on_another_stream_without_buffers(max_len):
+    # out and workspace are the call's own: allocated and zeroed on its stream, not the busy current one
+    cache, q, _ = make_cache(3, [300, 7, 130], 4, 2, 64, 32, "bf16", seed=66)
+    ref = oracle_step(cache, q)
+    before = cache.demand_pages.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy = torch.zeros(1 << 28, device=DEV)
+    for _ in range(20):
+        busy.add_(1.0)                                   # the current stream is behind
+    out = b.dilution_attn_paged_decode(q, cache, max_len, stream=side)
+    junk = [torch.full((1 << 20,), 7.0, device=DEV) for _ in range(8)]   # memory handed out meanwhile
+    side.synchronize()
+    check_step(cache, q, before, out, ref)
+    torch.cuda.synchronize()
+    assert len(junk) == 8
+
+
 def test_pool_past_32_bit_offsets():
     # pools of more than 2^32 bytes and 2^31 elements: the sequence's pages lie at the end
     page, d, Hkv = 256, 128, 4
