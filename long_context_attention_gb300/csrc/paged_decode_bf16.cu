@@ -566,8 +566,13 @@ static int launch_pgt_t(const PagedDecode &p, const PgtPlan &w, cudaStream_t str
   if (!make_page_map(&km, p.c.k_pages, num > 0 ? num : 1, p.c.page_size, pgt_tile(D), D, DA_BF16) ||
       !make_page_map(&vm, p.c.v_pages, num > 0 ? num : 1, p.c.page_size, pgt_tile(D), D, DA_BF16))
     return DA_ERR_CUDA;
-  constexpr int k_stages = (kPgtSmemPerCta - 1024) / kStageBytes;
-  static_assert(k_stages <= 8, "the ring's barriers");
+  // Stages of pgt_keys: 4 leave room for the next kernel's CTAs to begin beside
+  // the last of this one (8 x 12 x 131072: 510 us a step, 518 with 6); with a
+  // prefix its CTAs are few and short, and 6 measured 19.2 against 20.6 us (16 x
+  // 12 x 2048 + 300).
+  const int k_stages = p.prefix_len == 0 ? 4 : 6;
+  constexpr int k_most = 1024 + 6 * kStageBytes;
+  static_assert(k_most <= kPgtSmemPerCta, "two CTAs an SM");
   pgt_keys<D, HH><<<w.ctas, pgt_threads(D), 1024 + k_stages * kStageBytes, stream>>>(p, w, km, k_stages);
   if (w.wide) {
     const int st = launch_pgx_keys(p, w, stream);
