@@ -350,9 +350,9 @@ int dilution_attn_rope_bwd(const void *dq_out, const int64_t *dq_out_strides, co
  * once before its first use (and again after DA_ERR_TIMEOUT), and
  * dilution_attn_get_error reads and clears the first error recorded since.  A
  * decode step overwrites the rest of its workspace: calls that may overlap on
- * the GPU need workspaces of their own.  At most 2^14 heads, 2^31 - 1 pages x
- * key heads and 2^32 - 1 runs of 16 rows in the demand pool
- * (DA_ERR_UNSUPPORTED beyond).
+ * the GPU need workspaces of their own.  At most 2^14 heads and 2^24 sequences x
+ * query heads, and for a decode step 2^31 - 1 pages x key heads and 2^32 - 1 runs
+ * of 16 rows in the demand pool (DA_ERR_UNSUPPORTED beyond).
  * ---------------------------------------------------------------------- */
 typedef struct dilution_attn_paged_cache {
   void *k_pages, *v_pages;               /* DEVICE, dtype */
@@ -374,7 +374,8 @@ typedef struct dilution_attn_paged_cache {
  * q [N,Hq,d], k, v [N,Hkv,d]: *_strides are HOST arrays of two element strides
  * (token, head) or NULL for contiguous; demand fp32 [N,Hq] likewise.
  * cu_tokens: DEVICE [S+1] int32, starting at 0 and not decreasing; tokens from
- * cu_tokens[S] on are padding, neither read nor written.
+ * cu_tokens[S] on are padding: their values are not used, their rows of q_out
+ * not written.  q_out may be q itself (then contiguous).
  * spec: NULL appends k and q unrotated.  positions: DEVICE [n_axes][N], or NULL
  * for the token's place in its sequence on every axis.
  * workspace: 256 bytes (dilution_attn_paged_append_workspace_size()). */

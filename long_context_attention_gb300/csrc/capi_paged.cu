@@ -256,7 +256,6 @@ int dilution_attn_paged_decode(const void *q, const dilution_attn_paged_cache *c
   p.out = out;
   p.prefix_table = n_prefix_pages > 0 ? prefix_table : nullptr;
   p.prefix_len = prefix_len;
-  p.prefix_pages = n_prefix_pages;
   p.max_len = max_len;
   const double per_tau = 1.4426950408889634 / std::sqrt((double)c.d);
   p.hs = HeadScale{tau_bh, (float)((double)tau * per_tau), per_tau};

@@ -13,7 +13,6 @@ struct PagedDecode {
   void *out;
   const int32_t *prefix_table;   // null without a prefix
   int prefix_len;                // tokens of the shared prefix, a multiple of page_size
-  int prefix_pages;
   int max_len;                   // host bound of seq_lens
   HeadScale hs;
   float eps;
@@ -33,15 +32,6 @@ __device__ __forceinline__ int paged_len(const PagedDecode &p, int s, int *statu
     return 0;
   }
   return len;
-}
-// Page id from a table, -1 (recorded) where it is outside the pool.
-__device__ __forceinline__ int checked_page(const int32_t *entry, int num_pages, int *status) {
-  const int pg = __ldg(entry);
-  if (pg < 0 || pg >= num_pages) {
-    atomicCAS(status, DA_OK, DA_ERR_INVALID);
-    return -1;
-  }
-  return pg;
 }
 #endif
 

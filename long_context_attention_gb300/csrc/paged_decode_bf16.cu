@@ -1,7 +1,9 @@
 // Decode step over the paged cache in bf16: streaming tensor-core kernels.
 //
-// Mathematics: as paged_decode.cu.  Two passes over the keys, joined by the
-// softmax normaliser that a share needs:
+// Mathematics, for one query head against the keys of its sequence: p = softmax(x),
+// share = p / (D + p + eps) of each key's demand total D (D + eps with the earlier
+// demand only), out = sum share v / sum share, D += p.  Two passes over the keys,
+// joined by the softmax normaliser that a share needs:
 //   pgt_keys    x = q . k (tau / sqrt(d) log2 e) of every key into a scratch of
 //               4 bytes per (row, key), and each piece's (max, sum 2^(x - max));
 //   pgt_values  lse2 from the pieces, p = 2^(x - lse2), share = p / (D + p +

@@ -1,6 +1,6 @@
 // Decode step over a shared prefix with many query rows: tcgen05 kernels.
 //
-// Mathematics: as paged_decode.cu, for the part of every sequence that lies in
+// Mathematics: as paged_decode_bf16.cu, for the part of every sequence that lies in
 // the shared prefix.  A segment is 64 rows (sequence, query head) of one key
 // head; the prefix's keys and values are read once per pass for all of them.
 //   pgx_keys    (max, sum 2^(x - max)) of every row over the CTA's key tiles;

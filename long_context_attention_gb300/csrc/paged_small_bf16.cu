@@ -1,6 +1,6 @@
 // Decode step over short paged caches in bf16: one launch.
 //
-// Mathematics: as paged_decode.cu.  A short step is bound by latency, not by
+// Mathematics: as paged_decode_bf16.cu.  A short step is bound by latency, not by
 // bytes: three kernels that follow one another cost 12 us on the device and 10
 // us of launches for 1 x 12 x 500 keys (0.2 us of copies).  Here a cluster of up
 // to 8 CTAs takes one (sequence, key head): every CTA holds its share of the

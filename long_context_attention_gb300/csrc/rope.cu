@@ -9,10 +9,10 @@
 // the 24-bit mantissa of inv_freq_j times the first 64 bits of 1 / (2 pi),
 // shifted by the exponent, within one unit.  n * F mod 2^64 is then the angle to
 // n 2^-64 turns, of which the upper 32 bits (2^-33 turns, 7e-10 radians, below
-// fp32's rounding of the cosine) go to sine and cosine, formed from their series.  No fp64 (GB300 has few
-// fp64 units), no long fp32 products; 32-bit multiplies and funnel shifts (a
-// version in 64-bit operations cost 140 instructions a pair and bounded the
-// append).  The products x cos - y sin run in fp32 and round once to the output's
+// fp32's rounding of the cosine) go to sine and cosine, formed from their series.
+// No fp64 (GB300 has few fp64 units), no long fp32 products; 32-bit multiplies and
+// funnel shifts (a version in 64-bit operations cost 140 instructions a pair and
+// bounded the append).  The products x cos - y sin run in fp32 and round once to the output's
 // type.
 //
 // What bounds it: bytes.  Each element is read once and written once; sin and
@@ -239,7 +239,8 @@ __device__ __forceinline__ uint4 ld_once(const void *p) {
 // grid.x: (token, unit) pairs, grid.y: groups of hpt heads of q followed by k.
 template <typename E, bool ADJ>
 __global__ void __launch_bounds__(kRopeThreads)
-    rope_kernel(RopeTensor q, RopeTensor k, const __grid_constant__ RopeParams rp, int Hq, int Hk, int T, long long n_units, int units, int hpt) {
+    rope_kernel(RopeTensor q, RopeTensor k, const __grid_constant__ RopeParams rp, int Hq, int Hk, int T,
+                long long n_units, int units, int hpt) {
   const long long i = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
   if (i >= n_units) return;
   const long long tok = i / units;
@@ -379,8 +380,8 @@ __device__ __forceinline__ void rope_pair(const E *src, E *dst, int j, int n_pai
 // Any alignment: one thread per pair of elements (d / 2 of them a row).
 template <typename E>
 __global__ void __launch_bounds__(kRopeThreads)
-    rope_scalar_kernel(RopeTensor q, RopeTensor k, const __grid_constant__ RopeParams rp, int adjacent, int Hq, int Hk, int T,
-                       long long n_units, int units, int hpt) {
+    rope_scalar_kernel(RopeTensor q, RopeTensor k, const __grid_constant__ RopeParams rp, int adjacent, int Hq,
+                       int Hk, int T, long long n_units, int units, int hpt) {
   const long long i = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
   if (i >= n_units) return;
   const long long tok = i / units;
@@ -413,7 +414,8 @@ cudaError_t launch_rope(const RopeTensor &q, const RopeTensor &k, const RopePara
   const int n = dtype == DA_BF16 ? 8 : 4;
   const int units = path == kRopeUnits ? d / (2 * n) : path == kRopeAny ? d / n : d / 2;
   const long long n_units = (long long)B * T * units;
-  const int hpt = heads_per_thread(n_units, Hq + Hk, 16);   // (2 x 32 heads x 51971 x 128 bf16: 272 us, 8 heads 296, 24 heads 276)
+  // 2 x 32 heads x 51971 x 128 bf16: 272 us with 16 heads at most, 296 with 8, 276 with 24
+  const int hpt = heads_per_thread(n_units, Hq + Hk, 16);
   const dim3 grid((unsigned)((n_units + kRopeThreads - 1) / kRopeThreads), (unsigned)((Hq + Hk + hpt - 1) / hpt));
 #define DA_ROPE_ARGS q, k, rp, Hq, Hk, T, n_units, units, hpt
   if (path == kRopeAny) {
@@ -450,12 +452,13 @@ cudaError_t launch_rope(const RopeTensor &q, const RopeTensor &k, const RopePara
 // on where the token goes); meanwhile the block's threads place all the tokens,
 // one each: the sequence by a binary search of cu_tokens (held in shared memory
 // with the lengths up to kAppendSearch sequences, so one global read serves
-// both), the pages from the tables.  Then it walks the run.  Placing takes three dependent
-// reads (~3 us), on which blocks of 16 tokens spent most of their time.  The demand goes out with
-// neighbouring threads on neighbouring tokens.
+// both), the pages from the tables.  Then it walks the run.  Placing takes three
+// dependent reads (~3 us), on which blocks of 16 tokens spent most of their time.
+// The demand goes out with neighbouring threads on neighbouring tokens.
 // ---------------------------------------------------------------------------
 constexpr int kAppendSearch = 1024;
-constexpr int kAppendHeads = 16;   // that share a thread's sines and cosines (48 rows of 64: 228 us, 8 heads 259, 4 heads 323)
+// Heads that share a thread's sines and cosines (48 rows of 64: 228 us, 8 heads 259, 4 heads 323).
+constexpr int kAppendHeads = 16;
 
 struct TokenPlace {
   int pos;            // place in its sequence; -1: skip this token

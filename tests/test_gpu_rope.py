@@ -260,6 +260,18 @@ def test_append_long_runs_of_tokens():
     assert torch.equal(cache.demand_pages[dpg, :, at % 64], demand[:N - 3])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [32, 11])     # 11: pairs that no 16-byte pieces hold
+def test_append_turns_queries_in_place(dtype, n):
+    cache, _, _ = make_cache(3, [9, 40, 70], 4, 2, 64, 16, dtype, seed=17)
+    spec, inv, pa = spec_of(n, 1, False)
+    rows = torch.randn(3, 8, 64, generator=torch.Generator().manual_seed(18)).to(TYPES[dtype]).to(DEV)
+    q = rows[:, :4].contiguous()
+    cu = torch.arange(4, dtype=torch.int32, device=DEV)
+    assert b.dilution_attn_paged_append(q, rows[:, 4:6], rows[:, 6:], cache, cu, q, rope=spec) is q
+    close(q, rows[:, :4], op.rope_angles(cache.seq_lens.cpu().numpy()[None] - 1, inv.cpu().numpy(), pa)[:, None], False)
+
+
 def test_append_many_sequences():
     # more sequences than the search holds in shared memory, one token each
     S = 1500
