@@ -33,7 +33,7 @@ int check_spec(const dilution_attn_rope_spec *spec, int d, RopeParams &rp) {
   if (spec->n_pairs > 0 && (spec->inv_freq == nullptr || !aligned(spec->inv_freq, 4))) return DA_ERR_INVALID;
   for (int j = 0; j < spec->n_pairs; ++j) {
     if (spec->pair_axis[j] >= spec->n_axes) return DA_ERR_INVALID;
-    rp.pair_axis[j] = spec->pair_axis[j];
+    rp.axis_bits[j / 16] |= (uint32_t)spec->pair_axis[j] << (2 * (j % 16));
   }
   rp.inv_freq = spec->inv_freq;
   rp.n_pairs = spec->n_pairs;

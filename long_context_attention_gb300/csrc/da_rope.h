@@ -12,7 +12,7 @@ struct RopeParams {
   long long pos_stride_b;     // elements between batch entries (0: shared)
   int n_pairs, n_axes;
   float sign;                 // +1 forward, -1 backward
-  uint8_t pair_axis[DA_MAX_ROPE_PAIRS];
+  uint32_t axis_bits[DA_MAX_ROPE_PAIRS / 16];   // the pairs' axes, two bits each
 };
 
 // One [B, H, T, d] operand pair of the rotation (element strides).

@@ -17,11 +17,12 @@
 //
 // What bounds it: bytes.  Each element is read once and written once; sin and
 // cos are computed in registers for one token and 16 bytes of a head's row and
-// serve `hpt` heads in turn, so they are a small part of the instructions.  The
-// loads of kRopeBatch heads are issued together before the first store: an output
-// may be its input, so the compiler cannot move a load over a store by itself
-// (one head at a time kept 32 bytes a thread in flight: 4.9 TB/s at 4 x 24 x
-// 16384 x 64 bf16).
+// serve `hpt` heads in turn, so they are a small part of the instructions (of two
+// heads they are most of them: 4 x 36238 tokens of 2 x 128 bf16 take 39.8 us, the
+// bytes 22).  The loads of several heads are issued together before the first
+// store: an output may be its input, so the compiler cannot move a load over a
+// store by itself (one head at a time kept 32 bytes a thread in flight: 4.9 TB/s at
+// 4 x 24 x 16384 x 64 bf16; now 5.9, and 6.7 at 24 x 131072 x 128 fp32).
 #include "da_rope.h"
 #include "da_ptx.cuh"
 
@@ -84,11 +85,6 @@ __device__ __forceinline__ void rope_sincos(uint2 F, bool ok, int pos, float sig
   if (quarter & 2u) s = -s;          // quarters 2, 3
   s *= sign;
   if (!ok) c = s = __int_as_float(0x7fc00000);
-}
-__device__ __forceinline__ void rope_sincos(float inv_freq, int pos, float sign, float &c, float &s) {
-  bool ok;
-  const uint2 F = turns_fixed(inv_freq, ok);
-  rope_sincos(F, ok, pos, sign, c, s);
 }
 
 template <typename E>
@@ -224,7 +220,38 @@ struct RopePlace {
 };
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeBatch = 4;   // heads loaded together
+// Heads loaded together: 4 in the rotation of more than 2 heads a thread (131072 x
+// 24 x 128 fp32: 480 us, 497 with 2), 2 of fewer (4 x 36238 tokens of 2 heads of 128:
+// 39.4 us, 42.7 with 4), where rows exchange their parts (121 us, 135 with 4, for 6
+// heads of the same tokens) and in the append (16 prompts: 24 us, 28 with 4).
+constexpr int kRopeBatch = 4, kFewBatch = 2;
+
+// The pairs' frequencies in turns and their axes, formed once a warp (every
+// thread for its own pairs cost half the instructions of a rotation of few heads,
+// and reads of the axes by lanes of different pairs one after another).  The
+// pairs N u + i of neighbouring pieces u lie next to each other.
+template <int N>
+struct RopeTable {
+  uint4 e[DA_MAX_ROPE_PAIRS];   // frequency (hi, lo), axis, whether it is finite and below 2^24
+  static __device__ __forceinline__ int slot(int j) { return j % N * (DA_MAX_ROPE_PAIRS / N) + j / N; }
+  __device__ __forceinline__ void fill(const RopeParams &rp) {   // all lanes of the warp
+#pragma unroll
+    for (int i = 0; i < DA_MAX_ROPE_PAIRS / 32; ++i) {
+      const int j = 32 * i + threadIdx.x % 32;
+      if (j < rp.n_pairs) {
+        bool ok;
+        const uint2 F = turns_fixed(__ldg(rp.inv_freq + j), ok);
+        const uint32_t w = j % 32 < 16 ? rp.axis_bits[2 * i] : rp.axis_bits[2 * i + 1];
+        e[slot(j)] = make_uint4(F.x, F.y, (w >> (2 * (j % 16))) & 3u, ok);
+      }
+    }
+    __syncwarp();
+  }
+  __device__ __forceinline__ void angle(int j, const RopePlace &at, float sign, float &c, float &s) const {
+    const uint4 v = e[slot(j)];
+    rope_sincos(make_uint2(v.x, v.y), v.w != 0u, at.on((int)v.z), sign, c, s);
+  }
+};
 
 // 16 bytes that are read once or written once: kept out of L1.
 __device__ __forceinline__ uint4 ld_once(const void *p) {
@@ -236,50 +263,63 @@ __device__ __forceinline__ uint4 ld_once(const void *p) {
   return r;
 }
 
-// grid.x: (token, unit) pairs, grid.y: groups of hpt heads of q followed by k.
-template <typename E, bool ADJ>
-__global__ void __launch_bounds__(kRopeThreads)
-    rope_kernel(RopeTensor q, RopeTensor k, const __grid_constant__ RopeParams rp, int Hq, int Hk, int T,
-                long long n_units, int units, int hpt) {
-  const long long i = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
-  if (i >= n_units) return;
-  const long long tok = i / units;
-  const int u = (int)(i - tok * units);
-  const long long b = tok / T, t = tok - b * T;
+// The tokens of the rotation kernels: a thread takes piece (or pair) u of one.
+struct RopeWalk {
+  int tokens, T, shift;   // shift: log2 of a row's pieces (or pairs)
+  __device__ __forceinline__ int piece() const { return threadIdx.x & ((1 << shift) - 1); }
+  __device__ __forceinline__ int token() const { return blockIdx.x * (kRopeThreads >> shift) + (threadIdx.x >> shift); }
+};
+// Its rows of every head.
+template <typename E>
+struct RopeRows {
+  int b, t, Hq;
+  const E *qi, *ki;
+  E *qo, *ko;
+  long long qih, kih, qoh, koh;
+  __device__ __forceinline__ RopeRows(const RopeTensor &q, const RopeTensor &k, int heads_q, int tok, int T)
+      : b((unsigned)tok / (unsigned)T), t(tok - b * T), Hq(heads_q), qih(q.in_h), kih(k.in_h), qoh(q.out_h), koh(k.out_h) {
+    qi = static_cast<const E *>(q.in) + (b * q.in_b + t * q.in_t);
+    ki = static_cast<const E *>(k.in) + (b * k.in_b + t * k.in_t);
+    qo = static_cast<E *>(q.out) + (b * q.out_b + t * q.out_t);
+    ko = static_cast<E *>(k.out) + (b * k.out_b + t * k.out_t);
+  }
+  __device__ __forceinline__ const E *in(int h) const { return h < Hq ? qi + h * qih : ki + (h - Hq) * kih; }
+  __device__ __forceinline__ E *out(int h) const { return h < Hq ? qo + h * qoh : ko + (h - Hq) * koh; }
+};
+
+// grid.x: runs of tokens, grid.y: groups of hpt heads of q followed by k.
+template <typename E, bool ADJ, int BATCH>
+__global__ void __launch_bounds__(kRopeThreads, BATCH > 2 ? 7 : 8)
+    rope_kernel(RopeTensor q, RopeTensor k, const __grid_constant__ RopeParams rp, RopeWalk w, int Hq, int Hk, int hpt) {
+  __shared__ RopeTable<RopeVec<E>::N> tables[kRopeThreads / 32];
   const int h0 = blockIdx.y * hpt, h1 = min(h0 + hpt, Hq + Hk);
   RopeUnit<E, ADJ> ru;
-  ru.place(u, rp.n_pairs);
-  auto source = [&](int h) -> const E * {
-    const bool isq = h < Hq;
-    const RopeTensor &x = isq ? q : k;
-    return static_cast<const E *>(x.in) + b * x.in_b + (isq ? h : h - Hq) * x.in_h + t * x.in_t;
-  };
-  auto target = [&](int h) -> E * {
-    const bool isq = h < Hq;
-    const RopeTensor &x = isq ? q : k;
-    return static_cast<E *>(x.out) + b * x.out_b + (isq ? h : h - Hq) * x.out_h + t * x.out_t;
-  };
-  bool first = true;
-  for (int hb = h0; hb < h1; hb += kRopeBatch) {
-    uint4 va[kRopeBatch], vb[kRopeBatch];
+  ru.place(w.piece(), rp.n_pairs);
+  const bool live = w.token() < w.tokens;
+  const RopeRows<E> at(q, k, Hq, live ? w.token() : 0, w.T);
+  uint4 va[BATCH], vb[BATCH];
+  auto load = [&](int hb) {
 #pragma unroll
-    for (int j = 0; j < kRopeBatch; ++j)
+    for (int j = 0; j < BATCH; ++j)
       if (hb + j < h1) {
-        const E *src = source(hb + j);
+        const E *src = at.in(hb + j);
         va[j] = ld_once(src + ru.va);
         vb[j] = ld_once(src + ru.vb);
       }
-    if (first) {   // the angles while the first loads are on their way
-      const RopePlace at(rp, b, t, 0);
-      ru.turn([&](int j, float &c, float &s) {
-        rope_sincos(__ldg(rp.inv_freq + j), at.on(rp.pair_axis[j]), rp.sign, c, s);
-      });
-      first = false;
-    }
+  };
+  // the angles while the first loads are on their way
+  if (live) load(h0);
+  RopeTable<RopeVec<E>::N> &table = tables[threadIdx.x / 32];
+  const RopePlace place(rp, at.b, at.t, 0);
+  table.fill(rp);
+  if (!live) return;
+  ru.turn([&](int j, float &c, float &s) { table.angle(j, place, rp.sign, c, s); });
+  for (int hb = h0; hb < h1; hb += BATCH) {
+    if (hb > h0) load(hb);
 #pragma unroll
-    for (int j = 0; j < kRopeBatch; ++j)
+    for (int j = 0; j < BATCH; ++j)
       if (hb + j < h1) {
-        E *dst = target(hb + j);
+        E *dst = at.out(hb + j);
         ru.apply(va[j], vb[j]);
         __stcs(reinterpret_cast<uint4 *>(dst + ru.va), va[j]);
         __stcs(reinterpret_cast<uint4 *>(dst + ru.vb), vb[j]);
@@ -294,46 +334,38 @@ __global__ void __launch_bounds__(kRopeThreads)
 // bf16 with 3 pairs, whose copies take 188.)
 template <typename E>
 __global__ void __launch_bounds__(kRopeThreads)
-    rope_any_kernel(RopeTensor q, RopeTensor k, const __grid_constant__ RopeParams rp, int Hq, int Hk, int T,
-                    long long n_units, int d, int hpt) {
-  constexpr int N = RopeVec<E>::N, B = kRopeBatch;
+    rope_any_kernel(RopeTensor q, RopeTensor k, const __grid_constant__ RopeParams rp, RopeWalk w, int Hq, int Hk, int hpt) {
+  constexpr int N = RopeVec<E>::N, B = kFewBatch;
   __shared__ __align__(16) E s_rows[B][kRopeThreads * N];   // the block's rows, one after another
-  const long long i = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
-  const int units = d / N, n = rp.n_pairs;   // lanes of a row: 8 to 32, so a row is one warp's
-  const long long tok = min(i, n_units - 1) / units;
-  const bool live = i < n_units;
-  const int u = threadIdx.x % units, base = (threadIdx.x - u) * N;
-  const long long b = tok / T, t = tok - b * T;
+  __shared__ RopeTable<N> tables[kRopeThreads / 32];
+  const int u = w.piece(), base = (threadIdx.x - u) * N, n = rp.n_pairs;   // lanes of a row: 8 to 32, so a row is one warp's
+  const int h0 = blockIdx.y * hpt, h1 = min(h0 + hpt, Hq + Hk);
+  RopeTable<N> &table = tables[threadIdx.x / 32];
+  const bool live = w.token() < w.tokens;
+  const RopeRows<E> at(q, k, Hq, live ? w.token() : 0, w.T);
   // the turn of each element: x cos + partner sin (the sine negative for the first of a pair)
   float c[N], s[N];
   int other[N];
   {
-    const RopePlace at(rp, b, t, 0);
+    const RopePlace place(rp, at.b, at.t, 0);
+    table.fill(rp);
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       const int x = u * N + e;
       other[e] = -1;
       if (x < 2 * n) {
         const int j = x < n ? x : x - n;
-        rope_sincos(__ldg(rp.inv_freq + j), at.on(rp.pair_axis[j]), rp.sign, c[e], s[e]);
+        table.angle(j, place, rp.sign, c[e], s[e]);
         other[e] = base + (x < n ? x + n : x - n);
         if (x < n) s[e] = -s[e];
       }
     }
   }
-  const int h0 = blockIdx.y * hpt, h1 = min(h0 + hpt, Hq + Hk);
-  auto row = [&](int h, bool out) -> const E * {
-    const bool isq = h < Hq;
-    const RopeTensor &x = isq ? q : k;
-    const int hh = isq ? h : h - Hq;
-    return out ? static_cast<const E *>(x.out) + b * x.out_b + hh * x.out_h + t * x.out_t + u * N
-               : static_cast<const E *>(x.in) + b * x.in_b + hh * x.in_h + t * x.in_t + u * N;
-  };
   for (int hb = h0; hb < h1; hb += B) {
     uint4 v[B];
 #pragma unroll
     for (int j = 0; j < B; ++j)
-      if (live && hb + j < h1) v[j] = ld_once(row(hb + j, false));
+      if (live && hb + j < h1) v[j] = ld_once(at.in(hb + j) + u * N);
 #pragma unroll
     for (int j = 0; j < B; ++j)
       if (live && hb + j < h1) *reinterpret_cast<uint4 *>(&s_rows[j][threadIdx.x * N]) = v[j];
@@ -351,7 +383,7 @@ __global__ void __launch_bounds__(kRopeThreads)
           if (other[e] >= 0) from_f32(fmaf(x[e], c[e], to_f32(s_rows[j][other[e]]) * s[e]), y[e]);
         v[j] = *reinterpret_cast<uint4 *>(y);
       }
-      __stcs(reinterpret_cast<uint4 *>(const_cast<E *>(row(hb + j, true))), v[j]);
+      __stcs(reinterpret_cast<uint4 *>(at.out(hb + j) + u * N), v[j]);
     }
     __syncwarp();
   }
@@ -380,67 +412,61 @@ __device__ __forceinline__ void rope_pair(const E *src, E *dst, int j, int n_pai
 // Any alignment: one thread per pair of elements (d / 2 of them a row).
 template <typename E>
 __global__ void __launch_bounds__(kRopeThreads)
-    rope_scalar_kernel(RopeTensor q, RopeTensor k, const __grid_constant__ RopeParams rp, int adjacent, int Hq,
-                       int Hk, int T, long long n_units, int units, int hpt) {
-  const long long i = (long long)blockIdx.x * kRopeThreads + threadIdx.x;
-  if (i >= n_units) return;
-  const long long tok = i / units;
-  const int j = (int)(i - tok * units);
-  const long long b = tok / T, t = tok - b * T;
-  float c = 1.f, s = 0.f;
-  if (j < rp.n_pairs)
-    rope_sincos(__ldg(rp.inv_freq + j), RopePlace(rp, b, t, 0).on(rp.pair_axis[j]), rp.sign, c, s);
+    rope_scalar_kernel(RopeTensor q, RopeTensor k, const __grid_constant__ RopeParams rp, int adjacent, RopeWalk w, int Hq,
+                       int Hk, int hpt) {
+  __shared__ RopeTable<1> tables[kRopeThreads / 32];
+  const int j = w.piece();
   const int h0 = blockIdx.y * hpt, h1 = min(h0 + hpt, Hq + Hk);
-  for (int h = h0; h < h1; ++h) {
-    const bool isq = h < Hq;
-    const RopeTensor &x = isq ? q : k;
-    const int hh = isq ? h : h - Hq;
-    rope_pair(static_cast<const E *>(x.in) + b * x.in_b + hh * x.in_h + t * x.in_t,
-              static_cast<E *>(x.out) + b * x.out_b + hh * x.out_h + t * x.out_t, j, rp.n_pairs, adjacent != 0,
-              [&](int, float &cc, float &ss) { cc = c, ss = s; });
-  }
+  RopeTable<1> &table = tables[threadIdx.x / 32];
+  table.fill(rp);
+  if (w.token() >= w.tokens) return;
+  const RopeRows<E> at(q, k, Hq, w.token(), w.T);
+  float c = 1.f, s = 0.f;
+  if (j < rp.n_pairs) table.angle(j, RopePlace(rp, at.b, at.t, 0), rp.sign, c, s);
+  for (int h = h0; h < h1; ++h)
+    rope_pair(at.in(h), at.out(h), j, rp.n_pairs, adjacent != 0, [&](int, float &cc, float &ss) { cc = c, ss = s; });
 }
 
 // Heads per thread: sin and cos are shared by the heads a thread visits, but a
 // short input needs the heads spread over threads to fill the GPU.
 static int heads_per_thread(long long n_units, int heads, int most) {
   const long long threads = n_units * heads, want = 152ll * 1024;
-  const long long h = threads / want;
-  return (int)(h < 1 ? 1 : h > most ? most : h);
+  const long long h = threads / want, cap = heads < most ? heads : most;
+  return (int)(h < 1 ? 1 : h > cap ? cap : h);
 }
 
 cudaError_t launch_rope(const RopeTensor &q, const RopeTensor &k, const RopeParams &rp, bool adjacent, RopePath path,
                         int B, int Hq, int Hk, int T, int d, int dtype, cudaStream_t stream) {
   const int n = dtype == DA_BF16 ? 8 : 4;
-  const int units = path == kRopeUnits ? d / (2 * n) : path == kRopeAny ? d / n : d / 2;
-  const long long n_units = (long long)B * T * units;
+  const int units = path == kRopeUnits ? d / (2 * n) : path == kRopeAny ? d / n : d / 2;   // a power of two
+  RopeWalk w;
+  w.tokens = B * T;
+  w.T = T;
+  w.shift = 0;
+  while ((1 << w.shift) < units) ++w.shift;
   // 2 x 32 heads x 51971 x 128 bf16: 272 us with 16 heads at most, 296 with 8, 276 with 24
-  const int hpt = heads_per_thread(n_units, Hq + Hk, 16);
-  const dim3 grid((unsigned)((n_units + kRopeThreads - 1) / kRopeThreads), (unsigned)((Hq + Hk + hpt - 1) / hpt));
-#define DA_ROPE_ARGS q, k, rp, Hq, Hk, T, n_units, units, hpt
-  if (path == kRopeAny) {
-    if (dtype == DA_BF16)
-      rope_any_kernel<__nv_bfloat16><<<grid, kRopeThreads, 0, stream>>>(q, k, rp, Hq, Hk, T, n_units, d, hpt);
-    else
-      rope_any_kernel<float><<<grid, kRopeThreads, 0, stream>>>(q, k, rp, Hq, Hk, T, n_units, d, hpt);
-  } else if (path == kRopeScalar) {
-    if (dtype == DA_BF16)
-      rope_scalar_kernel<__nv_bfloat16>
-          <<<grid, kRopeThreads, 0, stream>>>(q, k, rp, adjacent, Hq, Hk, T, n_units, units, hpt);
-    else
-      rope_scalar_kernel<float><<<grid, kRopeThreads, 0, stream>>>(q, k, rp, adjacent, Hq, Hk, T, n_units, units, hpt);
-  } else if (dtype == DA_BF16) {
-    if (adjacent)
-      rope_kernel<__nv_bfloat16, true><<<grid, kRopeThreads, 0, stream>>>(DA_ROPE_ARGS);
-    else
-      rope_kernel<__nv_bfloat16, false><<<grid, kRopeThreads, 0, stream>>>(DA_ROPE_ARGS);
+  const int hpt = heads_per_thread((long long)w.tokens * units, Hq + Hk, 16);
+  const int run = kRopeThreads >> w.shift;
+  const dim3 grid((unsigned)(((int64_t)w.tokens + run - 1) / run), (unsigned)((Hq + Hk + hpt - 1) / hpt));
+#define DA_ROPE_UNITS(E, BATCH)                                                                      \
+  adjacent ? rope_kernel<E, true, BATCH><<<grid, kRopeThreads, 0, stream>>>(q, k, rp, w, Hq, Hk, hpt) \
+           : rope_kernel<E, false, BATCH><<<grid, kRopeThreads, 0, stream>>>(q, k, rp, w, Hq, Hk, hpt)
+#define DA_ROPE(E)                                                                                   \
+  if (path == kRopeAny)                                                                              \
+    rope_any_kernel<E><<<grid, kRopeThreads, 0, stream>>>(q, k, rp, w, Hq, Hk, hpt);                 \
+  else if (path == kRopeScalar)                                                                      \
+    rope_scalar_kernel<E><<<grid, kRopeThreads, 0, stream>>>(q, k, rp, adjacent, w, Hq, Hk, hpt);    \
+  else if (hpt > 2)                                                                                  \
+    DA_ROPE_UNITS(E, kRopeBatch);                                                                    \
+  else                                                                                               \
+    DA_ROPE_UNITS(E, kFewBatch);
+  if (dtype == DA_BF16) {
+    DA_ROPE(__nv_bfloat16)
   } else {
-    if (adjacent)
-      rope_kernel<float, true><<<grid, kRopeThreads, 0, stream>>>(DA_ROPE_ARGS);
-    else
-      rope_kernel<float, false><<<grid, kRopeThreads, 0, stream>>>(DA_ROPE_ARGS);
+    DA_ROPE(float)
   }
-#undef DA_ROPE_ARGS
+#undef DA_ROPE
+#undef DA_ROPE_UNITS
   return cudaGetLastError();
 }
 
@@ -502,6 +528,8 @@ __global__ void __launch_bounds__(kRopeThreads)
                   const __grid_constant__ RopeParams rp) {
   __shared__ int32_t s_cu[kAppendSearch], s_len[kAppendSearch];
   __shared__ TokenPlace s_place[kRopeThreads];
+  __shared__ RopeTable<VEC ? RopeVec<E>::N : 1> tables[kRopeThreads / 32];
+  RopeTable<VEC ? RopeVec<E>::N : 1> &table = tables[threadIdx.x / 32];
   const int Hq = a.q != nullptr ? c.Hq : 0;
   const int rows = Hq + 2 * c.Hkv;
   const int groups = (rows + a.hpt - 1) / a.hpt;
@@ -519,10 +547,10 @@ __global__ void __launch_bounds__(kRopeThreads)
     return static_cast<const E *>(a.v) + n * a.v_t + (h - h_turn) * a.v_h;
   };
   RopeUnit<E, ADJ> ru;
-  uint4 va[kRopeBatch], vb[kRopeBatch];
+  uint4 va[kFewBatch], vb[kFewBatch];
   auto load = [&](int tt, int hb) {
 #pragma unroll
-    for (int j = 0; j < kRopeBatch; ++j)
+    for (int j = 0; j < kFewBatch; ++j)
       if (hb + j < h1) {
         const E *src = source(n0 + tt, hb + j);
         va[j] = ld_once(src + ru.va);
@@ -533,6 +561,7 @@ __global__ void __launch_bounds__(kRopeThreads)
     ru.place(u, h0 < h_turn ? rp.n_pairs : 0);
     if (mine && tt0 < last) load(tt0, h0);
   }
+  table.fill(rp);
   const int32_t *cu = a.cu_tokens, *lens = c.seq_lens;
   if (c.S + 1 <= kAppendSearch) {
     for (int i = threadIdx.x; i <= c.S; i += kRopeThreads) {
@@ -565,7 +594,7 @@ __global__ void __launch_bounds__(kRopeThreads)
     if (p.pos >= 0) {
       const RopePlace where(rp, 0, n, p.pos);
       auto angle = [&](int j, float &cc, float &ss) {
-        rope_sincos(__ldg(rp.inv_freq + j), where.on(rp.pair_axis[j]), 1.f, cc, ss);
+        table.angle(j, where, 1.f, cc, ss);
       };
       auto target = [&](int h) -> E * {
         if (h < Hq) return static_cast<E *>(a.q_out) + ((size_t)n * c.Hq + h) * c.d;
@@ -575,10 +604,10 @@ __global__ void __launch_bounds__(kRopeThreads)
       };
       if constexpr (VEC) {
         if (h0 < h_turn) ru.turn(angle);
-        for (int hb = h0; hb < h1; hb += kRopeBatch) {
+        for (int hb = h0; hb < h1; hb += kFewBatch) {
           if (hb > h0) load(tt, hb);
 #pragma unroll
-          for (int j = 0; j < kRopeBatch; ++j)
+          for (int j = 0; j < kFewBatch; ++j)
             if (hb + j < h1) {
               E *dst = target(hb + j);
               if (hb + j < h_turn) ru.apply(va[j], vb[j]);
