@@ -24,21 +24,23 @@ constexpr int kPgtHead = 4;   // units of a segment before its first tile (a pie
 // prefix's keys from L2 once per 16 rows; the tcgen05 kernels take 64 rows, but
 // are two launches more.  Device time of a step, tcgen05 against streaming, in us:
 // 96 rows x 12 key heads x 16384 keys (19 M pairs) 77 against 111, 24 x 12 x 16384
-// (4.7 M) 44.6 against 44.5, 44 x 2 x 37808 (3.3 M) 37 against 30, 80 x 8 x 4096
-// (2.6 M) 38 against 33.
+// (4.7 M) 40.9 against 44.0, 17 x 12 x 16384 (3.3 M) 39.1 against 41.4, 44 x 2 x 37824
+// (3.3 M) 36.7 against 30.3, 24 x 12 x 8192 (2.4 M) 33.3 against 31.8, 96 x 2 x 16384
+// (3.1 M) 37.4 against 33.0.
 constexpr int kPgxMinRows = 17;
 constexpr int64_t kPgxMinPairs = 4ll << 20;
 enum PgxUse { kPgxAuto, kPgxNever, kPgxAlways };
-constexpr int kPgxRows = 64;      // rows of a segment there
+constexpr int kPgxRows = 64;      // rows of a segment there, at most
 constexpr int kPgxTile = 128;     // keys of a tile
 constexpr int kPgxCtas = 152;     // pgx_values: one CTA an SM
 constexpr int kPgxKeyCtas = 304;  // pgx_keys: two
 // Beginning and ending a piece there costs about as much as this many tiles (8 us
-// of normalisers, queries and first copies, 3 us of sums; a tile 2.5 us; pgx_keys
+// of normalisers, queries and first copies, 3 us of sums; a tile 1 to 2 us; pgx_keys
 // 3 us and 1 us): a segment takes as many units before its first tile, so that a
-// CTA with two pieces gets fewer tiles (a step with 32 x 16 heads x 32768: 71.1
-// us, 72.3 with 4, 74.3 with 3).
-constexpr int kPgxHead = 6;
+// CTA with two pieces gets fewer tiles (steps with 32 x 16 heads x 32768 / 64 x 12
+// x 131072 / 32 x 12 x 32768: 76.8 / 255.6 / 70.9 us, with 5 81.0 / 257.0 / 72.8, with
+// 10 78.0 / 254.9 / 69.5).
+constexpr int kPgxHead = 8;
 
 // Equal cut of `total` units into stretches of base or base + 1.
 struct PgtCut {
@@ -65,7 +67,7 @@ struct PgtPlan {
   int logit_key0;                    // key of the logits' first column
   int wide;                          // the prefix goes to the tcgen05 kernels: 64-row segments, their own cuts
   int pre_rows;                      // rows of a prefix slot
-  int x_groups, x_tiles, x_segs;     // segments of the tcgen05 kernels
+  int x_groups, x_rows, x_tiles, x_segs;   // segments of the tcgen05 kernels: groups of equally many rows
   PgtCut x_keys, x_values;
   size_t logit_off, own_ml_off, own_acc_off, pre_ml_off, pre_acc_off, total;
 };
@@ -90,6 +92,7 @@ inline PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_l
   w.prefix_segs = Hkv * w.prefix_groups;
   w.x_tiles = w.wide ? (prefix_len + kPgxTile - 1) / kPgxTile : 0;
   w.x_groups = w.wide ? (rows + kPgxRows - 1) / kPgxRows : 0;
+  w.x_rows = w.wide ? (rows + w.x_groups - 1) / w.x_groups : 0;
   w.x_segs = Hkv * w.x_groups;
   w.x_keys = pgt_cut(w.x_segs * (w.x_tiles + kPgxHead), kPgxKeyCtas);
   w.x_values = pgt_cut(w.x_segs * (w.x_tiles + kPgxHead), kPgxCtas);
@@ -270,13 +273,13 @@ __device__ __forceinline__ PgtPieces pgt_pieces(const PagedDecode &p, const PgtP
   if (L.len[s] == 0) return r;
   const int hkv = hq / w.G, g = hq % w.G;
   if (w.wide) {
-    const int R = s * w.G + g, seg = hkv * w.x_groups + R / kPgxRows;
+    const int R = s * w.G + g, seg = hkv * w.x_groups + R / w.x_rows;
     const PgtCut &c = values ? w.x_values : w.x_keys;
     const int first = seg * (w.x_tiles + kPgxHead) + kPgxHead;
     const int c0 = c.cta_of(first), c1 = c.cta_of(first + w.x_tiles - 1);
     r.pre0 = c0 + seg;
     r.npre = c1 - c0 + 1;
-    r.pre_row = R % kPgxRows;
+    r.pre_row = R % w.x_rows;
   } else if (w.prefix_tiles > 0) {
     const int R = s * w.G + g, seg = hkv * w.prefix_groups + R / w.row_tile;
     const int a = seg * (w.prefix_tiles + kPgtHead) + kPgtHead;

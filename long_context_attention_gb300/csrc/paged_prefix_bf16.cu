@@ -41,6 +41,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 namespace da {
 
 bool make_page_map(CUtensorMap *m, const void *base, int64_t num, int page_size, int rows, int d,
@@ -49,7 +51,7 @@ bool make_page_map(CUtensorMap *m, const void *base, int64_t num, int page_size,
 constexpr uint32_t kXHalf = 128 * 128;        // 128 rows x 64 bf16
 constexpr uint32_t kXQHalf = kPgxRows * 128;  // 64 rows x 64 bf16
 constexpr uint32_t kNoDemand = 0xFFFFFFFFu;
-constexpr int kTabPitch = 72, kTabWords = 8 * kTabPitch;   // a demand-page table (no bank conflicts between groups)
+constexpr int kTabPitch = 72, kTabWords = 8 * kTabPitch;   // a demand-page table (no bank conflicts between entries)
 
 __device__ __forceinline__ uint64_t x_kmajor(const uint8_t *tile) { return smem_desc(smem_u32(tile), 16, 1024); }
 
@@ -69,6 +71,14 @@ struct XPiece {
   int hkv, row0, nrows;   // rows of the batch
   int seg, tile, n;       // segment, first key tile, tiles
   int run;                // tiles of the pieces before
+  // pgx_values deals a piece's rows out to both halves of its 64 places, so that
+  // the warps of both have as many (80 rows as 64 + 16, filled from the first place
+  // on, took 93.5 us a step of 40 x 8 heads x 52736, as 40 + 40 dealt out 89.5).
+  // The row in a place; nrows or above: none.
+  __device__ __forceinline__ int half() const { return (nrows + 15) / 16 * 8; }   // rows of the first half
+  __device__ __forceinline__ int row_at(int place) const {
+    return place >= 32 ? half() + place - 32 : place < half() ? place : kPgxRows;
+  }
 };
 struct XWalk {
   XPiece c;
@@ -82,8 +92,8 @@ struct XWalk {
     at = c.seg * units + kPgxHead + c.tile;   // the piece's first tile
     c.n = max(min(w.x_tiles - c.tile, to - at), 0);
     c.hkv = c.seg / w.x_groups;
-    c.row0 = c.seg % w.x_groups * kPgxRows;
-    c.nrows = min(kPgxRows, p.c.S * w.G - c.row0);
+    c.row0 = c.seg % w.x_groups * w.x_rows;
+    c.nrows = min(w.x_rows, p.c.S * w.G - c.row0);
   }
   __device__ __forceinline__ void start(const PagedDecode &p, const PgtPlan &w, const PgtCut &cut) {
     at = cut.first(blockIdx.x);
@@ -336,7 +346,7 @@ struct XVal {
   static constexpr uint32_t kOffSh = kOffV + kVStages * kTB;
   static constexpr uint32_t kOffOnes = kOffSh + 2 * kShBytes;   // above every V tile (positive offset)
   static constexpr uint32_t kOffDem = kOffOnes + 2048;          // demand: 16 warps x 2 x [8 rows][32 keys]
-  static constexpr uint32_t kOffTab = kOffDem + 16 * 2048;      // 4 tables [8 groups of 16 keys][64 rows, padded]
+  static constexpr uint32_t kOffTab = kOffDem + 16 * 2048;      // 4 tables [up to 8 pages][64 rows, padded]
   static constexpr uint32_t kOffRow = kOffTab + 4 * kTabWords * 4;       // c2, then -lse2, of the rows
   static constexpr uint32_t kOffBar = kOffRow + kPgxRows * 8;
   static constexpr int kSmemBytes = 1024 + kOffBar + 512;
@@ -485,47 +495,67 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
     }
   } else if (warp == C::kDemandWarps + 3) {
     // ------------------------------------------------------------ demand pages
-    // Table of a tile: for every 16-key group and row, the group's place in the
-    // demand pool in units of 16 floats.
+    // Table of a tile: for every row and page (or the tile's part of one), its place
+    // in the demand pool in units of 16 floats.  One warp issues about one
+    // instruction every 6 cycles, and the demand warps wait for the table first, so
+    // it is short: with an entry for every 16 keys they waited 4200 of the 6700
+    // cycles between their tiles.
     const int sh = w.page_shift, ps = 1 << sh;
+    const uint32_t page_places = (uint32_t)p.c.Hq << (sh - 4);
     bool ok = true;
-    for (; ok && it.c.n > 0; it.next(p, w)) {
-      const int32_t *dtab[2];
-      uint32_t head[2];
-      bool on[2];
+    auto tiles = [&](auto entries) {
+      constexpr int E = decltype(entries)::value, KEYS = kPgxTile / E;
+      for (; ok && it.c.n > 0; it.next(p, w)) {
+        const int32_t *dtab[2];
+        uint32_t head[2];
+        bool on[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = lane + 32 * h, R = it.c.row0 + r, s = r < it.c.nrows ? R / w.G : 0;
-        on[h] = r < it.c.nrows && L.len[s] > 0;          // idle slots and rows past the piece's have no demand
-        dtab[h] = p.c.demand_table + (size_t)s * p.c.max_pages;
-        head[h] = (uint32_t)(it.c.hkv * w.G + R % w.G);
+        for (int h = 0; h < 2; ++h) {
+          const int r = it.c.row_at(lane + 32 * h), R = it.c.row0 + r, s = r < it.c.nrows ? R / w.G : 0;
+          on[h] = r < it.c.nrows && L.len[s] > 0;          // idle slots and rows past the piece's have no demand
+          dtab[h] = p.c.demand_table + (size_t)s * p.c.max_pages;
+          head[h] = (uint32_t)(it.c.hkv * w.G + R % w.G) << (sh - 4);
+        }
+        int id[2][E];
+        auto fetch = [&](int k) {
+          const int key0 = (it.c.tile + k) * kPgxTile;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              id[h][e] = on[h] && k < it.c.n && key0 + KEYS * e < p.prefix_len ? __ldg(dtab[h] + ((key0 + KEYS * e) >> sh)) : -1;
+        };
+        fetch(0);
+        for (int k = 0; k < it.c.n; ++k) {
+          const int t = it.c.run + k, b = t & 3, key0 = (it.c.tile + k) * kPgxTile;
+          ok = warp_wait(&tab_free[b], ((t >> 2) & 1) ^ 1, wc);
+          if (!ok) break;
+          const uint32_t part = E == 1 ? (uint32_t)(key0 & (ps - 1)) >> 4 : 0u;   // the tile's place in its page
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              uint32_t at = kNoDemand;
+              if ((unsigned)id[h][e] < (unsigned)p.c.num_demand_pages)
+                at = (uint32_t)id[h][e] * page_places + (head[h] + part);
+              else if (on[h] && key0 + KEYS * e < p.prefix_len)
+                atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
+              sTab[b * kTabWords + e * kTabPitch + lane + 32 * h] = at;
+            }
+          fetch(k + 1);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tab_full[b]);
+        }
       }
-      for (int k = 0; k < it.c.n; ++k) {
-        const int t = it.c.run + k, b = t & 3;
-        ok = warp_wait(&tab_free[b], ((t >> 2) & 1) ^ 1, wc);
-        if (!ok) break;
-        const int key0 = (it.c.tile + k) * kPgxTile;
-        int id[2][8];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            id[h][j] = on[h] && key0 + 16 * j < p.prefix_len ? __ldg(dtab[h] + ((key0 + 16 * j) >> sh)) : -1;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint32_t at = kNoDemand;
-            if ((unsigned)id[h][j] < (unsigned)p.c.num_demand_pages)
-              at = (((uint32_t)id[h][j] * p.c.Hq + head[h]) << (sh - 4)) + (((key0 + 16 * j) & (ps - 1)) >> 4);
-            else if (on[h] && key0 + 16 * j < p.prefix_len)
-              atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
-            sTab[b * kTabWords + j * kTabPitch + lane + 32 * h] = at;
-          }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tab_full[b]);
-      }
-    }
+    };
+    if (sh >= 7)
+      tiles(std::integral_constant<int, 1>());
+    else if (sh == 6)
+      tiles(std::integral_constant<int, 2>());
+    else if (sh == 5)
+      tiles(std::integral_constant<int, 4>());
+    else
+      tiles(std::integral_constant<int, 8>());
   } else {
     // ------------------------------------------------------------ demand warpgroups
     const int g = warp / 4 & 1, rh = warp / 8, quarter = warp % 4;   // tile parity, row half, TMEM quarter
@@ -536,8 +566,10 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
     // the warp's demand: lane -> row 4 j + lane / 8, keys 4 (lane % 8) .. of the warp's 32
     float *const dem = reinterpret_cast<float *>(smem + C::kOffDem + warp * 2048);
     const int dr = lane / 8, dk = 4 * (lane % 8);
-    const uint32_t *tab_lane = sTab + ((quarter * 32 + dk) >> 4) * kTabPitch + 32 * rh + dr;
-    float *const pool = p.c.demand_pages + (dk & 15);
+    // its 16-key group: entry (group >> es) of the table, and the rest of the place
+    const int group = (quarter * 32 + dk) >> 4, es = min(w.page_shift - 4, 3);
+    const uint32_t *tab_lane = sTab + (group >> es) * kTabPitch + 32 * rh + dr;
+    float *const pool = p.c.demand_pages + 16 * (group & ((1 << es) - 1)) + (dk & 15);
     float *const slot = dem + dr * 32 + dk;
     float *const mine = dem + lane;                  // this thread's key: row r of a group at 32 r
     int piece = 0;
@@ -546,27 +578,29 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
       // rows: scale and normaliser (a row without a sequence bids nothing)
       {
         static_assert(4 * C::kDemandWarps == kPgxRows, "8 lanes a row");
-        const int r = warp * 4 + lane / 8, R = it.c.row0 + min(r, it.c.nrows - 1), s = R / w.G;
+        const int place = warp * 4 + lane / 8, r = it.c.row_at(place);
+        const int R = it.c.row0 + min(r, it.c.nrows - 1), s = R / w.G;
         const int hq = it.c.hkv * w.G + R % w.G;
         const float lse = pgt_row_lse<8>(p, w, line, L, s, hq, lane);
         const bool on = r < it.c.nrows && L.len[s] > 0;
         if (lane % 8 == 0) {
-          sC2[r] = on ? fmaxf(head_c2(p.hs, s * p.c.Hq + hq, nullptr), 1e-30f) : 1e-30f;
-          sNl[r] = on ? -lse : -INFINITY;
+          sC2[place] = on ? fmaxf(head_c2(p.hs, s * p.c.Hq + hq, nullptr), 1e-30f) : 1e-30f;
+          sNl[place] = on ? -lse : -INFINITY;
         }
       }
       for (int e = tid; e < kPgxRows * (D / 8); e += 512) {   // Q: the K-major B operand
         const int r = e / (D / 8), i = e % (D / 8);
         *reinterpret_cast<uint4 *>(sQ + (i >> 3) * kXQHalf + r * 128 + (((i & 7) ^ (r & 7)) << 4)) =
-            x_query<D>(p, w, it.c, r, i);
+            x_query<D>(p, w, it.c, it.c.row_at(r), i);
       }
       fence_proxy_async_smem();
       named_bar_sync(1, 512);
       if (tid == 0) mbar_arrive(q_full);
       const bool dead = __any_sync(0xffffffffu, *abort_flag != 0);
       const int k0 = (g ^ (it.c.run & 1));           // the warpgroup's first tile: alternate over the whole run
-      const int groups = min(4, (it.c.nrows - 32 * rh + 7) / 8);   // 8-row groups of the half with rows (or < 1)
-      for (int i = max(groups, 0); i < 4; ++i) {   // rows past them: no share (the products before are done)
+      // 8-row groups of the half with rows
+      const int groups = (max(0, rh == 0 ? min(it.c.half(), it.c.nrows) : it.c.nrows - it.c.half()) + 7) / 8;
+      for (int i = groups; i < 4; ++i) {   // rows past them: no share (the products before are done)
         const int to = ((4 * rh + i) ^ (key_l & 7)) << 4;
         *reinterpret_cast<uint4 *>(sh_row + to) = make_uint4(0u, 0u, 0u, 0u);
         *reinterpret_cast<uint4 *>(sh_row + 16384 + to) = make_uint4(0u, 0u, 0u, 0u);
@@ -679,7 +713,7 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
         const bool have = warp_wait(d_full, piece & 1, wc);
         tc_fence_after();
         const uint32_t td = tmem + C::kTmemD + ((uint32_t)(quarter * 32) << 16);
-        const int r = key_l % kPgxRows;
+        const int place = key_l % kPgxRows, r = it.c.row_at(place);
         float *part = reinterpret_cast<float *>(p.ws + w.pre_acc_off) +
                       ((size_t)(blockIdx.x + it.c.seg) * w.pre_rows + r) * acc_stride(D);
         auto column = [&](int c) { return td + (D == 128 && c >= 64 ? C::kTmemDHi - C::kTmemD + c - 64 : c); };
@@ -690,13 +724,13 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
             tmem_ld32(column(c), x);
             tmem_wait_ld_r(x);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) stage[r * C::kLd + c + e] = x[e];
+            for (int e = 0; e < 32; ++e) stage[place * C::kLd + c + e] = x[e];
           }
           float s1;
           tmem_ld1(td + 64, s1);
           tmem_wait_ld();
           asm volatile("" : "+f"(s1));
-          stage[r * C::kLd + D] = s1;
+          stage[place * C::kLd + D] = s1;
         }
         named_bar_sync(2, 128);
         if (have && quarter < 2) {
@@ -709,15 +743,15 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
                 *reinterpret_cast<float4 *>(part + c + e) =
-                    make_float4(x[e] + stage[r * C::kLd + c + e], x[e + 1] + stage[r * C::kLd + c + e + 1],
-                                x[e + 2] + stage[r * C::kLd + c + e + 2], x[e + 3] + stage[r * C::kLd + c + e + 3]);
+                    make_float4(x[e] + stage[place * C::kLd + c + e], x[e + 1] + stage[place * C::kLd + c + e + 1],
+                                x[e + 2] + stage[place * C::kLd + c + e + 2], x[e + 3] + stage[place * C::kLd + c + e + 3]);
             }
           }
           float s1;
           tmem_ld1(td + 64, s1);
           tmem_wait_ld();
           asm volatile("" : "+f"(s1));
-          if (r < it.c.nrows) part[D] = s1 + stage[r * C::kLd + D];
+          if (r < it.c.nrows) part[D] = s1 + stage[place * C::kLd + D];
         }
         x_release(d_free, lane);
       }
