@@ -12,7 +12,7 @@ namespace da {
 constexpr int kPgtMaxSeqs = 704;                  // lengths kept in shared memory (a larger batch goes in parts)
 // Keys per stage (16 KB of K or V) and rows of a segment at most.
 DA_HD constexpr int pgt_tile(int d, int dtype = DA_BF16) { return (dtype == DA_BF16 ? 8192 : 4096) / d; }
-DA_HD constexpr int pgt_row_tile(int dtype) { return dtype == DA_BF16 ? 16 : 8; }
+constexpr int kPgtRowTile = 16;
 DA_HD constexpr int pgt_warps(int d) { return pgt_tile(d) / 16; }    // pgt_keys: consumer warps, 16 keys of a stage each
 DA_HD constexpr int pgt_threads(int d) { return 32 * pgt_warps(d) + 32; }   // and the producer warp
 constexpr int kPgtMaxCtas = 2 * 152;              // two resident CTAs on each SM
@@ -63,7 +63,7 @@ DA_HD PgtCut pgt_cut(int total, int ctas) {   // no stretch without a unit
 
 // Host plan of a call; slots and scratch offsets.
 struct PgtPlan {
-  int ctas, tile, row_tile, page_shift, G, own_rows, own_groups, prefix_groups, prefix_tiles, own_segs, prefix_segs, Lp;
+  int ctas, tile, page_shift, G, own_rows, own_groups, prefix_groups, prefix_tiles, own_segs, prefix_segs, Lp;
   int logit_key0;                    // key of the logits' first column
   int wide;                          // the prefix goes to the tcgen05 kernels: 64-row segments, their own cuts
   int pre_rows;                      // rows of a prefix slot
@@ -75,12 +75,11 @@ struct PgtPlan {
 inline PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int page_size, int dtype,
                         PgxUse use = kPgxAuto) {
   PgtPlan w;
-  w.row_tile = pgt_row_tile(dtype);
   w.page_shift = 0;
   while ((1 << w.page_shift) < page_size) ++w.page_shift;
   w.G = Hq / Hkv;
-  w.own_rows = w.G < w.row_tile ? w.G : w.row_tile;
-  w.own_groups = (w.G + w.row_tile - 1) / w.row_tile;
+  w.own_rows = w.G < kPgtRowTile ? w.G : kPgtRowTile;
+  w.own_groups = (w.G + kPgtRowTile - 1) / kPgtRowTile;
   w.tile = pgt_tile(d, dtype);
   w.own_segs = S * Hkv * w.own_groups;
   const int rows = S * w.G;
@@ -88,7 +87,7 @@ inline PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_l
            (use == kPgxAlways || (int64_t)rows * Hkv * prefix_len >= kPgxMinPairs);
   const bool narrow = prefix_len > 0 && !w.wide;
   w.prefix_tiles = narrow ? (prefix_len + w.tile - 1) / w.tile : 0;
-  w.prefix_groups = narrow ? (rows + w.row_tile - 1) / w.row_tile : 0;
+  w.prefix_groups = narrow ? (rows + kPgtRowTile - 1) / kPgtRowTile : 0;
   w.prefix_segs = Hkv * w.prefix_groups;
   w.x_tiles = w.wide ? (prefix_len + kPgxTile - 1) / kPgxTile : 0;
   w.x_groups = w.wide ? (rows + kPgxRows - 1) / kPgxRows : 0;
@@ -96,7 +95,7 @@ inline PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_l
   w.x_segs = Hkv * w.x_groups;
   w.x_keys = pgt_cut(w.x_segs * (w.x_tiles + kPgxHead), kPgxKeyCtas);
   w.x_values = pgt_cut(w.x_segs * (w.x_tiles + kPgxHead), kPgxCtas);
-  w.pre_rows = w.wide ? kPgxRows : w.row_tile;
+  w.pre_rows = w.wide ? kPgxRows : kPgtRowTile;
   w.logit_key0 = w.wide ? prefix_len : 0;
   const int64_t own_tiles = (max_len - prefix_len + w.tile - 1) / w.tile;
   const int64_t most = w.own_segs * (own_tiles > 0 ? own_tiles + kPgtHead : 0) +
@@ -196,15 +195,15 @@ struct PgtSeg {
     n = min(left, stop - unit);
     if (s < 0) {
       hkv = seg / w.prefix_groups;
-      row0 = seg % w.prefix_groups * w.row_tile;
-      nrows = min(w.row_tile, p.c.S * w.G - row0);
+      row0 = seg % w.prefix_groups * kPgtRowTile;
+      nrows = min(kPgtRowTile, p.c.S * w.G - row0);
       key0 = tile * w.tile;
       end = p.prefix_len;
     } else {
       const int h = seg - s * t.per_own;
       hkv = h / w.own_groups;
-      row0 = h % w.own_groups * w.row_tile;
-      nrows = min(w.row_tile, w.G - row0);
+      row0 = h % w.own_groups * kPgtRowTile;
+      nrows = min(kPgtRowTile, w.G - row0);
       key0 = p.prefix_len + tile * w.tile;
       end = L.len[s];
     }
@@ -281,21 +280,21 @@ __device__ __forceinline__ PgtPieces pgt_pieces(const PagedDecode &p, const PgtP
     r.npre = c1 - c0 + 1;
     r.pre_row = R % w.x_rows;
   } else if (w.prefix_tiles > 0) {
-    const int R = s * w.G + g, seg = hkv * w.prefix_groups + R / w.row_tile;
+    const int R = s * w.G + g, seg = hkv * w.prefix_groups + R / kPgtRowTile;
     const int a = seg * (w.prefix_tiles + kPgtHead) + kPgtHead;
     const int c0 = t.cut.cta_of(a), c1 = t.cut.cta_of(a + w.prefix_tiles - 1);
     r.pre0 = c0 + seg;
     r.npre = c1 - c0 + 1;
-    r.pre_row = R % w.row_tile;
+    r.pre_row = R % kPgtRowTile;
   }
   const int units = L.cum[s + 1] - L.cum[s];
   if (units > 0) {
-    const int h = hkv * w.own_groups + g / w.row_tile;
+    const int h = hkv * w.own_groups + g / kPgtRowTile;
     const int a = t.prefix + L.cum[s] * t.per_own + h * units + kPgtHead;
     const int c0 = t.cut.cta_of(a), c1 = t.cut.cta_of(a + units - kPgtHead - 1);
     r.own0 = c0 + s * t.per_own + h;
     r.nown = c1 - c0 + 1;
-    r.own_row = g % w.row_tile;
+    r.own_row = g % kPgtRowTile;
   }
   return r;
 }

@@ -542,7 +542,7 @@ size_t pgt_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len,
 // Units on the line at most (int arithmetic on the device).
 bool pgt_fits(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int dtype) {
   if (S > kPgtMaxSeqs) S = kPgtMaxSeqs;
-  const int64_t G = Hq / Hkv, tile = pgt_tile(d, dtype), rt = pgt_row_tile(dtype), rows = (S * G + rt - 1) / rt;
+  const int64_t G = Hq / Hkv, tile = pgt_tile(d, dtype), rt = kPgtRowTile, rows = (S * G + rt - 1) / rt;
   const int64_t own = (max_len - prefix_len + tile - 1) / tile + kPgtHead;
   const int64_t pre = (prefix_len + tile - 1) / tile + kPgtHead;
   return S * (int64_t)Hkv * ((G + rt - 1) / rt) * own + (prefix_len > 0 ? Hkv * rows * pre : 0) < 0x7FFF0000ll;

@@ -10,15 +10,15 @@
 // the line of work, the page ring and the join are those of paged_decode_bf16.cu.
 //
 // What bounds it: HBM up to about 4 rows a key head, then the fp32 units and the
-// shared-memory reads of the products: 8 rows a segment keep the two near each
-// other (more rows would read a key once for more, but wait for the products).
+// shared-memory reads of the products.
 //
-// A warp takes 32 keys at a time, one a lane.  pgf_keys: each lane walks its key's
-// row (16-byte pieces, swizzled by TMA, so that 8 lanes read 8 banks' groups)
-// against the rows' queries, which all lanes read at one address (broadcast).
-// pgf_values: shares by key as there, then by column: a lane owns d / 32 columns
-// of the numerators and walks the keys, whose shares are broadcast.
-// 4 x 12 x 4001 .. 16001 keys: 97 us with plain loads and no ring.
+// A warp takes 32 keys at a time.  pgf_keys: a lane forms the products of up to 4
+// keys and 4 rows (16 rows: 8 lanes of keys by 4 of rows), so that 8 reads of 16
+// bytes, one shared-memory cycle each, feed 32 packed multiply-adds.  (A key a lane
+// and 8 rows a segment took 12 cycles for 16: 32 x 16 heads x 44928 keys, d = 128,
+// 281 us, now 180; the step 554 and 391.)  pgf_values: shares by key, then by column: a lane owns d / 32
+// columns of the numerators and walks the keys, 4 at a time, whose shares are
+// broadcast.  4 x 12 x 4001 .. 16001 keys: 97 us with plain loads and no ring.
 #include "da_paged_ring.cuh"
 
 namespace da {
@@ -35,15 +35,23 @@ struct PgfSteps {
   static constexpr int kStride = kPgfWarps / kPerTile;
 };
 
-template <int D, int R>   // R: rows of a segment at most (1, 2, 4, 8)
+// Lanes of pgf_keys: kRowLanes of rows by kKeyLanes of keys.
+template <int R>   // rows of a segment at most (1, 2, 4, 8, 16)
+struct PgfBlock {
+  static constexpr int kRowLanes = R > 4 ? R / 4 : 1, kKeyLanes = 32 / kRowLanes;
+  static constexpr int kRows = R / kRowLanes, kKeys = 32 / kKeyLanes;   // of a lane: rows j kRowLanes + .., keys i kKeyLanes + ..
+};
+
+template <int D, int R>
 __global__ void __launch_bounds__(kPgfThreads, 2)
     pgf_keys(PagedDecode p, PgtPlan w, const __grid_constant__ CUtensorMap kmap) {
   using T = PgfSteps<D>;
+  using B = PgfBlock<R>;
   constexpr int TILE = T::kTile, STAGES = (kPgfSmemPerCta - 1024) / kStageBytes / T::kStride * T::kStride;
   static_assert(STAGES <= 8 && STAGES >= T::kStride, "ring");
   __shared__ PgtLens L;
   __shared__ PgtRing ring;
-  __shared__ __align__(16) float s_q[R][D];
+  __shared__ __align__(16) float s_q[R][D + 4];   // (padded: the lanes of different rows read different banks)
   __shared__ float s_c2[R];
   __shared__ float2 s_ml[kPgfWarps][R];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -58,7 +66,7 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
     produce<TILE, 32>(p, w, line, L, ring, &kmap, smem_u32(smem), STAGES, from, to, wc);
     return;
   }
-  const int sub = warp % T::kPerTile * 32;
+  const int sub = warp % T::kPerTile * 32, kl = lane % B::kKeyLanes, rl = lane / B::kKeyLanes;
   PgtSeg g;
   for (g.start(p, w, line, L, from, to); g.n > 0; g.next(p, w, line, L)) {
     for (int i = tid; i < R * D; i += 32 * kPgfWarps) {
@@ -73,14 +81,15 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
       s_q[r][i % D] = v;
     }
     named_bar_sync(1, 32 * kPgfWarps);
-    float m[R], l[R], *xrow[R];
+    float m[B::kRows], l[B::kRows], *xrow[B::kRows];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      m[r] = -INFINITY;
-      l[r] = 0.f;
+    for (int j = 0; j < B::kRows; ++j) {
+      m[j] = -INFINITY;
+      l[j] = 0.f;
+      const int r = j * B::kRowLanes + rl;
       int s = 0, hq = 0;
       if (r < g.nrows) g.row(w.G, r, s, hq);
-      xrow[r] = reinterpret_cast<float *>(p.ws + w.logit_off) + ((size_t)s * p.c.Hq + hq) * w.Lp;
+      xrow[j] = reinterpret_cast<float *>(p.ws + w.logit_off) + ((size_t)s * p.c.Hq + hq) * w.Lp;
     }
     const int tile0 = (warp / T::kPerTile + T::kStride - g.run % T::kStride) % T::kStride;
     int steps = g.n > tile0 ? (g.n - tile0 + T::kStride - 1) / T::kStride : 0;
@@ -88,46 +97,63 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
     for (int k = 0; k < steps; ++k) {
       const int st = g.run + tile0 + k * T::kStride, slot = st % STAGES;
       if (!warp_wait(&ring.full[slot], (uint32_t)((st / STAGES) & 1), wc)) break;
-      const int key = g.key0 + (tile0 + k * T::kStride) * TILE + sub + lane;
-      if (key - lane < g.end) {
+      const int key = g.key0 + (tile0 + k * T::kStride) * TILE + sub + kl;   // the lane's first key
+      if (key - kl < g.end) {
         const uint8_t *tile = smem + slot * kStageBytes;
-        float2 acc[R];
+        float2 acc[B::kKeys][B::kRows];
 #pragma unroll
-        for (int r = 0; r < R; ++r) acc[r] = make_float2(0.f, 0.f);
+        for (int i = 0; i < B::kKeys; ++i)
+#pragma unroll
+          for (int j = 0; j < B::kRows; ++j) acc[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 8
-        for (int i = 0; i < D / 4; ++i) {
-          const float4 kv = *reinterpret_cast<const float4 *>(tile + tile_off<TILE>(sub + lane, i));
+        for (int c = 0; c < D / 4; ++c) {
+          float4 kv[B::kKeys];
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const float4 qv = *reinterpret_cast<const float4 *>(&s_q[r][4 * i]);
-            acc[r] = ffma2(make_float2(kv.x, kv.y), make_float2(qv.x, qv.y), acc[r]);
-            acc[r] = ffma2(make_float2(kv.z, kv.w), make_float2(qv.z, qv.w), acc[r]);
+          for (int i = 0; i < B::kKeys; ++i)
+            kv[i] = *reinterpret_cast<const float4 *>(tile + tile_off<TILE>(sub + kl + i * B::kKeyLanes, c));
+#pragma unroll
+          for (int j = 0; j < B::kRows; ++j) {
+            const float4 qv = *reinterpret_cast<const float4 *>(&s_q[j * B::kRowLanes + rl][4 * c]);
+#pragma unroll
+            for (int i = 0; i < B::kKeys; ++i) {
+              acc[i][j] = ffma2(make_float2(kv[i].x, kv[i].y), make_float2(qv.x, qv.y), acc[i][j]);
+              acc[i][j] = ffma2(make_float2(kv[i].z, kv[i].w), make_float2(qv.z, qv.w), acc[i][j]);
+            }
           }
         }
-        const bool in = key < g.end;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
+        for (int j = 0; j < B::kRows; ++j) {
+          const int r = j * B::kRowLanes + rl;
           if (r >= g.nrows) break;
-          const float x = in ? (acc[r].x + acc[r].y) * s_c2[r] : -INFINITY;
-          if (in) xrow[r][key] = x;
-          const float mn = fmaxf(m[r], x), ms = mn == -INFINITY ? 0.f : mn;
-          l[r] = l[r] * ex2_approx(m[r] - ms) + ex2_approx(x - ms);
-          m[r] = mn;
+          const float c2 = s_c2[r];
+          float x[B::kKeys], mn = m[j];
+#pragma unroll
+          for (int i = 0; i < B::kKeys; ++i) {
+            const bool in = key + i * B::kKeyLanes < g.end;
+            x[i] = in ? (acc[i][j].x + acc[i][j].y) * c2 : -INFINITY;
+            if (in) xrow[j][key + i * B::kKeyLanes] = x[i];
+            mn = fmaxf(mn, x[i]);
+          }
+          const float ms = mn == -INFINITY ? 0.f : mn;
+          l[j] *= ex2_approx(m[j] - ms);
+#pragma unroll
+          for (int i = 0; i < B::kKeys; ++i) l[j] += ex2_approx(x[i] - ms);
+          m[j] = mn;
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.empty[slot]);
     }
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int j = 0; j < B::kRows; ++j) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor_sync(0xffffffffu, m[r], o), l2 = __shfl_xor_sync(0xffffffffu, l[r], o);
-        const float mn = fmaxf(m[r], m2), ms = mn == -INFINITY ? 0.f : mn;
-        l[r] = l[r] * ex2_approx(m[r] - ms) + l2 * ex2_approx(m2 - ms);
-        m[r] = mn;
+      for (int o = B::kKeyLanes / 2; o > 0; o >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m[j], o), l2 = __shfl_xor_sync(0xffffffffu, l[j], o);
+        const float mn = fmaxf(m[j], m2), ms = mn == -INFINITY ? 0.f : mn;
+        l[j] = l[j] * ex2_approx(m[j] - ms) + l2 * ex2_approx(m2 - ms);
+        m[j] = mn;
       }
-      if (lane == 0) s_ml[warp][r] = make_float2(m[r], l[r]);
+      if (kl == 0) s_ml[warp][j * B::kRowLanes + rl] = make_float2(m[j], l[j]);
     }
     named_bar_sync(1, 32 * kPgfWarps);
     if (tid < g.nrows) {
@@ -148,31 +174,37 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
 
 // Each warp brings the logits and demand of its next step by 16-byte asynchronous
 // copies into its own place, [row][32 keys] of each, two steps in turn; the shares
-// take the logits' place, and the new demand goes back from the demand's.
+// take the logits' place, and the new demand goes back from the demand's.  16 rows
+// are two warps' work, each with 8 rows of the same 32 keys: one warp's numerators of
+// 16 rows do not fit the registers (32 x 16 heads x 44928, d = 128: 373 us with
+// spills, 231 us so).
 template <int D, int R>
 struct PgfVal {
-  static constexpr int kSide = 2 * 2 * R * 32 * 4;                  // a warp's logits and demand, two steps
-  static constexpr int kRed = R * D * 4;                            // its numerators, afterwards
+  static constexpr int kRows = R > 8 ? 8 : R;                       // of a warp
+  static constexpr int kTile = pgt_tile(D, DA_F32), kSubs = kTile / 32;
+  static constexpr int kPerTile = kSubs * (R / kRows);              // warps of a tile: by rows, then by keys
+  static constexpr int kStride = kPgfWarps / kPerTile;              // tiles between a warp's steps (see PgtVal on the ring)
+  static constexpr int kSide = 2 * 2 * kRows * 32 * 4;              // a warp's logits and demand, two steps
+  static constexpr int kRed = kRows * D * 4;                        // its numerators, afterwards
   static constexpr int kWarpBytes = kSide > kRed ? kSide : kRed;
   static constexpr int kRoom = (kPgfSmemPerCta - 1024 - kPgfWarps * kWarpBytes) / kStageBytes;
-  static constexpr int kStages = (kRoom < 8 ? kRoom : 8) / PgfSteps<D>::kStride * PgfSteps<D>::kStride;
-  static_assert(kStages >= 2 && kStages >= PgfSteps<D>::kStride, "a slot for every warp");
+  static constexpr int kStages = (kRoom < 8 ? kRoom : 8) / kStride * kStride;
+  static_assert(kStages >= 2 && kStages >= kStride, "a slot for every warp");
   static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kPgfWarps * kWarpBytes;
 };
 
-template <int D, int R>
+template <int D, int ROWS>   // of a segment at most
 __global__ void __launch_bounds__(kPgfThreads, 2)
     pgf_values(PagedDecode p, PgtPlan w, const __grid_constant__ CUtensorMap vmap) {
-  using T = PgfSteps<D>;
-  using V = PgfVal<D, R>;
-  constexpr int TILE = T::kTile, STRIDE = T::kStride * TILE, NC = D / 32;   // columns of a lane
+  using V = PgfVal<D, ROWS>;
+  constexpr int R = V::kRows, TILE = V::kTile, STRIDE = V::kStride * TILE, NC = D / 32;   // NC: columns of a lane
   constexpr int PIECES = (R * 8 + 31) / 32;                                 // 16-byte pieces of a lane (rows x 8)
   __shared__ PgtLens L;
   __shared__ PgtRing ring;
-  __shared__ float s_lse[R];
+  __shared__ float s_lse[ROWS];
   __shared__ float s_sum[kPgfWarps][R];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  if (tid == 0) ring.init(V::kStages, T::kPerTile);
+  if (tid == 0) ring.init(V::kStages, V::kPerTile);
   pgt_load_lens<kPgfThreads>(p, w, L, nullptr);
   const PgtLine line = pgt_line(p, w, L);
   const int from = line.cut.first(blockIdx.x), to = line.cut.first(blockIdx.x + 1);
@@ -184,8 +216,9 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
   }
   uint8_t *const base = smem + V::kStages * kStageBytes;
   float *const mine = reinterpret_cast<float *>(base + warp * V::kWarpBytes);   // [2 steps][x, D][R][32]
-  const int sh = w.page_shift, ps = 1 << sh, sub = warp % T::kPerTile * 32;
-  const int pr = lane / 8, pk = 4 * (lane % 8);   // the lane's pieces: rows pr, pr + 4, keys pk .. of a step
+  const int sh = w.page_shift, ps = 1 << sh, sub = warp % V::kSubs * 32;
+  const int r0 = warp % V::kPerTile / V::kSubs * R;   // the warp's first row
+  const int pr = lane / 8, pk = 4 * (lane % 8);       // the lane's pieces: rows pr, pr + 4 of the warp's, keys pk .. of a step
   // byte offsets of the lane's columns in a tile, for key & 7 = 0 .. 7
   uint32_t col[8];
 #pragma unroll
@@ -196,8 +229,8 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
   bool waited = false;
   PgtSeg g;
   for (g.start(p, w, line, L, from, to); g.n > 0; g.next(p, w, line, L)) {
-    const int tile0 = (warp / T::kPerTile + T::kStride - g.run % T::kStride) % T::kStride;
-    int steps = g.n > tile0 ? (g.n - tile0 + T::kStride - 1) / T::kStride : 0;
+    const int tile0 = (warp / V::kPerTile + V::kStride - g.run % V::kStride) % V::kStride;
+    int steps = g.n > tile0 ? (g.n - tile0 + V::kStride - 1) / V::kStride : 0;
     if (__any_sync(0xffffffffu, ring.abort_word != 0)) steps = 0;   // a wait gave up: touch no barrier again
     const int step0 = g.key0 + tile0 * TILE + sub;                  // the warp's first key
     // the lane's pieces
@@ -207,9 +240,9 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
     bool on[PIECES];
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      const int r = pr + 4 * i;
+      const int r = r0 + pr + 4 * i;
       int s = 0, hq = 0;
-      on[i] = r < g.nrows;
+      on[i] = pr + 4 * i < R && r < g.nrows;
       if (on[i]) g.row(w.G, r, s, hq);
       on[i] = on[i] && L.len[s] > 0;   // an idle slot bids nothing
       xrow[i] = reinterpret_cast<const float *>(p.ws + w.logit_off) + ((size_t)s * p.c.Hq + hq) * w.Lp;
@@ -279,8 +312,8 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
       const bool in = lane < left;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        if (r >= g.nrows) break;
-        const float lse = s_lse[r];
+        if (r0 + r >= g.nrows) break;
+        const float lse = s_lse[r0 + r];
         float share = 0.f;
         if (in && lse != INFINITY) {
           const float bid = ex2_approx(x[r * 32 + lane] - lse), d = dm[r * 32 + lane], nd = d + bid;
@@ -309,7 +342,7 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
         pages[0][i] = pages[1][i];
         pages[1][i] = next[i];
       }
-      const int st = g.run + tile0 + k * T::kStride, slot = st % V::kStages;
+      const int st = g.run + tile0 + k * V::kStride, slot = st % V::kStages;
       if (!warp_wait(&ring.full[slot], (uint32_t)((st / V::kStages) & 1), wc)) break;
       const uint8_t *tile = smem + slot * kStageBytes + sub * 128;
       // columns: 4 keys at a time (rows past the end are left out: they may hold anything)
@@ -336,7 +369,7 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
           float4 sv[R];
 #pragma unroll
           for (int r = 0; r < R; ++r)
-            sv[r] = r < g.nrows ? *reinterpret_cast<const float4 *>(x + r * 32 + k4) : make_float4(0.f, 0.f, 0.f, 0.f);
+            sv[r] = r0 + r < g.nrows ? *reinterpret_cast<const float4 *>(x + r * 32 + k4) : make_float4(0.f, 0.f, 0.f, 0.f);
           float s0[R], s1[R], s2[R], s3[R];
 #pragma unroll
           for (int r = 0; r < R; ++r) s0[r] = sv[r].x, s1[r] = sv[r].y, s2[r] = sv[r].z, s3[r] = sv[r].w;
@@ -350,7 +383,7 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
         for (int kk = 0; kk < left; ++kk) {
           float sv[R];
 #pragma unroll
-          for (int r = 0; r < R; ++r) sv[r] = r < g.nrows ? x[r * 32 + kk] : 0.f;
+          for (int r = 0; r < R; ++r) sv[r] = r0 + r < g.nrows ? x[r * 32 + kk] : 0.f;
           const int c = lane * NC * 4 / 16;
           take(kk, sv,
                (uint32_t)((c >> 3) * TILE * 128 + (((c & 7) ^ (kk & 7)) << 4) + (NC == 2 ? (lane & 1) * 8 : 0)));
@@ -377,13 +410,16 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
     for (int j = tid; j < g.nrows * D; j += 32 * kPgfWarps) {
       float a = 0.f;
 #pragma unroll
-      for (int v = 0; v < kPgfWarps; ++v) a += reinterpret_cast<const float *>(base + v * V::kWarpBytes)[j];
+      for (int v = 0; v < kPgfWarps; ++v)
+        if (R == ROWS || v % V::kPerTile / V::kSubs == j / D / R)   // the warps of the row
+          a += reinterpret_cast<const float *>(base + v * V::kWarpBytes)[j % (R * D)];
       part[j / D * acc_stride(D) + j % D] = a;
     }
     if (tid < g.nrows) {
       float a = 0.f;
 #pragma unroll
-      for (int v = 0; v < kPgfWarps; ++v) a += s_sum[v][tid];
+      for (int v = 0; v < kPgfWarps; ++v)
+        if (R == ROWS || v % V::kPerTile / V::kSubs == tid / R) a += s_sum[v][tid % R];
       part[tid * acc_stride(D) + D] = a;
     }
     named_bar_sync(1, 32 * kPgfWarps);
@@ -426,11 +462,12 @@ template <int D>
 static int launch_pgf_d(const PagedDecode &p, cudaStream_t stream) {
   const PgtPlan w = pgt_plan(p.c.S, p.c.Hq, p.c.Hkv, D, p.max_len, p.prefix_len, p.c.page_size, DA_F32);
   int rows = w.own_rows;   // the most rows of a segment
-  if (w.prefix_segs > 0) rows = p.c.S * w.G < w.row_tile ? p.c.S * w.G : w.row_tile;
+  if (w.prefix_segs > 0) rows = p.c.S * w.G < kPgtRowTile ? p.c.S * w.G : kPgtRowTile;
   if (rows <= 1) return launch_pgf_t<D, 1>(p, w, stream);
   if (rows <= 2) return launch_pgf_t<D, 2>(p, w, stream);
   if (rows <= 4) return launch_pgf_t<D, 4>(p, w, stream);
-  return launch_pgf_t<D, 8>(p, w, stream);
+  if (rows <= 8) return launch_pgf_t<D, 8>(p, w, stream);
+  return launch_pgf_t<D, 16>(p, w, stream);
 }
 
 int launch_paged_f32(const PagedDecode &p, cudaStream_t stream) {
