@@ -84,26 +84,73 @@ def test_shared_prefix_matches_oracle(dtype, S, own, Hq, Hkv, d, page, prefix):
     both_sizes(cache, q, max(lens), prefix_table=pt)
 
 
-@pytest.mark.parametrize("d", [64, 128])
-def test_prefix_rows_beyond_one_segment_over_many_tiles(d):
-    # 20 sequences x 4 heads a key head: two 64-row segments of 157 tiles each, cut over all CTAs; idle slots inside
-    prefix = 20000 // 32 * 32
-    lens = [0 if i % 7 == 2 else prefix + 1 + i for i in range(20)]
-    cache, q, pt = make_cache(20, lens, 8, 2, d, 32, "bf16", seed=97 + d, prefix=prefix)
+# Prefixes long enough for the kernels that take many rows at once (17 rows of a key
+# head and 2^22 (row, key, key head) triples), and one that stays below them.
+LONG_PREFIX = [
+    (64, 20, 8, 2, 32, 26240),        # 80 rows in two segments of 40, 205 tiles each, cut over all CTAs
+    (128, 20, 8, 2, 32, 26240),
+    (64, 17, 8, 8, 16, 30848),        # 17 rows: one in the second half
+    (128, 11, 12, 4, 64, 32768),      # 33 rows
+    (64, 65, 2, 1, 16, 32272),        # 130 rows in three segments; a last tile of 16 keys
+    (128, 64, 1, 1, 256, 65792),      # 64 rows; pages of two tiles, the last tile's page half used
+    (64, 48, 6, 3, 128, 14592),       # 96 rows in two segments of 48
+    (64, 12, 4, 4, 256, 132096),      # 12 rows: 16-row segments, keys that do not stay in L2
+]
+
+
+@pytest.mark.parametrize("d,S,Hq,Hkv,page,prefix", LONG_PREFIX)
+def test_long_prefix_with_idle_slots(d, S, Hq, Hkv, page, prefix):
+    lens = [0 if i % 7 == 2 else prefix + i % 40 for i in range(S)]
+    cache, q, pt = make_cache(S, lens, Hq, Hkv, d, page, "bf16", seed=97 + d + S, prefix=prefix)
     before = cache.demand_pages.clone()
     for flags in (0, b.DA_FLAG_EARLIER_DEMAND_ONLY):
         cache.demand_pages.copy_(before)
         out = b.dilution_attn_paged_decode(q, cache, max(lens), prefix_table=pt, flags=flags, eps=1e-4)
-        h, rows = 5, [0, 1, 2, 19]                  # the oracle on one query head of four sequences
-        one = b.PagedCache(cache.k_pages[:, 1:2].contiguous(), cache.v_pages[:, 1:2].contiguous(),
-                           before[:, h:h + 1].contiguous(), cache.page_table[rows].contiguous(),
-                           cache.demand_table[rows].contiguous(), cache.seq_lens[rows].contiguous())
-        ref = oracle_step(one, q[rows, h:h + 1], eps=1e-4, earlier=bool(flags))
-        mine = torch.zeros(one.demand_pages.shape[0], dtype=torch.bool, device=DEV)
-        mine[one.demand_table[one.demand_table >= 0].long()] = True
-        old = one.demand_pages.clone()
-        one.demand_pages[mine] = cache.demand_pages[mine, h:h + 1]
-        check_step(one, q[rows, h:h + 1], old, out[rows, h:h + 1], ref)
+        for h, rows in ((Hq - 1, [0, 1, 2, S - 1]), (0, [S // 2, S // 2 + 1])):   # the oracle on a query head of some
+            kv = h // (Hq // Hkv)
+            one = b.PagedCache(cache.k_pages[:, kv:kv + 1].contiguous(), cache.v_pages[:, kv:kv + 1].contiguous(),
+                               before[:, h:h + 1].contiguous(), cache.page_table[rows].contiguous(),
+                               cache.demand_table[rows].contiguous(), cache.seq_lens[rows].contiguous())
+            ref = oracle_step(one, q[rows, h:h + 1], eps=1e-4, earlier=bool(flags))
+            mine = torch.zeros(one.demand_pages.shape[0], dtype=torch.bool, device=DEV)
+            mine[one.demand_table[one.demand_table >= 0].long()] = True
+            old = one.demand_pages.clone()
+            one.demand_pages[mine] = cache.demand_pages[mine, h:h + 1]
+            check_step(one, q[rows, h:h + 1], old, out[rows, h:h + 1], ref)
+
+
+@pytest.mark.parametrize("d,S,Hq,Hkv,page,prefix", LONG_PREFIX[:3])
+def test_long_prefix_reports_bad_pages_and_repeats_its_bits(d, S, Hq, Hkv, page, prefix):
+    lens = [prefix + 1 + i for i in range(S)]
+    cache, q, pt = make_cache(S, lens, Hq, Hkv, d, page, "bf16", seed=3, prefix=prefix)
+    ws = b.dilution_attn_paged_decode_workspace(cache, max(lens), 1)     # the size knows no length of the prefix
+    before = cache.demand_pages.clone()
+
+    def run(table=pt):
+        cache.demand_pages.copy_(before)
+        out = b.dilution_attn_paged_decode(q, cache, max(lens), prefix_table=table, workspace=ws)
+        return out, cache.demand_pages.clone(), b.dilution_attn_get_error(ws)
+
+    good, demand, status = run()
+    assert status == b.DA_OK
+    again, demand2, _ = run()
+    assert torch.equal(good, again) and torch.equal(demand, demand2)
+    for bad in (-1, -7, cache.k_pages.shape[0], 1 << 30):
+        table = pt.clone()
+        table[table.numel() // 2] = bad
+        assert run(table)[2] == b.DA_ERR_INVALID
+    for bad in (-1, cache.demand_pages.shape[0], 1 << 30):               # sequence 4 alone suffers
+        keep = cache.demand_table[4, 3].item()
+        cache.demand_table[4, 3] = bad
+        out, new, status = run()
+        cache.demand_table[4, 3] = keep
+        others = [i for i in range(S) if i != 4]
+        assert status == b.DA_ERR_INVALID and torch.equal(out[others], good[others])
+        theirs = cache.demand_table[others].flatten().unique().long()
+        theirs = theirs[theirs >= 0]
+        assert torch.equal(new[theirs], demand[theirs])
+        assert torch.equal(new[keep], before[keep])                      # the page that lost its place
+    assert torch.equal(run()[0], good)
 
 
 def test_more_sequences_than_one_part():
