@@ -13,6 +13,14 @@ constexpr int kPgtMaxSeqs = 704;                  // lengths kept in shared memo
 // Keys per stage (16 KB of K or V) and rows of a segment at most.
 DA_HD constexpr int pgt_tile(int d, int dtype = DA_BF16) { return (dtype == DA_BF16 ? 8192 : 4096) / d; }
 constexpr int kPgtRowTile = 16;
+// Rows of a prefix's segment in bf16 at d = 64, if no segment has more and the keys
+// stay in L2 until they are read again: 9 to 16 rows are a product more for every 16
+// keys and two exponentials a lane instead of one.  16 x 12 heads x 2048 + 300 / 8192
+// + 300 / 32768 (50 MB of keys): 17.5 / 23.5 / 44.1 us a step, with 16 rows 20.5 / 27.3 /
+// 46.6; 12 x 12 x 65536 (101 MB) 75.6 against 67.5; at d = 128 37.3 against 32.4 for 96
+// rows x 2 heads x 16384.
+constexpr int kPgtPreRows = 8;
+constexpr int64_t kPgtPreBytes = 64ll << 20;
 DA_HD constexpr int pgt_warps(int d) { return pgt_tile(d) / 16; }    // pgt_keys: consumer warps, 16 keys of a stage each
 DA_HD constexpr int pgt_threads(int d) { return 32 * pgt_warps(d) + 32; }   // and the producer warp
 constexpr int kPgtMaxCtas = 2 * 152;              // two resident CTAs on each SM
@@ -87,7 +95,10 @@ inline PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_l
            (use == kPgxAlways || (int64_t)rows * Hkv * prefix_len >= kPgxMinPairs);
   const bool narrow = prefix_len > 0 && !w.wide;
   w.prefix_tiles = narrow ? (prefix_len + w.tile - 1) / w.tile : 0;
-  w.prefix_groups = narrow ? (rows + kPgtRowTile - 1) / kPgtRowTile : 0;
+  const bool few = use == kPgxAuto && dtype == DA_BF16 && d == 64 && w.own_rows <= kPgtPreRows &&
+                   (int64_t)Hkv * prefix_len * d * 2 <= kPgtPreBytes;
+  w.pre_rows = w.wide ? kPgxRows : few ? kPgtPreRows : kPgtRowTile;   // (the workspace is that of the most rows)
+  w.prefix_groups = narrow ? (rows + w.pre_rows - 1) / w.pre_rows : 0;
   w.prefix_segs = Hkv * w.prefix_groups;
   w.x_tiles = w.wide ? (prefix_len + kPgxTile - 1) / kPgxTile : 0;
   w.x_groups = w.wide ? (rows + kPgxRows - 1) / kPgxRows : 0;
@@ -95,7 +106,6 @@ inline PgtPlan pgt_plan(int S, int Hq, int Hkv, int d, int max_len, int prefix_l
   w.x_segs = Hkv * w.x_groups;
   w.x_keys = pgt_cut(w.x_segs * (w.x_tiles + kPgxHead), kPgxKeyCtas);
   w.x_values = pgt_cut(w.x_segs * (w.x_tiles + kPgxHead), kPgxCtas);
-  w.pre_rows = w.wide ? kPgxRows : kPgtRowTile;
   w.logit_key0 = w.wide ? prefix_len : 0;
   const int64_t own_tiles = (max_len - prefix_len + w.tile - 1) / w.tile;
   const int64_t most = w.own_segs * (own_tiles > 0 ? own_tiles + kPgtHead : 0) +
@@ -195,8 +205,8 @@ struct PgtSeg {
     n = min(left, stop - unit);
     if (s < 0) {
       hkv = seg / w.prefix_groups;
-      row0 = seg % w.prefix_groups * kPgtRowTile;
-      nrows = min(kPgtRowTile, p.c.S * w.G - row0);
+      row0 = seg % w.prefix_groups * w.pre_rows;
+      nrows = min(w.pre_rows, p.c.S * w.G - row0);
       key0 = tile * w.tile;
       end = p.prefix_len;
     } else {
@@ -280,12 +290,12 @@ __device__ __forceinline__ PgtPieces pgt_pieces(const PagedDecode &p, const PgtP
     r.npre = c1 - c0 + 1;
     r.pre_row = R % w.x_rows;
   } else if (w.prefix_tiles > 0) {
-    const int R = s * w.G + g, seg = hkv * w.prefix_groups + R / kPgtRowTile;
+    const int R = s * w.G + g, seg = hkv * w.prefix_groups + R / w.pre_rows;
     const int a = seg * (w.prefix_tiles + kPgtHead) + kPgtHead;
     const int c0 = t.cut.cta_of(a), c1 = t.cut.cta_of(a + w.prefix_tiles - 1);
     r.pre0 = c0 + seg;
     r.npre = c1 - c0 + 1;
-    r.pre_row = R % kPgtRowTile;
+    r.pre_row = R % w.pre_rows;
   }
   const int units = L.cum[s + 1] - L.cum[s];
   if (units > 0) {

@@ -542,7 +542,7 @@ size_t pgt_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len,
 // Units on the line at most (int arithmetic on the device).
 bool pgt_fits(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int dtype) {
   if (S > kPgtMaxSeqs) S = kPgtMaxSeqs;
-  const int64_t G = Hq / Hkv, tile = pgt_tile(d, dtype), rt = kPgtRowTile, rows = (S * G + rt - 1) / rt;
+  const int64_t G = Hq / Hkv, tile = pgt_tile(d, dtype), rt = kPgtRowTile, rows = (S * G + kPgtPreRows - 1) / kPgtPreRows;
   const int64_t own = (max_len - prefix_len + tile - 1) / tile + kPgtHead;
   const int64_t pre = (prefix_len + tile - 1) / tile + kPgtHead;
   return S * (int64_t)Hkv * ((G + rt - 1) / rt) * own + (prefix_len > 0 ? Hkv * rows * pre : 0) < 0x7FFF0000ll;
@@ -595,7 +595,7 @@ template <int D>
 static int launch_pgt_d(const PagedDecode &p, cudaStream_t stream) {
   const PgtPlan w = pgt_plan(p.c.S, p.c.Hq, p.c.Hkv, D, p.max_len, p.prefix_len, p.c.page_size, DA_BF16);
   int rows = w.own_rows;                                 // the most rows of a segment
-  if (w.prefix_segs > 0) rows = p.c.S * w.G < 16 ? p.c.S * w.G : 16;
+  if (w.prefix_segs > 0) rows = p.c.S * w.G < w.pre_rows ? p.c.S * w.G : w.pre_rows;
   if (rows <= 1) return launch_pgt_t<D, 1>(p, w, stream);
   if (rows <= 2) return launch_pgt_t<D, 2>(p, w, stream);
   if (rows <= 4) return launch_pgt_t<D, 4>(p, w, stream);
