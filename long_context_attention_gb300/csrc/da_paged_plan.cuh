@@ -31,10 +31,10 @@ constexpr int kPgtHead = 4;   // units of a segment before its first tile (a pie
 // the batch's sequences x query heads of one key head) at a time and read the
 // prefix's keys from L2 once per 16 rows; the tcgen05 kernels take 64 rows, but
 // are two launches more.  Device time of a step, tcgen05 against streaming, in us:
-// 96 rows x 12 key heads x 16384 keys (19 M pairs) 77 against 111, 24 x 12 x 16384
-// (4.7 M) 40.9 against 44.0, 17 x 12 x 16384 (3.3 M) 39.1 against 41.4, 44 x 2 x 37824
-// (3.3 M) 36.7 against 30.3, 24 x 12 x 8192 (2.4 M) 33.3 against 31.8, 96 x 2 x 16384
-// (3.1 M) 37.4 against 33.0.
+// 96 rows x 12 key heads x 16384 keys (19 M pairs) 77 against 111, 64 x 12 x 8192 (6.3
+// M) 46.7 against 55.3, 46 x 12 x 9216 (5.1 M) 41.9 against 45.5, 24 x 12 x 16384 (4.7
+// M) 40.5 against 38.4, 17 x 12 x 16384 (3.3 M) 38.1 against 35.8, 44 x 2 x 37824 (3.3 M)
+// 36.1 against 30.0, 96 x 2 x 16384 at d = 128 (3.1 M) 37.4 against 33.0.
 constexpr int kPgxMinRows = 17;
 constexpr int64_t kPgxMinPairs = 4ll << 20;
 enum PgxUse { kPgxAuto, kPgxNever, kPgxAlways };
