@@ -289,7 +289,7 @@ struct RopeRows {
 
 // grid.x: runs of tokens, grid.y: groups of hpt heads of q followed by k.
 template <typename E, bool ADJ, int BATCH>
-__global__ void __launch_bounds__(kRopeThreads, BATCH > 2 ? 7 : 8)
+__global__ void __launch_bounds__(kRopeThreads, BATCH <= 2 ? 8 : sizeof(E) == 2 ? 7 : 6)
     rope_kernel(RopeTensor q, RopeTensor k, const __grid_constant__ RopeParams rp, RopeWalk w, int Hq, int Hk, int hpt) {
   __shared__ RopeTable<RopeVec<E>::N> tables[kRopeThreads / 32];
   const int h0 = blockIdx.y * hpt, h1 = min(h0 + hpt, Hq + Hk);
