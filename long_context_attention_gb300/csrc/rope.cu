@@ -59,16 +59,17 @@ __device__ __forceinline__ uint2 turns_fixed(float f, bool &ok) {
   return make_uint2(hi, lo);
 }
 
-// cos and sin of position * inv_freq, from the frequency in turns (F).  The
-// angle's top bits give the nearest quarter turn, the rest an angle of at most
-// pi / 4, whose Taylor series to the 9th and 8th power are within 2e-9 and 3e-8
-// (half an fp32 step of 1); a quarter turn swaps the two and sets the signs.
-__device__ __forceinline__ void rope_sincos(uint2 F, bool ok, int pos, float sign, float &c, float &s) {
+// cos and sin of the angle pos F, F in turns per position.  The angle's top bits
+// give the nearest quarter turn, the rest an angle of at most pi / 4, whose Taylor
+// series to the 9th and 8th power are within 2e-9 and 3e-8 (half an fp32 step of 1);
+// a quarter turn swaps the two and sets the signs.  unit: radians of the angle's
+// last bit (NaN: the frequency is not valid).
+__device__ __forceinline__ void rope_sincos(uint2 F, float unit, int pos, float &c, float &s) {
   // the upper word of pos F mod 2^64: the angle as a signed 0.32 turn
   uint32_t a = F.x * (uint32_t)pos + __umulhi(F.y, (uint32_t)pos);
   if (pos < 0) a -= F.y;
-  const uint32_t quarter = (a + 0x20000000u) >> 30;
-  const float x = (float)(int)(a - (quarter << 30)) * 1.4629180792671596e-9f;   // 2 pi 2^-32: radians
+  const uint32_t q = a + 0x20000000u;   // its top two bits: the quarter
+  const float x = (float)(int)(a - (q & 0xC0000000u)) * unit;
   const float x2 = x * x;
   float sn = fmaf(x2, 2.7557319e-6f, -1.9841270e-4f);                           // 1 / 9!, -1 / 7!
   sn = fmaf(x2, sn, 8.3333333e-3f);
@@ -78,13 +79,10 @@ __device__ __forceinline__ void rope_sincos(uint2 F, bool ok, int pos, float sig
   cs = fmaf(x2, cs, 4.1666667e-2f);
   cs = fmaf(x2, cs, -0.5f);
   cs = fmaf(x2, cs, 1.f);
-  const bool swap = quarter & 1u;
-  c = swap ? sn : cs;
-  s = swap ? cs : sn;
-  if ((quarter + 1u) & 2u) c = -c;   // quarters 1, 2
-  if (quarter & 2u) s = -s;          // quarters 2, 3
-  s *= sign;
-  if (!ok) c = s = __int_as_float(0x7fc00000);
+  const bool swap = (q & 0x40000000u) != 0u;
+  // the cosine is negative in quarters 1 and 2, the sine in 2 and 3
+  c = __uint_as_float(__float_as_uint(swap ? sn : cs) ^ ((q + 0x40000000u) & 0x80000000u));
+  s = __uint_as_float(__float_as_uint(swap ? cs : sn) ^ (q & 0x80000000u));
 }
 
 template <typename E>
@@ -232,7 +230,7 @@ constexpr int kRopeBatch = 4, kFewBatch = 2;
 // pairs N u + i of neighbouring pieces u lie next to each other.
 template <int N>
 struct RopeTable {
-  uint4 e[DA_MAX_ROPE_PAIRS];   // frequency (hi, lo), axis, whether it is finite and below 2^24
+  uint4 e[DA_MAX_ROPE_PAIRS];   // frequency (hi, lo; turned back: negated), axis, unit (see rope_sincos)
   static __device__ __forceinline__ int slot(int j) { return j % N * (DA_MAX_ROPE_PAIRS / N) + j / N; }
   __device__ __forceinline__ void fill(const RopeParams &rp) {   // all lanes of the warp
 #pragma unroll
@@ -240,16 +238,18 @@ struct RopeTable {
       const int j = 32 * i + threadIdx.x % 32;
       if (j < rp.n_pairs) {
         bool ok;
-        const uint2 F = turns_fixed(__ldg(rp.inv_freq + j), ok);
+        const uint2 F = turns_fixed(__ldg(rp.inv_freq + j) * rp.sign, ok);
         const uint32_t w = j % 32 < 16 ? rp.axis_bits[2 * i] : rp.axis_bits[2 * i + 1];
-        e[slot(j)] = make_uint4(F.x, F.y, (w >> (2 * (j % 16))) & 3u, ok);
+        const float unit = ok ? 1.4629180792671596e-9f : __int_as_float(0x7fc00000);   // 2 pi 2^-32
+        e[slot(j)] = make_uint4(F.x, F.y, (w >> (2 * (j % 16))) & 3u, __float_as_uint(unit));
       }
     }
     __syncwarp();
   }
-  __device__ __forceinline__ void angle(int j, const RopePlace &at, float sign, float &c, float &s) const {
+  template <bool ONE>   // of one axis
+  __device__ __forceinline__ void angle(int j, const RopePlace &at, float &c, float &s) const {
     const uint4 v = e[slot(j)];
-    rope_sincos(make_uint2(v.x, v.y), v.w != 0u, at.on((int)v.z), sign, c, s);
+    rope_sincos(make_uint2(v.x, v.y), __uint_as_float(v.w), ONE ? at.v[0] : at.on((int)v.z), c, s);
   }
 };
 
@@ -313,7 +313,10 @@ __global__ void __launch_bounds__(kRopeThreads, BATCH <= 2 ? 8 : sizeof(E) == 2 
   const RopePlace place(rp, at.b, at.t, 0);
   table.fill(rp);
   if (!live) return;
-  ru.turn([&](int j, float &c, float &s) { table.angle(j, place, rp.sign, c, s); });
+  if (rp.n_axes == 1)
+    ru.turn([&](int j, float &c, float &s) { table.template angle<true>(j, place, c, s); });
+  else
+    ru.turn([&](int j, float &c, float &s) { table.template angle<false>(j, place, c, s); });
   for (int hb = h0; hb < h1; hb += BATCH) {
     if (hb > h0) load(hb);
 #pragma unroll
@@ -355,7 +358,7 @@ __global__ void __launch_bounds__(kRopeThreads)
       other[e] = -1;
       if (x < 2 * n) {
         const int j = x < n ? x : x - n;
-        table.angle(j, place, rp.sign, c[e], s[e]);
+        table.template angle<false>(j, place, c[e], s[e]);
         other[e] = base + (x < n ? x + n : x - n);
         if (x < n) s[e] = -s[e];
       }
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(kRopeThreads)
   if (w.token() >= w.tokens) return;
   const RopeRows<E> at(q, k, Hq, w.token(), w.T);
   float c = 1.f, s = 0.f;
-  if (j < rp.n_pairs) table.angle(j, RopePlace(rp, at.b, at.t, 0), rp.sign, c, s);
+  if (j < rp.n_pairs) table.angle<false>(j, RopePlace(rp, at.b, at.t, 0), c, s);
   for (int h = h0; h < h1; ++h)
     rope_pair(at.in(h), at.out(h), j, rp.n_pairs, adjacent != 0, [&](int, float &cc, float &ss) { cc = c, ss = s; });
 }
@@ -593,9 +596,7 @@ __global__ void __launch_bounds__(kRopeThreads)
     const long long n = n0 + tt;
     if (p.pos >= 0) {
       const RopePlace where(rp, 0, n, p.pos);
-      auto angle = [&](int j, float &cc, float &ss) {
-        table.angle(j, where, 1.f, cc, ss);
-      };
+      auto angle = [&](int j, float &cc, float &ss) { table.template angle<false>(j, where, cc, ss); };
       auto target = [&](int h) -> E * {
         if (h < Hq) return static_cast<E *>(a.q_out) + ((size_t)n * c.Hq + h) * c.d;
         const bool is_k = h < h_turn;
