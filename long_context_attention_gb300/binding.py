@@ -456,21 +456,25 @@ def rope_spec(inv_freq, pair_axis=None, n_axes: int = 1, adjacent: bool = False)
 # The calls of a serving loop are short (a few microseconds on the GPU), so their
 # checks are written for the case that passes: one condition per tensor, the
 # device and the stream read once, strides kept as C arrays by their values.
+_Tensor = torch.Tensor
+
+
 def _fit(t, name, shape, dtype, dev):
     """_need for a contiguous tensor on device ``dev`` (the current one)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape
             and t.is_contiguous()):
         _need(t, name, tuple(shape), dtype)
 
 
 def _fit_rows(t, name, shape, dtype, dev):
-    """The same for a tensor whose last dimension alone is contiguous; returns its strides."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape):
+    """The same for a tensor whose last dimension alone is contiguous; returns the
+    strides of the others as a C array."""
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape):
         _need_any_strides(t, name, tuple(shape), dtype)
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    return st
+    return _stride_arrays.get(st) or _c_strides(st, len(st) - 1)
 
 
 def _need_any_strides(t, name, shape, dtype):
@@ -481,22 +485,29 @@ def _need_any_strides(t, name, shape, dtype):
     _need(t, name)
 
 
-_stride_arrays: dict = {}
+_stride_arrays: dict = {}   # of tensors of rows: strides -> all but the last as a C array
 
 
 def _c_strides(st, n):
-    """The first n of a tensor's strides as a C array."""
-    key = st[:n]
-    got = _stride_arrays.get(key)
-    if got is None:
+    """The first n of a tensor's strides as a C array, kept if they are all but the last."""
+    got = (ctypes.c_int64 * n)(*st[:n])
+    if n == len(st) - 1:
         if len(_stride_arrays) >= 4096:
             _stride_arrays.clear()
-        got = _stride_arrays[key] = (ctypes.c_int64 * n)(*key)
+        _stride_arrays[st] = got
     return got
 
 
+_cuda_up = False
+
+
 def _current_device() -> int:
-    return _get_device() if torch.cuda.is_initialized() else torch.cuda.current_device()
+    global _cuda_up
+    if not _cuda_up:
+        if not torch.cuda.is_initialized():
+            return torch.cuda.current_device()
+        _cuda_up = True
+    return _get_device()
 
 
 # absent in a torch without CUDA, where every call fails its tensor checks before
@@ -541,27 +552,30 @@ def _rope_call(name, q, k, positions, rope, q_out, k_out, stream, check):
     lib = _lib or load()
     if type(rope) is not RopeSpec:
         raise TypeError("rope must be a RopeSpec (see rope_spec)")
-    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+    if not isinstance(q, _Tensor) or q.dim() != 4:
         raise ValueError("q must be a [B, H, T, d] tensor")
     shape, dtype = q.shape, q.dtype
     B, Hq, T, d = shape
-    dt = _CODES[dtype] if dtype in _CODES else _dtype_code(q)
+    dt = _CODES.get(dtype)
+    if dt is None:
+        dt = _dtype_code(q)
     dev = _current_device()
-    sq = _c_strides(_fit_rows(q, "q", shape, dtype, dev), 3)
+    sq = _fit_rows(q, "q", shape, dtype, dev)
     if q_out is None:
-        q_out = _new(shape, dtype, q.device, stream)
+        q_out = torch.empty(shape, dtype=dtype, device=q.device) if stream is None else _new(shape, dtype, q.device, stream)
         so = None
     else:
-        so = _c_strides(_fit_rows(q_out, "q_out", shape, dtype, dev), 3)
+        so = _fit_rows(q_out, "q_out", shape, dtype, dev)
     if k is not None:
-        Hk = k.shape[1] if isinstance(k, torch.Tensor) and k.dim() == 4 else 0
-        kshape = (B, Hk, T, d)
-        sk, kp = _c_strides(_fit_rows(k, "k", kshape, dtype, dev), 3), k.data_ptr()
+        Hk = k.shape[1] if isinstance(k, _Tensor) and k.dim() == 4 else 0
+        kshape = shape if Hk == Hq else (B, Hk, T, d)
+        sk, kp = _fit_rows(k, "k", kshape, dtype, dev), k.data_ptr()
         if k_out is None:
-            k_out = _new(kshape, dtype, q.device, stream)
+            k_out = torch.empty(kshape, dtype=dtype, device=q.device) if stream is None else \
+                _new(kshape, dtype, q.device, stream)
             sko = None
         else:
-            sko = _c_strides(_fit_rows(k_out, "k_out", kshape, dtype, dev), 3)
+            sko = _fit_rows(k_out, "k_out", kshape, dtype, dev)
         kop = k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
@@ -676,19 +690,20 @@ def dilution_attn_paged_append(q, k, v, cache, cu_tokens, q_out=None, *, rope=No
     lib = _lib or load()
     dev = _need_cache(cache)
     Hq, Hkv, d, dtype = cache.Hq, cache.Hkv, cache.d, cache.dtype
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+    if not isinstance(k, _Tensor) or k.dim() != 3:
         raise ValueError("k must be [N, Hkv, d]")
     N = k.shape[0]
     kvshape = (N, Hkv, d)
-    sk = _c_strides(_fit_rows(k, "k", kvshape, dtype, dev), 2)
-    sv = _c_strides(_fit_rows(v, "v", kvshape, dtype, dev), 2)
+    sk = _fit_rows(k, "k", kvshape, dtype, dev)
+    sv = _fit_rows(v, "v", kvshape, dtype, dev)
     _fit(cu_tokens, "cu_tokens", cache._cu_shape, torch.int32, dev)
     qp = sq = qop = dp = sd = None
     if q is not None:
         qshape = (N, Hq, d)
-        sq, qp = _c_strides(_fit_rows(q, "q", qshape, dtype, dev), 2), q.data_ptr()
+        sq, qp = _fit_rows(q, "q", qshape, dtype, dev), q.data_ptr()
         if q_out is None:
-            q_out = _new(qshape, dtype, cache.device, stream)
+            q_out = torch.empty(qshape, dtype=dtype, device=cache.device) if stream is None else \
+                _new(qshape, dtype, cache.device, stream)
         else:
             _fit(q_out, "q_out", qshape, dtype, dev)
         qop = q_out.data_ptr()
