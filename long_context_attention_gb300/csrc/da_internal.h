@@ -280,7 +280,7 @@ struct HeadScale {
 // (when given) and yields 0, i.e. uniform bids.
 __device__ __forceinline__ float head_c2(const HeadScale &hs, int bh, int *status) {
   if (hs.tau_bh == nullptr) return hs.c2;
-  const float t = __ldg(hs.tau_bh + bh);
+  const float t = __ldcg(hs.tau_bh + bh);
   if (!(t >= 0.f && t <= 3.0e38f)) {
     if (status != nullptr) atomicCAS(status, DA_OK, DA_ERR_INVALID);
     return 0.f;

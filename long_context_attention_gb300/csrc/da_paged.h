@@ -25,7 +25,7 @@ struct PagedDecode {
 // Length of sequence s, 0 where it is not valid (then recorded once by the
 // caller that passes `status`).
 __device__ __forceinline__ int paged_len(const PagedDecode &p, int s, int *status) {
-  const int len = __ldg(p.c.seq_lens + s);
+  const int len = __ldcg(p.c.seq_lens + s);
   if (len == 0) return 0;
   if (len < 0 || len > p.max_len || len < p.prefix_len) {
     if (status != nullptr) atomicCAS(status, DA_OK, DA_ERR_INVALID);

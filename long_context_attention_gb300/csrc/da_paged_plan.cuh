@@ -135,9 +135,6 @@ struct PgtLens {
   int warp_sum[32];
 };
 
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // All threads of the block: fills L; ends with a block barrier.
 template <int THREADS>
 __device__ void pgt_load_lens(const PagedDecode &p, const PgtPlan &w, PgtLens &L, int *status) {
@@ -320,8 +317,8 @@ __device__ __forceinline__ float pgt_row_lse(const PagedDecode &p, const PgtPlan
   float m = -INFINITY, l = 0.f;
 #pragma unroll 4
   for (int c = lane % WIDTH; c < pc.npre + pc.nown; c += WIDTH) {
-    const float2 ml = c < pc.npre ? pre[(size_t)(pc.pre0 + c) * w.pre_rows + pc.pre_row]
-                                  : own[(size_t)(pc.own0 + c - pc.npre) * w.own_rows + pc.own_row];
+    const float2 ml = __ldcg(c < pc.npre ? pre + (size_t)(pc.pre0 + c) * w.pre_rows + pc.pre_row
+                                         : own + (size_t)(pc.own0 + c - pc.npre) * w.own_rows + pc.own_row);
     const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
     l = l * ex2_approx(m - ms) + ml.y * ex2_approx(ml.x - ms);
     m = mn;
@@ -364,29 +361,15 @@ __device__ __forceinline__ int group_key(int c, int half) { return 4 * (c >> 1) 
 
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// Launch that may begin before its predecessor in the stream has finished: as
-// soon as the predecessor's CTAs have called pdl_launch_dependents.  Kernels of
-// one decode step, in launch order:
-//   pgt_keys    waits for everything before it (an ordinary launch);
+// Kernels of one decode step, in launch order (see launch_after):
+//   pgt_keys    waits for everything before the step, then lets its successor begin;
 //   pgx_keys    needs nothing of pgt_keys; it waits for it before it ends;
 //   pgt_values  waits for the keys' kernels, then lets its successor begin;
 //   pgx_values  so begins after the keys' kernels; waits for pgt_values before it ends;
 //   pgt_combine waits for its predecessor, and with it for all of them.
-template <typename... KArgs, typename... Args>
-static cudaError_t launch_after(void (*kernel)(KArgs...), int grid, int threads, int smem, cudaStream_t stream,
-                                Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
+// What they read before a wait of their own, of the caller's or of each other's, is
+// in L2 by then, and they read it there (__ldcg, asynchronous copies): an SM's L1 may
+// hold what it saw before.
 #endif  // __CUDACC__
 
 }  // namespace da

@@ -69,9 +69,9 @@ __device__ void produce(const PagedDecode &p, const PgtPlan &w, const PgtLine &l
     const int32_t *table = g.s >= 0 ? p.c.page_table + (size_t)g.s * p.c.max_pages : p.prefix_table;
     int key = g.key0 + lane * rows;                                   // this lane's piece
     const int limit = lane * rows < TILE ? g.end : 0;                 // lanes past the tile bring nothing
-    int page = key < limit ? __ldg(table + (key >> sh)) : -1;
+    int page = key < limit ? __ldcg(table + (key >> sh)) : -1;
     for (int k = 0; k < g.n; ++k, ++issued) {
-      const int ahead = k + 1 < g.n && key + TILE < limit ? __ldg(table + ((key + TILE) >> sh)) : -1;
+      const int ahead = k + 1 < g.n && key + TILE < limit ? __ldcg(table + ((key + TILE) >> sh)) : -1;
       if (!warp_wait(&ring.empty[slot], parity, wc)) {
         if (lane == 0) drain(ring.full, stages, issued);
         return;

@@ -82,8 +82,9 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
   __shared__ PgtRing ring;
   __shared__ float2 s_ml[WARPS][16];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  pdl_launch_dependents();
   if (tid == 0) ring.init(stages, WARPS);
+  pdl_wait();   // for everything before the step
+  pdl_launch_dependents();
   pgt_load_lens<pgt_threads(D)>(p, w, L, blockIdx.x == 0 ? p.status : nullptr);
   const PgtLine line = pgt_line(p, w, L);
   const int from = line.cut.first(blockIdx.x), to = line.cut.first(blockIdx.x + 1);
@@ -120,8 +121,8 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
           reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)s * p.c.Hq + hq) * D);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        qa[ks][hh] = ok ? __ldg(qr + ks * 8 + t) : 0u;
-        qa[ks][2 + hh] = ok ? __ldg(qr + ks * 8 + 4 + t) : 0u;
+        qa[ks][hh] = ok ? qr[ks * 8 + t] : 0u;
+        qa[ks][2 + hh] = ok ? qr[ks * 8 + 4 + t] : 0u;
       }
     }
     float m[HH], l[HH];
@@ -274,7 +275,8 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
     }
     auto demand_page = [&](int k, int hh) -> int {     // of the lane's keys of step k
       const int key = key0 + k * STRIDE;
-      return on[hh] && k < steps && key < g.end ? __ldg(dtab[hh] + (key >> sh)) : -1;
+      const int32_t *at = dtab[hh] + (key >> sh);
+      return on[hh] && k < steps && key < g.end ? (waited ? *at : __ldcg(at)) : -1;
     };
     auto demand_at = [&](int k, int hh, int pg) -> float * {
       return dpool[hh] + (size_t)pg * page_floats + ((key0 + k * STRIDE) & (ps - 1));
@@ -499,9 +501,9 @@ __global__ void __launch_bounds__(kPgtCombThreads) pgt_combine(PagedDecode p, Pg
   for (int c = way; c < pc.npre + pc.nown; c += WAYS) {
     const float *pa = c < pc.npre ? pre + (size_t)(pc.pre0 + c) * w.pre_rows * acc_stride(D)
                                   : own + (size_t)(pc.own0 + c - pc.npre) * w.own_rows * acc_stride(D);
-    const float4 v = *reinterpret_cast<const float4 *>(pa + 4 * e);
+    const float4 v = __ldcg(reinterpret_cast<const float4 *>(pa + 4 * e));
     a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-    rs += pa[D];
+    rs += __ldcg(pa + D);
   }
   s_a[way][e] = a;
   if (e == 0) s_r[way] = rs;
@@ -575,7 +577,9 @@ static int launch_pgt_t(const PagedDecode &p, const PgtPlan &w, cudaStream_t str
   const int k_stages = p.prefix_len == 0 ? 4 : 6;
   constexpr int k_most = 1024 + 6 * kStageBytes;
   static_assert(k_most <= kPgtSmemPerCta, "two CTAs an SM");
-  pgt_keys<D, HH><<<w.ctas, pgt_threads(D), 1024 + k_stages * kStageBytes, stream>>>(p, w, km, k_stages);
+  if (launch_after(pgt_keys<D, HH>, w.ctas, pgt_threads(D), 1024 + k_stages * kStageBytes, stream, p, w, km, k_stages) !=
+      cudaSuccess)
+    return DA_ERR_CUDA;
   if (w.wide) {
     const int st = launch_pgx_keys(p, w, stream);
     if (st != DA_OK) return st;

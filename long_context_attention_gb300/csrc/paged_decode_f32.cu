@@ -55,8 +55,9 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
   __shared__ float s_c2[R];
   __shared__ float2 s_ml[kPgfWarps][R];
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  pdl_launch_dependents();
   if (tid == 0) ring.init(STAGES, T::kPerTile);
+  pdl_wait();
+  pdl_launch_dependents();
   pgt_load_lens<kPgfThreads>(p, w, L, blockIdx.x == 0 ? p.status : nullptr);
   const PgtLine line = pgt_line(p, w, L);
   const int from = line.cut.first(blockIdx.x), to = line.cut.first(blockIdx.x + 1);
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
       if (r < g.nrows) {
         int s, hq;
         g.row(w.G, r, s, hq);
-        v = __ldg(static_cast<const float *>(p.q) + ((size_t)s * p.c.Hq + hq) * D + i % D);
+        v = static_cast<const float *>(p.q)[((size_t)s * p.c.Hq + hq) * D + i % D];
         if (i % D == 0) s_c2[r] = head_c2(p.hs, s * p.c.Hq + hq, p.status);
       }
       s_q[r][i % D] = v;
@@ -251,7 +252,8 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
     }
     auto demand_page = [&](int k, int i) -> int {
       const int key = step0 + k * STRIDE + pk;
-      return on[i] && k < steps && key < g.end ? __ldg(dtab[i] + (key >> sh)) : -1;
+      const int32_t *at = dtab[i] + (key >> sh);
+      return on[i] && k < steps && key < g.end ? (waited ? *at : __ldcg(at)) : -1;
     };
     auto bring = [&](int k, const int (&pg)[PIECES]) {
       float *x = mine + (k & 1) * (2 * R * 32);
@@ -451,8 +453,8 @@ static int launch_pgf_t(const PagedDecode &p, const PgtPlan &w, cudaStream_t str
   if (!make_page_map(&km, p.c.k_pages, num > 0 ? num : 1, p.c.page_size, T::kTile, D, DA_F32) ||
       !make_page_map(&vm, p.c.v_pages, num > 0 ? num : 1, p.c.page_size, T::kTile, D, DA_F32))
     return DA_ERR_CUDA;
-  pgf_keys<D, R><<<w.ctas, kPgfThreads, k_smem, stream>>>(p, w, km);
-  if (launch_after(pgf_values<D, R>, w.ctas, kPgfThreads, PgfVal<D, R>::kSmemBytes, stream, p, w, vm) != cudaSuccess ||
+  if (launch_after(pgf_keys<D, R>, w.ctas, kPgfThreads, k_smem, stream, p, w, km) != cudaSuccess ||
+      launch_after(pgf_values<D, R>, w.ctas, kPgfThreads, PgfVal<D, R>::kSmemBytes, stream, p, w, vm) != cudaSuccess ||
       launch_combine(p, w, stream) != cudaSuccess)
     return DA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;

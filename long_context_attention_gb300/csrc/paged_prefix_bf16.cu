@@ -115,7 +115,7 @@ template <int D>
 __device__ __forceinline__ int x_page(const PagedDecode &p, const PgtPlan &w, int tile, int lane) {
   const int rows = min(1 << w.page_shift, kPgxTile);
   const int key = tile * kPgxTile + lane * rows;
-  return lane * rows < kPgxTile && key < p.prefix_len ? __ldg(p.prefix_table + (key >> w.page_shift)) : -1;
+  return lane * rows < kPgxTile && key < p.prefix_len ? __ldcg(p.prefix_table + (key >> w.page_shift)) : -1;
 }
 template <int D>
 __device__ __forceinline__ void x_load(const PagedDecode &p, const PgtPlan &w, const CUtensorMap *map, uint8_t *dst,
@@ -139,7 +139,7 @@ template <int D>
 __device__ __forceinline__ uint4 x_query(const PagedDecode &p, const PgtPlan &w, const XPiece &c, int r, int i) {
   if (r >= c.nrows) return make_uint4(0u, 0u, 0u, 0u);
   const int R = c.row0 + r, s = R / w.G, hq = c.hkv * w.G + R % w.G;
-  return __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)s * p.c.Hq + hq) * D) + i);
+  return __ldcg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)s * p.c.Hq + hq) * D) + i);
 }
 
 // ============================================================================ pass 1
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int e = 0; e < E; ++e)
-              id[h][e] = on[h] && k < it.c.n && key0 + KEYS * e < p.prefix_len ? __ldg(dtab[h] + ((key0 + KEYS * e) >> sh)) : -1;
+              id[h][e] = on[h] && k < it.c.n && key0 + KEYS * e < p.prefix_len ? __ldcg(dtab[h] + ((key0 + KEYS * e) >> sh)) : -1;
         };
         fetch(0);
         for (int k = 0; k < it.c.n; ++k) {

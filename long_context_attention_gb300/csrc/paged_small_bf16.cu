@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(kSmallThreads)
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x / csize, s = pair / p.c.Hkv, hkv = pair % p.c.Hkv;
   const int ps = 1 << page_shift;
+  pdl_wait();
   const int len = paged_len(p, s, hkv == 0 && rank == 0 && tid == 0 ? p.status : nullptr);
   const int share_keys = ((len + csize - 1) / csize + 15) & ~15;      // keys of each CTA
   const int key0 = rank * share_keys, nk = max(0, min(share_keys, len - key0)), fill = (nk + 15) & ~15;
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(kSmallThreads)
     for (int j = 0; j < IT; ++j) {
       const int r = r0 + j * STEP, key = key0 + r;
       page[j] = -1;
-      if (r < nk) page[j] = __ldg((key < p.prefix_len ? p.prefix_table : table) + (key >> page_shift));
+      if (r < nk) page[j] = (key < p.prefix_len ? p.prefix_table : table)[key >> page_shift];
     }
     size_t at[IT];
 #pragma unroll
@@ -136,8 +137,8 @@ __global__ void __launch_bounds__(kSmallThreads)
         reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)s * p.c.Hq + hq) * D);
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      qa[ks][hh] = on[hh] ? __ldg(qr + ks * 8 + t) : 0u;
-      qa[ks][2 + hh] = on[hh] ? __ldg(qr + ks * 8 + 4 + t) : 0u;
+      qa[ks][hh] = on[hh] ? qr[ks * 8 + t] : 0u;
+      qa[ks][2 + hh] = on[hh] ? qr[ks * 8 + 4 + t] : 0u;
     }
   }
   // the lane's demand: 4 keys of its rows in each of the warp's groups
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kSmallThreads)
       dp[j][hh] = nullptr;
       dem[j][hh] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (on[hh] && kl < nk) {
-        const int dpg = __ldg(dtab + (key >> page_shift));
+        const int dpg = dtab[key >> page_shift];
         if ((unsigned)dpg < (unsigned)p.c.num_demand_pages) {
           dp[j][hh] = p.c.demand_pages + (((size_t)dpg * p.c.Hq + hkv * G + g + 8 * hh) << page_shift) + (key & (ps - 1));
           dem[j][hh] = *reinterpret_cast<const float4 *>(dp[j][hh]);
@@ -362,12 +363,14 @@ static int launch_small_t(const PagedDecode &p, int csize, cudaStream_t stream) 
   cfg.blockDim = dim3(kSmallThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)csize;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // (see launch_after)
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, pgs_small<D, WIDE>, p, p.c.Hq / p.c.Hkv, shift, csize) == cudaSuccess ? DA_OK
                                                                                                         : DA_ERR_CUDA;
 }

@@ -209,7 +209,7 @@ struct RopePlace {
     for (int a = 0; a < DA_MAX_ROPE_AXES; ++a) {
       v[a] = fallback;
       if (rp.positions != nullptr && a < rp.n_axes)
-        v[a] = __ldg(rp.positions + a * rp.pos_stride_axis + b * rp.pos_stride_b + t);
+        v[a] = rp.positions[a * rp.pos_stride_axis + b * rp.pos_stride_b + t];
     }
   }
   __device__ __forceinline__ int on(int axis) const {
@@ -238,7 +238,7 @@ struct RopeTable {
       const int j = 32 * i + threadIdx.x % 32;
       if (j < rp.n_pairs) {
         bool ok;
-        const uint2 F = turns_fixed(__ldg(rp.inv_freq + j) * rp.sign, ok);
+        const uint2 F = turns_fixed(rp.inv_freq[j] * rp.sign, ok);
         const uint32_t w = j % 32 < 16 ? rp.axis_bits[2 * i] : rp.axis_bits[2 * i + 1];
         const float unit = ok ? 1.4629180792671596e-9f : __int_as_float(0x7fc00000);   // 2 pi 2^-32
         e[slot(j)] = make_uint4(F.x, F.y, (w >> (2 * (j % 16))) & 3u, __float_as_uint(unit));
@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kRopeThreads, BATCH <= 2 ? 8 : sizeof(E) == 2 
       }
   };
   // the angles while the first loads are on their way
+  pdl_wait();
   if (live) load(h0);
   RopeTable<RopeVec<E>::N> &table = tables[threadIdx.x / 32];
   const RopePlace place(rp, at.b, at.t, 0);
@@ -349,6 +350,7 @@ __global__ void __launch_bounds__(kRopeThreads)
   // the turn of each element: x cos + partner sin (the sine negative for the first of a pair)
   float c[N], s[N];
   int other[N];
+  pdl_wait();
   {
     const RopePlace place(rp, at.b, at.t, 0);
     table.fill(rp);
@@ -421,6 +423,7 @@ __global__ void __launch_bounds__(kRopeThreads)
   const int j = w.piece();
   const int h0 = blockIdx.y * hpt, h1 = min(h0 + hpt, Hq + Hk);
   RopeTable<1> &table = tables[threadIdx.x / 32];
+  pdl_wait();
   table.fill(rp);
   if (w.token() >= w.tokens) return;
   const RopeRows<E> at(q, k, Hq, w.token(), w.T);
@@ -451,18 +454,16 @@ cudaError_t launch_rope(const RopeTensor &q, const RopeTensor &k, const RopePara
   const int hpt = heads_per_thread((long long)w.tokens * units, Hq + Hk, 16);
   const int run = kRopeThreads >> w.shift;
   const dim3 grid((unsigned)(((int64_t)w.tokens + run - 1) / run), (unsigned)((Hq + Hk + hpt - 1) / hpt));
-#define DA_ROPE_UNITS(E, BATCH)                                                                      \
-  adjacent ? rope_kernel<E, true, BATCH><<<grid, kRopeThreads, 0, stream>>>(q, k, rp, w, Hq, Hk, hpt) \
-           : rope_kernel<E, false, BATCH><<<grid, kRopeThreads, 0, stream>>>(q, k, rp, w, Hq, Hk, hpt)
-#define DA_ROPE(E)                                                                                   \
-  if (path == kRopeAny)                                                                              \
-    rope_any_kernel<E><<<grid, kRopeThreads, 0, stream>>>(q, k, rp, w, Hq, Hk, hpt);                 \
-  else if (path == kRopeScalar)                                                                      \
-    rope_scalar_kernel<E><<<grid, kRopeThreads, 0, stream>>>(q, k, rp, adjacent, w, Hq, Hk, hpt);    \
-  else if (hpt > 2)                                                                                  \
-    DA_ROPE_UNITS(E, kRopeBatch);                                                                    \
-  else                                                                                               \
-    DA_ROPE_UNITS(E, kFewBatch);
+#define DA_ROPE_UNITS(E, BATCH)                                                                                 \
+  adjacent ? launch_after(rope_kernel<E, true, BATCH>, grid, kRopeThreads, 0, stream, q, k, rp, w, Hq, Hk, hpt) \
+           : launch_after(rope_kernel<E, false, BATCH>, grid, kRopeThreads, 0, stream, q, k, rp, w, Hq, Hk, hpt)
+#define DA_ROPE(E)                                                                                              \
+  if (path == kRopeAny)                                                                                         \
+    return launch_after(rope_any_kernel<E>, grid, kRopeThreads, 0, stream, q, k, rp, w, Hq, Hk, hpt);           \
+  if (path == kRopeScalar)                                                                                      \
+    return launch_after(rope_scalar_kernel<E>, grid, kRopeThreads, 0, stream, q, k, rp, (int)adjacent, w, Hq,   \
+                        Hk, hpt);                                                                               \
+  return hpt > 2 ? DA_ROPE_UNITS(E, kRopeBatch) : DA_ROPE_UNITS(E, kFewBatch);
   if (dtype == DA_BF16) {
     DA_ROPE(__nv_bfloat16)
   } else {
@@ -470,7 +471,6 @@ cudaError_t launch_rope(const RopeTensor &q, const RopeTensor &k, const RopePara
   }
 #undef DA_ROPE
 #undef DA_ROPE_UNITS
-  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -512,8 +512,8 @@ __device__ __forceinline__ TokenPlace place_token(int n, const int32_t *cu, cons
   const long long pg = pos / c.page_size;
   bool ok = first >= 0 && first <= n && n < end && end <= a.N && pos >= 0 && end - first <= len && pg < c.max_pages;
   if (ok) {
-    p.page = __ldg(c.page_table + (size_t)lo * c.max_pages + pg);
-    p.dpage = __ldg(c.demand_table + (size_t)lo * c.max_pages + pg);
+    p.page = __ldcg(c.page_table + (size_t)lo * c.max_pages + pg);
+    p.dpage = __ldcg(c.demand_table + (size_t)lo * c.max_pages + pg);
     ok = p.page >= 0 && p.page < c.num_pages && p.dpage >= 0 && p.dpage < c.num_demand_pages;
   }
   if (ok)
@@ -560,6 +560,7 @@ __global__ void __launch_bounds__(kRopeThreads)
         vb[j] = ld_once(src + ru.vb);
       }
   };
+  pdl_wait();
   if constexpr (VEC) {
     ru.place(u, h0 < h_turn ? rp.n_pairs : 0);
     if (mine && tt0 < last) load(tt0, h0);
@@ -568,8 +569,8 @@ __global__ void __launch_bounds__(kRopeThreads)
   const int32_t *cu = a.cu_tokens, *lens = c.seq_lens;
   if (c.S + 1 <= kAppendSearch) {
     for (int i = threadIdx.x; i <= c.S; i += kRopeThreads) {
-      s_cu[i] = __ldg(a.cu_tokens + i);
-      if (i < c.S) s_len[i] = __ldg(c.seq_lens + i);
+      s_cu[i] = __ldcg(a.cu_tokens + i);
+      if (i < c.S) s_len[i] = __ldcg(c.seq_lens + i);
     }
     cu = s_cu;
     lens = s_len;
@@ -642,20 +643,14 @@ cudaError_t launch_append(const AppendArgs &args, const dilution_attn_paged_cach
   if (turns > kRopeThreads / step) turns = kRopeThreads / step;
   a.tokens = step * (int)(turns < 1 ? 1 : turns);
   const dim3 grid((unsigned)((a.N + a.tokens - 1) / a.tokens), (unsigned)heads);
-#define DA_APPEND(E, ADJ, VEC) append_kernel<E, ADJ, VEC><<<grid, kRopeThreads, 0, stream>>>(a, c, rp)
+#define DA_APPEND(E, ADJ, VEC) launch_after(append_kernel<E, ADJ, VEC>, grid, kRopeThreads, 0, stream, a, c, rp)
   if (c.dtype == DA_BF16) {
-    if (vec)
-      a.adjacent ? DA_APPEND(__nv_bfloat16, true, true) : DA_APPEND(__nv_bfloat16, false, true);
-    else
-      a.adjacent ? DA_APPEND(__nv_bfloat16, true, false) : DA_APPEND(__nv_bfloat16, false, false);
-  } else {
-    if (vec)
-      a.adjacent ? DA_APPEND(float, true, true) : DA_APPEND(float, false, true);
-    else
-      a.adjacent ? DA_APPEND(float, true, false) : DA_APPEND(float, false, false);
+    if (vec) return a.adjacent ? DA_APPEND(__nv_bfloat16, true, true) : DA_APPEND(__nv_bfloat16, false, true);
+    return a.adjacent ? DA_APPEND(__nv_bfloat16, true, false) : DA_APPEND(__nv_bfloat16, false, false);
   }
+  if (vec) return a.adjacent ? DA_APPEND(float, true, true) : DA_APPEND(float, false, true);
+  return a.adjacent ? DA_APPEND(float, true, false) : DA_APPEND(float, false, false);
 #undef DA_APPEND
-  return cudaGetLastError();
 }
 
 }  // namespace da

@@ -405,3 +405,79 @@ def test_captured_append_and_decode_step():
         assert b.dilution_attn_get_error(ws) == b.DA_OK
         assert torch.equal(qn, qc) and torch.equal(cache.k_pages, copy.k_pages)
         check_step(cache, qn, before, out, ref)
+
+
+@pytest.mark.parametrize("cap", [200, 2600])      # one kernel, and the kernels for long caches
+def test_fork_and_join_around_the_calls(cap):
+    """Lengths, queries and new keys made by other kernels just before each call, on a
+    forked stream and on the call's own, run eagerly and as a captured graph."""
+    S, H, d, page = 5, 4, 64, 32
+    cache, _, _ = make_cache(S, [100, 31, 64, 1, 150], H, 2, d, page, "bf16", seed=23)
+    start = torch.tensor([90, 20, 50, 0, 140], dtype=torch.int32, device=DEV)
+    spec, inv, pa = spec_of(32, 1, False)
+    cu = torch.arange(S + 1, dtype=torch.int32, device=DEV)
+    src = torch.randn(S, H + 4, d, device=DEV).bfloat16()
+    new = torch.zeros_like(src)
+    ws = b.dilution_attn_paged_decode_workspace(cache, cap)
+    ws2 = b.dilution_attn_paged_append_workspace(cache)
+    qn, out = torch.empty(2, S, H, d, dtype=torch.bfloat16, device=DEV).unbind(0)
+    pools = [x.clone() for x in (cache.k_pages, cache.v_pages, cache.demand_pages)]
+    work, work2 = torch.zeros(2, 1 << 22, device=DEV).unbind(0)
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        work.add_(1.0)                                   # something long before the writes below
+        cache.seq_lens.add_(1)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            work.mul_(0.5)
+            new.copy_(src)
+            new.mul_(2.0)
+            b.dilution_attn_paged_append(new[:, :H], new[:, H:H + 2], new[:, H + 2:], cache, cu, qn, rope=spec, workspace=ws2)
+        work2.sub_(1.0)
+        main.wait_stream(side)
+        b.dilution_attn_paged_decode(qn, cache, cap, out, workspace=ws)
+
+    def reset():
+        for x, y in zip((cache.k_pages, cache.v_pages, cache.demand_pages), pools):
+            x.copy_(y)
+        cache.seq_lens.copy_(start)
+
+    def expect(steps):
+        """The same steps one at a time, each against the oracle."""
+        reset()
+        outs = []
+        for _ in range(steps):
+            cache.seq_lens.add_(1)
+            two = src * 2
+            torch.cuda.synchronize()
+            q = b.dilution_attn_paged_append(two[:, :H], two[:, H:H + 2], two[:, H + 2:], cache, cu, rope=spec)
+            torch.cuda.synchronize()
+            before, ref = cache.demand_pages.clone(), oracle_step(cache, q)
+            torch.cuda.synchronize()
+            o = b.dilution_attn_paged_decode(q, cache, cap)
+            torch.cuda.synchronize()
+            check_step(cache, q, before, o, ref)
+            outs.append(o)
+        return outs[-1], cache.demand_pages.clone()
+
+    want, demand = expect(8)
+    reset()
+    for _ in range(8):
+        step()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(cache.demand_pages, demand)
+    reset()
+    capture = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=capture):
+        step()
+    reset()
+    out.zero_()
+    for _ in range(8):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(cache.demand_pages, demand)
+    assert b.dilution_attn_get_error(ws) == b.DA_OK and b.dilution_attn_get_error(ws2) == b.DA_OK
