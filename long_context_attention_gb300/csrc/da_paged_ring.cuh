@@ -54,8 +54,11 @@ __device__ __forceinline__ void drain(uint64_t *full, int stages, int issued) {
 // dependent instruction every 5 cycles, and a tile has 0.7 us at HBM rate, so
 // the loop is short: no divisions, one table entry per lane, fetched a tile
 // ahead.
-// A tile is TILE rows of 16384 / TILE bytes; XSTEP: elements in 128 bytes.
-template <int TILE, int XSTEP>
+// A tile is TILE rows of 16384 / TILE bytes; XSTEP: elements in 128 bytes.  AFTER_WAIT:
+// the kernel has waited for its predecessor (see launch_after).  Otherwise its
+// consumers wait before they free a slot, so that from the second round on entries
+// may come from L1 (all from L2: 531 us for 8 x 12 x 131072, so 519).
+template <int TILE, int XSTEP, bool AFTER_WAIT>
 __device__ void produce(const PagedDecode &p, const PgtPlan &w, const PgtLine &line, const PgtLens &L, PgtRing &ring,
                         const CUtensorMap *map, uint32_t base, int stages, int from, int to, const WaitCtx &wc) {
   constexpr int BOXES = kStageBytes / (TILE * 128);
@@ -69,9 +72,10 @@ __device__ void produce(const PagedDecode &p, const PgtPlan &w, const PgtLine &l
     const int32_t *table = g.s >= 0 ? p.c.page_table + (size_t)g.s * p.c.max_pages : p.prefix_table;
     int key = g.key0 + lane * rows;                                   // this lane's piece
     const int limit = lane * rows < TILE ? g.end : 0;                 // lanes past the tile bring nothing
-    int page = key < limit ? __ldcg(table + (key >> sh)) : -1;
+    auto entry = [&](int at, bool l1) { return l1 ? table[at >> sh] : __ldcg(table + (at >> sh)); };
+    int page = key < limit ? entry(key, AFTER_WAIT) : -1;
     for (int k = 0; k < g.n; ++k, ++issued) {
-      const int ahead = k + 1 < g.n && key + TILE < limit ? __ldcg(table + ((key + TILE) >> sh)) : -1;
+      const int ahead = k + 1 < g.n && key + TILE < limit ? entry(key + TILE, AFTER_WAIT || issued > stages) : -1;
       if (!warp_wait(&ring.empty[slot], parity, wc)) {
         if (lane == 0) drain(ring.full, stages, issued);
         return;

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
   const WaitCtx wc{&ring.abort_word, p.status};
   const uint32_t base = smem_u32(pgt_smem_base());
   if (warp == WARPS) {
-    produce<pgt_tile(D), 64>(p, w, line, L, ring, &kmap, base, stages, from, to, wc);
+    produce<pgt_tile(D), 64, true>(p, w, line, L, ring, &kmap, base, stages, from, to, wc);
     return;
   }
   const int gid = lane / 4, t = lane % 4;
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
   uint8_t *const smem = pgt_smem_base();
   const uint32_t base = smem_u32(smem);
   if (warp == WARPS) {   // the values do not depend on the first pass
-    produce<pgt_tile(D), 64>(p, w, line, L, ring, &vmap, base, V::kStages, from, to, wc);
+    produce<pgt_tile(D), 64, false>(p, w, line, L, ring, &vmap, base, V::kStages, from, to, wc);
     return;
   }
   uint8_t *const mine = smem + V::kStages * 16384 + warp * V::kWarpBytes;
@@ -273,10 +273,10 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
       dtab[hh] = p.c.demand_table + (size_t)s * p.c.max_pages;
       dpool[hh] = p.c.demand_pages + ((size_t)hq << sh);
     }
-    auto demand_page = [&](int k, int hh) -> int {     // of the lane's keys of step k
+    auto demand_page = [&](int k, int hh, bool after_wait) -> int {   // of the lane's keys of step k
       const int key = key0 + k * STRIDE;
       const int32_t *at = dtab[hh] + (key >> sh);
-      return on[hh] && k < steps && key < g.end ? (waited ? *at : __ldcg(at)) : -1;
+      return on[hh] && k < steps && key < g.end ? (after_wait ? *at : __ldcg(at)) : -1;
     };
     auto demand_at = [&](int k, int hh, int pg) -> float * {
       return dpool[hh] + (size_t)pg * page_floats + ((key0 + k * STRIDE) & (ps - 1));
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
 #pragma unroll
     for (int a = 0; a < AHEAD; ++a)
 #pragma unroll
-      for (int hh = 0; hh < HH; ++hh) pages[a][hh] = demand_page(a, hh);
+      for (int hh = 0; hh < HH; ++hh) pages[a][hh] = demand_page(a, hh, waited);
     if (!waited) {   // the demand does not depend on the first pass: to L2 meanwhile
 #pragma unroll
       for (int a = 0; a < AHEAD - 1; ++a)
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
     for (int k = 0; k < steps; ++k) {
       bring(k + AHEAD - 1, pages[AHEAD - 1]);
 #pragma unroll
-      for (int hh = 0; hh < HH; ++hh) pages[AHEAD][hh] = demand_page(k + AHEAD, hh);
+      for (int hh = 0; hh < HH; ++hh) pages[AHEAD][hh] = demand_page(k + AHEAD, hh, true);
       asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");   // step k's have landed
       const int left = g.end - (step0 + k * STRIDE);     // keys of the step before the end
       const int valid = left - 16 * q - 4 * t;           // of the lane's four

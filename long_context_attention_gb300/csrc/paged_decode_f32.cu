@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
   const WaitCtx wc{&ring.abort_word, p.status};
   uint8_t *const smem = pgt_smem_base();
   if (warp == kPgfWarps) {
-    produce<TILE, 32>(p, w, line, L, ring, &kmap, smem_u32(smem), STAGES, from, to, wc);
+    produce<TILE, 32, true>(p, w, line, L, ring, &kmap, smem_u32(smem), STAGES, from, to, wc);
     return;
   }
   const int sub = warp % T::kPerTile * 32, kl = lane % B::kKeyLanes, rl = lane / B::kKeyLanes;
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
   const WaitCtx wc{&ring.abort_word, p.status};
   uint8_t *const smem = pgt_smem_base();
   if (warp == kPgfWarps) {   // the values do not depend on the first pass
-    produce<TILE, 32>(p, w, line, L, ring, &vmap, smem_u32(smem), V::kStages, from, to, wc);
+    produce<TILE, 32, false>(p, w, line, L, ring, &vmap, smem_u32(smem), V::kStages, from, to, wc);
     return;
   }
   uint8_t *const base = smem + V::kStages * kStageBytes;
@@ -250,10 +250,10 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
       dtab[i] = p.c.demand_table + (size_t)s * p.c.max_pages;
       dpool[i] = p.c.demand_pages + ((size_t)hq << sh);
     }
-    auto demand_page = [&](int k, int i) -> int {
+    auto demand_page = [&](int k, int i, bool after_wait) -> int {
       const int key = step0 + k * STRIDE + pk;
       const int32_t *at = dtab[i] + (key >> sh);
-      return on[i] && k < steps && key < g.end ? (waited ? *at : __ldcg(at)) : -1;
+      return on[i] && k < steps && key < g.end ? (after_wait ? *at : __ldcg(at)) : -1;
     };
     auto bring = [&](int k, const int (&pg)[PIECES]) {
       float *x = mine + (k & 1) * (2 * R * 32);
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
 #pragma unroll
     for (int a = 0; a < 2; ++a)
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i) pages[a][i] = demand_page(a, i);
+      for (int i = 0; i < PIECES; ++i) pages[a][i] = demand_page(a, i, waited);
     if (!waited) {   // the demand does not depend on the first pass: to L2 meanwhile
 #pragma unroll
       for (int i = 0; i < PIECES; ++i)
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
       bring(k + 1, pages[1]);
       int next[PIECES];
 #pragma unroll
-      for (int i = 0; i < PIECES; ++i) next[i] = demand_page(k + 2, i);
+      for (int i = 0; i < PIECES; ++i) next[i] = demand_page(k + 2, i, true);
       asm volatile("cp.async.wait_group 1;" ::: "memory");   // step k's have landed
       __syncwarp();
       float *x = mine + (k & 1) * (2 * R * 32), *dm = x + R * 32;
