@@ -18,11 +18,11 @@
 // What bounds it: bytes.  Each element is read once and written once; sin and
 // cos are computed in registers for one token and 16 bytes of a head's row and
 // serve `hpt` heads in turn, so they are a small part of the instructions (of two
-// heads they are most of them: 4 x 36238 tokens of 2 x 128 bf16 take 39.8 us, the
+// heads they are most of them: 4 x 36238 tokens of 2 x 128 bf16 take 37.2 us, the
 // bytes 22).  The loads of several heads are issued together before the first
 // store: an output may be its input, so the compiler cannot move a load over a
 // store by itself (one head at a time kept 32 bytes a thread in flight: 4.9 TB/s at
-// 4 x 24 x 16384 x 64 bf16; now 5.9, and 6.7 at 24 x 131072 x 128 fp32).
+// 4 x 24 x 16384 x 64 bf16; now 6.3, and 6.8 at 24 x 131072 x 128 fp32).
 #include "da_rope.h"
 #include "da_ptx.cuh"
 
