@@ -35,7 +35,7 @@
 // Roles: warps 0-15 demand, then a warp each for K copies, V copies, MMA issue
 // and the demand-page table of the next tiles.  Waits are bounded; rows of
 // missing or invalid pages are filled with zeros by reading past the pool's end;
-// a key past the prefix's end has eps = infinity and so no share.
+// a key past the prefix's end has the logit -infinity, and so no bid and no share.
 #include "da_paged_plan.cuh"
 
 #include <cuda.h>
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
       for (int k = k0; ok && k < n; k += 2) {
         const int t = it.c.run + k;
         const bool more = k + 2 < n;
-        // a key past the prefix's end gets no share
+        // infinity: a key past the prefix's end, which bids nothing
         const float eps = (it.c.tile + k) * kPgxTile + key_l < p.prefix_len ? p.eps : INFINITY;
         const float2 eps2 = make_float2(eps, eps);
         ok = !more || warp_wait(&tab_full[(t + 2) & 3], ((t + 2) >> 2) & 1, wc);
@@ -655,6 +655,12 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
             __syncwarp();                                        // .. those of every lane
             tmem_wait_ld_r8(x);
             if (c == groups - 1) x_release(&s_free[g], lane);    // the next tile's S may be formed
+            // A place past the prefix's end has the logit 0 of a row of zeros: where all of a
+            // query's logits lie below -89 its bid would be 2^128 and its share infinity x 0.
+            if (__any_sync(0xffffffffu, eps == INFINITY)) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = eps == INFINITY ? -INFINITY : x[e];
+            }
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {

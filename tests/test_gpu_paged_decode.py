@@ -153,6 +153,38 @@ def test_long_prefix_reports_bad_pages_and_repeats_its_bits(d, S, Hq, Hkv, page,
     assert torch.equal(run()[0], good)
 
 
+# Prefixes that end inside a tile of the kernels that take many rows at once.
+@pytest.mark.parametrize("flags", [0, b.DA_FLAG_EARLIER_DEMAND_ONLY])
+@pytest.mark.parametrize("page,prefix", [(16, 26256), (32, 26272), (64, 26304)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_prefix_whose_logits_lie_far_below_zero(d, page, prefix, flags):
+    # a strong common component of the keys, which the queries oppose: every logit is near -150.  A softmax does not
+    # depend on the offset, so the bids are ordinary; 2^(0 - lse2) of a place without a key is not.
+    S, Hq, Hkv = 20, 8, 2
+    lens = [prefix + 1 + i for i in range(S)]
+    cache, q, pt = make_cache(S, lens, Hq, Hkv, d, page, "bf16", seed=d + page, prefix=prefix)
+    g = torch.Generator(device=DEV).manual_seed(prefix)
+    u = torch.randint(0, 2, (d,), generator=g, device=DEV) * 2.0 - 1.0
+    cache.k_pages.copy_(4.0 * u + 0.3 * torch.randn(cache.k_pages.shape, generator=g, device=DEV))
+    q.copy_(-150.0 / (4.0 * d ** 0.5) * u * (1.0 + 0.05 * torch.rand(q.shape, generator=g, device=DEV)))
+    before = cache.demand_pages.clone()
+    ws = b.dilution_attn_paged_decode_workspace(cache, max(lens), prefix // page)
+    out = b.dilution_attn_paged_decode(q, cache, max(lens), prefix_table=pt, workspace=ws, flags=flags, eps=1e-4)
+    assert b.dilution_attn_get_error(ws) == b.DA_OK
+    assert out.isfinite().all() and cache.demand_pages.isfinite().all()
+    for h, rows in ((0, [0, 7]), (Hq - 1, [S - 1])):
+        kv = h // (Hq // Hkv)
+        one = b.PagedCache(cache.k_pages[:, kv:kv + 1].contiguous(), cache.v_pages[:, kv:kv + 1].contiguous(),
+                           before[:, h:h + 1].contiguous(), cache.page_table[rows].contiguous(),
+                           cache.demand_table[rows].contiguous(), cache.seq_lens[rows].contiguous())
+        ref = oracle_step(one, q[rows, h:h + 1], eps=1e-4, earlier=bool(flags))
+        mine = torch.zeros(one.demand_pages.shape[0], dtype=torch.bool, device=DEV)
+        mine[one.demand_table[one.demand_table >= 0].long()] = True
+        old = one.demand_pages.clone()
+        one.demand_pages[mine] = cache.demand_pages[mine, h:h + 1]
+        check_step(one, q[rows, h:h + 1], old, out[rows, h:h + 1], ref)
+
+
 def test_more_sequences_than_one_part():
     lens = [64 + i % 3 for i in range(900)]
     cache, q, pt = make_cache(900, lens, 1, 1, 64, 16, "bf16", seed=98, prefix=64)
