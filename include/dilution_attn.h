@@ -299,7 +299,9 @@ typedef struct dilution_attn_rope_spec {
  * strides may be 0 (a head or batch entry read several times).  Outputs must
  * not address an element twice (their strides, sorted, must each step over
  * the extent below; else DA_ERR_INVALID).  An output may be its own input
- * (same pointer and strides); other overlaps are not allowed.
+ * (same pointer and strides); other overlaps are not allowed (an output at an
+ * input's pointer with other strides, or at another operand's pointer, is
+ * DA_ERR_INVALID; the rest is not checked).
  * positions: DEVICE int32 [n_axes][pos_batch][T], pos_batch 1 (every batch
  * entry alike) or B; negative positions are valid.
  * spec is a HOST struct, read during the call.  No workspace.  Errors as for
@@ -375,7 +377,8 @@ typedef struct dilution_attn_paged_cache {
  * (token, head) or NULL for contiguous; demand fp32 [N,Hq] likewise.
  * cu_tokens: DEVICE [S+1] int32, starting at 0 and not decreasing; tokens from
  * cu_tokens[S] on are padding: their values are not used, their rows of q_out
- * not written.  q_out may be q itself (then contiguous).
+ * not written.  q_out may be q itself (then contiguous); a q_out that lies over
+ * rows of q, k, v or demand in any other way is DA_ERR_INVALID.
  * spec: NULL appends k and q unrotated.  positions: DEVICE [n_axes][N], or NULL
  * for the token's place in its sequence on every axis.
  * workspace: 256 bytes (dilution_attn_paged_append_workspace_size()). */

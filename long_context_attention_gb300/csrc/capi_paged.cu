@@ -76,6 +76,20 @@ bool strides_sane(const long long *strides, int n) {
   return true;
 }
 
+// Whether one of n x h rows of row_bytes bytes, at byte strides step (n) and
+// head (h), meets the bytes [lo, hi).
+bool rows_meet(const void *p, long long n, long long step, int h, long long head, long long row_bytes, const void *lo_,
+               long long len) {
+  const long long at = (long long)reinterpret_cast<uintptr_t>(p), lo = (long long)reinterpret_cast<uintptr_t>(lo_);
+  if (at >= lo + len || at + (n - 1) * step + (h - 1) * head + row_bytes <= lo) return false;
+  for (int i = 0; i < h; ++i) {
+    const long long row = at + i * head, gap = lo - (row + row_bytes);   // the first row that ends behind lo
+    const long long t = gap < 0 ? 0 : step > 0 ? gap / step + 1 : n;
+    if (t < n && row + t * step < lo + len) return true;
+  }
+  return false;
+}
+
 int rope_call(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides, void *q_out,
               const int64_t *q_out_strides, void *k_out, const int64_t *k_out_strides, const int32_t *positions,
               int pos_batch, const dilution_attn_rope_spec *spec, int B, int Hq, int Hk, int T, int d, int dtype,
@@ -111,9 +125,13 @@ int rope_call(const void *q, const int64_t *q_strides, const void *k, const int6
       so[j] = os[i] != nullptr ? os[i][j] : dense[j];
     }
     if (!strides_sane(si, 3) || !strides_sane(so, 3) || !distinct(so, ext, 3, d)) return DA_ERR_INVALID;
+    if (out[i] == in[i])   // in place: every row where it was
+      for (int j = 0; j < 3; ++j)
+        if (ext[j] > 1 && si[j] != so[j]) return DA_ERR_INVALID;
     vec = vec && pieces_ok(in[i], si, ext, 3, dtype) && pieces_ok(out[i], so, ext, 3, dtype);
     t[i] = RopeTensor{in[i], out[i], si[0], si[1], si[2], so[0], so[1], so[2]};
   }
+  if (Hq > 0 && Hk > 0 && (q_out == k_out || q_out == k || k_out == q)) return DA_ERR_INVALID;
   const RopePath path = !vec ? kRopeScalar : pairs_ok(rp.n_pairs, spec->adjacent, dtype) ? kRopeUnits : kRopeAny;
   return launch_rope(t[0], t[1], rp, spec->adjacent != 0, path, B, Hq, Hk, T, d, dtype,
                      reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -212,6 +230,13 @@ int dilution_attn_paged_append(const void *q, const int64_t *q_strides, const vo
   const long long ds[2] = {demand_strides != nullptr ? demand_strides[0] : c.Hq,
                            demand_strides != nullptr ? demand_strides[1] : 1};
   if (!strides_sane(ds, 2)) return DA_ERR_INVALID;
+  if (q_out != nullptr) {   // what is still to be read: q_out may be a contiguous q, and lies over nothing else
+    const long long len = (long long)N * c.Hq * c.d * eb;
+    const bool dense = (N == 1 || s[0][0] == (long long)c.Hq * c.d) && (c.Hq == 1 || s[0][1] == c.d);
+    for (int i = q_out == q && dense ? 1 : 0; i < 3; ++i)
+      if (rows_meet(in[i], N, s[i][0] * eb, H[i], s[i][1] * eb, (long long)c.d * eb, q_out, len)) return DA_ERR_INVALID;
+    if (demand != nullptr && rows_meet(demand, N, ds[0] * 4, c.Hq, ds[1] * 4, 4, q_out, len)) return DA_ERR_INVALID;
+  }
   a.q = q, a.k = k, a.v = v, a.demand = demand, a.q_out = q_out, a.cu_tokens = cu_tokens;
   a.q_t = s[0][0], a.q_h = s[0][1], a.k_t = s[1][0], a.k_h = s[1][1], a.v_t = s[2][0], a.v_h = s[2][1];
   a.dem_t = ds[0], a.dem_h = ds[1];

@@ -272,6 +272,28 @@ def test_append_turns_queries_in_place(dtype, n):
     close(q, rows[:, :4], op.rope_angles(cache.seq_lens.cpu().numpy()[None] - 1, inv.cpu().numpy(), pa)[:, None], False)
 
 
+def test_append_queries_between_the_rows_of_the_keys():
+    # q_out inside the range of the strided keys and values, over none of their rows
+    cache, _, _ = make_cache(3, [9, 40, 70], 2, 2, 64, 16, "bf16", seed=17)
+    spec, inv, pa = spec_of(32, 1, False)
+    buf = torch.randn(3, 2048, generator=torch.Generator().manual_seed(5)).bfloat16().to(DEV)
+    k, v = buf[:, :128].unflatten(-1, (2, 64)), buf[:, 1024:1152].unflatten(-1, (2, 64))
+    q, q_out = torch.randn(3, 2, 64, device=DEV).bfloat16(), buf[1, 512:896].view(3, 2, 64)
+    kept = buf.clone()
+    cu = torch.arange(4, dtype=torch.int32, device=DEV)
+    ang = op.rope_angles(cache.seq_lens.cpu().numpy()[None] - 1, inv.cpu().numpy(), pa)[:, None]
+    assert b.dilution_attn_paged_append(q, k, v, cache, cu, q_out, rope=spec) is q_out
+    close(q_out, q, ang, False)
+    at = (cache.seq_lens - 1).long()
+    pg = cache.page_table[torch.arange(3, device=DEV), at // 16].long()
+    close(cache.k_pages[pg, :, at % 16], k, ang, False)
+    assert torch.equal(cache.v_pages[pg, :, at % 16], v)
+    kept[1, 512:896] = buf[1, 512:896]
+    assert torch.equal(buf, kept)
+    with pytest.raises(b.DilutionAttnError):                  # over the second token's keys
+        b.dilution_attn_paged_append(q, k, v, cache, cu, buf[1, 64:448].view(3, 2, 64), rope=spec)
+
+
 def test_append_many_sequences():
     # more sequences than the search holds in shared memory, one token each
     S = 1500

@@ -130,6 +130,41 @@ def test_decode_refusals(lib):
     assert call(cache(S=0), q=None) == b.DA_OK
 
 
+def test_outputs_that_lie_over_inputs_are_refused(lib):
+    """Rows written by one block that another still has to read: an output at an input's address with other strides,
+    or at another operand's address."""
+    def rope(q=FAKE, k=FAKE << 4, qo=FAKE << 5, ko=FAKE << 6, qs=None, ks=None, qos=None):
+        arr = lambda x: None if x is None else (ctypes.c_int64 * 3)(*x)
+        return lib.dilution_attn_rope(q, arr(qs), k, arr(ks), qo, arr(qos), ko, None, FAKE, 1, ctypes.byref(spec()), 2,
+                                      2, 2, 8, 64, 1, None)
+    fused = (8 * 256, 64, 256)                                # [B, T, 4 heads of 64]
+    assert rope(qo=FAKE, qs=fused) == b.DA_ERR_INVALID        # a projection's queries, turned into its first half
+    assert rope(qo=FAKE, qos=fused) == b.DA_ERR_INVALID
+    assert rope(ko=FAKE << 4, ks=fused) == b.DA_ERR_INVALID
+    assert rope(qo=FAKE, qs=(1024, 0, 64)) == b.DA_ERR_INVALID   # a head read twice, written in place
+    assert rope(ko=FAKE << 5) == b.DA_ERR_INVALID             # both outputs in one place
+    assert rope(qo=FAKE << 4) == b.DA_ERR_INVALID             # the queries over the keys
+    assert rope(ko=FAKE) == b.DA_ERR_INVALID
+
+    def append(q=FAKE, k=FAKE << 4, v=FAKE << 5, qo=FAKE, qs=None, ks=None, dem=None):
+        arr = lambda x: None if x is None else (ctypes.c_int64 * 2)(*x)
+        c = cache()
+        return lib.dilution_attn_paged_append(q, arr(qs), k, arr(ks), v, None, dem, None, qo, FAKE, 4, ctypes.byref(c),
+                                              None, None, FAKE, 256, None)
+    assert append(qs=(8 * 64, 64)) == b.DA_ERR_INVALID                  # the first heads of a projection of 8
+    assert append(qs=(4 * 64, 128)) == b.DA_ERR_INVALID
+    assert append(qs=(0, 64)) == b.DA_ERR_INVALID
+    assert append(qo=FAKE << 4) == b.DA_ERR_INVALID
+    assert append(qo=FAKE << 5) == b.DA_ERR_INVALID
+    row, n = 8 * 64 * 2, 4 * 4 * 64 * 2                                 # bytes of a projection's row and of q_out
+    at = FAKE << 4
+    assert append(qo=at + row, ks=(8 * 64, 64)) == b.DA_ERR_INVALID     # over the second token's keys
+    assert append(qo=at + 3 * row + 2 * 128 - 16, ks=(8 * 64, 64)) == b.DA_ERR_INVALID   # the end of the last one
+    assert append(qo=at - n + 16) == b.DA_ERR_INVALID                   # the beginning of the first
+    assert append(q=FAKE, qo=FAKE + 1024) == b.DA_ERR_INVALID           # one token further on
+    assert append(dem=FAKE << 6, qo=(FAKE << 6) + 32) == b.DA_ERR_INVALID
+
+
 def test_workspace_sizes_grow(lib):
     size = b.dilution_attn_paged_decode_workspace_size
     assert size(4, 8, 2, 64, 1000, 0, 16, 1) > 256
