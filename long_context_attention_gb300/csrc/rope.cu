@@ -6,10 +6,12 @@
 // theta = n * inv_freq_j radians.  Only theta modulo one turn matters, so the
 // frequency is held in turns per position as a 64-bit fixed-point fraction
 //     F = inv_freq_j / (2 pi) * 2^64  mod 2^64:
-// the 24-bit mantissa of inv_freq_j times the first 64 bits of 1 / (2 pi),
-// shifted by the exponent, within one unit.  n * F mod 2^64 is then the angle to
-// n 2^-64 turns, of which the upper 32 bits (2^-33 turns, 7e-10 radians, below
-// fp32's rounding of the cosine) go to sine and cosine, formed from their series.
+// the 24-bit mantissa of inv_freq_j times the first 96 bits of 1 / (2 pi),
+// shifted by the exponent, within 1.01 units for every |inv_freq_j| < 2^24 (with the
+// first 64 bits alone within inv_freq_j / 2 units: 2^24 - 1 at position 2^31 was off by
+// 6e-3 radians).  n * F mod 2^64 is then the angle to n 2^-64 turns, of which the upper
+// 32 bits (to 2^-32 turns, 1.5e-9 radians, below fp32's rounding of the cosine) go to
+// sine and cosine, formed from their series.
 // No fp64 (GB300 has few fp64 units), no long fp32 products; 32-bit multiplies and
 // funnel shifts (a version in 64-bit operations cost 140 instructions a pair and
 // bounded the append).  The products x cos - y sin run in fp32 and round once to the output's
@@ -33,7 +35,7 @@ namespace da {
 // inv_freq in turns per position, times 2^64 modulo 2^64 (hi, lo).  Frequencies
 // of magnitude 2^24 and above, infinities and NaN give ok = false.
 __device__ __forceinline__ uint2 turns_fixed(float f, bool &ok) {
-  constexpr uint32_t kHi = 0x28BE60DBu, kLo = 0x9391054Au;   // floor(2^64 / (2 pi))
+  constexpr uint32_t kHi = 0x28BE60DBu, kMid = 0x9391054Au, kLo = 0x7F09D5F4u;   // floor(2^96 / (2 pi))
   const uint32_t u = __float_as_uint(f);
   int e = (int)((u >> 23) & 0xffu);
   uint32_t m = u & 0x7fffffu;
@@ -43,8 +45,9 @@ __device__ __forceinline__ uint2 turns_fixed(float f, bool &ok) {
     m |= 0x800000u;
   const int shift = 150 - e;   // |f| = m 2^-shift
   ok = shift >= 0;
-  // the 86-bit product, least word first
-  const unsigned long long p0 = (unsigned long long)m * kLo, p1 = (unsigned long long)m * kHi + (p0 >> 32);
+  // the 118-bit product without its lowest word, least word first
+  const unsigned long long p0 = (unsigned long long)m * kMid + (((unsigned long long)m * kLo) >> 32);
+  const unsigned long long p1 = (unsigned long long)m * kHi + (p0 >> 32);
   const uint32_t w0 = (uint32_t)p0, w1 = (uint32_t)p1, w2 = (uint32_t)(p1 >> 32);
   // bits shift .. shift + 63 of it
   const int words = shift >> 5;

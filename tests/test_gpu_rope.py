@@ -130,6 +130,20 @@ def test_rope_far_positions(far):
     close(qo, x, ang, False)
 
 
+@pytest.mark.parametrize("adjacent", [False, True])
+def test_rope_high_frequencies_at_far_positions(adjacent):
+    # every frequency and position that is taken keeps the angle: references in exact integer arithmetic
+    from fractions import Fraction
+    inv = torch.tensor([2.0 ** 24 - 1, -(2.0 ** 24 - 1), 2.0 ** 20, 12345678.0, 1234.5, 6.2831855, 1.0, 1e-30], device=DEV)
+    pos = torch.tensor([[(1 << 31) - 1, -(1 << 31), 1 << 24, (1 << 30) + 12345, -1, 1]], dtype=torch.int32, device=DEV)
+    pi2 = Fraction(31415926535897932384626433832795028841971693993751, 5 * 10 ** 48)
+    ang = np.array([[float(Fraction(int(p)) * Fraction(float(f)) % pi2) for f in inv.cpu().numpy()] for p in pos[0].tolist()])
+    x = torch.randn(1, 2, 6, 64, generator=torch.Generator().manual_seed(9)).to(DEV)
+    spec = b.rope_spec(inv, adjacent=adjacent)
+    close(b.dilution_attn_rope(x, None, pos, spec)[0], x, ang, adjacent)
+    close(b.dilution_attn_rope_bwd(x, None, pos, spec)[0], x, ang, adjacent, back=True)
+
+
 def test_rope_gradient_against_differences():
     # the map is linear: a central difference of sum(w rope(x)) is exact up to fp32 rounding
     spec, _, _ = spec_of(32, 2, False)
