@@ -410,13 +410,23 @@ int dilution_attn_paged_append(const void *q, const int64_t *q_strides, const vo
  * size depends on whether there is a prefix, not on its length.  tau_bh: nullable device [S*Hq], index
  * s*Hq + h.  tau, eps, flags (DA_FLAG_EARLIER_DEMAND_ONLY) as for
  * dilution_attn_decode_step_ex; DA_BF16 needs eps >= 1e-18 as the forward.
- * Repeated calls give equal bits.  Errors as for dilution_attn_decode_step_ex. */
+ * Repeated calls give equal bits.  Errors as for dilution_attn_decode_step_ex.
+ *
+ * dilution_attn_paged_decode_ex records what the kernels find in `status` (DEVICE,
+ * 256 bytes, 256-byte aligned, zeroed once by the caller) instead of the
+ * workspace's first 256 bytes: for workspaces that do not outlive the call.
+ * Calls that overlap on the GPU may share a status block. */
 size_t dilution_attn_paged_decode_workspace_size(int S, int Hq, int Hkv, int d, int max_len, int n_prefix_pages,
                                                  int page_size, int dtype);
 
 int dilution_attn_paged_decode(const void *q, const dilution_attn_paged_cache *cache, const int32_t *prefix_table,
                                int n_prefix_pages, int max_len, void *out, float tau, const float *tau_bh,
                                float eps, int flags, void *workspace, size_t workspace_bytes, void *stream);
+
+int dilution_attn_paged_decode_ex(const void *q, const dilution_attn_paged_cache *cache, const int32_t *prefix_table,
+                                  int n_prefix_pages, int max_len, void *out, float tau, const float *tau_bh,
+                                  float eps, int flags, void *workspace, size_t workspace_bytes, void *status,
+                                  void *stream);
 
 /* ------------------------------------------------------------------------
  * Synchronises `stream`, reads the status word that kernels of the last call

@@ -67,6 +67,8 @@ _SIGNATURES = {
     "dilution_attn_paged_decode_workspace_size": (_c_size_t, [_c_int] * 8),
     "dilution_attn_paged_decode": (_c_int, [_c_void_p] * 3 + [_c_int, _c_int, _c_void_p, _c_float, _c_void_p, _c_float,
                                                              _c_int, _c_void_p, _c_size_t, _c_void_p]),
+    "dilution_attn_paged_decode_ex": (_c_int, [_c_void_p] * 3 + [_c_int, _c_int, _c_void_p, _c_float, _c_void_p, _c_float,
+                                                                _c_int, _c_void_p, _c_size_t, _c_void_p, _c_void_p]),
     "dilution_attn_get_error": (_c_int, [_c_void_p, _c_void_p]),
     "dilution_attn_debug_last_timeout": (_c_int, [_c_void_p, _c_void_p]),
     "dilution_attn_debug_tile_schedule": (_c_int, [_c_int, _c_int, _c_int, _c_void_p, _c_size_t]),
@@ -532,17 +534,13 @@ def _need_table(table, dev):
         raise ValueError("prefix_table must be one-dimensional")
 
 
-def _new(shape, dtype, device, stream, zero_head=0):
-    """A tensor for a call on ``stream`` (None: the current one), allocated, and
-    its first bytes zeroed, on that stream: its memory is then not handed on
-    before the call has used it."""
+def _new(shape, dtype, device, stream):
+    """A tensor for a call on ``stream`` (None: the current one), allocated on
+    that stream: its memory is then not handed on before the call has used it."""
     if stream is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
-        if zero_head:
-            t[:zero_head].zero_()
-        return t
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return _new(shape, dtype, device, None, zero_head)
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 _CODES = {torch.float32: DA_F32, torch.bfloat16: DA_BF16}
@@ -623,9 +621,11 @@ class PagedCache:
     [num_pages, Hkv, page_size, d], demand_pages [num_demand_pages, Hq,
     page_size] fp32, page_table and demand_table [S, max_pages] int32, seq_lens
     [S] int32.  Checked once here; the tables and lengths are the caller's to
-    update in place between calls."""
+    update in place between calls.  ``status``: the status block of the calls
+    that are given no workspace; dilution_attn_get_error(cache.status) reads and
+    clears the first bad length or page that they found."""
 
-    __slots__ = ("k_pages", "v_pages", "demand_pages", "page_table", "demand_table", "seq_lens", "S", "Hq", "Hkv", "d",
+    __slots__ = ("k_pages", "v_pages", "demand_pages", "page_table", "demand_table", "seq_lens", "status", "S", "Hq", "Hkv", "d",
                  "page_size", "max_pages", "dtype", "device", "_code", "_c", "_ref", "_dev", "_q_shape", "_cu_shape")
 
     def __init__(self, k_pages, v_pages, demand_pages, page_table, demand_table, seq_lens):
@@ -655,6 +655,7 @@ class PagedCache:
                                                         seq_lens)), S, Hq, Hkv, d, page_size, num_pages,
                                num_demand_pages, max_pages, self._code)
         self._ref = ctypes.byref(self._c)
+        self.status = torch.zeros(256, dtype=torch.uint8, device=self.device)
         self._dev, self._q_shape, self._cu_shape = k_pages.get_device(), torch.Size((S, Hq, d)), torch.Size((S + 1,))
 
 
@@ -686,7 +687,9 @@ def dilution_attn_paged_append(q, k, v, cache, cu_tokens, q_out=None, *, rope=No
     on the way, by ``positions`` (int32 [n_axes, N]) or by their place in the
     sequence.  ``demand`` [N, Hq] fp32: the keys' totals (a prompt's
     demand_out after prefill), 0 when omitted.  q [N, Hq, d] (or None) turns
-    likewise into ``q_out`` (contiguous), which is returned."""
+    likewise into ``q_out`` (contiguous), which is returned.  Bad lengths or
+    page ids are found on the device: read them with dilution_attn_get_error on
+    ``workspace``, or on ``cache.status`` if none is given."""
     lib = _lib or load()
     dev = _need_cache(cache)
     Hq, Hkv, d, dtype = cache.Hq, cache.Hkv, cache.d, cache.dtype
@@ -722,7 +725,7 @@ def dilution_attn_paged_append(q, k, v, cache, cu_tokens, q_out=None, *, rope=No
             _need_any_strides(demand, "demand", (N, Hq), torch.float32)
         dp, sd = demand.data_ptr(), _c_strides(demand.stride(), 2)
     if workspace is None:
-        workspace = _new(dilution_attn_paged_append_workspace_size(), torch.uint8, cache.device, stream, 256)
+        workspace = cache.status     # an append needs nothing else
     else:
         _need_bytes(workspace, dev)
     st = lib.dilution_attn_paged_append(qp, sq, k.data_ptr(), sk, v.data_ptr(), sv, dp, sd, qop, cu_tokens.data_ptr(), N,
@@ -760,7 +763,8 @@ def dilution_attn_paged_decode(q, cache, max_len: int, out=None, *, prefix_table
     grows by its bid.  ``max_len``: upper bound of cache.seq_lens.
     ``prefix_table`` (int32 [n]): pages of the tokens that every sequence
     shares, read once for the batch.  Bad lengths or page ids are found on the
-    device: read them with dilution_attn_get_error on ``workspace``."""
+    device: read them with dilution_attn_get_error on ``workspace``, or on
+    ``cache.status`` if none is given."""
     lib = _lib or load()
     dev = _need_cache(cache)
     shape, dtype = cache._q_shape, cache.dtype
@@ -777,13 +781,14 @@ def dilution_attn_paged_decode(q, cache, max_len: int, out=None, *, prefix_table
     if workspace is None:
         need = dilution_attn_paged_decode_workspace_size(cache.S, cache.Hq, cache.Hkv, cache.d, int(max_len), n_prefix,
                                                          cache.page_size, cache._code)
-        workspace = _new(max(need, 256), torch.uint8, cache.device, stream, 256)
+        workspace, status = _new(max(need, 256), torch.uint8, cache.device, stream), cache.status.data_ptr()
     else:
         _need_bytes(workspace, dev)
-    st = lib.dilution_attn_paged_decode(q.data_ptr(), cache._ref, pt, n_prefix, int(max_len), out.data_ptr(), float(tau),
-                                        None if tau_bh is None else _tau_bh_ptr(tau_bh, cache.S, cache.Hq), float(eps),
-                                        int(flags), workspace.data_ptr(), workspace.numel(),
-                                        _raw_stream(dev) if stream is None else stream.cuda_stream)
+        status = workspace.data_ptr()
+    st = lib.dilution_attn_paged_decode_ex(q.data_ptr(), cache._ref, pt, n_prefix, int(max_len), out.data_ptr(), float(tau),
+                                           None if tau_bh is None else _tau_bh_ptr(tau_bh, cache.S, cache.Hq), float(eps),
+                                           int(flags), workspace.data_ptr(), workspace.numel(), status,
+                                           _raw_stream(dev) if stream is None else stream.cuda_stream)
     if check and st != DA_OK:
         _check(st, "dilution_attn_paged_decode")
     return out

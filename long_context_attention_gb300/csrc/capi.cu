@@ -84,7 +84,7 @@ const char *dilution_attn_status_string(int status) {
   }
 }
 
-int dilution_attn_version(void) { return 102; }
+int dilution_attn_version(void) { return 103; }
 
 size_t dilution_attn_fwd_workspace_size(int B, int H, int T, int d, int dtype) {
   (void)dtype;

@@ -257,6 +257,13 @@ size_t dilution_attn_paged_decode_workspace_size(int S, int Hq, int Hkv, int d, 
 int dilution_attn_paged_decode(const void *q, const dilution_attn_paged_cache *cache, const int32_t *prefix_table,
                                int n_prefix_pages, int max_len, void *out, float tau, const float *tau_bh, float eps,
                                int flags, void *workspace, size_t workspace_bytes, void *stream) {
+  return dilution_attn_paged_decode_ex(q, cache, prefix_table, n_prefix_pages, max_len, out, tau, tau_bh, eps, flags,
+                                       workspace, workspace_bytes, workspace, stream);
+}
+
+int dilution_attn_paged_decode_ex(const void *q, const dilution_attn_paged_cache *cache, const int32_t *prefix_table,
+                                  int n_prefix_pages, int max_len, void *out, float tau, const float *tau_bh, float eps,
+                                  int flags, void *workspace, size_t workspace_bytes, void *status, void *stream) {
   int st = check_cache(cache);
   if (st != DA_OK) return st;
   const dilution_attn_paged_cache &c = *cache;
@@ -271,6 +278,7 @@ int dilution_attn_paged_decode(const void *q, const dilution_attn_paged_cache *c
   const int prefix_len = n_prefix_pages * c.page_size;
   st = check_workspace(workspace, workspace_bytes, pgt_workspace(c.S, c.Hq, c.Hkv, c.d, max_len, prefix_len, c.dtype));
   if (st != DA_OK) return st;
+  if (status == nullptr || !aligned(status, 256)) return DA_ERR_INVALID;
   if ((int64_t)c.num_pages * c.Hkv > 0x7FFFFFFF) return DA_ERR_UNSUPPORTED;   // a copy's coordinate
   // what the kernels count in 32 bits: places in the demand pool (16 floats each), work units
   if ((int64_t)c.num_demand_pages * c.Hq * (c.page_size / 16) >= 0xFFFFFFFFll) return DA_ERR_UNSUPPORTED;
@@ -286,7 +294,7 @@ int dilution_attn_paged_decode(const void *q, const dilution_attn_paged_cache *c
   p.hs = HeadScale{tau_bh, (float)((double)tau * per_tau), per_tau};
   p.eps = eps;
   p.earlier = (flags & DA_FLAG_EARLIER_DEMAND_ONLY) != 0;
-  p.status = reinterpret_cast<int *>(workspace);
+  p.status = reinterpret_cast<int *>(status);
   p.ws = reinterpret_cast<uint8_t *>(workspace);
   return launch_paged_decode(p, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -291,6 +291,53 @@ def test_bad_device_data_is_reported(dtype, max_len, S):
     assert np.abs(host64(out)[keep] - ref[0][keep]).max() <= 2e-2
 
 
+@pytest.mark.parametrize("max_len,dtype", [(224, "bf16"), (LONG, "bf16"), (224, "f32")])
+def test_errors_of_calls_without_a_workspace_stay_readable(max_len, dtype):
+    lens = [70, 200, 64]
+    cache, q, pt = make_cache(3, lens, 4, 2, 64, 32, dtype, seed=61, prefix=64)
+    before = cache.demand_pages.clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    good = b.dilution_attn_paged_decode(q, cache, max_len, prefix_table=pt)
+    assert b.dilution_attn_get_error(cache.status) == b.DA_OK
+
+    def step(**kw):
+        cache.demand_pages.copy_(before)
+        torch.cuda.synchronize()
+        return b.dilution_attn_paged_decode(q, cache, max_len, **kw)
+
+    cache.seq_lens[1] = max_len + 1
+    step()
+    assert b.dilution_attn_get_error(cache.status) == b.DA_ERR_INVALID
+    assert b.dilution_attn_get_error(cache.status) == b.DA_OK          # read once
+    step(stream=side)
+    assert torch.equal(step(prefix_table=pt)[[0, 2]], good[[0, 2]])    # an error waits until it is read
+    torch.cuda.synchronize()
+    assert b.dilution_attn_get_error(cache.status, side) == b.DA_ERR_INVALID
+    cache.seq_lens[1] = 200
+    page = cache.page_table[1, 3].item()
+    cache.page_table[1, 3] = 10 ** 6
+    step()
+    assert b.dilution_attn_get_error(cache.status) == b.DA_ERR_INVALID
+    k = torch.zeros(3, 2, 64, dtype=q.dtype, device=DEV)
+    cache.demand_table[0, 2] = -1
+    b.dilution_attn_paged_append(None, k, k, cache, torch.arange(4, dtype=torch.int32, device=DEV))
+    assert b.dilution_attn_get_error(cache.status) == b.DA_ERR_INVALID
+    # a call with a workspace records in that
+    ws = b.dilution_attn_paged_decode_workspace(cache, max_len)
+    step(workspace=ws)
+    assert b.dilution_attn_get_error(cache.status) == b.DA_OK and b.dilution_attn_get_error(ws) == b.DA_ERR_INVALID
+    # a captured step without one
+    cache.page_table[1, 3] = page
+    cache.demand_table[0, 2] = 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = b.dilution_attn_paged_decode(q, cache, max_len)
+    cache.page_table[1, 3] = -3
+    graph.replay()
+    assert b.dilution_attn_get_error(cache.status) == b.DA_ERR_INVALID and out.shape == q.shape
+
+
 @pytest.mark.parametrize("max_len,dtype", [(264, "bf16"), (LONG, "bf16"), (264, "f32")])
 def test_graph_replay_with_growing_sequences(max_len, dtype):
     # one captured step replays over lengths and tables that change on the device

@@ -130,6 +130,17 @@ def test_decode_refusals(lib):
     assert call(cache(S=0), q=None) == b.DA_OK
 
 
+def test_decode_with_a_status_block_refuses_bad_ones(lib):
+    def call(status, ws=FAKE, wsb=1 << 30, max_len=64):
+        return lib.dilution_attn_paged_decode_ex(FAKE, ctypes.byref(cache()), None, 0, max_len, FAKE, 1.0, None, 1e-6, 0,
+                                                 ws, wsb, status, None)
+    assert call(None) == b.DA_ERR_INVALID
+    assert call(FAKE + 16) == b.DA_ERR_INVALID
+    assert call(FAKE, ws=None) == b.DA_ERR_WORKSPACE
+    assert call(FAKE, wsb=300) == b.DA_ERR_WORKSPACE
+    assert call(FAKE, max_len=65) == b.DA_ERR_INVALID
+
+
 def test_outputs_that_lie_over_inputs_are_refused(lib):
     """Rows written by one block that another still has to read: an output at an input's address with other strides,
     or at another operand's address."""
