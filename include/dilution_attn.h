@@ -467,6 +467,24 @@ int dilution_attn_debug_decode_stall(const void *q_new, const void *k_new, const
                                      void *workspace, size_t workspace_bytes, void *stream,
                                      int stall_chunk, int stall_bh, long long wait_limit_ns);
 
+/* The same for the paged step: one decode step like dilution_attn_paged_decode
+ * (tau_bh = NULL, flags = 0), except that in block `stall_block` of kernel
+ * `stall_kernel` (0: logits, 1: shares of the streaming kernels; 2, 3: those of
+ * a prefix with many rows) one warp keeps the first ring stage it read (3: the
+ * first table of demand pages is not handed over), and every wait of that kernel
+ * gives up after wait_limit_ns (1e3 .. 1e9 ns; kernel 3: after the ordinary 1 s,
+ * as it has no register left for the limit).  It has an effect where the call runs
+ * that kernel and the block has more tiles than ring stages (8).  The waits that
+ * run out record as above; the call completes, the device stays usable, out and
+ * the demand are unspecified, and the workspace's first 256 bytes have to be
+ * zeroed again.  Errors: those of dilution_attn_paged_decode, and DA_ERR_INVALID
+ * for a stall_kernel outside 0 .. 3, a negative stall_block or a wait_limit_ns
+ * outside the range. */
+int dilution_attn_debug_paged_decode_stall(const void *q, const dilution_attn_paged_cache *cache,
+                                           const int32_t *prefix_table, int n_prefix_pages, int max_len, void *out,
+                                           float tau, float eps, void *workspace, size_t workspace_bytes, void *stream,
+                                           int stall_kernel, int stall_block, long long wait_limit_ns);
+
 /* ------------------------------------------------------------------------
  * Host-only introspection of integer artefacts (no GPU needed).
  *

@@ -69,6 +69,9 @@ _SIGNATURES = {
                                                              _c_int, _c_void_p, _c_size_t, _c_void_p]),
     "dilution_attn_paged_decode_ex": (_c_int, [_c_void_p] * 3 + [_c_int, _c_int, _c_void_p, _c_float, _c_void_p, _c_float,
                                                                 _c_int, _c_void_p, _c_size_t, _c_void_p, _c_void_p]),
+    "dilution_attn_debug_paged_decode_stall": (_c_int, [_c_void_p] * 3 + [_c_int, _c_int, _c_void_p, _c_float, _c_float,
+                                                                         _c_void_p, _c_size_t, _c_void_p, _c_int, _c_int,
+                                                                         ctypes.c_longlong]),
     "dilution_attn_get_error": (_c_int, [_c_void_p, _c_void_p]),
     "dilution_attn_debug_last_timeout": (_c_int, [_c_void_p, _c_void_p]),
     "dilution_attn_debug_tile_schedule": (_c_int, [_c_int, _c_int, _c_int, _c_void_p, _c_size_t]),
@@ -792,6 +795,29 @@ def dilution_attn_paged_decode(q, cache, max_len: int, out=None, *, prefix_table
     if check and st != DA_OK:
         _check(st, "dilution_attn_paged_decode")
     return out
+
+
+def dilution_attn_debug_paged_decode_stall(q, cache, max_len: int, *, workspace, prefix_table=None, tau: float = 1.0,
+                                           eps: float = 1e-6, stream=None, stall_kernel: int = 0, stall_block: int = 0,
+                                           wait_limit_ns: int = 2_000_000):
+    """Test hook of the bounded waits: a paged decode step in which one block
+    of one kernel keeps what another role waits for (see the header).  Returns
+    (status, out); the kernel-side outcome is read with
+    dilution_attn_debug_last_timeout / dilution_attn_get_error on ``workspace``."""
+    lib = load()
+    dev = _need_cache(cache)
+    _fit(q, "q", cache._q_shape, cache.dtype, dev)
+    _need_bytes(workspace, dev)
+    n_prefix, pt = 0, None
+    if prefix_table is not None:
+        _need_table(prefix_table, dev)
+        n_prefix, pt = prefix_table.numel(), prefix_table.data_ptr()
+    out = _new(cache._q_shape, cache.dtype, cache.device, stream)
+    st = lib.dilution_attn_debug_paged_decode_stall(q.data_ptr(), cache._ref, pt, n_prefix, int(max_len), out.data_ptr(),
+                                                    float(tau), float(eps), workspace.data_ptr(), workspace.numel(),
+                                                    _stream_id(stream, dev), int(stall_kernel), int(stall_block),
+                                                    int(wait_limit_ns))
+    return int(st), out
 
 
 # ----------------------------------------------------------------------------- misc

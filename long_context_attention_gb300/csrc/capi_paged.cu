@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kMaxHeads = 1 << 14;   // a launch grid's second dimension counts rows of q, k and v
 constexpr int kMaxTokens = 1 << 30;
+constexpr unsigned long long kWaitLimitNsHost = 1000ull * 1000ull * 1000ull;
 
 int elem_bytes(int dtype) { return dtype == DA_BF16 ? 2 : 4; }
 bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -166,6 +167,51 @@ int check_workspace(const void *ws, size_t bytes, size_t need) {
   return aligned(ws, 256) ? DA_OK : DA_ERR_INVALID;
 }
 
+PagedDebug no_stall() {
+  PagedDebug d;
+  for (int k = 0; k < kPagedKernels; ++k) d.limit_ns[k] = kWaitLimitNsHost, d.stall_block[k] = -1;
+  return d;
+}
+
+int decode_call(const void *q, const dilution_attn_paged_cache *cache, const int32_t *prefix_table, int n_prefix_pages,
+                int max_len, void *out, float tau, const float *tau_bh, float eps, int flags, void *workspace,
+                size_t workspace_bytes, void *status, void *stream, const PagedDebug &dbg) {
+  int st = check_cache(cache);
+  if (st != DA_OK) return st;
+  const dilution_attn_paged_cache &c = *cache;
+  if (!std::isfinite(tau) || tau < 0.f || !std::isfinite(eps) || eps <= 0.f) return DA_ERR_INVALID;
+  if ((flags & ~DA_FLAG_EARLIER_DEMAND_ONLY) != 0 || !aligned(tau_bh, 4)) return DA_ERR_INVALID;
+  if (max_len < 0 || (int64_t)max_len > (int64_t)c.max_pages * c.page_size) return DA_ERR_INVALID;
+  if (n_prefix_pages < 0 || (int64_t)n_prefix_pages * c.page_size > max_len) return DA_ERR_INVALID;
+  if (n_prefix_pages > 0 && (prefix_table == nullptr || !aligned(prefix_table, 4))) return DA_ERR_INVALID;
+  if (c.dtype == DA_BF16 && eps < 1e-18f) return DA_ERR_UNSUPPORTED;
+  if (c.S == 0) return DA_OK;
+  if (q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 16)) return DA_ERR_INVALID;
+  const int prefix_len = n_prefix_pages * c.page_size;
+  st = check_workspace(workspace, workspace_bytes, pgt_workspace(c.S, c.Hq, c.Hkv, c.d, max_len, prefix_len, c.dtype));
+  if (st != DA_OK) return st;
+  if (status == nullptr || !aligned(status, 256)) return DA_ERR_INVALID;
+  if ((int64_t)c.num_pages * c.Hkv > 0x7FFFFFFF) return DA_ERR_UNSUPPORTED;   // a copy's coordinate
+  // what the kernels count in 32 bits: places in the demand pool (16 floats each), work units
+  if ((int64_t)c.num_demand_pages * c.Hq * (c.page_size / 16) >= 0xFFFFFFFFll) return DA_ERR_UNSUPPORTED;
+  if (!pgt_fits(c.S, c.Hq, c.Hkv, c.d, max_len, prefix_len, c.dtype)) return DA_ERR_UNSUPPORTED;
+  PagedDecode p{};
+  p.c = c;
+  p.q = q;
+  p.out = out;
+  p.prefix_table = n_prefix_pages > 0 ? prefix_table : nullptr;
+  p.prefix_len = prefix_len;
+  p.max_len = max_len;
+  const double per_tau = 1.4426950408889634 / std::sqrt((double)c.d);
+  p.hs = HeadScale{tau_bh, (float)((double)tau * per_tau), per_tau};
+  p.eps = eps;
+  p.earlier = (flags & DA_FLAG_EARLIER_DEMAND_ONLY) != 0;
+  p.status = reinterpret_cast<int *>(status);
+  p.ws = reinterpret_cast<uint8_t *>(workspace);
+  p.dbg = dbg;
+  return launch_paged_decode(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -257,46 +303,29 @@ size_t dilution_attn_paged_decode_workspace_size(int S, int Hq, int Hkv, int d, 
 int dilution_attn_paged_decode(const void *q, const dilution_attn_paged_cache *cache, const int32_t *prefix_table,
                                int n_prefix_pages, int max_len, void *out, float tau, const float *tau_bh, float eps,
                                int flags, void *workspace, size_t workspace_bytes, void *stream) {
-  return dilution_attn_paged_decode_ex(q, cache, prefix_table, n_prefix_pages, max_len, out, tau, tau_bh, eps, flags,
-                                       workspace, workspace_bytes, workspace, stream);
+  return decode_call(q, cache, prefix_table, n_prefix_pages, max_len, out, tau, tau_bh, eps, flags, workspace,
+                     workspace_bytes, workspace, stream, no_stall());
 }
 
 int dilution_attn_paged_decode_ex(const void *q, const dilution_attn_paged_cache *cache, const int32_t *prefix_table,
                                   int n_prefix_pages, int max_len, void *out, float tau, const float *tau_bh, float eps,
                                   int flags, void *workspace, size_t workspace_bytes, void *status, void *stream) {
-  int st = check_cache(cache);
-  if (st != DA_OK) return st;
-  const dilution_attn_paged_cache &c = *cache;
-  if (!std::isfinite(tau) || tau < 0.f || !std::isfinite(eps) || eps <= 0.f) return DA_ERR_INVALID;
-  if ((flags & ~DA_FLAG_EARLIER_DEMAND_ONLY) != 0 || !aligned(tau_bh, 4)) return DA_ERR_INVALID;
-  if (max_len < 0 || (int64_t)max_len > (int64_t)c.max_pages * c.page_size) return DA_ERR_INVALID;
-  if (n_prefix_pages < 0 || (int64_t)n_prefix_pages * c.page_size > max_len) return DA_ERR_INVALID;
-  if (n_prefix_pages > 0 && (prefix_table == nullptr || !aligned(prefix_table, 4))) return DA_ERR_INVALID;
-  if (c.dtype == DA_BF16 && eps < 1e-18f) return DA_ERR_UNSUPPORTED;
-  if (c.S == 0) return DA_OK;
-  if (q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 16)) return DA_ERR_INVALID;
-  const int prefix_len = n_prefix_pages * c.page_size;
-  st = check_workspace(workspace, workspace_bytes, pgt_workspace(c.S, c.Hq, c.Hkv, c.d, max_len, prefix_len, c.dtype));
-  if (st != DA_OK) return st;
-  if (status == nullptr || !aligned(status, 256)) return DA_ERR_INVALID;
-  if ((int64_t)c.num_pages * c.Hkv > 0x7FFFFFFF) return DA_ERR_UNSUPPORTED;   // a copy's coordinate
-  // what the kernels count in 32 bits: places in the demand pool (16 floats each), work units
-  if ((int64_t)c.num_demand_pages * c.Hq * (c.page_size / 16) >= 0xFFFFFFFFll) return DA_ERR_UNSUPPORTED;
-  if (!pgt_fits(c.S, c.Hq, c.Hkv, c.d, max_len, prefix_len, c.dtype)) return DA_ERR_UNSUPPORTED;
-  PagedDecode p{};
-  p.c = c;
-  p.q = q;
-  p.out = out;
-  p.prefix_table = n_prefix_pages > 0 ? prefix_table : nullptr;
-  p.prefix_len = prefix_len;
-  p.max_len = max_len;
-  const double per_tau = 1.4426950408889634 / std::sqrt((double)c.d);
-  p.hs = HeadScale{tau_bh, (float)((double)tau * per_tau), per_tau};
-  p.eps = eps;
-  p.earlier = (flags & DA_FLAG_EARLIER_DEMAND_ONLY) != 0;
-  p.status = reinterpret_cast<int *>(status);
-  p.ws = reinterpret_cast<uint8_t *>(workspace);
-  return launch_paged_decode(p, reinterpret_cast<cudaStream_t>(stream));
+  return decode_call(q, cache, prefix_table, n_prefix_pages, max_len, out, tau, tau_bh, eps, flags, workspace,
+                     workspace_bytes, status, stream, no_stall());
+}
+
+int dilution_attn_debug_paged_decode_stall(const void *q, const dilution_attn_paged_cache *cache,
+                                           const int32_t *prefix_table, int n_prefix_pages, int max_len, void *out,
+                                           float tau, float eps, void *workspace, size_t workspace_bytes, void *stream,
+                                           int stall_kernel, int stall_block, long long wait_limit_ns) {
+  if (stall_kernel < 0 || stall_kernel >= kPagedKernels || stall_block < 0 || wait_limit_ns < 1000 ||
+      wait_limit_ns > (long long)kWaitLimitNsHost)
+    return DA_ERR_INVALID;
+  PagedDebug dbg = no_stall();
+  dbg.limit_ns[stall_kernel] = (unsigned long long)wait_limit_ns;
+  dbg.stall_block[stall_kernel] = stall_block;
+  return decode_call(q, cache, prefix_table, n_prefix_pages, max_len, out, tau, nullptr, eps, 0, workspace,
+                     workspace_bytes, workspace, stream, dbg);
 }
 
 }  // extern "C"

@@ -6,6 +6,17 @@
 
 namespace da {
 
+// The kernels of a step that wait on barriers, for the test hook of their waits.
+enum PagedKernel { kPagedKeys, kPagedValues, kPagedPrefixKeys, kPagedPrefixValues, kPagedKernels };
+
+// Test hook: block stall_block[k] of kernel k keeps one thing that another role of
+// it waits for (-1: none), and its waits give up after limit_ns[k] (the prefix's value
+// kernel after the ordinary limit: it has no register left for another).
+struct PagedDebug {
+  unsigned long long limit_ns[kPagedKernels];
+  int stall_block[kPagedKernels];
+};
+
 // One paged decode call.
 struct PagedDecode {
   dilution_attn_paged_cache c;
@@ -19,6 +30,7 @@ struct PagedDecode {
   bool earlier;
   int *status;
   uint8_t *ws;
+  PagedDebug dbg;
 };
 
 #if defined(__CUDACC__)

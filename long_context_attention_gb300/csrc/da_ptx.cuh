@@ -70,7 +70,7 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
 struct WaitCtx {
   volatile int *abort_flag;  // shared memory
   int *status;               // global status word (workspace)
-  unsigned long long limit_ns = kWaitLimitNs;   // shortened only by the decode test hook
+  unsigned long long limit_ns = kWaitLimitNs;   // shortened only by the decode steps' test hooks
 };
 
 // The first wait that gives up also records where: status[1] = shared-memory

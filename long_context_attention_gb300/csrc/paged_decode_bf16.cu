@@ -88,13 +88,14 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
   pgt_load_lens<pgt_threads(D)>(p, w, L, blockIdx.x == 0 ? p.status : nullptr);
   const PgtLine line = pgt_line(p, w, L);
   const int from = line.cut.first(blockIdx.x), to = line.cut.first(blockIdx.x + 1);
-  const WaitCtx wc{&ring.abort_word, p.status};
+  const WaitCtx wc{&ring.abort_word, p.status, p.dbg.limit_ns[kPagedKeys]};
   const uint32_t base = smem_u32(pgt_smem_base());
   if (warp == WARPS) {
     produce<pgt_tile(D), 64, true>(p, w, line, L, ring, &kmap, base, stages, from, to, wc);
     return;
   }
   const int gid = lane / 4, t = lane % 4;
+  const bool keep = warp == 0 && (int)blockIdx.x == p.dbg.stall_block[kPagedKeys];   // test hook
   // lane -> the row it addresses: matrices (half 0, k 0-7), (half 0, k 8-15), (half 1, ..), (half 1, ..)
   const int row = warp * 16 + group_key(lane & 7, lane >> 4);
   int slot = 0;
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(pgt_threads(D), 2)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ring.empty[slot]);
+      if (lane == 0 && !(keep && k == 0)) mbar_arrive(&ring.empty[slot]);
       if (++slot == stages) {
         slot = 0;
         parity ^= 1;
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
   pgt_load_lens<V::kThreads>(p, w, L, nullptr);
   const PgtLine line = pgt_line(p, w, L);
   const int from = line.cut.first(blockIdx.x), to = line.cut.first(blockIdx.x + 1);
-  const WaitCtx wc{&ring.abort_word, p.status};
+  const WaitCtx wc{&ring.abort_word, p.status, p.dbg.limit_ns[kPagedValues]};
   uint8_t *const smem = pgt_smem_base();
   const uint32_t base = smem_u32(smem);
   if (warp == WARPS) {   // the values do not depend on the first pass
@@ -243,6 +244,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
   const int gid = lane / 4, t = lane % 4, sh = w.page_shift, ps = 1 << sh;
   const int q = V::kWide ? 0 : gid / GE, r0 = V::kWide ? gid : gid % GE;   // the lane's group and row
   const int sub = warp % V::kStepsPerTile * V::kStep;    // the warp's keys inside a tile
+  const bool keep = warp == 0 && (int)blockIdx.x == p.dbg.stall_block[kPagedValues];   // test hook
   // lane -> row: matrices (k half 0, n 0-7), (k half 1, n 0-7), (k half 0, n 8-15), (k half 1, n 8-15)
   const int vrow = sub + group_key(lane & 7, (lane >> 3) & 1);
   bool waited = false;
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(PgtVal<D, GE>::kThreads, 2)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ring.empty[slot]);
+      if (lane == 0 && !(keep && k == 0)) mbar_arrive(&ring.empty[slot]);
     }
     cp_async_wait_all();
     __syncwarp();

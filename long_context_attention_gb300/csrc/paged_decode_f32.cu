@@ -61,12 +61,13 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
   pgt_load_lens<kPgfThreads>(p, w, L, blockIdx.x == 0 ? p.status : nullptr);
   const PgtLine line = pgt_line(p, w, L);
   const int from = line.cut.first(blockIdx.x), to = line.cut.first(blockIdx.x + 1);
-  const WaitCtx wc{&ring.abort_word, p.status};
+  const WaitCtx wc{&ring.abort_word, p.status, p.dbg.limit_ns[kPagedKeys]};
   uint8_t *const smem = pgt_smem_base();
   if (warp == kPgfWarps) {
     produce<TILE, 32, true>(p, w, line, L, ring, &kmap, smem_u32(smem), STAGES, from, to, wc);
     return;
   }
+  const bool keep = warp == 0 && (int)blockIdx.x == p.dbg.stall_block[kPagedKeys];   // test hook
   const int sub = warp % T::kPerTile * 32, kl = lane % B::kKeyLanes, rl = lane / B::kKeyLanes;
   PgtSeg g;
   for (g.start(p, w, line, L, from, to); g.n > 0; g.next(p, w, line, L)) {
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ring.empty[slot]);
+      if (lane == 0 && !(keep && k == 0)) mbar_arrive(&ring.empty[slot]);
     }
 #pragma unroll
     for (int j = 0; j < B::kRows; ++j) {
@@ -209,7 +210,7 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
   pgt_load_lens<kPgfThreads>(p, w, L, nullptr);
   const PgtLine line = pgt_line(p, w, L);
   const int from = line.cut.first(blockIdx.x), to = line.cut.first(blockIdx.x + 1);
-  const WaitCtx wc{&ring.abort_word, p.status};
+  const WaitCtx wc{&ring.abort_word, p.status, p.dbg.limit_ns[kPagedValues]};
   uint8_t *const smem = pgt_smem_base();
   if (warp == kPgfWarps) {   // the values do not depend on the first pass
     produce<TILE, 32, false>(p, w, line, L, ring, &vmap, smem_u32(smem), V::kStages, from, to, wc);
@@ -219,6 +220,7 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
   float *const mine = reinterpret_cast<float *>(base + warp * V::kWarpBytes);   // [2 steps][x, D][R][32]
   const int sh = w.page_shift, ps = 1 << sh, sub = warp % V::kSubs * 32;
   const int r0 = warp % V::kPerTile / V::kSubs * R;   // the warp's first row
+  const bool keep = warp == 0 && (int)blockIdx.x == p.dbg.stall_block[kPagedValues];   // test hook
   const int pr = lane / 8, pk = 4 * (lane % 8);       // the lane's pieces: rows pr, pr + 4 of the warp's, keys pk .. of a step
   // byte offsets of the lane's columns in a tile, for key & 7 = 0 .. 7
   uint32_t col[8];
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(kPgfThreads, 2)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ring.empty[slot]);
+      if (lane == 0 && !(keep && k == 0)) mbar_arrive(&ring.empty[slot]);
     }
     cp_async_wait_all();
     __syncwarp();

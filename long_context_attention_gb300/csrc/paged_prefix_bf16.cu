@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(XKeys<D>::kThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const WaitCtx wc{abort_flag, p.status};
+  const WaitCtx wc{abort_flag, p.status, p.dbg.limit_ns[kPagedPrefixKeys]};
   XWalk it;
   it.start(p, w, w.x_keys);
   if (warp == 8) {
@@ -227,7 +227,8 @@ __global__ void __launch_bounds__(XKeys<D>::kThreads, 2)
           if constexpr (D == 128)
             MmaRun<0, 4, 2, 2, false>::go(tmem + b * 128, dQ + (kXHalf >> 4), dKs + (kXHalf >> 4), idesc, 1u);
           mma_commit(&s_full[b]);
-          mma_commit(&k_empty[s]);
+          if (t > 0 || (int)blockIdx.x != p.dbg.stall_block[kPagedPrefixKeys])   // (test hook: one stage is kept)
+            mma_commit(&k_empty[s]);
         }
       }
       mma_commit(done);
@@ -544,7 +545,8 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
             }
           fetch(k + 1);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&tab_full[b]);
+          if (lane == 0 && (t > 0 || (int)blockIdx.x != p.dbg.stall_block[kPagedPrefixValues]))   // (test hook: a table
+            mbar_arrive(&tab_full[b]);                                                            // is not handed over)
         }
       }
     };

@@ -431,3 +431,47 @@ def test_pool_past_32_bit_offsets():
     before = long.demand_pages.clone()
     out = b.dilution_attn_paged_decode(q, long, LONG)
     check_step(long, q, before, out, ref)
+
+
+# ------------------------------------------------------------------ waits that run out
+def run_out(cache, q, pt, max_len, kernel, block):
+    """A step in which one block's hand-over is kept: the waits of its kernel give up, the call completes and says so,
+    and the next step gives the bits of the step before."""
+    ws = b.dilution_attn_paged_decode_workspace(cache, max_len)
+    before = cache.demand_pages.clone()
+    good = b.dilution_attn_paged_decode(q, cache, max_len, prefix_table=pt, workspace=ws)
+    demand = cache.demand_pages.clone()
+    assert b.dilution_attn_get_error(ws) == b.DA_OK
+    cache.demand_pages.copy_(before)
+    st, _ = b.dilution_attn_debug_paged_decode_stall(q, cache, max_len, workspace=ws, prefix_table=pt, stall_kernel=kernel,
+                                                     stall_block=block)
+    assert st == b.DA_OK                                      # launched; the failure is on the device
+    words = b.dilution_attn_debug_last_timeout(ws)            # synchronises: the call completed
+    assert words[0] == b.DA_ERR_TIMEOUT and words[2] == block and words[1] > 0
+    assert b.dilution_attn_get_error(ws) == b.DA_ERR_TIMEOUT
+    ws[:256].zero_()
+    cache.demand_pages.copy_(before)
+    again = b.dilution_attn_paged_decode(q, cache, max_len, prefix_table=pt, workspace=ws)
+    assert b.dilution_attn_get_error(ws) == b.DA_OK
+    assert torch.equal(again, good) and torch.equal(cache.demand_pages, demand)
+    return words[3]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kernel", [0, 1])                    # logits, shares
+@pytest.mark.parametrize("G,d", [(1, 64), (3, 128), (16, 64)])
+def test_streaming_waits_that_run_out_are_reported_and_recovered(G, d, kernel, dtype):
+    # 2 x 4 key heads x 60000 keys: more than 8 tiles for each of 304 blocks
+    cache, q, _ = make_cache(2, [60000, 59000], 4 * G, 4, d, 64, dtype, seed=7)
+    thread = run_out(cache, q, None, 60000, kernel, 17)
+    assert 0 <= thread < 288
+
+
+@pytest.mark.parametrize("kernel", [2, 3])
+@pytest.mark.parametrize("d,S", [(64, 17), (128, 40)])
+def test_prefix_waits_that_run_out_are_reported_and_recovered(d, S, kernel):
+    # one key head, one segment: 3856 tiles, 12 or 13 for a block of the first pass, 25 of the second
+    prefix = 493568
+    cache, q, pt = make_cache(S, [prefix + 1 + i for i in range(S)], 1, 1, d, 256, "bf16", seed=8, prefix=prefix)
+    thread = run_out(cache, q, pt, prefix + S, kernel, 17)
+    assert 0 <= thread < 640

@@ -141,6 +141,17 @@ def test_decode_with_a_status_block_refuses_bad_ones(lib):
     assert call(FAKE, max_len=65) == b.DA_ERR_INVALID
 
 
+def test_stall_hook_refusals(lib):
+    def call(kernel=0, block=0, limit=2_000_000, c=None, ws=FAKE):
+        c = cache() if c is None else c
+        return lib.dilution_attn_debug_paged_decode_stall(FAKE, ctypes.byref(c), None, 0, 64, FAKE, 1.0, 1e-6, ws, 1 << 30,
+                                                          None, kernel, block, limit)
+    for bad in (dict(kernel=-1), dict(kernel=4), dict(block=-1), dict(limit=999), dict(limit=1_000_000_001),
+                dict(c=cache(Hq=5))):
+        assert call(**bad) == b.DA_ERR_INVALID, bad
+    assert call(ws=None) == b.DA_ERR_WORKSPACE
+
+
 def test_outputs_that_lie_over_inputs_are_refused(lib):
     """Rows written by one block that another still has to read: an output at an input's address with other strides,
     or at another operand's address."""
