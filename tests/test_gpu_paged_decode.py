@@ -185,6 +185,38 @@ def test_long_prefix_whose_logits_lie_far_below_zero(d, page, prefix, flags):
         check_step(one, q[rows, h:h + 1], old, out[rows, h:h + 1], ref)
 
 
+@pytest.mark.parametrize("d,S,Hq,Hkv,page,prefix", [(64, 9, 4, 2, 64, 8192), (128, 3, 12, 2, 16, 6160), (64, 20, 1, 1, 256, 12288)])
+def test_long_prefix_in_fp32(d, S, Hq, Hkv, page, prefix):
+    # 18 to 20 rows of a key head: a segment of 16 and one of the rest
+    lens = [0 if i == 1 else prefix + 3 * i for i in range(S)]
+    cache, q, pt = make_cache(S, lens, Hq, Hkv, d, page, "f32", seed=prefix, prefix=prefix)
+    step_and_check(cache, q, max(lens), prefix_table=pt)
+
+
+@pytest.mark.parametrize("d,S,Hq,Hkv,page,prefix", LONG_PREFIX[:4])
+def test_captured_step_behind_a_long_prefix(d, S, Hq, Hkv, page, prefix):
+    # the kernels for many rows in a graph, replayed over lengths that change on the device: the bits of eager calls
+    cache, q, pt = make_cache(S, [prefix + 40] * S, Hq, Hkv, d, page, "bf16", seed=S, prefix=prefix)
+    ws = b.dilution_attn_paged_decode_workspace(cache, prefix + 40)
+    before, out = cache.demand_pages.clone(), torch.empty_like(q)
+    b.dilution_attn_paged_decode(q, cache, prefix + 40, out, prefix_table=pt, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.dilution_attn_paged_decode(q, cache, prefix + 40, out, prefix_table=pt, workspace=ws)
+    for step in range(3):
+        cache.seq_lens.copy_(torch.tensor([0 if (i + step) % 9 == 4 else prefix + (7 * i + step) % 40 for i in range(S)],
+                                          dtype=torch.int32))
+        cache.demand_pages.copy_(before)
+        want = b.dilution_attn_paged_decode(q, cache, prefix + 40, prefix_table=pt)
+        demand = cache.demand_pages.clone()
+        cache.demand_pages.copy_(before)
+        out.fill_(9.0)
+        graph.replay()
+        assert torch.equal(out, want) and torch.equal(cache.demand_pages, demand)
+        assert b.dilution_attn_get_error(ws) == b.DA_OK and b.dilution_attn_get_error(cache.status) == b.DA_OK
+
+
 def test_more_sequences_than_one_part():
     lens = [64 + i % 3 for i in range(900)]
     cache, q, pt = make_cache(900, lens, 1, 1, 64, 16, "bf16", seed=98, prefix=64)

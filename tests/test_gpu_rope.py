@@ -103,6 +103,29 @@ def test_rope_through_a_fused_projection(dtype, pad):
     assert (gh[:, Hq + Hk:] == 9.0).all() and (pad == 0 or (grad[..., -pad:] == 9.0).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,axes,d", [(32, 3, 64), (11, 1, 64), (61, 4, 128)])
+def test_rope_adjacent_pairs_of_unaligned_rows(dtype, n, axes, d):
+    # rows of a fused projection that start at any element: pairs move element by element, in both directions
+    B, Hq, Hk, T, pad, t = 2, 3, 1, 41, 3, TYPES[dtype]
+    width = (Hq + 2 * Hk) * d + pad
+    rows = torch.randn(B, T, width, generator=torch.Generator().manual_seed(n)).to(t).to(DEV)
+    heads = rows[..., 1:width - pad + 1].unflatten(-1, (-1, d)).transpose(1, 2)
+    q, k = heads[:, :Hq], heads[:, Hq:Hq + Hk]
+    spec, inv, pa = spec_of(n, axes, True)
+    pos = positions(axes, B, T, seed=n)
+    ang = op.rope_angles(pos.cpu().numpy(), inv.cpu().numpy(), pa)[:, None]
+    qo, ko = b.dilution_attn_rope(q, k, pos, spec)
+    close(qo, q, ang, True)
+    close(ko, k, ang, True)
+    grad = torch.full_like(rows, 9.0)
+    gh = grad[..., 1:width - pad + 1].unflatten(-1, (-1, d)).transpose(1, 2)
+    b.dilution_attn_rope_bwd(qo, ko, pos, spec, gh[:, :Hq], gh[:, Hq:Hq + Hk])
+    close(gh[:, :Hq], qo, ang, True, back=True)
+    close(gh[:, Hq:Hq + Hk], ko, ang, True, back=True)
+    assert (gh[:, Hq + Hk:] == 9.0).all() and (grad[..., 0] == 9.0).all() and (grad[..., 1 - pad:] == 9.0).all()
+
+
 def test_rope_in_place_broadcast_and_strided_positions():
     spec, inv, pa = spec_of(64, 1, True)
     x = torch.randn(2, 1, 33, 128, device=DEV)
