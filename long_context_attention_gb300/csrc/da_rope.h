@@ -28,7 +28,7 @@ struct AppendArgs {
   long long q_t, q_h, k_t, k_h, v_t, v_h, dem_t, dem_h;   // element strides (token, head)
   void *q_out;
   const int32_t *cu_tokens;
-  int N, adjacent, rotate, hpt, units, tokens;            // tokens: a block's run
+  int N, adjacent, hpt, units, tokens;                    // tokens: a block's run
   int *status;
 };
 

@@ -111,7 +111,6 @@ struct XWalk {
 // One warp: key tile `tile` of the prefix for key head hkv into `dst`.  Pages
 // past the prefix's end, or not in the pool, are read past the pool's end:
 // zeros.  `page` is this lane's page of the tile (x_page), fetched beforehand.
-template <int D>
 __device__ __forceinline__ int x_page(const PagedDecode &p, const PgtPlan &w, int tile, int lane) {
   const int rows = min(1 << w.page_shift, kPgxTile);
   const int key = tile * kPgxTile + lane * rows;
@@ -194,10 +193,10 @@ __global__ void __launch_bounds__(XKeys<D>::kThreads, 2)
   if (warp == 8) {
     int issued = 0;
     for (; it.c.n > 0; it.next(p, w)) {
-      int page = x_page<D>(p, w, it.c.tile, lane);
+      int page = x_page(p, w, it.c.tile, lane);
       bool ok = true;
       for (int k = 0; k < it.c.n; ++k, ++issued) {
-        const int ahead = k + 1 < it.c.n ? x_page<D>(p, w, it.c.tile + k + 1, lane) : -1;
+        const int ahead = k + 1 < it.c.n ? x_page(p, w, it.c.tile + k + 1, lane) : -1;
         const int s = issued % C::kStages;
         ok = warp_wait(&k_empty[s], ((issued / C::kStages) & 1) ^ 1, wc);
         if (!ok) break;
@@ -425,10 +424,10 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
     const int stages = isk ? C::kKStages : C::kVStages;
     int issued = 0;
     for (; it.c.n > 0; it.next(p, w)) {
-      int page = x_page<D>(p, w, it.c.tile, lane);
+      int page = x_page(p, w, it.c.tile, lane);
       bool ok = true;
       for (int k = 0; k < it.c.n; ++k, ++issued) {
-        const int ahead = k + 1 < it.c.n ? x_page<D>(p, w, it.c.tile + k + 1, lane) : -1;
+        const int ahead = k + 1 < it.c.n ? x_page(p, w, it.c.tile + k + 1, lane) : -1;
         const int s = issued % stages;
         ok = warp_wait(&empty[s], ((issued / stages) & 1) ^ 1, wc);
         if (!ok) break;
@@ -777,11 +776,9 @@ __global__ void __launch_bounds__(XVal<D>::kThreads, 1)
 }
 
 // ============================================================================ host
-template <int D>
-static bool x_maps(const PagedDecode &p, CUtensorMap *km, CUtensorMap *vm) {
+static bool x_map(const PagedDecode &p, const void *pages, CUtensorMap *m) {
   const int64_t num = (int64_t)p.c.num_pages * p.c.Hkv;
-  return make_page_map(km, p.c.k_pages, num > 0 ? num : 1, p.c.page_size, kPgxTile, D, DA_BF16) &&
-         make_page_map(vm, p.c.v_pages, num > 0 ? num : 1, p.c.page_size, kPgxTile, D, DA_BF16);
+  return make_page_map(m, pages, num > 0 ? num : 1, p.c.page_size, kPgxTile, p.c.d, DA_BF16);
 }
 
 template <int D>
@@ -801,8 +798,8 @@ static int pgx_prepare() {
 
 template <int D>
 static int launch_keys_t(const PagedDecode &p, const PgtPlan &w, cudaStream_t stream) {
-  CUtensorMap km, vm;
-  if (pgx_prepare<D>() != DA_OK || !x_maps<D>(p, &km, &vm)) return DA_ERR_CUDA;
+  CUtensorMap km;
+  if (pgx_prepare<D>() != DA_OK || !x_map(p, p.c.k_pages, &km)) return DA_ERR_CUDA;
   return launch_after(pgx_keys<D>, w.x_keys.ctas, XKeys<D>::kThreads, XKeys<D>::kSmemBytes, stream, p, w, km) ==
                  cudaSuccess
              ? DA_OK
@@ -812,7 +809,7 @@ static int launch_keys_t(const PagedDecode &p, const PgtPlan &w, cudaStream_t st
 template <int D>
 static int launch_values_t(const PagedDecode &p, const PgtPlan &w, cudaStream_t stream) {
   CUtensorMap km, vm;
-  if (pgx_prepare<D>() != DA_OK || !x_maps<D>(p, &km, &vm)) return DA_ERR_CUDA;
+  if (pgx_prepare<D>() != DA_OK || !x_map(p, p.c.k_pages, &km) || !x_map(p, p.c.v_pages, &vm)) return DA_ERR_CUDA;
   const cudaError_t e = p.earlier ? launch_after(pgx_values<D, true>, w.x_values.ctas, XVal<D>::kThreads,
                                                  XVal<D>::kSmemBytes, stream, p, w, km, vm)
                                   : launch_after(pgx_values<D, false>, w.x_values.ctas, XVal<D>::kThreads,

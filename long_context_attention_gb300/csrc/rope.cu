@@ -130,7 +130,7 @@ template <typename E, bool ADJ>
 struct RopeUnit {
   static constexpr int N = RopeVec<E>::N;
   int va, vb;                 // element offsets of the two vectors
-  bool rot_a, rot_b;          // whether they rotate (half-split: both or none; adjacent: in part)
+  bool rot;                   // whether any of their pairs rotate (half-split: all or none)
   int pairs;
   float c[N], s[N];           // half-split: N pairs; adjacent: N / 2 of each vector
 
@@ -139,13 +139,12 @@ struct RopeUnit {
     if constexpr (ADJ) {
       va = 2 * u * N;
       vb = va + N;
-      rot_a = va < 2 * n_pairs;
-      rot_b = vb < 2 * n_pairs;
+      rot = va < 2 * n_pairs;
     } else {
       const int rot_units = n_pairs / N;
-      rot_a = rot_b = u < rot_units;
-      va = rot_a ? u * N : 2 * n_pairs + 2 * (u - rot_units) * N;
-      vb = rot_a ? va + n_pairs : va + N;
+      rot = u < rot_units;
+      va = rot ? u * N : 2 * n_pairs + 2 * (u - rot_units) * N;
+      vb = rot ? va + n_pairs : va + N;
     }
   }
   // `angle(j, c, s)` gives the cosine and sine of pair j.
@@ -157,7 +156,7 @@ struct RopeUnit {
       if constexpr (ADJ) {
         if (va / 2 + i < pairs) angle(va / 2 + i, c[i], s[i]);
       } else {
-        if (rot_a) angle(va + i, c[i], s[i]);
+        if (rot) angle(va + i, c[i], s[i]);
       }
     }
   }
@@ -171,7 +170,7 @@ struct RopeUnit {
   }
   __device__ __forceinline__ void apply(uint4 &a, uint4 &b) const {
     using V = RopeVec<E>;
-    if (!rot_a) return;       // passes bit for bit (rot_b implies rot_a)
+    if (!rot) return;         // passes bit for bit
     float x[N], y[N];
     V::unpack(a, x);
     V::unpack(b, y);
@@ -568,7 +567,7 @@ __global__ void __launch_bounds__(kRopeThreads)
     ru.place(u, h0 < h_turn ? rp.n_pairs : 0);
     if (mine && tt0 < last) load(tt0, h0);
   }
-  table.fill(rp);
+  if (!is_demand) table.fill(rp);
   const int32_t *cu = a.cu_tokens, *lens = c.seq_lens;
   if (c.S + 1 <= kAppendSearch) {
     for (int i = threadIdx.x; i <= c.S; i += kRopeThreads) {
