@@ -398,9 +398,10 @@ int dilution_attn_paged_append(const void *q, const int64_t *q_strides, const vo
  *
  * prefix_table (nullable): DEVICE [n_prefix_pages] page ids.  The first
  * n_prefix_pages * page_size tokens of EVERY sequence then live in those
- * pages, whose keys and values are read once for the whole batch (the first
- * n_prefix_pages entries of each page_table row are not read); each sequence
- * keeps its own demand over them.  A length below the prefix's, other than 0,
+ * pages, whose keys and values are read for 8 to 64 rows (sequence, query head)
+ * of a key head at a time; short calls read them for every sequence, from L2 (the
+ * first n_prefix_pages entries of each page_table row are not read).  Each
+ * sequence keeps its own demand over them.  A length below the prefix's, other than 0,
  * records DA_ERR_INVALID.  The result is that of the same call with the
  * prefix's pages in every page_table row.
  *
@@ -411,6 +412,10 @@ int dilution_attn_paged_append(const void *q, const int64_t *q_strides, const vo
  * s*Hq + h.  tau, eps, flags (DA_FLAG_EARLIER_DEMAND_ONLY) as for
  * dilution_attn_decode_step_ex; DA_BF16 needs eps >= 1e-18 as the forward.
  * Repeated calls give equal bits.  Errors as for dilution_attn_decode_step_ex.
+ * DA_BF16: products of bf16 operands summed in fp32; the shares enter the value
+ * product as two bf16 terms (2^-16 relative), exponentials and reciprocals are
+ * the approximate instructions: besides the logits' own rounding, out is within
+ * 2^-14 max |v| of the formula before its rounding to bf16.
  *
  * dilution_attn_paged_decode_ex records what the kernels find in `status` (DEVICE,
  * 256 bytes, 256-byte aligned, zeroed once by the caller) instead of the

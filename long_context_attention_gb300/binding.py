@@ -765,7 +765,7 @@ def dilution_attn_paged_decode(q, cache, max_len: int, out=None, *, prefix_table
     already appended): q [S, Hq, d] -> ``out`` [S, Hq, d]; each key's demand
     grows by its bid.  ``max_len``: upper bound of cache.seq_lens.
     ``prefix_table`` (int32 [n]): pages of the tokens that every sequence
-    shares, read once for the batch.  Bad lengths or page ids are found on the
+    shares, read for many sequences at once.  Bad lengths or page ids are found on the
     device: read them with dilution_attn_get_error on ``workspace``, or on
     ``cache.status`` if none is given."""
     lib = _lib or load()

@@ -30,11 +30,20 @@ constexpr int kPgtHead = 4;   // units of a segment before its first tile (a pie
 // Which kernels take a shared prefix.  The streaming kernels work on 16 rows (of
 // the batch's sequences x query heads of one key head) at a time and read the
 // prefix's keys from L2 once per 16 rows; the tcgen05 kernels take 64 rows, but
-// are two launches more.  Device time of a step, tcgen05 against streaming, in us:
-// 96 rows x 12 key heads x 16384 keys (19 M pairs) 77 against 111, 64 x 12 x 8192 (6.3
-// M) 46.7 against 55.3, 46 x 12 x 9216 (5.1 M) 41.9 against 45.5, 24 x 12 x 16384 (4.7
-// M) 40.5 against 38.4, 17 x 12 x 16384 (3.3 M) 38.1 against 35.8, 44 x 2 x 37824 (3.3 M)
-// 36.1 against 30.0, 96 x 2 x 16384 at d = 128 (3.1 M) 37.4 against 33.0.
+// are two launches more.  Device time of a step, tcgen05 against streaming, in us
+// (rows x key heads x keys; below 4 M pairs and above 6 M measured on other inputs):
+//   d = 64:  96 x 12 x 16384 (19 M pairs) 77 / 111, 64 x 12 x 8192 (6.3 M) 46.7 / 55.3,
+//            40 x 8 x 16384 (5.2 M) 45.7 / 45.7, 46 x 12 x 9216 (5.1 M) 48.1 / 52.1,
+//            24 x 12 x 16384 (4.7 M) 46.6 / 46.6, 64 x 2 x 36864 (4.7 M) 41.3 / 40.3,
+//            46 x 12 x 8192 (4.5 M) 45.4 / 46.9, 64 x 1 x 70016 (4.5 M) 48.2 / 37.7,
+//            24 x 12 x 14592 (4.2 M) 45.4 / 40.3, 17 x 8 x 30848 (4.2 M) 58.3 / 47.6,
+//            17 x 12 x 16384 (3.3 M) 38.1 / 35.8, 44 x 2 x 37824 (3.3 M) 36.1 / 30.0;
+//   d = 128: 40 x 8 x 16384 (5.2 M) 57.3 / 66.2, 24 x 12 x 16384 (4.7 M) 62.8 / 66.1,
+//            96 x 4 x 12288 (4.7 M) 43.8 / 42.9, 64 x 2 x 36864 (4.7 M) 50.4 / 49.3,
+//            64 x 1 x 73728 (4.7 M) 59.2 / 47.2, 24 x 12 x 14592 (4.2 M) 59.4 / 59.4,
+//            96 x 2 x 16384 (3.1 M) 37.4 / 33.0.
+// With many key heads the sides meet between 4.2 and 4.7 M pairs; with one key head or
+// 17 rows of a segment's 64 the streaming kernels are still faster just above the bound.
 constexpr int kPgxMinRows = 17;
 constexpr int64_t kPgxMinPairs = 4ll << 20;
 enum PgxUse { kPgxAuto, kPgxNever, kPgxAlways };

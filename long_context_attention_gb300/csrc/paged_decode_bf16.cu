@@ -573,9 +573,12 @@ static int launch_pgt_t(const PagedDecode &p, const PgtPlan &w, cudaStream_t str
       !make_page_map(&vm, p.c.v_pages, num > 0 ? num : 1, p.c.page_size, pgt_tile(D), D, DA_BF16))
     return DA_ERR_CUDA;
   // Stages of pgt_keys: 4 leave room for the next kernel's CTAs to begin beside
-  // the last of this one (8 x 12 x 131072: 510 us a step, 518 with 6); with a
-  // prefix its CTAs are few and short, and 6 measured 19.2 against 20.6 us (16 x
-  // 12 x 2048 + 300).
+  // the last of this one.  A step with 4 / 6 stages, us: 8 x 12 x 131072 519 / 525,
+  // three query heads a key head 204 / 206, 8 x 12 x 65536 at d = 128 499 / 502, 48
+  // ragged at d = 128 38.3 / 39.0.  With a prefix its CTAs are few and short: 16 x 12 x
+  // 2048 + 300 17.8 / 17.4, 64 x 12 x 131072 + 1000 261.2 / 260.9, 16 x 8192 + 300 with
+  // shared heads 20.6 / 20.5, 32 x 16 heads x 32768 at d = 128 76.3 / 76.4, 8 x 12 x 16384
+  // at d = 128 29.6 / 30.1.
   const int k_stages = p.prefix_len == 0 ? 4 : 6;
   constexpr int k_most = 1024 + 6 * kStageBytes;
   static_assert(k_most <= kPgtSmemPerCta, "two CTAs an SM");

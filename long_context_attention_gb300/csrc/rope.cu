@@ -222,8 +222,8 @@ struct RopePlace {
 constexpr int kRopeThreads = 128;
 // Heads loaded together: 4 in the rotation of more than 2 heads a thread (131072 x
 // 24 x 128 fp32: 480 us, 497 with 2), 2 of fewer (4 x 36238 tokens of 2 heads of 128:
-// 39.4 us, 42.7 with 4), where rows exchange their parts (121 us, 135 with 4, for 6
-// heads of the same tokens) and in the append (16 prompts: 24 us, 28 with 4).
+// 39.4 us, 42.7 with 4), where rows exchange their parts (6 heads of the same tokens, bf16:
+// 115 us, 135 with 4) and in the append (16 prompts: 24 us, 28 with 4).
 constexpr int kRopeBatch = 4, kFewBatch = 2;
 
 // The pairs' frequencies in turns and their axes, formed once a warp (every
@@ -337,7 +337,9 @@ __global__ void __launch_bounds__(kRopeThreads, BATCH <= 2 ? 8 : sizeof(E) == 2 
 // pieces (half-split pairs, n_pairs of any size: the partner of an element lies
 // anywhere in the row).  The lanes of a row exchange it through shared memory.
 // (One thread per pair with 2-byte accesses took 539 us for 2 x 48 x 51971 x 64
-// bf16 with 3 pairs, whose copies take 188.)
+// bf16 with 3 pairs, whose copies take 188.)  4 x 36238 tokens of 6 heads with 5 pairs
+// less than whole rows: bf16 of 64 / 128 61.6 / 115 us (the bytes 33 / 66), fp32 82.6 / 159
+// (66 / 131): every lane forms the angles of its own elements, so each pair's twice.
 template <typename E>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_any_kernel(RopeTensor q, RopeTensor k, const __grid_constant__ RopeParams rp, RopeWalk w, int Hq, int Hk, int hpt) {
@@ -416,7 +418,9 @@ __device__ __forceinline__ void rope_pair(const E *src, E *dst, int j, int n_pai
   from_f32(fmaf(y, c, x * s), dst[b]);
 }
 
-// Any alignment: one thread per pair of elements (d / 2 of them a row).
+// Any alignment: one thread per pair of elements (d / 2 of them a row).  Bound by the
+// accesses of one element: 4 x 36238 tokens of 6 heads, half-split or adjacent pairs
+// alike, bf16 of 64 / 128 92 / 188 us (the bytes 33 / 66), fp32 98 / 193 (66 / 131).
 template <typename E>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_scalar_kernel(RopeTensor q, RopeTensor k, const __grid_constant__ RopeParams rp, int adjacent, RopeWalk w, int Hq,
