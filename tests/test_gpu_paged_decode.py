@@ -225,6 +225,96 @@ def test_more_sequences_than_one_part():
     step_and_check(cache, q, 66, tau_bh=tau, prefix_table=pt)
 
 
+def test_parts_that_take_their_prefix_differently():
+    # 900 sequences go as 704 and 196: 704 rows x 8192 keys to the kernels for many rows, the rest to the streaming ones
+    S, prefix = 900, 8192
+    lens = [0 if i % 50 == 0 else prefix + i % 70 for i in range(S)]
+    cache, q, pt = make_cache(S, lens, 1, 1, 64, 64, "bf16", seed=7, prefix=prefix, extra_width=1)
+    before = cache.demand_pages.clone()
+    out = b.dilution_attn_paged_decode(q, cache, max(lens), prefix_table=pt)
+    assert b.dilution_attn_get_error(cache.status) == b.DA_OK
+    rows = [0, 1, 333, 703, 704, 750, 899]
+    one = b.PagedCache(cache.k_pages, cache.v_pages, before.clone(), cache.page_table[rows].contiguous(),
+                       cache.demand_table[rows].contiguous(), cache.seq_lens[rows].contiguous())
+    ref = oracle_step(one, q[rows])
+    mine = one.demand_table[one.demand_table >= 0].long()
+    one.demand_pages[mine] = cache.demand_pages[mine]
+    check_step(one, q[rows], before, out[rows], ref)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("S,Hq,Hkv,d,page,prefix", [(5, 4, 2, 64, 16, 272), (3, 4, 4, 128, 64, 2048)])
+def test_max_len_is_the_prefix(S, Hq, Hkv, d, page, prefix, dtype):
+    lens = [0 if i == 3 else prefix for i in range(S)]
+    cache, q, pt = make_cache(S, lens, Hq, Hkv, d, page, dtype, seed=3, prefix=prefix)
+    step_and_check(cache, q, prefix, prefix_table=pt)
+
+
+@pytest.mark.parametrize("dtype,S,Hq,page,prefix,lens", [
+    ("bf16", 3, 4, 64, 0, [700, 300, 1]), ("bf16", 3, 4, 64, 0, [7000, 3000, 1]), ("f32", 3, 4, 64, 0, [700, 300, 1]),
+    ("bf16", 20, 8, 64, 26304, [26304 + i for i in range(20)])])
+def test_demand_pool_past_32_bit_offsets(dtype, S, Hq, page, prefix, lens):
+    # the same pages at the end of a pool of more than 2^31 floats: the same bits, of an append and of a step
+    small, q, pt = make_cache(S, lens, Hq, 2, 64, page, dtype, seed=9, prefix=prefix)
+    n = small.demand_pages.shape[0]
+    skip = (1 << 31) // (Hq * page) + 3
+    pool = torch.empty(skip + n, Hq, page, device=DEV)
+    pool[skip:] = small.demand_pages
+    table = torch.where(small.demand_table >= 0, small.demand_table + skip, small.demand_table)
+    big = b.PagedCache(small.k_pages, small.v_pages, pool, small.page_table, table, small.seq_lens)
+    k, demand = torch.randn(S, 2, 64, device=DEV).to(q.dtype), torch.rand(S, Hq, device=DEV)
+    cu = torch.arange(S + 1, dtype=torch.int32, device=DEV)
+    outs = []
+    for c in (big, small):
+        b.dilution_attn_paged_append(None, k, k, c, cu, demand=demand)
+        outs.append(b.dilution_attn_paged_decode(q, c, max(lens), prefix_table=pt))
+        assert b.dilution_attn_get_error(c.status) == b.DA_OK
+    assert torch.equal(*outs) and torch.equal(pool[skip:], small.demand_pages)
+
+
+def test_threads_with_their_own_streams():
+    """Four host threads append and decode at once, each on its own stream and cache: the bits of one after another."""
+    import threading
+    cases = [(5, [300, 7, 130, 1, 900], 4, 2, 64, 32, "bf16", 0, 900), (4, [5000, 1, 0, 3000], 8, 2, 128, 64, "bf16", 0, 5000),
+             (3, [70, 2600, 500], 4, 4, 64, 16, "f32", 0, 2600), (20, [26272 + i for i in range(20)], 8, 2, 64, 32, "bf16", 26272, 26291)]
+    made, want, got = [], [], [None] * len(cases)
+    for i, (S, lens, Hq, Hkv, d, page, dtype, prefix, cap) in enumerate(cases):
+        cache, q, pt = make_cache(S, lens, Hq, Hkv, d, page, dtype, seed=200 + i, prefix=prefix)
+        k = torch.randn(S, Hkv, d, device=DEV).to(q.dtype)
+        cu = torch.tensor([0] + list(np.cumsum([min(n, 1) for n in lens])), dtype=torch.int32, device=DEV)
+        made.append((cache, q, pt, k, cu, cap, b.dilution_attn_paged_decode_workspace(cache, cap), torch.cuda.Stream()))
+
+    def steps(i, stream):
+        cache, q, pt, k, cu, cap, ws, _ = made[i]
+        b.dilution_attn_paged_append(None, k, k, cache, cu, workspace=ws, stream=stream)
+        for _ in range(5):
+            out = b.dilution_attn_paged_decode(q, cache, cap, prefix_table=pt, workspace=ws, stream=stream)
+        return out
+
+    before = [m[0].demand_pages.clone() for m in made]
+    torch.cuda.synchronize()
+    for i in range(len(cases)):
+        want.append((steps(i, None).clone(), made[i][0].demand_pages.clone()))
+        made[i][0].demand_pages.copy_(before[i])
+    torch.cuda.synchronize()
+    gate = threading.Barrier(len(cases))
+
+    def work(i):
+        gate.wait()
+        got[i] = steps(i, made[i][7])
+        made[i][7].synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i, (out, demand) in enumerate(want):
+        assert b.dilution_attn_get_error(made[i][6]) == b.DA_OK
+        assert torch.equal(got[i], out) and torch.equal(made[i][0].demand_pages, demand), i
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_shared_prefix_with_idle_slots_and_nothing_of_their_own(dtype):
     # idle slots among the sequences, and sequences that end with the prefix
