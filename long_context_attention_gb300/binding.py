@@ -613,6 +613,29 @@ def dilution_attn_rope_bwd(dq_out, dk_out, positions, rope, dq=None, dk=None, *,
 
 
 # ---------------------------------------------------------------------------- paged cache
+def _zeroed_status(device):
+    """A status block that is zero for calls on every stream, whatever the current one still has to do."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(256, dtype=torch.uint8, device=device)
+    side = torch.cuda.Stream(device)
+    with torch.cuda.stream(side):
+        t = torch.zeros(256, dtype=torch.uint8, device=device)
+    side.synchronize()
+    return t
+
+
+_graph_status: dict = {}   # the status blocks of captured calls: a graph may outlive the cache object
+
+
+def _own_status(cache, stream):
+    """The cache's status block for a call on ``stream``: not handed on, if the cache goes, before the call has ended
+    (of a captured call, not at all)."""
+    cache.status.record_stream(torch.cuda.current_stream() if stream is None else stream)
+    if torch.cuda.is_current_stream_capturing():
+        _graph_status[id(cache.status)] = cache.status
+    return cache.status
+
+
 class _CPagedCache(ctypes.Structure):
     _fields_ = [(n, _c_void_p) for n in ("k_pages", "v_pages", "demand_pages", "page_table", "demand_table", "seq_lens")] \
         + [(n, ctypes.c_int32) for n in ("S", "Hq", "Hkv", "d", "page_size", "num_pages", "num_demand_pages",
@@ -658,7 +681,7 @@ class PagedCache:
                                                         seq_lens)), S, Hq, Hkv, d, page_size, num_pages,
                                num_demand_pages, max_pages, self._code)
         self._ref = ctypes.byref(self._c)
-        self.status = torch.zeros(256, dtype=torch.uint8, device=self.device)
+        self.status = _zeroed_status(self.device)
         self._dev, self._q_shape, self._cu_shape = k_pages.get_device(), torch.Size((S, Hq, d)), torch.Size((S + 1,))
 
 
@@ -728,7 +751,7 @@ def dilution_attn_paged_append(q, k, v, cache, cu_tokens, q_out=None, *, rope=No
             _need_any_strides(demand, "demand", (N, Hq), torch.float32)
         dp, sd = demand.data_ptr(), _c_strides(demand.stride(), 2)
     if workspace is None:
-        workspace = cache.status     # an append needs nothing else
+        workspace = _own_status(cache, stream)     # an append needs nothing else
     else:
         _need_bytes(workspace, dev)
     st = lib.dilution_attn_paged_append(qp, sq, k.data_ptr(), sk, v.data_ptr(), sv, dp, sd, qop, cu_tokens.data_ptr(), N,
@@ -784,7 +807,7 @@ def dilution_attn_paged_decode(q, cache, max_len: int, out=None, *, prefix_table
     if workspace is None:
         need = dilution_attn_paged_decode_workspace_size(cache.S, cache.Hq, cache.Hkv, cache.d, int(max_len), n_prefix,
                                                          cache.page_size, cache._code)
-        workspace, status = _new(max(need, 256), torch.uint8, cache.device, stream), cache.status.data_ptr()
+        workspace, status = _new(max(need, 256), torch.uint8, cache.device, stream), _own_status(cache, stream).data_ptr()
     else:
         _need_bytes(workspace, dev)
         status = workspace.data_ptr()

@@ -518,6 +518,64 @@ def test_call_on_another_stream_without_buffers(max_len):
     assert len(junk) == 8
 
 
+def test_error_of_a_call_beside_a_busy_stream():
+    # a cache made while the current stream is behind: its status block is zero for a call on another stream already
+    made, q, _ = make_cache(3, [300, 7, 130], 4, 2, 64, 32, "bf16", seed=66)
+    tensors = [getattr(made, n) for n in ("k_pages", "v_pages", "demand_pages", "page_table", "demand_table", "seq_lens")]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    b.dilution_attn_paged_decode(q, made, 300, stream=side)   # memory for the call below: no allocation stops the device
+    made.page_table[0, 1] = 10 ** 6
+    junk = [torch.full((256,), 0x55, dtype=torch.uint8, device=DEV) for _ in range(64)]
+    busy = torch.zeros(1 << 28, device=DEV)
+    torch.cuda.synchronize()
+    del junk                                             # what the next small block may hold
+    for _ in range(50):
+        busy.add_(1.0)
+    cache = b.PagedCache(*tensors)
+    b.dilution_attn_paged_decode(q, cache, 300, stream=side)
+    side.synchronize()
+    assert b.dilution_attn_get_error(cache.status, side) == b.DA_ERR_INVALID
+    torch.cuda.synchronize()
+    assert b.dilution_attn_get_error(cache.status) == b.DA_OK
+
+
+def test_error_of_a_call_whose_cache_is_gone():
+    # the call still runs when its cache is dropped: its error does not land in a later cache's status block
+    made, q, _ = make_cache(3, [300, 7, 130], 4, 2, 64, 32, "bf16", seed=66)
+    tensors = [getattr(made, n) for n in ("k_pages", "v_pages", "demand_pages", "page_table", "demand_table", "seq_lens")]
+    k, cu = torch.zeros(3, 2, 64, dtype=q.dtype, device=DEV), torch.arange(4, dtype=torch.int32, device=DEV)
+    made.page_table[0, :] = 10 ** 6
+    busy = torch.zeros(1 << 28, device=DEV)
+    warm = [b.PagedCache(*tensors) for _ in range(64)]            # memory for what follows: no allocation stops the device
+    b.dilution_attn_paged_decode(q, made, 300)
+    torch.cuda.synchronize()
+    del warm
+    for call in ("append", "decode"):
+        for _ in range(50):
+            busy.add_(1.0)
+        cache = b.PagedCache(*tensors)
+        if call == "append":
+            b.dilution_attn_paged_append(None, k, k, cache, cu)
+        else:
+            b.dilution_attn_paged_decode(q, cache, 300)
+        del cache
+        later = [b.PagedCache(*tensors) for _ in range(64)]       # the streams of the blocks repeat after 32
+        torch.cuda.synchronize()
+        assert not any(c.status.any() for c in later)
+    # a graph outlives the cache object whose tensors it reads
+    cache = b.PagedCache(*tensors)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.dilution_attn_paged_append(None, k, k, cache, cu)
+        b.dilution_attn_paged_decode(q, cache, 300)
+    del cache, later
+    later = [b.PagedCache(*tensors) for _ in range(64)]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert not any(c.status.any() for c in later)
+
+
 def test_pool_past_32_bit_offsets():
     # pools of more than 2^32 bytes and 2^31 elements: the sequence's pages lie at the end
     page, d, Hkv = 256, 128, 4
