@@ -433,6 +433,76 @@ int dilution_attn_paged_decode_ex(const void *q, const dilution_attn_paged_cache
                                   float eps, int flags, void *workspace, size_t workspace_bytes, void *status,
                                   void *stream);
 
+/* Chunks of new tokens over the paged cache: several decode steps of every
+ * sequence at once, for drafted tokens to be verified, for parts of long
+ * prompts, and for whole prompts of different lengths packed one behind the
+ * other.  Sequence s has n = cu_tokens[s+1] - cu_tokens[s] queries: its LAST n
+ * tokens, which have been appended (with demand 0; seq_lens counts them).  For
+ * query i of them, at place P + i with P = seq_lens[s] - n, over the keys
+ * t <= P + i:
+ *     p_t = softmax_t(tau q.k_t / sqrt(d)),   total_t += p_t,
+ *     share_t = p_t / (total_t + eps),        out = sum share_t v_t / sum share_t,
+ * query after query, where total_t begins as what the key's demand page holds and
+ * goes back there after the last query.  (DA_FLAG_EARLIER_DEMAND_ONLY: the total
+ * before p_t.)  That is n calls of dilution_attn_paged_decode, a token longer each
+ * time; n = seq_lens[s] with demand 0 is dilution_attn_fwd of the prompt.
+ * q, out [N,Hq,d] contiguous; out may be q.  cu_tokens: DEVICE [S+1] int32 as for
+ * dilution_attn_paged_append; rows of q from cu_tokens[S] on are padding: not read,
+ * and their rows of out not written.  A sequence without new tokens is left as it is.
+ * max_new, max_len: host upper bounds of the sequences' new tokens and of seq_lens
+ * (max_len at most max_pages * page_size).  A sequence with more new tokens than
+ * max_new or than its length, a length outside 0 .. max_len, cu_tokens that decrease
+ * or pass N record DA_ERR_INVALID; such a sequence's rows of out are not written and
+ * its demand stays.  A page id outside the pool records it too, and the sequence's
+ * results are unspecified.
+ * tau_bh: nullable device [S*Hq], index s*Hq + h.  tau, eps, flags as for
+ * dilution_attn_paged_decode.  status: DEVICE, 256 bytes, 256-byte aligned, zeroed
+ * once by the caller, or NULL for the workspace's first 256 bytes.  The workspace is
+ * overwritten from byte 256 on: calls that may overlap on the GPU need workspaces
+ * of their own.  Repeated calls give equal bits.  Errors as for
+ * dilution_attn_paged_decode_ex. */
+size_t dilution_attn_paged_chunk_workspace_size(int S, int Hq, int Hkv, int d, int N, int max_new, int max_len, int dtype);
+
+int dilution_attn_paged_chunk(const void *q, const dilution_attn_paged_cache *cache, const int32_t *cu_tokens, int N,
+                              int max_new, int max_len, void *out, float tau, const float *tau_bh, float eps, int flags,
+                              void *workspace, size_t workspace_bytes, void *status, void *stream);
+
+/* Eviction: the cache keeps the tokens that have received the most attention.
+ * Sequence s keeps m = min(seq_lens[s], keep[s]) tokens of each key head: those with
+ * the highest score, equal scores by the lower place.  A token's score is the sum
+ * of the totals of the key head's query heads, added in fp32 in the heads' order;
+ * the first `sinks` and the last `recent` tokens, and those whose score is NaN,
+ * score +infinity.  The tokens that stay keep their order and become rows
+ * 0 .. m - 1 (keys, values and totals move together, bit for bit), so that after
+ * an eviction one row holds different tokens in different key heads: keys carry
+ * their rotation, and later tokens need their positions passed to
+ * dilution_attn_paged_append.
+ *   dst_page_table, dst_demand_table: both NULL: in place.  Otherwise DEVICE
+ *       [S][dst_max_pages] tables of the same pools, dst_max_pages * page_size at
+ *       least min(max_keep, max_len), that receive the rows that stay, of
+ *       sequences that lose nothing too.  A page named there is either the source's
+ *       at the same place of the same sequence or one that the call does not read.
+ *       Only rows whose place changes are written, so pages that sequences share
+ *       keep their contents as far as every key head keeps all their tokens (a
+ *       shared prefix of `sinks` tokens).
+ *   keep: DEVICE [S] int32.  max_keep, max_len: host upper bounds of m and of
+ *       seq_lens (max_len at most max_pages * page_size).
+ *   new_lens: DEVICE [S] int32, receives m; may be cache->seq_lens itself.
+ *   kept: nullable DEVICE [S][Hkv][max_keep] int32, receives the places that the
+ *       rows had, then -1.
+ * A length outside 0 .. max_len, a negative keep[s] or m > max_keep records
+ * DA_ERR_INVALID; the sequence is left as it is, new_lens[s] is its length, kept all
+ * -1.  A page id outside the pool records it too; its rows stay where they are, and
+ * which tokens the sequence keeps is unspecified.
+ * status and workspace as for dilution_attn_paged_chunk.  Repeated calls on equal
+ * contents give equal bits. */
+size_t dilution_attn_paged_evict_workspace_size(int S, int Hkv, int max_keep, int max_len);
+
+int dilution_attn_paged_evict(const dilution_attn_paged_cache *cache, const int32_t *dst_page_table,
+                              const int32_t *dst_demand_table, int dst_max_pages, const int32_t *keep, int max_keep,
+                              int max_len, int sinks, int recent, int32_t *new_lens, int32_t *kept, void *workspace,
+                              size_t workspace_bytes, void *status, void *stream);
+
 /* ------------------------------------------------------------------------
  * Synchronises `stream`, reads the status word that kernels of the last call
  * on `workspace` may have set, clears it and returns it (DA_OK if none).

@@ -69,6 +69,12 @@ _SIGNATURES = {
                                                              _c_int, _c_void_p, _c_size_t, _c_void_p]),
     "dilution_attn_paged_decode_ex": (_c_int, [_c_void_p] * 3 + [_c_int, _c_int, _c_void_p, _c_float, _c_void_p, _c_float,
                                                                 _c_int, _c_void_p, _c_size_t, _c_void_p, _c_void_p]),
+    "dilution_attn_paged_chunk_workspace_size": (_c_size_t, [_c_int] * 8),
+    "dilution_attn_paged_chunk": (_c_int, [_c_void_p] * 3 + [_c_int] * 3 + [_c_void_p, _c_float, _c_void_p, _c_float, _c_int,
+                                                                           _c_void_p, _c_size_t, _c_void_p, _c_void_p]),
+    "dilution_attn_paged_evict_workspace_size": (_c_size_t, [_c_int] * 4),
+    "dilution_attn_paged_evict": (_c_int, [_c_void_p] * 3 + [_c_int, _c_void_p] + [_c_int] * 4 + [_c_void_p] * 3 +
+                                  [_c_size_t, _c_void_p, _c_void_p]),
     "dilution_attn_debug_paged_decode_stall": (_c_int, [_c_void_p] * 3 + [_c_int, _c_int, _c_void_p, _c_float, _c_float,
                                                                          _c_void_p, _c_size_t, _c_void_p, _c_int, _c_int,
                                                                          ctypes.c_longlong]),
@@ -841,6 +847,125 @@ def dilution_attn_debug_paged_decode_stall(q, cache, max_len: int, *, workspace,
                                                     _stream_id(stream, dev), int(stall_kernel), int(stall_block),
                                                     int(wait_limit_ns))
     return int(st), out
+
+
+def dilution_attn_paged_chunk_workspace_size(S: int, Hq: int, Hkv: int, d: int, N: int, max_new: int, max_len: int,
+                                             dtype: int) -> int:
+    return int(load().dilution_attn_paged_chunk_workspace_size(S, Hq, Hkv, d, N, max_new, max_len, dtype))
+
+
+def dilution_attn_paged_chunk_workspace(cache, N: int, max_new: int, max_len: int):
+    """A workspace for dilution_attn_paged_chunk over ``cache`` with up to ``N``
+    new tokens, ``max_new`` of a sequence, and lengths up to ``max_len``, its
+    status block zeroed."""
+    need = dilution_attn_paged_chunk_workspace_size(cache.S, cache.Hq, cache.Hkv, cache.d, int(N), int(max_new), int(max_len),
+                                                    cache._code)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=cache.device)
+    ws[:256].zero_()
+    return ws
+
+
+def _call_workspace(cache, need, workspace, stream, dev):
+    """(workspace, status pointer) of a call: its own workspace or one for it alone, with the cache's status block."""
+    if workspace is None:
+        return _new((max(need(), 256),), torch.uint8, cache.device, stream), _own_status(cache, stream).data_ptr()
+    _need_bytes(workspace, dev)
+    return workspace, workspace.data_ptr()
+
+
+def dilution_attn_paged_chunk(q, cache, cu_tokens, max_new: int, max_len: int, out=None, *, tau: float = 1.0, tau_bh=None,
+                              eps: float = 1e-6, flags: int = 0, workspace=None, stream=None, check: bool = True):
+    """The new tokens of every sequence of ``cache`` (already appended) against
+    it, query after query: q [N, Hq, d], sequence s has queries cu_tokens[s] ..
+    cu_tokens[s+1]-1 (int32 [S+1]), its last tokens -> ``out`` [N, Hq, d]; each
+    key's demand grows by its bids.  Whole prompts are sequences whose tokens are
+    all new.  ``max_new``, ``max_len``: upper bounds of a sequence's new tokens and
+    of cache.seq_lens.  Rows from cu_tokens[S] on are neither read nor written.
+    Bad lengths or page ids are found on the device: read them with
+    dilution_attn_get_error on ``workspace``, or on ``cache.status`` if none is
+    given."""
+    lib = _lib or load()
+    dev = _need_cache(cache)
+    if not isinstance(q, _Tensor) or q.dim() != 3:
+        raise ValueError("q must be [N, Hq, d]")
+    N = q.shape[0]
+    shape, dtype = (N, cache.Hq, cache.d), cache.dtype
+    _fit(q, "q", shape, dtype, dev)
+    _fit(cu_tokens, "cu_tokens", cache._cu_shape, torch.int32, dev)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=cache.device) if stream is None else \
+            _new(shape, dtype, cache.device, stream)
+    else:
+        _fit(out, "out", shape, dtype, dev)
+    workspace, status = _call_workspace(
+        cache, lambda: dilution_attn_paged_chunk_workspace_size(cache.S, cache.Hq, cache.Hkv, cache.d, N, int(max_new),
+                                                                int(max_len), cache._code), workspace, stream, dev)
+    st = lib.dilution_attn_paged_chunk(q.data_ptr(), cache._ref, cu_tokens.data_ptr(), N, int(max_new), int(max_len),
+                                       out.data_ptr(), float(tau),
+                                       None if tau_bh is None else _tau_bh_ptr(tau_bh, cache.S, cache.Hq), float(eps),
+                                       int(flags), workspace.data_ptr(), workspace.numel(), status, _stream_id(stream, dev))
+    if check and st != DA_OK:
+        _check(st, "dilution_attn_paged_chunk")
+    return out
+
+
+def dilution_attn_paged_evict_workspace_size(S: int, Hkv: int, max_keep: int, max_len: int) -> int:
+    return int(load().dilution_attn_paged_evict_workspace_size(S, Hkv, max_keep, max_len))
+
+
+def dilution_attn_paged_evict_workspace(cache, max_keep: int, max_len: int):
+    """A workspace for dilution_attn_paged_evict over ``cache``, its status block zeroed."""
+    need = dilution_attn_paged_evict_workspace_size(cache.S, cache.Hkv, int(max_keep), int(max_len))
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=cache.device)
+    ws[:256].zero_()
+    return ws
+
+
+def dilution_attn_paged_evict(cache, keep, max_keep: int, max_len: int, new_lens=None, *, sinks: int = 0, recent: int = 0,
+                              dst_page_table=None, dst_demand_table=None, kept=None, workspace=None, stream=None,
+                              check: bool = True):
+    """Every sequence of ``cache`` keeps the min(length, keep[s]) tokens of each
+    key head with the most demand (the sum of its query heads' totals), with the
+    first ``sinks`` and the last ``recent`` before all others; they become its
+    first rows, in their order.  keep: int32 [S]; ``max_keep``, ``max_len``: upper
+    bounds of what stays and of cache.seq_lens.  Returns ``new_lens`` (int32 [S];
+    may be cache.seq_lens).  With ``dst_page_table`` and ``dst_demand_table``
+    (int32 [S, pages], both or neither) the rows go to those pages of the same
+    pools instead of their own first ones.  ``kept`` (int32 [S, Hkv, max_keep])
+    receives the places that they had, then -1.  Bad lengths or page ids are found
+    on the device: read them with dilution_attn_get_error on ``workspace``, or on
+    ``cache.status`` if none is given."""
+    lib = _lib or load()
+    dev = _need_cache(cache)
+    lens_shape = cache.seq_lens.shape
+    _fit(keep, "keep", lens_shape, torch.int32, dev)
+    if new_lens is None:
+        new_lens = torch.empty(lens_shape, dtype=torch.int32, device=cache.device) if stream is None else \
+            _new(lens_shape, torch.int32, cache.device, stream)
+    else:
+        _fit(new_lens, "new_lens", lens_shape, torch.int32, dev)
+    if (dst_page_table is None) != (dst_demand_table is None):
+        raise ValueError("dst_page_table and dst_demand_table belong together")
+    dp = dd = kp = None
+    width = 0
+    if dst_page_table is not None:
+        _need(dst_page_table, "dst_page_table", None, torch.int32)
+        if dst_page_table.dim() != 2 or dst_page_table.shape[0] != cache.S:
+            raise ValueError(f"dst_page_table must be [{cache.S}, pages]")
+        _need(dst_demand_table, "dst_demand_table", dst_page_table.shape, torch.int32)
+        dp, dd, width = dst_page_table.data_ptr(), dst_demand_table.data_ptr(), dst_page_table.shape[1]
+    if kept is not None:
+        _fit(kept, "kept", (cache.S, cache.Hkv, int(max_keep)), torch.int32, dev)
+        kp = kept.data_ptr()
+    workspace, status = _call_workspace(
+        cache, lambda: dilution_attn_paged_evict_workspace_size(cache.S, cache.Hkv, int(max_keep), int(max_len)), workspace,
+        stream, dev)
+    st = lib.dilution_attn_paged_evict(cache._ref, dp, dd, width, keep.data_ptr(), int(max_keep), int(max_len), int(sinks),
+                                       int(recent), new_lens.data_ptr(), kp, workspace.data_ptr(), workspace.numel(), status,
+                                       _stream_id(stream, dev))
+    if check and st != DA_OK:
+        _check(st, "dilution_attn_paged_evict")
+    return new_lens
 
 
 # ----------------------------------------------------------------------------- misc

@@ -1,7 +1,9 @@
-// C ABI of the rotary positions, the paged append and the paged decode step:
-// argument validation and dispatch to the kernels.
+// C ABI of the rotary positions and the paged cache (append, decode step, chunks,
+// eviction): argument validation and dispatch to the kernels.
 #include <cmath>
 
+#include "da_chunk.cuh"
+#include "da_evict.h"
 #include "da_paged.h"
 #include "da_rope.h"
 
@@ -9,6 +11,12 @@ namespace da {
 size_t pgt_workspace(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int dtype);
 bool pgt_fits(int S, int Hq, int Hkv, int d, int max_len, int prefix_len, int dtype);
 int launch_paged_decode(const PagedDecode &p, cudaStream_t stream);
+inline int chunk_most(int N, int max_new, int max_len) {   // new tokens of a sequence, at most
+  const int n = max_new < N ? max_new : N;
+  return n < max_len ? n : max_len;
+}
+size_t chunk_workspace(int S, int Hq, int Hkv, int d, long long N, int max_new, int dtype);
+int launch_paged_chunk(const PagedChunk &p, cudaStream_t stream);
 }  // namespace da
 
 using namespace da;
@@ -167,6 +175,19 @@ int check_workspace(const void *ws, size_t bytes, size_t need) {
   return aligned(ws, 256) ? DA_OK : DA_ERR_INVALID;
 }
 
+bool options_valid(float tau, const float *tau_bh, float eps, int flags) {
+  return std::isfinite(tau) && tau >= 0.f && std::isfinite(eps) && eps > 0.f &&
+         (flags & ~DA_FLAG_EARLIER_DEMAND_ONLY) == 0 && aligned(tau_bh, 4);
+}
+int check_options(float tau, const float *tau_bh, float eps, int flags, int dtype) {
+  if (!options_valid(tau, tau_bh, eps, flags)) return DA_ERR_INVALID;
+  return dtype == DA_BF16 && eps < 1e-18f ? DA_ERR_UNSUPPORTED : DA_OK;
+}
+HeadScale head_scale(float tau, const float *tau_bh, int d) {
+  const double per_tau = 1.4426950408889634 / std::sqrt((double)d);
+  return HeadScale{tau_bh, (float)((double)tau * per_tau), per_tau};
+}
+
 PagedDebug no_stall() {
   PagedDebug d;
   for (int k = 0; k < kPagedKernels; ++k) d.limit_ns[k] = kWaitLimitNsHost, d.stall_block[k] = -1;
@@ -179,8 +200,7 @@ int decode_call(const void *q, const dilution_attn_paged_cache *cache, const int
   int st = check_cache(cache);
   if (st != DA_OK) return st;
   const dilution_attn_paged_cache &c = *cache;
-  if (!std::isfinite(tau) || tau < 0.f || !std::isfinite(eps) || eps <= 0.f) return DA_ERR_INVALID;
-  if ((flags & ~DA_FLAG_EARLIER_DEMAND_ONLY) != 0 || !aligned(tau_bh, 4)) return DA_ERR_INVALID;
+  if (!options_valid(tau, tau_bh, eps, flags)) return DA_ERR_INVALID;
   if (max_len < 0 || (int64_t)max_len > (int64_t)c.max_pages * c.page_size) return DA_ERR_INVALID;
   if (n_prefix_pages < 0 || (int64_t)n_prefix_pages * c.page_size > max_len) return DA_ERR_INVALID;
   if (n_prefix_pages > 0 && (prefix_table == nullptr || !aligned(prefix_table, 4))) return DA_ERR_INVALID;
@@ -202,8 +222,7 @@ int decode_call(const void *q, const dilution_attn_paged_cache *cache, const int
   p.prefix_table = n_prefix_pages > 0 ? prefix_table : nullptr;
   p.prefix_len = prefix_len;
   p.max_len = max_len;
-  const double per_tau = 1.4426950408889634 / std::sqrt((double)c.d);
-  p.hs = HeadScale{tau_bh, (float)((double)tau * per_tau), per_tau};
+  p.hs = head_scale(tau, tau_bh, c.d);
   p.eps = eps;
   p.earlier = (flags & DA_FLAG_EARLIER_DEMAND_ONLY) != 0;
   p.status = reinterpret_cast<int *>(status);
@@ -312,6 +331,84 @@ int dilution_attn_paged_decode_ex(const void *q, const dilution_attn_paged_cache
                                   int flags, void *workspace, size_t workspace_bytes, void *status, void *stream) {
   return decode_call(q, cache, prefix_table, n_prefix_pages, max_len, out, tau, tau_bh, eps, flags, workspace,
                      workspace_bytes, status, stream, no_stall());
+}
+
+size_t dilution_attn_paged_chunk_workspace_size(int S, int Hq, int Hkv, int d, int N, int max_new, int max_len, int dtype) {
+  if (dtype != DA_F32 && dtype != DA_BF16) return 0;
+  if (S < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || N < 0 || max_new < 0 || max_len < 0 || !head_dim_supported(d)) return 0;
+  return chunk_workspace(S, Hq, Hkv, d, N, chunk_most(N, max_new, max_len), dtype);
+}
+
+int dilution_attn_paged_chunk(const void *q, const dilution_attn_paged_cache *cache, const int32_t *cu_tokens, int N,
+                              int max_new, int max_len, void *out, float tau, const float *tau_bh, float eps, int flags,
+                              void *workspace, size_t workspace_bytes, void *status, void *stream) {
+  int st = check_cache(cache);
+  if (st != DA_OK) return st;
+  const dilution_attn_paged_cache &c = *cache;
+  st = check_options(tau, tau_bh, eps, flags, c.dtype);
+  if (st != DA_OK) return st;
+  if (N < 0 || max_new < 0 || max_len < 0 || (int64_t)max_len > (int64_t)c.max_pages * c.page_size) return DA_ERR_INVALID;
+  if (N > kMaxTokens || (int64_t)c.num_pages * c.Hkv > 0x7FFFFFFF) return DA_ERR_UNSUPPORTED;   // (a copy's coordinate)
+  if (N == 0 || c.S == 0) return DA_OK;
+  if (q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 16)) return DA_ERR_INVALID;
+  if (cu_tokens == nullptr || !aligned(cu_tokens, 4)) return DA_ERR_INVALID;
+  max_new = chunk_most(N, max_new, max_len);
+  st = check_workspace(workspace, workspace_bytes, chunk_workspace(c.S, c.Hq, c.Hkv, c.d, N, max_new, c.dtype));
+  if (st != DA_OK) return st;
+  if (status != nullptr && !aligned(status, 256)) return DA_ERR_INVALID;
+  PagedChunk p{};
+  p.c = c;
+  p.q = q;
+  p.out = out;
+  p.cu = cu_tokens;
+  p.N = N;
+  p.max_new = max_new;
+  p.max_len = max_len;
+  p.hs = head_scale(tau, tau_bh, c.d);
+  p.eps = eps;
+  p.earlier = (flags & DA_FLAG_EARLIER_DEMAND_ONLY) != 0;
+  p.status = reinterpret_cast<int *>(status != nullptr ? status : workspace);
+  p.ws = reinterpret_cast<uint8_t *>(workspace);
+  return launch_paged_chunk(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t dilution_attn_paged_evict_workspace_size(int S, int Hkv, int max_keep, int max_len) {
+  if (S < 0 || Hkv < 1 || max_keep < 0 || max_len < 0) return 0;
+  return evict_workspace(S, Hkv, max_keep < max_len ? max_keep : max_len, max_len).total;
+}
+
+int dilution_attn_paged_evict(const dilution_attn_paged_cache *cache, const int32_t *dst_page_table,
+                              const int32_t *dst_demand_table, int dst_max_pages, const int32_t *keep, int max_keep,
+                              int max_len, int sinks, int recent, int32_t *new_lens, int32_t *kept, void *workspace,
+                              size_t workspace_bytes, void *status, void *stream) {
+  int st = check_cache(cache);
+  if (st != DA_OK) return st;
+  const dilution_attn_paged_cache &c = *cache;
+  if (max_keep < 0 || max_len < 0 || sinks < 0 || recent < 0 ||
+      (int64_t)max_len > (int64_t)c.max_pages * c.page_size)
+    return DA_ERR_INVALID;
+  if ((dst_page_table == nullptr) != (dst_demand_table == nullptr) || !aligned(dst_page_table, 4) ||
+      !aligned(dst_demand_table, 4))
+    return DA_ERR_INVALID;
+  if (kept == nullptr && max_keep > max_len) max_keep = max_len;   // (kept's rows hold max_keep)
+  const int most = max_keep < max_len ? max_keep : max_len;
+  if (dst_page_table != nullptr && (dst_max_pages < 0 || (int64_t)dst_max_pages * c.page_size < most)) return DA_ERR_INVALID;
+  if (c.S == 0) return DA_OK;
+  if (keep == nullptr || new_lens == nullptr || !aligned(keep, 4) || !aligned(new_lens, 4) || !aligned(kept, 4))
+    return DA_ERR_INVALID;
+  st = check_workspace(workspace, workspace_bytes, evict_workspace(c.S, c.Hkv, most, max_len).total);
+  if (st != DA_OK) return st;
+  if (status != nullptr && !aligned(status, 256)) return DA_ERR_INVALID;
+  EvictArgs a{};
+  a.c = c;
+  a.dst_page_table = dst_page_table, a.dst_demand_table = dst_demand_table;
+  a.dst_max_pages = dst_max_pages;
+  a.keep = keep;
+  a.max_keep = max_keep, a.max_len = max_len, a.sinks = sinks, a.recent = recent;
+  a.new_lens = new_lens, a.kept = kept;
+  a.status = reinterpret_cast<int *>(status != nullptr ? status : workspace);
+  a.ws = reinterpret_cast<uint8_t *>(workspace);
+  return launch_evict(a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int dilution_attn_debug_paged_decode_stall(const void *q, const dilution_attn_paged_cache *cache,

@@ -1,0 +1,315 @@
+// Chunks of new tokens over the paged cache: the host-side problem, the plan of
+// a call, the line of work that the CTAs share, and where partial results lie.
+// Shared by the kernels of both types (paged_chunk_f32.cu, paged_chunk_bf16.cu).
+//
+// Rows.  A row is one query of one query head.  The n new tokens of a sequence
+// take n8 = n rounded up to 8 rows for each of its query heads, head by head.
+// A column tile is up to `edge` rows that a CTA works on at once:
+//   wide   (n > edge / 2): `edge` successive queries of one query head;
+//   narrow (n <= edge / 2): all n8 rows of edge / n8 heads of one key head, so
+//          that the key head's keys are read once for them.
+// Key tiles are `edge` keys.
+//
+// The line.  A segment is what shares keys and totals: one query head of a wide
+// sequence, one key head of a narrow one.  Each begins with `head` units (what
+// beginning a piece costs), then has its key tiles, each worth the column tiles
+// that see it.  The segments of all sequences lie on a line, every CTA takes an
+// equal stretch of it, and the tiles of a segment that begin in the stretch are a
+// piece.  A piece walks its column tiles in the queries' order, and its key tiles
+// inside each, so that a key's total passes from query to query in one CTA.
+//
+// Partial results of a piece: those of a segment's first piece lie in the rows'
+// own places (a), those of the piece a CTA continues in the CTA's places (b).
+// They are joined in the line's order: equal calls give equal bits.
+#pragma once
+
+#include "da_paged.h"
+#include "da_ptx.cuh"
+
+namespace da {
+
+// One call.
+struct PagedChunk {
+  dilution_attn_paged_cache c;
+  const void *q;
+  void *out;
+  const int32_t *cu;   // [S + 1]
+  int N, max_new, max_len;
+  HeadScale hs;
+  float eps;
+  bool earlier;
+  int *status;
+  uint8_t *ws;
+};
+
+// A sequence as the kernels see it (n = 0: nothing to do, or not valid).
+struct ChunkSeq {
+  int len, n, row0, tok0;   // length, new tokens, n8 of the sequences before, first token
+};
+
+// Equal cut of the line.
+struct ChunkCut {
+  long long total, base;
+  int ctas, rem;
+  DA_HD long long first(int cta) const { return cta * base + (cta < rem ? cta : rem); }
+  DA_HD int cta_of(long long unit) const {
+    const long long cut = rem * (base + 1);
+    return (int)(unit < cut ? unit / (base + 1) : rem + (unit - cut) / base);
+  }
+};
+DA_HD ChunkCut chunk_cut(long long total, int ctas) {
+  ChunkCut c;
+  c.total = total;
+  c.ctas = (int)(ctas < total ? ctas : total);
+  if (c.ctas < 1) c.ctas = 1;
+  c.base = total / c.ctas;
+  c.rem = (int)(total - c.base * c.ctas);
+  if (c.base < 1) c.base = 1;   // an empty line
+  return c;
+}
+
+// What the units are: of a column tile at a key tile, of 8 of its rows there, of a
+// segment, and of each of its column tiles.
+struct ChunkCost {
+  int tile, rows8, head, head_tile;
+};
+
+struct ChunkPlan {
+  int edge, G, page_shift;
+  int ctas_keys, ctas_values;
+  ChunkCost cost;
+  long long rows;        // rows of all heads, at most
+  int cta_rows;          // rows of a CTA's places
+  size_t seq_off, cum_off, ml_a, ml_b, nl, acc_a, acc_b, total;
+};
+
+inline ChunkPlan chunk_plan(int S, int Hq, int Hkv, int d, long long N, int max_new, int page_size, int edge, int ctas_keys,
+                            int ctas_values, ChunkCost cost) {
+  ChunkPlan w{};
+  w.edge = edge;
+  w.G = Hq / Hkv;
+  while ((1 << w.page_shift) < page_size) ++w.page_shift;
+  w.ctas_keys = ctas_keys;
+  w.ctas_values = ctas_values;
+  w.cost = cost;
+  const long long busy = N < S ? N : S;   // sequences with new tokens
+  w.rows = (N + 7 * busy) * Hq;
+  const int narrow = (int)round_up(max_new < edge / 2 ? max_new : edge / 2, 8) * w.G;
+  const int wide = max_new > edge / 2 ? (int)round_up(max_new, 8) : 0;
+  w.cta_rows = narrow > wide ? narrow : wide;
+  const long long b_keys = (long long)ctas_keys * w.cta_rows, b_values = (long long)ctas_values * w.cta_rows;
+  auto next = [](size_t off, long long bytes) { return (size_t)round_up((int64_t)off + bytes, 256); };
+  w.seq_off = kStatusBytes;
+  w.cum_off = next(w.seq_off, ((long long)S + 1) * (long long)sizeof(ChunkSeq));   // (the last: how many rows a head)
+  w.ml_a = next(w.cum_off, ((long long)S + 1) * 8);
+  w.ml_b = next(w.ml_a, w.rows * 8);
+  w.nl = next(w.ml_b, b_keys * 8);
+  w.acc_a = next(w.nl, w.rows * 4);
+  w.acc_b = next(w.acc_a, w.rows * acc_stride(d) * 4);
+  w.total = next(w.acc_b, b_values * acc_stride(d) * 4);
+  return w;
+}
+
+// The segments of a sequence (all alike).
+struct ChunkShape {
+  int len, n, n8, P;       // P: place of the first query
+  int tiles, cols;         // key tiles, column tiles
+  int flat;                // key tiles before this one are seen by every column tile
+  int segs, step;          // segments; rows of a column tile
+  bool wide;
+  long long w, w1, head, units;   // of a flat key tile; of a column tile there; before the first; of the segment
+
+  DA_HD void set(int len_, int n_, int Hq, int Hkv, int edge, const ChunkCost &c) {
+    len = len_;
+    n = n_;
+    n8 = (n + 7) & ~7;
+    P = len - n;
+    tiles = (len + edge - 1) / edge;
+    wide = n > edge / 2;
+    const int G = Hq / Hkv;
+    if (wide) {
+      segs = Hq;
+      step = edge;
+      cols = (n + edge - 1) / edge;
+      flat = (P + edge - 1) / edge;
+      w1 = c.tile + c.rows8 * (edge / 8);
+      w = w1 * cols;
+    } else {
+      segs = Hkv;
+      step = edge / n8 * n8;
+      cols = (G * n8 + step - 1) / step;
+      flat = tiles;
+      w = (long long)c.tile * cols + (long long)c.rows8 * G * (n8 / 8);
+      w1 = 0;
+    }
+    head = c.head + (long long)c.head_tile * cols;
+    units = pos(tiles);
+  }
+  // Place of key tile t in the segment: tile flat + j is not seen by the first j column tiles.
+  DA_HD long long pos(int t) const {
+    const long long j = t > flat ? t - flat : 0;
+    return head + t * w - w1 * (j * (j - 1) / 2);
+  }
+  // The first key tile (or `tiles`) at place u or behind it.
+  DA_HD int first_at(long long u) const {
+    if (u <= head) return 0;
+    if (u > pos(tiles - 1)) return tiles;
+    const long long t = (u - head + w - 1) / w;   // exact while the tiles are flat
+    if (t <= flat) return (int)t;
+    int lo = flat, hi = tiles - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (pos(mid) >= u)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    return lo;
+  }
+  // Column tile b: the key tiles that it sees, and the first one that sees key tile t.
+  DA_HD int seen(int b, int edge) const {
+    const int last = wide ? P + (n < (b + 1) * edge ? n : (b + 1) * edge) : len;
+    return (last + edge - 1) / edge;
+  }
+  DA_HD int col0(int t) const { return wide && t > flat ? t - flat : 0; }
+};
+
+#if defined(__CUDACC__)
+struct ChunkLine {
+  const ChunkSeq *seq;    // [S + 1]
+  const long long *cum;   // [S + 1] units of the sequences before
+};
+__device__ __forceinline__ ChunkLine chunk_line(const PagedChunk &p, const ChunkPlan &w) {
+  return ChunkLine{reinterpret_cast<const ChunkSeq *>(p.ws + w.seq_off),
+                   reinterpret_cast<const long long *>(p.ws + w.cum_off)};
+}
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkLine &l, int s) {
+  const int4 v = __ldcg(reinterpret_cast<const int4 *>(l.seq + s));
+  return ChunkSeq{v.x, v.y, v.z, v.w};
+}
+
+// The last sequence with cum <= u (one with units, for u on the line).  A warp's
+// lanes look at 32 places at once.
+__device__ __forceinline__ int chunk_find(const ChunkLine &l, int S, long long u, int lane) {
+  int lo = 0, n = S;   // in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const bool le = lane * step < n && __ldcg(l.cum + at) <= u;
+    const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;   // cum does not decrease
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  return lo;
+}
+
+// Pieces of a CTA's stretch; every warp walks them for itself, all lanes alike.
+struct ChunkWalk {
+  ChunkShape g;
+  ChunkSeq q;
+  int s, seg;            // sequence, segment of it
+  int tile, end;         // key tiles of the piece (tile >= end: none left)
+  long long base, to;    // the segment's place; the stretch's end
+  __device__ __forceinline__ void load(const PagedChunk &p, const ChunkPlan &w, const ChunkLine &l) {
+    q = chunk_seq(l, s);
+    g.set(q.len, q.n, p.c.Hq, p.c.Hkv, w.edge, w.cost);
+  }
+  __device__ void start(const PagedChunk &p, const ChunkPlan &w, const ChunkLine &l, const ChunkCut &cut, int lane) {
+    tile = end = 0;
+    const long long from = cut.first(blockIdx.x);
+    to = (int)blockIdx.x < cut.ctas ? cut.first(blockIdx.x + 1) : 0;
+    if (from >= to || from >= cut.total) return;
+    s = chunk_find(l, p.c.S, from, lane);
+    load(p, w, l);
+    base = __ldcg(l.cum + s);
+    seg = (int)((from - base) / g.units);
+    base += seg * g.units;
+    tile = g.first_at(from - base);
+    end = min(g.first_at(to - base), g.tiles);
+    if (tile >= end) settle(p, w, l);
+  }
+  __device__ __forceinline__ bool any() const { return tile < end; }
+  __device__ void next(const PagedChunk &p, const ChunkPlan &w, const ChunkLine &l) {
+    tile = end;
+    settle(p, w, l);
+  }
+  // The next segment's first piece, if its first tile lies in the stretch.
+  __device__ void settle(const PagedChunk &p, const ChunkPlan &w, const ChunkLine &l) {
+    if (tile < g.tiles) {   // the stretch ends inside the segment
+      end = tile;
+      return;
+    }
+    base += g.units;
+    tile = end = 0;
+    if (base >= to) return;
+    if (++seg == g.segs) {
+      seg = 0;
+      do {   // on to the next sequence with new tokens: the line goes on
+        ++s;
+        q = chunk_seq(l, s);
+      } while (q.n == 0);
+      g.set(q.len, q.n, p.c.Hq, p.c.Hkv, w.edge, w.cost);
+    }
+    end = g.first_at(to - base);
+  }
+  // First row of the segment in the rows' own places.
+  __device__ __forceinline__ long long row0(const PagedChunk &p, const ChunkPlan &w) const {
+    return (long long)q.row0 * p.c.Hq + (long long)seg * (g.wide ? 1 : w.G) * g.n8;
+  }
+  __device__ __forceinline__ int hkv(const ChunkPlan &w) const { return g.wide ? seg / w.G : seg; }
+};
+
+// The place of the piece's row r (of the segment) among `stride` floats a row.
+__device__ __forceinline__ float *chunk_place(const PagedChunk &p, size_t a, size_t b, long long row0, int cta_rows, int tile,
+                                              int cta, int r, int stride) {
+  return reinterpret_cast<float *>(p.ws + (tile == 0 ? a : b)) +
+         ((tile == 0 ? row0 : (long long)cta * cta_rows) + r) * stride;
+}
+
+// A row found by its number among all rows of the call: its sequence, query head,
+// query and segment.  false: padding, or past the last row.
+struct ChunkRow {
+  ChunkShape g;
+  ChunkSeq q;
+  int s, hq, i;          // sequence, query head, query
+  int r;                 // row of the segment
+  int seen;              // key tiles that its column tile sees
+  long long base, row0;  // the segment's place on the line; its first row
+};
+__device__ __forceinline__ bool chunk_row(const PagedChunk &p, const ChunkPlan &w, const ChunkLine &l, long long row,
+                                          ChunkRow &x) {
+  int lo = 0, hi = p.c.S - 1;   // the last sequence whose first row is at or before this one
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if ((long long)__ldcg(&l.seq[mid].row0) * p.c.Hq <= row)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  x.s = lo;
+  x.q = chunk_seq(l, lo);
+  if (x.q.n == 0) return false;   // (of the sequences that begin there the last one: behind the last row)
+  x.g.set(x.q.len, x.q.n, p.c.Hq, p.c.Hkv, w.edge, w.cost);
+  const long long at = row - (long long)x.q.row0 * p.c.Hq;
+  x.hq = (int)(at / x.g.n8);
+  if (x.hq >= p.c.Hq) return false;
+  x.i = (int)(at - (long long)x.hq * x.g.n8);
+  if (x.i >= x.q.n) return false;
+  const int seg = x.g.wide ? x.hq : x.hq / w.G;
+  x.row0 = (long long)x.q.row0 * p.c.Hq + (long long)seg * (x.g.wide ? 1 : w.G) * x.g.n8;
+  x.r = (int)(row - x.row0);
+  x.seen = x.g.seen(x.r / x.g.step, w.edge);
+  x.base = __ldcg(l.cum + lo) + seg * x.g.units;
+  return true;
+}
+// Calls f(first tile, CTA) for every piece that a row's column tile takes part in, in order.
+template <typename F>
+__device__ __forceinline__ void chunk_pieces(const ChunkRow &x, const ChunkCut &cut, F &&f) {
+  for (int t = 0; t < x.seen;) {
+    const int cta = cut.cta_of(x.base + x.g.pos(t));
+    f(t, cta);
+    t = x.g.first_at(cut.first(cta + 1) - x.base);
+  }
+}
+#endif  // __CUDACC__
+
+}  // namespace da

@@ -1,0 +1,339 @@
+"""Chunks of new tokens over the paged cache against the float64 oracle.
+
+Tolerances (written before any run).  A logit is off by at most
+g = (2 d + 8) 2^-24 sum |q_i k_i| tau / sqrt(d), a bid by a factor 1 +- 2 g (see
+tests/_paged.py).  A total is a running fp32 sum: after n queries it is off by
+2 g and 2^-20 (the exponentials) of its bids and by n 2^-24 of itself; a share by
+4 g + n 2^-24 + 2^-19, and a row of A by twice that, which times the largest value
+bounds the row of out.  bf16: each share is rounded, by at most 2^-8 of itself, and
+numerator and sum hold the same rounded shares, so that out moves by at most
+2^-8 sum A |v - out| (1 + 2^-7); out itself is rounded by 2^-8.  Those roundings
+are independent with a standard deviation of at most 2^-8 / sqrt(3) each: the root
+mean square of the errors, each relative to its own standard deviation, is at most
+1; 1.5 allows for few rows (the smallest test has 128 elements: 4 standard errors).
+"""
+import numpy as np
+import pytest
+import torch
+
+from long_context_attention_gb300 import binding as b
+from long_context_attention_gb300 import rope_inv_freq
+from oracle import paged as op
+from tests._parity import host64
+from tests._paged import DEV, TYPES, make_cache, oracle_step
+
+pytestmark = pytest.mark.gpu
+
+
+def make(lens, news, Hq, Hkv, d, page, dtype, seed=0, junk=None, pad=0, spare=2, fresh=True):
+    """A cache whose sequences' last news[s] tokens are new (no demand yet), their queries and cu_tokens."""
+    cache, _, _ = make_cache(len(lens), lens, Hq, Hkv, d, page, dtype, seed=seed, junk=junk, spare=spare, extra_width=1)
+    g = torch.Generator().manual_seed(seed + 1)
+    cu = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+    N = int(cu[-1]) + pad
+    q = (torch.randn(N, Hq, d, generator=g) * 1.5).to(TYPES[dtype])
+    if pad:
+        q[int(cu[-1]):] = float("nan")
+    if fresh:
+        for s, n in enumerate(news):
+            if n:
+                t = torch.arange(lens[s] - n, lens[s], device=DEV)
+                cache.demand_pages[cache.demand_table[s, t // page].long(), :, t % page] = 0.0
+    return cache, q.to(DEV), torch.tensor(cu, device=DEV)
+
+
+def oracle(cache, q, cu, tau=1.0, eps=1e-6, earlier=False):
+    with np.errstate(invalid="ignore"):
+        return op.paged_chunk(host64(q), host64(cache.k_pages), host64(cache.v_pages), host64(cache.demand_pages),
+                              cache.page_table.cpu().numpy(), cache.demand_table.cpu().numpy(),
+                              cache.seq_lens.cpu().numpy(), cu.cpu().numpy(), tau, eps, earlier)
+
+
+def check(cache, q, cu, before, out, ref):
+    ro, rD, info = ref
+    n_rows, d, bf16 = int(cu[-1]), q.shape[-1], out.dtype == torch.bfloat16
+    got, ro = host64(out)[:n_rows], ro[:n_rows]
+    news = np.diff(cu.cpu().numpy())
+    per_row = np.repeat(news, news)[:, None]
+    g = (2 * d + 8) * 2.0 ** -24 * info["spread"][:n_rows]
+    base = (2 * (4 * g + per_row * 2.0 ** -24 + 2.0 ** -19) * info["vmax"][:n_rows])[..., None]
+    step = (2.0 ** -8 if bf16 else 2.0 ** -24) * np.abs(ro)
+    share = 2.0 ** -8 * (1 + 2.0 ** -7) * info["dev"][:n_rows] if bf16 else 0.0
+    err = np.abs(got - ro)
+    assert np.isfinite(got).all()
+    assert (err <= base + step + share).all(), float((err - base - step - share).max())
+    if bf16 and n_rows:
+        sd = np.sqrt(((2.0 ** -8 * info["dev2"][:n_rows]) ** 2 + step ** 2) / 3) + base
+        assert np.sqrt(np.mean((err / sd) ** 2)) <= 1.5
+    D, page, dt = host64(cache.demand_pages), cache.page_size, cache.demand_table.cpu().numpy()
+    seen = np.zeros(D.shape, dtype=bool)
+    cuh = cu.cpu().numpy()
+    for (s, h), p in info["bids"].items():
+        t = np.arange(len(p))
+        at = (dt[s][t // page], h, t % page)
+        seen[at] = True
+        gs = g[cuh[s]:cuh[s + 1], h].max()
+        bound = p * (2 * gs + 2.0 ** -20) + (news[s] + 1) * 2.0 ** -24 * rD[at] + 1e-30
+        assert (np.abs(D[at] - rD[at]) <= bound).all(), (s, h, float((np.abs(D[at] - rD[at]) - bound).max()))
+    assert np.array_equal(D[~seen], host64(before)[~seen], equal_nan=True)
+
+
+def run(cache, q, cu, max_new, max_len, **kw):
+    tau = kw.get("tau", 1.0) if kw.get("tau_bh") is None else host64(kw["tau_bh"]).reshape(cache.S, cache.Hq)
+    before = cache.demand_pages.clone()
+    ref = oracle(cache, q, cu, tau, kw.get("eps", 1e-6), bool(kw.get("flags", 0) & b.DA_FLAG_EARLIER_DEMAND_ONLY))
+    ws = b.dilution_attn_paged_chunk_workspace(cache, q.shape[0], max_new, max_len)
+    ws[256:] = 0xC7          # whatever an earlier call left
+    out = torch.full_like(q, 7.0)
+    got = b.dilution_attn_paged_chunk(q, cache, cu, max_new, max_len, out, workspace=ws, **kw)
+    assert got is out and b.dilution_attn_get_error(ws) == b.DA_OK
+    check(cache, q, cu, before, out, ref)
+    assert (out[int(cu[-1]):] == 7.0).all()          # rows behind the last sequence
+    return out
+
+
+# lengths and new tokens around every border: rows of 8, half and whole column tiles, key tiles, pages
+SHAPES = [
+    ([1], [1]), ([5], [5]), ([130], [1]), ([300], [7]), ([64], [64]), ([129], [33]), ([257], [65]), ([128], [128]),
+    ([200], [129]), ([385], [300]), ([1, 2, 3], [1, 2, 3]), ([70, 0, 150, 9, 260], [3, 0, 65, 0, 130]),
+    ([40, 41, 33, 500], [8, 9, 31, 64]), ([127, 255, 256], [63, 127, 256]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,page,Hq,Hkv", [(64, 16, 2, 2), (128, 32, 3, 1), (64, 256, 4, 2)])
+@pytest.mark.parametrize("lens,news", SHAPES)
+def test_shapes(lens, news, d, page, Hq, Hkv, dtype):
+    cache, q, cu = make(lens, news, Hq, Hkv, d, page, dtype, seed=len(lens) + sum(lens), junk=float("nan"), pad=3)
+    run(cache, q, cu, max(news), max(lens))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 1), (20, 1), (34, 2), (5, 5)])
+@pytest.mark.parametrize("n", [1, 9, 17, 40, 70])
+def test_groups(Hq, Hkv, n, dtype):
+    """Many query heads on a key head: narrow tiles of several heads, several column tiles of them."""
+    cache, q, cu = make([n + 150, 61], [n, min(n, 61)], Hq, Hkv, 64, 64, dtype, seed=Hq + n)
+    run(cache, q, cu, n + 5, n + 150)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_long(d, dtype):
+    """Many pieces a segment, several column tiles."""
+    cache, q, cu = make([2900, 1111, 1500], [200, 1, 30], 2, 1, d, 128, dtype, seed=3)
+    run(cache, q, cu, 200, 2900)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kw", [dict(tau=0.0), dict(tau=2.5), dict(eps=1.0), dict(eps=1e-3, flags=1), dict(flags=1),
+                                dict(tau=1.7, eps=1e-15)])
+def test_options(kw, dtype):
+    cache, q, cu = make([150, 90, 40], [70, 20, 3], 4, 2, 64, 16, dtype, seed=11, fresh=False)
+    run(cache, q, cu, 70, 150, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_tau_per_head(dtype):
+    cache, q, cu = make([150, 90], [70, 20], 4, 2, 64, 16, dtype, seed=12)
+    tau = torch.rand(8, generator=torch.Generator().manual_seed(1)).mul_(3).to(DEV)
+    run(cache, q, cu, 70, 150, tau_bh=tau)
+    tau[3] = float("nan")
+    ws = b.dilution_attn_paged_chunk_workspace(cache, q.shape[0], 70, 150)
+    b.dilution_attn_paged_chunk(q, cache, cu, 70, 150, tau_bh=tau, workspace=ws)
+    assert b.dilution_attn_get_error(ws) == b.DA_ERR_INVALID
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_single_tokens_are_a_decode_step(d, dtype):
+    """One new token each: the decode step's definition."""
+    lens = [700, 1, 33, 0, 256]
+    cache, q, cu = make(lens, [min(1, n) for n in lens], 6, 2, d, 32, dtype, seed=5)
+    before = cache.demand_pages.clone()
+    qs = torch.zeros(5, 6, d, dtype=q.dtype, device=DEV)
+    live = [i for i, n in enumerate(lens) if n]
+    qs[live] = q
+    ro, rD, _ = oracle_step(cache, qs)
+    out = run(cache, q, cu, 1, 700)
+    assert np.abs(host64(out) - ro[live]).max() < 0.05 and np.abs(host64(cache.demand_pages) - rD).max() < 1e-5
+    cache.demand_pages.copy_(before)
+    step = b.dilution_attn_paged_decode(qs, cache, 700)
+    assert (out.float() - step[live].float()).abs().max() < 0.05
+    torch.testing.assert_close(cache.demand_pages.cpu().double(), torch.tensor(rD), rtol=1e-5, atol=1e-6)
+
+
+@pytest.mark.parametrize("dtype,d,T", [("f32", 64, 200), ("bf16", 64, 330), ("bf16", 128, 129)])
+def test_whole_prompt_is_the_forward(dtype, d, T):
+    """n = length with no demand: dilution_attn_fwd of the prompt, its demand and its heads shared."""
+    cache, q, cu = make([T], [T], 4, 2, d, 32, dtype, seed=T)
+    at = torch.arange(T, device=DEV)
+    pages = cache.page_table[0, at // 32].long()
+    k, v = (x[pages, :, at % 32].transpose(0, 1)[None].repeat_interleave(2, 1).contiguous()
+            for x in (cache.k_pages, cache.v_pages))
+    demand = torch.empty(1, 4, T, device=DEV)
+    ref = b.dilution_attn_fwd(q.transpose(0, 1)[None].contiguous(), k, v, demand_out=demand)
+    out = run(cache, q, cu, T, T)
+    tol = 3e-2 if dtype == "bf16" else 2e-5
+    assert (out.transpose(0, 1)[None].float() - ref.float()).abs().max() < tol
+    got = cache.demand_pages[cache.demand_table[0, at // 32].long(), :, at % 32].t()[None]
+    torch.testing.assert_close(got, demand, rtol=2e-3 if dtype == "bf16" else 1e-5, atol=1e-4 if dtype == "bf16" else 1e-6)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_two_chunks_are_one(dtype):
+    """A prompt in two chunks leaves the totals of one chunk; outputs agree with the oracle in both."""
+    cache, q, cu = make([300], [300], 2, 2, 64, 64, dtype, seed=21)
+    start = cache.demand_pages.clone()
+    run(cache, q, cu, 300, 300)
+    whole = cache.demand_pages.clone()
+    cache.demand_pages.copy_(start)
+    for a, e in ((0, 110), (110, 300)):
+        cache.seq_lens.fill_(e)
+        run(cache, q[a:e].contiguous(), torch.tensor([0, e - a], dtype=torch.int32, device=DEV), 190, 300)
+    torch.testing.assert_close(cache.demand_pages, whole, rtol=1e-5, atol=1e-6)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_equal_bits_in_place_and_streams(dtype):
+    """Equal calls give equal bits: into q's own place, on another stream, without a workspace, from a graph."""
+    cache, q, cu = make([900, 120, 77], [130, 64, 5], 4, 2, 64, 32, dtype, seed=31, pad=2)
+    start = cache.demand_pages.clone()
+    ref = torch.zeros_like(q)
+    b.dilution_attn_paged_chunk(q, cache, cu, 130, 900, ref)
+    total = cache.demand_pages.clone()
+
+    def same(out):
+        n = int(cu[-1])
+        assert torch.equal(out[:n], ref[:n]) and torch.equal(cache.demand_pages, total)
+        cache.demand_pages.copy_(start)
+    cache.demand_pages.copy_(start)
+    own = q.clone()
+    b.dilution_attn_paged_chunk(own, cache, cu, 130, 900, own)
+    same(own)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = b.dilution_attn_paged_chunk(q, cache, cu, 130, 900, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    same(out)
+    ws = b.dilution_attn_paged_chunk_workspace(cache, q.shape[0], 130, 900)
+    g = torch.cuda.CUDAGraph()
+    out = torch.zeros_like(q)
+    with torch.cuda.graph(g):
+        b.dilution_attn_paged_chunk(q, cache, cu, 130, 900, out, workspace=ws)
+    for _ in range(2):
+        out.zero_()
+        g.replay()
+        same(out)
+    # the captured call follows lengths that change
+    cache.seq_lens.copy_(torch.tensor([800, 119, 70], dtype=torch.int32))
+    cu.copy_(torch.tensor([0, 3, 104, 104], dtype=torch.int32))
+    r = oracle(cache, q, cu)
+    g.replay()
+    check(cache, q, cu, start, out, r)
+    assert b.dilution_attn_get_error(ws) == b.DA_OK and b.dilution_attn_get_error(cache.status) == b.DA_OK
+
+
+def test_bad_lengths_and_pages():
+    """What the host cannot see: recorded, nothing else read or written, other sequences unharmed."""
+    for dtype in ("f32", "bf16"):
+        lens, news = [100, 200, 150], [20, 70, 5]
+
+        def call(change, max_new=70, max_len=200, good=(0, 2)):
+            cache, q, cu = make(lens, news, 4, 2, 64, 16, dtype, seed=41)
+            ro, rD, info = oracle(cache, q, cu)
+            start = cache.demand_pages.clone()
+            change(cache, cu)
+            ws = b.dilution_attn_paged_chunk_workspace(cache, q.shape[0], max_new, max_len)
+            out = torch.full_like(q, 7.0)
+            b.dilution_attn_paged_chunk(q, cache, cu, max_new, max_len, out, workspace=ws)
+            assert b.dilution_attn_get_error(ws) == b.DA_ERR_INVALID
+            assert b.dilution_attn_get_error(ws) == b.DA_OK
+            first = np.concatenate([[0], np.cumsum(news)])
+            for s in good:
+                r = slice(first[s], first[s + 1])
+                assert np.abs(host64(out)[r] - ro[r]).max() < 0.05
+            return cache, out, start
+
+        for bad in (-1, 201, 300, 69):      # 69: shorter than its new tokens
+            def change(cache, cu, bad=bad):
+                cache.seq_lens[1] = bad
+            cache, out, start = call(change)
+            assert (out[20:90] == 7.0).all()
+            t = torch.arange(lens[1], device=DEV)
+            at = cache.demand_table[1, t // 16].long(), slice(None), t % 16
+            assert torch.equal(cache.demand_pages[at], start[at])
+        call(lambda cache, cu: None, max_new=69)
+        for bad in (-1, 10 ** 9, -2 ** 31):
+            def change(cache, cu, bad=bad):
+                cache.page_table[1, 3] = bad
+            call(change)
+
+            def change(cache, cu, bad=bad):
+                cache.demand_table[1, 3] = bad
+            call(change)
+        call(lambda cache, cu: cu.copy_(torch.tensor([0, 20, 10, 95], dtype=torch.int32)), good=(0,))
+        call(lambda cache, cu: cu.copy_(torch.tensor([0, 20, 90, 99], dtype=torch.int32)), good=(0, 1))
+        call(lambda cache, cu: cu.copy_(torch.tensor([-5, 20, 90, 95], dtype=torch.int32)), good=(1, 2))
+        # tokens counted twice: more rows than there is room for
+        cache, q, cu = make([64, 64, 64, 64], [64, 0, 0, 0], 2, 2, 64, 16, dtype, seed=42)
+        cu.copy_(torch.tensor([0, 64, 0, 64, 0], dtype=torch.int32))
+        ws = b.dilution_attn_paged_chunk_workspace(cache, 64, 64, 64)
+        b.dilution_attn_paged_chunk(q, cache, cu, 64, 64, workspace=ws)
+        assert b.dilution_attn_get_error(ws) == b.DA_ERR_INVALID
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sharp_and_extreme_logits(dtype):
+    """Logits hundreds apart, all far below zero, and the type's largest values in rows past the end."""
+    cache, q, cu = make([300, 140], [100, 9], 2, 1, 64, 32, dtype, seed=51, junk=torch.finfo(TYPES[dtype]).max)
+    q[:40] *= 30.0
+    q[40:60] = -cache.k_pages[cache.page_table[0, 2], 0, 3] * 20.0
+    run(cache, q, cu, 100, 300)
+
+
+def test_serving_run_together():
+    """Rotation, append and chunk of ragged prompts, a second chunk behind them, eviction, single tokens and a decode step:
+    the calls of a serving loop, each against the oracle on the cache as it then is."""
+    torch.manual_seed(0)
+    S, Hq, Hkv, d, page, room = 3, 6, 2, 64, 32, 12
+    t = torch.bfloat16
+    tables = torch.randperm(S * room).to(torch.int32).view(S, room).to(DEV)
+    cache = b.PagedCache(torch.zeros(S * room, Hkv, page, d, dtype=t, device=DEV),
+                         torch.zeros(S * room, Hkv, page, d, dtype=t, device=DEV),
+                         torch.zeros(S * room, Hq, page, device=DEV), tables, tables.flip(0).contiguous(),
+                         torch.zeros(S, dtype=torch.int32, device=DEV))
+    spec = b.rope_spec(rope_inv_freq(d).to(DEV))
+    seen = np.zeros(S, dtype=np.int64)       # tokens so far, evicted ones among them
+    lens = np.zeros(S, dtype=np.int64)
+
+    def chunk(news):
+        nonlocal lens, seen
+        news = np.array(news)
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(news)]), dtype=torch.int32, device=DEV)
+        N = int(cu[-1])
+        rows = torch.randn(N, Hq + 2 * Hkv, d, dtype=t, device=DEV)
+        pos = np.concatenate([np.arange(seen[s], seen[s] + n) for s, n in enumerate(news)])
+        lens, seen = lens + news, seen + news
+        cache.seq_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        q = b.dilution_attn_paged_append(rows[:, :Hq], rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:], cache, cu, rope=spec,
+                                         positions=torch.tensor(pos[None], dtype=torch.int32, device=DEV))
+        run(cache, q, cu, int(news.max()), int(lens.max()))
+
+    chunk([100, 37, 250])
+    chunk([20, 1, 0])
+    keep = torch.tensor([64, 64, 64], dtype=torch.int32, device=DEV)
+    ref = op.paged_evict(host64(cache.k_pages), host64(cache.v_pages), cache.demand_pages.cpu().numpy(),
+                         tables.cpu().numpy(), tables.flip(0).cpu().numpy(), lens, [64] * 3, 64, 4, 16)
+    b.dilution_attn_paged_evict(cache, keep, 64, int(lens.max()), cache.seq_lens, sinks=4, recent=16)
+    for got, want in zip((cache.k_pages, cache.v_pages, cache.demand_pages), ref):
+        assert np.array_equal(host64(got), want.astype(np.float64))
+    lens = np.minimum(lens, 64)
+    assert cache.seq_lens.tolist() == lens.tolist()
+    chunk([1, 1, 1])
+    chunk([5, 0, 70])
+    q = torch.randn(S, Hq, d, dtype=t, device=DEV)
+    before = oracle_step(cache, q)
+    out = b.dilution_attn_paged_decode(q, cache, int(lens.max()))
+    assert np.abs(host64(out) - before[0]).max() < 0.03
+    assert b.dilution_attn_get_error(cache.status) == b.DA_OK
