@@ -68,10 +68,10 @@ DA_HD ChunkCut chunk_cut(long long total, int ctas) {
   return c;
 }
 
-// What the units are: of a column tile at a key tile, of 8 of its rows there, of a
-// segment, and of each of its column tiles.
+// What the units are: of a narrow key tile (its copies), of a column tile at a key
+// tile, of 8 of its rows there, of a segment, and of each of its column tiles.
 struct ChunkCost {
-  int tile, rows8, head, head_tile;
+  int keys, tile, rows8, head, head_tile;
 };
 
 struct ChunkPlan {
@@ -139,7 +139,7 @@ struct ChunkShape {
       step = edge / n8 * n8;
       cols = (G * n8 + step - 1) / step;
       flat = tiles;
-      w = (long long)c.tile * cols + (long long)c.rows8 * G * (n8 / 8);
+      w = c.keys + (long long)c.tile * cols + (long long)c.rows8 * G * (n8 / 8);
       w1 = 0;
     }
     head = c.head + (long long)c.head_tile * cols;

@@ -1051,6 +1051,20 @@ bool make_page_map(CUtensorMap *m, const void *base, int64_t num, int page_size,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// For chunks over the paged cache: bf16 rows [n][heads][d], copied `rows` of a head
+// by 128 bytes at a time.
+bool make_rows_map(CUtensorMap *m, const void *base, int64_t n, int heads, int d, int rows) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)n, (cuuint64_t)heads};
+  const cuuint64_t strides[2] = {(cuuint64_t)heads * d * 2, (cuuint64_t)d * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The fp32 accumulator [BH * Tp rows][d + 4] as a 2-D tensor; box = 32 rows
 // x 32 columns, 128B swizzle: the sweep epilogue's reduction box.
 static bool make_acc_map(CUtensorMap *m, float *acc, int64_t rows, int d) {

@@ -1,0 +1,966 @@
+// Chunks over the paged cache in bf16: tcgen05 kernels.
+//
+// Mathematics: as paged_chunk_f32.cu.
+//   ckx_keys    (max, sum 2^(x - max)) of every row over a piece's key tiles;
+//   ckx_values  p = 2^(x - lse2), total += p, share = p / (total + eps), and the
+//               sums of share v and share over them.
+//
+// What bounds it: with many rows the demand's arithmetic (an exponential, half a
+// reciprocal and a running sum a pair), as in the prompt's sweep (fwd_bf16.cu); with
+// few the pages, which both passes bring once for all rows of a key head.
+//
+// ckx_keys: S[row, key] = Q K^T (M = 128 rows, N = 128 keys), one thread a row with
+// a running maximum and sum; two warpgroups take alternate key tiles.
+//
+// ckx_values: S^T[key, row] = K Q^T (M = 128 keys), one thread a key, which walks
+// the rows of the column tile with the key's total in a register; kG warpgroups take
+// the key tiles of a piece in turn, each always the same ones, so that a total
+// comes back to the thread that left it.  The shares, rounded to bf16 once (the
+// product's operands have one type; 2^-8 of each share, and numerator and sum hold
+// the same ones), go to shared memory as the MN-major A operand of
+// D[row, :] += share^T [V | 1].  Unlike the prompt's sweep, the rows stay and the keys
+// stream: D stays in TMEM over a piece's key tiles and leaves once, as a partial
+// result of fixed place, so that equal calls give equal bits.
+//
+// Roles: demand (or reduction) warpgroups, a warpgroup that takes D out, and
+// control warps: a producer that walks the CTA's pieces, describes each column tile
+// in a small ring that every role reads, and brings Q, K and V by TMA; one MMA issuer
+// a demand warpgroup.  Waits are bounded; rows of missing or invalid pages are
+// filled with zeros by reading past the pool's end.
+#include "da_chunk.cuh"
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+namespace da {
+
+bool make_page_map(CUtensorMap *m, const void *base, int64_t num, int page_size, int rows, int d, int dtype);   // fwd_bf16.cu
+bool make_rows_map(CUtensorMap *m, const void *base, int64_t n, int heads, int d, int rows);
+
+constexpr int kCkxEdge = 128;
+constexpr int kCkxKeyCtas = 304, kCkxValueCtas = 152;
+constexpr uint32_t kCkxHalf = 128 * 128;   // 128 rows x 64 bf16
+
+ChunkPlan chunk_plan_bf16(int S, int Hq, int Hkv, int d, long long N, int max_new, int page_size) {
+  // a unit is 8 rows of a key tile, about 40 ns
+  return chunk_plan(S, Hq, Hkv, d, N, max_new, page_size, kCkxEdge, kCkxKeyCtas, kCkxValueCtas,
+                    ChunkCost{d == 128 ? 28 : 14, 3, 1, 64, 16});
+}
+
+// A column tile of a piece, as the producer describes it.
+struct CkxTile {
+  float *place;        // its rows' partial results
+  const float *nl;     // -lse2 of its rows
+  int s, hkv, hq0;     // sequence, key head, query head of row 0
+  int n8, n, i0;       // rows of a head (0: one head); queries; query of row 0
+  int P, len;          // place of query 0; length
+  int rows;            // 0: no more
+  int tile, end, t0;   // key tiles; number of the first among the CTA's
+  __device__ __forceinline__ int query(int c) const { return n8 ? c % n8 : i0 + c; }
+};
+constexpr int kCkxRing = 4;
+
+__device__ __forceinline__ void ckx_drain(uint64_t *bar, uint32_t parity) {   // lets copies and products in flight land
+  const unsigned long long t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer() - t0 > 100ull * 1000ull * 1000ull) break;
+}
+__device__ __forceinline__ void ckx_release(uint64_t *bar, int lane) {   // after the last tcgen05.ld of a buffer
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ uint64_t ckx_kmajor(const uint8_t *tile) { return smem_desc(smem_u32(tile), 16, 1024); }
+
+// One warp: this lane's page of key tile `tile`; the tile of K or V into `dst`.
+__device__ __forceinline__ int ckx_page(const PagedChunk &p, int sh, int s, int len, int tile, int lane) {
+  const int rows = min(1 << sh, kCkxEdge), key = tile * kCkxEdge + lane * rows;
+  return lane * rows < kCkxEdge && key < len ? __ldcg(p.c.page_table + (size_t)s * p.c.max_pages + (key >> sh)) : -1;
+}
+template <int D>
+__device__ __forceinline__ void ckx_load(const PagedChunk &p, int sh, const CUtensorMap *map, uint8_t *dst, uint64_t *bar,
+                                         int len, int tile, int hkv, int page, int lane) {
+  const int ps = 1 << sh, rows = min(ps, kCkxEdge), key = tile * kCkxEdge + lane * rows;
+  if (lane == 0) mbar_arrive_expect_tx(bar, kCkxEdge * D * 2);
+  __syncwarp();
+  if (lane * rows < kCkxEdge) {
+    const bool ok = (unsigned)page < (unsigned)p.c.num_pages;
+    if (!ok && key < len) atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
+    const int z = ok ? page * p.c.Hkv + hkv : max(p.c.num_pages * p.c.Hkv, 1);   // past the map's end: zeros
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h)
+      tma_load_3d(dst + h * kCkxHalf + lane * rows * 128, map, bar, h * 64, key & (ps - 1), z);
+  }
+}
+// Q of a column tile: 8 rows a box (what lies behind a tile's last row is read by no one).
+template <int D>
+__device__ __forceinline__ void ckx_queries(const CUtensorMap *map, uint8_t *dst, uint64_t *bar, int tok0, int hq0, int n8,
+                                            int i0, int rows, int lane) {
+  const int boxes = (rows + 7) / 8;
+  if (lane == 0) mbar_arrive_expect_tx(bar, boxes * 8 * D * 2);
+  __syncwarp();
+  if (lane < boxes) {
+    const int c = 8 * lane, hq = n8 ? hq0 + c / n8 : hq0, token = tok0 + (n8 ? c % n8 : i0 + c);
+#pragma unroll
+    for (int h = 0; h < D / 64; ++h) tma_load_3d(dst + h * kCkxHalf + lane * 1024, map, bar, h * 64, token, hq);
+  }
+}
+
+// The producer's walk: column tile after column tile.
+struct CkxWalk {
+  ChunkWalk k;
+  int b, t0;
+  __device__ __forceinline__ void start(const PagedChunk &p, const ChunkPlan &w, const ChunkLine &l, const ChunkCut &cut,
+                                        int lane) {
+    k.start(p, w, l, cut, lane);
+    t0 = 0;
+    b = k.any() ? k.g.col0(k.tile) : 0;
+  }
+  __device__ __forceinline__ CkxTile tile(const PagedChunk &p, const ChunkPlan &w, size_t place_a, size_t place_b,
+                                          int stride) const {
+    CkxTile x;
+    x.rows = 0;
+    if (!k.any()) return x;
+    const int r0 = b * k.g.step;
+    x.s = k.s;
+    x.hkv = k.hkv(w);
+    x.n = k.g.n;
+    x.P = k.g.P;
+    x.len = k.g.len;
+    if (k.g.wide) {
+      x.n8 = 0;
+      x.hq0 = k.seg;
+      x.i0 = r0;
+      x.rows = min(k.g.step, x.n - r0);
+    } else {
+      x.n8 = k.g.n8;
+      x.hq0 = k.seg * w.G + r0 / x.n8;
+      x.i0 = 0;
+      x.rows = min(k.g.step, w.G * x.n8 - r0);
+    }
+    x.tile = k.tile;
+    x.end = min(k.end, k.g.seen(b, kCkxEdge));
+    x.t0 = t0;
+    const long long row0 = k.row0(p, w);
+    x.place = chunk_place(p, place_a, place_b, row0, w.cta_rows, k.tile, blockIdx.x, r0, stride);
+    x.nl = reinterpret_cast<const float *>(p.ws + w.nl) + row0 + r0;
+    return x;
+  }
+  __device__ __forceinline__ void next(const PagedChunk &p, const ChunkPlan &w, const ChunkLine &l, const CkxTile &x) {
+    t0 += x.end - x.tile;
+    if (++b < k.g.cols) return;
+    k.next(p, w, l);
+    if (k.any()) b = k.g.col0(k.tile);
+  }
+};
+
+// ============================================================================ pass 1
+template <int D>
+struct CkxKeys {
+  static constexpr int kThreads = 320;                 // 2 x 4 reduction warps, producer, MMA issuer
+  static constexpr int kTB = kCkxEdge * D * 2;
+  static constexpr int kStages = D == 64 ? 4 : 2;
+  static constexpr uint32_t kOffK = kTB, kOffRing = kOffK + kStages * kTB, kOffMl = kOffRing + kCkxRing * sizeof(CkxTile);
+  static constexpr uint32_t kOffBar = kOffMl + 128 * 8;
+  static constexpr int kSmemBytes = 1024 + kOffBar + 512;
+  static constexpr int kTmemCols = 256;                // two S buffers of 128 columns; two CTAs an SM
+};
+
+template <int D>
+__global__ void __launch_bounds__(CkxKeys<D>::kThreads, 2)
+    ckx_keys(PagedChunk p, ChunkPlan w, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap) {
+  using C = CkxKeys<D>;
+  extern __shared__ __align__(1024) uint8_t ckx_smem_raw[];
+  uint8_t *smem = ckx_smem_raw + ((1024u - (smem_u32(ckx_smem_raw) & 1023u)) & 1023u);
+  uint8_t *sQ = smem, *sK = smem + C::kOffK;
+  CkxTile *ring = reinterpret_cast<CkxTile *>(smem + C::kOffRing);
+  float2 *s_ml = reinterpret_cast<float2 *>(smem + C::kOffMl);
+  uint64_t *r_full = reinterpret_cast<uint64_t *>(smem + C::kOffBar), *r_free = r_full + kCkxRing;
+  uint64_t *q_full = r_free + kCkxRing, *q_empty = q_full + 1, *k_full = q_empty + 1, *k_empty = k_full + C::kStages;
+  uint64_t *s_full = k_empty + C::kStages, *s_free = s_full + 2, *ml_full = s_free + 2, *ml_free = ml_full + 4;
+  uint64_t *done = ml_free + 4;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < kCkxRing; ++i) {
+      mbar_init(&r_full[i], 1);
+      mbar_init(&r_free[i], 9);   // 8 reduction warps and the issuer
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 4);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&ml_full[i], 1);
+      mbar_init(&ml_free[i], 1);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx wc{abort_flag, p.status};
+  if (warp == 8) {
+    // ---------------------------------------------------------------- producer
+    const ChunkLine l = chunk_line(p, w);
+    const ChunkCut cut = chunk_cut(__ldcg(l.cum + p.c.S), w.ctas_keys);
+    const int sh = w.page_shift;
+    CkxWalk it;
+    int i = 0, issued = 0;
+    bool ok = true;
+    for (it.start(p, w, l, cut, lane); ok; ++i) {
+      const CkxTile x = it.tile(p, w, w.ml_a, w.ml_b, 2);
+      ok = warp_wait(&r_free[i % kCkxRing], ((i / kCkxRing) & 1) ^ 1, wc);
+      if (!ok) break;
+      if (lane == 0) {
+        ring[i % kCkxRing] = x;
+        mbar_arrive(&r_full[i % kCkxRing]);
+      }
+      if (x.rows == 0) break;
+      ok = warp_wait(q_empty, (i & 1) ^ 1, wc);
+      if (!ok) break;
+      ckx_queries<D>(&qmap, sQ, q_full, it.k.q.tok0, x.hq0, x.n8, x.i0, x.rows, lane);
+      int page = ckx_page(p, sh, x.s, x.len, x.tile, lane);
+      for (int j = x.tile; j < x.end; ++j, ++issued) {
+        const int ahead = j + 1 < x.end ? ckx_page(p, sh, x.s, x.len, j + 1, lane) : -1;
+        const int st = issued % C::kStages;
+        ok = warp_wait(&k_empty[st], ((issued / C::kStages) & 1) ^ 1, wc);
+        if (!ok) break;
+        ckx_load<D>(p, sh, &kmap, sK + st * C::kTB, &k_full[st], x.len, j, x.hkv, page, lane);
+        page = ahead;
+      }
+      it.next(p, w, l, x);
+    }
+    if (*abort_flag && lane == 0) {
+      for (int t = issued > C::kStages ? issued - C::kStages : 0; t < issued; ++t)
+        ckx_drain(&k_full[t % C::kStages], (t / C::kStages) & 1);
+      if (i > 0) ckx_drain(q_full, (i - 1) & 1);
+      ckx_drain(q_full, i & 1);
+    }
+  } else if (warp == 9) {
+    // ---------------------------------------------------------------- MMA issue
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(128, kCkxEdge, false, false);
+      const uint64_t dQ = ckx_kmajor(sQ), dK = ckx_kmajor(sK);
+      int t = 0;
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        ok = mbar_wait(&r_full[i % kCkxRing], (i / kCkxRing) & 1, wc);
+        if (!ok) break;
+        const CkxTile &x = ring[i % kCkxRing];
+        const int rows = x.rows, tiles = x.end - x.tile;
+        mbar_arrive(&r_free[i % kCkxRing]);
+        if (rows == 0) break;
+        ok = mbar_wait(q_full, i & 1, wc);
+        for (int j = 0; ok && j < tiles; ++j, ++t) {
+          const int st = t % C::kStages, b = t & 1;
+          ok = mbar_wait(&k_full[st], (t / C::kStages) & 1, wc) && mbar_wait(&s_free[b], ((t >> 1) & 1) ^ 1, wc);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dKs = dK + (uint64_t)st * (C::kTB >> 4);
+          MmaRun<0, 4, 2, 2, false>::go(tmem + b * 128, dQ, dKs, idesc, 0u);
+          if constexpr (D == 128)
+            MmaRun<0, 4, 2, 2, false>::go(tmem + b * 128, dQ + (kCkxHalf >> 4), dKs + (kCkxHalf >> 4), idesc, 1u);
+          mma_commit(&s_full[b]);
+          mma_commit(&k_empty[st]);
+        }
+        if (ok) mma_commit(q_empty);
+      }
+      mma_commit(done);
+      ckx_drain(done, 0);
+    }
+  } else if (warp < 8) {
+    // ---------------------------------------------------------------- reduction
+    const int g = warp / 4, quarter = warp % 4, c = quarter * 32 + lane;   // tile parity; row of the column tile
+    const uint32_t ts = tmem + g * 128 + ((uint32_t)(quarter * 32) << 16);
+    for (int i = 0;; ++i) {
+      if (!warp_wait(&r_full[i % kCkxRing], (i / kCkxRing) & 1, wc)) break;
+      const CkxTile &x = ring[i % kCkxRing];
+      const int rows = x.rows, tiles = x.end - x.tile, t0 = x.t0, first = x.tile;
+      const int q = x.query(c);
+      const bool valid = c < rows && q < x.n;
+      const int last = valid ? x.P + q : -1;   // the last key that the row sees
+      float2 *to = reinterpret_cast<float2 *>(x.place) + c;
+      float c2 = 1e-30f;
+      if (valid)
+        c2 = fmaxf(head_c2(p.hs, x.s * p.c.Hq + x.hq0 + (x.n8 ? c / x.n8 : 0), g == 0 ? p.status : nullptr), 1e-30f);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&r_free[i % kCkxRing]);
+      if (rows == 0) break;
+      const bool work = quarter * 32 < rows;   // uniform over the warp
+      float m = -INFINITY;
+      float2 l0 = make_float2(0.f, 0.f), l1 = make_float2(0.f, 0.f);
+      auto take = [&](float (&v)[32], int left) {   // 32 keys, of which the row sees `left`
+        if (left < 32) {
+          if (left <= 0) return;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (e >= left) v[e] = -INFINITY;
+        }
+        float a[11];
+#pragma unroll
+        for (int e = 0; e < 10; ++e) a[e] = fmax3(v[3 * e], v[3 * e + 1], v[3 * e + 2]);
+        a[10] = fmaxf(v[30], v[31]);
+        const float top =
+            fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmax3(a[6], a[7], fmax3(a[8], a[9], a[10])));
+        if (top == -INFINITY) return;
+        const float mn = fmaxf(m, top * c2);
+        const float f = ex2_approx(m - mn);
+        m = mn;
+        l0 = fmul2(l0, make_float2(f, f));
+        l1 = fmul2(l1, make_float2(f, f));
+        const float2 c2v = make_float2(c2, c2), nm = make_float2(-mn, -mn);
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const float2 x0 = ffma2(make_float2(v[2 * e], v[2 * e + 1]), c2v, nm);
+          const float2 x1 = ffma2(make_float2(v[2 * e + 2], v[2 * e + 3]), c2v, nm);
+          l0 = fadd2(l0, make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
+          l1 = fadd2(l1, make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
+        }
+      };
+      bool ok = true;
+      for (int j = g ^ (t0 & 1); j < tiles; j += 2) {   // alternate tiles of the CTA
+        const int t = t0 + j;
+        ok = warp_wait(&s_full[g], (t >> 1) & 1, wc);
+        if (!ok) break;
+        tc_fence_after();
+        if (work) {
+          const int left = last + 1 - (first + j) * kCkxEdge;
+          float a[32], b[32];
+          tmem_ld32(ts, a);
+          tmem_wait_ld_r(a);
+          tmem_ld32(ts + 32, b);
+          take(a, left);
+          tmem_wait_ld_r(b);
+          tmem_ld32(ts + 64, a);
+          take(b, left - 32);
+          tmem_wait_ld_r(a);
+          tmem_ld32(ts + 96, b);
+          take(a, left - 64);
+          tmem_wait_ld_r(b);
+          ckx_release(&s_free[g], lane);
+          take(b, left - 96);
+        } else {
+          ckx_release(&s_free[g], lane);
+        }
+      }
+      if (!ok) break;
+      // the two warpgroups' halves of a row meet in warpgroup 0
+      const float sum = (l0.x + l0.y) + (l1.x + l1.y);
+      if (g == 1) {
+        if (!warp_wait(&ml_free[quarter], (i & 1) ^ 1, wc)) break;
+        s_ml[c] = make_float2(m, sum);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ml_full[quarter]);
+      } else {
+        if (!warp_wait(&ml_full[quarter], i & 1, wc)) break;
+        const float2 o = s_ml[c];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ml_free[quarter]);
+        const float mn = fmaxf(m, o.x), ms = mn == -INFINITY ? 0.f : mn;
+        if (valid) *to = make_float2(mn, sum * ex2_approx(m - ms) + o.y * ex2_approx(o.x - ms));
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// ============================================================================ pass 2
+// Registers (setmaxnreg): the block's at launch, kRegsLaunch a thread, are dealt out
+// anew to demand, epilogue and control warpgroups (checked on the host).
+template <int D>
+struct CkxVal {
+  static constexpr int kG = D == 64 ? 3 : 2;           // demand warpgroups
+  static constexpr int kThreads = (kG + 2) * 128;      // an epilogue and a control warpgroup
+  static constexpr int kRegsDemand = D == 64 ? 128 : 168, kRegsEpi = D == 64 ? 48 : 72, kRegsCtl = D == 64 ? 48 : 72;
+  static constexpr int kRegsLaunch = D == 64 ? 96 : 120;
+  static constexpr int kRegsNeeded = 128 * (kG * kRegsDemand + kRegsEpi + kRegsCtl);
+  static constexpr int kTB = kCkxEdge * D * 2;
+  static constexpr int kStages = D == 64 ? 3 : 2;      // of K, and of V
+  static constexpr uint32_t kShBytes = 32 * 1024;      // a warpgroup's shares: 2 x 64 rows x 128 keys
+  static constexpr uint32_t kOffQ = 0;
+  static constexpr uint32_t kOffK = kTB;
+  static constexpr uint32_t kOffV = kOffK + kStages * kTB;
+  static constexpr uint32_t kOffSh = kOffV + kStages * kTB;
+  static constexpr uint32_t kOffOnes = kOffSh + kG * kShBytes;   // above every V tile (positive offset)
+  static constexpr uint32_t kOffRing = kOffOnes + 2048;
+  static constexpr uint32_t kOffBar = kOffRing + kCkxRing * sizeof(CkxTile);
+  static constexpr int kSmemBytes = kOffBar + 384;     // (the base is 1024-byte aligned)
+  // TMEM: S^T of warpgroup g at 128 g; D (80 columns: values 0-63, share sum at 64);
+  // at d = 128 values 64-127 behind it.
+  static constexpr uint32_t kTmemD = kG * 128, kTmemDHi = kTmemD + 80;
+  static_assert(kSmemBytes <= 232448, "shared memory");
+  static_assert(kTmemDHi + D - 64 <= 512, "TMEM columns");
+  static_assert(kRegsNeeded <= kThreads * kRegsLaunch && kThreads * kRegsLaunch <= 65536, "register split");
+};
+template <int N>
+__device__ __forceinline__ void ckx_regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void ckx_regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// 32 rows of one key: bids (rows lo .. hi - 1 of the column tile see it), shares as
+// bf16 pairs.  `added`: what the column tile's rows have added to the key's total so
+// far, a sum of its own (a total of 1 would lose half of the bits of bids of 10^-5);
+// base: the total before them, and eps.  One reciprocal serves two rows,
+// 1 / (d0 d1), with d >= eps >= 1e-18.  nl: -lse2 of the 32 rows.
+template <bool MASK, bool EARLIER>
+__device__ __forceinline__ void ckx_shares(const float (&x)[32], int col0, int lo, int hi, float c2, const float *nl, float base,
+                                           float &added, uint32_t (&pk)[16]) {
+  const float2 c2v = make_float2(c2, c2), b2 = make_float2(base, base);
+  float p[32], d[32];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float4 n4 = reinterpret_cast<const float4 *>(nl)[i];
+    const float2 x0 = ffma2(make_float2(x[4 * i], x[4 * i + 1]), c2v, make_float2(n4.x, n4.y));
+    const float2 x1 = ffma2(make_float2(x[4 * i + 2], x[4 * i + 3]), c2v, make_float2(n4.z, n4.w));
+    p[4 * i] = ex2_approx(x0.x);
+    p[4 * i + 1] = ex2_approx(x0.y);
+    p[4 * i + 2] = ex2_approx(x1.x);
+    p[4 * i + 3] = ex2_approx(x1.y);
+  }
+  if (MASK) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if ((unsigned)(col0 + c - lo) >= (unsigned)(hi - lo)) p[c] = 0.f;
+  }
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    if (EARLIER) {
+      d[c] = added;
+      added += p[c];
+    } else {
+      added += p[c];
+      d[c] = added;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 dd = fadd2(make_float2(d[2 * i], d[2 * i + 1]), b2);
+    const float r = rcp_approx(dd.x * dd.y);
+    const float2 sh =
+        fmul2(fmul2(make_float2(p[2 * i], p[2 * i + 1]), make_float2(dd.y, dd.x)), make_float2(r, r));
+    pk[i] = pack_bf16x2(sh.x, sh.y);
+  }
+}
+
+template <int D, bool EARLIER>
+__global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>::kRegsLaunch)
+    ckx_values(PagedChunk p, ChunkPlan w, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+               const __grid_constant__ CUtensorMap vmap) {
+  using C = CkxVal<D>;
+  constexpr int kG = C::kG;
+  extern __shared__ __align__(1024) uint8_t ckx_smem_raw[];
+  uint8_t *smem = ckx_smem_raw;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (smem_u32(ckx_smem_raw) & 1023u) {   // no room to align it: refuse rather than compute with misaligned operands
+    if (threadIdx.x == 0) atomicCAS(p.status, DA_OK, DA_ERR_UNSUPPORTED);
+    return;
+  }
+  uint8_t *sQ = smem + C::kOffQ, *sK = smem + C::kOffK, *sV = smem + C::kOffV, *sSh = smem + C::kOffSh;
+  CkxTile *ring = reinterpret_cast<CkxTile *>(smem + C::kOffRing);
+  uint64_t *r_full = reinterpret_cast<uint64_t *>(smem + C::kOffBar), *r_free = r_full + kCkxRing;
+  uint64_t *q_full = r_free + kCkxRing, *q_empty = q_full + 1, *k_full = q_empty + 1, *k_empty = k_full + C::kStages;
+  uint64_t *v_full = k_empty + C::kStages, *v_empty = v_full + C::kStages, *s_full = v_empty + C::kStages;
+  uint64_t *s_free = s_full + kG, *sh_full = s_free + kG, *sh_free = sh_full + kG, *d_full = sh_free + kG;
+  uint64_t *d_free = d_full + 1, *done = d_free + 1;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + kG);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, wg = warp / 4;
+  constexpr int kWarpCtl = (kG + 1) * 4;
+  if (tid == 0) {
+    for (int i = 0; i < kCkxRing; ++i) {
+      mbar_init(&r_full[i], 1);
+      mbar_init(&r_free[i], kG + 4 + 4 * kG);   // issuers, epilogue and demand warps
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, kG);   // one commit per issuer
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int g = 0; g < kG; ++g) {
+      mbar_init(&s_full[g], 1);
+      mbar_init(&s_free[g], 4);
+      mbar_init(&sh_full[g], 4);
+      mbar_init(&sh_free[g], 1);
+      mbar_init(&done[g], 1);
+    }
+    mbar_init(d_full, kG);    // one commit per issuer
+    mbar_init(d_free, 4);     // phase i: D holds zeros for column tile i
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  for (int e = tid; e < 2048 / 4; e += C::kThreads)   // the ones beside V: bf16 1.0
+    reinterpret_cast<uint32_t *>(smem + C::kOffOnes)[e] = 0x3F803F80u;
+  fence_proxy_async_smem();
+  if (warp == kWarpCtl) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtx wc{abort_flag, p.status};
+
+  if (wg == kG + 1) {
+    ckx_regs_dec<C::kRegsCtl>();
+    if (warp == kWarpCtl) {
+      // -------------------------------------------------------------- producer
+      // V follows K a tile behind: the products with V come later.
+      const ChunkLine l = chunk_line(p, w);
+      const ChunkCut cut = chunk_cut(__ldcg(l.cum + p.c.S), w.ctas_values);
+      const int sh = w.page_shift;
+      CkxWalk it;
+      int i = 0, nk = 0, nv = 0;
+      bool ok = true;
+      int v_len = 0, v_tile = 0, v_hkv = 0, v_page = -1;   // V still to be brought
+      bool v_any = false;
+      auto bring_v = [&]() {
+        if (!v_any) return true;
+        const int st = nv % C::kStages;
+        if (!warp_wait(&v_empty[st], ((nv / C::kStages) & 1) ^ 1, wc)) return false;
+        ckx_load<D>(p, sh, &vmap, sV + st * C::kTB, &v_full[st], v_len, v_tile, v_hkv, v_page, lane);
+        ++nv;
+        v_any = false;
+        return true;
+      };
+      for (it.start(p, w, l, cut, lane); ok; ++i) {
+        const CkxTile x = it.tile(p, w, w.acc_a, w.acc_b, acc_stride(D));
+        ok = warp_wait(&r_free[i % kCkxRing], ((i / kCkxRing) & 1) ^ 1, wc);
+        if (!ok) break;
+        if (lane == 0) {
+          ring[i % kCkxRing] = x;
+          mbar_arrive(&r_full[i % kCkxRing]);
+        }
+        ok = bring_v();
+        if (!ok || x.rows == 0) break;
+        int page = ckx_page(p, sh, x.s, x.len, x.tile, lane);
+        ok = warp_wait(q_empty, (i & 1) ^ 1, wc);
+        if (!ok) break;
+        ckx_queries<D>(&qmap, sQ, q_full, it.k.q.tok0, x.hq0, x.n8, x.i0, x.rows, lane);
+        for (int j = x.tile; j < x.end; ++j) {
+          const int ahead = j + 1 < x.end ? ckx_page(p, sh, x.s, x.len, j + 1, lane) : -1;
+          const int st = nk % C::kStages;
+          ok = warp_wait(&k_empty[st], ((nk / C::kStages) & 1) ^ 1, wc);
+          if (!ok) break;
+          ckx_load<D>(p, sh, &kmap, sK + st * C::kTB, &k_full[st], x.len, j, x.hkv, page, lane);
+          ++nk;
+          ok = bring_v();
+          if (!ok) break;
+          v_any = true;
+          v_len = x.len, v_tile = j, v_hkv = x.hkv, v_page = page;
+          page = ahead;
+        }
+        it.next(p, w, l, x);
+      }
+      if (*abort_flag && lane == 0) {
+        for (int t = nk > C::kStages ? nk - C::kStages : 0; t < nk; ++t)
+          ckx_drain(&k_full[t % C::kStages], (t / C::kStages) & 1);
+        for (int t = nv > C::kStages ? nv - C::kStages : 0; t < nv; ++t)
+          ckx_drain(&v_full[t % C::kStages], (t / C::kStages) & 1);
+        if (i > 0) ckx_drain(q_full, (i - 1) & 1);
+        ckx_drain(q_full, i & 1);
+      }
+    } else if (warp <= kWarpCtl + kG && lane == 0) {
+      // -------------------------------------------------------------- MMA issuers
+      // S of the warpgroup's next key tile goes before the value product of the one
+      // at hand: its slot is free before the shares are written.  An issuer without
+      // tiles in a column tile takes part in its barriers all the same, and after
+      // those of the one before (d_free).
+      const int g = warp - kWarpCtl - 1;
+      const uint32_t idesc_pv = idesc_bf16(128, 80, true, true), idesc_hi = idesc_bf16(128, 64, true, true);
+      const uint32_t ones = smem_u32(smem + C::kOffOnes);
+      const uint64_t dQ = ckx_kmajor(sQ), dK = ckx_kmajor(sK);
+      // share^T: 64-row blocks 16 KB apart, 8-key groups 1 KB apart
+      const uint64_t dSh = smem_desc(smem_u32(sSh) + g * C::kShBytes, 16384, 1024);
+      int m = 0, mv = 0;          // tiles of this warpgroup: S issued, value products issued
+      int vt = 0, vi = 0;         // the tile whose value product is due, its column tile
+      bool due = false, ends = false;
+      bool ok = true;
+      auto values = [&]() {       // D += share^T [V | 1]
+        if (!due) return true;
+        due = false;
+        const int st = vt % C::kStages;
+        if (!mbar_wait(d_free, vi & 1, wc) || !mbar_wait(&v_full[st], (vt / C::kStages) & 1, wc) ||
+            !mbar_wait(&sh_full[g], mv & 1, wc))
+          return false;
+        ++mv;
+        tc_fence_after();
+        const uint32_t v = smem_u32(sV) + st * C::kTB;
+        MmaRun<0, 8, 128, 128 - (128ll << 16), false>::go(tmem + C::kTmemD, dSh, smem_desc(v, ones - v, 1024), idesc_pv, 1u);
+        if constexpr (D == 128)
+          MmaRun<0, 8, 128, 128, false>::go(tmem + C::kTmemDHi, dSh, smem_desc(v + kCkxHalf, kCkxHalf, 1024), idesc_hi, 1u);
+        mma_commit(&sh_free[g]);
+        mma_commit(&v_empty[st]);
+        if (ends) mma_commit(d_full);
+        return true;
+      };
+      // Before the first S of column tile i, with a value product due: whichever can go
+      // first.  The keys that S needs may come only after values whose place that very
+      // product frees (5 tiles, then 3: the producer waits with V(5) for the product of
+      // tile 2, before it brings K(7)).
+      auto first_of = [&](int i, uint64_t *k_bar, uint32_t k_parity) {
+        const int st = vt % C::kStages;
+        const unsigned long long began = globaltimer();
+        while (!(mbar_test_wait(q_full, i & 1) && mbar_test_wait(k_bar, k_parity) &&
+                 mbar_test_wait(&s_free[g], (m & 1) ^ 1))) {
+          if (mbar_test_wait(d_free, vi & 1) && mbar_test_wait(&v_full[st], (vt / C::kStages) & 1) &&
+              mbar_test_wait(&sh_full[g], mv & 1))
+            return values();
+          if (*abort_flag) return false;
+          if (globaltimer() - began > wc.limit_ns) {
+            raise_timeout(wc, k_bar);
+            return false;
+          }
+          __nanosleep(40);
+        }
+        return true;
+      };
+      for (int i = 0; ok; ++i) {
+        ok = mbar_wait(&r_full[i % kCkxRing], (i / kCkxRing) & 1, wc);
+        if (!ok) break;
+        const CkxTile &x = ring[i % kCkxRing];
+        const int rows = x.rows, tiles = x.end - x.tile, t0 = x.t0;
+        mbar_arrive(&r_free[i % kCkxRing]);
+        if (rows == 0) break;
+        const uint32_t idesc_s = idesc_bf16(128, (rows + 15) & ~15, false, false);
+        for (int j = g; ok && j < tiles; j += kG, ++m) {
+          const int t = t0 + j, st = t % C::kStages;
+          if (j == g && due) ok = first_of(i, &k_full[st], (t / C::kStages) & 1);
+          ok = ok && mbar_wait(q_full, i & 1, wc) && mbar_wait(&k_full[st], (t / C::kStages) & 1, wc) &&
+               mbar_wait(&s_free[g], (m & 1) ^ 1, wc);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dKs = dK + (uint64_t)st * (C::kTB >> 4);
+          MmaRun<0, 4, 2, 2, false>::go(tmem + g * 128, dKs, dQ, idesc_s, 0u);
+          if constexpr (D == 128)
+            MmaRun<0, 4, 2, 2, false>::go(tmem + g * 128, dKs + (kCkxHalf >> 4), dQ + (kCkxHalf >> 4), idesc_s, 1u);
+          mma_commit(&s_full[g]);
+          mma_commit(&k_empty[st]);
+          if (j + kG >= tiles) mma_commit(q_empty);   // its last S of the column tile
+          ok = values();
+          due = true;
+          vt = t;
+          vi = i;
+          ends = j + kG >= tiles;
+        }
+        if (!ok) break;
+        if (g >= tiles) {
+          ok = mbar_wait(q_full, i & 1, wc);
+          if (!ok) break;
+          mma_commit(q_empty);
+          ok = values() && mbar_wait(d_free, i & 1, wc);
+          if (ok) mma_commit(d_full);
+        }
+      }
+      if (ok) values();
+      mma_commit(&done[g]);
+      ckx_drain(&done[g], 0);
+    }
+  } else if (wg == kG) {
+    // ---------------------------------------------------------------- epilogue
+    ckx_regs_dec<C::kRegsEpi>();
+    const int quarter = warp % 4, c = quarter * 32 + lane;
+    const uint32_t td = tmem + C::kTmemD + ((uint32_t)(quarter * 32) << 16);
+    auto zero = [&]() {
+      tmem_zero80(td);
+      if constexpr (D == 128) tmem_zero64(td + (C::kTmemDHi - C::kTmemD));
+      tmem_wait_st();
+      ckx_release(d_free, lane);
+    };
+    zero();
+    for (int i = 0;; ++i) {
+      if (!warp_wait(&r_full[i % kCkxRing], (i / kCkxRing) & 1, wc)) break;
+      const CkxTile &x = ring[i % kCkxRing];
+      const int rows = x.rows;
+      float *to = x.place + (size_t)c * acc_stride(D);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&r_free[i % kCkxRing]);
+      if (rows == 0) break;
+      if (!warp_wait(d_full, i & 1, wc)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int e = 0; e < D; e += 16) {
+        float a[8], b[8];
+        const uint32_t at = td + (e < 64 ? e : C::kTmemDHi - C::kTmemD + e - 64);
+        tmem_ld8(at, a);
+        tmem_ld8(at + 8, b);
+        tmem_wait_ld_r8(a);
+        tmem_wait_ld_r8(b);
+        if (c < rows) {
+          float4 *o = reinterpret_cast<float4 *>(to + e);
+          o[0] = make_float4(a[0], a[1], a[2], a[3]);
+          o[1] = make_float4(a[4], a[5], a[6], a[7]);
+          o[2] = make_float4(b[0], b[1], b[2], b[3]);
+          o[3] = make_float4(b[4], b[5], b[6], b[7]);
+        }
+        __syncwarp();
+      }
+      float sum;
+      tmem_ld1(td + 64, sum);
+      tmem_wait_ld();
+      asm volatile("" : "+f"(sum));
+      if (c < rows) to[D] = sum;
+      __syncwarp();
+      zero();
+    }
+  } else {
+    // ---------------------------------------------------------------- demand
+    ckx_regs_inc<C::kRegsDemand>();
+    const int g = wg, quarter = warp % 4, key_l = quarter * 32 + lane, swz = key_l & 7;   // key of the tile
+    const uint32_t ts = tmem + g * 128 + ((uint32_t)(quarter * 32) << 16);
+    uint8_t *sh_row = sSh + g * C::kShBytes + (key_l / 8) * 1024 + (key_l % 8) * 128;
+    const int sh = w.page_shift, ps = 1 << sh;
+    int m = 0;   // the warpgroup's tiles so far
+    // 32 shares of chunk c of the rows: 64-row block c / 2, pieces (c % 2) 4 .. of this key's row
+    auto store = [&](const uint32_t (&pk)[16], int c) {
+      uint8_t *dst = sh_row + (c >> 1) * 16384;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4 *>(dst + ((((c & 1) * 4 + i) ^ swz) << 4)) =
+            make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+    };
+    for (int i = 0;; ++i) {
+      if (!warp_wait(&r_full[i % kCkxRing], (i / kCkxRing) & 1, wc)) break;
+      const CkxTile &x = ring[i % kCkxRing];
+      if (x.rows == 0) break;
+      bool ok = true;
+      // the page of this thread's key in tile j, for the totals; -1: none
+      auto page_of = [&](int j) {
+        const int key = j * kCkxEdge + key_l;
+        return key < x.len ? __ldcg(p.c.demand_table + (size_t)x.s * p.c.max_pages + (key >> sh)) : -1;
+      };
+      auto total_at = [&](int page, int j) -> float * {   // of query head hq0
+        const int key = j * kCkxEdge + key_l;
+        if ((unsigned)page < (unsigned)p.c.num_demand_pages)
+          return p.c.demand_pages + ((((size_t)page * p.c.Hq + x.hq0) << sh) + (key & (ps - 1)));
+        if (key < x.len) atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
+        return nullptr;
+      };
+      int j = x.tile + g;
+      float *at = j < x.end ? total_at(page_of(j), j) : nullptr;
+      float total = at != nullptr ? __ldcg(at) : 0.f;
+      for (; j < x.end; j += kG, ++m) {
+        const int next_page = j + kG < x.end ? page_of(j + kG) : -1;
+        const int key = j * kCkxEdge + key_l;
+        float *next_at = nullptr;
+        float next_total = 0.f;
+        ok = warp_wait(&s_full[g], m & 1, wc);
+        if (!ok) break;
+        tc_fence_after();
+        if ((j + 1) * kCkxEdge > x.len) {
+          // rows of V past the sequence's end may hold anything, and 0 times that is not 0
+          const int t = x.t0 + (j - x.tile), st = t % C::kStages;
+          ok = warp_wait(&v_full[st], (t / C::kStages) & 1, wc);
+          if (!ok) break;
+          if (key >= x.len) {
+#pragma unroll
+            for (int e = 0; e < D / 8; ++e)
+              *reinterpret_cast<uint4 *>(sV + st * C::kTB + (e >> 3) * kCkxHalf + key_l * 128 + ((e & 7) << 4)) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+        if (x.n8 == 0) {
+          // one head: 32 rows at a time, the load of the next ones in flight meanwhile
+          const int rows = x.rows, first = x.P + x.i0;   // place of row 0
+          const int lo = key < x.len ? min(max(key - first, 0), rows) : rows, hi = rows;   // rows that see the key
+          const bool mask = (j + 1) * kCkxEdge - 1 > first || rows < kCkxEdge;
+          const float c2 = fmaxf(head_c2(p.hs, x.s * p.c.Hq + x.hq0, nullptr), 1e-30f);
+          const float *nl = x.nl;
+          const float base = total + p.eps;
+          float added = 0.f;
+          float a[32], b[32];
+          uint32_t pk[16];
+          auto shares = [&](const float (&v)[32], int c) {
+            if (mask)
+              ckx_shares<true, EARLIER>(v, 32 * c, lo, hi, c2, nl + 32 * c, base, added, pk);
+            else
+              ckx_shares<false, EARLIER>(v, 32 * c, lo, hi, c2, nl + 32 * c, base, added, pk);
+            store(pk, c);
+          };
+          tmem_ld32(ts, a);
+          tmem_wait_ld_r(a);
+          tmem_ld32(ts + 32, b);
+          ok = warp_wait(&sh_free[g], (m & 1) ^ 1, wc);   // the product of the tile before has read the shares
+          if (!ok) break;
+          shares(a, 0);
+          tmem_wait_ld_r(b);
+          tmem_ld32(ts + 64, a);
+          if (j + kG < x.end) {
+            next_at = total_at(next_page, j + kG);
+            if (next_at != nullptr) next_total = __ldcg(next_at);
+          }
+          if (rows > 32) shares(b, 1);
+          tmem_ld32(ts + 96, b);
+          tmem_wait_ld_r(a);
+          tmem_wait_ld_r(b);
+          ckx_release(&s_free[g], lane);   // the next tile's S while the last two chunks are formed
+          if (rows > 64) shares(a, 2);
+          if (rows > 96) shares(b, 3);
+          if (at != nullptr) __stcg(at, total + added);
+        } else {
+          // several heads of n8 rows: 8 rows at a time, a head's total from its first rows to its last
+          const int groups = x.rows / 8, per = x.n8 / 8;
+          const int lo = key < x.len ? max(key - x.P, 0) : x.n, hi = x.n;   // queries that see the key
+          if (j + kG < x.end) {
+            next_at = total_at(next_page, j + kG);
+            if (next_at != nullptr) next_total = __ldcg(next_at);
+          }
+          float *head_at = at;
+          float head_next = 0.f, added = 0.f;
+          float c2 = 0.f;
+          int q = 0;   // query of the group's first row
+          float v[8];
+          tmem_ld8(ts, v);
+          ok = warp_wait(&sh_free[g], (m & 1) ^ 1, wc);
+          if (!ok) break;
+          for (int u = 0, h = 0; u < groups; ++u) {
+            if (q == 0) {
+              c2 = fmaxf(head_c2(p.hs, x.s * p.c.Hq + x.hq0 + h, nullptr), 1e-30f);
+              if (u + per < groups && head_at != nullptr) head_next = __ldcg(head_at + ps);
+            }
+            float nlv[8];
+            *reinterpret_cast<float4 *>(nlv) = *reinterpret_cast<const float4 *>(x.nl + 8 * u);
+            *reinterpret_cast<float4 *>(nlv + 4) = *reinterpret_cast<const float4 *>(x.nl + 8 * u + 4);
+            tmem_wait_ld_r8(v);
+            float bid[8], d[8];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const float2 y = ffma2(make_float2(v[e], v[e + 1]), make_float2(c2, c2), make_float2(nlv[e], nlv[e + 1]));
+              bid[e] = (unsigned)(q + e - lo) < (unsigned)(hi - lo) ? ex2_approx(y.x) : 0.f;
+              bid[e + 1] = (unsigned)(q + e + 1 - lo) < (unsigned)(hi - lo) ? ex2_approx(y.y) : 0.f;
+            }
+            if (u + 1 < groups)
+              tmem_ld8(ts + 8 * (u + 1), v);
+            else
+              ckx_release(&s_free[g], lane);
+            uint32_t pk[4];
+            const float2 b2 = make_float2(total + p.eps, total + p.eps);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              d[e] = added;
+              added += bid[e];
+              if (!EARLIER) d[e] = added;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 dd = fadd2(make_float2(d[2 * e], d[2 * e + 1]), b2);
+              const float r = rcp_approx(dd.x * dd.y);
+              const float2 s2 =
+                  fmul2(fmul2(make_float2(bid[2 * e], bid[2 * e + 1]), make_float2(dd.y, dd.x)), make_float2(r, r));
+              pk[e] = pack_bf16x2(s2.x, s2.y);
+            }
+            *reinterpret_cast<uint4 *>(sh_row + (u >> 3) * 16384 + (((u & 7) ^ swz) << 4)) =
+                make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            q += 8;
+            if (q == x.n8) {   // the head's last rows
+              q = 0;
+              ++h;
+              if (head_at != nullptr) {
+                __stcg(head_at, total + added);
+                head_at += ps;
+              }
+              total = head_next;
+              added = 0.f;
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh_full[g]);
+        at = next_at;
+        total = next_total;
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&r_free[i % kCkxRing]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpCtl) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ============================================================================ host
+cudaError_t launch_chunk_plan(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream);   // paged_chunk.cu
+cudaError_t launch_chunk_join(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream);
+cudaError_t launch_chunk_combine(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream);
+
+// A register split larger than what the block is launched with would never
+// resolve: refuse unless the compiled register count covers it.
+template <int D, bool EARLIER>
+static int ckx_prepare_values() {
+  using C = CkxVal<D>;
+  if (cudaFuncSetAttribute(ckx_values<D, EARLIER>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
+    return DA_ERR_CUDA;
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, ckx_values<D, EARLIER>) != cudaSuccess) return DA_ERR_CUDA;
+  return fa.numRegs * C::kThreads < C::kRegsNeeded || fa.numRegs > C::kRegsDemand || fa.numRegs < C::kRegsEpi
+             ? DA_ERR_UNSUPPORTED
+             : DA_OK;
+}
+
+template <int D>
+static int launch_ckx(const PagedChunk &p, cudaStream_t stream) {
+  static PerDeviceOnce once;
+  const int prep = once.run([] {
+    if (cudaFuncSetAttribute(ckx_keys<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, CkxKeys<D>::kSmemBytes) != cudaSuccess)
+      return DA_ERR_CUDA;
+    const int st = ckx_prepare_values<D, false>();
+    return st != DA_OK ? st : ckx_prepare_values<D, true>();
+  });
+  if (prep != DA_OK) return prep;
+  const ChunkPlan w = chunk_plan_bf16(p.c.S, p.c.Hq, p.c.Hkv, D, p.N, p.max_new, p.c.page_size);
+  const int64_t num = (int64_t)p.c.num_pages * p.c.Hkv;
+  CUtensorMap qm, km, vm;
+  // (an empty pool has no pages to map: every page id then fails its check)
+  if (!make_rows_map(&qm, p.q, p.N, p.c.Hq, D, 8) ||
+      !make_page_map(&km, p.c.k_pages, num > 0 ? num : 1, p.c.page_size, kCkxEdge, D, DA_BF16) ||
+      !make_page_map(&vm, p.c.v_pages, num > 0 ? num : 1, p.c.page_size, kCkxEdge, D, DA_BF16))
+    return DA_ERR_CUDA;
+  using V = CkxVal<D>;
+  if (launch_chunk_plan(p, w, stream) != cudaSuccess ||
+      launch_after(ckx_keys<D>, w.ctas_keys, CkxKeys<D>::kThreads, CkxKeys<D>::kSmemBytes, stream, p, w, qm, km) !=
+          cudaSuccess ||
+      launch_chunk_join(p, w, stream) != cudaSuccess ||
+      (p.earlier ? launch_after(ckx_values<D, true>, w.ctas_values, V::kThreads, V::kSmemBytes, stream, p, w, qm, km, vm)
+                 : launch_after(ckx_values<D, false>, w.ctas_values, V::kThreads, V::kSmemBytes, stream, p, w, qm, km, vm)) !=
+          cudaSuccess ||
+      launch_chunk_combine(p, w, stream) != cudaSuccess)
+    return DA_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+int launch_chunk_bf16(const PagedChunk &p, cudaStream_t stream) {
+  return p.c.d == 128 ? launch_ckx<128>(p, stream) : launch_ckx<64>(p, stream);
+}
+
+}  // namespace da

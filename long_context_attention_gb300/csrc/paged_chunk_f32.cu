@@ -25,7 +25,7 @@ constexpr int kCkfThreads = 256;
 constexpr int kCkfCtas = 304;   // two CTAs an SM
 
 ChunkPlan chunk_plan_f32(int S, int Hq, int Hkv, int d, long long N, int max_new, int page_size) {
-  return chunk_plan(S, Hq, Hkv, d, N, max_new, page_size, kCkfEdge, kCkfCtas, kCkfCtas, ChunkCost{8, 0, 8, 4});
+  return chunk_plan(S, Hq, Hkv, d, N, max_new, page_size, kCkfEdge, kCkfCtas, kCkfCtas, ChunkCost{0, 8, 0, 8, 4});
 }
 
 template <int D>
@@ -262,7 +262,8 @@ __global__ void __launch_bounds__(kCkfThreads, 2) ckf_values(PagedChunk p, Chunk
         if (t.n8 == 0) {   // one head: 16 rows a thread
           const int part = tid / kCkfEdge;
           float *at = ckf_total(p, w, k, key, t.hq0);
-          float run = at != nullptr ? __ldcg(at) : 0.f, mine = 0.f;
+          const float before = at != nullptr ? __ldcg(at) : 0.f;
+          float mine = 0.f, run = 0.f;   // the rows' bids, summed apart from the total: it would take their last bits
 #pragma unroll
           for (int c = 0; c < 16; ++c) mine += col[(16 * part + c) * C::kLdP];
           sPart[part * kCkfEdge + tid % kCkfEdge] = mine;
@@ -271,20 +272,21 @@ __global__ void __launch_bounds__(kCkfThreads, 2) ckf_values(PagedChunk p, Chunk
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             const float bid = col[(16 * part + c) * C::kLdP], after = run + bid;
-            col[(16 * part + c) * C::kLdP] = bid / ((p.earlier ? run : after) + p.eps);
+            col[(16 * part + c) * C::kLdP] = bid / (before + (p.earlier ? run : after) + p.eps);
             run = after;
           }
-          if (part == 3 && at != nullptr) __stcg(at, run);
+          if (part == 3 && at != nullptr) __stcg(at, before + run);
         } else {
           for (int h = tid / kCkfEdge; h * t.n8 < t.rows; h += kCkfThreads / kCkfEdge) {
             float *at = ckf_total(p, w, k, key, t.hq0 + h);
-            float run = at != nullptr ? __ldcg(at) : 0.f;
+            const float before = at != nullptr ? __ldcg(at) : 0.f;
+            float run = 0.f;
             for (int c = h * t.n8; c < h * t.n8 + t.n; ++c) {
               const float bid = col[c * C::kLdP], after = run + bid;
-              col[c * C::kLdP] = bid / ((p.earlier ? run : after) + p.eps);
+              col[c * C::kLdP] = bid / (before + (p.earlier ? run : after) + p.eps);
               run = after;
             }
-            if (at != nullptr) __stcg(at, run);
+            if (at != nullptr) __stcg(at, before + run);
           }
         }
         __syncthreads();
@@ -360,12 +362,4 @@ static int launch_ckf(const PagedChunk &p, cudaStream_t stream) {
 int launch_chunk_f32(const PagedChunk &p, cudaStream_t stream) {
   return p.c.d == 128 ? launch_ckf<128, float>(p, stream) : launch_ckf<64, float>(p, stream);
 }
-// the type's first kernels
-ChunkPlan chunk_plan_bf16(int S, int Hq, int Hkv, int d, long long N, int max_new, int page_size) {
-  return chunk_plan_f32(S, Hq, Hkv, d, N, max_new, page_size);
-}
-int launch_chunk_bf16(const PagedChunk &p, cudaStream_t stream) {
-  return p.c.d == 128 ? launch_ckf<128, __nv_bfloat16>(p, stream) : launch_ckf<64, __nv_bfloat16>(p, stream);
-}
-
 }  // namespace da

@@ -125,6 +125,16 @@ def test_long(d, dtype):
     run(cache, q, cu, 200, 2900)
 
 
+@pytest.mark.parametrize("d,Hq,Hkv,page,lens,news", [
+    (64, 12, 12, 64, [40000], [4]), (64, 6, 6, 16, [30000, 5000], [5, 130]), (64, 8, 2, 32, [20000], [150]),
+    (128, 12, 4, 256, [40000], [3]), (128, 6, 6, 64, [25000, 300], [140, 300]),
+])
+def test_long_pieces(d, Hq, Hkv, page, lens, news):
+    """A dozen key tiles and several column tiles a piece: every order of the rings, of all remainders."""
+    cache, q, cu = make(lens, news, Hq, Hkv, d, page, "bf16", seed=d + lens[0])
+    run(cache, q, cu, max(news), max(lens))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("kw", [dict(tau=0.0), dict(tau=2.5), dict(eps=1.0), dict(eps=1e-3, flags=1), dict(flags=1),
                                 dict(tau=1.7, eps=1e-15)])
