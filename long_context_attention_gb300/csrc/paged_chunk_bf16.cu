@@ -50,7 +50,7 @@ ChunkPlan chunk_plan_bf16(int S, int Hq, int Hkv, int d, long long N, int max_ne
 // A column tile of a piece, as the producer describes it.
 struct CkxTile {
   float *place;        // its rows' partial results
-  const float *nl;     // -lse2 of its rows
+  float c2;            // of one head's rows: the logits' scale
   int s, hkv, hq0;     // sequence, key head, query head of row 0
   int n8, n, i0;       // rows of a head (0: one head); queries; query of row 0
   int P, len;          // place of query 0; length
@@ -143,8 +143,16 @@ struct CkxWalk {
     x.t0 = t0;
     const long long row0 = k.row0(p, w);
     x.place = chunk_place(p, place_a, place_b, row0, w.cta_rows, k.tile, blockIdx.x, r0, stride);
-    x.nl = reinterpret_cast<const float *>(p.ws + w.nl) + row0 + r0;
+    x.c2 = k.g.wide ? fmaxf(head_c2(p.hs, k.s * p.c.Hq + x.hq0, nullptr), 1e-30f) : 0.f;
     return x;
+  }
+  // -lse2 of the column tile's rows 4 lane ..
+  __device__ __forceinline__ float4 nl(const PagedChunk &p, const ChunkPlan &w, const CkxTile &x, int lane) const {
+    const float4 v = __ldcg(reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(p.ws + w.nl) + k.row0(p, w) +
+                                                             b * k.g.step) + lane);
+    const int c = 4 * lane;
+    return make_float4(c < x.rows ? v.x : -INFINITY, c + 1 < x.rows ? v.y : -INFINITY, c + 2 < x.rows ? v.z : -INFINITY,
+                       c + 3 < x.rows ? v.w : -INFINITY);
   }
   __device__ __forceinline__ void next(const PagedChunk &p, const ChunkPlan &w, const ChunkLine &l, const CkxTile &x) {
     t0 += x.end - x.tile;
@@ -398,15 +406,21 @@ struct CkxVal {
   static constexpr int kRegsNeeded = 128 * (kG * kRegsDemand + kRegsEpi + kRegsCtl);
   static constexpr int kTB = kCkxEdge * D * 2;
   static constexpr int kStages = D == 64 ? 3 : 2;      // of K, and of V
+  // Barriers of what has landed: two rounds of stages, since those that wait for a
+  // tile need not have seen the one before it in its stage land, and a barrier's
+  // parity tells a round from the next alone.  (That before it in its barrier has been
+  // read: its stage was filled again since, before the column tile's queries came.)
+  static constexpr int kFull = 2 * kStages;
   static constexpr uint32_t kShBytes = 32 * 1024;      // a warpgroup's shares: 2 x 64 rows x 128 keys
+  static constexpr int kQs = D == 64 ? 2 : 1;          // of Q
   static constexpr uint32_t kOffQ = 0;
-  static constexpr uint32_t kOffK = kTB;
+  static constexpr uint32_t kOffK = kQs * kTB;
   static constexpr uint32_t kOffV = kOffK + kStages * kTB;
   static constexpr uint32_t kOffSh = kOffV + kStages * kTB;
   static constexpr uint32_t kOffOnes = kOffSh + kG * kShBytes;   // above every V tile (positive offset)
   static constexpr uint32_t kOffRing = kOffOnes + 2048;
   static constexpr uint32_t kOffBar = kOffRing + kCkxRing * sizeof(CkxTile);
-  static constexpr int kSmemBytes = kOffBar + 384;     // (the base is 1024-byte aligned)
+  static constexpr int kSmemBytes = kOffBar + 448;     // (the base is 1024-byte aligned)
   // TMEM: S^T of warpgroup g at 128 g; D (80 columns: values 0-63, share sum at 64);
   // at d = 128 values 64-127 behind it.
   static constexpr uint32_t kTmemD = kG * 128, kTmemDHi = kTmemD + 80;
@@ -419,30 +433,38 @@ __device__ __forceinline__ void ckx_regs_inc() { asm volatile("setmaxnreg.inc.sy
 template <int N>
 __device__ __forceinline__ void ckx_regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// 32 rows of one key: bids (rows lo .. hi - 1 of the column tile see it), shares as
-// bf16 pairs.  `added`: what the column tile's rows have added to the key's total so
+// -lse2 of a column tile's rows lies in the ones block, in the 16-byte pieces that the
+// product does not read: of its 16 rows of 128 bytes (swizzled as V) pieces 0 and 1
+// are the ones, 2 and 3, or 4 and 5, hold the values of 8 rows, for every other
+// column tile.  The place of values 4 i .. 4 i + 3 of column tile b.
+__device__ __forceinline__ uint32_t ckx_nl_place(int i, int b) {
+  return (uint32_t)((i >> 1) * 128 + (((2 + 2 * (b & 1) + (i & 1)) ^ ((i >> 1) & 7)) << 4));
+}
+// The same for constant i: bases[m] = block + ((2 + 2 (b & 1)) ^ 2 m) 16.
+__device__ __forceinline__ float4 ckx_nl(const uint8_t *const (&bases)[4], int i, int off) {
+  const int row = i >> 1;
+  return *reinterpret_cast<const float4 *>(bases[(row & 7) >> 1] + off + row * 128 + (((i ^ row) & 1) << 4));
+}
+
+// 32 rows of one key (its logits; -infinity where a row does not see it): bids, then
+// shares as bf16 pairs.  `added`: what the column tile's rows have added to the key's total so
 // far, a sum of its own (a total of 1 would lose half of the bits of bids of 10^-5);
 // base: the total before them, and eps.  One reciprocal serves two rows,
-// 1 / (d0 d1), with d >= eps >= 1e-18.  nl: -lse2 of the 32 rows.
-template <bool MASK, bool EARLIER>
-__device__ __forceinline__ void ckx_shares(const float (&x)[32], int col0, int lo, int hi, float c2, const float *nl, float base,
-                                           float &added, uint32_t (&pk)[16]) {
+// 1 / (d0 d1), with d >= eps >= 1e-18.
+template <int CHUNK, bool EARLIER>
+__device__ __forceinline__ void ckx_shares(const float (&x)[32], float c2, const uint8_t *const (&nl)[4], int off, float base, float &added,
+                                           uint32_t (&pk)[16]) {
   const float2 c2v = make_float2(c2, c2), b2 = make_float2(base, base);
   float p[32], d[32];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float4 n4 = reinterpret_cast<const float4 *>(nl)[i];
+    const float4 n4 = ckx_nl(nl, 8 * CHUNK + i, off);
     const float2 x0 = ffma2(make_float2(x[4 * i], x[4 * i + 1]), c2v, make_float2(n4.x, n4.y));
     const float2 x1 = ffma2(make_float2(x[4 * i + 2], x[4 * i + 3]), c2v, make_float2(n4.z, n4.w));
     p[4 * i] = ex2_approx(x0.x);
     p[4 * i + 1] = ex2_approx(x0.y);
     p[4 * i + 2] = ex2_approx(x1.x);
     p[4 * i + 3] = ex2_approx(x1.y);
-  }
-  if (MASK) {
-#pragma unroll
-    for (int c = 0; c < 32; ++c)
-      if ((unsigned)(col0 + c - lo) >= (unsigned)(hi - lo)) p[c] = 0.f;
   }
 #pragma unroll
   for (int c = 0; c < 32; ++c) {
@@ -481,10 +503,10 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
   uint8_t *sQ = smem + C::kOffQ, *sK = smem + C::kOffK, *sV = smem + C::kOffV, *sSh = smem + C::kOffSh;
   CkxTile *ring = reinterpret_cast<CkxTile *>(smem + C::kOffRing);
   uint64_t *r_full = reinterpret_cast<uint64_t *>(smem + C::kOffBar), *r_free = r_full + kCkxRing;
-  uint64_t *q_full = r_free + kCkxRing, *q_empty = q_full + 1, *k_full = q_empty + 1, *k_empty = k_full + C::kStages;
-  uint64_t *v_full = k_empty + C::kStages, *v_empty = v_full + C::kStages, *s_full = v_empty + C::kStages;
+  uint64_t *q_full = r_free + kCkxRing, *q_empty = q_full + C::kQs, *k_full = q_empty + C::kQs, *k_empty = k_full + C::kFull;
+  uint64_t *v_full = k_empty + C::kStages, *v_empty = v_full + C::kFull, *s_full = v_empty + C::kStages;
   uint64_t *s_free = s_full + kG, *sh_full = s_free + kG, *sh_free = sh_full + kG, *d_full = sh_free + kG;
-  uint64_t *d_free = d_full + 1, *done = d_free + 1;
+  uint64_t *d_free = d_full + 1, *turn = d_free + 1, *done = turn + 4;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + kG);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, wg = warp / 4;
@@ -494,14 +516,19 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       mbar_init(&r_full[i], 1);
       mbar_init(&r_free[i], kG + 4 + 4 * kG);   // issuers, epilogue and demand warps
     }
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, kG);   // one commit per issuer
+    for (int i = 0; i < C::kQs; ++i) {
+      mbar_init(&q_full[i], 2);     // the queries' bytes, and -lse2
+      mbar_init(&q_empty[i], kG);   // one commit per issuer
+    }
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&k_full[i], 1);
       mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 1);
       mbar_init(&v_empty[i], 1);
     }
+    for (int i = 0; i < C::kFull; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&v_full[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&turn[i], 1);
     for (int g = 0; g < kG; ++g) {
       mbar_init(&s_full[g], 1);
       mbar_init(&s_free[g], 4);
@@ -543,7 +570,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
         if (!v_any) return true;
         const int st = nv % C::kStages;
         if (!warp_wait(&v_empty[st], ((nv / C::kStages) & 1) ^ 1, wc)) return false;
-        ckx_load<D>(p, sh, &vmap, sV + st * C::kTB, &v_full[st], v_len, v_tile, v_hkv, v_page, lane);
+        ckx_load<D>(p, sh, &vmap, sV + st * C::kTB, &v_full[nv % C::kFull], v_len, v_tile, v_hkv, v_page, lane);
         ++nv;
         v_any = false;
         return true;
@@ -556,18 +583,27 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
           ring[i % kCkxRing] = x;
           mbar_arrive(&r_full[i % kCkxRing]);
         }
-        ok = bring_v();
-        if (!ok || x.rows == 0) break;
+        if (x.rows == 0) {
+          ok = bring_v();
+          break;
+        }
         int page = ckx_page(p, sh, x.s, x.len, x.tile, lane);
-        ok = warp_wait(q_empty, (i & 1) ^ 1, wc);
+        const float4 nl = it.nl(p, w, x, lane);
+        const int qs = i % C::kQs;
+        // every role is done with column tile i - 2, whose -lse2 this one's replace
+        ok = (i < 2 || warp_wait(&r_free[(i - 2) % kCkxRing], ((i - 2) / kCkxRing) & 1, wc)) &&
+             warp_wait(&q_empty[qs], ((i / C::kQs) & 1) ^ 1, wc);
         if (!ok) break;
-        ckx_queries<D>(&qmap, sQ, q_full, it.k.q.tok0, x.hq0, x.n8, x.i0, x.rows, lane);
+        *reinterpret_cast<float4 *>(smem + C::kOffOnes + ckx_nl_place(lane, i)) = nl;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[qs]);
+        ckx_queries<D>(&qmap, sQ + qs * C::kTB, &q_full[qs], it.k.q.tok0, x.hq0, x.n8, x.i0, x.rows, lane);
         for (int j = x.tile; j < x.end; ++j) {
           const int ahead = j + 1 < x.end ? ckx_page(p, sh, x.s, x.len, j + 1, lane) : -1;
           const int st = nk % C::kStages;
           ok = warp_wait(&k_empty[st], ((nk / C::kStages) & 1) ^ 1, wc);
           if (!ok) break;
-          ckx_load<D>(p, sh, &kmap, sK + st * C::kTB, &k_full[st], x.len, j, x.hkv, page, lane);
+          ckx_load<D>(p, sh, &kmap, sK + st * C::kTB, &k_full[nk % C::kFull], x.len, j, x.hkv, page, lane);
           ++nk;
           ok = bring_v();
           if (!ok) break;
@@ -579,11 +615,10 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       }
       if (*abort_flag && lane == 0) {
         for (int t = nk > C::kStages ? nk - C::kStages : 0; t < nk; ++t)
-          ckx_drain(&k_full[t % C::kStages], (t / C::kStages) & 1);
+          ckx_drain(&k_full[t % C::kFull], (t / C::kFull) & 1);
         for (int t = nv > C::kStages ? nv - C::kStages : 0; t < nv; ++t)
-          ckx_drain(&v_full[t % C::kStages], (t / C::kStages) & 1);
-        if (i > 0) ckx_drain(q_full, (i - 1) & 1);
-        ckx_drain(q_full, i & 1);
+          ckx_drain(&v_full[t % C::kFull], (t / C::kFull) & 1);
+        for (int t = i > C::kQs ? i - C::kQs : 0; t <= i; ++t) ckx_drain(&q_full[t % C::kQs], (t / C::kQs) & 1);
       }
     } else if (warp <= kWarpCtl + kG && lane == 0) {
       // -------------------------------------------------------------- MMA issuers
@@ -601,12 +636,16 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       int vt = 0, vi = 0;         // the tile whose value product is due, its column tile
       bool due = false, ends = false;
       bool ok = true;
-      auto values = [&]() {       // D += share^T [V | 1]
+      // D += share^T [V | 1], in the tiles' order (sums in another order would have other
+      // last bits).  Once V of tile t is there, the product of t - kStages has been formed,
+      // so that four barriers tell whose turn it is.
+      auto values = [&]() {
         if (!due) return true;
         due = false;
         const int st = vt % C::kStages;
-        if (!mbar_wait(d_free, vi & 1, wc) || !mbar_wait(&v_full[st], (vt / C::kStages) & 1, wc) ||
-            !mbar_wait(&sh_full[g], mv & 1, wc))
+        if (!mbar_wait(d_free, vi & 1, wc) || !mbar_wait(&v_full[vt % C::kFull], (vt / C::kFull) & 1, wc) ||
+            !mbar_wait(&sh_full[g], mv & 1, wc) ||
+            (vt > 0 && !mbar_wait(&turn[(vt - 1) & 3], ((vt - 1) >> 2) & 1, wc)))
           return false;
         ++mv;
         tc_fence_after();
@@ -617,6 +656,8 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
         mma_commit(&sh_free[g]);
         mma_commit(&v_empty[st]);
         if (ends) mma_commit(d_full);
+        tc_fence_before();
+        mbar_arrive(&turn[vt & 3]);
         return true;
       };
       // Before the first S of column tile i, with a value product due: whichever can go
@@ -624,12 +665,11 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       // product frees (5 tiles, then 3: the producer waits with V(5) for the product of
       // tile 2, before it brings K(7)).
       auto first_of = [&](int i, uint64_t *k_bar, uint32_t k_parity) {
-        const int st = vt % C::kStages;
         const unsigned long long began = globaltimer();
-        while (!(mbar_test_wait(q_full, i & 1) && mbar_test_wait(k_bar, k_parity) &&
+        while (!(mbar_test_wait(&q_full[i % C::kQs], (i / C::kQs) & 1) && mbar_test_wait(k_bar, k_parity) &&
                  mbar_test_wait(&s_free[g], (m & 1) ^ 1))) {
-          if (mbar_test_wait(d_free, vi & 1) && mbar_test_wait(&v_full[st], (vt / C::kStages) & 1) &&
-              mbar_test_wait(&sh_full[g], mv & 1))
+          if (mbar_test_wait(d_free, vi & 1) && mbar_test_wait(&v_full[vt % C::kFull], (vt / C::kFull) & 1) &&
+              mbar_test_wait(&sh_full[g], mv & 1) && (vt == 0 || mbar_test_wait(&turn[(vt - 1) & 3], ((vt - 1) >> 2) & 1)))
             return values();
           if (*abort_flag) return false;
           if (globaltimer() - began > wc.limit_ns) {
@@ -650,18 +690,18 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
         const uint32_t idesc_s = idesc_bf16(128, (rows + 15) & ~15, false, false);
         for (int j = g; ok && j < tiles; j += kG, ++m) {
           const int t = t0 + j, st = t % C::kStages;
-          if (j == g && due) ok = first_of(i, &k_full[st], (t / C::kStages) & 1);
-          ok = ok && mbar_wait(q_full, i & 1, wc) && mbar_wait(&k_full[st], (t / C::kStages) & 1, wc) &&
+          if (j == g && due) ok = first_of(i, &k_full[t % C::kFull], (t / C::kFull) & 1);
+          ok = ok && mbar_wait(&q_full[i % C::kQs], (i / C::kQs) & 1, wc) && mbar_wait(&k_full[t % C::kFull], (t / C::kFull) & 1, wc) &&
                mbar_wait(&s_free[g], (m & 1) ^ 1, wc);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t dKs = dK + (uint64_t)st * (C::kTB >> 4);
-          MmaRun<0, 4, 2, 2, false>::go(tmem + g * 128, dKs, dQ, idesc_s, 0u);
+          const uint64_t dKs = dK + (uint64_t)st * (C::kTB >> 4), dQs = dQ + (uint64_t)(i % C::kQs) * (C::kTB >> 4);
+          MmaRun<0, 4, 2, 2, false>::go(tmem + g * 128, dKs, dQs, idesc_s, 0u);
           if constexpr (D == 128)
-            MmaRun<0, 4, 2, 2, false>::go(tmem + g * 128, dKs + (kCkxHalf >> 4), dQ + (kCkxHalf >> 4), idesc_s, 1u);
+            MmaRun<0, 4, 2, 2, false>::go(tmem + g * 128, dKs + (kCkxHalf >> 4), dQs + (kCkxHalf >> 4), idesc_s, 1u);
           mma_commit(&s_full[g]);
           mma_commit(&k_empty[st]);
-          if (j + kG >= tiles) mma_commit(q_empty);   // its last S of the column tile
+          if (j + kG >= tiles) mma_commit(&q_empty[i % C::kQs]);   // its last S of the column tile
           ok = values();
           due = true;
           vt = t;
@@ -670,9 +710,9 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
         }
         if (!ok) break;
         if (g >= tiles) {
-          ok = mbar_wait(q_full, i & 1, wc);
+          ok = mbar_wait(&q_full[i % C::kQs], (i / C::kQs) & 1, wc);
           if (!ok) break;
-          mma_commit(q_empty);
+          mma_commit(&q_empty[i % C::kQs]);
           ok = values() && mbar_wait(d_free, i & 1, wc);
           if (ok) mma_commit(d_full);
         }
@@ -749,6 +789,9 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       const CkxTile &x = ring[i % kCkxRing];
       if (x.rows == 0) break;
       bool ok = true;
+      const uint8_t *nl[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) nl[e] = smem + C::kOffOnes + (((2 + 2 * (i & 1)) ^ (2 * e)) << 4);
       // the page of this thread's key in tile j, for the totals; -1: none
       auto page_of = [&](int j) {
         const int key = j * kCkxEdge + key_l;
@@ -775,7 +818,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
         if ((j + 1) * kCkxEdge > x.len) {
           // rows of V past the sequence's end may hold anything, and 0 times that is not 0
           const int t = x.t0 + (j - x.tile), st = t % C::kStages;
-          ok = warp_wait(&v_full[st], (t / C::kStages) & 1, wc);
+          ok = warp_wait(&v_full[t % C::kFull], (t / C::kFull) & 1, wc);
           if (!ok) break;
           if (key >= x.len) {
 #pragma unroll
@@ -789,38 +832,47 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
           const int rows = x.rows, first = x.P + x.i0;   // place of row 0
           const int lo = key < x.len ? min(max(key - first, 0), rows) : rows, hi = rows;   // rows that see the key
           const bool mask = (j + 1) * kCkxEdge - 1 > first || rows < kCkxEdge;
-          const float c2 = fmaxf(head_c2(p.hs, x.s * p.c.Hq + x.hq0, nullptr), 1e-30f);
-          const float *nl = x.nl;
+          const float c2 = x.c2;
           const float base = total + p.eps;
           float added = 0.f;
           float a[32], b[32];
           uint32_t pk[16];
-          auto shares = [&](const float (&v)[32], int c) {
-            if (mask)
-              ckx_shares<true, EARLIER>(v, 32 * c, lo, hi, c2, nl + 32 * c, base, added, pk);
-            else
-              ckx_shares<false, EARLIER>(v, 32 * c, lo, hi, c2, nl + 32 * c, base, added, pk);
-            store(pk, c);
+          auto hide = [&](float (&v)[32], int c) {
+            if (mask) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if ((unsigned)(32 * c + e - lo) >= (unsigned)(hi - lo)) v[e] = -INFINITY;
+            }
           };
-          tmem_ld32(ts, a);
-          tmem_wait_ld_r(a);
-          tmem_ld32(ts + 32, b);
           ok = warp_wait(&sh_free[g], (m & 1) ^ 1, wc);   // the product of the tile before has read the shares
           if (!ok) break;
-          shares(a, 0);
-          tmem_wait_ld_r(b);
-          tmem_ld32(ts + 64, a);
+          tmem_ld32(ts, a);
           if (j + kG < x.end) {
             next_at = total_at(next_page, j + kG);
             if (next_at != nullptr) next_total = __ldcg(next_at);
           }
-          if (rows > 32) shares(b, 1);
-          tmem_ld32(ts + 96, b);
           tmem_wait_ld_r(a);
-          tmem_wait_ld_r(b);
-          ckx_release(&s_free[g], lane);   // the next tile's S while the last two chunks are formed
-          if (rows > 64) shares(a, 2);
-          if (rows > 96) shares(b, 3);
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            const bool last = half == 1 || rows <= 64;
+            tmem_ld32(ts + 64 * half + 32, b);
+            if (last) {   // the next tile's S is formed while the last two chunks are
+              tmem_wait_ld_r(b);
+              ckx_release(&s_free[g], lane);
+            }
+            hide(a, 2 * half);
+            ckx_shares<0, EARLIER>(a, c2, nl, half * 1024, base, added, pk);
+            store(pk, 2 * half);
+            if (!last) {
+              tmem_wait_ld_r(b);
+              tmem_ld32(ts + 64, a);
+            }
+            hide(b, 2 * half + 1);
+            ckx_shares<1, EARLIER>(b, c2, nl, half * 1024, base, added, pk);
+            store(pk, 2 * half + 1);
+            if (last) break;
+            tmem_wait_ld_r(a);
+          }
           if (at != nullptr) __stcg(at, total + added);
         } else {
           // several heads of n8 rows: 8 rows at a time, a head's total from its first rows to its last
@@ -844,8 +896,9 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
               if (u + per < groups && head_at != nullptr) head_next = __ldcg(head_at + ps);
             }
             float nlv[8];
-            *reinterpret_cast<float4 *>(nlv) = *reinterpret_cast<const float4 *>(x.nl + 8 * u);
-            *reinterpret_cast<float4 *>(nlv + 4) = *reinterpret_cast<const float4 *>(x.nl + 8 * u + 4);
+            *reinterpret_cast<float4 *>(nlv) = *reinterpret_cast<const float4 *>(smem + C::kOffOnes + ckx_nl_place(2 * u, i));
+            *reinterpret_cast<float4 *>(nlv + 4) =
+                *reinterpret_cast<const float4 *>(smem + C::kOffOnes + ckx_nl_place(2 * u + 1, i));
             tmem_wait_ld_r8(v);
             float bid[8], d[8];
 #pragma unroll
