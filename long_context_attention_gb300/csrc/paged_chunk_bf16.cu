@@ -411,6 +411,7 @@ struct CkxVal {
   // parity tells a round from the next alone.  (That before it in its barrier has been
   // read: its stage was filled again since, before the column tile's queries came.)
   static constexpr int kFull = 2 * kStages;
+  static constexpr int kLag = kG - 1;                  // V behind K
   static constexpr uint32_t kShBytes = 32 * 1024;      // a warpgroup's shares: 2 x 64 rows x 128 keys
   static constexpr int kQs = D == 64 ? 2 : 1;          // of Q
   static constexpr uint32_t kOffQ = 0;
@@ -557,22 +558,27 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
     ckx_regs_dec<C::kRegsCtl>();
     if (warp == kWarpCtl) {
       // -------------------------------------------------------------- producer
-      // V follows K a tile behind: the products with V come later.
+      // V follows K kLag tiles behind: a place for V is free a warpgroup's whole item later
+      // than one for K, and K is needed an item earlier.  (kLag = 1 at d = 64: the demand
+      // warps waited 2085 cycles an item for S, 2048 queries at 131072.)
       const ChunkLine l = chunk_line(p, w);
       const ChunkCut cut = chunk_cut(__ldcg(l.cum + p.c.S), w.ctas_values);
       const int sh = w.page_shift;
       CkxWalk it;
       int i = 0, nk = 0, nv = 0;
       bool ok = true;
-      int v_len = 0, v_tile = 0, v_hkv = 0, v_page = -1;   // V still to be brought
-      bool v_any = false;
+      int v_len[C::kLag] = {}, v_tile[C::kLag] = {}, v_hkv[C::kLag] = {}, v_page[C::kLag] = {};   // V still to be brought
+      int v_due = 0;
+      bool part = false;   // the column tile before held a sequence's last keys, not a whole tile of them
       auto bring_v = [&]() {
-        if (!v_any) return true;
         const int st = nv % C::kStages;
         if (!warp_wait(&v_empty[st], ((nv / C::kStages) & 1) ^ 1, wc)) return false;
-        ckx_load<D>(p, sh, &vmap, sV + st * C::kTB, &v_full[nv % C::kFull], v_len, v_tile, v_hkv, v_page, lane);
+        ckx_load<D>(p, sh, &vmap, sV + st * C::kTB, &v_full[nv % C::kFull], v_len[0], v_tile[0], v_hkv[0], v_page[0], lane);
         ++nv;
-        v_any = false;
+#pragma unroll
+        for (int e = 1; e < C::kLag; ++e)
+          v_len[e - 1] = v_len[e], v_tile[e - 1] = v_tile[e], v_hkv[e - 1] = v_hkv[e], v_page[e - 1] = v_page[e];
+        --v_due;
         return true;
       };
       for (it.start(p, w, l, cut, lane); ok; ++i) {
@@ -584,11 +590,15 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
           mbar_arrive(&r_full[i % kCkxRing]);
         }
         if (x.rows == 0) {
-          ok = bring_v();
+          while (ok && v_due > 0) ok = bring_v();
           break;
         }
         int page = ckx_page(p, sh, x.s, x.len, x.tile, lane);
         const float4 nl = it.nl(p, w, x, lane);
+        // (its demand warps wait for V, and what follows here waits for them)
+        while (part && ok && v_due > 0) ok = bring_v();
+        if (!ok) break;
+        part = x.end * kCkxEdge > x.len;
         const int qs = i % C::kQs;
         // every role is done with column tile i - 2, whose -lse2 this one's replace
         ok = (i < 2 || warp_wait(&r_free[(i - 2) % kCkxRing], ((i - 2) / kCkxRing) & 1, wc)) &&
@@ -605,10 +615,12 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
           if (!ok) break;
           ckx_load<D>(p, sh, &kmap, sK + st * C::kTB, &k_full[nk % C::kFull], x.len, j, x.hkv, page, lane);
           ++nk;
-          ok = bring_v();
+          if (v_due == C::kLag) ok = bring_v();
           if (!ok) break;
-          v_any = true;
-          v_len = x.len, v_tile = j, v_hkv = x.hkv, v_page = page;
+#pragma unroll
+          for (int e = 0; e < C::kLag; ++e)
+            if (e == v_due) v_len[e] = x.len, v_tile[e] = j, v_hkv[e] = x.hkv, v_page[e] = page;
+          ++v_due;
           page = ahead;
         }
         it.next(p, w, l, x);
@@ -844,8 +856,6 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
                 if ((unsigned)(32 * c + e - lo) >= (unsigned)(hi - lo)) v[e] = -INFINITY;
             }
           };
-          ok = warp_wait(&sh_free[g], (m & 1) ^ 1, wc);   // the product of the tile before has read the shares
-          if (!ok) break;
           tmem_ld32(ts, a);
           if (j + kG < x.end) {
             next_at = total_at(next_page, j + kG);
@@ -862,6 +872,10 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
             }
             hide(a, 2 * half);
             ckx_shares<0, EARLIER>(a, c2, nl, half * 1024, base, added, pk);
+            if (half == 0) {   // the product of the tile before has read the shares
+              ok = warp_wait(&sh_free[g], (m & 1) ^ 1, wc);
+              if (!ok) break;
+            }
             store(pk, 2 * half);
             if (!last) {
               tmem_wait_ld_r(b);
@@ -873,6 +887,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
             if (last) break;
             tmem_wait_ld_r(a);
           }
+          if (!ok) break;
           if (at != nullptr) __stcg(at, total + added);
         } else {
           // several heads of n8 rows: 8 rows at a time, a head's total from its first rows to its last
@@ -888,8 +903,6 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
           int q = 0;   // query of the group's first row
           float v[8];
           tmem_ld8(ts, v);
-          ok = warp_wait(&sh_free[g], (m & 1) ^ 1, wc);
-          if (!ok) break;
           for (int u = 0, h = 0; u < groups; ++u) {
             if (q == 0) {
               c2 = fmaxf(head_c2(p.hs, x.s * p.c.Hq + x.hq0 + h, nullptr), 1e-30f);
@@ -927,6 +940,10 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
                   fmul2(fmul2(make_float2(bid[2 * e], bid[2 * e + 1]), make_float2(dd.y, dd.x)), make_float2(r, r));
               pk[e] = pack_bf16x2(s2.x, s2.y);
             }
+            if (u == 0) {   // the product of the tile before has read the shares
+              ok = warp_wait(&sh_free[g], (m & 1) ^ 1, wc);
+              if (!ok) break;
+            }
             *reinterpret_cast<uint4 *>(sh_row + (u >> 3) * 16384 + (((u & 7) ^ swz) << 4)) =
                 make_uint4(pk[0], pk[1], pk[2], pk[3]);
             q += 8;
@@ -941,6 +958,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
               added = 0.f;
             }
           }
+          if (!ok) break;
         }
         fence_proxy_async_smem();
         __syncwarp();
