@@ -401,7 +401,7 @@ template <int D>
 struct CkxVal {
   static constexpr int kG = D == 64 ? 3 : 2;           // demand warpgroups
   static constexpr int kThreads = (kG + 2) * 128;      // an epilogue and a control warpgroup
-  static constexpr int kRegsDemand = D == 64 ? 128 : 168, kRegsEpi = D == 64 ? 48 : 72, kRegsCtl = D == 64 ? 48 : 72;
+  static constexpr int kRegsDemand = D == 64 ? 128 : 168, kRegsEpi = D == 64 ? 40 : 72, kRegsCtl = D == 64 ? 56 : 72;
   static constexpr int kRegsLaunch = D == 64 ? 96 : 120;
   static constexpr int kRegsNeeded = 128 * (kG * kRegsDemand + kRegsEpi + kRegsCtl);
   static constexpr int kTB = kCkxEdge * D * 2;
@@ -479,10 +479,9 @@ __device__ __forceinline__ void ckx_shares(const float (&x)[32], float c2, const
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float2 dd = fadd2(make_float2(d[2 * i], d[2 * i + 1]), b2);
+    const float2 dd = fadd2(make_float2(d[2 * i + 1], d[2 * i]), b2);   // (swapped: each share takes the other's)
     const float r = rcp_approx(dd.x * dd.y);
-    const float2 sh =
-        fmul2(fmul2(make_float2(p[2 * i], p[2 * i + 1]), make_float2(dd.y, dd.x)), make_float2(r, r));
+    const float2 sh = fmul2(fmul2(make_float2(p[2 * i], p[2 * i + 1]), dd), make_float2(r, r));
     pk[i] = pack_bf16x2(sh.x, sh.y);
   }
 }
@@ -847,45 +846,38 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
           const float c2 = x.c2;
           const float base = total + p.eps;
           float added = 0.f;
-          float a[32], b[32];
-          uint32_t pk[16];
           auto hide = [&](float (&v)[32], int c) {
-            if (mask) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if ((unsigned)(32 * c + e - lo) >= (unsigned)(hi - lo)) v[e] = -INFINITY;
-            }
+            for (int e = 0; e < 32; ++e)
+              if ((unsigned)(32 * c + e - lo) >= (unsigned)(hi - lo)) v[e] = -INFINITY;
           };
-          tmem_ld32(ts, a);
           if (j + kG < x.end) {
             next_at = total_at(next_page, j + kG);
             if (next_at != nullptr) next_total = __ldcg(next_at);
           }
-          tmem_wait_ld_r(a);
+          // 64 rows at a time; not unrolled: the code of all 128 misses the instruction cache
+          const int halves = rows > 64 ? 2 : 1;
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            const bool last = half == 1 || rows <= 64;
+          for (int half = 0; half < halves; ++half) {
+            float a[32], b[32];
+            uint32_t pk[16];
+            tmem_ld32(ts + 64 * half, a);
             tmem_ld32(ts + 64 * half + 32, b);
-            if (last) {   // the next tile's S is formed while the last two chunks are
-              tmem_wait_ld_r(b);
-              ckx_release(&s_free[g], lane);
+            tmem_wait_ld_r(a);
+            tmem_wait_ld_r(b);
+            if (half + 1 == halves) ckx_release(&s_free[g], lane);   // the next tile's S while these rows are formed
+            if (mask) {
+              hide(a, 2 * half);
+              hide(b, 2 * half + 1);
             }
-            hide(a, 2 * half);
             ckx_shares<0, EARLIER>(a, c2, nl, half * 1024, base, added, pk);
             if (half == 0) {   // the product of the tile before has read the shares
               ok = warp_wait(&sh_free[g], (m & 1) ^ 1, wc);
               if (!ok) break;
             }
             store(pk, 2 * half);
-            if (!last) {
-              tmem_wait_ld_r(b);
-              tmem_ld32(ts + 64, a);
-            }
-            hide(b, 2 * half + 1);
             ckx_shares<1, EARLIER>(b, c2, nl, half * 1024, base, added, pk);
             store(pk, 2 * half + 1);
-            if (last) break;
-            tmem_wait_ld_r(a);
           }
           if (!ok) break;
           if (at != nullptr) __stcg(at, total + added);
@@ -934,10 +926,9 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 dd = fadd2(make_float2(d[2 * e], d[2 * e + 1]), b2);
+              const float2 dd = fadd2(make_float2(d[2 * e + 1], d[2 * e]), b2);
               const float r = rcp_approx(dd.x * dd.y);
-              const float2 s2 =
-                  fmul2(fmul2(make_float2(bid[2 * e], bid[2 * e + 1]), make_float2(dd.y, dd.x)), make_float2(r, r));
+              const float2 s2 = fmul2(fmul2(make_float2(bid[2 * e], bid[2 * e + 1]), dd), make_float2(r, r));
               pk[e] = pack_bf16x2(s2.x, s2.y);
             }
             if (u == 0) {   // the product of the tile before has read the shares
