@@ -47,6 +47,11 @@ struct ChunkSeq {
   int len, n, row0, tok0;   // length, new tokens, n8 of the sequences before, first token
 };
 
+// a / b of numbers that are mostly short: a 64-bit division takes several times as long.
+DA_HD long long chunk_div(long long a, long long b) {
+  return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+
 // Equal cut of the line.
 struct ChunkCut {
   long long total, base;
@@ -54,7 +59,7 @@ struct ChunkCut {
   DA_HD long long first(int cta) const { return cta * base + (cta < rem ? cta : rem); }
   DA_HD int cta_of(long long unit) const {
     const long long cut = rem * (base + 1);
-    return (int)(unit < cut ? unit / (base + 1) : rem + (unit - cut) / base);
+    return (int)(unit < cut ? chunk_div(unit, base + 1) : rem + chunk_div(unit - cut, base));
   }
 };
 DA_HD ChunkCut chunk_cut(long long total, int ctas) {
@@ -62,7 +67,7 @@ DA_HD ChunkCut chunk_cut(long long total, int ctas) {
   c.total = total;
   c.ctas = (int)(ctas < total ? ctas : total);
   if (c.ctas < 1) c.ctas = 1;
-  c.base = total / c.ctas;
+  c.base = chunk_div(total, c.ctas);
   c.rem = (int)(total - c.base * c.ctas);
   if (c.base < 1) c.base = 1;   // an empty line
   return c;
@@ -154,7 +159,7 @@ struct ChunkShape {
   DA_HD int first_at(long long u) const {
     if (u <= head) return 0;
     if (u > pos(tiles - 1)) return tiles;
-    const long long t = (u - head + w - 1) / w;   // exact while the tiles are flat
+    const long long t = chunk_div(u - head + w - 1, w);   // exact while the tiles are flat
     if (t <= flat) return (int)t;
     int lo = flat, hi = tiles - 1;
     while (lo < hi) {
@@ -221,7 +226,7 @@ struct ChunkWalk {
     s = chunk_find(l, p.c.S, from, lane);
     load(p, w, l);
     base = __ldcg(l.cum + s);
-    seg = (int)((from - base) / g.units);
+    seg = (int)chunk_div(from - base, g.units);
     base += seg * g.units;
     tile = g.first_at(from - base);
     end = min(g.first_at(to - base), g.tiles);
@@ -265,35 +270,35 @@ __device__ __forceinline__ float *chunk_place(const PagedChunk &p, size_t a, siz
          ((tile == 0 ? row0 : (long long)cta * cta_rows) + r) * stride;
 }
 
-// A row found by its number among all rows of the call: its sequence, query head,
-// query and segment.  false: padding, or past the last row.
-struct ChunkRow {
+// Eight rows (of one query head and one column tile), found by their number among
+// all rows of the call: their sequence, query head, first query and segment.  All
+// lanes of a warp call it alike.  false: behind the last row.
+struct ChunkRows {
   ChunkShape g;
   ChunkSeq q;
-  int s, hq, i;          // sequence, query head, query
-  int r;                 // row of the segment
-  int seen;              // key tiles that its column tile sees
+  int s, hq, i;          // sequence, query head, first query
+  int r;                 // first row of the eight in the segment
+  int seen;              // key tiles that their column tile sees
   long long base, row0;  // the segment's place on the line; its first row
 };
-__device__ __forceinline__ bool chunk_row(const PagedChunk &p, const ChunkPlan &w, const ChunkLine &l, long long row,
-                                          ChunkRow &x) {
-  int lo = 0, hi = p.c.S - 1;   // the last sequence whose first row is at or before this one
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if ((long long)__ldcg(&l.seq[mid].row0) * p.c.Hq <= row)
-      lo = mid;
-    else
-      hi = mid - 1;
+__device__ __forceinline__ bool chunk_rows(const PagedChunk &p, const ChunkPlan &w, const ChunkLine &l, long long row, int lane,
+                                           ChunkRows &x) {
+  int lo = 0, n = p.c.S;   // the last sequence whose first row is at or before this one (see chunk_find)
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const bool le = lane * step < n && (long long)__ldcg(&l.seq[at].row0) * p.c.Hq <= row;
+    const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;
+    lo += k * step;
+    n = min(step, n - k * step);
   }
   x.s = lo;
   x.q = chunk_seq(l, lo);
   if (x.q.n == 0) return false;   // (of the sequences that begin there the last one: behind the last row)
   x.g.set(x.q.len, x.q.n, p.c.Hq, p.c.Hkv, w.edge, w.cost);
   const long long at = row - (long long)x.q.row0 * p.c.Hq;
-  x.hq = (int)(at / x.g.n8);
+  x.hq = (int)chunk_div(at, x.g.n8);
   if (x.hq >= p.c.Hq) return false;
   x.i = (int)(at - (long long)x.hq * x.g.n8);
-  if (x.i >= x.q.n) return false;
   const int seg = x.g.wide ? x.hq : x.hq / w.G;
   x.row0 = (long long)x.q.row0 * p.c.Hq + (long long)seg * (x.g.wide ? 1 : w.G) * x.g.n8;
   x.r = (int)(row - x.row0);
@@ -301,15 +306,18 @@ __device__ __forceinline__ bool chunk_row(const PagedChunk &p, const ChunkPlan &
   x.base = __ldcg(l.cum + lo) + seg * x.g.units;
   return true;
 }
-// Calls f(first tile, CTA) for every piece that a row's column tile takes part in, in order.
-template <typename F>
-__device__ __forceinline__ void chunk_pieces(const ChunkRow &x, const ChunkCut &cut, F &&f) {
-  for (int t = 0; t < x.seen;) {
-    const int cta = cut.cta_of(x.base + x.g.pos(t));
-    f(t, cta);
-    t = x.g.first_at(cut.first(cta + 1) - x.base);
+// The pieces that the rows' column tile takes part in, 32 CTAs at a time: the first
+// key tile of CTA `cta`'s piece, or -1.
+struct ChunkPieces {
+  int first, last;   // CTAs
+  __device__ __forceinline__ ChunkPieces(const ChunkRows &x, const ChunkCut &cut)
+      : first(cut.cta_of(x.base + x.g.pos(0))), last(cut.cta_of(x.base + x.g.pos(x.seen - 1))) {}
+  __device__ __forceinline__ int tile(const ChunkRows &x, const ChunkCut &cut, int cta) const {
+    if (cta > last) return -1;
+    const int t = cta == first ? 0 : x.g.first_at(cut.first(cta) - x.base);
+    return t < x.seen && x.base + x.g.pos(t) < cut.first(cta + 1) ? t : -1;
   }
-}
+};
 #endif  // __CUDACC__
 
 }  // namespace da

@@ -90,63 +90,104 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(PagedChunk p, 
   }
 }
 
-// -lse2 of every row, from (max, sum) of its pieces.
-__global__ void __launch_bounds__(256) chunk_join(PagedChunk p, ChunkPlan w) {
+constexpr int kRowWarps = 8;   // of a block: eight rows each
+
+// -lse2 of every row, from (max, sum) of its pieces: a lane takes a row's every
+// fourth piece.
+__global__ void __launch_bounds__(32 * kRowWarps) chunk_join(PagedChunk p, ChunkPlan w) {
   pdl_wait();
   pdl_launch_dependents();
+  const int lane = threadIdx.x % 32, r = lane % 8, part = lane / 8;
   const ChunkLine l = chunk_line(p, w);
   const long long rows = (long long)__ldcg(&l.seq[p.c.S].row0) * p.c.Hq;
   const ChunkCut cut = chunk_cut(__ldcg(l.cum + p.c.S), w.ctas_keys);
   float *nl = reinterpret_cast<float *>(p.ws + w.nl);
-  for (long long row = (long long)blockIdx.x * 256 + threadIdx.x; row < rows; row += (long long)gridDim.x * 256) {
-    ChunkRow x;
-    if (!chunk_row(p, w, l, row, x)) continue;
+  for (long long row = 8ll * (blockIdx.x * kRowWarps + threadIdx.x / 32); row < rows; row += 8ll * gridDim.x * kRowWarps) {
+    ChunkRows x;
+    if (!chunk_rows(p, w, l, row, lane, x)) continue;
+    const bool valid = x.i + r < x.q.n;
+    const ChunkPieces pc(x, cut);
     float m = -INFINITY, sum = 0.f;
-    chunk_pieces(x, cut, [&](int tile, int cta) {
-      const float2 ml = __ldcg(
-          reinterpret_cast<const float2 *>(chunk_place(p, w.ml_a, w.ml_b, x.row0, w.cta_rows, tile, cta, x.r, 2)));
-      const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
-      sum = sum * ex2_approx(m - ms) + ml.y * ex2_approx(ml.x - ms);
+    for (int c = pc.first; c <= pc.last; c += 32) {
+      const int tile = pc.tile(x, cut, c + lane);
+      const unsigned have = __ballot_sync(0xffffffffu, tile >= 0);
+      for (int k = 0; k < __popc(have); k += 4) {
+        const int from = k + part < __popc(have) ? __fns(have, 0, k + part + 1) : 0;
+        const int t = __shfl_sync(0xffffffffu, tile, from);
+        if (k + part < __popc(have) && valid) {
+          const float2 ml = __ldcg(reinterpret_cast<const float2 *>(
+              chunk_place(p, w.ml_a, w.ml_b, x.row0, w.cta_rows, t, c + from, x.r + r, 2)));
+          const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
+          sum = sum * ex2_approx(m - ms) + ml.y * ex2_approx(ml.x - ms);
+          m = mn;
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, sum, o);
+      const float mn = fmaxf(m, m2), ms = mn == -INFINITY ? 0.f : mn;
+      sum = sum * ex2_approx(m - ms) + s2 * ex2_approx(m2 - ms);
       m = mn;
-    });
-    nl[row] = -(m + log2f(sum));
+    }
+    if (part == 0 && valid) nl[row + r] = -(m + log2f(sum));
   }
 }
 
 // out = numerators / shares, summed over the pieces in the line's order.
 template <int D, typename E>
-__global__ void __launch_bounds__(256) chunk_combine(PagedChunk p, ChunkPlan w) {
-  constexpr int LANES = D / 4;   // of a row
+__global__ void __launch_bounds__(32 * kRowWarps) chunk_combine(PagedChunk p, ChunkPlan w) {
+  constexpr int COLS = D / 4, PER = 8 * COLS / 32;   // float4 columns of a row; of a lane
   pdl_wait();
   pdl_launch_dependents();
+  const int lane = threadIdx.x % 32;
   const ChunkLine l = chunk_line(p, w);
   const long long rows = (long long)__ldcg(&l.seq[p.c.S].row0) * p.c.Hq;
   const ChunkCut cut = chunk_cut(__ldcg(l.cum + p.c.S), w.ctas_values);
-  const int c = threadIdx.x % LANES;
-  for (long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LANES; row < rows;
-       row += (long long)gridDim.x * 256 / LANES) {
-    ChunkRow x;
-    if (!chunk_row(p, w, l, row, x)) continue;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    chunk_pieces(x, cut, [&](int tile, int cta) {
-      const float *at = chunk_place(p, w.acc_a, w.acc_b, x.row0, w.cta_rows, tile, cta, x.r, acc_stride(D));
-      const float4 v = __ldcg(reinterpret_cast<const float4 *>(at) + c);
-      a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-      sum += __ldcg(at + D);
-    });
-    const size_t to = ((size_t)(x.q.tok0 + x.i) * p.c.Hq + x.hq) * D + 4 * c;
-    a.x /= sum, a.y /= sum, a.z /= sum, a.w /= sum;
-    if constexpr (sizeof(E) == 4)
-      *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + to) = a;
-    else
-      *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + to) =
-          make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  for (long long row = 8ll * (blockIdx.x * kRowWarps + threadIdx.x / 32); row < rows; row += 8ll * gridDim.x * kRowWarps) {
+    ChunkRows x;
+    if (!chunk_rows(p, w, l, row, lane, x)) continue;
+    const int left = x.q.n - x.i;   // valid rows
+    const ChunkPieces pc(x, cut);
+    float4 a[PER];
+    float sum = 0.f;                // of row `lane`
+#pragma unroll
+    for (int e = 0; e < PER; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = pc.first; c <= pc.last; c += 32) {
+      const int tile = pc.tile(x, cut, c + lane);
+      for (unsigned have = __ballot_sync(0xffffffffu, tile >= 0); have; have &= have - 1) {
+        const int from = __ffs(have) - 1, t = __shfl_sync(0xffffffffu, tile, from);
+        const float *at = chunk_place(p, w.acc_a, w.acc_b, x.row0, w.cta_rows, t, c + from, x.r, acc_stride(D));
+        float4 v[PER];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+          const int q = lane + 32 * e, r = q / COLS;
+          v[e] = r < left ? __ldcg(reinterpret_cast<const float4 *>(at + r * acc_stride(D)) + q % COLS)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (lane < min(left, 8)) sum += __ldcg(at + lane * acc_stride(D) + D);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) a[e].x += v[e].x, a[e].y += v[e].y, a[e].z += v[e].z, a[e].w += v[e].w;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < PER; ++e) {
+      const int q = lane + 32 * e, r = q / COLS;
+      const float d = __shfl_sync(0xffffffffu, sum, r);
+      if (r >= left) continue;
+      const size_t to = ((size_t)(x.q.tok0 + x.i + r) * p.c.Hq + x.hq) * D + 4 * (q % COLS);
+      if constexpr (sizeof(E) == 4)
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + to) =
+            make_float4(a[e].x / d, a[e].y / d, a[e].z / d, a[e].w / d);
+      else
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + to) =
+            make_uint2(pack_bf16x2(a[e].x / d, a[e].y / d), pack_bf16x2(a[e].z / d, a[e].w / d));
+    }
   }
 }
 
-static int row_blocks(long long rows, int per_block) {
-  const long long n = (rows + per_block - 1) / per_block, most = 152 * 8;
+static int row_blocks(long long rows) {
+  const long long n = (rows + 8 * kRowWarps - 1) / (8 * kRowWarps), most = 152 * 8;
   return (int)(n < 1 ? 1 : n < most ? n : most);
 }
 
@@ -154,15 +195,15 @@ cudaError_t launch_chunk_plan(const PagedChunk &p, const ChunkPlan &w, cudaStrea
   return launch_after(chunk_plan_kernel, 1, kPlanThreads, 0, stream, p, w);
 }
 cudaError_t launch_chunk_join(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream) {
-  return launch_after(chunk_join, row_blocks(w.rows, 256), 256, 0, stream, p, w);
+  return launch_after(chunk_join, row_blocks(w.rows), 32 * kRowWarps, 0, stream, p, w);
+}
+template <typename E>
+static cudaError_t launch_combine_t(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream) {
+  return p.c.d == 128 ? launch_after(chunk_combine<128, E>, row_blocks(w.rows), 32 * kRowWarps, 0, stream, p, w)
+                      : launch_after(chunk_combine<64, E>, row_blocks(w.rows), 32 * kRowWarps, 0, stream, p, w);
 }
 cudaError_t launch_chunk_combine(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream) {
-  const int blocks = row_blocks(w.rows, 256 / (p.c.d / 4));
-  if (p.c.dtype == DA_F32)
-    return p.c.d == 128 ? launch_after(chunk_combine<128, float>, blocks, 256, 0, stream, p, w)
-                        : launch_after(chunk_combine<64, float>, blocks, 256, 0, stream, p, w);
-  return p.c.d == 128 ? launch_after(chunk_combine<128, __nv_bfloat16>, blocks, 256, 0, stream, p, w)
-                      : launch_after(chunk_combine<64, __nv_bfloat16>, blocks, 256, 0, stream, p, w);
+  return p.c.dtype == DA_F32 ? launch_combine_t<float>(p, w, stream) : launch_combine_t<__nv_bfloat16>(p, w, stream);
 }
 
 // The plans of the types: edge, CTAs of the passes, costs (see the kernels).
