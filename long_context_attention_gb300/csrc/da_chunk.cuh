@@ -309,9 +309,11 @@ __device__ __forceinline__ bool chunk_rows(const PagedChunk &p, const ChunkPlan 
 // The pieces that the rows' column tile takes part in, 32 CTAs at a time: the first
 // key tile of CTA `cta`'s piece, or -1.
 struct ChunkPieces {
-  int first, last;   // CTAs
-  __device__ __forceinline__ ChunkPieces(const ChunkRows &x, const ChunkCut &cut)
-      : first(cut.cta_of(x.base + x.g.pos(0))), last(cut.cta_of(x.base + x.g.pos(x.seen - 1))) {}
+  int first = 0, last = -1;   // CTAs
+  __device__ __forceinline__ void find(const ChunkRows &x, const ChunkCut &cut) {
+    first = cut.cta_of(x.base + x.g.pos(0));
+    last = cut.cta_of(x.base + x.g.pos(x.seen - 1));
+  }
   __device__ __forceinline__ int tile(const ChunkRows &x, const ChunkCut &cut, int cta) const {
     if (cta > last) return -1;
     const int t = cta == first ? 0 : x.g.first_at(cut.first(cta) - x.base);

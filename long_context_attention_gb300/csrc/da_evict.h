@@ -19,7 +19,7 @@ struct EvictArgs {
 
 // Keys of a sequence in a cluster's shared memory; scores of more lie in the workspace.
 constexpr int kEvictCtas = 8;
-constexpr int kEvictKeys = 48 * 1024;   // a CTA's
+constexpr int kEvictKeys = 40 * 1024;   // a CTA's
 
 struct EvictWorkspace {
   size_t info_off, list_off, key_off, total;

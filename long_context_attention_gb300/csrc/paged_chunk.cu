@@ -90,11 +90,32 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(PagedChunk p, 
   }
 }
 
-constexpr int kRowWarps = 8;   // of a block: eight rows each
+constexpr int kRowWarps = 8;   // of a block
+
+// A warp's rows: `run` times eight in succession, found once for each column tile.
+template <typename F>
+__device__ __forceinline__ void row_groups(const PagedChunk &p, const ChunkPlan &w, const ChunkLine &l, long long rows, int run,
+                                           int lane, F &&f) {
+  for (long long r0 = 8ll * run * (blockIdx.x * kRowWarps + threadIdx.x / 32); r0 < rows;
+       r0 += 8ll * run * gridDim.x * kRowWarps) {
+    ChunkRows x;
+    bool known = false, fresh = false;
+    for (long long row = r0; row < r0 + 8 * run && row < rows; row += 8) {
+      if (known && x.i + 8 < x.g.n8 && (x.r + 8) / x.g.step == x.r / x.g.step) {
+        x.i += 8;
+        x.r += 8;
+        fresh = false;
+      } else {
+        known = fresh = chunk_rows(p, w, l, row, lane, x);
+      }
+      if (known) f(x, row, fresh);
+    }
+  }
+}
 
 // -lse2 of every row, from (max, sum) of its pieces: a lane takes a row's every
 // fourth piece.
-__global__ void __launch_bounds__(32 * kRowWarps) chunk_join(PagedChunk p, ChunkPlan w) {
+__global__ void __launch_bounds__(32 * kRowWarps) chunk_join(PagedChunk p, ChunkPlan w, int run) {
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x % 32, r = lane % 8, part = lane / 8;
@@ -102,14 +123,17 @@ __global__ void __launch_bounds__(32 * kRowWarps) chunk_join(PagedChunk p, Chunk
   const long long rows = (long long)__ldcg(&l.seq[p.c.S].row0) * p.c.Hq;
   const ChunkCut cut = chunk_cut(__ldcg(l.cum + p.c.S), w.ctas_keys);
   float *nl = reinterpret_cast<float *>(p.ws + w.nl);
-  for (long long row = 8ll * (blockIdx.x * kRowWarps + threadIdx.x / 32); row < rows; row += 8ll * gridDim.x * kRowWarps) {
-    ChunkRows x;
-    if (!chunk_rows(p, w, l, row, lane, x)) continue;
+  ChunkPieces pc;
+  int tile0 = -1;   // of the first 32 CTAs
+  row_groups(p, w, l, rows, run, lane, [&](const ChunkRows &x, long long row, bool fresh) {
+    if (fresh) {
+      pc.find(x, cut);
+      tile0 = pc.tile(x, cut, pc.first + lane);
+    }
     const bool valid = x.i + r < x.q.n;
-    const ChunkPieces pc(x, cut);
     float m = -INFINITY, sum = 0.f;
     for (int c = pc.first; c <= pc.last; c += 32) {
-      const int tile = pc.tile(x, cut, c + lane);
+      const int tile = c == pc.first ? tile0 : pc.tile(x, cut, c + lane);
       const unsigned have = __ballot_sync(0xffffffffu, tile >= 0);
       for (int k = 0; k < __popc(have); k += 4) {
         const int from = k + part < __popc(have) ? __fns(have, 0, k + part + 1) : 0;
@@ -131,12 +155,12 @@ __global__ void __launch_bounds__(32 * kRowWarps) chunk_join(PagedChunk p, Chunk
       m = mn;
     }
     if (part == 0 && valid) nl[row + r] = -(m + log2f(sum));
-  }
+  });
 }
 
 // out = numerators / shares, summed over the pieces in the line's order.
 template <int D, typename E>
-__global__ void __launch_bounds__(32 * kRowWarps) chunk_combine(PagedChunk p, ChunkPlan w) {
+__global__ void __launch_bounds__(32 * kRowWarps) chunk_combine(PagedChunk p, ChunkPlan w, int run) {
   constexpr int COLS = D / 4, PER = 8 * COLS / 32;   // float4 columns of a row; of a lane
   pdl_wait();
   pdl_launch_dependents();
@@ -144,17 +168,20 @@ __global__ void __launch_bounds__(32 * kRowWarps) chunk_combine(PagedChunk p, Ch
   const ChunkLine l = chunk_line(p, w);
   const long long rows = (long long)__ldcg(&l.seq[p.c.S].row0) * p.c.Hq;
   const ChunkCut cut = chunk_cut(__ldcg(l.cum + p.c.S), w.ctas_values);
-  for (long long row = 8ll * (blockIdx.x * kRowWarps + threadIdx.x / 32); row < rows; row += 8ll * gridDim.x * kRowWarps) {
-    ChunkRows x;
-    if (!chunk_rows(p, w, l, row, lane, x)) continue;
+  ChunkPieces pc;
+  int tile0 = -1;   // of the first 32 CTAs
+  row_groups(p, w, l, rows, run, lane, [&](const ChunkRows &x, long long, bool fresh) {
+    if (fresh) {
+      pc.find(x, cut);
+      tile0 = pc.tile(x, cut, pc.first + lane);
+    }
     const int left = x.q.n - x.i;   // valid rows
-    const ChunkPieces pc(x, cut);
     float4 a[PER];
     float sum = 0.f;                // of row `lane`
 #pragma unroll
     for (int e = 0; e < PER; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c = pc.first; c <= pc.last; c += 32) {
-      const int tile = pc.tile(x, cut, c + lane);
+      const int tile = c == pc.first ? tile0 : pc.tile(x, cut, c + lane);
       for (unsigned have = __ballot_sync(0xffffffffu, tile >= 0); have; have &= have - 1) {
         const int from = __ffs(have) - 1, t = __shfl_sync(0xffffffffu, tile, from);
         const float *at = chunk_place(p, w.acc_a, w.acc_b, x.row0, w.cta_rows, t, c + from, x.r, acc_stride(D));
@@ -183,11 +210,16 @@ __global__ void __launch_bounds__(32 * kRowWarps) chunk_combine(PagedChunk p, Ch
         *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + to) =
             make_uint2(pack_bf16x2(a[e].x / d, a[e].y / d), pack_bf16x2(a[e].z / d, a[e].w / d));
     }
-  }
+  });
 }
 
+// Eight rows a warp where there are few, up to 64 where the GPU is full.
+static int row_run(long long rows) {
+  const long long run = rows / (8ll * 152 * 32);
+  return (int)(run < 1 ? 1 : run > 8 ? 8 : run);
+}
 static int row_blocks(long long rows) {
-  const long long n = (rows + 8 * kRowWarps - 1) / (8 * kRowWarps), most = 152 * 8;
+  const long long each = 8ll * kRowWarps * row_run(rows), n = (rows + each - 1) / each, most = 152 * 8;
   return (int)(n < 1 ? 1 : n < most ? n : most);
 }
 
@@ -195,12 +227,12 @@ cudaError_t launch_chunk_plan(const PagedChunk &p, const ChunkPlan &w, cudaStrea
   return launch_after(chunk_plan_kernel, 1, kPlanThreads, 0, stream, p, w);
 }
 cudaError_t launch_chunk_join(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream) {
-  return launch_after(chunk_join, row_blocks(w.rows), 32 * kRowWarps, 0, stream, p, w);
+  return launch_after(chunk_join, row_blocks(w.rows), 32 * kRowWarps, 0, stream, p, w, row_run(w.rows));
 }
 template <typename E>
 static cudaError_t launch_combine_t(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream) {
-  return p.c.d == 128 ? launch_after(chunk_combine<128, E>, row_blocks(w.rows), 32 * kRowWarps, 0, stream, p, w)
-                      : launch_after(chunk_combine<64, E>, row_blocks(w.rows), 32 * kRowWarps, 0, stream, p, w);
+  return p.c.d == 128 ? launch_after(chunk_combine<128, E>, row_blocks(w.rows), 32 * kRowWarps, 0, stream, p, w, row_run(w.rows))
+                      : launch_after(chunk_combine<64, E>, row_blocks(w.rows), 32 * kRowWarps, 0, stream, p, w, row_run(w.rows));
 }
 cudaError_t launch_chunk_combine(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream) {
   return p.c.dtype == DA_F32 ? launch_combine_t<float>(p, w, stream) : launch_combine_t<__nv_bfloat16>(p, w, stream);

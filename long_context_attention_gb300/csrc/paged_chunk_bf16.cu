@@ -406,12 +406,12 @@ struct CkxVal {
   static constexpr int kRegsNeeded = 128 * (kG * kRegsDemand + kRegsEpi + kRegsCtl);
   static constexpr int kTB = kCkxEdge * D * 2;
   static constexpr int kStages = D == 64 ? 3 : 2;      // of K, and of V
-  // Barriers of what has landed: two rounds of stages, since those that wait for a
-  // tile need not have seen the one before it in its stage land, and a barrier's
-  // parity tells a round from the next alone.  (That before it in its barrier has been
-  // read: its stage was filled again since, before the column tile's queries came.)
-  static constexpr int kFull = 2 * kStages;
-  static constexpr int kLag = kG - 1;                  // V behind K
+  static constexpr int kLag = kG;                      // V behind K, in tiles
+  // Barriers of what has landed: three rounds of stages, since those that wait for a
+  // tile need not have seen the ones before it in its stage land, and a barrier's
+  // parity tells a round from the next alone.  (The tile before it in its barrier has
+  // been read: its stage was filled again since, before K of this one came.)
+  static constexpr int kFull = 3 * kStages;
   static constexpr uint32_t kShBytes = 32 * 1024;      // a warpgroup's shares: 2 x 64 rows x 128 keys
   static constexpr int kQs = D == 64 ? 2 : 1;          // of Q
   static constexpr uint32_t kOffQ = 0;
@@ -421,7 +421,7 @@ struct CkxVal {
   static constexpr uint32_t kOffOnes = kOffSh + kG * kShBytes;   // above every V tile (positive offset)
   static constexpr uint32_t kOffRing = kOffOnes + 2048;
   static constexpr uint32_t kOffBar = kOffRing + kCkxRing * sizeof(CkxTile);
-  static constexpr int kSmemBytes = kOffBar + 448;     // (the base is 1024-byte aligned)
+  static constexpr int kSmemBytes = kOffBar + 512;     // (the base is 1024-byte aligned)
   // TMEM: S^T of warpgroup g at 128 g; D (80 columns: values 0-63, share sum at 64);
   // at d = 128 values 64-127 behind it.
   static constexpr uint32_t kTmemD = kG * 128, kTmemDHi = kTmemD + 80;
@@ -557,9 +557,9 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
     ckx_regs_dec<C::kRegsCtl>();
     if (warp == kWarpCtl) {
       // -------------------------------------------------------------- producer
-      // V follows K kLag tiles behind: a place for V is free a warpgroup's whole item later
-      // than one for K, and K is needed an item earlier.  (kLag = 1 at d = 64: the demand
-      // warps waited 2085 cycles an item for S, 2048 queries at 131072.)
+      // V follows K kLag tiles behind: a place for V is free a warpgroup's whole tile later
+      // than one for K, and K is needed a tile earlier.  (One tile behind at d = 64: the
+      // demand warps waited 2085 cycles a tile for S, 2048 queries at 131072.)
       const ChunkLine l = chunk_line(p, w);
       const ChunkCut cut = chunk_cut(__ldcg(l.cum + p.c.S), w.ctas_values);
       const int sh = w.page_shift;
@@ -569,6 +569,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       int v_len[C::kLag] = {}, v_tile[C::kLag] = {}, v_hkv[C::kLag] = {}, v_page[C::kLag] = {};   // V still to be brought
       int v_due = 0;
       bool part = false;   // the column tile before held a sequence's last keys, not a whole tile of them
+      int before = 0;      // its first key tile's number
       auto bring_v = [&]() {
         const int st = nv % C::kStages;
         if (!warp_wait(&v_empty[st], ((nv / C::kStages) & 1) ^ 1, wc)) return false;
@@ -594,10 +595,12 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
         }
         int page = ckx_page(p, sh, x.s, x.len, x.tile, lane);
         const float4 nl = it.nl(p, w, x, lane);
-        // (its demand warps wait for V, and what follows here waits for them)
-        while (part && ok && v_due > 0) ok = bring_v();
+        // What follows waits for the demand warps of column tile i - 2, and those for the
+        // products of what came before; of a sequence's last, partial tile for V itself.
+        while (ok && v_due > 0 && (part || nv < before)) ok = bring_v();
         if (!ok) break;
         part = x.end * kCkxEdge > x.len;
+        before = x.t0;
         const int qs = i % C::kQs;
         // every role is done with column tile i - 2, whose -lse2 this one's replace
         ok = (i < 2 || warp_wait(&r_free[(i - 2) % kCkxRing], ((i - 2) / kCkxRing) & 1, wc)) &&

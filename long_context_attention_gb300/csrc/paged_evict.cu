@@ -26,6 +26,7 @@ namespace da {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kCopies = 4;   // of the counts: neighbouring lanes' scores fall into few bins
 
 EvictWorkspace evict_workspace(int S, int Hkv, int max_keep, int max_len) {
   EvictWorkspace w;
@@ -69,7 +70,7 @@ __device__ __forceinline__ uint32_t ev_key(float f) {
 
 __global__ void __launch_bounds__(kSelThreads) evict_select(EvictArgs a, EvictWorkspace w, int page_shift) {
   extern __shared__ uint32_t sel_keys[];
-  __shared__ uint32_t s_hist[2][kBins];
+  __shared__ uint32_t s_hist[kCopies + 1][kBins];   // the first pass's (the third's in its first copy); the second's
   __shared__ uint32_t s_above[kSelWarps], s_equal[kSelWarps], s_count[2], s_pick[2];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const uint32_t rank = ev_rank(), C = (uint32_t)w.cluster;
@@ -97,38 +98,50 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(EvictArgs a, EvictWo
                             : reinterpret_cast<uint32_t *>(a.ws + w.key_off) + ((size_t)item * w.cluster + rank) * w.slice;
   const int32_t *dtab = a.c.demand_table + (size_t)s * a.c.max_pages;
   const int ps = 1 << page_shift;
-  for (int i = tid; i < 2 * kBins; i += kSelThreads) s_hist[0][i] = 0;
+  for (int i = tid; i < (kCopies + 1) * kBins; i += kSelThreads) s_hist[0][i] = 0;
   __syncthreads();
-#pragma unroll 4
-  for (int i = tid; i < cnt; i += kSelThreads) {
+  // four tokens a thread: they lie in one page
+#pragma unroll 2
+  for (int i = 4 * tid; i < cnt; i += 4 * kSelThreads) {
     const int t = t0 + i, page = __ldcg(dtab + (t >> page_shift));
-    float f = INFINITY;
-    if (t >= a.sinks && t < len - a.recent) {
-      if ((unsigned)page < (unsigned)a.c.num_demand_pages) {
-        const float *at = a.c.demand_pages + ((((size_t)page * a.c.Hq + (size_t)h * G) << page_shift) + (t & (ps - 1)));
-        f = __ldcg(at);
-        for (int g = 1; g < G; ++g) f = __fadd_rn(f, __ldcg(at + ((size_t)g << page_shift)));
-      } else {
-        atomicCAS(a.status, DA_OK, DA_ERR_INVALID);
-        f = 0.f;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if ((unsigned)page < (unsigned)a.c.num_demand_pages) {
+      const float *at = a.c.demand_pages + ((((size_t)page * a.c.Hq + (size_t)h * G) << page_shift) + (t & (ps - 1)));
+      f = __ldcg(reinterpret_cast<const float4 *>(at));
+#pragma unroll 2
+      for (int g = 1; g < G; ++g) {
+        const float4 o = __ldcg(reinterpret_cast<const float4 *>(at + ((size_t)g << page_shift)));
+        f.x = __fadd_rn(f.x, o.x), f.y = __fadd_rn(f.y, o.y), f.z = __fadd_rn(f.z, o.z), f.w = __fadd_rn(f.w, o.w);
       }
+    } else {
+      atomicCAS(a.status, DA_OK, DA_ERR_INVALID);
     }
-    const uint32_t key = ev_key(f);
-    keys[i] = key;
-    atomicAdd(&s_hist[0][key >> 21], 1u);
+    const float v[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (i + e >= cnt) break;
+      const uint32_t key = ev_key(t + e < a.sinks || t + e >= len - a.recent ? INFINITY : v[e]);
+      keys[i + e] = key;
+      atomicAdd(&s_hist[lane % kCopies][key >> 21], 1u);
+    }
   }
+  __syncthreads();
   // three counts: the digits of the m-th highest key, and how many keys equal to it stay
   uint32_t prefix = 0, need = (uint32_t)m;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-    uint32_t *hist = s_hist[pass & 1];
+    uint32_t *hist = s_hist[pass == 1 ? kCopies : 0];
     if (pass > 0) {
       const int above = pass == 1 ? 21 : 10;
       for (int i = tid; i < cnt; i += kSelThreads) {
         const uint32_t key = keys[i];
         if (key >> above == prefix) atomicAdd(&hist[(key >> shift) & (uint32_t)(bins - 1)], 1u);
       }
+    } else {
+      for (int i = tid; i < kBins; i += kSelThreads)
+#pragma unroll
+        for (int k = 1; k < kCopies; ++k) hist[i] += hist[k * kBins + i];
     }
     if (C > 1)
       ev_sync();
@@ -241,17 +254,33 @@ __device__ __forceinline__ uint4 ev_load<uint4>(const uint8_t *p) { return __ldc
 template <>
 __device__ __forceinline__ float ev_load<float>(const uint8_t *p) { return __ldcg(reinterpret_cast<const float *>(p)); }
 
+// Rows from .. to - 1 of the list, a batch of kMoveLoads steps at a time.  The places
+// of a batch are found while the one before it is on its way: one read after the
+// other (list, tables, rows) took 4.5 us a batch.
 template <typename V>
 __device__ __forceinline__ void move_rows(const EvictArgs &a, const MoveRows &x, const int32_t *list, int from, int to, int lane_row,
                                           int lane_byte, int rows_per_step, int sh, int *status) {
   const int ps = 1 << sh;
-  int t[kMoveLoads];
+  int t[kMoveLoads], ip[kMoveLoads], op[kMoveLoads];
+  auto entries = [&](int r0) {   // of the list
 #pragma unroll
-  for (int u = 0; u < kMoveLoads; ++u) {
-    const int r = from + lane_row + u * rows_per_step;
-    t[u] = r < to ? __ldcg(list + r) : -1;
-  }
-  for (int r0 = from; r0 < to; r0 += kMoveLoads * rows_per_step) {
+    for (int u = 0; u < kMoveLoads; ++u) {
+      const int r = r0 + lane_row + u * rows_per_step;
+      t[u] = r < to ? __ldcg(list + r) : -1;
+    }
+  };
+  auto pages = [&](int r0) {
+#pragma unroll
+    for (int u = 0; u < kMoveLoads; ++u) {
+      const int r = r0 + lane_row + u * rows_per_step;
+      ip[u] = t[u] >= 0 ? __ldg(x.src + (t[u] >> sh)) : 0;
+      op[u] = t[u] >= 0 ? __ldg(x.dst + (r >> sh)) : 0;
+    }
+  };
+  const int batch = kMoveLoads * rows_per_step;
+  entries(from);
+  pages(from);
+  for (int r0 = from; r0 < to; r0 += batch) {
     V v[kMoveLoads];
     uint8_t *at[kMoveLoads];
 #pragma unroll
@@ -259,10 +288,9 @@ __device__ __forceinline__ void move_rows(const EvictArgs &a, const MoveRows &x,
       const int r = r0 + lane_row + u * rows_per_step;
       at[u] = nullptr;
       if (t[u] >= 0) {
-        const int ip = __ldg(x.src + (t[u] >> sh)), op = __ldg(x.dst + (r >> sh));
-        if ((unsigned)ip < (unsigned)x.num_pages && (unsigned)op < (unsigned)x.num_pages) {
-          const uint8_t *p = x.in + (size_t)ip * x.page_bytes + (size_t)(t[u] & (ps - 1)) * x.row_bytes + lane_byte;
-          uint8_t *q = x.out + (size_t)op * x.page_bytes + (size_t)(r & (ps - 1)) * x.row_bytes + lane_byte;
+        if ((unsigned)ip[u] < (unsigned)x.num_pages && (unsigned)op[u] < (unsigned)x.num_pages) {
+          const uint8_t *p = x.in + (size_t)ip[u] * x.page_bytes + (size_t)((t[u] & (ps - 1)) * x.row_bytes + lane_byte);
+          uint8_t *q = x.out + (size_t)op[u] * x.page_bytes + (size_t)((r & (ps - 1)) * x.row_bytes + lane_byte);
           if (p != q) {
             at[u] = q;
             v[u] = ev_load<V>(p);
@@ -272,11 +300,8 @@ __device__ __forceinline__ void move_rows(const EvictArgs &a, const MoveRows &x,
         }
       }
     }
-#pragma unroll
-    for (int u = 0; u < kMoveLoads; ++u) {
-      const int r = r0 + (kMoveLoads + u) * rows_per_step + lane_row;
-      t[u] = r < to ? __ldcg(list + r) : -1;
-    }
+    entries(r0 + batch);
+    pages(r0 + batch);
     __syncthreads();   // the batch has been read
 #pragma unroll
     for (int u = 0; u < kMoveLoads; ++u)
