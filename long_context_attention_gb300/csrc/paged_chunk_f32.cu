@@ -71,35 +71,38 @@ __device__ __forceinline__ void ckf_queries(const PagedChunk &p, const ChunkWalk
   }
 }
 
-// Asynchronous copies of key tile `tile` of K or V: one group.  Zeros past the
-// sequence's end and where there is no page (recorded).  A thread's rows lie
-// kCkfThreads / (d / 4) apart.
+// The rows of a key tile that a thread copies, kCkfThreads / (d / 4) apart: their pages
+// (-1 past the sequence's end), and asynchronous copies of K or V from them: one group.
+// Zeros past the end and where there is no page (recorded).
 template <int D>
-__device__ __forceinline__ void ckf_rows(const PagedChunk &p, const ChunkPlan &w, const ChunkWalk &k, const void *pages,
-                                         int tile, float *to) {
-  constexpr int STEP = kCkfThreads / (D / 4), ROWS = kCkfEdge / STEP;
-  const int sh = w.page_shift, ps = 1 << sh, hkv = k.hkv(w);
-  const int j0 = threadIdx.x / (D / 4), x = threadIdx.x % (D / 4);
-  const int32_t *table = p.c.page_table + (size_t)k.s * p.c.max_pages;
+struct CkfPages {
+  static constexpr int STEP = kCkfThreads / (D / 4), ROWS = kCkfEdge / STEP;
   int page[ROWS];
+  __device__ __forceinline__ void find(const PagedChunk &p, const ChunkPlan &w, const ChunkWalk &k, int tile) {
+    const int32_t *table = p.c.page_table + (size_t)k.s * p.c.max_pages;
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int key = tile * kCkfEdge + j0 + i * STEP;
-    page[i] = key < k.g.len ? __ldcg(table + (key >> sh)) : -1;
+    for (int i = 0; i < ROWS; ++i) {
+      const int key = tile * kCkfEdge + threadIdx.x / (D / 4) + i * STEP;
+      page[i] = key < k.g.len ? __ldcg(table + (key >> w.page_shift)) : -1;
+    }
   }
+  __device__ __forceinline__ void copy(const PagedChunk &p, const ChunkPlan &w, const ChunkWalk &k, const void *pages, int tile,
+                                       float *to) const {
+    const int sh = w.page_shift, ps = 1 << sh, hkv = k.hkv(w), x = threadIdx.x % (D / 4);
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int j = j0 + i * STEP, key = tile * kCkfEdge + j;
-    const bool ok = (unsigned)page[i] < (unsigned)p.c.num_pages;
-    if (!ok && key < k.g.len) atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
-    const float *from = static_cast<const float *>(pages);
-    if (ok) from += ((((size_t)page[i] * p.c.Hkv + hkv) << sh) + (key & (ps - 1))) * D + 4 * x;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to + j * Ckf<D>::kLd + 4 * x)),
-                 "l"(reinterpret_cast<uint64_t>(from)), "r"(ok ? 16 : 0)
-                 : "memory");
+    for (int i = 0; i < ROWS; ++i) {
+      const int j = threadIdx.x / (D / 4) + i * STEP, key = tile * kCkfEdge + j;
+      const bool ok = (unsigned)page[i] < (unsigned)p.c.num_pages;
+      if (!ok && key < k.g.len) atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
+      const float *from = static_cast<const float *>(pages);
+      if (ok) from += ((((size_t)page[i] * p.c.Hkv + hkv) << sh) + (key & (ps - 1))) * D + 4 * x;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to + j * Ckf<D>::kLd + 4 * x)),
+                   "l"(reinterpret_cast<uint64_t>(from)), "r"(ok ? 16 : 0)
+                   : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
+};
 template <int N>
 __device__ __forceinline__ void ckf_landed() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
@@ -115,25 +118,40 @@ __device__ __forceinline__ float *ckf_total(const PagedChunk &p, const ChunkPlan
   return p.c.demand_pages + ((((size_t)page * p.c.Hq + hq) << sh) + (key & ((1 << sh) - 1)));
 }
 
-// Rows 4 ty .. by keys tx + 16 j: q . k.
-template <int D>
-__device__ __forceinline__ void ckf_products(const float *sQ, const float *sK, float (&x)[4][4]) {
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  float2 acc[4][4];
+// A thread's part of a tile.  Many rows: 4 rows (4 ty ..) by 4 keys (tx + 16 j).  Up to
+// 16 rows: 4 rows (4 (ty % 4) ..) by one key (16 (ty / 4) + tx), so that all warps work
+// (as many rows: 64 keys by 8 rows in one warp, 223 us for 4 sequences of 1001 .. 8001).
+template <bool FEW>
+struct CkfPart {
+  static constexpr int kKeys = FEW ? 1 : 4;
+  int row, key;   // its first row and key
+  __device__ __forceinline__ CkfPart() {
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    row = FEW ? 4 * (ty % 4) : 4 * ty;
+    key = FEW ? 16 * (ty / 4) + tx : tx;
+  }
+};
+
+// q . k of the thread's part.
+template <int D, bool FEW>
+__device__ __forceinline__ void ckf_products(const float *sQ, const float *sK, float (&x)[4][CkfPart<FEW>::kKeys]) {
+  constexpr int NK = CkfPart<FEW>::kKeys;
+  const CkfPart<FEW> t;
+  float2 acc[4][NK];
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[r][j] = make_float2(0.f, 0.f);
+    for (int j = 0; j < NK; ++j) acc[r][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
   for (int e = 0; e < D; e += 4) {
-    float4 kv[4];
+    float4 kv[NK];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * j) * Ckf<D>::kLd + e);
+    for (int j = 0; j < NK; ++j) kv[j] = *reinterpret_cast<const float4 *>(sK + (t.key + 16 * j) * Ckf<D>::kLd + e);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float4 q = *reinterpret_cast<const float4 *>(sQ + (4 * ty + r) * Ckf<D>::kLd + e);
+      const float4 q = *reinterpret_cast<const float4 *>(sQ + (t.row + r) * Ckf<D>::kLd + e);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < NK; ++j) {
         acc[r][j] = ffma2(make_float2(q.x, q.y), make_float2(kv[j].x, kv[j].y), acc[r][j]);
         acc[r][j] = ffma2(make_float2(q.z, q.w), make_float2(kv[j].z, kv[j].w), acc[r][j]);
       }
@@ -142,83 +160,127 @@ __device__ __forceinline__ void ckf_products(const float *sQ, const float *sK, f
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[r][j] = acc[r][j].x + acc[r][j].y;
+    for (int j = 0; j < NK; ++j) x[r][j] = acc[r][j].x + acc[r][j].y;
+}
+
+// The rows of a thread's part: scale, last key that each sees (-1: none), -lse2.
+template <bool FEW>
+struct CkfRows {
+  float c2[4], nl[4];
+  int last[4];
+  __device__ __forceinline__ CkfRows(const PagedChunk &p, const ChunkPlan &w, const ChunkWalk &k, const CkfCols &t, bool first) {
+    const CkfPart<FEW> part;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int c = part.row + r;
+      last[r] = t.valid(c) ? k.g.P + t.query(c) : -1;
+      c2[r] = last[r] >= 0 ? head_c2(p.hs, k.s * p.c.Hq + t.head(c), first ? p.status : nullptr) : 0.f;
+      nl[r] = !first && last[r] >= 0
+                  ? __ldcg(reinterpret_cast<const float *>(p.ws + w.nl) + k.row0(p, w) + t.r0 + c) : 0.f;
+    }
+  }
+};
+
+__device__ __forceinline__ void ckf_merge(float &m, float &sum, float m2, float s2) {
+  const float mn = fmaxf(m, m2), ms = mn == -INFINITY ? 0.f : mn;
+  sum = sum * ex2_approx(m - ms) + s2 * ex2_approx(m2 - ms);
+  m = mn;
+}
+
+template <int D, bool FEW>
+__device__ __forceinline__ void ckf_keys_tile(const PagedChunk &p, const ChunkPlan &w, const ChunkWalk &k, const CkfCols &t, int end,
+                                              float *smem) {
+  using C = Ckf<D>;
+  constexpr int NK = CkfPart<FEW>::kKeys;
+  float *sQ = smem, *sK = sQ + kCkfEdge * C::kLd;   // two key tiles
+  float2 *s_ml = reinterpret_cast<float2 *>(smem + 3 * kCkfEdge * C::kLd);
+  const CkfPart<FEW> part;
+  const int tx = threadIdx.x % 16, kg = threadIdx.x / 64;
+  const bool work = FEW || threadIdx.x / 32 * 8 < t.rows;   // uniform over the warp
+  CkfPages<D> pages;
+  pages.find(p, w, k, k.tile);
+  pages.copy(p, w, k, p.c.k_pages, k.tile, sK);
+  if (k.tile + 1 < end) pages.find(p, w, k, k.tile + 1);
+  ckf_queries<D>(p, k, t, sQ);
+  const CkfRows<FEW> rows(p, w, k, t, true);
+  float m[4], sum[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) m[r] = -INFINITY, sum[r] = 0.f;
+  for (int tile = k.tile; tile < end; ++tile) {
+    float *now = sK + ((tile - k.tile) & 1) * kCkfEdge * C::kLd;
+    if (tile + 1 < end) {   // into the place of the tile before this one, which has been read
+      pages.copy(p, w, k, p.c.k_pages, tile + 1, sK + ((tile + 1 - k.tile) & 1) * kCkfEdge * C::kLd);
+      if (tile + 2 < end) pages.find(p, w, k, tile + 2);
+      ckf_landed<1>();
+    } else {
+      ckf_landed<0>();
+    }
+    __syncthreads();
+    if (work) {
+      float x[4][NK];
+      ckf_products<D, FEW>(sQ, now, x);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float mn = m[r];
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+          x[r][j] = tile * kCkfEdge + part.key + 16 * j <= rows.last[r] ? x[r][j] * rows.c2[r] : -INFINITY;
+          mn = fmaxf(mn, x[r][j]);
+        }
+        const float ms = mn == -INFINITY ? 0.f : mn;
+        sum[r] *= ex2_approx(m[r] - ms);
+#pragma unroll
+        for (int j = 0; j < NK; ++j) sum[r] += ex2_approx(x[r][j] - ms);
+        m[r] = mn;
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+      ckf_merge(m[r], sum[r], __shfl_xor_sync(0xffffffffu, m[r], o), __shfl_xor_sync(0xffffffffu, sum[r], o));
+  auto put = [&](int row, float2 ml) {
+    *reinterpret_cast<float2 *>(chunk_place(p, w.ml_a, w.ml_b, k.row0(p, w), w.cta_rows, k.tile, blockIdx.x, t.r0 + row, 2)) = ml;
+  };
+  if constexpr (FEW) {   // four threads a row, each with a fourth of the keys
+    if (tx == 0)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s_ml[kg * 16 + part.row + r] = make_float2(m[r], sum[r]);
+    __syncthreads();
+    if (threadIdx.x < 16 && t.valid(threadIdx.x)) {
+      float2 a = s_ml[threadIdx.x];
+#pragma unroll
+      for (int g = 1; g < 4; ++g) ckf_merge(a.x, a.y, s_ml[g * 16 + threadIdx.x].x, s_ml[g * 16 + threadIdx.x].y);
+      put(threadIdx.x, a);
+    }
+  } else {
+    if (tx == 0)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (rows.last[r] >= 0) put(part.row + r, make_float2(m[r], sum[r]));
+  }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kCkfThreads, D == 64 ? 2 : 1) ckf_keys(PagedChunk p, ChunkPlan w) {
-  using C = Ckf<D>;
   extern __shared__ __align__(16) float ckf_smem[];
-  float *sQ = ckf_smem, *sK = sQ + kCkfEdge * C::kLd;   // two key tiles
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
   pdl_wait();
   pdl_launch_dependents();
   const ChunkLine l = chunk_line(p, w);
   const ChunkCut cut = chunk_cut(__ldcg(l.cum + p.c.S), w.ctas_keys);
   ChunkWalk k;
-  for (k.start(p, w, l, cut, threadIdx.x % 32); k.any(); k.next(p, w, l)) {
+  for (k.start(p, w, l, cut, threadIdx.x % 32); k.any(); k.next(p, w, l))
     for (int b = k.g.col0(k.tile); b < k.g.cols; ++b) {
       const CkfCols t(k, w, b);
       const int end = min(k.end, k.g.seen(b, kCkfEdge));
-      const bool work = threadIdx.x / 32 * 8 < t.rows;   // uniform over the warp
       __syncthreads();
-      ckf_rows<D>(p, w, k, p.c.k_pages, k.tile, sK);
-      ckf_queries<D>(p, k, t, sQ);
-      float m[4], sum[4], c2[4];
-      int last[4];   // the last key that the row sees
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int c = 4 * ty + r;
-        m[r] = -INFINITY;
-        sum[r] = 0.f;
-        last[r] = t.valid(c) ? k.g.P + t.query(c) : -1;
-        c2[r] = last[r] >= 0 ? head_c2(p.hs, k.s * p.c.Hq + t.head(c), p.status) : 0.f;
-      }
-      for (int tile = k.tile; tile < end; ++tile) {
-        float *now = sK + ((tile - k.tile) & 1) * kCkfEdge * C::kLd;
-        if (tile + 1 < end) {   // into the place of the tile before this one, which the barrier below follows
-          ckf_rows<D>(p, w, k, p.c.k_pages, tile + 1, sK + ((tile + 1 - k.tile) & 1) * kCkfEdge * C::kLd);
-          ckf_landed<1>();
-        } else {
-          ckf_landed<0>();
-        }
-        __syncthreads();
-        if (work) {
-          float x[4][4];
-          ckf_products<D>(sQ, now, x);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float mn = m[r];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              x[r][j] = tile * kCkfEdge + tx + 16 * j <= last[r] ? x[r][j] * c2[r] : -INFINITY;
-              mn = fmaxf(mn, x[r][j]);
-            }
-            const float ms = mn == -INFINITY ? 0.f : mn;
-            sum[r] *= ex2_approx(m[r] - ms);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sum[r] += ex2_approx(x[r][j] - ms);
-            m[r] = mn;
-          }
-        }
-        __syncthreads();
-      }
-      if (!work) continue;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-          const float m2 = __shfl_xor_sync(0xffffffffu, m[r], o), s2 = __shfl_xor_sync(0xffffffffu, sum[r], o);
-          const float mn = fmaxf(m[r], m2), ms = mn == -INFINITY ? 0.f : mn;
-          sum[r] = sum[r] * ex2_approx(m[r] - ms) + s2 * ex2_approx(m2 - ms);
-          m[r] = mn;
-        }
-        if (tx == 0 && last[r] >= 0)
-          *reinterpret_cast<float2 *>(chunk_place(p, w.ml_a, w.ml_b, k.row0(p, w), w.cta_rows, k.tile, blockIdx.x,
-                                                  t.r0 + 4 * ty + r, 2)) = make_float2(m[r], sum[r]);
-      }
+      if (t.rows <= 16)
+        ckf_keys_tile<D, true>(p, w, k, t, end, ckf_smem);
+      else
+        ckf_keys_tile<D, false>(p, w, k, t, end, ckf_smem);
     }
-  }
 }
 
 // bid / den, den > 0 (a reciprocal within an ulp); 0 without a bid, whatever den.
@@ -228,146 +290,182 @@ __device__ __forceinline__ float ckf_share(float bid, float den) {
   return bid > 0.f ? bid * r : bid;
 }
 
+template <int D, bool FEW>
+__device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const ChunkPlan &w, const ChunkWalk &k, const CkfCols &t, int end,
+                                                float *smem) {
+  using C = Ckf<D>;
+  constexpr int NV = D / 64, NK = CkfPart<FEW>::kKeys;   // 4-column groups, keys of a thread
+  float *sQ = smem, *sK = sQ + kCkfEdge * C::kLd, *sV = sK + kCkfEdge * C::kLd, *sP = sV + kCkfEdge * C::kLd,
+        *sPart = sP + kCkfEdge * C::kLdP;
+  const int tid = threadIdx.x, tx = tid % 16;
+  const CkfPart<FEW> part;
+  const bool work = FEW || tid / 32 * 8 < t.rows;   // uniform over the warp
+  const int j0 = FEW ? tid / 64 * 16 : 0, j1 = FEW ? j0 + 16 : kCkfEdge;   // keys of the thread's value products
+  CkfPages<D> pages;
+  pages.find(p, w, k, k.tile);
+  pages.copy(p, w, k, p.c.k_pages, k.tile, sK);
+  pages.copy(p, w, k, p.c.v_pages, k.tile, sV);
+  if (k.tile + 1 < end) pages.find(p, w, k, k.tile + 1);
+  ckf_queries<D>(p, k, t, sQ);
+  const CkfRows<FEW> rows(p, w, k, t, false);
+  float num[4][4 * NV], sum[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    sum[r] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4 * NV; ++e) num[r][e] = 0.f;
+  }
+  const int key_l = tid % kCkfEdge, quarter = tid / kCkfEdge;
+  const bool several = t.n8 != 0, mine_too = !several || quarter * t.n8 < t.rows;
+  float *col = sP + key_l;
+  for (int tile = k.tile; tile < end; ++tile) {
+    const int key = tile * kCkfEdge + key_l;
+    // the total of this thread's (first) head: one head, or head `quarter` of several
+    float *at = mine_too ? ckf_total(p, w, k, key, t.hq0 + (several ? quarter : 0)) : nullptr;
+    const float before = at != nullptr ? __ldcg(at) : 0.f;
+    ckf_landed<1>();   // K (V is the newer group)
+    __syncthreads();
+    if (work) {
+      float x[4][NK];
+      ckf_products<D, FEW>(sQ, sK, x);
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int j = 0; j < NK; ++j) {
+          const bool sees = tile * kCkfEdge + part.key + 16 * j <= rows.last[r];
+          sP[(part.row + r) * C::kLdP + part.key + 16 * j] = sees ? ex2_approx(fmaf(x[r][j], rows.c2[r], rows.nl[r])) : 0.f;
+        }
+    }
+    __syncthreads();
+    if (tile + 1 < end) pages.copy(p, w, k, p.c.k_pages, tile + 1, sK);
+    if (!several) {   // one head: 16 rows a thread
+      const int n = min(16, t.rows - 16 * quarter);
+      float mine = 0.f, run = 0.f;   // the rows' bids, summed apart from the total: it would take their last bits
+#pragma unroll 4
+      for (int c = 0; c < n; ++c) mine += col[(16 * quarter + c) * C::kLdP];
+      sPart[quarter * kCkfEdge + key_l] = mine;
+      __syncthreads();
+      for (int i = 0; i < quarter; ++i) run += sPart[i * kCkfEdge + key_l];
+#pragma unroll 4
+      for (int c = 0; c < n; ++c) {
+        const float bid = col[(16 * quarter + c) * C::kLdP], after = run + bid;
+        col[(16 * quarter + c) * C::kLdP] = ckf_share(bid, before + (p.earlier ? run : after) + p.eps);
+        run = after;
+      }
+      if (quarter == 3 && at != nullptr) __stcg(at, before + run);
+    } else {
+      float held = before;
+      for (int h = quarter; h * t.n8 < t.rows; h += kCkfThreads / kCkfEdge) {
+        if (h != quarter) {
+          at = ckf_total(p, w, k, key, t.hq0 + h);
+          held = at != nullptr ? __ldcg(at) : 0.f;
+        }
+        float run = 0.f;
+#pragma unroll 4
+        for (int c = h * t.n8; c < h * t.n8 + t.n; ++c) {
+          const float bid = col[c * C::kLdP], after = run + bid;
+          col[c * C::kLdP] = ckf_share(bid, held + (p.earlier ? run : after) + p.eps);
+          run = after;
+        }
+        if (at != nullptr) __stcg(at, held + run);
+      }
+    }
+    if (tile + 1 < end)
+      ckf_landed<1>();   // V (the next K is the newer group)
+    else
+      ckf_landed<0>();
+    __syncthreads();
+    if (work) {
+#pragma unroll 4
+      for (int j = j0; j < j1; j += 4) {
+        float4 sh[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          sh[r] = *reinterpret_cast<const float4 *>(sP + (part.row + r) * C::kLdP + j);
+          if ((j - j0) / 4 == tx) sum[r] += (sh[r].x + sh[r].y) + (sh[r].z + sh[r].w);
+        }
+#pragma unroll
+        for (int e = 0; e < NV; ++e) {
+          float4 v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const float4 *>(sV + (j + i) * C::kLd + 64 * e + 4 * tx);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float s4[4] = {sh[r].x, sh[r].y, sh[r].z, sh[r].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float2 &lo = *reinterpret_cast<float2 *>(&num[r][4 * e]), &hi = *reinterpret_cast<float2 *>(&num[r][4 * e + 2]);
+              lo = ffma2(make_float2(s4[i], s4[i]), make_float2(v[i].x, v[i].y), lo);
+              hi = ffma2(make_float2(s4[i], s4[i]), make_float2(v[i].z, v[i].w), hi);
+            }
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (tile + 1 < end) {
+      pages.copy(p, w, k, p.c.v_pages, tile + 1, sV);
+      if (tile + 2 < end) pages.find(p, w, k, tile + 2);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], o);
+  float *to = chunk_place(p, w.acc_a, w.acc_b, k.row0(p, w), w.cta_rows, k.tile, blockIdx.x, t.r0, acc_stride(D));
+  if constexpr (FEW) {   // the four fourths of the keys, in order
+    constexpr int LD = D + 4;
+    float *stage = sK;   // [fourth][16 rows][d, sum]; the tile's K and V have been read
+    static_assert(4 * 16 * LD <= 2 * kCkfEdge * C::kLd, "stage");
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float *row = stage + (tid / 64 * 16 + part.row + r) * LD;
+#pragma unroll
+      for (int e = 0; e < NV; ++e)
+        *reinterpret_cast<float4 *>(row + 64 * e + 4 * tx) =
+            make_float4(num[r][4 * e], num[r][4 * e + 1], num[r][4 * e + 2], num[r][4 * e + 3]);
+      if (tx == 0) row[D] = sum[r];
+    }
+    __syncthreads();
+    for (int i = tid; i < t.rows * (D + 1); i += kCkfThreads) {
+      const int r = i / (D + 1), c = i % (D + 1);
+      float a = 0.f;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) a += stage[(g * 16 + r) * LD + c];
+      if (t.valid(r)) to[(size_t)r * acc_stride(D) + c] = a;
+    }
+  } else if (work) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (rows.last[r] < 0) continue;
+      float *row = to + (size_t)(part.row + r) * acc_stride(D);
+#pragma unroll
+      for (int e = 0; e < NV; ++e)
+        *reinterpret_cast<float4 *>(row + 64 * e + 4 * tx) =
+            make_float4(num[r][4 * e], num[r][4 * e + 1], num[r][4 * e + 2], num[r][4 * e + 3]);
+      if (tx == 0) row[D] = sum[r];
+    }
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kCkfThreads, D == 64 ? 2 : 1) ckf_values(PagedChunk p, ChunkPlan w) {
-  using C = Ckf<D>;
-  constexpr int NV = D / 64;   // 4-column groups of a thread
   extern __shared__ __align__(16) float ckf_smem[];
-  float *sQ = ckf_smem, *sK = sQ + kCkfEdge * C::kLd, *sV = sK + kCkfEdge * C::kLd, *sP = sV + kCkfEdge * C::kLd,
-        *sPart = sP + kCkfEdge * C::kLdP;
-  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
   pdl_wait();
   pdl_launch_dependents();
   const ChunkLine l = chunk_line(p, w);
   const ChunkCut cut = chunk_cut(__ldcg(l.cum + p.c.S), w.ctas_values);
-  const float *nl_all = reinterpret_cast<const float *>(p.ws + w.nl);
   ChunkWalk k;
-  for (k.start(p, w, l, cut, tid % 32); k.any(); k.next(p, w, l)) {
+  for (k.start(p, w, l, cut, threadIdx.x % 32); k.any(); k.next(p, w, l))
     for (int b = k.g.col0(k.tile); b < k.g.cols; ++b) {
       const CkfCols t(k, w, b);
       const int end = min(k.end, k.g.seen(b, kCkfEdge));
-      const bool work = tid / 32 * 8 < t.rows;   // uniform over the warp
       __syncthreads();
-      ckf_rows<D>(p, w, k, p.c.k_pages, k.tile, sK);
-      ckf_rows<D>(p, w, k, p.c.v_pages, k.tile, sV);
-      ckf_queries<D>(p, k, t, sQ);
-      float c2[4], nl[4], num[4][4 * NV], sum[4];
-      int last[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int c = 4 * ty + r;
-        last[r] = t.valid(c) ? k.g.P + t.query(c) : -1;
-        c2[r] = last[r] >= 0 ? head_c2(p.hs, k.s * p.c.Hq + t.head(c), nullptr) : 0.f;
-        nl[r] = last[r] >= 0 ? __ldcg(nl_all + k.row0(p, w) + t.r0 + c) : 0.f;
-        sum[r] = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4 * NV; ++e) num[r][e] = 0.f;
-      }
-      // the totals of one head's keys are brought a tile ahead (their thread writes them
-      // in this column tile's tile, and reads them in the next column tile's)
-      const int key_l = tid % kCkfEdge, part = tid / kCkfEdge;
-      for (int tile = k.tile; tile < end; ++tile) {
-        const int key = tile * kCkfEdge + key_l;
-        float *col = sP + key_l, *at = nullptr;
-        float before = 0.f;
-        if (t.n8 == 0) {
-          at = ckf_total(p, w, k, key, t.hq0);
-          if (at != nullptr) before = __ldcg(at);
-        }
-        ckf_landed<1>();   // K (V is the newer group)
-        __syncthreads();
-        if (work) {
-          float x[4][4];
-          ckf_products<D>(sQ, sK, x);
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const bool sees = tile * kCkfEdge + tx + 16 * j <= last[r];
-              sP[(4 * ty + r) * C::kLdP + tx + 16 * j] = sees ? ex2_approx(fmaf(x[r][j], c2[r], nl[r])) : 0.f;
-            }
-        }
-        __syncthreads();
-        if (tile + 1 < end) ckf_rows<D>(p, w, k, p.c.k_pages, tile + 1, sK);
-        if (t.n8 == 0) {   // one head: 16 rows a thread
-          const int rows = min(16, t.rows - 16 * part);
-          float mine = 0.f, run = 0.f;   // the rows' bids, summed apart from the total: it would take their last bits
-          for (int c = 0; c < rows; ++c) mine += col[(16 * part + c) * C::kLdP];
-          sPart[part * kCkfEdge + key_l] = mine;
-          __syncthreads();
-          for (int i = 0; i < part; ++i) run += sPart[i * kCkfEdge + key_l];
-#pragma unroll 4
-          for (int c = 0; c < rows; ++c) {
-            const float bid = col[(16 * part + c) * C::kLdP], after = run + bid;
-            col[(16 * part + c) * C::kLdP] = ckf_share(bid, before + (p.earlier ? run : after) + p.eps);
-            run = after;
-          }
-          if (part == 3 && at != nullptr) __stcg(at, before + run);
-        } else {
-          for (int h = part; h * t.n8 < t.rows; h += kCkfThreads / kCkfEdge) {
-            float *head_at = ckf_total(p, w, k, key, t.hq0 + h);
-            const float held = head_at != nullptr ? __ldcg(head_at) : 0.f;
-            float run = 0.f;
-#pragma unroll 4
-            for (int c = h * t.n8; c < h * t.n8 + t.n; ++c) {
-              const float bid = col[c * C::kLdP], after = run + bid;
-              col[c * C::kLdP] = ckf_share(bid, held + (p.earlier ? run : after) + p.eps);
-              run = after;
-            }
-            if (head_at != nullptr) __stcg(head_at, held + run);
-          }
-        }
-        if (tile + 1 < end)
-          ckf_landed<1>();   // V (the next K is the newer group)
-        else
-          ckf_landed<0>();
-        __syncthreads();
-        if (work) {
-#pragma unroll 4
-          for (int j = 0; j < kCkfEdge; j += 4) {
-            float4 sh[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              sh[r] = *reinterpret_cast<const float4 *>(sP + (4 * ty + r) * C::kLdP + j);
-              if (j / 4 == tx) sum[r] += (sh[r].x + sh[r].y) + (sh[r].z + sh[r].w);
-            }
-#pragma unroll
-            for (int e = 0; e < NV; ++e) {
-              float4 v[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const float4 *>(sV + (j + i) * C::kLd + 64 * e + 4 * tx);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                const float s4[4] = {sh[r].x, sh[r].y, sh[r].z, sh[r].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  float2 &lo = *reinterpret_cast<float2 *>(&num[r][4 * e]), &hi = *reinterpret_cast<float2 *>(&num[r][4 * e + 2]);
-                  lo = ffma2(make_float2(s4[i], s4[i]), make_float2(v[i].x, v[i].y), lo);
-                  hi = ffma2(make_float2(s4[i], s4[i]), make_float2(v[i].z, v[i].w), hi);
-                }
-              }
-            }
-          }
-        }
-        __syncthreads();
-        if (tile + 1 < end) ckf_rows<D>(p, w, k, p.c.v_pages, tile + 1, sV);
-      }
-      if (!work) continue;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], o);
-        if (last[r] < 0) continue;
-        float *to = chunk_place(p, w.acc_a, w.acc_b, k.row0(p, w), w.cta_rows, k.tile, blockIdx.x, t.r0 + 4 * ty + r,
-                                acc_stride(D));
-#pragma unroll
-        for (int e = 0; e < NV; ++e)
-          *reinterpret_cast<float4 *>(to + 64 * e + 4 * tx) =
-              make_float4(num[r][4 * e], num[r][4 * e + 1], num[r][4 * e + 2], num[r][4 * e + 3]);
-        if (tx == 0) to[D] = sum[r];
-      }
+      if (t.rows <= 16)
+        ckf_values_tile<D, true>(p, w, k, t, end, ckf_smem);
+      else
+        ckf_values_tile<D, false>(p, w, k, t, end, ckf_smem);
     }
-  }
 }
 
 cudaError_t launch_chunk_plan(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream);      // paged_chunk.cu
