@@ -21,8 +21,12 @@ struct EvictArgs {
 constexpr int kEvictCtas = 8;
 constexpr int kEvictKeys = 40 * 1024;   // a CTA's
 
+constexpr int kEvictRows = 128;         // of 256 bytes (keys and values), a block's share
+constexpr int kEvictTotals = 2048;      // totals, a block's share
+
 struct EvictWorkspace {
-  size_t info_off, list_off, key_off, total;
+  size_t info_off, list_off, flag_off, key_off, total;
+  int total_chunks;     // of a query head
   int cluster, slice;   // CTAs a key head; keys of each, at most
   bool shared;          // the scores fit in shared memory
 };

@@ -11,11 +11,16 @@
 // of 11, 11 and 10 bits, the CTAs' counts summed through distributed shared
 // memory; then each CTA writes the places of its tokens that stay.
 //
-// evict_move: rows to their new places.  In place, token list[r] >= r goes to r, so
-// a block that takes rows in order, has read a batch before it writes it, and is
-// alone on its bytes, never overwrites what is still to be read.  Blocks are
-// therefore alone on a slice of a key head's rows (down to 32 bytes, a sector)
-// instead of a part of the rows; to other pages the rows are split.
+// evict_place: rows to their new places in the same pages.  Row r takes the row of
+// token list[r] >= r, so a block that takes rows in order, has read a batch before it
+// writes it, and is alone on its bytes, never overwrites what is still to be read.
+// Blocks are therefore alone on a slice of a head's rows of keys or values (down to
+// 32 bytes, a sector) or on the totals of a query head, for all rows.  (Not kept,
+// 4 x 4 heads x 32768 of 131072 rows, a slice 150 us: a cluster a head, whole rows,
+// a cluster barrier a batch 207; chunks of rows on any block, with a flag each that
+// it has been read, 232 to 1100.)
+//
+// evict_move: rows to other pages; blocks take chunk after chunk by tickets.
 //
 // What bounds it: HBM (4 bytes a total, then the rows that stay, once each way).
 #include "da_evict.h"
@@ -40,7 +45,9 @@ EvictWorkspace evict_workspace(int S, int Hkv, int max_keep, int max_len) {
   auto next = [](size_t off, int64_t bytes) { return (size_t)round_up((int64_t)off + bytes, 256); };
   w.info_off = kStatusBytes;
   w.list_off = next(w.info_off, (int64_t)S * 8);
-  w.key_off = next(w.list_off, items * max_keep * 4);
+  w.flag_off = next(w.list_off, items * max_keep * 4);
+  w.total_chunks = (max_keep + kEvictTotals - 1) / kEvictTotals;
+  w.key_off = next(w.flag_off, 4);
   w.total = next(w.key_off, w.shared ? 0 : items * c * w.slice * 4);
   return w;
 }
@@ -84,6 +91,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(EvictArgs a, EvictWo
     if (!good) atomicCAS(a.status, DA_OK, DA_ERR_INVALID);
     reinterpret_cast<int2 *>(a.ws + w.info_off)[s] = make_int2(m, good ? m : len);
   }
+  if (blockIdx.x == 0 && tid == 0) *reinterpret_cast<int32_t *>(a.ws + w.flag_off) = 0;   // evict_move's ticket
   int32_t *list = (a.kept != nullptr ? a.kept : reinterpret_cast<int32_t *>(a.ws + w.list_off)) + (size_t)item * a.max_keep;
   if (a.kept != nullptr)
     for (int i = m + (int)rank * kSelThreads + tid; i < a.max_keep; i += (int)C * kSelThreads) list[i] = -1;
@@ -235,131 +243,315 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(EvictArgs a, EvictWo
 
 // ------------------------------------------------------------------------- the rows
 constexpr int kMoveThreads = 256;
-constexpr int kMoveLoads = 8;   // of a thread in flight
+constexpr int kMoveBlocks = 3 * 152;   // resident
+constexpr int kMoveLoads = 8;   // of a thread: 16 bytes, or a total
+static_assert(kMoveThreads * kMoveLoads == kEvictTotals && kMoveThreads * kMoveLoads * 16 == kEvictRows * 256, "a block's share");
 
-// One block: rows of a slice of one key head's keys or values (part < 2 slices), or
-// the totals of one of its query heads.
-struct MoveRows {
-  const uint8_t *in;     // of page 0, first row of the head
-  uint8_t *out;
-  size_t page_bytes;     // from page to page
-  int row_bytes, num_pages;
-  const int32_t *src, *dst;
-};
-
-template <typename V>
-__device__ __forceinline__ V ev_load(const uint8_t *p);
-template <>
-__device__ __forceinline__ uint4 ev_load<uint4>(const uint8_t *p) { return __ldcg(reinterpret_cast<const uint4 *>(p)); }
-template <>
-__device__ __forceinline__ float ev_load<float>(const uint8_t *p) { return __ldcg(reinterpret_cast<const float *>(p)); }
-
-// Rows from .. to - 1 of the list, a batch of kMoveLoads steps at a time.  The places
-// of a batch are found while the one before it is on its way: one read after the
-// other (list, tables, rows) took 4.5 us a batch.
-template <typename V>
-__device__ __forceinline__ void move_rows(const EvictArgs &a, const MoveRows &x, const int32_t *list, int from, int to, int lane_row,
-                                          int lane_byte, int rows_per_step, int sh, int *status) {
-  const int ps = 1 << sh;
-  int t[kMoveLoads], ip[kMoveLoads], op[kMoveLoads];
-  auto entries = [&](int r0) {   // of the list
-#pragma unroll
-    for (int u = 0; u < kMoveLoads; ++u) {
-      const int r = r0 + lane_row + u * rows_per_step;
-      t[u] = r < to ? __ldcg(list + r) : -1;
-    }
-  };
-  auto pages = [&](int r0) {
-#pragma unroll
-    for (int u = 0; u < kMoveLoads; ++u) {
-      const int r = r0 + lane_row + u * rows_per_step;
-      ip[u] = t[u] >= 0 ? __ldg(x.src + (t[u] >> sh)) : 0;
-      op[u] = t[u] >= 0 ? __ldg(x.dst + (r >> sh)) : 0;
-    }
-  };
-  const int batch = kMoveLoads * rows_per_step;
-  entries(from);
-  pages(from);
-  for (int r0 = from; r0 < to; r0 += batch) {
-    V v[kMoveLoads];
-    uint8_t *at[kMoveLoads];
-#pragma unroll
-    for (int u = 0; u < kMoveLoads; ++u) {
-      const int r = r0 + lane_row + u * rows_per_step;
-      at[u] = nullptr;
-      if (t[u] >= 0) {
-        if ((unsigned)ip[u] < (unsigned)x.num_pages && (unsigned)op[u] < (unsigned)x.num_pages) {
-          const uint8_t *p = x.in + (size_t)ip[u] * x.page_bytes + (size_t)((t[u] & (ps - 1)) * x.row_bytes + lane_byte);
-          uint8_t *q = x.out + (size_t)op[u] * x.page_bytes + (size_t)((r & (ps - 1)) * x.row_bytes + lane_byte);
-          if (p != q) {
-            at[u] = q;
-            v[u] = ev_load<V>(p);
-          }
-        } else {
-          atomicCAS(status, DA_OK, DA_ERR_INVALID);
-        }
-      }
-    }
-    entries(r0 + batch);
-    pages(r0 + batch);
-    __syncthreads();   // the batch has been read
-#pragma unroll
-    for (int u = 0; u < kMoveLoads; ++u)
-      if (at[u] != nullptr) *reinterpret_cast<V *>(at[u]) = v[u];
+// Row numbers (page, row in it) of a place in a sequence; -1 without a page (recorded).
+__device__ __forceinline__ long long ev_row(const int32_t *table, int t, int sh, int num_pages, int *status) {
+  const int page = __ldg(table + (t >> sh));
+  if ((unsigned)page >= (unsigned)num_pages) {
+    atomicCAS(status, DA_OK, DA_ERR_INVALID);
+    return -1;
   }
+  return ((long long)page << sh) | (t & ((1 << sh) - 1));
 }
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move(EvictArgs a, EvictWorkspace w, int sh, int slices) {
+// 0, once the loads behind `words` have returned: a barrier that says "read" must not
+// overtake them.
+__device__ __forceinline__ int ev_arrived(uint32_t words) {
+  uint32_t same;
+  asm volatile("mov.b32 %0, %1;" : "=r"(same) : "r"(words));
+  return (int)(same ^ words);
+}
+
+template <typename V>
+__device__ __forceinline__ V ev_load(const uint8_t *p) { return __ldcg(reinterpret_cast<const V *>(p)); }
+__device__ __forceinline__ uint32_t ev_words(const uint4 &v) { return v.x | v.y | v.z | v.w; }
+__device__ __forceinline__ uint32_t ev_words(float v) { return __float_as_uint(v); }
+
+// A head's rows, or a query head's totals: where they come from and go.
+struct MoveHead {
+  const int32_t *list, *src, *dst;
+  int s, h, m;
+  __device__ __forceinline__ MoveHead(const EvictArgs &a, const EvictWorkspace &w, int s_, int h_, bool totals) : s(s_), h(h_) {
+    m = __ldcg(reinterpret_cast<const int2 *>(a.ws + w.info_off) + s).x;
+    list = (a.kept != nullptr ? a.kept : reinterpret_cast<const int32_t *>(a.ws + w.list_off)) +
+           ((size_t)s * a.c.Hkv + (totals ? h / (a.c.Hq / a.c.Hkv) : h)) * a.max_keep;
+    src = (totals ? a.c.demand_table : a.c.page_table) + (size_t)s * a.c.max_pages;
+    dst = a.dst_page_table == nullptr ? src : (totals ? a.dst_demand_table : a.dst_page_table) + (size_t)s * a.dst_max_pages;
+  }
+};
+// Of its row r, which takes token t's: both rows in the pool; false where nothing moves.
+__device__ __forceinline__ bool ev_rows(const MoveHead &k, int t, int r, int sh, int num_pages, int *status, long long &from,
+                                        long long &to) {
+  from = ev_row(k.src, t, sh, num_pages, status);
+  to = ev_row(k.dst, r, sh, num_pages, status);
+  return from >= 0 && to >= 0 && from != to;
+}
+
+// 2048 totals: rows r0 .. + 2047 of those before `end`.
+struct MoveTotals {
+  float v[kMoveLoads];
+  float *to[kMoveLoads];
+  __device__ __forceinline__ void read(const EvictArgs &a, const MoveHead &k, int r0, int end, int sh) {
+    int t[kMoveLoads];
+#pragma unroll
+    for (int u = 0; u < kMoveLoads; ++u) {
+      const int r = r0 + (int)threadIdx.x + u * kMoveThreads;
+      t[u] = r < end ? __ldcg(k.list + r) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kMoveLoads; ++u) {
+      const int r = r0 + (int)threadIdx.x + u * kMoveThreads;
+      long long i, o;
+      to[u] = nullptr;
+      if (t[u] >= 0 && ev_rows(k, t[u], r, sh, a.c.num_demand_pages, a.status, i, o)) {
+        const int in_page = (1 << sh) - 1;   // of the pool: page, head, row
+        v[u] = __ldcg(a.c.demand_pages + ((((size_t)(i >> sh) * a.c.Hq + k.h) << sh) + (size_t)(i & in_page)));
+        to[u] = a.c.demand_pages + ((((size_t)(o >> sh) * a.c.Hq + k.h) << sh) + (size_t)(o & in_page));
+      }
+    }
+  }
+  __device__ __forceinline__ void write() {
+#pragma unroll
+    for (int u = 0; u < kMoveLoads; ++u)
+      if (to[u] != nullptr) *to[u] = v[u];
+  }
+};
+
+// 16-byte pieces of rows of keys and values, each thread's of a batch.
+struct MovePieces {
+  uint8_t *k, *v;        // the pools, at the key head's first row
+  size_t page_bytes;
+  int row_bytes, half, shift, page_shift;
+  __device__ __forceinline__ MovePieces(const EvictArgs &a, int h, int sh) : page_shift(sh) {
+    row_bytes = a.c.d * (a.c.dtype == DA_BF16 ? 2 : 4);
+    half = row_bytes / 16;                 // powers of two
+    shift = __ffs(2 * half) - 1;
+    page_bytes = ((size_t)a.c.Hkv * row_bytes) << sh;
+    k = reinterpret_cast<uint8_t *>(a.c.k_pages) + (((size_t)h * row_bytes) << sh);
+    v = reinterpret_cast<uint8_t *>(a.c.v_pages) + (((size_t)h * row_bytes) << sh);
+  }
+  __device__ __forceinline__ int row(int u) const { return ((int)threadIdx.x + u * kMoveThreads) >> shift; }
+  __device__ __forceinline__ uint4 *at(long long row, int u) const {
+    const int piece = ((int)threadIdx.x + u * kMoveThreads) & (2 * half - 1);
+    return reinterpret_cast<uint4 *>((piece < half ? k : v) + (size_t)(row >> page_shift) * page_bytes +
+                                     (size_t)(row & ((1 << page_shift) - 1)) * row_bytes) +
+           (piece & (half - 1));
+  }
+};
+
+// Rows from .. m - 1 of a head, in place: `lanes` threads with one V each for a row's
+// slice, a batch of kMoveLoads steps at a time.  The next batch's places are found
+// while one is on its way.  (With two batches on their way, 128 registers spill: 189 us
+// where one takes 150.)
+template <typename V>
+struct MovePlace {
+  uint8_t *pool;           // at the head's first row and the thread's bytes
+  size_t page_bytes;
+  int row_bytes, sh, num_pages, step, row0, m;   // rows of a step; the thread's first row
+  int *status;
+  const int32_t *list, *table;
+  __device__ __forceinline__ uint8_t *at(int page, int t) const {
+    return pool + (size_t)page * page_bytes + (size_t)((t & ((1 << sh) - 1)) * row_bytes);
+  }
+  __device__ __forceinline__ int row(int b, int u) const { return row0 + (b * kMoveLoads + u) * step; }
+  __device__ __forceinline__ void tokens(int b, int (&t)[kMoveLoads]) const {
+#pragma unroll
+    for (int u = 0; u < kMoveLoads; ++u) t[u] = row(b, u) < m ? __ldcg(list + row(b, u)) : -1;
+  }
+  __device__ __forceinline__ void pages(int b, const int (&t)[kMoveLoads], int (&from)[kMoveLoads], int (&to)[kMoveLoads]) const {
+#pragma unroll
+    for (int u = 0; u < kMoveLoads; ++u) {
+      from[u] = t[u] >= 0 ? __ldg(table + (t[u] >> sh)) : 0;
+      to[u] = t[u] >= 0 ? __ldg(table + (row(b, u) >> sh)) : 0;
+    }
+  }
+  // to: -1 where nothing moves
+  __device__ __forceinline__ void read(int b, const int (&t)[kMoveLoads], const int (&from)[kMoveLoads], int (&to)[kMoveLoads],
+                                       V (&v)[kMoveLoads]) const {
+#pragma unroll
+    for (int u = 0; u < kMoveLoads; ++u) {
+      const bool have = t[u] >= 0, ok = (unsigned)from[u] < (unsigned)num_pages && (unsigned)to[u] < (unsigned)num_pages;
+      if (have && !ok) atomicCAS(status, DA_OK, DA_ERR_INVALID);
+      if (have && ok && t[u] != row(b, u))
+        v[u] = ev_load<V>(at(from[u], t[u]));
+      else
+        to[u] = -1;
+    }
+  }
+  __device__ __forceinline__ void run() const {
+    const int batches = (m - row0 + (int)threadIdx.x / ((int)blockDim.x / step) + kMoveLoads * step - 1) / (kMoveLoads * step);
+    int t[kMoveLoads], from[kMoveLoads], to[kMoveLoads];
+    tokens(0, t);
+    pages(0, t, from, to);
+#pragma unroll 1
+    for (int b = 0; b < batches; ++b) {
+      V v[kMoveLoads];
+      uint8_t *out[kMoveLoads];
+      read(b, t, from, to, v);
+#pragma unroll
+      for (int u = 0; u < kMoveLoads; ++u) out[u] = to[u] >= 0 ? at(to[u], row(b, u)) : nullptr;
+      tokens(b + 1, t);
+      pages(b + 1, t, from, to);
+      uint32_t words = 0;
+#pragma unroll
+      for (int u = 0; u < kMoveLoads; ++u)
+        if (out[u] != nullptr) words |= ev_words(v[u]);
+      __syncthreads_or(ev_arrived(words));   // the batch has been read
+#pragma unroll
+      for (int u = 0; u < kMoveLoads; ++u)
+        if (out[u] != nullptr) *reinterpret_cast<V *>(out[u]) = v[u];
+    }
+  }
+};
+
+__global__ void __launch_bounds__(kMoveThreads, 2) evict_place(EvictArgs a, EvictWorkspace w, int sh, int slices) {
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, G = a.c.Hq / a.c.Hkv, parts = 2 * slices + G;
-  const int item = blockIdx.x / parts, part = blockIdx.x % parts, s = item / a.c.Hkv, h = item % a.c.Hkv;
-  const int2 info = __ldcg(reinterpret_cast<const int2 *>(a.ws + w.info_off) + s);
-  const int m = info.x;
-  if (h == 0 && part == 0 && blockIdx.y == 0 && tid == 0) a.new_lens[s] = info.y;
-  const int32_t *list = (a.kept != nullptr ? a.kept : reinterpret_cast<const int32_t *>(a.ws + w.list_off)) +
-                        (size_t)item * a.max_keep;
-  const bool place = a.dst_page_table == nullptr;
-  int from = 0, to = m;
-  if (place) {   // the first row that moves: list[r] - r does not decrease
-    int n = m;
-    while (n > 0) {
-      const int step = (n + kMoveThreads - 1) / kMoveThreads, r = from + tid * step;
-      const int k = __syncthreads_count(tid * step < n && __ldcg(list + r) == r);
-      if (k == 0) break;
-      const int skip = (k - 1) * step + 1;
-      from += skip;
-      n = min(step - 1, n - skip);
-    }
-  } else {
-    const int per = (m + gridDim.y - 1) / gridDim.y;
-    from = min((int)blockIdx.y * per, m);
-    to = min(from + per, m);
+  const int item = blockIdx.x / parts, part = blockIdx.x % parts;
+  const bool totals = part >= 2 * slices;
+  const int s = item / a.c.Hkv, hkv = item % a.c.Hkv;
+  const MoveHead k(a, w, s, totals ? hkv * G + part - 2 * slices : hkv, totals);
+  if (part == 0 && hkv == 0 && tid == 0) a.new_lens[s] = __ldcg(reinterpret_cast<const int2 *>(a.ws + w.info_off) + s).y;
+  // the first row that moves: list[r] - r does not decrease
+  int from = 0;
+  for (int n = k.m; n > 0;) {
+    const int step = (n + kMoveThreads - 1) / kMoveThreads, r = from + tid * step;
+    const int same = __syncthreads_count(tid * step < n && __ldcg(k.list + r) == r);
+    if (same == 0) break;
+    const int skip = (same - 1) * step + 1;
+    from += skip;
+    n = min(step - 1, n - skip);
   }
-  if (from >= to) return;
-  const size_t smax = (size_t)s * a.c.max_pages, dmax = (size_t)s * (place ? a.c.max_pages : a.dst_max_pages);
-  MoveRows x;
-  if (part < 2 * slices) {
-    const int eb = a.c.dtype == DA_BF16 ? 2 : 4;
-    x.row_bytes = a.c.d * eb;
-    x.page_bytes = ((size_t)a.c.Hkv * x.row_bytes) << sh;
-    uint8_t *pool = reinterpret_cast<uint8_t *>(part < slices ? a.c.k_pages : a.c.v_pages) + (((size_t)h * x.row_bytes) << sh);
-    x.in = x.out = pool;
-    x.num_pages = a.c.num_pages;
-    x.src = a.c.page_table + smax;
-    x.dst = (place ? a.c.page_table : a.dst_page_table) + dmax;
-    const int bytes = x.row_bytes / slices, lanes = bytes / 16;   // of a row: powers of two
-    move_rows<uint4>(a, x, list, from, to, tid / lanes, part % slices * bytes + tid % lanes * 16, kMoveThreads / lanes, sh,
-                     a.status);
+  if (from >= k.m) return;
+  if (totals) {
+    MovePlace<float> x{reinterpret_cast<uint8_t *>(a.c.demand_pages) + (((size_t)k.h * 4) << sh), ((size_t)a.c.Hq * 4) << sh, 4, sh,
+                       a.c.num_demand_pages, kMoveThreads, from + tid, k.m, a.status, k.list, k.src};
+    x.run();
   } else {
-    const int hq = h * G + part - 2 * slices;
-    x.row_bytes = 4;
-    x.page_bytes = ((size_t)a.c.Hq * 4) << sh;
-    x.in = x.out = reinterpret_cast<uint8_t *>(a.c.demand_pages) + (((size_t)hq * 4) << sh);
-    x.num_pages = a.c.num_demand_pages;
-    x.src = a.c.demand_table + smax;
-    x.dst = (place ? a.c.demand_table : a.dst_demand_table) + dmax;
-    move_rows<float>(a, x, list, from, to, tid, 0, kMoveThreads, sh, a.status);
+    const int row_bytes = a.c.d * (a.c.dtype == DA_BF16 ? 2 : 4), bytes = row_bytes / slices, lanes = bytes / 16;   // powers of two
+    uint8_t *pool = reinterpret_cast<uint8_t *>(part < slices ? a.c.k_pages : a.c.v_pages);
+    MovePlace<uint4> x{pool + (((size_t)k.h * row_bytes) << sh) + part % slices * bytes + tid % lanes * 16,
+                       ((size_t)a.c.Hkv * row_bytes) << sh, row_bytes, sh, a.c.num_pages, kMoveThreads / lanes, from + tid / lanes, k.m,
+                       a.status, k.list, k.src};
+    x.run();
+  }
+}
+
+// To other pages.  The next chunk's places are found while the one at hand is on its
+// way: ticket, list, tables and rows one after the other took 10 us a chunk.
+constexpr int kMoveSeqs = 1024;   // sequences whose chunks are counted; more take equally many each
+__global__ void __launch_bounds__(kMoveThreads, 3) evict_move(EvictArgs a, EvictWorkspace w, int sh) {
+  __shared__ int s_cum[kMoveSeqs + 1];                   // chunks of a key head before each sequence
+  __shared__ int s_warp[kMoveThreads / 32];
+  __shared__ long long s_from[2][kEvictRows], s_to[2][kEvictRows];
+  __shared__ int s_ticket[2];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, S = a.c.S, Hkv = a.c.Hkv;
+  pdl_wait();
+  pdl_launch_dependents();
+  int32_t *counter = reinterpret_cast<int32_t *>(a.ws + w.flag_off);
+  const int rows = kEvictRows * 128 / (a.c.d * (a.c.dtype == DA_BF16 ? 2 : 4));   // of a chunk
+  const int2 *info = reinterpret_cast<const int2 *>(a.ws + w.info_off);
+  for (int s = blockIdx.x * kMoveThreads + tid; s < S; s += gridDim.x * kMoveThreads) a.new_lens[s] = __ldcg(info + s).y;
+  const bool counted = S <= kMoveSeqs;
+  if (counted) {
+    constexpr int PER = kMoveSeqs / kMoveThreads;
+    int c[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int s = tid * PER + i;
+      c[i] = sum;
+      if (s < S) sum += (__ldcg(info + s).x + rows - 1) / rows;
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_warp[warp] = inc;
+    __syncthreads();
+    int base = inc - sum;
+    for (int i = 0; i < warp; ++i) base += s_warp[i];
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (tid * PER + i <= S) s_cum[tid * PER + i] = base + c[i];
+    if (tid == kMoveThreads - 1 && S == kMoveSeqs) s_cum[S] = base + sum;
+  }
+  if (tid == 0) {
+    s_ticket[0] = atomicAdd(counter, 1);
+    s_ticket[1] = atomicAdd(counter, 1);
+  }
+  __syncthreads();
+  const int most = (int)((a.max_keep < a.max_len ? a.max_keep : a.max_len) + rows - 1) / rows;
+  const long long chunks = (long long)Hkv * (counted ? s_cum[S] : (long long)S * most);
+  const long long tickets = chunks + (long long)S * a.c.Hq * w.total_chunks;
+  int cs = 0, ch = 0, cr = 0, ct = -1;                   // of the next chunk: sequence, key head, this thread's row and its token
+  auto find = [&](int ticket) {
+    ct = -1;
+    if (ticket >= chunks) return;
+    int first, each = most;
+    if (counted) {
+      int lo = 0, hi = S - 1;                             // the last sequence whose chunks begin at or before
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if ((long long)Hkv * s_cum[mid] <= ticket)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      cs = lo;
+      first = Hkv * s_cum[lo];
+      each = s_cum[lo + 1] - s_cum[lo];
+    } else {
+      cs = ticket / (Hkv * most);
+      first = cs * Hkv * most;
+    }
+    ch = (ticket - first) / each;
+    cr = (ticket - first) % each * rows + tid;
+    const MoveHead k(a, w, cs, ch, false);
+    if (tid < rows && cr < k.m) ct = __ldcg(k.list + cr);
+  };
+  auto places = [&](int buf) {
+    if (tid >= rows) return;
+    long long i = -1, o = -1;
+    const bool moves = ct >= 0 && ev_rows(MoveHead(a, w, cs, ch, false), ct, cr, sh, a.c.num_pages, a.status, i, o);
+    s_from[buf][tid] = moves ? i : -1;
+    s_to[buf][tid] = o;
+  };
+  int now = s_ticket[0];
+  find(now);
+  places(0);
+  for (int turn = 0; now < tickets; ++turn) {
+    const int buf = turn & 1, next = s_ticket[buf ^ 1];
+    __syncthreads();                                      // the chunk's places are there
+    if (now >= chunks) {
+      const int item = (int)((now - chunks) / w.total_chunks), r0 = (int)((now - chunks) % w.total_chunks) * kEvictTotals;
+      const MoveHead k(a, w, item / a.c.Hq, item % a.c.Hq, true);
+      MoveTotals t;
+      t.read(a, k, r0, min(k.m, r0 + kEvictTotals), sh);
+      if (tid == 0) s_ticket[buf] = atomicAdd(counter, 1);
+      t.write();
+    } else {
+      const MovePieces x(a, ch, sh);
+      uint4 v[kMoveLoads];
+#pragma unroll
+      for (int u = 0; u < kMoveLoads; ++u) {
+        const long long i = s_from[buf][x.row(u)];
+        if (i >= 0) v[u] = __ldcg(x.at(i, u));
+      }
+      find(next);                                         // (its list is on its way)
+      if (tid == 0) s_ticket[buf] = atomicAdd(counter, 1);   // (of the chunk after the next)
+      if (next < chunks) places(buf ^ 1);
+#pragma unroll
+      for (int u = 0; u < kMoveLoads; ++u)
+        if (s_from[buf][x.row(u)] >= 0) *x.at(s_to[buf][x.row(u)], u) = v[u];
+    }
+    now = next;
+    __syncthreads();                                      // the places have been read
   }
 }
 
@@ -374,6 +566,11 @@ int launch_evict(const EvictArgs &a, cudaStream_t stream) {
   const EvictWorkspace w = evict_workspace(a.c.S, a.c.Hkv, a.max_keep < a.max_len ? a.max_keep : a.max_len, a.max_len);
   int sh = 0;
   while ((1 << sh) < a.c.page_size) ++sh;
+  const int rows = kEvictRows * 128 / (a.c.d * (a.c.dtype == DA_BF16 ? 2 : 4));
+  const int64_t items = (int64_t)a.c.S * a.c.Hkv, totals = (int64_t)a.c.S * a.c.Hq, most = a.max_keep < a.max_len ? a.max_keep : a.max_len;
+  const int64_t tickets = items * ((most + rows - 1) / rows) + totals * w.total_chunks;
+  if (tickets > 0x7F000000 || items * w.cluster > 0x7FFFFFFF || items * 64 + totals > 0x7FFFFFFF)
+    return DA_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.c.S * a.c.Hkv * w.cluster));
   cfg.blockDim = dim3(kSelThreads);
@@ -388,19 +585,18 @@ int launch_evict(const EvictArgs &a, cudaStream_t stream) {
   cfg.attrs = at;
   cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, evict_select, a, w, sh) != cudaSuccess) return DA_ERR_CUDA;
-  // in place, blocks come from slices of the rows; to other pages, from parts of the list
-  const int64_t rows = (int64_t)a.c.S * a.c.Hkv * 2;
-  const int row_bytes = a.c.d * (a.c.dtype == DA_BF16 ? 2 : 4);
-  int slices = 1, chunks = 1;
-  if (a.dst_page_table == nullptr)
-    while (rows * slices < 608 && row_bytes / slices > 32) slices *= 2;
-  else
-    while (rows * chunks < 1216 && chunks * 512 < a.max_keep) chunks *= 2;
-  const int64_t blocks = (int64_t)a.c.S * a.c.Hkv * (2 * slices + a.c.Hq / a.c.Hkv);
-  return launch_after(evict_move, dim3((unsigned)blocks, (unsigned)chunks), kMoveThreads, 0, stream, a, w, sh, slices) ==
-                 cudaSuccess
-             ? DA_OK
-             : DA_ERR_CUDA;
+  if (a.dst_page_table == nullptr) {
+    const int row_bytes = a.c.d * (a.c.dtype == DA_BF16 ? 2 : 4);
+    int slices = 1;
+    while (items * 2 * slices < 4 * 152 && row_bytes / slices > 32) slices *= 2;
+    return launch_after(evict_place, dim3((unsigned)(items * (2 * slices + a.c.Hq / a.c.Hkv))), kMoveThreads, 0, stream, a, w, sh,
+                        slices) == cudaSuccess
+               ? DA_OK
+               : DA_ERR_CUDA;
+  }
+  const int64_t blocks = tickets < 1 ? 1 : tickets < kMoveBlocks ? tickets : kMoveBlocks;
+  return launch_after(evict_move, dim3((unsigned)blocks), kMoveThreads, 0, stream, a, w, sh) == cudaSuccess ? DA_OK
+                                                                                                          : DA_ERR_CUDA;
 }
 
 }  // namespace da
