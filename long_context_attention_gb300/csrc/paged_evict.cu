@@ -67,6 +67,14 @@ __device__ __forceinline__ uint32_t ev_peer(const void *local, uint32_t rank) { 
   return v;
 }
 
+__device__ __forceinline__ uint4 ev_peer4(const void *local, uint32_t rank) {   // four words, 16-byte aligned
+  uint32_t a;
+  uint4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
 // Scores as integers of the same order; NaN as +infinity, -0 as 0.
 __device__ __forceinline__ uint32_t ev_key(float f) {
   const uint32_t u = __float_as_uint(f);
@@ -77,7 +85,7 @@ __device__ __forceinline__ uint32_t ev_key(float f) {
 
 __global__ void __launch_bounds__(kSelThreads) evict_select(EvictArgs a, EvictWorkspace w, int page_shift) {
   extern __shared__ uint32_t sel_keys[];
-  __shared__ uint32_t s_hist[kCopies + 1][kBins];   // the first pass's (the third's in its first copy); the second's
+  __shared__ __align__(16) uint32_t s_hist[kCopies + 1][kBins];   // the first pass's (the third's in its first copy); the second's
   __shared__ uint32_t s_above[kSelWarps], s_equal[kSelWarps], s_count[2], s_pick[2];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const uint32_t rank = ev_rank(), C = (uint32_t)w.cluster;
@@ -108,23 +116,33 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(EvictArgs a, EvictWo
   const int ps = 1 << page_shift;
   for (int i = tid; i < (kCopies + 1) * kBins; i += kSelThreads) s_hist[0][i] = 0;
   __syncthreads();
-  // four tokens a thread: they lie in one page
+  // four tokens a thread, which lie in one page; the totals of four query heads on their
+  // way at once
+  auto page_of = [&](int i) { return i < cnt ? __ldcg(dtab + ((t0 + i) >> page_shift)) : 0; };
+  int page = page_of(4 * tid);
 #pragma unroll 2
   for (int i = 4 * tid; i < cnt; i += 4 * kSelThreads) {
-    const int t = t0 + i, page = __ldcg(dtab + (t >> page_shift));
-    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int t = t0 + i, next = page_of(i + 4 * kSelThreads);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
     if ((unsigned)page < (unsigned)a.c.num_demand_pages) {
       const float *at = a.c.demand_pages + ((((size_t)page * a.c.Hq + (size_t)h * G) << page_shift) + (t & (ps - 1)));
-      f = __ldcg(reinterpret_cast<const float4 *>(at));
-#pragma unroll 2
-      for (int g = 1; g < G; ++g) {
-        const float4 o = __ldcg(reinterpret_cast<const float4 *>(at + ((size_t)g << page_shift)));
-        f.x = __fadd_rn(f.x, o.x), f.y = __fadd_rn(f.y, o.y), f.z = __fadd_rn(f.z, o.z), f.w = __fadd_rn(f.w, o.w);
+      for (int g = 0; g < G; g += 4) {
+        float4 f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (g + e < G) f[e] = __ldcg(reinterpret_cast<const float4 *>(at + ((size_t)(g + e) << page_shift)));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (g + e >= G) break;
+          const float x[4] = {f[e].x, f[e].y, f[e].z, f[e].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = g + e == 0 ? x[k] : __fadd_rn(v[k], x[k]);
+        }
       }
     } else {
       atomicCAS(a.status, DA_OK, DA_ERR_INVALID);
     }
-    const float v[4] = {f.x, f.y, f.z, f.w};
+    page = next;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (i + e >= cnt) break;
@@ -155,21 +173,23 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(EvictArgs a, EvictWo
       ev_sync();
     else
       __syncthreads();
-    // thread i: 4 bins (2 in the last pass) from the top
-    const int own = bins / kSelThreads;
-    uint32_t c[4], sum = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      c[j] = 0;
-      if (j < own) {
-        const int bin = bins - 1 - (tid * own + j);
-        if (C > 1)
-          for (uint32_t r = 0; r < C; ++r) c[j] += ev_peer(hist + bin, r);
-        else
-          c[j] = hist[bin];
+    // thread i: 4 bins from the top.  (A CTA reads its peers' counts 16 bytes at a time: word
+    // by word, 18 us for 8 CTAs.)
+    const int bin0 = bins - 4 - 4 * tid;   // the lowest of the thread's
+    uint32_t c[4] = {0, 0, 0, 0};
+    if (bin0 >= 0) {
+      if (C > 1) {
+#pragma unroll 8
+        for (uint32_t r = 0; r < C; ++r) {
+          const uint4 x = ev_peer4(hist + bin0, r);
+          c[0] += x.w, c[1] += x.z, c[2] += x.y, c[3] += x.x;
+        }
+      } else {
+        const uint4 x = *reinterpret_cast<const uint4 *>(hist + bin0);
+        c[0] = x.w, c[1] = x.z, c[2] = x.y, c[3] = x.x;
       }
-      sum += c[j];
     }
+    const uint32_t sum = c[0] + c[1] + c[2] + c[3];
     uint32_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -183,8 +203,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(EvictArgs a, EvictWo
     if (before < need && need <= before + sum) {   // one thread
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (j < own && before < need && need <= before + c[j]) {
-          s_pick[0] = (uint32_t)(bins - 1 - (tid * own + j));
+        if (before < need && need <= before + c[j]) {
+          s_pick[0] = (uint32_t)(bin0 + 3 - j);
           s_pick[1] = need - before;
           break;
         }
