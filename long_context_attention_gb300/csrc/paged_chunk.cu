@@ -12,6 +12,8 @@ namespace da {
 
 int launch_chunk_f32(const PagedChunk &p, cudaStream_t stream);
 int launch_chunk_bf16(const PagedChunk &p, cudaStream_t stream);
+int chunk_small_cluster(int S, int Hq, int Hkv, int max_new, int max_len);
+int launch_chunk_small(const PagedChunk &p, int csize, cudaStream_t stream);
 
 // Lengths and new tokens of every sequence, checked once; rows and units before
 // each.  What is not valid is recorded and has no new tokens, so that no later
@@ -248,7 +250,9 @@ size_t chunk_workspace(int S, int Hq, int Hkv, int d, long long N, int max_new, 
 }
 
 int launch_paged_chunk(const PagedChunk &p, cudaStream_t stream) {
-  return p.c.dtype == DA_F32 ? launch_chunk_f32(p, stream) : launch_chunk_bf16(p, stream);
+  if (p.c.dtype == DA_F32) return launch_chunk_f32(p, stream);
+  const int c = chunk_small_cluster(p.c.S, p.c.Hq, p.c.Hkv, p.max_new, p.max_len);
+  return c > 0 ? launch_chunk_small(p, c, stream) : launch_chunk_bf16(p, stream);
 }
 
 }  // namespace da

@@ -20,14 +20,14 @@ from long_context_attention_gb300 import binding as b
 from long_context_attention_gb300 import rope_inv_freq
 from oracle import paged as op
 from tests._parity import host64
-from tests._paged import DEV, TYPES, make_cache, oracle_step
+from tests._paged import DEV, LONG, TYPES, make_cache, oracle_step
 
 pytestmark = pytest.mark.gpu
 
 
 def make(lens, news, Hq, Hkv, d, page, dtype, seed=0, junk=None, pad=0, spare=2, fresh=True):
     """A cache whose sequences' last news[s] tokens are new (no demand yet), their queries and cu_tokens."""
-    cache, _, _ = make_cache(len(lens), lens, Hq, Hkv, d, page, dtype, seed=seed, junk=junk, spare=spare, extra_width=1)
+    cache, _, _ = make_cache(len(lens), lens, Hq, Hkv, d, page, dtype, seed=seed, junk=junk, spare=spare)
     g = torch.Generator().manual_seed(seed + 1)
     cu = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
     N = int(cu[-1]) + pad
@@ -79,16 +79,20 @@ def check(cache, q, cu, before, out, ref):
 
 
 def run(cache, q, cu, max_new, max_len, **kw):
+    """The call with max_len and with one past what the kernel for short calls takes, which the result does not depend
+    on; the cache is left as after one call."""
     tau = kw.get("tau", 1.0) if kw.get("tau_bh") is None else host64(kw["tau_bh"]).reshape(cache.S, cache.Hq)
     before = cache.demand_pages.clone()
     ref = oracle(cache, q, cu, tau, kw.get("eps", 1e-6), bool(kw.get("flags", 0) & b.DA_FLAG_EARLIER_DEMAND_ONLY))
-    ws = b.dilution_attn_paged_chunk_workspace(cache, q.shape[0], max_new, max_len)
-    ws[256:] = 0xC7          # whatever an earlier call left
-    out = torch.full_like(q, 7.0)
-    got = b.dilution_attn_paged_chunk(q, cache, cu, max_new, max_len, out, workspace=ws, **kw)
-    assert got is out and b.dilution_attn_get_error(ws) == b.DA_OK
-    check(cache, q, cu, before, out, ref)
-    assert (out[int(cu[-1]):] == 7.0).all()          # rows behind the last sequence
+    for most in sorted({max_len, max(max_len, min(LONG, cache.max_pages * cache.page_size))}):
+        cache.demand_pages.copy_(before)
+        ws = b.dilution_attn_paged_chunk_workspace(cache, q.shape[0], max_new, most)
+        ws[256:] = 0xC7          # whatever an earlier call left
+        out = torch.full_like(q, 7.0)
+        got = b.dilution_attn_paged_chunk(q, cache, cu, max_new, most, out, workspace=ws, **kw)
+        assert got is out and b.dilution_attn_get_error(ws) == b.DA_OK
+        check(cache, q, cu, before, out, ref)
+        assert (out[int(cu[-1]):] == 7.0).all()          # rows behind the last sequence
     return out
 
 
@@ -205,12 +209,13 @@ def test_two_chunks_are_one(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-def test_equal_bits_in_place_and_streams(dtype):
+@pytest.mark.parametrize("news,most", [([130, 64, 5], 130), ([20, 30, 5], 32)])
+def test_equal_bits_in_place_and_streams(news, most, dtype):
     """Equal calls give equal bits: into q's own place, on another stream, without a workspace, from a graph."""
-    cache, q, cu = make([900, 120, 77], [130, 64, 5], 4, 2, 64, 32, dtype, seed=31, pad=2)
+    cache, q, cu = make([900, 120, 77], news, 4, 2, 64, 32, dtype, seed=31, pad=2)
     start = cache.demand_pages.clone()
     ref = torch.zeros_like(q)
-    b.dilution_attn_paged_chunk(q, cache, cu, 130, 900, ref)
+    b.dilution_attn_paged_chunk(q, cache, cu, most, 900, ref)
     total = cache.demand_pages.clone()
 
     def same(out):
@@ -219,78 +224,78 @@ def test_equal_bits_in_place_and_streams(dtype):
         cache.demand_pages.copy_(start)
     cache.demand_pages.copy_(start)
     own = q.clone()
-    b.dilution_attn_paged_chunk(own, cache, cu, 130, 900, own)
+    b.dilution_attn_paged_chunk(own, cache, cu, most, 900, own)
     same(own)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    out = b.dilution_attn_paged_chunk(q, cache, cu, 130, 900, stream=side)
+    out = b.dilution_attn_paged_chunk(q, cache, cu, most, 900, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     same(out)
-    ws = b.dilution_attn_paged_chunk_workspace(cache, q.shape[0], 130, 900)
+    ws = b.dilution_attn_paged_chunk_workspace(cache, q.shape[0], most, 900)
     g = torch.cuda.CUDAGraph()
     out = torch.zeros_like(q)
     with torch.cuda.graph(g):
-        b.dilution_attn_paged_chunk(q, cache, cu, 130, 900, out, workspace=ws)
+        b.dilution_attn_paged_chunk(q, cache, cu, most, 900, out, workspace=ws)
     for _ in range(2):
         out.zero_()
         g.replay()
         same(out)
     # the captured call follows lengths that change
     cache.seq_lens.copy_(torch.tensor([800, 119, 70], dtype=torch.int32))
-    cu.copy_(torch.tensor([0, 3, 104, 104], dtype=torch.int32))
+    cu.copy_(torch.tensor([0, 3, 30, 30], dtype=torch.int32))
     r = oracle(cache, q, cu)
     g.replay()
     check(cache, q, cu, start, out, r)
     assert b.dilution_attn_get_error(ws) == b.DA_OK and b.dilution_attn_get_error(cache.status) == b.DA_OK
 
 
-def test_bad_lengths_and_pages():
-    """What the host cannot see: recorded, nothing else read or written, other sequences unharmed."""
-    for dtype in ("f32", "bf16"):
-        lens, news = [100, 200, 150], [20, 70, 5]
+@pytest.mark.parametrize("dtype,mid", [("f32", 70), ("bf16", 70), ("bf16", 30)])
+def test_bad_lengths_and_pages(dtype, mid):
+    """What the host cannot see: recorded, nothing else read or written, other sequences unharmed.  (Up to 32 new tokens
+    take the kernel for short calls.)"""
+    lens, news = [100, 200, 150], [20, mid, 5]
+    first = np.concatenate([[0], np.cumsum(news)])
 
-        def call(change, max_new=70, max_len=200, good=(0, 2)):
-            cache, q, cu = make(lens, news, 4, 2, 64, 16, dtype, seed=41)
-            ro, rD, info = oracle(cache, q, cu)
-            start = cache.demand_pages.clone()
-            change(cache, cu)
-            ws = b.dilution_attn_paged_chunk_workspace(cache, q.shape[0], max_new, max_len)
-            out = torch.full_like(q, 7.0)
-            b.dilution_attn_paged_chunk(q, cache, cu, max_new, max_len, out, workspace=ws)
-            assert b.dilution_attn_get_error(ws) == b.DA_ERR_INVALID
-            assert b.dilution_attn_get_error(ws) == b.DA_OK
-            first = np.concatenate([[0], np.cumsum(news)])
-            for s in good:
-                r = slice(first[s], first[s + 1])
-                assert np.abs(host64(out)[r] - ro[r]).max() < 0.05
-            return cache, out, start
-
-        for bad in (-1, 201, 300, 69):      # 69: shorter than its new tokens
-            def change(cache, cu, bad=bad):
-                cache.seq_lens[1] = bad
-            cache, out, start = call(change)
-            assert (out[20:90] == 7.0).all()
-            t = torch.arange(lens[1], device=DEV)
-            at = cache.demand_table[1, t // 16].long(), slice(None), t % 16
-            assert torch.equal(cache.demand_pages[at], start[at])
-        call(lambda cache, cu: None, max_new=69)
-        for bad in (-1, 10 ** 9, -2 ** 31):
-            def change(cache, cu, bad=bad):
-                cache.page_table[1, 3] = bad
-            call(change)
-
-            def change(cache, cu, bad=bad):
-                cache.demand_table[1, 3] = bad
-            call(change)
-        call(lambda cache, cu: cu.copy_(torch.tensor([0, 20, 10, 95], dtype=torch.int32)), good=(0,))
-        call(lambda cache, cu: cu.copy_(torch.tensor([0, 20, 90, 99], dtype=torch.int32)), good=(0, 1))
-        call(lambda cache, cu: cu.copy_(torch.tensor([-5, 20, 90, 95], dtype=torch.int32)), good=(1, 2))
-        # tokens counted twice: more rows than there is room for
-        cache, q, cu = make([64, 64, 64, 64], [64, 0, 0, 0], 2, 2, 64, 16, dtype, seed=42)
-        cu.copy_(torch.tensor([0, 64, 0, 64, 0], dtype=torch.int32))
-        ws = b.dilution_attn_paged_chunk_workspace(cache, 64, 64, 64)
-        b.dilution_attn_paged_chunk(q, cache, cu, 64, 64, workspace=ws)
+    def call(change, max_new=mid, max_len=200, good=(0, 2)):
+        cache, q, cu = make(lens, news, 4, 2, 64, 16, dtype, seed=41)
+        ro, rD, info = oracle(cache, q, cu)
+        start = cache.demand_pages.clone()
+        change(cache, cu)
+        ws = b.dilution_attn_paged_chunk_workspace(cache, q.shape[0], max_new, max_len)
+        out = torch.full_like(q, 7.0)
+        b.dilution_attn_paged_chunk(q, cache, cu, max_new, max_len, out, workspace=ws)
         assert b.dilution_attn_get_error(ws) == b.DA_ERR_INVALID
+        assert b.dilution_attn_get_error(ws) == b.DA_OK
+        for s in good:
+            r = slice(first[s], first[s + 1])
+            assert np.abs(host64(out)[r] - ro[r]).max() < 0.05
+        return cache, out, start
+
+    def set_cu(*values):
+        return lambda cache, cu: cu.copy_(torch.tensor(values, dtype=torch.int32))
+
+    def set_at(name, at, value):
+        return lambda cache, cu: getattr(cache, name).__setitem__(at, value)
+    a, e, N = (int(x) for x in first[1:])
+    for bad in (-1, 201, 300, mid - 1):      # the last: shorter than its new tokens
+        cache, out, start = call(set_at("seq_lens", 1, bad))
+        assert (out[a:e] == 7.0).all()
+        t = torch.arange(lens[1], device=DEV)
+        at = cache.demand_table[1, t // 16].long(), slice(None), t % 16
+        assert torch.equal(cache.demand_pages[at], start[at])
+    call(lambda cache, cu: None, max_new=mid - 1)
+    for bad in (-1, 10 ** 9, -2 ** 31):
+        call(set_at("page_table", (1, 3), bad))
+        call(set_at("demand_table", (1, 3), bad))
+    call(set_cu(0, a, a - 10, N), good=(0,))
+    call(set_cu(0, a, e, N + 4), good=(0, 1))
+    call(set_cu(-5, a, e, N), good=(1, 2))
+    # tokens counted twice: more rows than there is room for
+    cache, q, cu = make([mid] * 4, [mid, 0, 0, 0], 2, 2, 64, 16, dtype, seed=42)
+    cu.copy_(torch.tensor([0, mid, 0, mid, 0], dtype=torch.int32))
+    ws = b.dilution_attn_paged_chunk_workspace(cache, mid, mid, mid)
+    b.dilution_attn_paged_chunk(q, cache, cu, mid, mid, workspace=ws)
+    assert b.dilution_attn_get_error(ws) == b.DA_ERR_INVALID
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
