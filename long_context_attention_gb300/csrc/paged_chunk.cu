@@ -12,7 +12,7 @@ namespace da {
 
 int launch_chunk_f32(const PagedChunk &p, cudaStream_t stream);
 int launch_chunk_bf16(const PagedChunk &p, cudaStream_t stream);
-int chunk_small_cluster(int S, int Hq, int Hkv, int max_new, int max_len);
+int chunk_small_cluster(int S, int Hq, int Hkv, int max_new, int max_len, int dtype);
 int launch_chunk_small(const PagedChunk &p, int csize, cudaStream_t stream);
 
 // Lengths and new tokens of every sequence, checked once; rows and units before
@@ -40,6 +40,59 @@ __device__ __forceinline__ long long plan_scan(long long v, long long *warp_sum,
   return base + inc - v;
 }
 
+// One sequence, checked: its new tokens, or 0.
+__device__ __forceinline__ ChunkSeq plan_seq(const PagedChunk &p, int s) {
+  const int len = __ldcg(p.c.seq_lens + s), a = __ldcg(p.cu + s), b = __ldcg(p.cu + s + 1), n = b - a;
+  if (len < 0 || len > p.max_len || a < 0 || b < a || b > p.N || n > p.max_new || n > len) {
+    atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
+    return ChunkSeq{0, 0, 0, a};
+  }
+  return ChunkSeq{n > 0 ? len : 0, n, 0, a};
+}
+__device__ __forceinline__ long long plan_units(const PagedChunk &p, const ChunkPlan &w, const ChunkSeq &q) {
+  if (q.n == 0) return 0;
+  ChunkShape g;
+  g.set(q.len, q.n, p.c.Hq, p.c.Hkv, w.edge, w.cost);
+  return g.units * g.segs;
+}
+
+__device__ __forceinline__ void plan_few(const PagedChunk &p, const ChunkPlan &w, ChunkSeq *seq, long long *cum) {
+  const int lane = threadIdx.x, S = p.c.S;
+  if (lane >= 32) return;
+  const long long cap = w.rows / p.c.Hq;
+  ChunkSeq q = lane < S ? plan_seq(p, lane) : ChunkSeq{0, 0, 0, 0};
+  const int n8 = (q.n + 7) & ~7;
+  long long rows = n8;   // at most 32 x 2^30
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, rows, o);
+    if (lane >= o) rows += y;
+  }
+  const long long all = __shfl_sync(0xffffffffu, rows, 31);
+  rows -= n8;
+  q.row0 = (int)(rows < cap ? rows : cap);
+  if (rows + n8 > cap && q.n > 0) {   // cu_tokens counts tokens twice
+    atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
+    q.n = 0;
+    q.row0 = (int)cap;
+  }
+  const long long mine = plan_units(p, w, q);
+  long long units = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, units, o);
+    if (lane >= o) units += y;
+  }
+  if (lane < S) {
+    seq[lane] = q;
+    cum[lane] = units - mine;
+  }
+  if (lane == 31) {
+    seq[S] = ChunkSeq{0, 0, (int)(all < cap ? all : cap), 0};
+    cum[S] = units;
+  }
+}
+
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(PagedChunk p, ChunkPlan w) {
   __shared__ long long warp_sum[kPlanThreads / 32];
   pdl_wait();
@@ -47,18 +100,16 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(PagedChunk p, 
   ChunkSeq *seq = reinterpret_cast<ChunkSeq *>(p.ws + w.seq_off);
   long long *cum = reinterpret_cast<long long *>(p.ws + w.cum_off);
   const int tid = threadIdx.x, S = p.c.S;
+  if (S <= 32) {   // one warp: no block barriers
+    plan_few(p, w, seq, cum);
+    return;
+  }
   const int per = (S + kPlanThreads - 1) / kPlanThreads, s0 = min(tid * per, S), s1 = min(s0 + per, S);
   const long long cap = w.rows / p.c.Hq;
   long long rows = 0, units = 0, total;
   for (int s = s0; s < s1; ++s) {
-    const int len = __ldcg(p.c.seq_lens + s), a = __ldcg(p.cu + s), b = __ldcg(p.cu + s + 1);
-    int n = b - a;
-    if (len < 0 || len > p.max_len || a < 0 || b < a || b > p.N || n > p.max_new || n > len) {
-      atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
-      n = 0;
-    }
-    seq[s] = ChunkSeq{n > 0 ? len : 0, n, 0, a};
-    rows += (n + 7) & ~7;
+    seq[s] = plan_seq(p, s);
+    rows += (seq[s].n + 7) & ~7;
   }
   rows = plan_scan(rows, warp_sum, total);
   if (tid == 0) seq[S] = ChunkSeq{0, 0, (int)(total < cap ? total : cap), 0};
@@ -73,22 +124,14 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(PagedChunk p, 
     }
     rows += n8;
     seq[s] = q;
-    if (q.n > 0) {
-      ChunkShape g;
-      g.set(q.len, q.n, p.c.Hq, p.c.Hkv, w.edge, w.cost);
-      units += g.units * g.segs;
-    }
+    units += plan_units(p, w, q);
   }
   units = plan_scan(units, warp_sum, total);
   if (tid == 0) cum[S] = total;
   for (int s = s0; s < s1; ++s) {
     const ChunkSeq q = seq[s];
     cum[s] = units;
-    if (q.n > 0) {
-      ChunkShape g;
-      g.set(q.len, q.n, p.c.Hq, p.c.Hkv, w.edge, w.cost);
-      units += g.units * g.segs;
-    }
+    units += plan_units(p, w, q);
   }
 }
 
@@ -226,7 +269,7 @@ static int row_blocks(long long rows) {
 }
 
 cudaError_t launch_chunk_plan(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream) {
-  return launch_after(chunk_plan_kernel, 1, kPlanThreads, 0, stream, p, w);
+  return launch_after(chunk_plan_kernel, 1, p.c.S <= 32 ? 32 : kPlanThreads, 0, stream, p, w);
 }
 cudaError_t launch_chunk_join(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream) {
   return launch_after(chunk_join, row_blocks(w.rows), 32 * kRowWarps, 0, stream, p, w, row_run(w.rows));
@@ -250,9 +293,9 @@ size_t chunk_workspace(int S, int Hq, int Hkv, int d, long long N, int max_new, 
 }
 
 int launch_paged_chunk(const PagedChunk &p, cudaStream_t stream) {
-  if (p.c.dtype == DA_F32) return launch_chunk_f32(p, stream);
-  const int c = chunk_small_cluster(p.c.S, p.c.Hq, p.c.Hkv, p.max_new, p.max_len);
-  return c > 0 ? launch_chunk_small(p, c, stream) : launch_chunk_bf16(p, stream);
+  const int c = chunk_small_cluster(p.c.S, p.c.Hq, p.c.Hkv, p.max_new, p.max_len, p.c.dtype);
+  if (c > 0) return launch_chunk_small(p, c, stream);
+  return p.c.dtype == DA_F32 ? launch_chunk_f32(p, stream) : launch_chunk_bf16(p, stream);
 }
 
 }  // namespace da

@@ -190,9 +190,9 @@ __global__ void __launch_bounds__(CkxKeys<D>::kThreads, 2)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  pdl_wait();
-  pdl_launch_dependents();
   if (tid == 0) {
+    prefetch_tmap(&qmap);
+    prefetch_tmap(&kmap);
     for (int i = 0; i < kCkxRing; ++i) {
       mbar_init(&r_full[i], 1);
       mbar_init(&r_free[i], 9);   // 8 reduction warps and the issuer
@@ -221,6 +221,8 @@ __global__ void __launch_bounds__(CkxKeys<D>::kThreads, 2)
   }
   __syncthreads();
   tc_fence_after();
+  pdl_wait();   // nothing before touches memory
+  pdl_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{abort_flag, p.status};
   if (warp == 8) {
@@ -494,9 +496,8 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
   constexpr int kG = C::kG;
   extern __shared__ __align__(1024) uint8_t ckx_smem_raw[];
   uint8_t *smem = ckx_smem_raw;
-  pdl_wait();
-  pdl_launch_dependents();
   if (smem_u32(ckx_smem_raw) & 1023u) {   // no room to align it: refuse rather than compute with misaligned operands
+    pdl_wait();
     if (threadIdx.x == 0) atomicCAS(p.status, DA_OK, DA_ERR_UNSUPPORTED);
     return;
   }
@@ -512,6 +513,9 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, wg = warp / 4;
   constexpr int kWarpCtl = (kG + 1) * 4;
   if (tid == 0) {
+    prefetch_tmap(&qmap);
+    prefetch_tmap(&kmap);
+    prefetch_tmap(&vmap);
     for (int i = 0; i < kCkxRing; ++i) {
       mbar_init(&r_full[i], 1);
       mbar_init(&r_free[i], kG + 4 + 4 * kG);   // issuers, epilogue and demand warps
@@ -550,6 +554,8 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
   }
   __syncthreads();
   tc_fence_after();
+  pdl_wait();   // nothing before touches memory
+  pdl_launch_dependents();
   const uint32_t tmem = *tmem_slot;
   const WaitCtx wc{abort_flag, p.status};
 
