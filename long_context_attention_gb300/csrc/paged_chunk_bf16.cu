@@ -444,9 +444,16 @@ __device__ __forceinline__ uint32_t ckx_nl_place(int i, int b) {
   return (uint32_t)((i >> 1) * 128 + (((2 + 2 * (b & 1) + (i & 1)) ^ ((i >> 1) & 7)) << 4));
 }
 // The same for constant i: bases[m] = block + ((2 + 2 (b & 1)) ^ 2 m) 16.
-__device__ __forceinline__ float4 ckx_nl(const uint8_t *const (&bases)[4], int i, int off) {
+__device__ __forceinline__ float4 ckx_nl(const uint32_t (&bases)[4], int i) {
   const int row = i >> 1;
-  return *reinterpret_cast<const float4 *>(bases[(row & 7) >> 1] + off + row * 128 + (((i ^ row) & 1) << 4));
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(bases[(row & 7) >> 1] + (uint32_t)(row * 128 + (((i ^ row) & 1) << 4))));
+  return v;
+}
+__device__ __forceinline__ void ckx_put(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 // 32 rows of one key (its logits; -infinity where a row does not see it): bids, then
@@ -454,37 +461,46 @@ __device__ __forceinline__ float4 ckx_nl(const uint8_t *const (&bases)[4], int i
 // far, a sum of its own (a total of 1 would lose half of the bits of bids of 10^-5);
 // base: the total before them, and eps.  One reciprocal serves two rows,
 // 1 / (d0 d1), with d >= eps >= 1e-18.
+// They go to the key's row of the warpgroup's shares: `to`, the places of its 16-byte
+// pieces 0 .. 3 (of the first 32 rows of 64; of the second 64 bytes on or back).
 template <int CHUNK, bool EARLIER>
-__device__ __forceinline__ void ckx_shares(const float (&x)[32], float c2, const uint8_t *const (&nl)[4], int off, float base, float &added,
-                                           uint32_t (&pk)[16]) {
-  const float2 c2v = make_float2(c2, c2), b2 = make_float2(base, base);
-  float p[32], d[32];
+__device__ __forceinline__ void ckx_bids(float (&x)[32], float c2, const uint32_t (&nl)[4]) {
+  const float2 c2v = make_float2(c2, c2);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float4 n4 = ckx_nl(nl, 8 * CHUNK + i, off);
+    const float4 n4 = ckx_nl(nl, 8 * CHUNK + i);
     const float2 x0 = ffma2(make_float2(x[4 * i], x[4 * i + 1]), c2v, make_float2(n4.x, n4.y));
     const float2 x1 = ffma2(make_float2(x[4 * i + 2], x[4 * i + 3]), c2v, make_float2(n4.z, n4.w));
-    p[4 * i] = ex2_approx(x0.x);
-    p[4 * i + 1] = ex2_approx(x0.y);
-    p[4 * i + 2] = ex2_approx(x1.x);
-    p[4 * i + 3] = ex2_approx(x1.y);
+    x[4 * i] = ex2_approx(x0.x);
+    x[4 * i + 1] = ex2_approx(x0.y);
+    x[4 * i + 2] = ex2_approx(x1.x);
+    x[4 * i + 3] = ex2_approx(x1.y);
   }
+}
+template <int CHUNK, bool EARLIER>
+__device__ __forceinline__ void ckx_shares(const float (&p)[32], float2 base, float &added, const uint32_t (&to)[4]) {
 #pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    if (EARLIER) {
-      d[c] = added;
-      added += p[c];
-    } else {
-      added += p[c];
-      d[c] = added;
+  for (int q = 0; q < 4; ++q) {   // 8 rows
+    float d[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (EARLIER) {
+        d[c] = added;
+        added += p[8 * q + c];
+      } else {
+        added += p[8 * q + c];
+        d[c] = added;
+      }
     }
-  }
+    uint32_t pk[4];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float2 dd = fadd2(make_float2(d[2 * i + 1], d[2 * i]), b2);   // (swapped: each share takes the other's)
-    const float r = rcp_approx(dd.x * dd.y);
-    const float2 sh = fmul2(fmul2(make_float2(p[2 * i], p[2 * i + 1]), dd), make_float2(r, r));
-    pk[i] = pack_bf16x2(sh.x, sh.y);
+    for (int i = 0; i < 4; ++i) {
+      const float2 dd = fadd2(make_float2(d[2 * i + 1], d[2 * i]), base);   // (swapped: each share takes the other's)
+      const float r = rcp_approx(dd.x * dd.y);
+      const float2 sh = fmul2(fmul2(make_float2(p[8 * q + 2 * i], p[8 * q + 2 * i + 1]), dd), make_float2(r, r));
+      pk[i] = pack_bf16x2(sh.x, sh.y);
+    }
+    ckx_put(CHUNK == 0 ? to[q] : to[q] ^ 64u, pk[0], pk[1], pk[2], pk[3]);
   }
 }
 
@@ -793,120 +809,132 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
     ckx_regs_inc<C::kRegsDemand>();
     const int g = wg, quarter = warp % 4, key_l = quarter * 32 + lane, swz = key_l & 7;   // key of the tile
     const uint32_t ts = tmem + g * 128 + ((uint32_t)(quarter * 32) << 16);
-    uint8_t *sh_row = sSh + g * C::kShBytes + (key_l / 8) * 1024 + (key_l % 8) * 128;
+    // this key's row of the warpgroup's shares: 64-row blocks 16 KB apart, pieces swizzled by the key
+    const uint32_t sh_row = smem_u32(sSh) + g * C::kShBytes + (key_l / 8) * 1024 + (key_l % 8) * 128;
     const int sh = w.page_shift, ps = 1 << sh;
+    const size_t page_totals = (size_t)p.c.Hq << sh;
     int m = 0;   // the warpgroup's tiles so far
-    // 32 shares of chunk c of the rows: 64-row block c / 2, pieces (c % 2) 4 .. of this key's row
-    auto store = [&](const uint32_t (&pk)[16], int c) {
-      uint8_t *dst = sh_row + (c >> 1) * 16384;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4 *>(dst + ((((c & 1) * 4 + i) ^ swz) << 4)) =
-            make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-    };
     for (int i = 0;; ++i) {
       if (!warp_wait(&r_full[i % kCkxRing], (i / kCkxRing) & 1, wc)) break;
       const CkxTile &x = ring[i % kCkxRing];
-      if (x.rows == 0) break;
+      const int rows = x.rows, end = x.end, len = x.len, n8 = x.n8;
+      if (rows == 0) break;
       bool ok = true;
-      const uint8_t *nl[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) nl[e] = smem + C::kOffOnes + (((2 + 2 * (i & 1)) ^ (2 * e)) << 4);
-      // the page of this thread's key in tile j, for the totals; -1: none
+      const uint32_t ones = smem_u32(smem + C::kOffOnes);
+      // the page of this thread's key in tile j, for the totals (-1: none), and its place
+      const int32_t *const table = p.c.demand_table + (size_t)x.s * p.c.max_pages;
+      float *const pool = p.c.demand_pages + ((size_t)x.hq0 << sh);   // of query head hq0
       auto page_of = [&](int j) {
         const int key = j * kCkxEdge + key_l;
-        return key < x.len ? __ldcg(p.c.demand_table + (size_t)x.s * p.c.max_pages + (key >> sh)) : -1;
+        return key < len ? __ldcg(table + (key >> sh)) : -1;
       };
-      auto total_at = [&](int page, int j) -> float * {   // of query head hq0
+      auto total_at = [&](int page, int j) -> float * {
         const int key = j * kCkxEdge + key_l;
-        if ((unsigned)page < (unsigned)p.c.num_demand_pages)
-          return p.c.demand_pages + ((((size_t)page * p.c.Hq + x.hq0) << sh) + (key & (ps - 1)));
-        if (key < x.len) atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
+        if ((unsigned)page < (unsigned)p.c.num_demand_pages) return pool + page * page_totals + (key & (ps - 1));
+        if (key < len) atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
         return nullptr;
       };
-      int j = x.tile + g;
-      float *at = j < x.end ? total_at(page_of(j), j) : nullptr;
-      float total = at != nullptr ? __ldcg(at) : 0.f;
-      for (; j < x.end; j += kG, ++m) {
-        const int next_page = j + kG < x.end ? page_of(j + kG) : -1;
-        const int key = j * kCkxEdge + key_l;
-        float *next_at = nullptr;
-        float next_total = 0.f;
-        ok = warp_wait(&s_full[g], m & 1, wc);
-        if (!ok) break;
+      // The tile's S, and in a sequence's last tile zeros in the rows of V past its end,
+      // which may hold anything: 0 times that is not 0.
+      auto tile_ready = [&](int j) {
+        if (!warp_wait(&s_full[g], m & 1, wc)) return false;
         tc_fence_after();
-        if ((j + 1) * kCkxEdge > x.len) {
-          // rows of V past the sequence's end may hold anything, and 0 times that is not 0
+        if ((j + 1) * kCkxEdge > len) {
           const int t = x.t0 + (j - x.tile), st = t % C::kStages;
-          ok = warp_wait(&v_full[t % C::kFull], (t / C::kFull) & 1, wc);
-          if (!ok) break;
-          if (key >= x.len) {
+          if (!warp_wait(&v_full[t % C::kFull], (t / C::kFull) & 1, wc)) return false;
+          if (j * kCkxEdge + key_l >= len) {
 #pragma unroll
             for (int e = 0; e < D / 8; ++e)
               *reinterpret_cast<uint4 *>(sV + st * C::kTB + (e >> 3) * kCkxHalf + key_l * 128 + ((e & 7) << 4)) =
                   make_uint4(0u, 0u, 0u, 0u);
           }
         }
-        if (x.n8 == 0) {
-          // one head: 32 rows at a time, the load of the next ones in flight meanwhile
-          const int rows = x.rows, first = x.P + x.i0;   // place of row 0
-          const int lo = key < x.len ? min(max(key - first, 0), rows) : rows, hi = rows;   // rows that see the key
-          const bool mask = (j + 1) * kCkxEdge - 1 > first || rows < kCkxEdge;
-          const float c2 = x.c2;
-          const float base = total + p.eps;
-          float added = 0.f;
-          auto hide = [&](float (&v)[32], int c) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if ((unsigned)(32 * c + e - lo) >= (unsigned)(hi - lo)) v[e] = -INFINITY;
-          };
-          if (j + kG < x.end) {
+        return true;
+      };
+      int j = x.tile + g;
+      float *at = j < end ? total_at(page_of(j), j) : nullptr;
+      float total = at != nullptr ? __ldcg(at) : 0.f;
+      if (n8 == 0) {
+        // one head
+        const int first = x.P + x.i0;   // place of row 0
+        const float c2 = x.c2;
+        for (; j < end; j += kG, ++m) {
+          const int next_page = j + kG < end ? page_of(j + kG) : -1;
+          float *next_at = nullptr;
+          float next_total = 0.f;
+          ok = tile_ready(j);
+          if (!ok) break;
+          if (j + kG < end) {
             next_at = total_at(next_page, j + kG);
             if (next_at != nullptr) next_total = __ldcg(next_at);
           }
+          const bool mask = (j + 1) * kCkxEdge - 1 > first || rows < kCkxEdge;
+          const float2 base = make_float2(total + p.eps, total + p.eps);
+          float added = 0.f;
+          uint32_t nl[4], to[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) nl[e] = ones + (((2 + 2 * (i & 1)) ^ (2 * e)) << 4), to[e] = sh_row + ((e ^ swz) << 4);
           // 64 rows at a time; not unrolled: the code of all 128 misses the instruction cache
           const int halves = rows > 64 ? 2 : 1;
 #pragma unroll 1
           for (int half = 0; half < halves; ++half) {
             float a[32], b[32];
-            uint32_t pk[16];
             tmem_ld32(ts + 64 * half, a);
             tmem_ld32(ts + 64 * half + 32, b);
             tmem_wait_ld_r(a);
             tmem_wait_ld_r(b);
             if (half + 1 == halves) ckx_release(&s_free[g], lane);   // the next tile's S while these rows are formed
-            if (mask) {
-              hide(a, 2 * half);
-              hide(b, 2 * half + 1);
+            if (mask) {   // rows lo .. rows - 1 see the key
+              const int key = j * kCkxEdge + key_l;
+              const int lo = (key < len ? min(max(key - first, 0), rows) : rows) - 64 * half, n = rows - 64 * half - lo;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                if ((unsigned)(e - lo) >= (unsigned)n) a[e] = -INFINITY;
+                if ((unsigned)(32 + e - lo) >= (unsigned)n) b[e] = -INFINITY;
+              }
             }
-            ckx_shares<0, EARLIER>(a, c2, nl, half * 1024, base, added, pk);
+            ckx_bids<0, EARLIER>(a, c2, nl);
             if (half == 0) {   // the product of the tile before has read the shares
               ok = warp_wait(&sh_free[g], (m & 1) ^ 1, wc);
               if (!ok) break;
             }
-            store(pk, 2 * half);
-            ckx_shares<1, EARLIER>(b, c2, nl, half * 1024, base, added, pk);
-            store(pk, 2 * half + 1);
+            ckx_shares<0, EARLIER>(a, base, added, to);
+            ckx_bids<1, EARLIER>(b, c2, nl);
+            ckx_shares<1, EARLIER>(b, base, added, to);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) nl[e] += 1024, to[e] += 16384;
           }
           if (!ok) break;
           if (at != nullptr) __stcg(at, total + added);
-        } else {
-          // several heads of n8 rows: 8 rows at a time, a head's total from its first rows to its last
-          const int groups = x.rows / 8, per = x.n8 / 8;
-          const int lo = key < x.len ? max(key - x.P, 0) : x.n, hi = x.n;   // queries that see the key
-          if (j + kG < x.end) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh_full[g]);
+          at = next_at;
+          total = next_total;
+        }
+      } else {
+        // several heads of n8 rows: 8 rows at a time, a head's total from its first rows to its last
+        const int groups = rows / 8, per = n8 / 8, n = x.n, P = x.P, head0 = x.s * p.c.Hq + x.hq0;
+        for (; j < end; j += kG, ++m) {
+          const int next_page = j + kG < end ? page_of(j + kG) : -1;
+          float *next_at = nullptr;
+          float next_total = 0.f;
+          ok = tile_ready(j);
+          if (!ok) break;
+          if (j + kG < end) {
             next_at = total_at(next_page, j + kG);
             if (next_at != nullptr) next_total = __ldcg(next_at);
           }
+          const int key = j * kCkxEdge + key_l;
+          const int lo = key < len ? max(key - P, 0) : n;   // queries lo .. n - 1 see the key
           float *head_at = at;
-          float head_next = 0.f, added = 0.f;
-          float c2 = 0.f;
+          float head_next = 0.f, added = 0.f, c2 = 0.f;
           int q = 0;   // query of the group's first row
           float v[8];
           tmem_ld8(ts, v);
           for (int u = 0, h = 0; u < groups; ++u) {
             if (q == 0) {
-              c2 = fmaxf(head_c2(p.hs, x.s * p.c.Hq + x.hq0 + h, nullptr), 1e-30f);
+              c2 = fmaxf(head_c2(p.hs, head0 + h, nullptr), 1e-30f);
               if (u + per < groups && head_at != nullptr) head_next = __ldcg(head_at + ps);
             }
             float nlv[8];
@@ -918,8 +946,8 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
               const float2 y = ffma2(make_float2(v[e], v[e + 1]), make_float2(c2, c2), make_float2(nlv[e], nlv[e + 1]));
-              bid[e] = (unsigned)(q + e - lo) < (unsigned)(hi - lo) ? ex2_approx(y.x) : 0.f;
-              bid[e + 1] = (unsigned)(q + e + 1 - lo) < (unsigned)(hi - lo) ? ex2_approx(y.y) : 0.f;
+              bid[e] = (unsigned)(q + e - lo) < (unsigned)(n - lo) ? ex2_approx(y.x) : 0.f;
+              bid[e + 1] = (unsigned)(q + e + 1 - lo) < (unsigned)(n - lo) ? ex2_approx(y.y) : 0.f;
             }
             if (u + 1 < groups)
               tmem_ld8(ts + 8 * (u + 1), v);
@@ -944,10 +972,9 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
               ok = warp_wait(&sh_free[g], (m & 1) ^ 1, wc);
               if (!ok) break;
             }
-            *reinterpret_cast<uint4 *>(sh_row + (u >> 3) * 16384 + (((u & 7) ^ swz) << 4)) =
-                make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            ckx_put(sh_row + (u >> 3) * 16384 + (((u & 7) ^ swz) << 4), pk[0], pk[1], pk[2], pk[3]);
             q += 8;
-            if (q == x.n8) {   // the head's last rows
+            if (q == n8) {   // the head's last rows
               q = 0;
               ++h;
               if (head_at != nullptr) {
@@ -959,12 +986,12 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
             }
           }
           if (!ok) break;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh_full[g]);
+          at = next_at;
+          total = next_total;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh_full[g]);
-        at = next_at;
-        total = next_total;
       }
       if (!ok) break;
       __syncwarp();
