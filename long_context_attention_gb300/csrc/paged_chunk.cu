@@ -2,8 +2,9 @@
 // the call's work on its line, chunk_join makes each row's normaliser of the first
 // pass's pieces, chunk_combine its output of the second's.
 //
-// What bounds them: latency.  The plan is one block; the other two read a few
-// pieces a row, (max, sum) and d + 1 floats each.
+// What bounds them: latency; the plan is one block, and the other two read a few
+// pieces a row, (max, sum) and d + 1 floats each.  Over many rows chunk_combine comes to
+// 5 TB/s (16 prompts of d = 128: 550 MB in 110 us).
 #include "da_chunk.cuh"
 
 #include <cuda_bf16.h>
@@ -136,6 +137,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(PagedChunk p, 
 }
 
 constexpr int kRowWarps = 8;   // of a block
+constexpr int kJoinCtas = 4, kCombineCtas = 2;   // blocks an SM (three of the second would not hold a row group's loads: 145 us for 110)
 
 // A warp's rows: `run` times eight in succession, found once for each column tile.
 template <typename F>
@@ -160,7 +162,7 @@ __device__ __forceinline__ void row_groups(const PagedChunk &p, const ChunkPlan 
 
 // -lse2 of every row, from (max, sum) of its pieces: a lane takes a row's every
 // fourth piece.
-__global__ void __launch_bounds__(32 * kRowWarps) chunk_join(PagedChunk p, ChunkPlan w, int run) {
+__global__ void __launch_bounds__(32 * kRowWarps, kJoinCtas) chunk_join(PagedChunk p, ChunkPlan w, int run) {
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x % 32, r = lane % 8, part = lane / 8;
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) chunk_join(PagedChunk p, Chunk
 
 // out = numerators / shares, summed over the pieces in the line's order.
 template <int D, typename E>
-__global__ void __launch_bounds__(32 * kRowWarps) chunk_combine(PagedChunk p, ChunkPlan w, int run) {
+__global__ void __launch_bounds__(32 * kRowWarps, kCombineCtas) chunk_combine(PagedChunk p, ChunkPlan w, int run) {
   constexpr int COLS = D / 4, PER = 8 * COLS / 32;   // float4 columns of a row; of a lane
   pdl_wait();
   pdl_launch_dependents();
@@ -247,24 +249,33 @@ __global__ void __launch_bounds__(32 * kRowWarps) chunk_combine(PagedChunk p, Ch
       const int q = lane + 32 * e, r = q / COLS;
       const float d = __shfl_sync(0xffffffffu, sum, r);
       if (r >= left) continue;
+      float4 v = a[e];
+      if (d >= 0x1p-100f && d <= 0x1p100f) {   // its reciprocal is normal, and one division does for four
+        const float inv = 1.f / d;
+        v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+      } else {
+        v.x /= d, v.y /= d, v.z /= d, v.w /= d;
+      }
       const size_t to = ((size_t)(x.q.tok0 + x.i + r) * p.c.Hq + x.hq) * D + 4 * (q % COLS);
       if constexpr (sizeof(E) == 4)
         *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + to) =
-            make_float4(a[e].x / d, a[e].y / d, a[e].z / d, a[e].w / d);
+            v;
       else
         *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + to) =
-            make_uint2(pack_bf16x2(a[e].x / d, a[e].y / d), pack_bf16x2(a[e].z / d, a[e].w / d));
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     }
   });
 }
 
-// Eight rows a warp where there are few, up to 64 where the GPU is full.
-static int row_run(long long rows) {
-  const long long run = rows / (8ll * 152 * 32);
-  return (int)(run < 1 ? 1 : run > 8 ? 8 : run);
+// Eight rows a warp where there are few, and where there are many up to 32 (16 prompts of
+// d = 128, 325,000 rows: combine 122, 112, 110, 124 us at 8, 16, 32 and 64, join 59, 43, 39,
+// 48: a few rows find their segment again and again, many leave some warps far behind).
+static int row_run(long long rows, int ctas) {
+  const long long fill = 8ll * kRowWarps * 152 * ctas, run = (rows + fill - 1) / fill;
+  return (int)(run < 1 ? 1 : run > 4 ? 4 : run);
 }
-static int row_blocks(long long rows) {
-  const long long each = 8ll * kRowWarps * row_run(rows), n = (rows + each - 1) / each, most = 152 * 8;
+static int row_blocks(long long rows, int ctas) {
+  const long long each = 8ll * kRowWarps * row_run(rows, ctas), n = (rows + each - 1) / each, most = 152 * 64;
   return (int)(n < 1 ? 1 : n < most ? n : most);
 }
 
@@ -272,12 +283,12 @@ cudaError_t launch_chunk_plan(const PagedChunk &p, const ChunkPlan &w, cudaStrea
   return launch_after(chunk_plan_kernel, 1, p.c.S <= 32 ? 32 : kPlanThreads, 0, stream, p, w);
 }
 cudaError_t launch_chunk_join(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream) {
-  return launch_after(chunk_join, row_blocks(w.rows), 32 * kRowWarps, 0, stream, p, w, row_run(w.rows));
+  return launch_after(chunk_join, row_blocks(w.rows, kJoinCtas), 32 * kRowWarps, 0, stream, p, w, row_run(w.rows, kJoinCtas));
 }
 template <typename E>
 static cudaError_t launch_combine_t(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream) {
-  return p.c.d == 128 ? launch_after(chunk_combine<128, E>, row_blocks(w.rows), 32 * kRowWarps, 0, stream, p, w, row_run(w.rows))
-                      : launch_after(chunk_combine<64, E>, row_blocks(w.rows), 32 * kRowWarps, 0, stream, p, w, row_run(w.rows));
+  return p.c.d == 128 ? launch_after(chunk_combine<128, E>, row_blocks(w.rows, kCombineCtas), 32 * kRowWarps, 0, stream, p, w, row_run(w.rows, kCombineCtas))
+                      : launch_after(chunk_combine<64, E>, row_blocks(w.rows, kCombineCtas), 32 * kRowWarps, 0, stream, p, w, row_run(w.rows, kCombineCtas));
 }
 cudaError_t launch_chunk_combine(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream) {
   return p.c.dtype == DA_F32 ? launch_combine_t<float>(p, w, stream) : launch_combine_t<__nv_bfloat16>(p, w, stream);

@@ -13,7 +13,8 @@
 // by a dozen rows.  A tile is 64 rows by 64 keys, 256 threads with 4 x 4 products
 // each, 8 reads of 16 bytes for 32 packed multiply-adds; warps without rows leave the
 // products out.  K and V have a place each, filled by asynchronous copies as soon as
-// the tile before has been read.  A key's total runs over the rows of a tile: four
+// the tile before has been read (rings of three to six places, one barrier a tile: as
+// long, and 5 us more a call to fill).  A key's total runs over the rows of a tile: four
 // threads a key take 16 rows each, after they have exchanged the sums of their bids
 // (one thread a key left 3/4 of the block idle).
 #include "da_chunk.cuh"
@@ -121,12 +122,16 @@ __device__ __forceinline__ float *ckf_total(const PagedChunk &p, const ChunkPlan
 // A thread's part of a tile.  Many rows: 4 rows (4 ty ..) by 4 keys (tx + 16 j).  Up to
 // 16 rows: 4 rows (4 (ty % 4) ..) by one key (16 (ty / 4) + tx), so that all warps work
 // (as many rows: 64 keys by 8 rows in one warp, 223 us for 4 sequences of 1001 .. 8001).
+// Neighbouring lanes have the same key and two groups of rows: half a warp's 16-byte reads
+// of K then fall on 8 places, once over the banks (16 keys a half-warp: twice).
 template <bool FEW>
 struct CkfPart {
   static constexpr int kKeys = FEW ? 1 : 4;
   int row, key;   // its first row and key
+  int tx;         // 0 .. 15
   __device__ __forceinline__ CkfPart() {
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int ty = threadIdx.x / 32 * 2 + threadIdx.x % 2;
+    tx = threadIdx.x % 32 / 2;
     row = FEW ? 4 * (ty % 4) : 4 * ty;
     key = FEW ? 16 * (ty / 4) + tx : tx;
   }
@@ -195,7 +200,7 @@ __device__ __forceinline__ void ckf_keys_tile(const PagedChunk &p, const ChunkPl
   float *sQ = smem, *sK = sQ + kCkfEdge * C::kLd;   // two key tiles
   float2 *s_ml = reinterpret_cast<float2 *>(smem + 3 * kCkfEdge * C::kLd);
   const CkfPart<FEW> part;
-  const int tx = threadIdx.x % 16, kg = threadIdx.x / 64;
+  const int tx = part.tx, kg = threadIdx.x / 64;
   const bool work = FEW || threadIdx.x / 32 * 8 < t.rows;   // uniform over the warp
   CkfPages<D> pages;
   pages.find(p, w, k, k.tile);
@@ -239,7 +244,7 @@ __device__ __forceinline__ void ckf_keys_tile(const PagedChunk &p, const ChunkPl
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1)
+    for (int o = 16; o > 1; o >>= 1)
       ckf_merge(m[r], sum[r], __shfl_xor_sync(0xffffffffu, m[r], o), __shfl_xor_sync(0xffffffffu, sum[r], o));
   auto put = [&](int row, float2 ml) {
     *reinterpret_cast<float2 *>(chunk_place(p, w.ml_a, w.ml_b, k.row0(p, w), w.cta_rows, k.tile, blockIdx.x, t.r0 + row, 2)) = ml;
@@ -297,8 +302,8 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
   constexpr int NV = D / 64, NK = CkfPart<FEW>::kKeys;   // 4-column groups, keys of a thread
   float *sQ = smem, *sK = sQ + kCkfEdge * C::kLd, *sV = sK + kCkfEdge * C::kLd, *sP = sV + kCkfEdge * C::kLd,
         *sPart = sP + kCkfEdge * C::kLdP;
-  const int tid = threadIdx.x, tx = tid % 16;
   const CkfPart<FEW> part;
+  const int tid = threadIdx.x, tx = part.tx;
   const bool work = FEW || tid / 32 * 8 < t.rows;   // uniform over the warp
   const int j0 = FEW ? tid / 64 * 16 : 0, j1 = FEW ? j0 + 16 : kCkfEdge;   // keys of the thread's value products
   CkfPages<D> pages;
@@ -411,7 +416,7 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
 #pragma unroll
   for (int r = 0; r < 4; ++r)
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], o);
+    for (int o = 16; o > 1; o >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], o);
   float *to = chunk_place(p, w.acc_a, w.acc_b, k.row0(p, w), w.cta_rows, k.tile, blockIdx.x, t.r0, acc_stride(D));
   if constexpr (FEW) {   // the four fourths of the keys, in order
     constexpr int LD = D + 4;
