@@ -450,7 +450,7 @@ int dilution_attn_paged_decode_ex(const void *q, const dilution_attn_paged_cache
  * dilution_attn_paged_append; rows of q from cu_tokens[S] on are padding: not read,
  * and their rows of out not written.  A sequence without new tokens is left as it is.
  * max_new, max_len: host upper bounds of the sequences' new tokens and of seq_lens
- * (max_len at most max_pages * page_size).  A sequence with more new tokens than
+ * (max_len at most max_pages * page_size and 2^30).  A sequence with more new tokens than
  * max_new or than its length, a length outside 0 .. max_len, cu_tokens that decrease
  * or pass N record DA_ERR_INVALID; such a sequence's rows of out are not written and
  * its demand stays.  A page id outside the pool records it too, and the sequence's
@@ -486,7 +486,7 @@ int dilution_attn_paged_chunk(const void *q, const dilution_attn_paged_cache *ca
  *       keep their contents as far as every key head keeps all their tokens (a
  *       shared prefix of `sinks` tokens).
  *   keep: DEVICE [S] int32.  max_keep, max_len: host upper bounds of m and of
- *       seq_lens (max_len at most max_pages * page_size).
+ *       seq_lens (max_len at most max_pages * page_size and 2^30).
  *   new_lens: DEVICE [S] int32, receives m; may be cache->seq_lens itself.
  *   kept: nullable DEVICE [S][Hkv][max_keep] int32, receives the places that the
  *       rows had, then -1.

@@ -335,7 +335,9 @@ int dilution_attn_paged_decode_ex(const void *q, const dilution_attn_paged_cache
 
 size_t dilution_attn_paged_chunk_workspace_size(int S, int Hq, int Hkv, int d, int N, int max_new, int max_len, int dtype) {
   if (dtype != DA_F32 && dtype != DA_BF16) return 0;
-  if (S < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || N < 0 || max_new < 0 || max_len < 0 || !head_dim_supported(d)) return 0;
+  if (S < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || N < 0 || max_new < 0 || max_len < 0 || max_len > kMaxTokens ||
+      !head_dim_supported(d))
+    return 0;
   return chunk_workspace(S, Hq, Hkv, d, N, chunk_most(N, max_new, max_len), dtype);
 }
 
@@ -348,7 +350,8 @@ int dilution_attn_paged_chunk(const void *q, const dilution_attn_paged_cache *ca
   st = check_options(tau, tau_bh, eps, flags, c.dtype);
   if (st != DA_OK) return st;
   if (N < 0 || max_new < 0 || max_len < 0 || (int64_t)max_len > (int64_t)c.max_pages * c.page_size) return DA_ERR_INVALID;
-  if (N > kMaxTokens || (int64_t)c.num_pages * c.Hkv > 0x7FFFFFFF) return DA_ERR_UNSUPPORTED;   // (a copy's coordinate)
+  if (N > kMaxTokens || max_len > kMaxTokens || (int64_t)c.num_pages * c.Hkv > 0x7FFFFFFF)   // (a copy's coordinate)
+    return DA_ERR_UNSUPPORTED;
   if (N == 0 || c.S == 0) return DA_OK;
   if (q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 16)) return DA_ERR_INVALID;
   if (cu_tokens == nullptr || !aligned(cu_tokens, 4)) return DA_ERR_INVALID;
@@ -373,7 +376,7 @@ int dilution_attn_paged_chunk(const void *q, const dilution_attn_paged_cache *ca
 }
 
 size_t dilution_attn_paged_evict_workspace_size(int S, int Hkv, int max_keep, int max_len) {
-  if (S < 0 || Hkv < 1 || max_keep < 0 || max_len < 0) return 0;
+  if (S < 0 || Hkv < 1 || max_keep < 0 || max_len < 0 || max_len > kMaxTokens) return 0;
   return evict_workspace(S, Hkv, max_keep < max_len ? max_keep : max_len, max_len).total;
 }
 
@@ -390,6 +393,7 @@ int dilution_attn_paged_evict(const dilution_attn_paged_cache *cache, const int3
   if ((dst_page_table == nullptr) != (dst_demand_table == nullptr) || !aligned(dst_page_table, 4) ||
       !aligned(dst_demand_table, 4))
     return DA_ERR_INVALID;
+  if (max_len > kMaxTokens) return DA_ERR_UNSUPPORTED;
   if (kept == nullptr && max_keep > max_len) max_keep = max_len;   // (kept's rows hold max_keep)
   const int most = max_keep < max_len ? max_keep : max_len;
   if (dst_page_table != nullptr && (dst_max_pages < 0 || (int64_t)dst_max_pages * c.page_size < most)) return DA_ERR_INVALID;

@@ -33,7 +33,7 @@ def test_chunk_refusals(lib):
                dict(c=cache(pages=-1)), dict(c=cache(page=0))):
         assert call(**kw) == b.DA_ERR_INVALID, kw
     for kw in (dict(eps=1e-19), dict(N=(1 << 30) + 1), dict(c=cache(d=96)), dict(c=cache(page=8)), dict(c=cache(page=24)),
-               dict(c=cache(pages=1 << 30, Hkv=2)), dict(c=cache(S=1 << 23))):
+               dict(c=cache(pages=1 << 30, Hkv=2)), dict(c=cache(S=1 << 23)), dict(c=cache(width=1 << 27), max_len=(1 << 30) + 1)):
         assert call(**kw) == b.DA_ERR_UNSUPPORTED, kw
     assert lib.dilution_attn_paged_chunk(FAKE, None, FAKE, 5, 5, 5, FAKE, 1.0, None, 1e-6, 0, FAKE, BIG, None, None) == \
         b.DA_ERR_INVALID
@@ -48,7 +48,8 @@ def test_chunk_refusals(lib):
 def test_chunk_workspace_size(lib):
     size = b.dilution_attn_paged_chunk_workspace_size
     for bad in ((-1, 4, 2, 64, 5, 5, 9, 1), (2, 0, 2, 64, 5, 5, 9, 1), (2, 4, 3, 64, 5, 5, 9, 1), (2, 4, 2, 96, 5, 5, 9, 1),
-                (2, 4, 2, 64, -1, 5, 9, 1), (2, 4, 2, 64, 5, -1, 9, 1), (2, 4, 2, 64, 5, 5, -1, 1), (2, 4, 2, 64, 5, 5, 9, 3)):
+                (2, 4, 2, 64, -1, 5, 9, 1), (2, 4, 2, 64, 5, -1, 9, 1), (2, 4, 2, 64, 5, 5, -1, 1), (2, 4, 2, 64, 5, 5, 9, 3),
+                (2, 4, 2, 64, 5, 5, (1 << 30) + 1, 1)):
         assert size(*bad) == 0
     for dt in (0, 1):
         assert size(2, 4, 2, 64, 5, 50, 100, dt) == size(2, 4, 2, 64, 5, 5, 100, dt)      # never more than N of a sequence
@@ -68,7 +69,8 @@ def test_evict_refusals(lib):
                dict(lens=FAKE + 1), dict(kept=FAKE + 1), dict(ws=FAKE + 16), dict(status=FAKE + 16), dict(c=cache(Hq=5)),
                dict(c=cache(k=None)), dict(c=cache(dtype=2))):
         assert call(**kw) == b.DA_ERR_INVALID, kw
-    for kw in (dict(c=cache(d=96)), dict(c=cache(page=8)), dict(c=cache(S=1 << 23))):
+    for kw in (dict(c=cache(d=96)), dict(c=cache(page=8)), dict(c=cache(S=1 << 23)),
+               dict(c=cache(width=1 << 27), max_len=(1 << 30) + 1)):
         assert call(**kw) == b.DA_ERR_UNSUPPORTED, kw
     need = b.dilution_attn_paged_evict_workspace_size(2, 2, 50, 100)
     assert call(n=need - 1) == b.DA_ERR_WORKSPACE and call(ws=None) == b.DA_ERR_WORKSPACE
@@ -77,7 +79,7 @@ def test_evict_refusals(lib):
 
 def test_evict_workspace_size(lib):
     size = b.dilution_attn_paged_evict_workspace_size
-    assert size(-1, 1, 5, 5) == size(1, 0, 5, 5) == size(1, 1, -1, 5) == size(1, 1, 5, -1) == 0
+    assert size(-1, 1, 5, 5) == size(1, 0, 5, 5) == size(1, 1, -1, 5) == size(1, 1, 5, -1) == size(1, 1, 5, (1 << 30) + 1) == 0
     assert size(2, 3, 500, 100) == size(2, 3, 100, 100)
     assert size(64, 64, 1 << 20, 1 << 20) > 1 << 33
 

@@ -307,6 +307,160 @@ def test_sharp_and_extreme_logits(dtype):
     run(cache, q, cu, 100, 300)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("S,wide", [(33, 0), (33, 70), (1100, 0), (1100, 90), (2500, 40)])
+def test_many_sequences(S, wide, dtype):
+    """More sequences than a warp's lanes, and than a block's threads, most of them short, some without new tokens."""
+    lens = [s * 7 % 23 for s in range(S)]
+    news = [min(n, s % 5) for s, n in enumerate(lens)]
+    if wide:
+        lens[S // 2] = news[S // 2] = wide
+    cache, _, _ = make_cache(S, lens, 2, 1, 64, 16, dtype, seed=S + wide, extra_width=8)
+    cu = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+    q = (torch.randn(int(cu[-1]), 2, 64, generator=torch.Generator().manual_seed(2)) * 1.5).to(TYPES[dtype]).to(DEV)
+    run(cache, q, torch.tensor(cu, device=DEV), max(news), max(lens))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_nothing_to_do(dtype):
+    """No tokens, no sequence with any, bounds of zero: nothing is written."""
+    cache, q, cu = make([50, 0], [0, 0], 2, 2, 64, 16, dtype, seed=61, pad=4)
+    before = cache.demand_pages.clone()
+    for rows, most, length in ((4, 0, 50), (4, 30, 50), (0, 0, 0), (0, 5, 50), (4, 100, 2600)):
+        out = torch.full_like(q[:rows], 7.0)
+        ws = b.dilution_attn_paged_chunk_workspace(cache, rows, most, length)
+        b.dilution_attn_paged_chunk(q[:rows], cache, cu, most, length, out, workspace=ws)
+        assert (out == 7.0).all() and torch.equal(cache.demand_pages, before)
+        assert b.dilution_attn_get_error(ws) == b.DA_OK
+    # a bound of zero that a sequence passes
+    cache, q, cu = make([50, 20], [3, 0], 2, 2, 64, 16, dtype, seed=62)
+    out = torch.full_like(q, 7.0)
+    ws = b.dilution_attn_paged_chunk_workspace(cache, 3, 0, 50)
+    b.dilution_attn_paged_chunk(q, cache, cu, 0, 50, out, workspace=ws)
+    assert (out == 7.0).all() and b.dilution_attn_get_error(ws) == b.DA_ERR_INVALID
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_nan_scale_of_a_short_call(dtype):
+    cache, q, cu = make([50, 20], [3, 2], 4, 2, 64, 16, dtype, seed=63)
+    tau = torch.ones(8, device=DEV)
+    tau[6] = float("nan")
+    ws = b.dilution_attn_paged_chunk_workspace(cache, 5, 3, 50)
+    b.dilution_attn_paged_chunk(q, cache, cu, 3, 50, tau_bh=tau, workspace=ws)
+    assert b.dilution_attn_get_error(ws) == b.DA_ERR_INVALID
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_calls_at_once(dtype):
+    """Four caches on four streams, long and short calls and evictions in each, against the same calls one by one."""
+    shapes = [([3000, 400], [150, 30]), ([500, 60], [5, 1]), ([2500], [4]), ([700, 0, 333], [64, 0, 333])]
+    keep = torch.full((3,), 200, dtype=torch.int32, device=DEV)
+
+    def calls(i, stream=None):
+        lens, news = shapes[i]
+        cache, q, cu = make(lens, news, 4, 2, 64, 32, dtype, seed=70 + i)
+        outs = []
+        torch.cuda.synchronize()
+
+        def go():
+            for _ in range(6):
+                outs.append(b.dilution_attn_paged_chunk(q, cache, cu, max(news), max(lens), stream=stream))
+            b.dilution_attn_paged_evict(cache, keep[:len(lens)], 200, max(lens), cache.seq_lens, sinks=2, recent=100, stream=stream)
+        return go, outs, cache
+    ref = [calls(i) for i in range(4)]
+    for go, _, _ in ref:
+        go()
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = [calls(i, streams[i]) for i in range(4)]
+    for go, _, _ in got:
+        go()
+    torch.cuda.synchronize()
+    for (_, a, x), (_, c, y) in zip(ref, got):
+        assert all(torch.equal(m, n) for m, n in zip(a, c))
+        for pool in ("k_pages", "v_pages", "demand_pages", "seq_lens"):
+            assert torch.equal(getattr(x, pool), getattr(y, pool))
+        assert b.dilution_attn_get_error(y.status) == b.DA_OK
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_graphs_that_share_a_workspace(dtype):
+    """A long call, a short one and an eviction, each captured with the same workspace, replayed by turns."""
+    caches = [make(lens, news, 4, 2, 64, 32, dtype, seed=100 + i)
+              for i, (lens, news) in enumerate((([900, 77], [130, 5]), ([300, 40], [4, 1])))]
+    keep = torch.tensor([150, 30], dtype=torch.int32, device=DEV)
+    third = make([700, 90], [1, 1], 4, 2, 64, 32, dtype, seed=102)[0]
+
+    def calls(outs, ws):
+        return [lambda i=i, most=most: b.dilution_attn_paged_chunk(*caches[i][1::-1], caches[i][2], *most, outs[i], workspace=ws)
+                for i, most in enumerate(((130, 900), (4, 300)))] + \
+               [lambda: b.dilution_attn_paged_evict(third, keep, 150, 700, outs[2], sinks=1, recent=20, workspace=ws)]
+    pools = [caches[0][0].demand_pages, caches[1][0].demand_pages, third.demand_pages, third.k_pages, third.v_pages]
+    start = [x.clone() for x in pools]
+
+    def reset():
+        for x, y in zip(pools, start):
+            x.copy_(y)
+    outs = lambda: [torch.zeros_like(c[1]) for c in caches] + [torch.zeros(2, dtype=torch.int32, device=DEV)]
+    ref = outs()
+    for f in calls(ref, None):
+        f()
+    ref += [x.clone() for x in pools]
+    reset()
+    ws = max((b.dilution_attn_paged_chunk_workspace(caches[0][0], 135, 130, 900),
+              b.dilution_attn_paged_evict_workspace(third, 150, 700)), key=len)
+    got, graphs = outs(), []
+    for f in calls(got, ws):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            f()
+    for order in ((0, 1, 2), (2, 1, 0), (1, 2, 0)):
+        reset()
+        for i in order:
+            graphs[i].replay()
+        assert all(torch.equal(x, y) for x, y in zip(ref, got + pools))
+        assert b.dilution_attn_get_error(ws) == b.DA_OK
+
+
+@pytest.mark.parametrize("d,lens,news", [(64, [9000], [4]), (64, [6000, 100], [140, 3]), (128, [7000], [130])])
+def test_long_pieces_repeat_their_bits(d, lens, news):
+    cache, q, cu = make(lens, news, 6, 3, d, 64, "bf16", seed=81)
+    start, ref = cache.demand_pages.clone(), None
+    for _ in range(12):
+        cache.demand_pages.copy_(start)
+        out = b.dilution_attn_paged_chunk(q, cache, cu, max(news), max(lens))
+        now = (out, cache.demand_pages.clone())
+        ref = ref or now
+        assert torch.equal(now[0], ref[0]) and torch.equal(now[1], ref[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,news", [([300, 90], [20, 5]), ([700, 90], [130, 5])])
+def test_pools_past_32_bits(lens, news, dtype):
+    """Pages whose first elements lie past 2^31: the bits of the same cache in a small pool, and of its eviction."""
+    cache, q, cu = make(lens, news, 8, 8, 128, 64, dtype, seed=91)
+    kv, dem = 2 ** 31 // (8 * 64 * 128), 2 ** 31 // (8 * 64)
+    n_kv, n_dem = cache.k_pages.shape[0], cache.demand_pages.shape[0]
+    pools = []
+    for small, first in ((cache.k_pages, kv), (cache.v_pages, kv), (cache.demand_pages, dem)):
+        big = torch.empty((first + small.shape[0] + 1, *small.shape[1:]), dtype=small.dtype, device=DEV)
+        big[first:first + small.shape[0]] = small
+        pools.append(big)
+    shift = lambda t, by: torch.where(t >= 0, t + by, t)
+    far = b.PagedCache(*pools, shift(cache.page_table, kv), shift(cache.demand_table, dem), cache.seq_lens.clone())
+    keep = torch.tensor([100, 90], dtype=torch.int32, device=DEV)
+    for max_len in (max(lens), LONG):
+        outs = [b.dilution_attn_paged_chunk(q, c, cu, max(news), max_len) for c in (cache, far)]
+        assert torch.equal(*outs)
+        assert torch.equal(far.demand_pages[dem:dem + n_dem], cache.demand_pages)
+    for c in (cache, far):
+        b.dilution_attn_paged_evict(c, keep, 100, max(lens), c.seq_lens, sinks=1, recent=9)
+        assert c.seq_lens.tolist() == [100, 90] and b.dilution_attn_get_error(c.status) == b.DA_OK
+    for name, first, n in (("k_pages", kv, n_kv), ("v_pages", kv, n_kv), ("demand_pages", dem, n_dem)):
+        x, y = getattr(far, name)[first:first + n], getattr(cache, name)
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
 def test_serving_run_together():
     """Rotation, append and chunk of ragged prompts, a second chunk behind them, eviction, single tokens and a decode step:
     the calls of a serving loop, each against the oracle on the cache as it then is."""

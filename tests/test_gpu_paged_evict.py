@@ -114,6 +114,36 @@ def test_scores_in_the_workspace():
     evict(cache, [3000], [1000], 1000, 3000, 3, 50, kept=False)
 
 
+@pytest.mark.parametrize("place", [True, False])
+@pytest.mark.parametrize("S", [33, 1024, 1100])
+def test_many_sequences(S, place):
+    """More sequences than the counted chunks of the moving kernel, empty and untouched ones among them."""
+    lens = [s * 11 % 41 for s in range(S)]
+    keeps = [s * 5 % 29 for s in range(S)]
+    most = max(min(n, k) for n, k in zip(lens, keeps))
+    spare = sum(-(-min(n, k) // 16) for n, k in zip(lens, keeps)) + 2
+    cache, _, _ = make_cache(S, lens, 4, 2, 64, 16, "bf16", seed=S, spare=spare, extra_width=1)
+    evict(cache, lens, keeps, most, max(lens), 1, 3, None if place else dst_tables(cache, lens, keeps, 4))
+
+
+def test_nothing_to_do():
+    """Bounds of zero, sequences without tokens."""
+    cache, _, _ = make_cache(2, [0, 0], 2, 1, 64, 16, "bf16", seed=14, extra_width=2)
+    evict(cache, [0, 0], [5, 0], 0, 0)
+    evict(cache, [0, 0], [5, 0], 5, 20)
+    cache, _, _ = make_cache(2, [30, 0], 2, 1, 64, 16, "bf16", seed=15, extra_width=2)
+    evict(cache, [30, 0], [0, 7], 0, 30)
+    evict(cache, [30, 0], [30, 7], 30, 30, 2 ** 31 - 1, 2 ** 31 - 1)
+
+
+def test_groups_of_heads():
+    """Groups that are no multiple of four heads, sums in the heads' order."""
+    for Hq, Hkv in ((7, 1), (10, 2), (9, 9), (15, 3)):
+        cache, _, _ = make_cache(2, [333, 65], Hq, Hkv, 128, 32, "bf16", seed=Hq, spare=30, extra_width=1)
+        cache.demand_pages.mul_(torch.logspace(-6, 6, Hq, device=DEV)[None, :, None])
+        evict(cache, [333, 65], [111, 64], 111, 333, 0, 3)
+
+
 def test_shared_prefix_keeps_its_pages():
     """Two sequences share the pages of 64 tokens; both keep them all (sinks), to tables that name the same pages."""
     cache, _, prefix = make_cache(2, [300, 200], 2, 1, 64, 32, "bf16", seed=10, prefix=64, spare=20, extra_width=1)
