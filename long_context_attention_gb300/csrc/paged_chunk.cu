@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, kJoinCtas) chunk_join(PagedChu
 // out = numerators / shares, summed over the pieces in the line's order.
 template <int D, typename E>
 __global__ void __launch_bounds__(32 * kRowWarps, kCombineCtas) chunk_combine(PagedChunk p, ChunkPlan w, int run) {
-  constexpr int COLS = D / 4, PER = 8 * COLS / 32;   // float4 columns of a row; of a lane
+  constexpr int PER = D / 16;   // 16-byte pieces of a lane
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x % 32;
@@ -222,9 +222,10 @@ __global__ void __launch_bounds__(32 * kRowWarps, kCombineCtas) chunk_combine(Pa
       pc.find(x, cut);
       tile0 = pc.tile(x, cut, pc.first + lane);
     }
-    const int left = x.q.n - x.i;   // valid rows
+    const int r = lane % 8;                     // the lane's row
+    const bool valid = x.i + r < x.q.n;
     float4 a[PER];
-    float sum = 0.f;                // of row `lane`
+    float sum = 0.f;
 #pragma unroll
     for (int e = 0; e < PER; ++e) a[e] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c = pc.first; c <= pc.last; c += 32) {
@@ -232,36 +233,31 @@ __global__ void __launch_bounds__(32 * kRowWarps, kCombineCtas) chunk_combine(Pa
       for (unsigned have = __ballot_sync(0xffffffffu, tile >= 0); have; have &= have - 1) {
         const int from = __ffs(have) - 1, t = __shfl_sync(0xffffffffu, tile, from);
         const float *at = chunk_place(p, w.acc_a, w.acc_b, x.row0, w.cta_rows, t, c + from, x.r, acc_stride(D));
+        if (!valid) continue;
         float4 v[PER];
 #pragma unroll
-        for (int e = 0; e < PER; ++e) {
-          const int q = lane + 32 * e, r = q / COLS;
-          v[e] = r < left ? __ldcg(reinterpret_cast<const float4 *>(at + r * acc_stride(D)) + q % COLS)
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        if (lane < min(left, 8)) sum += __ldcg(at + lane * acc_stride(D) + D);
+        for (int e = 0; e < PER; ++e) v[e] = __ldcg(reinterpret_cast<const float4 *>(at + chunk_acc(D, r, lane / 8 + 4 * e)));
+        sum += __ldcg(at + chunk_acc_sum(D, r));
 #pragma unroll
         for (int e = 0; e < PER; ++e) a[e].x += v[e].x, a[e].y += v[e].y, a[e].z += v[e].z, a[e].w += v[e].w;
       }
     }
+    if (!valid) return;
+    // a normal reciprocal: one division does for the row
+    const bool plain = sum >= 0x1p-100f && sum <= 0x1p100f;
+    const float inv = plain ? 1.f / sum : 0.f;
+    const size_t to = ((size_t)(x.q.tok0 + x.i + r) * p.c.Hq + x.hq) * D + lane / 8 * 4;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-      const int q = lane + 32 * e, r = q / COLS;
-      const float d = __shfl_sync(0xffffffffu, sum, r);
-      if (r >= left) continue;
       float4 v = a[e];
-      if (d >= 0x1p-100f && d <= 0x1p100f) {   // its reciprocal is normal, and one division does for four
-        const float inv = 1.f / d;
+      if (plain)
         v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-      } else {
-        v.x /= d, v.y /= d, v.z /= d, v.w /= d;
-      }
-      const size_t to = ((size_t)(x.q.tok0 + x.i + r) * p.c.Hq + x.hq) * D + 4 * (q % COLS);
-      if constexpr (sizeof(E) == 4)
-        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + to) =
-            v;
       else
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + to) =
+        v.x /= sum, v.y /= sum, v.z /= sum, v.w /= sum;
+      if constexpr (sizeof(E) == 4)
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + to + 16 * e) = v;
+      else
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + to + 16 * e) =
             make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     }
   });

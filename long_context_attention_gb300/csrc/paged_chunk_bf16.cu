@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       if (!warp_wait(&r_full[i % kCkxRing], (i / kCkxRing) & 1, wc)) break;
       const CkxTile &x = ring[i % kCkxRing];
       const int rows = x.rows;
-      float *to = x.place + (size_t)c * acc_stride(D);
+      float *to = x.place + chunk_acc(D, c, 0), *to_sum = x.place + chunk_acc_sum(D, c);
       __syncwarp();
       if (lane == 0) mbar_arrive(&r_free[i % kCkxRing]);
       if (rows == 0) break;
@@ -788,11 +788,11 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
         tmem_wait_ld_r8(a);
         tmem_wait_ld_r8(b);
         if (c < rows) {
-          float4 *o = reinterpret_cast<float4 *>(to + e);
+          float4 *o = reinterpret_cast<float4 *>(to + 8 * e);
           o[0] = make_float4(a[0], a[1], a[2], a[3]);
-          o[1] = make_float4(a[4], a[5], a[6], a[7]);
-          o[2] = make_float4(b[0], b[1], b[2], b[3]);
-          o[3] = make_float4(b[4], b[5], b[6], b[7]);
+          o[8] = make_float4(a[4], a[5], a[6], a[7]);
+          o[16] = make_float4(b[0], b[1], b[2], b[3]);
+          o[24] = make_float4(b[4], b[5], b[6], b[7]);
         }
         __syncwarp();
       }
@@ -800,7 +800,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       tmem_ld1(td + 64, sum);
       tmem_wait_ld();
       asm volatile("" : "+f"(sum));
-      if (c < rows) to[D] = sum;
+      if (c < rows) *to_sum = sum;
       __syncwarp();
       zero();
     }

@@ -432,23 +432,24 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
       if (tx == 0) row[D] = sum[r];
     }
     __syncthreads();
-    for (int i = tid; i < t.rows * (D + 1); i += kCkfThreads) {
-      const int r = i / (D + 1), c = i % (D + 1);
+    for (int i = tid; i < (t.rows + 7) / 8 * 8 * (D + 1); i += kCkfThreads) {   // eight rows after eight, as they lie
+      const int r8 = i / (8 * (D + 1)) * 8, e = i % (8 * (D + 1)), r = r8 + (e < 8 * D ? e / 4 % 8 : e - 8 * D),
+                c = e < 8 * D ? e / 32 * 4 + e % 4 : D;
       float a = 0.f;
 #pragma unroll
       for (int g = 0; g < 4; ++g) a += stage[(g * 16 + r) * LD + c];
-      if (t.valid(r)) to[(size_t)r * acc_stride(D) + c] = a;
+      if (t.valid(r)) to[c < D ? chunk_acc(D, r, c / 4) + c % 4 : chunk_acc_sum(D, r)] = a;
     }
   } else if (work) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       if (rows.last[r] < 0) continue;
-      float *row = to + (size_t)(part.row + r) * acc_stride(D);
+      const int row = part.row + r;
 #pragma unroll
       for (int e = 0; e < NV; ++e)
-        *reinterpret_cast<float4 *>(row + 64 * e + 4 * tx) =
+        *reinterpret_cast<float4 *>(to + chunk_acc(D, row, 16 * e + tx)) =
             make_float4(num[r][4 * e], num[r][4 * e + 1], num[r][4 * e + 2], num[r][4 * e + 3]);
-      if (tx == 0) row[D] = sum[r];
+      if (tx == 0) to[chunk_acc_sum(D, row)] = sum[r];
     }
   }
 }
