@@ -409,6 +409,7 @@ struct CkxVal {
   static constexpr int kTB = kCkxEdge * D * 2;
   static constexpr int kStages = D == 64 ? 3 : 2;      // of K, and of V
   static constexpr int kLag = kG;                      // V behind K, in tiles
+  static constexpr int kDrain = D == 64 ? 16 : 32;     // columns of D that the epilogue's registers hold
   // Barriers of what has landed: three rounds of stages, since those that wait for a
   // tile need not have seen the ones before it in its stage land, and a barrier's
   // parity tells a round from the next alone.  (The tile before it in its barrier has
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       mbar_init(&done[g], 1);
     }
     mbar_init(d_full, kG);    // one commit per issuer
-    mbar_init(d_free, 4);     // phase i: D holds zeros for column tile i
+    mbar_init(d_free, 4);     // phase i: D is free for column tile i
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       const uint64_t dSh = smem_desc(smem_u32(sSh) + g * C::kShBytes, 16384, 1024);
       int m = 0, mv = 0;          // tiles of this warpgroup: S issued, value products issued
       int vt = 0, vi = 0;         // the tile whose value product is due, its column tile
-      bool due = false, ends = false;
+      bool due = false, begins = false, ends = false;
       bool ok = true;
       // D += share^T [V | 1], in the tiles' order (sums in another order would have other
       // last bits).  Once V of tile t is there, the product of t - kStages has been formed,
@@ -686,9 +687,10 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
         ++mv;
         tc_fence_after();
         const uint32_t v = smem_u32(sV) + st * C::kTB;
-        MmaRun<0, 8, 128, 128 - (128ll << 16), false>::go(tmem + C::kTmemD, dSh, smem_desc(v, ones - v, 1024), idesc_pv, 1u);
+        MmaRun<0, 8, 128, 128 - (128ll << 16), false>::go(tmem + C::kTmemD, dSh, smem_desc(v, ones - v, 1024), idesc_pv, begins ? 0u : 1u);
         if constexpr (D == 128)
-          MmaRun<0, 8, 128, 128, false>::go(tmem + C::kTmemDHi, dSh, smem_desc(v + kCkxHalf, kCkxHalf, 1024), idesc_hi, 1u);
+          MmaRun<0, 8, 128, 128, false>::go(tmem + C::kTmemDHi, dSh, smem_desc(v + kCkxHalf, kCkxHalf, 1024), idesc_hi,
+                                                          begins ? 0u : 1u);
         mma_commit(&sh_free[g]);
         mma_commit(&v_empty[st]);
         if (ends) mma_commit(d_full);
@@ -742,6 +744,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
           due = true;
           vt = t;
           vi = i;
+          begins = j == 0;
           ends = j + kG >= tiles;
         }
         if (!ok) break;
@@ -762,13 +765,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
     ckx_regs_dec<C::kRegsEpi>();
     const int quarter = warp % 4, c = quarter * 32 + lane;
     const uint32_t td = tmem + C::kTmemD + ((uint32_t)(quarter * 32) << 16);
-    auto zero = [&]() {
-      tmem_zero80(td);
-      if constexpr (D == 128) tmem_zero64(td + (C::kTmemDHi - C::kTmemD));
-      tmem_wait_st();
-      ckx_release(d_free, lane);
-    };
-    zero();
+    ckx_release(d_free, lane);
     for (int i = 0;; ++i) {
       if (!warp_wait(&r_full[i % kCkxRing], (i / kCkxRing) & 1, wc)) break;
       const CkxTile &x = ring[i % kCkxRing];
@@ -779,30 +776,30 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       if (rows == 0) break;
       if (!warp_wait(d_full, i & 1, wc)) break;
       tc_fence_after();
+      float sums[8];   // alike
+      tmem_ld8(td + 64, sums);
+      tmem_wait_ld_r8(sums);
 #pragma unroll
-      for (int e = 0; e < D; e += 16) {
-        float a[8], b[8];
+      for (int e = 0; e < D; e += C::kDrain) {
+        float a[C::kDrain / 8][8];
         const uint32_t at = td + (e < 64 ? e : C::kTmemDHi - C::kTmemD + e - 64);
-        tmem_ld8(at, a);
-        tmem_ld8(at + 8, b);
-        tmem_wait_ld_r8(a);
-        tmem_wait_ld_r8(b);
+#pragma unroll
+        for (int k = 0; k < C::kDrain / 8; ++k) tmem_ld8(at + 8 * k, a[k]);
+#pragma unroll
+        for (int k = 0; k < C::kDrain / 8; ++k) tmem_wait_ld_r8(a[k]);
+        if (e + C::kDrain == D) ckx_release(d_free, lane);   // read: the next column tile's products while these are written
         if (c < rows) {
           float4 *o = reinterpret_cast<float4 *>(to + 8 * e);
-          o[0] = make_float4(a[0], a[1], a[2], a[3]);
-          o[8] = make_float4(a[4], a[5], a[6], a[7]);
-          o[16] = make_float4(b[0], b[1], b[2], b[3]);
-          o[24] = make_float4(b[4], b[5], b[6], b[7]);
+#pragma unroll
+          for (int k = 0; k < C::kDrain / 8; ++k) {
+            o[16 * k] = make_float4(a[k][0], a[k][1], a[k][2], a[k][3]);
+            o[16 * k + 8] = make_float4(a[k][4], a[k][5], a[k][6], a[k][7]);
+          }
         }
         __syncwarp();
       }
-      float sum;
-      tmem_ld1(td + 64, sum);
-      tmem_wait_ld();
-      asm volatile("" : "+f"(sum));
-      if (c < rows) *to_sum = sum;
+      if (c < rows) *to_sum = sums[0];
       __syncwarp();
-      zero();
     }
   } else {
     // ---------------------------------------------------------------- demand
