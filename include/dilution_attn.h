@@ -480,11 +480,11 @@ int dilution_attn_paged_chunk(const void *q, const dilution_attn_paged_cache *ca
  *   dst_page_table, dst_demand_table: both NULL: in place.  Otherwise DEVICE
  *       [S][dst_max_pages] tables of the same pools, dst_max_pages * page_size at
  *       least min(max_keep, max_len), that receive the rows that stay, of
- *       sequences that lose nothing too.  A page named there is either the source's
- *       at the same place of the same sequence or one that the call does not read.
- *       Only rows whose place changes are written, so pages that sequences share
- *       keep their contents as far as every key head keeps all their tokens (a
- *       shared prefix of `sinks` tokens).
+ *       sequences that lose nothing too.  A page named there is one that the call does
+ *       not read, or the source's at the same place of the same sequence where every
+ *       key head keeps all tokens of that page and before it (a prefix of at most
+ *       `sinks` tokens, which sequences may share): only rows whose place changes are
+ *       written.
  *   keep: DEVICE [S] int32.  max_keep, max_len: host upper bounds of m and of
  *       seq_lens (max_len at most max_pages * page_size and 2^30).
  *   new_lens: DEVICE [S] int32, receives m; may be cache->seq_lens itself.

@@ -22,6 +22,9 @@
 //
 // evict_move: rows to other pages; blocks take chunk after chunk by tickets.
 //
+// evict_small: all of it for up to 512 tokens a sequence in one launch, a block per
+// (sequence, key head).
+//
 // What bounds it: HBM (4 bytes a total, then the rows that stay, once each way).
 #include "da_evict.h"
 #include "da_ptx.cuh"
@@ -341,6 +344,7 @@ struct MoveTotals {
 };
 
 // 16-byte pieces of rows of keys and values, each thread's of a batch.
+template <int THREADS>
 struct MovePieces {
   uint8_t *k, *v;        // the pools, at the key head's first row
   size_t page_bytes;
@@ -353,9 +357,9 @@ struct MovePieces {
     k = reinterpret_cast<uint8_t *>(a.c.k_pages) + (((size_t)h * row_bytes) << sh);
     v = reinterpret_cast<uint8_t *>(a.c.v_pages) + (((size_t)h * row_bytes) << sh);
   }
-  __device__ __forceinline__ int row(int u) const { return ((int)threadIdx.x + u * kMoveThreads) >> shift; }
+  __device__ __forceinline__ int row(int u) const { return ((int)threadIdx.x + u * THREADS) >> shift; }
   __device__ __forceinline__ uint4 *at(long long row, int u) const {
-    const int piece = ((int)threadIdx.x + u * kMoveThreads) & (2 * half - 1);
+    const int piece = ((int)threadIdx.x + u * THREADS) & (2 * half - 1);
     return reinterpret_cast<uint4 *>((piece < half ? k : v) + (size_t)(row >> page_shift) * page_bytes +
                                      (size_t)(row & ((1 << page_shift) - 1)) * row_bytes) +
            (piece & (half - 1));
@@ -556,7 +560,7 @@ __global__ void __launch_bounds__(kMoveThreads, 3) evict_move(EvictArgs a, Evict
       if (tid == 0) s_ticket[buf] = atomicAdd(counter, 1);
       t.write();
     } else {
-      const MovePieces x(a, ch, sh);
+      const MovePieces<kMoveThreads> x(a, ch, sh);
       uint4 v[kMoveLoads];
 #pragma unroll
       for (int u = 0; u < kMoveLoads; ++u) {
@@ -575,6 +579,138 @@ __global__ void __launch_bounds__(kMoveThreads, 3) evict_move(EvictArgs a, Evict
   }
 }
 
+// Up to kSmallKeys tokens a sequence.  Thread t has token t; the m-th highest score is
+// found bit by bit, a count over the block each.  (Every score compared with every other:
+// 4 us of one SM's instructions for 500.)  Then rows in order, a batch read before it is written, so that in place nothing is overwritten
+// that is still to be read (see evict_place).
+constexpr int kSmallKeys = 512, kSmallThreads = kSmallKeys, kSmallLoads = 8;
+__global__ void __launch_bounds__(kSmallThreads) evict_small(EvictArgs a, int sh) {
+  __shared__ int s_list[kSmallKeys], s_warp[kSmallThreads / 32];
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int s = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv, G = a.c.Hq / a.c.Hkv;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int len = __ldcg(a.c.seq_lens + s), keep = __ldcg(a.keep + s);
+  const bool good = len >= 0 && len <= a.max_len && keep >= 0 && min(len, keep) <= a.max_keep;
+  const int m = good ? min(len, keep) : 0;
+  if (h == 0 && tid == 0) {
+    if (!good) atomicCAS(a.status, DA_OK, DA_ERR_INVALID);
+    a.new_lens[s] = good ? m : len;   // (no other block reads it: see launch_evict)
+  }
+  int32_t *kept = a.kept != nullptr ? a.kept + (size_t)blockIdx.x * a.max_keep : nullptr;
+  if (kept != nullptr)
+    for (int i = m + tid; i < a.max_keep; i += kSmallThreads) kept[i] = -1;
+  if (m == 0) return;
+  const int32_t *dtab = a.c.demand_table + (size_t)s * a.c.max_pages;
+  const int in_page = (1 << sh) - 1;
+  uint32_t key = 0;   // below every score
+  if (tid < len && m < len) {
+    const int page = __ldcg(dtab + (tid >> sh));
+    float v = 0.f;
+    if ((unsigned)page < (unsigned)a.c.num_demand_pages) {
+      const float *at = a.c.demand_pages + ((((size_t)page * a.c.Hq + (size_t)h * G) << sh) + (tid & in_page));
+      for (int g = 0; g < G; g += 4) {
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (g + e < G) f[e] = __ldcg(at + ((size_t)(g + e) << sh));
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (g + e < G) v = g + e == 0 ? f[e] : __fadd_rn(v, f[e]);
+      }
+    } else {
+      atomicCAS(a.status, DA_OK, DA_ERR_INVALID);
+    }
+    key = ev_key(tid < a.sinks || tid >= len - a.recent ? INFINITY : v);
+  }
+  // the m-th highest key, bit by bit from the top, until just m are at least as high
+  uint32_t least = 0;
+  if (m < len) {
+    for (int bit = 31; bit >= 0; --bit) {
+      const int n = __syncthreads_count(key >= (least | 1u << bit));
+      if (n >= m) least |= 1u << bit;
+      if (n == m) break;
+    }
+  }
+  const bool above = tid < len && key > least, equal = tid < len && key == least;
+  const unsigned va = __ballot_sync(0xffffffffu, above), ve = __ballot_sync(0xffffffffu, equal), lt = (1u << lane) - 1u;
+  if (lane == 0) s_warp[warp] = __popc(va) << 16 | __popc(ve);
+  __syncthreads();
+  int na = 0, ne = 0, all = 0;   // before this warp, and all that are above
+  for (int i = 0; i < kSmallThreads / 32; ++i) {
+    const int n = s_warp[i];
+    all += n >> 16;
+    if (i < warp) na += n >> 16, ne += n & 0xffff;
+  }
+  na += __popc(va & lt);
+  ne += __popc(ve & lt);
+  const int need = m - all;      // equal ones that stay, the first of them
+  if (above || (equal && ne < need)) {
+    const int place = na + min(ne, need);
+    s_list[place] = tid;
+    if (kept != nullptr) kept[place] = tid;
+  }
+  __syncthreads();
+  const bool same = a.dst_page_table == nullptr;
+  const int32_t *psrc = a.c.page_table + (size_t)s * a.c.max_pages, *pdst = same ? psrc : a.dst_page_table + (size_t)s * a.dst_max_pages;
+  const int32_t *ddst = same ? dtab : a.dst_demand_table + (size_t)s * a.dst_max_pages;
+  const MovePieces<kSmallThreads> x(a, h, sh);
+  const int rows = kSmallThreads * kSmallLoads >> x.shift;   // of a batch
+  for (int r0 = 0, g = 0; r0 < m || g < G; r0 += rows, g += 4) {
+    uint4 v[kSmallLoads];
+    uint4 *out[kSmallLoads];
+    float f[4];
+    float *to[4];
+    uint32_t words = 0;
+#pragma unroll
+    for (int u = 0; u < kSmallLoads; ++u) {
+      const int r = r0 + x.row(u);
+      out[u] = nullptr;
+      if (r >= m) continue;
+      const int t = s_list[r];
+      const long long i = ev_row(psrc, t, sh, a.c.num_pages, a.status), o = ev_row(pdst, r, sh, a.c.num_pages, a.status);
+      if (i < 0 || o < 0 || i == o) continue;
+      v[u] = __ldcg(x.at(i, u));
+      out[u] = x.at(o, u);
+    }
+    // four query heads' totals, a row a thread
+#pragma unroll
+    for (int e = 0; e < 4; ++e) to[e] = nullptr;
+    if (g < G && tid < m) {
+      const long long i = ev_row(dtab, s_list[tid], sh, a.c.num_demand_pages, a.status),
+                      o = ev_row(ddst, tid, sh, a.c.num_demand_pages, a.status);
+      if (i >= 0 && o >= 0 && i != o) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (g + e >= G) break;
+          const size_t head = (size_t)h * G + g + e;
+          f[e] = __ldcg(a.c.demand_pages + ((((size_t)(i >> sh) * a.c.Hq + head) << sh) + (size_t)(i & in_page)));
+          to[e] = a.c.demand_pages + ((((size_t)(o >> sh) * a.c.Hq + head) << sh) + (size_t)(o & in_page));
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kSmallLoads; ++u)
+      if (out[u] != nullptr) words |= ev_words(v[u]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (to[e] != nullptr) words |= ev_words(f[e]);
+    __syncthreads_or(ev_arrived(words));   // the batch has been read
+#pragma unroll
+    for (int u = 0; u < kSmallLoads; ++u)
+      if (out[u] != nullptr) *out[u] = v[u];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (to[e] != nullptr) *to[e] = f[e];
+  }
+}
+
+// Whether `n` 32-bit words at a and at b share bytes.
+static bool words_meet(const void *a, const void *b, int64_t n) {
+  const intptr_t d = reinterpret_cast<intptr_t>(a) - reinterpret_cast<intptr_t>(b);
+  return d < 4 * n && -d < 4 * n;
+}
+
 int launch_evict(const EvictArgs &a, cudaStream_t stream) {
   static PerDeviceOnce once;
   const int prep = once.run([] {
@@ -591,6 +727,9 @@ int launch_evict(const EvictArgs &a, cudaStream_t stream) {
   const int64_t tickets = items * ((most + rows - 1) / rows) + totals * w.total_chunks;
   if (tickets > 0x7F000000 || items * w.cluster > 0x7FFFFFFF || items * 64 + totals > 0x7FFFFFFF)
     return DA_ERR_UNSUPPORTED;
+  // One launch, unless the lengths are written where blocks still read them.
+  if (a.max_len <= kSmallKeys && !words_meet(a.new_lens, a.c.seq_lens, a.c.S) && !words_meet(a.new_lens, a.keep, a.c.S))
+    return launch_after(evict_small, dim3((unsigned)items), kSmallThreads, 0, stream, a, sh) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.c.S * a.c.Hkv * w.cluster));
   cfg.blockDim = dim3(kSelThreads);

@@ -33,24 +33,31 @@ def dst_tables(cache, lens, keeps, seed):
 
 
 def evict(cache, lens, keeps, max_keep, max_len, sinks=0, recent=0, to=None, kept=True, **kw):
-    """The call against the oracle, everything compared."""
+    """The call against the oracle, everything compared; then with the lengths written where they are read, which the
+    kernel for short sequences does not take."""
     before = pools(cache)
+    start = [x.clone() for x in (cache.k_pages, cache.v_pages, cache.demand_pages)]
     tables = [x.cpu().numpy() for x in (cache.page_table, cache.demand_table)]
     dst = [None, None] if to is None else [x.cpu().numpy() for x in to]
     rK, rV, rD, rl, rk = op.paged_evict(*before, *tables, lens, keeps, max_keep, sinks, recent, *dst)
-    ws = b.dilution_attn_paged_evict_workspace(cache, max_keep, max_len)
-    ws[256:] = 0xC7
-    kt = torch.full((cache.S, cache.Hkv, max_keep), 99, dtype=torch.int32, device=DEV) if kept else None
-    got = b.dilution_attn_paged_evict(cache, torch.tensor(keeps, dtype=torch.int32, device=DEV), max_keep, max_len,
-                                      sinks=sinks, recent=recent, kept=kt, workspace=ws,
-                                      dst_page_table=None if to is None else to[0],
-                                      dst_demand_table=None if to is None else to[1], **kw)
-    assert b.dilution_attn_get_error(ws) == b.DA_OK
-    assert got.tolist() == rl.tolist()
-    if kept:
-        assert np.array_equal(kt.cpu().numpy(), rk)
-    for x, y in zip(pools(cache), (rK, rV, rD)):
-        assert np.array_equal(x, y, equal_nan=True)
+    lengths = cache.seq_lens.clone()
+    for new_lens in (None, cache.seq_lens):
+        for x, y in zip((cache.k_pages, cache.v_pages, cache.demand_pages), start):
+            x.copy_(y)
+        ws = b.dilution_attn_paged_evict_workspace(cache, max_keep, max_len)
+        ws[256:] = 0xC7
+        kt = torch.full((cache.S, cache.Hkv, max_keep), 99, dtype=torch.int32, device=DEV) if kept else None
+        got = b.dilution_attn_paged_evict(cache, torch.tensor(keeps, dtype=torch.int32, device=DEV), max_keep, max_len, new_lens,
+                                          sinks=sinks, recent=recent, kept=kt, workspace=ws,
+                                          dst_page_table=None if to is None else to[0],
+                                          dst_demand_table=None if to is None else to[1], **kw)
+        assert b.dilution_attn_get_error(ws) == b.DA_OK
+        assert got.tolist() == rl.tolist()
+        if kept:
+            assert np.array_equal(kt.cpu().numpy(), rk)
+        for x, y in zip(pools(cache), (rK, rV, rD)):
+            assert np.array_equal(x, y, equal_nan=True)
+    cache.seq_lens.copy_(lengths)
 
 
 @pytest.mark.parametrize("place", [True, False])
@@ -59,7 +66,7 @@ def evict(cache, lens, keeps, max_keep, max_len, sinks=0, recent=0, to=None, kep
 @pytest.mark.parametrize("lens,keeps,sinks,recent", [
     ([1], [1], 0, 0), ([1], [0], 0, 0), ([2], [1], 0, 0), ([40], [39], 0, 0), ([40], [39], 4, 8), ([300], [100], 4, 33),
     ([500, 0, 257, 1, 90], [250, 5, 1, 1, 200], 2, 10), ([600], [64], 0, 0), ([700, 33], [699, 0], 1, 1),
-    ([128], [20], 16, 16), ([1500, 1100], [700, 1099], 0, 64),
+    ([128], [20], 16, 16), ([1500, 1100], [700, 1099], 0, 64), ([507, 512, 31], [300, 511, 20], 1, 7), ([513], [512], 0, 0),
 ])
 def test_evict(lens, keeps, sinks, recent, dtype, d, page, Hq, Hkv, place):
     most = max(min(n, k) for n, k in zip(lens, keeps))
@@ -191,7 +198,9 @@ def test_lengths_in_place_streams_and_graphs():
         same(cache)
 
 
-def test_bad_lengths_budgets_and_pages():
+@pytest.mark.parametrize("inside", [False, True])
+def test_bad_lengths_budgets_and_pages(inside):
+    """``inside``: the lengths written where they are read."""
     lens, keeps = [100, 200, 150], [50, 60, 70]
     for place in (True, False):
         def call(change, max_keep=70, max_len=200, keeps=keeps, good=(0, 2), whole=True):
@@ -210,7 +219,7 @@ def test_bad_lengths_budgets_and_pages():
             ws = b.dilution_attn_paged_evict_workspace(cache, max_keep, max_len)
             kept = torch.full((3, 2, max_keep), 99, dtype=torch.int32, device=DEV)
             got = b.dilution_attn_paged_evict(cache, torch.tensor(keeps, dtype=torch.int32, device=DEV), max_keep, max_len,
-                                              sinks=1, recent=5, kept=kept, workspace=ws,
+                                              cache.seq_lens if inside else None, sinks=1, recent=5, kept=kept, workspace=ws,
                                               dst_page_table=None if place else to[0], dst_demand_table=None if place else to[1])
             assert b.dilution_attn_get_error(ws) == b.DA_ERR_INVALID
             assert b.dilution_attn_get_error(ws) == b.DA_OK
