@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libdilution_attn.so")
 
 SOURCES = ["capi.cu", "capi_paged.cu", "rope.cu", "paged_decode_f32.cu", "paged_decode_bf16.cu",
            "paged_prefix_bf16.cu", "paged_small_bf16.cu", "paged_chunk.cu", "paged_chunk_f32.cu",
-           "paged_chunk_bf16.cu", "paged_chunk_small.cu", "paged_evict.cu",
+           "paged_chunk_bf16.cu", "paged_chunk_few.cu", "paged_chunk_small.cu", "paged_evict.cu",
            "fwd_f32.cu", "fwd_bf16.cu", "decode.cu", "bwd.cu", "bwd_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -15,7 +15,7 @@ inline int chunk_most(int N, int max_new, int max_len) {   // new tokens of a se
   const int n = max_new < N ? max_new : N;
   return n < max_len ? n : max_len;
 }
-size_t chunk_workspace(int S, int Hq, int Hkv, int d, long long N, int max_new, int dtype);
+size_t chunk_workspace(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len, int dtype);
 int launch_paged_chunk(const PagedChunk &p, cudaStream_t stream);
 }  // namespace da
 
@@ -338,7 +338,7 @@ size_t dilution_attn_paged_chunk_workspace_size(int S, int Hq, int Hkv, int d, i
   if (S < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || N < 0 || max_new < 0 || max_len < 0 || max_len > kMaxTokens ||
       !head_dim_supported(d))
     return 0;
-  return chunk_workspace(S, Hq, Hkv, d, N, chunk_most(N, max_new, max_len), dtype);
+  return chunk_workspace(S, Hq, Hkv, d, N, chunk_most(N, max_new, max_len), max_len, dtype);
 }
 
 int dilution_attn_paged_chunk(const void *q, const dilution_attn_paged_cache *cache, const int32_t *cu_tokens, int N,
@@ -356,7 +356,7 @@ int dilution_attn_paged_chunk(const void *q, const dilution_attn_paged_cache *ca
   if (q == nullptr || out == nullptr || !aligned(q, 16) || !aligned(out, 16)) return DA_ERR_INVALID;
   if (cu_tokens == nullptr || !aligned(cu_tokens, 4)) return DA_ERR_INVALID;
   max_new = chunk_most(N, max_new, max_len);
-  st = check_workspace(workspace, workspace_bytes, chunk_workspace(c.S, c.Hq, c.Hkv, c.d, N, max_new, c.dtype));
+  st = check_workspace(workspace, workspace_bytes, chunk_workspace(c.S, c.Hq, c.Hkv, c.d, N, max_new, max_len, c.dtype));
   if (st != DA_OK) return st;
   if (status != nullptr && !aligned(status, 256)) return DA_ERR_INVALID;
   PagedChunk p{};

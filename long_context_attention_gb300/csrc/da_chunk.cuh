@@ -86,7 +86,10 @@ struct ChunkPlan {
   long long rows;        // rows of all heads, at most
   int cta_rows;          // rows of a CTA's places
   size_t seq_off, cum_off, ml_a, ml_b, nl, acc_a, acc_b, total;
+  size_t logits;         // q . k of (token, query head) and key, where they are kept
+  int logits_ld;         // their keys (0: not kept)
 };
+constexpr int kChunkLogits = 128;   // their keys are a multiple of this, a key tile of bf16
 
 inline ChunkPlan chunk_plan(int S, int Hq, int Hkv, int d, long long N, int max_new, int page_size, int edge, int ctas_keys,
                             int ctas_values, ChunkCost cost) {

@@ -292,11 +292,11 @@ cudaError_t launch_chunk_combine(const PagedChunk &p, const ChunkPlan &w, cudaSt
 
 // The plans of the types: edge, CTAs of the passes, costs (see the kernels).
 ChunkPlan chunk_plan_f32(int S, int Hq, int Hkv, int d, long long N, int max_new, int page_size);
-ChunkPlan chunk_plan_bf16(int S, int Hq, int Hkv, int d, long long N, int max_new, int page_size);
+ChunkPlan chunk_plan_bf16(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len, int page_size);
 
-size_t chunk_workspace(int S, int Hq, int Hkv, int d, long long N, int max_new, int dtype) {
+size_t chunk_workspace(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len, int dtype) {
   return (dtype == DA_F32 ? chunk_plan_f32(S, Hq, Hkv, d, N, max_new, 16)
-                          : chunk_plan_bf16(S, Hq, Hkv, d, N, max_new, 16)).total;
+                          : chunk_plan_bf16(S, Hq, Hkv, d, N, max_new, max_len, 16)).total;
 }
 
 int launch_paged_chunk(const PagedChunk &p, cudaStream_t stream) {

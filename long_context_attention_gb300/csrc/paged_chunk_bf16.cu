@@ -40,11 +40,21 @@ bool make_rows_map(CUtensorMap *m, const void *base, int64_t n, int heads, int d
 constexpr int kCkxEdge = 128;
 constexpr int kCkxKeyCtas = 304, kCkxValueCtas = 152;
 constexpr uint32_t kCkxHalf = 128 * 128;   // 128 rows x 64 bf16
+static_assert(kChunkLogits == kCkxEdge, "kept logits are whole key tiles");
 
-ChunkPlan chunk_plan_bf16(int S, int Hq, int Hkv, int d, long long N, int max_new, int page_size) {
+bool chunk_few(int Hq, int Hkv, long long N, int max_new, int max_len, int dtype);   // paged_chunk_few.cu
+cudaError_t launch_chunk_few(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream);
+
+ChunkPlan chunk_plan_bf16(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len, int page_size) {
   // a unit is 8 rows of a key tile, about 40 ns
-  return chunk_plan(S, Hq, Hkv, d, N, max_new, page_size, kCkxEdge, kCkxKeyCtas, kCkxValueCtas,
-                    ChunkCost{d == 128 ? 28 : 14, 3, 1, 64, 16});
+  ChunkPlan w = chunk_plan(S, Hq, Hkv, d, N, max_new, page_size, kCkxEdge, kCkxKeyCtas, kCkxValueCtas,
+                           ChunkCost{d == 128 ? 28 : 14, 3, 1, 64, 16});
+  if (chunk_few(Hq, Hkv, N, max_new, max_len, DA_BF16)) {
+    w.logits = w.total;
+    w.logits_ld = (int)round_up(max_len, kChunkLogits);
+    w.total += (size_t)N * Hq * w.logits_ld * 4;
+  }
+  return w;
 }
 
 // A column tile of a piece, as the producer describes it.
@@ -54,6 +64,7 @@ struct CkxTile {
   int s, hkv, hq0;     // sequence, key head, query head of row 0
   int n8, n, i0;       // rows of a head (0: one head); queries; query of row 0
   int P, len;          // place of query 0; length
+  int tok0;            // query 0 among all
   int rows;            // 0: no more
   int tile, end, t0;   // key tiles; number of the first among the CTA's
   __device__ __forceinline__ int query(int c) const { return n8 ? c % n8 : i0 + c; }
@@ -126,6 +137,7 @@ struct CkxWalk {
     x.hkv = k.hkv(w);
     x.n = k.g.n;
     x.P = k.g.P;
+    x.tok0 = k.q.tok0;
     x.len = k.g.len;
     if (k.g.wide) {
       x.n8 = 0;
@@ -174,7 +186,9 @@ struct CkxKeys {
   static constexpr int kTmemCols = 256;                // two S buffers of 128 columns; two CTAs an SM
 };
 
-template <int D>
+// KEEP: the logits are kept for a second pass that does not read the keys again
+// (paged_chunk_few.cu).
+template <int D, bool KEEP>
 __global__ void __launch_bounds__(CkxKeys<D>::kThreads, 2)
     ckx_keys(PagedChunk p, ChunkPlan w, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap) {
   using C = CkxKeys<D>;
@@ -309,13 +323,22 @@ __global__ void __launch_bounds__(CkxKeys<D>::kThreads, 2)
       float c2 = 1e-30f;
       if (valid)
         c2 = fmaxf(head_c2(p.hs, x.s * p.c.Hq + x.hq0 + (x.n8 ? c / x.n8 : 0), g == 0 ? p.status : nullptr), 1e-30f);
+      float *kept = nullptr;
+      if (KEEP && valid)
+        kept = reinterpret_cast<float *>(p.ws + w.logits) +
+               ((size_t)(x.tok0 + q) * p.c.Hq + x.hq0 + (x.n8 ? c / x.n8 : 0)) * (size_t)w.logits_ld + first * kCkxEdge;
       __syncwarp();
       if (lane == 0) mbar_arrive(&r_free[i % kCkxRing]);
       if (rows == 0) break;
       const bool work = quarter * 32 < rows;   // uniform over the warp
       float m = -INFINITY;
       float2 l0 = make_float2(0.f, 0.f), l1 = make_float2(0.f, 0.f);
-      auto take = [&](float (&v)[32], int left) {   // 32 keys, of which the row sees `left`
+      auto take = [&](float (&v)[32], int left, int key) {   // 32 keys (from `key` of the piece), of which the row sees `left`
+        if (KEEP && left > 0) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4 *>(kept + key + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+        }
         if (left < 32) {
           if (left <= 0) return;
 #pragma unroll
@@ -355,16 +378,16 @@ __global__ void __launch_bounds__(CkxKeys<D>::kThreads, 2)
           tmem_ld32(ts, a);
           tmem_wait_ld_r(a);
           tmem_ld32(ts + 32, b);
-          take(a, left);
+          take(a, left, j * kCkxEdge);
           tmem_wait_ld_r(b);
           tmem_ld32(ts + 64, a);
-          take(b, left - 32);
+          take(b, left - 32, j * kCkxEdge + 32);
           tmem_wait_ld_r(a);
           tmem_ld32(ts + 96, b);
-          take(a, left - 64);
+          take(a, left - 64, j * kCkxEdge + 64);
           tmem_wait_ld_r(b);
           ckx_release(&s_free[g], lane);
-          take(b, left - 96);
+          take(b, left - 96, j * kCkxEdge + 96);
         } else {
           ckx_release(&s_free[g], lane);
         }
@@ -1027,13 +1050,16 @@ template <int D>
 static int launch_ckx(const PagedChunk &p, cudaStream_t stream) {
   static PerDeviceOnce once;
   const int prep = once.run([] {
-    if (cudaFuncSetAttribute(ckx_keys<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, CkxKeys<D>::kSmemBytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(ckx_keys<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, CkxKeys<D>::kSmemBytes) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(ckx_keys<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, CkxKeys<D>::kSmemBytes) !=
+            cudaSuccess)
       return DA_ERR_CUDA;
     const int st = ckx_prepare_values<D, false>();
     return st != DA_OK ? st : ckx_prepare_values<D, true>();
   });
   if (prep != DA_OK) return prep;
-  const ChunkPlan w = chunk_plan_bf16(p.c.S, p.c.Hq, p.c.Hkv, D, p.N, p.max_new, p.c.page_size);
+  const ChunkPlan w = chunk_plan_bf16(p.c.S, p.c.Hq, p.c.Hkv, D, p.N, p.max_new, p.max_len, p.c.page_size);
   const int64_t num = (int64_t)p.c.num_pages * p.c.Hkv;
   CUtensorMap qm, km, vm;
   // (an empty pool has no pages to map: every page id then fails its check)
@@ -1042,12 +1068,14 @@ static int launch_ckx(const PagedChunk &p, cudaStream_t stream) {
       !make_page_map(&vm, p.c.v_pages, num > 0 ? num : 1, p.c.page_size, kCkxEdge, D, DA_BF16))
     return DA_ERR_CUDA;
   using V = CkxVal<D>;
+  const bool few = w.logits_ld > 0;
   if (launch_chunk_plan(p, w, stream) != cudaSuccess ||
-      launch_after(ckx_keys<D>, w.ctas_keys, CkxKeys<D>::kThreads, CkxKeys<D>::kSmemBytes, stream, p, w, qm, km) !=
-          cudaSuccess ||
+      launch_after(few ? ckx_keys<D, true> : ckx_keys<D, false>, w.ctas_keys, CkxKeys<D>::kThreads, CkxKeys<D>::kSmemBytes, stream,
+                   p, w, qm, km) != cudaSuccess ||
       launch_chunk_join(p, w, stream) != cudaSuccess ||
-      (p.earlier ? launch_after(ckx_values<D, true>, w.ctas_values, V::kThreads, V::kSmemBytes, stream, p, w, qm, km, vm)
-                 : launch_after(ckx_values<D, false>, w.ctas_values, V::kThreads, V::kSmemBytes, stream, p, w, qm, km, vm)) !=
+      (few         ? launch_chunk_few(p, w, stream)
+       : p.earlier ? launch_after(ckx_values<D, true>, w.ctas_values, V::kThreads, V::kSmemBytes, stream, p, w, qm, km, vm)
+                   : launch_after(ckx_values<D, false>, w.ctas_values, V::kThreads, V::kSmemBytes, stream, p, w, qm, km, vm)) !=
           cudaSuccess ||
       launch_chunk_combine(p, w, stream) != cudaSuccess)
     return DA_ERR_CUDA;
