@@ -4,12 +4,14 @@
 // paged_chunk_bf16.cu, and their sums are those of the rounded shares.
 //
 // What bounds it: HBM.  A key head's group has few rows (drafted tokens), so that the
-// cache is read for little work: what the kernel for many rows does, K once more for
-// the same logits, costs half of its bytes.  Here the first pass keeps the logits
-// (ckx_keys), 4 bytes a row and key for K's 2 d.  A warp works alone: 32 keys at a time,
-// their values, logits and totals copied asynchronously some steps ahead, one key a lane
-// for bids, shares and totals, m16n8k16 products for share^T V (2 % of the time; tcgen05's
-// 128 rows would be mostly padding).  The warps' sums meet at a piece's end, in order.
+// cache is read for little work, and half of what the kernel for many rows reads is K,
+// for the logits that the first pass has had.  Here that pass keeps them (ckx_keys), 4
+// bytes a row and key for K's 2 d.  A warp works alone, on every kWarps-th 32 keys: their
+// values, logits and totals are copied asynchronously a step ahead; a lane has a key for
+// bids, shares and totals; m16n8k16 forms share^T V (tcgen05's 128 rows would be mostly
+// padding).  The warps' sums meet at a piece's end, in their order.
+// 8 x 12 x 131072, 4 tokens, d = 64: 300 us, 6.4 TB/s of values, logits and totals;
+// the first pass 288, 6.3 TB/s of keys and logits.
 #include "da_chunk.cuh"
 #include "da_paged_plan.cuh"
 
@@ -21,7 +23,7 @@ constexpr int kCklKeys = 32, kCklRows = 16;   // keys of a step; rows of a group
 
 template <int D, int ROWS>
 struct Ckl {
-  static constexpr int kWarps = D == 64 ? (ROWS == 8 ? 16 : 12) : (ROWS == 8 ? 10 : 8);   // what shared memory holds
+  static constexpr int kWarps = D == 64 ? 16 : ROWS == 8 ? 10 : 8;     // what shared memory holds (16 of 8: 300 us for 557)
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kOffX = kCklKeys * D * 2;                       // a stage: values, logits, totals
   static constexpr int kOffT = kOffX + ROWS * kCklKeys * 4;
@@ -33,11 +35,16 @@ struct Ckl {
   static_assert(kSmemBytes <= 231424 && ROWS * kLd * 4 <= kWarp, "shared memory");
 };
 
-// Whether a call's logits are kept: a key head's group has at most 16 rows, and they
-// take at most 2 GB of workspace.
-bool chunk_few(int Hq, int Hkv, long long N, int max_new, int max_len, int dtype) {
-  return dtype == DA_BF16 && (long long)(Hq / Hkv) * max_new <= kCklRows &&
-         N * Hq * round_up(max_len, kChunkLogits) * 4 <= 2ll << 30;
+// Whether a call's logits are kept: a key head's group has at most d / 8 rows, whose
+// logits, written and read, are half of the bytes of K, and they take at most 2 GB of
+// workspace.  Times in us of both second passes' calls (sequences x query / key heads x
+// keys, new tokens; kept / not):
+//   d = 64, 8 x 12/12 x 131072: 1 583 / 838, 4 620 / 818, 8 699 / 834, 16 1167 / 844;
+//     8 x 12/4 x 32768: 1 113 / 139, 2 116 / 140, 5 (15 rows) 140 / 138;
+//     64 x 12/12 x 4096: 4 215 / 277, 16 337 / 281; 1 x 12/12 x 16384: 4 62 / 67;
+//   d = 128, 8 x 16/4 x 131072: 4 (16 rows) 547 / 614; 4 x 32/2 x 65536: 1 (16 rows) 155 / 265.
+bool chunk_few(int Hq, int Hkv, int d, long long N, int max_new, int max_len, int dtype) {
+  return dtype == DA_BF16 && (long long)(Hq / Hkv) * max_new * 8 <= d && N * Hq * round_up(max_len, kChunkLogits) * 4 <= 2ll << 30;
 }
 
 __device__ __forceinline__ void ckl_copy(uint32_t dst, const void *src, bool have) {   // zeros where !have
@@ -206,9 +213,8 @@ static cudaError_t launch_ckl(const PagedChunk &p, const ChunkPlan &w, cudaStrea
   return launch_after(ckl_values<D, ROWS>, w.ctas_values, C::kThreads, C::kSmemBytes, stream, p, w);
 }
 cudaError_t launch_chunk_few(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream) {
-  const bool eight = w.G * p.max_new <= 8;
-  return p.c.d == 128 ? (eight ? launch_ckl<128, 8>(p, w, stream) : launch_ckl<128, 16>(p, w, stream))
-                      : (eight ? launch_ckl<64, 8>(p, w, stream) : launch_ckl<64, 16>(p, w, stream));
+  if (p.c.d == 64) return launch_ckl<64, 8>(p, w, stream);
+  return w.G * p.max_new <= 8 ? launch_ckl<128, 8>(p, w, stream) : launch_ckl<128, 16>(p, w, stream);
 }
 
 }  // namespace da

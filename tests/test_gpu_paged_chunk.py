@@ -131,12 +131,46 @@ def test_long(d, dtype):
 
 @pytest.mark.parametrize("d,Hq,Hkv,page,lens,news", [
     (64, 12, 12, 64, [40000], [4]), (64, 6, 6, 16, [30000, 5000], [5, 130]), (64, 8, 2, 32, [20000], [150]),
-    (128, 12, 4, 256, [40000], [3]), (128, 6, 6, 64, [25000, 300], [140, 300]),
+    (128, 12, 4, 256, [40000], [3]), (128, 6, 6, 64, [25000, 300], [140, 300]), (64, 12, 12, 64, [40000], [10]),
+    (128, 12, 4, 16, [40000], [9]),
 ])
 def test_long_pieces(d, Hq, Hkv, page, lens, news):
     """A dozen key tiles and several column tiles a piece: every order of the rings, of all remainders."""
     cache, q, cu = make(lens, news, Hq, Hkv, d, page, "bf16", seed=d + lens[0])
     run(cache, q, cu, max(news), max(lens))
+
+
+@pytest.mark.parametrize("flags", [0, 1])
+@pytest.mark.parametrize("d,Hq,Hkv,page,news", [
+    (64, 8, 8, 16, [8, 1, 3]), (64, 8, 1, 32, [1, 0, 1]), (64, 6, 2, 64, [2, 1, 2]), (128, 16, 1, 16, [1, 1, 0]),
+    (128, 8, 2, 256, [4, 2, 3]), (128, 3, 3, 32, [16, 9, 1]), (128, 12, 4, 128, [5, 0, 4]), (128, 6, 6, 64, [7, 8, 1]),
+])
+def test_few_rows(d, Hq, Hkv, page, news, flags):
+    """Up to d / 8 rows a key head over lengths past the one-launch kernel's, with odd ends and pages inside a tile."""
+    lens = [5003, 2700, 31]
+    cache, q, cu = make(lens, news, Hq, Hkv, d, page, "bf16", seed=d + Hq, junk=float("nan"), pad=2)
+    tau = torch.rand(3 * Hq, generator=torch.Generator().manual_seed(3)).mul_(2).to(DEV)
+    start = cache.demand_pages.clone()
+    out = run(cache, q, cu, max(news), 5003, flags=flags, tau_bh=tau)
+    total = cache.demand_pages.clone()
+    cache.demand_pages.copy_(start)
+    again = b.dilution_attn_paged_chunk(q, cache, cu, max(news), 5003, flags=flags, tau_bh=tau)
+    n = int(cu[-1])
+    assert torch.equal(out[:n], again[:n]) and torch.equal(cache.demand_pages.view(torch.int32), total.view(torch.int32))
+
+
+def test_few_rows_with_bad_pages():
+    lens, news = [2700, 2800, 2650], [2, 3, 1]
+    for name in ("page_table", "demand_table"):
+        for bad in (-1, 10 ** 9, -2 ** 31):
+            cache, q, cu = make(lens, news, 4, 2, 64, 32, "bf16", seed=44)
+            ro, rD, info = oracle(cache, q, cu)
+            getattr(cache, name)[1, 50:53] = bad
+            ws = b.dilution_attn_paged_chunk_workspace(cache, 6, 3, 2800)
+            out = b.dilution_attn_paged_chunk(q, cache, cu, 3, 2800, workspace=ws)
+            assert b.dilution_attn_get_error(ws) == b.DA_ERR_INVALID
+            got = host64(out)
+            assert np.abs(got[:2] - ro[:2]).max() < 0.05 and np.abs(got[5:] - ro[5:]).max() < 0.05
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
