@@ -940,7 +940,7 @@ def dilution_attn_paged_evict(cache, keep, max_keep: int, max_len: int, new_lens
     lens_shape = cache.seq_lens.shape
     _fit(keep, "keep", lens_shape, torch.int32, dev)
     if new_lens is None:
-        new_lens = torch.empty(lens_shape, dtype=torch.int32, device=cache.device) if stream is None else \
+        new_lens = torch.empty_like(cache.seq_lens) if stream is None else \
             _new(lens_shape, torch.int32, cache.device, stream)
     else:
         _fit(new_lens, "new_lens", lens_shape, torch.int32, dev)

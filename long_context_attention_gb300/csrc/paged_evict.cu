@@ -586,13 +586,26 @@ __global__ void __launch_bounds__(kMoveThreads, 3) evict_move(EvictArgs a, Evict
 constexpr int kSmallKeys = 512, kSmallThreads = kSmallKeys, kSmallLoads = 8;
 __global__ void __launch_bounds__(kSmallThreads) evict_small(EvictArgs a, int sh) {
   __shared__ int s_list[kSmallKeys], s_warp[kSmallThreads / 32];
+  __shared__ int s_page[4][kSmallKeys / 16];   // of keys and values, of totals: from, and where to
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int s = blockIdx.x / a.c.Hkv, h = blockIdx.x % a.c.Hkv, G = a.c.Hq / a.c.Hkv;
   pdl_wait();
   pdl_launch_dependents();
+  // tables and lengths at once: one after the other they were 1.3 us
+  const bool same = a.dst_page_table == nullptr;
+  if (tid < 4 * (kSmallKeys / 16)) {
+    const int which = tid / (kSmallKeys / 16), i = tid % (kSmallKeys / 16);
+    const int tokens = which < 2 || same ? a.max_len : min(a.max_keep, a.max_len), width = which < 2 || same ? a.c.max_pages : a.dst_max_pages;
+    const int32_t *table = which == 0 || (same && which == 2) ? a.c.page_table
+                           : which == 1 || same               ? a.c.demand_table
+                           : which == 2                       ? a.dst_page_table
+                                                              : a.dst_demand_table;
+    s_page[which][i] = i << sh < tokens ? __ldcg(table + (size_t)s * width + i) : -1;
+  }
   const int len = __ldcg(a.c.seq_lens + s), keep = __ldcg(a.keep + s);
   const bool good = len >= 0 && len <= a.max_len && keep >= 0 && min(len, keep) <= a.max_keep;
   const int m = good ? min(len, keep) : 0;
+  __syncthreads();
   if (h == 0 && tid == 0) {
     if (!good) atomicCAS(a.status, DA_OK, DA_ERR_INVALID);
     a.new_lens[s] = good ? m : len;   // (no other block reads it: see launch_evict)
@@ -601,11 +614,10 @@ __global__ void __launch_bounds__(kSmallThreads) evict_small(EvictArgs a, int sh
   if (kept != nullptr)
     for (int i = m + tid; i < a.max_keep; i += kSmallThreads) kept[i] = -1;
   if (m == 0) return;
-  const int32_t *dtab = a.c.demand_table + (size_t)s * a.c.max_pages;
   const int in_page = (1 << sh) - 1;
   uint32_t key = 0;   // below every score
   if (tid < len && m < len) {
-    const int page = __ldcg(dtab + (tid >> sh));
+    const int page = s_page[1][tid >> sh];
     float v = 0.f;
     if ((unsigned)page < (unsigned)a.c.num_demand_pages) {
       const float *at = a.c.demand_pages + ((((size_t)page * a.c.Hq + (size_t)h * G) << sh) + (tid & in_page));
@@ -651,9 +663,13 @@ __global__ void __launch_bounds__(kSmallThreads) evict_small(EvictArgs a, int sh
     if (kept != nullptr) kept[place] = tid;
   }
   __syncthreads();
-  const bool same = a.dst_page_table == nullptr;
-  const int32_t *psrc = a.c.page_table + (size_t)s * a.c.max_pages, *pdst = same ? psrc : a.dst_page_table + (size_t)s * a.dst_max_pages;
-  const int32_t *ddst = same ? dtab : a.dst_demand_table + (size_t)s * a.dst_max_pages;
+  // the row of a place: -1 without a page (recorded)
+  auto row_of = [&](int table, int t, int num_pages) -> long long {
+    const int page = s_page[table][t >> sh];
+    if ((unsigned)page < (unsigned)num_pages) return ((long long)page << sh) | (t & in_page);
+    atomicCAS(a.status, DA_OK, DA_ERR_INVALID);
+    return -1;
+  };
   const MovePieces<kSmallThreads> x(a, h, sh);
   const int rows = kSmallThreads * kSmallLoads >> x.shift;   // of a batch
   for (int r0 = 0, g = 0; r0 < m || g < G; r0 += rows, g += 4) {
@@ -668,7 +684,7 @@ __global__ void __launch_bounds__(kSmallThreads) evict_small(EvictArgs a, int sh
       out[u] = nullptr;
       if (r >= m) continue;
       const int t = s_list[r];
-      const long long i = ev_row(psrc, t, sh, a.c.num_pages, a.status), o = ev_row(pdst, r, sh, a.c.num_pages, a.status);
+      const long long i = row_of(0, t, a.c.num_pages), o = row_of(2, r, a.c.num_pages);
       if (i < 0 || o < 0 || i == o) continue;
       v[u] = __ldcg(x.at(i, u));
       out[u] = x.at(o, u);
@@ -677,8 +693,7 @@ __global__ void __launch_bounds__(kSmallThreads) evict_small(EvictArgs a, int sh
 #pragma unroll
     for (int e = 0; e < 4; ++e) to[e] = nullptr;
     if (g < G && tid < m) {
-      const long long i = ev_row(dtab, s_list[tid], sh, a.c.num_demand_pages, a.status),
-                      o = ev_row(ddst, tid, sh, a.c.num_demand_pages, a.status);
+      const long long i = row_of(1, s_list[tid], a.c.num_demand_pages), o = row_of(3, tid, a.c.num_demand_pages);
       if (i >= 0 && o >= 0 && i != o) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -727,8 +742,12 @@ int launch_evict(const EvictArgs &a, cudaStream_t stream) {
   const int64_t tickets = items * ((most + rows - 1) / rows) + totals * w.total_chunks;
   if (tickets > 0x7F000000 || items * w.cluster > 0x7FFFFFFF || items * 64 + totals > 0x7FFFFFFF)
     return DA_ERR_UNSUPPORTED;
-  // One launch, unless the lengths are written where blocks still read them.
-  if (a.max_len <= kSmallKeys && !words_meet(a.new_lens, a.c.seq_lens, a.c.S) && !words_meet(a.new_lens, a.keep, a.c.S))
+  // One launch for short sequences whose rows are up to 96 MB, unless the lengths are
+  // written where blocks still read them (us of one launch / two, half of about 500
+  // tokens kept: 12 key heads of d = 64, 1 sequence 12.9 / 16.0, 8 12.9 / 24.2; d = 128, 64 x 4
+  // 27.3 / 38.5, 64 x 12 (100 MB) 67.6 / 67.6, in fp32 (200 MB) 106.5 / 98.3).
+  const int64_t row_bytes2 = 2 * a.c.d * (a.c.dtype == DA_BF16 ? 2 : 4);
+  if (a.max_len <= kSmallKeys && items * most * row_bytes2 <= 96ll << 20 && !words_meet(a.new_lens, a.c.seq_lens, a.c.S) && !words_meet(a.new_lens, a.keep, a.c.S))
     return launch_after(evict_small, dim3((unsigned)items), kSmallThreads, 0, stream, a, sh) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.c.S * a.c.Hkv * w.cluster));
