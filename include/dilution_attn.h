@@ -459,7 +459,8 @@ int dilution_attn_paged_decode_ex(const void *q, const dilution_attn_paged_cache
  * dilution_attn_paged_decode.  status: DEVICE, 256 bytes, 256-byte aligned, zeroed
  * once by the caller, or NULL for the workspace's first 256 bytes.  The workspace is
  * overwritten from byte 256 on: calls that may overlap on the GPU need workspaces
- * of their own.  Repeated calls give equal bits.  Errors as for
+ * of their own.  One that was sized for some N, max_new and max_len serves every call
+ * of this cache within them.  Repeated calls give equal bits.  Errors as for
  * dilution_attn_paged_decode_ex. */
 size_t dilution_attn_paged_chunk_workspace_size(int S, int Hq, int Hkv, int d, int N, int max_new, int max_len, int dtype);
 
@@ -477,7 +478,8 @@ int dilution_attn_paged_chunk(const void *q, const dilution_attn_paged_cache *ca
  * an eviction one row holds different tokens in different key heads: keys carry
  * their rotation, and later tokens need their positions passed to
  * dilution_attn_paged_append.
- *   dst_page_table, dst_demand_table: both NULL: in place.  Otherwise DEVICE
+ *   dst_page_table, dst_demand_table: both NULL: in place (pages that sequences share
+ *       then hold only tokens that every key head of theirs keeps, as below).  Otherwise DEVICE
  *       [S][dst_max_pages] tables of the same pools, dst_max_pages * page_size at
  *       least min(max_keep, max_len), that receive the rows that stay, of
  *       sequences that lose nothing too.  A page named there is one that the call does

@@ -293,10 +293,17 @@ cudaError_t launch_chunk_combine(const PagedChunk &p, const ChunkPlan &w, cudaSt
 // The plans of the types: edge, CTAs of the passes, costs (see the kernels).
 ChunkPlan chunk_plan_f32(int S, int Hq, int Hkv, int d, long long N, int max_new, int page_size);
 ChunkPlan chunk_plan_bf16(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len, int page_size);
+size_t chunk_few_room(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len, long long &tokens, int &most);
 
+// Enough for all calls within these bounds, those that keep their logits among them.
 size_t chunk_workspace(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len, int dtype) {
-  return (dtype == DA_F32 ? chunk_plan_f32(S, Hq, Hkv, d, N, max_new, 16)
-                          : chunk_plan_bf16(S, Hq, Hkv, d, N, max_new, max_len, 16)).total;
+  if (dtype == DA_F32) return chunk_plan_f32(S, Hq, Hkv, d, N, max_new, 16).total;
+  long long tokens;
+  int most;
+  const size_t room = chunk_few_room(S, Hq, Hkv, d, N, max_new, max_len, tokens, most);
+  const size_t few = chunk_plan_bf16(S, Hq, Hkv, d, tokens, most, max_len, 16).total + room;
+  const size_t all = chunk_plan_bf16(S, Hq, Hkv, d, N, max_new, max_len, 16).total;
+  return all > few ? all : few;
 }
 
 int launch_paged_chunk(const PagedChunk &p, cudaStream_t stream) {

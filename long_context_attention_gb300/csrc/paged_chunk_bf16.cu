@@ -42,17 +42,16 @@ constexpr int kCkxKeyCtas = 304, kCkxValueCtas = 152;
 constexpr uint32_t kCkxHalf = 128 * 128;   // 128 rows x 64 bf16
 static_assert(kChunkLogits == kCkxEdge, "kept logits are whole key tiles");
 
-bool chunk_few(int Hq, int Hkv, int d, long long N, int max_new, int max_len, int dtype);   // paged_chunk_few.cu
+bool chunk_few(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len);   // paged_chunk_few.cu
 cudaError_t launch_chunk_few(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream);
 
 ChunkPlan chunk_plan_bf16(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len, int page_size) {
   // a unit is 8 rows of a key tile, about 40 ns
   ChunkPlan w = chunk_plan(S, Hq, Hkv, d, N, max_new, page_size, kCkxEdge, kCkxKeyCtas, kCkxValueCtas,
                            ChunkCost{d == 128 ? 28 : 14, 3, 1, 64, 16});
-  if (chunk_few(Hq, Hkv, d, N, max_new, max_len, DA_BF16)) {
+  if (chunk_few(S, Hq, Hkv, d, N, max_new, max_len)) {   // behind what every call needs
     w.logits = w.total;
     w.logits_ld = (int)round_up(max_len, kChunkLogits);
-    w.total += (size_t)N * Hq * w.logits_ld * 4;
   }
   return w;
 }

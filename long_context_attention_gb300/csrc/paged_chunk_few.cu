@@ -19,6 +19,7 @@
 
 namespace da {
 
+constexpr long long kChunkLogitBytes = 2ll << 30;
 constexpr int kCklKeys = 32, kCklRows = 16;   // keys of a step; rows of a group, at most
 
 template <int D, int ROWS>
@@ -37,14 +38,24 @@ struct Ckl {
 
 // Whether a call's logits are kept: a key head's group has at most d / 8 rows, whose
 // logits, written and read, are half of the bytes of K, and they take at most 2 GB of
-// workspace.  Times in us of both second passes' calls (sequences x query / key heads x
+// workspace (and no sequence's share of the tokens is padding).  Times in us of both second passes' calls (sequences x query / key heads x
 // keys, new tokens; kept / not):
 //   d = 64, 8 x 12/12 x 131072: 1 583 / 838, 4 620 / 818, 8 699 / 834, 16 1167 / 844;
 //     8 x 12/4 x 32768: 1 113 / 139, 2 116 / 140, 5 (15 rows) 140 / 138;
 //     64 x 12/12 x 4096: 4 215 / 277, 16 337 / 281; 1 x 12/12 x 16384: 4 62 / 67;
 //   d = 128, 8 x 16/4 x 131072: 4 (16 rows) 547 / 614; 4 x 32/2 x 65536: 1 (16 rows) 155 / 265.
-bool chunk_few(int Hq, int Hkv, int d, long long N, int max_new, int max_len, int dtype) {
-  return dtype == DA_BF16 && (long long)(Hq / Hkv) * max_new * 8 <= d && N * Hq * round_up(max_len, kChunkLogits) * 4 <= 2ll << 30;
+bool chunk_few(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len) {
+  return (long long)(Hq / Hkv) * max_new * 8 <= d && N <= (long long)S * max_new &&
+         N * Hq * round_up(max_len, kChunkLogits) * 4 <= kChunkLogitBytes;
+}
+// Their room in a workspace that serves all calls within these bounds: of those with
+// the most tokens and rows that keep them.
+size_t chunk_few_room(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len, long long &tokens, int &most) {
+  const int rows = d / 8 / (Hq / Hkv);
+  most = max_new < rows ? max_new : rows;
+  tokens = N < (long long)S * most ? N : (long long)S * most;
+  const long long bytes = tokens * Hq * round_up(max_len, kChunkLogits) * 4;
+  return (size_t)(bytes < kChunkLogitBytes ? bytes : kChunkLogitBytes);
 }
 
 __device__ __forceinline__ void ckl_copy(uint32_t dst, const void *src, bool have) {   // zeros where !have

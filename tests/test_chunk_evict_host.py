@@ -56,6 +56,13 @@ def test_chunk_workspace_size(lib):
         assert size(2, 4, 2, 64, 500, 50, 7, dt) == size(2, 4, 2, 64, 500, 7, 7, dt)      # nor more than its length
         assert size(4, 4, 2, 64, 500, 50, 100, dt) >= size(2, 4, 2, 64, 500, 50, 100, dt)
         assert size(64, 64, 2, 128, 1 << 20, 1 << 20, 1 << 20, dt) > 1 << 33              # past 32 bits
+        # a workspace serves every call within its bounds
+        for hq, hkv, d in ((12, 12, 64), (16, 4, 128), (32, 1, 64), (8, 8, 128)):
+            for S in (1, 7, 300):
+                steps = ((1, 1, 1), (3, 1, 100), (5, 3, 5000), (8, 8, 5000), (9, 8, 131072), (300, 8, 131072), (300, 16, 131072),
+                         (4000, 16, 131072), (4000, 2048, 131072), (4000, 2048, 1 << 22), (40000, 40000, 1 << 24))
+                sizes = [size(S, hq, hkv, d, *x, dt) for x in steps]
+                assert sizes == sorted(sizes), (S, hq, hkv, d)
 
 
 def test_evict_refusals(lib):
@@ -82,6 +89,10 @@ def test_evict_workspace_size(lib):
     assert size(-1, 1, 5, 5) == size(1, 0, 5, 5) == size(1, 1, -1, 5) == size(1, 1, 5, -1) == size(1, 1, 5, (1 << 30) + 1) == 0
     assert size(2, 3, 500, 100) == size(2, 3, 100, 100)
     assert size(64, 64, 1 << 20, 1 << 20) > 1 << 33
+    for S, hkv in ((1, 1), (3, 12), (200, 4)):       # a workspace serves every call within its bounds
+        sizes = [size(S, hkv, *x) for x in ((0, 1), (1, 1), (5, 500), (500, 500), (500, 513), (500, 40000), (500, 1 << 19), (500, 1 << 20),
+                                            (1 << 19, 1 << 20), (1 << 19, 1 << 24))]
+        assert sizes == sorted(sizes), (S, hkv)
 
 
 def rand_cache(g, lens, Hq, Hkv, d, page):

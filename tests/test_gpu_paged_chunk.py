@@ -159,6 +159,23 @@ def test_few_rows(d, Hq, Hkv, page, news, flags):
     assert torch.equal(out[:n], again[:n]) and torch.equal(cache.demand_pages.view(torch.int32), total.view(torch.int32))
 
 
+def test_one_workspace_for_all_calls():
+    """A workspace sized for long parts serves drafts, single tokens and a padded batch."""
+    news = [[130, 70, 200], [4, 3, 1], [1, 1, 1], [5, 4, 5], [2, 0, 4]]
+    caches = [make([5000, 2700, 400], n, 6, 3, 64, 32, "bf16", seed=45 + i, pad=i) for i, n in enumerate(news)]
+    ws = b.dilution_attn_paged_chunk_workspace(caches[0][0], 412, 200, 5000)
+    for (cache, q, cu), n in zip(caches, news):
+        start = cache.demand_pages.clone()
+        ref = b.dilution_attn_paged_chunk(q, cache, cu, max(n), 5000)
+        total = cache.demand_pages.clone()
+        cache.demand_pages.copy_(start)
+        ws[256:] = 0xC7
+        out = b.dilution_attn_paged_chunk(q, cache, cu, max(n), 5000, workspace=ws)
+        used = int(cu[-1])
+        assert torch.equal(out[:used], ref[:used]) and torch.equal(cache.demand_pages, total)
+        assert b.dilution_attn_get_error(ws) == b.DA_OK
+
+
 def test_few_rows_with_bad_pages():
     lens, news = [2700, 2800, 2650], [2, 3, 1]
     for name in ("page_table", "demand_table"):
