@@ -479,6 +479,13 @@ __device__ __forceinline__ void ckx_put(uint32_t at, uint32_t a, uint32_t b, uin
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// The denominators' first part: 1e18 at most, so that the product of two is finite and an
+// infinite total leaves its key no share to speak of; NaN stays.
+__device__ __forceinline__ float ckx_den(float total, float eps) {
+  const float d = total + eps;
+  return d > 1e18f ? 1e18f : d;
+}
+
 // 32 rows of one key (its logits; -infinity where a row does not see it): bids, then
 // shares as bf16 pairs.  `added`: what the column tile's rows have added to the key's total so
 // far, a sum of its own (a total of 1 would lose half of the bits of bids of 10^-5);
@@ -888,7 +895,8 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
             if (next_at != nullptr) next_total = __ldcg(next_at);
           }
           const bool mask = (j + 1) * kCkxEdge - 1 > first || rows < kCkxEdge;
-          const float2 base = make_float2(total + p.eps, total + p.eps);
+          const float den = ckx_den(total, p.eps);
+          const float2 base = make_float2(den, den);
           float added = 0.f;
           uint32_t nl[4], to[4];
 #pragma unroll
@@ -973,7 +981,8 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
             else
               ckx_release(&s_free[g], lane);
             uint32_t pk[4];
-            const float2 b2 = make_float2(total + p.eps, total + p.eps);
+            const float den = ckx_den(total, p.eps);
+            const float2 b2 = make_float2(den, den);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               d[e] = added;

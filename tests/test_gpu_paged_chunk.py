@@ -512,6 +512,25 @@ def test_pools_past_32_bits(lens, news, dtype):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,news", [([300, 90], [4, 2]), ([300, 90], [20, 3]), ([700, 90], [130, 5])])
+def test_infinite_totals(lens, news, dtype):
+    """Keys with an infinite total take part in the softmax and have no share; their totals stay."""
+    cache, q, cu = make(lens, news, 4, 2, 64, 32, dtype, seed=95)
+    t = torch.arange(5, 60, 3, device=DEV)
+    at = cache.demand_table[0, t // 32].long(), slice(None), t % 32
+    cache.demand_pages[at] = float("inf")
+    cache.demand_pages[cache.demand_table[1, 0].long(), 1, 7] = 3e38
+    start = cache.demand_pages.clone()
+    with np.errstate(invalid="ignore", over="ignore"):
+        ro = oracle(cache, q, cu)[0]
+    for max_len in (max(lens), LONG):
+        cache.demand_pages.copy_(start)
+        out = b.dilution_attn_paged_chunk(q, cache, cu, max(news), max_len)
+        assert np.abs(host64(out) - ro).max() < (0.05 if dtype == "bf16" else 1e-4)
+        assert (cache.demand_pages[at] == float("inf")).all() and not torch.isnan(cache.demand_pages).any()
+
+
 def test_serving_run_together():
     """Rotation, append and chunk of ragged prompts, a second chunk behind them, eviction, single tokens and a decode step:
     the calls of a serving loop, each against the oracle on the cache as it then is."""
