@@ -359,7 +359,7 @@ def test_sharp_and_extreme_logits(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("S,wide", [(33, 0), (33, 70), (1100, 0), (1100, 90), (2500, 40)])
+@pytest.mark.parametrize("S,wide", [(33, 0), (33, 70), (128, 70), (129, 70), (1100, 0), (1100, 90), (2500, 40)])
 def test_many_sequences(S, wide, dtype):
     """More sequences than a warp's lanes, and than a block's threads, most of them short, some without new tokens."""
     lens = [s * 7 % 23 for s in range(S)]
