@@ -658,7 +658,8 @@ class PagedCache:
     clears the first bad length or page that they found."""
 
     __slots__ = ("k_pages", "v_pages", "demand_pages", "page_table", "demand_table", "seq_lens", "status", "S", "Hq", "Hkv", "d",
-                 "page_size", "max_pages", "dtype", "device", "_code", "_c", "_ref", "_dev", "_q_shape", "_cu_shape")
+                 "page_size", "max_pages", "dtype", "device", "_code", "_c", "_ref", "_dev", "_q_shape", "_cu_shape",
+                 "_lens_shape")
 
     def __init__(self, k_pages, v_pages, demand_pages, page_table, demand_table, seq_lens):
         _need(k_pages, "k_pages")
@@ -689,6 +690,7 @@ class PagedCache:
         self._ref = ctypes.byref(self._c)
         self.status = _zeroed_status(self.device)
         self._dev, self._q_shape, self._cu_shape = k_pages.get_device(), torch.Size((S, Hq, d)), torch.Size((S + 1,))
+        self._lens_shape = torch.Size((S,))
 
 
 def _need_cache(cache) -> int:
@@ -893,8 +895,7 @@ def dilution_attn_paged_chunk(q, cache, cu_tokens, max_new: int, max_len: int, o
     _fit(q, "q", shape, dtype, dev)
     _fit(cu_tokens, "cu_tokens", cache._cu_shape, torch.int32, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=cache.device) if stream is None else \
-            _new(shape, dtype, cache.device, stream)
+        out = torch.empty_like(q) if stream is None else _new(shape, dtype, cache.device, stream)
     else:
         _fit(out, "out", shape, dtype, dev)
     workspace, status = _call_workspace(
@@ -937,7 +938,7 @@ def dilution_attn_paged_evict(cache, keep, max_keep: int, max_len: int, new_lens
     ``cache.status`` if none is given."""
     lib = _lib or load()
     dev = _need_cache(cache)
-    lens_shape = cache.seq_lens.shape
+    lens_shape = cache._lens_shape
     _fit(keep, "keep", lens_shape, torch.int32, dev)
     if new_lens is None:
         new_lens = torch.empty_like(cache.seq_lens) if stream is None else \
@@ -949,11 +950,13 @@ def dilution_attn_paged_evict(cache, keep, max_keep: int, max_len: int, new_lens
     dp = dd = kp = None
     width = 0
     if dst_page_table is not None:
-        _need(dst_page_table, "dst_page_table", None, torch.int32)
-        if dst_page_table.dim() != 2 or dst_page_table.shape[0] != cache.S:
+        if not isinstance(dst_page_table, _Tensor) or dst_page_table.dim() != 2 or dst_page_table.size(0) != cache.S:
+            _need(dst_page_table, "dst_page_table", None, torch.int32)
             raise ValueError(f"dst_page_table must be [{cache.S}, pages]")
-        _need(dst_demand_table, "dst_demand_table", dst_page_table.shape, torch.int32)
-        dp, dd, width = dst_page_table.data_ptr(), dst_demand_table.data_ptr(), dst_page_table.shape[1]
+        shape = dst_page_table.shape
+        _fit(dst_page_table, "dst_page_table", shape, torch.int32, dev)
+        _fit(dst_demand_table, "dst_demand_table", shape, torch.int32, dev)
+        dp, dd, width = dst_page_table.data_ptr(), dst_demand_table.data_ptr(), shape[1]
     if kept is not None:
         _fit(kept, "kept", (cache.S, cache.Hkv, int(max_keep)), torch.int32, dev)
         kp = kept.data_ptr()
