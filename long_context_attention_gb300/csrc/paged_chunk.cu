@@ -309,7 +309,11 @@ size_t chunk_few_room(int S, int Hq, int Hkv, int d, long long N, int max_new, i
 
 // Enough for all calls within these bounds, those that keep their logits among them.
 size_t chunk_workspace(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len, int dtype) {
-  if (dtype == DA_F32) return chunk_plan_f32(S, Hq, Hkv, d, N, max_new, 16).total;
+  if (dtype == DA_F32) {   // (up to 8 rows on more CTAs)
+    const size_t all = chunk_plan_f32(S, Hq, Hkv, d, N, max_new, 16).total,
+                 eight = chunk_plan_f32(S, Hq, Hkv, d, N, max_new < 8 ? max_new : 8, 16).total;
+    return all > eight ? all : eight;
+  }
   long long tokens;
   int most;
   const size_t room = chunk_few_room(S, Hq, Hkv, d, N, max_new, max_len, tokens, most);

@@ -23,17 +23,23 @@ namespace da {
 
 constexpr int kCkfEdge = 64;
 constexpr int kCkfThreads = 256;
-constexpr int ckf_ctas(int d) { return d == 64 ? 304 : 152; }   // two CTAs an SM, or one
+// CTAs an SM.  `eight`: no column tile of the call has more than 8 rows, and the kernels
+// have that part alone (one kernel for all: 4 % more for many rows, 229 us for 8 x 12 x 8001
+// and 3 tokens; its own, with registers for three CTAs, 195; as up to 16 rows 282; 2 x 12 x
+// 131072 and 4 tokens 648, 774 and 980).
+constexpr int ckf_ctas(int d, bool eight) { return eight ? 3 : d == 64 ? 2 : 1; }
+static bool ckf_eight(int Hq, int Hkv, int max_new) { return (long long)(Hq / Hkv) * round_up(max_new, 8) <= 8; }
 
 ChunkPlan chunk_plan_f32(int S, int Hq, int Hkv, int d, long long N, int max_new, int page_size) {
-  return chunk_plan(S, Hq, Hkv, d, N, max_new, page_size, kCkfEdge, ckf_ctas(d), ckf_ctas(d), ChunkCost{4, 4, 1, 8, 4});
+  const int ctas = 152 * ckf_ctas(d, ckf_eight(Hq, Hkv, max_new));
+  return chunk_plan(S, Hq, Hkv, d, N, max_new, page_size, kCkfEdge, ctas, ctas, ChunkCost{4, 4, 1, 8, 4});
 }
 
-template <int D>
+template <int D, int ROWS = kCkfEdge>
 struct Ckf {
   static constexpr int kLd = D + 4;            // floats of a staged row: lanes of different rows read different banks
   static constexpr int kLdP = kCkfEdge + 4;
-  static constexpr int kSmemBytes = (3 * kCkfEdge * kLd + kCkfEdge * kLdP + 4 * kCkfEdge) * 4;
+  static constexpr int kSmemBytes = (ROWS * (kLd + kLdP) + 2 * kCkfEdge * kLd + 4 * kCkfEdge) * 4;
 };
 
 // A column tile: row c of it is query head hq(c), query i(c).
@@ -60,9 +66,9 @@ struct CkfCols {
   __device__ __forceinline__ bool valid(int c) const { return c < rows && query(c) < n; }
 };
 
-template <int D>
+template <int D, int ROWS>
 __device__ __forceinline__ void ckf_queries(const PagedChunk &p, const ChunkWalk &k, const CkfCols &t, float *sQ) {
-  for (int e = threadIdx.x; e < kCkfEdge * (D / 4); e += kCkfThreads) {
+  for (int e = threadIdx.x; e < ROWS * (D / 4); e += kCkfThreads) {
     const int c = e / (D / 4), x = e % (D / 4);
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (t.valid(c))
@@ -122,29 +128,31 @@ __device__ __forceinline__ float *ckf_total(const PagedChunk &p, const ChunkPlan
 // A thread's part of a tile.  Many rows: 4 rows (4 ty ..) by 4 keys (tx + 16 j).  Up to
 // 16 rows: 4 rows (4 (ty % 4) ..) by one key (16 (ty / 4) + tx), so that all warps work
 // (as many rows: 64 keys by 8 rows in one warp, 223 us for 4 sequences of 1001 .. 8001).
+// Up to 8 rows: 2 rows by one key.
 // Neighbouring lanes have the same key and two groups of rows: half a warp's 16-byte reads
 // of K then fall on 8 places, once over the banks (16 keys a half-warp: twice).
-template <bool FEW>
+template <int MAX>   // rows: 64, or few: 16, 8
 struct CkfPart {
-  static constexpr int kKeys = FEW ? 1 : 4;
+  static constexpr bool kFew = MAX <= 16;
+  static constexpr int kKeys = kFew ? 1 : 4, kRows = MAX == 8 ? 2 : 4;
   int row, key;   // its first row and key
   int tx;         // 0 .. 15
   __device__ __forceinline__ CkfPart() {
     const int ty = threadIdx.x / 32 * 2 + threadIdx.x % 2;
     tx = threadIdx.x % 32 / 2;
-    row = FEW ? 4 * (ty % 4) : 4 * ty;
-    key = FEW ? 16 * (ty / 4) + tx : tx;
+    row = kFew ? kRows * (ty % 4) : 4 * ty;
+    key = kFew ? 16 * (ty / 4) + tx : tx;
   }
 };
 
 // q . k of the thread's part.
-template <int D, bool FEW>
-__device__ __forceinline__ void ckf_products(const float *sQ, const float *sK, float (&x)[4][CkfPart<FEW>::kKeys]) {
-  constexpr int NK = CkfPart<FEW>::kKeys;
-  const CkfPart<FEW> t;
-  float2 acc[4][NK];
+template <int D, int MAX>
+__device__ __forceinline__ void ckf_products(const float *sQ, const float *sK, float (&x)[CkfPart<MAX>::kRows][CkfPart<MAX>::kKeys]) {
+  constexpr int NK = CkfPart<MAX>::kKeys, NR = CkfPart<MAX>::kRows;
+  const CkfPart<MAX> t;
+  float2 acc[NR][NK];
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+  for (int r = 0; r < NR; ++r)
 #pragma unroll
     for (int j = 0; j < NK; ++j) acc[r][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
@@ -153,7 +161,7 @@ __device__ __forceinline__ void ckf_products(const float *sQ, const float *sK, f
 #pragma unroll
     for (int j = 0; j < NK; ++j) kv[j] = *reinterpret_cast<const float4 *>(sK + (t.key + 16 * j) * Ckf<D>::kLd + e);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < NR; ++r) {
       const float4 q = *reinterpret_cast<const float4 *>(sQ + (t.row + r) * Ckf<D>::kLd + e);
 #pragma unroll
       for (int j = 0; j < NK; ++j) {
@@ -163,20 +171,21 @@ __device__ __forceinline__ void ckf_products(const float *sQ, const float *sK, f
     }
   }
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+  for (int r = 0; r < NR; ++r)
 #pragma unroll
     for (int j = 0; j < NK; ++j) x[r][j] = acc[r][j].x + acc[r][j].y;
 }
 
 // The rows of a thread's part: scale, last key that each sees (-1: none), -lse2.
-template <bool FEW>
+template <int MAX>
 struct CkfRows {
-  float c2[4], nl[4];
-  int last[4];
+  static constexpr int NR = CkfPart<MAX>::kRows;
+  float c2[NR], nl[NR];
+  int last[NR];
   __device__ __forceinline__ CkfRows(const PagedChunk &p, const ChunkPlan &w, const ChunkWalk &k, const CkfCols &t, bool first) {
-    const CkfPart<FEW> part;
+    const CkfPart<MAX> part;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < NR; ++r) {
       const int c = part.row + r;
       last[r] = t.valid(c) ? k.g.P + t.query(c) : -1;
       c2[r] = last[r] >= 0 ? head_c2(p.hs, k.s * p.c.Hq + t.head(c), first ? p.status : nullptr) : 0.f;
@@ -192,25 +201,26 @@ __device__ __forceinline__ void ckf_merge(float &m, float &sum, float m2, float 
   m = mn;
 }
 
-template <int D, bool FEW>
+template <int D, int MAX>
 __device__ __forceinline__ void ckf_keys_tile(const PagedChunk &p, const ChunkPlan &w, const ChunkWalk &k, const CkfCols &t, int end,
                                               float *smem) {
   using C = Ckf<D>;
-  constexpr int NK = CkfPart<FEW>::kKeys;
-  float *sQ = smem, *sK = sQ + kCkfEdge * C::kLd;   // two key tiles
-  float2 *s_ml = reinterpret_cast<float2 *>(smem + 3 * kCkfEdge * C::kLd);
-  const CkfPart<FEW> part;
+  constexpr int NK = CkfPart<MAX>::kKeys, NR = CkfPart<MAX>::kRows;
+  constexpr bool FEW = CkfPart<MAX>::kFew;
+  float *sQ = smem, *sK = sQ + (MAX == 8 ? 8 : kCkfEdge) * C::kLd;   // two key tiles
+  float2 *s_ml = reinterpret_cast<float2 *>(sK + 2 * kCkfEdge * C::kLd);
+  const CkfPart<MAX> part;
   const int tx = part.tx, kg = threadIdx.x / 64;
   const bool work = FEW || threadIdx.x / 32 * 8 < t.rows;   // uniform over the warp
   CkfPages<D> pages;
   pages.find(p, w, k, k.tile);
   pages.copy(p, w, k, p.c.k_pages, k.tile, sK);
   if (k.tile + 1 < end) pages.find(p, w, k, k.tile + 1);
-  ckf_queries<D>(p, k, t, sQ);
-  const CkfRows<FEW> rows(p, w, k, t, true);
-  float m[4], sum[4];
+  ckf_queries<D, MAX == 8 ? 8 : kCkfEdge>(p, k, t, sQ);
+  const CkfRows<MAX> rows(p, w, k, t, true);
+  float m[NR], sum[NR];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) m[r] = -INFINITY, sum[r] = 0.f;
+  for (int r = 0; r < NR; ++r) m[r] = -INFINITY, sum[r] = 0.f;
   for (int tile = k.tile; tile < end; ++tile) {
     float *now = sK + ((tile - k.tile) & 1) * kCkfEdge * C::kLd;
     if (tile + 1 < end) {   // into the place of the tile before this one, which has been read
@@ -222,10 +232,10 @@ __device__ __forceinline__ void ckf_keys_tile(const PagedChunk &p, const ChunkPl
     }
     __syncthreads();
     if (work) {
-      float x[4][NK];
-      ckf_products<D, FEW>(sQ, now, x);
+      float x[NR][NK];
+      ckf_products<D, MAX>(sQ, now, x);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
+      for (int r = 0; r < NR; ++r) {
         float mn = m[r];
 #pragma unroll
         for (int j = 0; j < NK; ++j) {
@@ -242,7 +252,7 @@ __device__ __forceinline__ void ckf_keys_tile(const PagedChunk &p, const ChunkPl
     __syncthreads();
   }
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+  for (int r = 0; r < NR; ++r)
 #pragma unroll
     for (int o = 16; o > 1; o >>= 1)
       ckf_merge(m[r], sum[r], __shfl_xor_sync(0xffffffffu, m[r], o), __shfl_xor_sync(0xffffffffu, sum[r], o));
@@ -252,7 +262,7 @@ __device__ __forceinline__ void ckf_keys_tile(const PagedChunk &p, const ChunkPl
   if constexpr (FEW) {   // four threads a row, each with a fourth of the keys
     if (tx == 0)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) s_ml[kg * 16 + part.row + r] = make_float2(m[r], sum[r]);
+      for (int r = 0; r < NR; ++r) s_ml[kg * 16 + part.row + r] = make_float2(m[r], sum[r]);
     __syncthreads();
     if (threadIdx.x < 16 && t.valid(threadIdx.x)) {
       float2 a = s_ml[threadIdx.x];
@@ -263,13 +273,13 @@ __device__ __forceinline__ void ckf_keys_tile(const PagedChunk &p, const ChunkPl
   } else {
     if (tx == 0)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < NR; ++r)
         if (rows.last[r] >= 0) put(part.row + r, make_float2(m[r], sum[r]));
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kCkfThreads, D == 64 ? 2 : 1) ckf_keys(PagedChunk p, ChunkPlan w) {
+template <int D, bool EIGHT>
+__global__ void __launch_bounds__(kCkfThreads, ckf_ctas(D, EIGHT)) ckf_keys(PagedChunk p, ChunkPlan w) {
   extern __shared__ __align__(16) float ckf_smem[];
   pdl_wait();
   pdl_launch_dependents();
@@ -281,10 +291,14 @@ __global__ void __launch_bounds__(kCkfThreads, D == 64 ? 2 : 1) ckf_keys(PagedCh
       const CkfCols t(k, w, b);
       const int end = min(k.end, k.g.seen(b, kCkfEdge));
       __syncthreads();
-      if (t.rows <= 16)
-        ckf_keys_tile<D, true>(p, w, k, t, end, ckf_smem);
-      else
-        ckf_keys_tile<D, false>(p, w, k, t, end, ckf_smem);
+      if constexpr (EIGHT) {
+        ckf_keys_tile<D, 8>(p, w, k, t, end, ckf_smem);
+      } else {
+        if (t.rows <= 16)
+          ckf_keys_tile<D, 16>(p, w, k, t, end, ckf_smem);
+        else
+          ckf_keys_tile<D, 64>(p, w, k, t, end, ckf_smem);
+      }
     }
 }
 
@@ -295,14 +309,16 @@ __device__ __forceinline__ float ckf_share(float bid, float den) {
   return bid > 0.f ? bid * r : bid;
 }
 
-template <int D, bool FEW>
+template <int D, int MAX>
 __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const ChunkPlan &w, const ChunkWalk &k, const CkfCols &t, int end,
                                                 float *smem) {
   using C = Ckf<D>;
-  constexpr int NV = D / 64, NK = CkfPart<FEW>::kKeys;   // 4-column groups, keys of a thread
-  float *sQ = smem, *sK = sQ + kCkfEdge * C::kLd, *sV = sK + kCkfEdge * C::kLd, *sP = sV + kCkfEdge * C::kLd,
-        *sPart = sP + kCkfEdge * C::kLdP;
-  const CkfPart<FEW> part;
+  constexpr int NV = D / 64, NK = CkfPart<MAX>::kKeys, NR = CkfPart<MAX>::kRows;   // 4-column groups, keys and rows of a thread
+  constexpr bool FEW = CkfPart<MAX>::kFew;
+  constexpr int ROWS = MAX == 8 ? 8 : kCkfEdge;
+  float *sQ = smem, *sK = sQ + ROWS * C::kLd, *sV = sK + kCkfEdge * C::kLd, *sP = sV + kCkfEdge * C::kLd,
+        *sPart = sP + ROWS * C::kLdP;
+  const CkfPart<MAX> part;
   const int tid = threadIdx.x, tx = part.tx;
   const bool work = FEW || tid / 32 * 8 < t.rows;   // uniform over the warp
   const int j0 = FEW ? tid / 64 * 16 : 0, j1 = FEW ? j0 + 16 : kCkfEdge;   // keys of the thread's value products
@@ -311,11 +327,11 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
   pages.copy(p, w, k, p.c.k_pages, k.tile, sK);
   pages.copy(p, w, k, p.c.v_pages, k.tile, sV);
   if (k.tile + 1 < end) pages.find(p, w, k, k.tile + 1);
-  ckf_queries<D>(p, k, t, sQ);
-  const CkfRows<FEW> rows(p, w, k, t, false);
-  float num[4][4 * NV], sum[4];
+  ckf_queries<D, MAX == 8 ? 8 : kCkfEdge>(p, k, t, sQ);
+  const CkfRows<MAX> rows(p, w, k, t, false);
+  float num[NR][4 * NV], sum[NR];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
+  for (int r = 0; r < NR; ++r) {
     sum[r] = 0.f;
 #pragma unroll
     for (int e = 0; e < 4 * NV; ++e) num[r][e] = 0.f;
@@ -331,10 +347,10 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
     ckf_landed<1>();   // K (V is the newer group)
     __syncthreads();
     if (work) {
-      float x[4][NK];
-      ckf_products<D, FEW>(sQ, sK, x);
+      float x[NR][NK];
+      ckf_products<D, MAX>(sQ, sK, x);
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int j = 0; j < NK; ++j) {
           const bool sees = tile * kCkfEdge + part.key + 16 * j <= rows.last[r];
@@ -383,9 +399,9 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
     if (work) {
 #pragma unroll 4
       for (int j = j0; j < j1; j += 4) {
-        float4 sh[4];
+        float4 sh[NR];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < NR; ++r) {
           sh[r] = *reinterpret_cast<const float4 *>(sP + (part.row + r) * C::kLdP + j);
           if ((j - j0) / 4 == tx) sum[r] += (sh[r].x + sh[r].y) + (sh[r].z + sh[r].w);
         }
@@ -395,7 +411,7 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const float4 *>(sV + (j + i) * C::kLd + 64 * e + 4 * tx);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
+          for (int r = 0; r < NR; ++r) {
             const float s4[4] = {sh[r].x, sh[r].y, sh[r].z, sh[r].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -414,7 +430,7 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
     }
   }
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+  for (int r = 0; r < NR; ++r)
 #pragma unroll
     for (int o = 16; o > 1; o >>= 1) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], o);
   float *to = chunk_place(p, w.acc_a, w.acc_b, k.row0(p, w), w.cta_rows, k.tile, blockIdx.x, t.r0, acc_stride(D));
@@ -423,7 +439,7 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
     float *stage = sK;   // [fourth][16 rows][d, sum]; the tile's K and V have been read
     static_assert(4 * 16 * LD <= 2 * kCkfEdge * C::kLd, "stage");
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < NR; ++r) {
       float *row = stage + (tid / 64 * 16 + part.row + r) * LD;
 #pragma unroll
       for (int e = 0; e < NV; ++e)
@@ -442,7 +458,7 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
     }
   } else if (work) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < NR; ++r) {
       if (rows.last[r] < 0) continue;
       const int row = part.row + r;
 #pragma unroll
@@ -454,8 +470,8 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kCkfThreads, D == 64 ? 2 : 1) ckf_values(PagedChunk p, ChunkPlan w) {
+template <int D, bool EIGHT>
+__global__ void __launch_bounds__(kCkfThreads, ckf_ctas(D, EIGHT)) ckf_values(PagedChunk p, ChunkPlan w) {
   extern __shared__ __align__(16) float ckf_smem[];
   pdl_wait();
   pdl_launch_dependents();
@@ -467,10 +483,14 @@ __global__ void __launch_bounds__(kCkfThreads, D == 64 ? 2 : 1) ckf_values(Paged
       const CkfCols t(k, w, b);
       const int end = min(k.end, k.g.seen(b, kCkfEdge));
       __syncthreads();
-      if (t.rows <= 16)
-        ckf_values_tile<D, true>(p, w, k, t, end, ckf_smem);
-      else
-        ckf_values_tile<D, false>(p, w, k, t, end, ckf_smem);
+      if constexpr (EIGHT) {
+        ckf_values_tile<D, 8>(p, w, k, t, end, ckf_smem);
+      } else {
+        if (t.rows <= 16)
+          ckf_values_tile<D, 16>(p, w, k, t, end, ckf_smem);
+        else
+          ckf_values_tile<D, 64>(p, w, k, t, end, ckf_smem);
+      }
     }
 }
 
@@ -478,29 +498,30 @@ cudaError_t launch_chunk_plan(const PagedChunk &p, const ChunkPlan &w, cudaStrea
 cudaError_t launch_chunk_join(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream);
 cudaError_t launch_chunk_combine(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream);
 
-template <int D>
+template <int D, bool EIGHT>
 static int launch_ckf(const PagedChunk &p, cudaStream_t stream) {
+  constexpr int bytes = Ckf<D, EIGHT ? 8 : kCkfEdge>::kSmemBytes;
   static PerDeviceOnce once;
   const int prep = once.run([] {
-    return (cudaFuncSetAttribute(ckf_keys<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ckf<D>::kSmemBytes) !=
-                cudaSuccess ||
-            cudaFuncSetAttribute(ckf_values<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ckf<D>::kSmemBytes) !=
-                cudaSuccess)
+    return (cudaFuncSetAttribute(ckf_keys<D, EIGHT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+            cudaFuncSetAttribute(ckf_values<D, EIGHT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
                ? DA_ERR_CUDA
                : DA_OK;
   });
   if (prep != DA_OK) return prep;
   const ChunkPlan w = chunk_plan_f32(p.c.S, p.c.Hq, p.c.Hkv, D, p.N, p.max_new, p.c.page_size);
   if (launch_chunk_plan(p, w, stream) != cudaSuccess ||
-      launch_after(ckf_keys<D>, w.ctas_keys, kCkfThreads, Ckf<D>::kSmemBytes, stream, p, w) != cudaSuccess ||
+      launch_after(ckf_keys<D, EIGHT>, w.ctas_keys, kCkfThreads, bytes, stream, p, w) != cudaSuccess ||
       launch_chunk_join(p, w, stream) != cudaSuccess ||
-      launch_after(ckf_values<D>, w.ctas_values, kCkfThreads, Ckf<D>::kSmemBytes, stream, p, w) != cudaSuccess ||
+      launch_after(ckf_values<D, EIGHT>, w.ctas_values, kCkfThreads, bytes, stream, p, w) != cudaSuccess ||
       launch_chunk_combine(p, w, stream) != cudaSuccess)
     return DA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 int launch_chunk_f32(const PagedChunk &p, cudaStream_t stream) {
-  return p.c.d == 128 ? launch_ckf<128>(p, stream) : launch_ckf<64>(p, stream);
+  if (ckf_eight(p.c.Hq, p.c.Hkv, p.max_new))
+    return p.c.d == 128 ? launch_ckf<128, true>(p, stream) : launch_ckf<64, true>(p, stream);
+  return p.c.d == 128 ? launch_ckf<128, false>(p, stream) : launch_ckf<64, false>(p, stream);
 }
 }  // namespace da

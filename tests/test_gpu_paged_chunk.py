@@ -159,6 +159,14 @@ def test_few_rows(d, Hq, Hkv, page, news, flags):
     assert torch.equal(out[:n], again[:n]) and torch.equal(cache.demand_pages.view(torch.int32), total.view(torch.int32))
 
 
+@pytest.mark.parametrize("flags", [0, 1])
+@pytest.mark.parametrize("d,Hq,page,news", [(64, 5, 16, [8, 1, 3]), (64, 2, 256, [1, 0, 1]), (128, 3, 32, [4, 8, 2]), (128, 1, 128, [0, 7, 0])])
+def test_up_to_eight_rows_in_fp32(d, Hq, page, news, flags):
+    lens = [5003, 2700, 31]
+    cache, q, cu = make(lens, news, Hq, Hq, d, page, "f32", seed=d + Hq, junk=float("nan"), pad=1)
+    run(cache, q, cu, 8, 5003, flags=flags)
+
+
 def test_one_workspace_for_all_calls():
     """A workspace sized for long parts serves drafts, single tokens and a padded batch."""
     news = [[130, 70, 200], [4, 3, 1], [1, 1, 1], [5, 4, 5], [2, 0, 4]]
