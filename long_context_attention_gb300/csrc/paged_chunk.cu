@@ -309,10 +309,11 @@ size_t chunk_few_room(int S, int Hq, int Hkv, int d, long long N, int max_new, i
 
 // Enough for all calls within these bounds, those that keep their logits among them.
 size_t chunk_workspace(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len, int dtype) {
-  if (dtype == DA_F32) {   // (up to 8 rows on more CTAs)
+  if (dtype == DA_F32) {   // up to 16 rows a key head have more CTAs
+    const int few = 16 / (Hq / Hkv) / 8 * 8;
     const size_t all = chunk_plan_f32(S, Hq, Hkv, d, N, max_new, 16).total,
-                 eight = chunk_plan_f32(S, Hq, Hkv, d, N, max_new < 8 ? max_new : 8, 16).total;
-    return all > eight ? all : eight;
+                 some = chunk_plan_f32(S, Hq, Hkv, d, N, max_new < few ? max_new : few, 16).total;
+    return all > some ? all : some;
   }
   long long tokens;
   int most;

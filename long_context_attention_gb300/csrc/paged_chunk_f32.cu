@@ -23,15 +23,19 @@ namespace da {
 
 constexpr int kCkfEdge = 64;
 constexpr int kCkfThreads = 256;
-// CTAs an SM.  `eight`: no column tile of the call has more than 8 rows, and the kernels
-// have that part alone (one kernel for all: 4 % more for many rows, 229 us for 8 x 12 x 8001
-// and 3 tokens; its own, with registers for three CTAs, 195; as up to 16 rows 282; 2 x 12 x
-// 131072 and 4 tokens 648, 774 and 980).
-constexpr int ckf_ctas(int d, bool eight) { return eight ? 3 : d == 64 ? 2 : 1; }
-static bool ckf_eight(int Hq, int Hkv, int max_new) { return (long long)(Hq / Hkv) * round_up(max_new, 8) <= 8; }
+// CTAs an SM, where no column tile of the call has more than `most` rows: up to 8 and up
+// to 16 have kernels of their own, with registers for as many (one kernel for all: 4 % more for
+// many rows; us of 8 x 12 x 8001 with 3 tokens 195, as a part of one kernel 229, as up to 16
+// rows 282; 2 x 12 x 131072 with 4 tokens 648, 774, 980; 8 x 12 x 8001 with 14 tokens 265, in one
+// kernel 292; d = 128, 4 x 12 x 8001 with 14 tokens 270, in one kernel 356, three CTAs 401).
+constexpr int ckf_ctas(int d, int most) { return most <= 8 ? 3 : most <= 16 ? (d == 64 ? 3 : 2) : d == 64 ? 2 : 1; }
+static int ckf_most(int Hq, int Hkv, int max_new) {
+  const long long rows = (long long)(Hq / Hkv) * round_up(max_new, 8);
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : kCkfEdge;
+}
 
 ChunkPlan chunk_plan_f32(int S, int Hq, int Hkv, int d, long long N, int max_new, int page_size) {
-  const int ctas = 152 * ckf_ctas(d, ckf_eight(Hq, Hkv, max_new));
+  const int ctas = 152 * ckf_ctas(d, ckf_most(Hq, Hkv, max_new));
   return chunk_plan(S, Hq, Hkv, d, N, max_new, page_size, kCkfEdge, ctas, ctas, ChunkCost{4, 4, 1, 8, 4});
 }
 
@@ -201,13 +205,13 @@ __device__ __forceinline__ void ckf_merge(float &m, float &sum, float m2, float 
   m = mn;
 }
 
-template <int D, int MAX>
+template <int D, int MAX, int PLACES>
 __device__ __forceinline__ void ckf_keys_tile(const PagedChunk &p, const ChunkPlan &w, const ChunkWalk &k, const CkfCols &t, int end,
                                               float *smem) {
   using C = Ckf<D>;
   constexpr int NK = CkfPart<MAX>::kKeys, NR = CkfPart<MAX>::kRows;
   constexpr bool FEW = CkfPart<MAX>::kFew;
-  float *sQ = smem, *sK = sQ + (MAX == 8 ? 8 : kCkfEdge) * C::kLd;   // two key tiles
+  float *sQ = smem, *sK = sQ + PLACES * C::kLd;   // two key tiles
   float2 *s_ml = reinterpret_cast<float2 *>(sK + 2 * kCkfEdge * C::kLd);
   const CkfPart<MAX> part;
   const int tx = part.tx, kg = threadIdx.x / 64;
@@ -216,7 +220,7 @@ __device__ __forceinline__ void ckf_keys_tile(const PagedChunk &p, const ChunkPl
   pages.find(p, w, k, k.tile);
   pages.copy(p, w, k, p.c.k_pages, k.tile, sK);
   if (k.tile + 1 < end) pages.find(p, w, k, k.tile + 1);
-  ckf_queries<D, MAX == 8 ? 8 : kCkfEdge>(p, k, t, sQ);
+  ckf_queries<D, PLACES>(p, k, t, sQ);
   const CkfRows<MAX> rows(p, w, k, t, true);
   float m[NR], sum[NR];
 #pragma unroll
@@ -278,8 +282,8 @@ __device__ __forceinline__ void ckf_keys_tile(const PagedChunk &p, const ChunkPl
   }
 }
 
-template <int D, bool EIGHT>
-__global__ void __launch_bounds__(kCkfThreads, ckf_ctas(D, EIGHT)) ckf_keys(PagedChunk p, ChunkPlan w) {
+template <int D, int MOST>
+__global__ void __launch_bounds__(kCkfThreads, ckf_ctas(D, MOST)) ckf_keys(PagedChunk p, ChunkPlan w) {
   extern __shared__ __align__(16) float ckf_smem[];
   pdl_wait();
   pdl_launch_dependents();
@@ -291,13 +295,13 @@ __global__ void __launch_bounds__(kCkfThreads, ckf_ctas(D, EIGHT)) ckf_keys(Page
       const CkfCols t(k, w, b);
       const int end = min(k.end, k.g.seen(b, kCkfEdge));
       __syncthreads();
-      if constexpr (EIGHT) {
-        ckf_keys_tile<D, 8>(p, w, k, t, end, ckf_smem);
+      if constexpr (MOST <= 16) {
+        ckf_keys_tile<D, MOST, MOST>(p, w, k, t, end, ckf_smem);
       } else {
         if (t.rows <= 16)
-          ckf_keys_tile<D, 16>(p, w, k, t, end, ckf_smem);
+          ckf_keys_tile<D, 16, MOST>(p, w, k, t, end, ckf_smem);
         else
-          ckf_keys_tile<D, 64>(p, w, k, t, end, ckf_smem);
+          ckf_keys_tile<D, MOST, MOST>(p, w, k, t, end, ckf_smem);
       }
     }
 }
@@ -309,15 +313,14 @@ __device__ __forceinline__ float ckf_share(float bid, float den) {
   return bid > 0.f ? bid * r : bid;
 }
 
-template <int D, int MAX>
+template <int D, int MAX, int PLACES>
 __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const ChunkPlan &w, const ChunkWalk &k, const CkfCols &t, int end,
                                                 float *smem) {
   using C = Ckf<D>;
   constexpr int NV = D / 64, NK = CkfPart<MAX>::kKeys, NR = CkfPart<MAX>::kRows;   // 4-column groups, keys and rows of a thread
   constexpr bool FEW = CkfPart<MAX>::kFew;
-  constexpr int ROWS = MAX == 8 ? 8 : kCkfEdge;
-  float *sQ = smem, *sK = sQ + ROWS * C::kLd, *sV = sK + kCkfEdge * C::kLd, *sP = sV + kCkfEdge * C::kLd,
-        *sPart = sP + ROWS * C::kLdP;
+  float *sQ = smem, *sK = sQ + PLACES * C::kLd, *sV = sK + kCkfEdge * C::kLd, *sP = sV + kCkfEdge * C::kLd,
+        *sPart = sP + PLACES * C::kLdP;
   const CkfPart<MAX> part;
   const int tid = threadIdx.x, tx = part.tx;
   const bool work = FEW || tid / 32 * 8 < t.rows;   // uniform over the warp
@@ -327,7 +330,7 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
   pages.copy(p, w, k, p.c.k_pages, k.tile, sK);
   pages.copy(p, w, k, p.c.v_pages, k.tile, sV);
   if (k.tile + 1 < end) pages.find(p, w, k, k.tile + 1);
-  ckf_queries<D, MAX == 8 ? 8 : kCkfEdge>(p, k, t, sQ);
+  ckf_queries<D, PLACES>(p, k, t, sQ);
   const CkfRows<MAX> rows(p, w, k, t, false);
   float num[NR][4 * NV], sum[NR];
 #pragma unroll
@@ -470,8 +473,8 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
   }
 }
 
-template <int D, bool EIGHT>
-__global__ void __launch_bounds__(kCkfThreads, ckf_ctas(D, EIGHT)) ckf_values(PagedChunk p, ChunkPlan w) {
+template <int D, int MOST>
+__global__ void __launch_bounds__(kCkfThreads, ckf_ctas(D, MOST)) ckf_values(PagedChunk p, ChunkPlan w) {
   extern __shared__ __align__(16) float ckf_smem[];
   pdl_wait();
   pdl_launch_dependents();
@@ -483,13 +486,13 @@ __global__ void __launch_bounds__(kCkfThreads, ckf_ctas(D, EIGHT)) ckf_values(Pa
       const CkfCols t(k, w, b);
       const int end = min(k.end, k.g.seen(b, kCkfEdge));
       __syncthreads();
-      if constexpr (EIGHT) {
-        ckf_values_tile<D, 8>(p, w, k, t, end, ckf_smem);
+      if constexpr (MOST <= 16) {
+        ckf_values_tile<D, MOST, MOST>(p, w, k, t, end, ckf_smem);
       } else {
         if (t.rows <= 16)
-          ckf_values_tile<D, 16>(p, w, k, t, end, ckf_smem);
+          ckf_values_tile<D, 16, MOST>(p, w, k, t, end, ckf_smem);
         else
-          ckf_values_tile<D, 64>(p, w, k, t, end, ckf_smem);
+          ckf_values_tile<D, MOST, MOST>(p, w, k, t, end, ckf_smem);
       }
     }
 }
@@ -498,30 +501,32 @@ cudaError_t launch_chunk_plan(const PagedChunk &p, const ChunkPlan &w, cudaStrea
 cudaError_t launch_chunk_join(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream);
 cudaError_t launch_chunk_combine(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream);
 
-template <int D, bool EIGHT>
+template <int D, int MOST>
 static int launch_ckf(const PagedChunk &p, cudaStream_t stream) {
-  constexpr int bytes = Ckf<D, EIGHT ? 8 : kCkfEdge>::kSmemBytes;
+  constexpr int bytes = Ckf<D, MOST>::kSmemBytes;
   static PerDeviceOnce once;
   const int prep = once.run([] {
-    return (cudaFuncSetAttribute(ckf_keys<D, EIGHT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
-            cudaFuncSetAttribute(ckf_values<D, EIGHT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return (cudaFuncSetAttribute(ckf_keys<D, MOST>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+            cudaFuncSetAttribute(ckf_values<D, MOST>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
                ? DA_ERR_CUDA
                : DA_OK;
   });
   if (prep != DA_OK) return prep;
   const ChunkPlan w = chunk_plan_f32(p.c.S, p.c.Hq, p.c.Hkv, D, p.N, p.max_new, p.c.page_size);
   if (launch_chunk_plan(p, w, stream) != cudaSuccess ||
-      launch_after(ckf_keys<D, EIGHT>, w.ctas_keys, kCkfThreads, bytes, stream, p, w) != cudaSuccess ||
+      launch_after(ckf_keys<D, MOST>, w.ctas_keys, kCkfThreads, bytes, stream, p, w) != cudaSuccess ||
       launch_chunk_join(p, w, stream) != cudaSuccess ||
-      launch_after(ckf_values<D, EIGHT>, w.ctas_values, kCkfThreads, bytes, stream, p, w) != cudaSuccess ||
+      launch_after(ckf_values<D, MOST>, w.ctas_values, kCkfThreads, bytes, stream, p, w) != cudaSuccess ||
       launch_chunk_combine(p, w, stream) != cudaSuccess)
     return DA_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 int launch_chunk_f32(const PagedChunk &p, cudaStream_t stream) {
-  if (ckf_eight(p.c.Hq, p.c.Hkv, p.max_new))
-    return p.c.d == 128 ? launch_ckf<128, true>(p, stream) : launch_ckf<64, true>(p, stream);
-  return p.c.d == 128 ? launch_ckf<128, false>(p, stream) : launch_ckf<64, false>(p, stream);
+  switch (ckf_most(p.c.Hq, p.c.Hkv, p.max_new)) {
+    case 8: return p.c.d == 128 ? launch_ckf<128, 8>(p, stream) : launch_ckf<64, 8>(p, stream);
+    case 16: return p.c.d == 128 ? launch_ckf<128, 16>(p, stream) : launch_ckf<64, 16>(p, stream);
+    default: return p.c.d == 128 ? launch_ckf<128, kCkfEdge>(p, stream) : launch_ckf<64, kCkfEdge>(p, stream);
+  }
 }
 }  // namespace da

@@ -160,11 +160,14 @@ def test_few_rows(d, Hq, Hkv, page, news, flags):
 
 
 @pytest.mark.parametrize("flags", [0, 1])
-@pytest.mark.parametrize("d,Hq,page,news", [(64, 5, 16, [8, 1, 3]), (64, 2, 256, [1, 0, 1]), (128, 3, 32, [4, 8, 2]), (128, 1, 128, [0, 7, 0])])
-def test_up_to_eight_rows_in_fp32(d, Hq, page, news, flags):
+@pytest.mark.parametrize("d,Hq,Hkv,page,news", [
+    (64, 5, 5, 16, [8, 1, 3]), (64, 2, 2, 256, [1, 0, 1]), (128, 3, 3, 32, [4, 8, 2]), (128, 1, 1, 128, [0, 7, 0]),
+    (64, 3, 3, 64, [16, 9, 11]), (64, 6, 3, 32, [8, 1, 5]), (128, 4, 2, 16, [3, 8, 0]), (128, 2, 2, 64, [12, 0, 16]),
+])
+def test_few_rows_in_fp32(d, Hq, Hkv, page, news, flags):
     lens = [5003, 2700, 31]
-    cache, q, cu = make(lens, news, Hq, Hq, d, page, "f32", seed=d + Hq, junk=float("nan"), pad=1)
-    run(cache, q, cu, 8, 5003, flags=flags)
+    cache, q, cu = make(lens, news, Hq, Hkv, d, page, "f32", seed=d + Hq, junk=float("nan"), pad=1)
+    run(cache, q, cu, max(news), 5003, flags=flags)
 
 
 def test_one_workspace_for_all_calls():
