@@ -27,8 +27,10 @@ constexpr int kCkfThreads = 256;
 // to 16 have kernels of their own, with registers for as many (one kernel for all: 4 % more for
 // many rows; us of 8 x 12 x 8001 with 3 tokens 195, as a part of one kernel 229, as up to 16
 // rows 282; 2 x 12 x 131072 with 4 tokens 648, 774, 980; 8 x 12 x 8001 with 14 tokens 265, in one
-// kernel 292; d = 128, 4 x 12 x 8001 with 14 tokens 270, in one kernel 356, three CTAs 401).
-constexpr int ckf_ctas(int d, int most) { return most <= 8 ? 3 : most <= 16 ? (d == 64 ? 3 : 2) : d == 64 ? 2 : 1; }
+// kernel 292; d = 128, 4 x 12 x 8001 with 14 tokens 270, in one kernel 356, three CTAs 401).  Two for
+// many rows at d = 128 too, which their bids' place over K makes room for (4 sequences of 1001 ..
+// 8001 with 301 .. 3 tokens 492 -> 395, 4 prompts of 2000 tokens 2829 -> 2788).
+constexpr int ckf_ctas(int d, int most) { return most <= 8 || (most <= 16 && d == 64) ? 3 : 2; }
 static int ckf_most(int Hq, int Hkv, int max_new) {
   const long long rows = (long long)(Hq / Hkv) * round_up(max_new, 8);
   return rows <= 8 ? 8 : rows <= 16 ? 16 : kCkfEdge;
@@ -43,7 +45,8 @@ template <int D, int ROWS = kCkfEdge>
 struct Ckf {
   static constexpr int kLd = D + 4;            // floats of a staged row: lanes of different rows read different banks
   static constexpr int kLdP = kCkfEdge + 4;
-  static constexpr int kSmemBytes = (ROWS * (kLd + kLdP) + 2 * kCkfEdge * kLd + 4 * kCkfEdge) * 4;
+  static constexpr bool kOver = D == 128 && ROWS == kCkfEdge;   // bids over K, once it has been read: two CTAs fit
+  static constexpr int kSmemBytes = (ROWS * (kLd + (kOver ? 0 : kLdP)) + 2 * kCkfEdge * kLd + 4 * kCkfEdge) * 4;
 };
 
 // A column tile: row c of it is query head hq(c), query i(c).
@@ -316,11 +319,12 @@ __device__ __forceinline__ float ckf_share(float bid, float den) {
 template <int D, int MAX, int PLACES>
 __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const ChunkPlan &w, const ChunkWalk &k, const CkfCols &t, int end,
                                                 float *smem) {
-  using C = Ckf<D>;
+  using C = Ckf<D, PLACES>;
+  constexpr bool OVER = C::kOver;
   constexpr int NV = D / 64, NK = CkfPart<MAX>::kKeys, NR = CkfPart<MAX>::kRows;   // 4-column groups, keys and rows of a thread
   constexpr bool FEW = CkfPart<MAX>::kFew;
-  float *sQ = smem, *sK = sQ + PLACES * C::kLd, *sV = sK + kCkfEdge * C::kLd, *sP = sV + kCkfEdge * C::kLd,
-        *sPart = sP + PLACES * C::kLdP;
+  float *sQ = smem, *sK = sQ + PLACES * C::kLd, *sV = sK + kCkfEdge * C::kLd, *sP = OVER ? sK : sV + kCkfEdge * C::kLd,
+        *sPart = OVER ? sV + kCkfEdge * C::kLd : sP + PLACES * C::kLdP;
   const CkfPart<MAX> part;
   const int tid = threadIdx.x, tx = part.tx;
   const bool work = FEW || tid / 32 * 8 < t.rows;   // uniform over the warp
@@ -349,9 +353,10 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
     const float before = at != nullptr ? __ldcg(at) : 0.f;
     ckf_landed<1>();   // K (V is the newer group)
     __syncthreads();
+    float x[NR][NK];
+    if (work) ckf_products<D, MAX>(sQ, sK, x);
+    if constexpr (OVER) __syncthreads();   // K has been read
     if (work) {
-      float x[NR][NK];
-      ckf_products<D, MAX>(sQ, sK, x);
 #pragma unroll
       for (int r = 0; r < NR; ++r)
 #pragma unroll
@@ -361,7 +366,7 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
         }
     }
     __syncthreads();
-    if (tile + 1 < end) pages.copy(p, w, k, p.c.k_pages, tile + 1, sK);
+    if (!OVER && tile + 1 < end) pages.copy(p, w, k, p.c.k_pages, tile + 1, sK);
     if (!several) {   // one head: 16 rows a thread
       const int n = min(16, t.rows - 16 * quarter);
       float mine = 0.f, run = 0.f;   // the rows' bids, summed apart from the total: it would take their last bits
@@ -394,7 +399,7 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
         if (at != nullptr) __stcg(at, held + run);
       }
     }
-    if (tile + 1 < end)
+    if (!OVER && tile + 1 < end)
       ckf_landed<1>();   // V (the next K is the newer group)
     else
       ckf_landed<0>();
@@ -428,6 +433,7 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
     }
     __syncthreads();
     if (tile + 1 < end) {
+      if (OVER) pages.copy(p, w, k, p.c.k_pages, tile + 1, sK);
       pages.copy(p, w, k, p.c.v_pages, tile + 1, sV);
       if (tile + 2 < end) pages.find(p, w, k, tile + 2);
     }
