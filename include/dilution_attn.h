@@ -461,7 +461,14 @@ int dilution_attn_paged_decode_ex(const void *q, const dilution_attn_paged_cache
  * overwritten from byte 256 on: calls that may overlap on the GPU need workspaces
  * of their own.  One that was sized for some N, max_new and max_len serves every call
  * of this cache within them.  Repeated calls give equal bits.  Errors as for
- * dilution_attn_paged_decode_ex. */
+ * dilution_attn_paged_decode_ex.
+ * DA_BF16: products, exponentials and reciprocals as in dilution_attn_paged_decode.  The
+ * shares enter the value product as two bf16 terms (2^-16 relative), as there, where a
+ * key head's rows, the new tokens rounded up to 8 for each of its query heads, are up to 64
+ * (drafted and single tokens: also beside long parts), and where no sequence of the call
+ * has more than d / 8 (max_new times query heads a key head) and the logits take up to
+ * 2 GB; in larger parts they are rounded to bf16 once, as in dilution_attn_fwd, which
+ * moves out by at most 2^-8 of the values' mean distance from it. */
 size_t dilution_attn_paged_chunk_workspace_size(int S, int Hq, int Hkv, int d, int N, int max_new, int max_len, int dtype);
 
 int dilution_attn_paged_chunk(const void *q, const dilution_attn_paged_cache *cache, const int32_t *cu_tokens, int N,

@@ -18,7 +18,10 @@
 // comes back to the thread that left it.  The shares, rounded to bf16 once (the
 // product's operands have one type; 2^-8 of each share, and numerator and sum hold
 // the same ones), go to shared memory as the MN-major A operand of
-// D[row, :] += share^T [V | 1].  Unlike the prompt's sweep, the rows stay and the keys
+// D[row, :] += share^T [V | 1].  Of several heads' rows, up to 64 in all (drafted and
+// single tokens beside parts of prompts), what the rounding left is a second term in the
+// places of the other 64, and a second product: those shares keep 2^-16, as in a decode
+// step (mixed batch of 48: 353 -> 359 us).  Unlike the prompt's sweep, the rows stay and the keys
 // stream: D stays in TMEM over a piece's key tiles and leaves once, as a partial
 // result of fixed place, so that equal calls give equal bits.
 //
@@ -67,6 +70,7 @@ struct CkxTile {
   int rows;            // 0: no more
   int tile, end, t0;   // key tiles; number of the first among the CTA's
   __device__ __forceinline__ int query(int c) const { return n8 ? c % n8 : i0 + c; }
+  __device__ __forceinline__ bool two_terms() const { return n8 != 0 && rows <= 64; }   // of a share
 };
 constexpr int kCkxRing = 4;
 
@@ -440,10 +444,10 @@ struct CkxVal {
   static constexpr uint32_t kShBytes = 32 * 1024;      // a warpgroup's shares: 2 x 64 rows x 128 keys
   static constexpr int kQs = D == 64 ? 2 : 1;          // of Q
   static constexpr uint32_t kOffQ = 0;
-  static constexpr uint32_t kOffK = kQs * kTB;
+  static constexpr uint32_t kOffSh = kQs * kTB;
+  static constexpr uint32_t kOffK = kOffSh + kG * kShBytes;      // behind the shares: see the second term's product
   static constexpr uint32_t kOffV = kOffK + kStages * kTB;
-  static constexpr uint32_t kOffSh = kOffV + kStages * kTB;
-  static constexpr uint32_t kOffOnes = kOffSh + kG * kShBytes;   // above every V tile (positive offset)
+  static constexpr uint32_t kOffOnes = kOffV + kStages * kTB;    // above every V tile (positive offset)
   static constexpr uint32_t kOffRing = kOffOnes + 2048;
   static constexpr uint32_t kOffBar = kOffRing + kCkxRing * sizeof(CkxTile);
   static constexpr int kSmemBytes = kOffBar + 512;     // (the base is 1024-byte aligned)
@@ -698,16 +702,19 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       const uint64_t dQ = ckx_kmajor(sQ), dK = ckx_kmajor(sK);
       // share^T: 64-row blocks 16 KB apart, 8-key groups 1 KB apart
       const uint64_t dSh = smem_desc(smem_u32(sSh) + g * C::kShBytes, 16384, 1024);
+      // Second terms lie where the first of rows 64 .. would; behind them the next warpgroup's
+      // shares, or K: what that makes of rows 64 .. no one reads.
+      static_assert(C::kOffK == C::kOffSh + kG * C::kShBytes && C::kStages * C::kTB >= 16384, "64 rows behind the last shares");
       int m = 0, mv = 0;          // tiles of this warpgroup: S issued, value products issued
       int vt = 0, vi = 0;         // the tile whose value product is due, its column tile
-      bool due = false, begins = false, ends = false;
+      int due = 0;                // 0, or of the following (each in a register: 4 % of 16 prompts of d = 128)
+      constexpr int kDue = 1, kBegins = 2, kEnds = 4, kTwo = 8;
       bool ok = true;
       // D += share^T [V | 1], in the tiles' order (sums in another order would have other
       // last bits).  Once V of tile t is there, the product of t - kStages has been formed,
       // so that four barriers tell whose turn it is.
       auto values = [&]() {
-        if (!due) return true;
-        due = false;
+        if (due == 0) return true;
         const int st = vt % C::kStages;
         if (!mbar_wait(d_free, vi & 1, wc) || !mbar_wait(&v_full[vt % C::kFull], (vt / C::kFull) & 1, wc) ||
             !mbar_wait(&sh_full[g], mv & 1, wc) ||
@@ -716,13 +723,17 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
         ++mv;
         tc_fence_after();
         const uint32_t v = smem_u32(sV) + st * C::kTB;
-        MmaRun<0, 8, 128, 128 - (128ll << 16), false>::go(tmem + C::kTmemD, dSh, smem_desc(v, ones - v, 1024), idesc_pv, begins ? 0u : 1u);
-        if constexpr (D == 128)
-          MmaRun<0, 8, 128, 128, false>::go(tmem + C::kTmemDHi, dSh, smem_desc(v + kCkxHalf, kCkxHalf, 1024), idesc_hi,
-                                                          begins ? 0u : 1u);
+        uint32_t onto = due & kBegins ? 0u : 1u;
+        const uint64_t last = dSh + (due & kTwo ? 16384 >> 4 : 0);
+        for (uint64_t sh = dSh; sh <= last; sh += 16384 >> 4, onto = 1u) {
+          MmaRun<0, 8, 128, 128 - (128ll << 16), false>::go(tmem + C::kTmemD, sh, smem_desc(v, ones - v, 1024), idesc_pv, onto);
+          if constexpr (D == 128)
+            MmaRun<0, 8, 128, 128, false>::go(tmem + C::kTmemDHi, sh, smem_desc(v + kCkxHalf, kCkxHalf, 1024), idesc_hi, onto);
+        }
         mma_commit(&sh_free[g]);
         mma_commit(&v_empty[st]);
-        if (ends) mma_commit(d_full);
+        if (due & kEnds) mma_commit(d_full);
+        due = 0;
         tc_fence_before();
         mbar_arrive(&turn[vt & 3]);
         return true;
@@ -752,12 +763,13 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
         if (!ok) break;
         const CkxTile &x = ring[i % kCkxRing];
         const int rows = x.rows, tiles = x.end - x.tile, t0 = x.t0;
+        const bool terms = x.two_terms();
         mbar_arrive(&r_free[i % kCkxRing]);
         if (rows == 0) break;
         const uint32_t idesc_s = idesc_bf16(128, (rows + 15) & ~15, false, false);
         for (int j = g; ok && j < tiles; j += kG, ++m) {
           const int t = t0 + j, st = t % C::kStages;
-          if (j == g && due) ok = first_of(i, &k_full[t % C::kFull], (t / C::kFull) & 1);
+          if (j == g && due != 0) ok = first_of(i, &k_full[t % C::kFull], (t / C::kFull) & 1);
           ok = ok && mbar_wait(&q_full[i % C::kQs], (i / C::kQs) & 1, wc) && mbar_wait(&k_full[t % C::kFull], (t / C::kFull) & 1, wc) &&
                mbar_wait(&s_free[g], (m & 1) ^ 1, wc);
           if (!ok) break;
@@ -770,11 +782,9 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
           mma_commit(&k_empty[st]);
           if (j + kG >= tiles) mma_commit(&q_empty[i % C::kQs]);   // its last S of the column tile
           ok = values();
-          due = true;
           vt = t;
           vi = i;
-          begins = j == 0;
-          ends = j + kG >= tiles;
+          due = kDue | (j == 0 ? kBegins : 0) | (j + kG >= tiles ? kEnds : 0) | (terms ? kTwo : 0);
         }
         if (!ok) break;
         if (g >= tiles) {
@@ -942,6 +952,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       } else {
         // several heads of n8 rows: 8 rows at a time, a head's total from its first rows to its last
         const int groups = rows / 8, per = n8 / 8, n = x.n, P = x.P, head0 = x.s * p.c.Hq + x.hq0;
+        const bool two = x.two_terms();
         for (; j < end; j += kG, ++m) {
           const int next_page = j + kG < end ? page_of(j + kG) : -1;
           float *next_at = nullptr;
@@ -980,7 +991,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
               tmem_ld8(ts + 8 * (u + 1), v);
             else
               ckx_release(&s_free[g], lane);
-            uint32_t pk[4];
+            uint32_t pk[4], pk2[4];
             const float den = ckx_den(total, p.eps);
             const float2 b2 = make_float2(den, den);
 #pragma unroll
@@ -995,12 +1006,14 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
               const float r = rcp_approx(dd.x * dd.y);
               const float2 s2 = fmul2(fmul2(make_float2(bid[2 * e], bid[2 * e + 1]), dd), make_float2(r, r));
               pk[e] = pack_bf16x2(s2.x, s2.y);
+              pk2[e] = pack_bf16x2(s2.x - __uint_as_float(pk[e] << 16), s2.y - __uint_as_float(pk[e] & 0xffff0000u));
             }
             if (u == 0) {   // the product of the tile before has read the shares
               ok = warp_wait(&sh_free[g], (m & 1) ^ 1, wc);
               if (!ok) break;
             }
             ckx_put(sh_row + (u >> 3) * 16384 + (((u & 7) ^ swz) << 4), pk[0], pk[1], pk[2], pk[3]);
+            if (two) ckx_put(sh_row + 16384 + ((u ^ swz) << 4), pk2[0], pk2[1], pk2[2], pk2[3]);
             q += 8;
             if (q == n8) {   // the head's last rows
               q = 0;

@@ -1,7 +1,8 @@
 // Chunks of few rows over the paged cache in bf16: the second pass over kept logits.
 //
-// Mathematics: as paged_chunk_f32.cu; shares are rounded to bf16 once, as in
-// paged_chunk_bf16.cu, and their sums are those of the rounded shares.
+// Mathematics: as paged_chunk_f32.cu.  A share enters the product as two bf16 terms (2^-16
+// of itself, as in a decode step; one would double the output's rounding error), and the
+// sums are those of the terms.
 //
 // What bounds it: HBM.  A key head's group has few rows (drafted tokens), so that the
 // cache is read for little work, and half of what the kernel for many rows reads is K,
@@ -20,7 +21,7 @@
 namespace da {
 
 constexpr long long kChunkLogitBytes = 2ll << 30;
-constexpr int kCklKeys = 32, kCklRows = 16;   // keys of a step; rows of a group, at most
+constexpr int kCklKeys = 32;   // of a step
 
 template <int D, int ROWS>
 struct Ckl {
@@ -30,7 +31,8 @@ struct Ckl {
   static constexpr int kOffT = kOffX + ROWS * kCklKeys * 4;
   static constexpr int kStage = kOffT + ROWS * kCklKeys * 4;
   static constexpr int kShRow = 80;                                    // bytes of a row of shares: 8 rows on all banks
-  static constexpr int kWarp = 2 * kStage + kCklRows * kShRow;
+  static constexpr int kShRows = 2 * ROWS;                             // their first terms, their second: up to 8 in one operand
+  static constexpr int kWarp = 2 * kStage + kShRows * kShRow;
   static constexpr int kSmemBytes = kWarps * kWarp;
   static constexpr int kLd = D + 4;                                    // floats of a row of a warp's sums
   static_assert(kSmemBytes <= 231424 && ROWS * kLd * 4 <= kWarp, "shared memory");
@@ -93,7 +95,7 @@ __global__ void __launch_bounds__(Ckl<D, ROWS>::kThreads, 1) ckl_values(PagedChu
       s_logits[tid] = reinterpret_cast<uint64_t>(reinterpret_cast<const float *>(p.ws + w.logits) +
                                                  ((size_t)(k.q.tok0 + q) * p.c.Hq + hq0 + h) * (size_t)w.logits_ld);
     }
-    for (int e = lane; e < kCklRows * C::kShRow / 4; e += 32) reinterpret_cast<uint32_t *>(shares)[e] = 0u;   // rows from R on stay 0
+    for (int e = lane; e < C::kShRows * C::kShRow / 4; e += 32) reinterpret_cast<uint32_t *>(shares)[e] = 0u;   // rows from R on stay 0
     __syncthreads();
     const int32_t *vtab = p.c.page_table + (size_t)k.s * p.c.max_pages, *dtab = p.c.demand_table + (size_t)k.s * p.c.max_pages;
     // this lane's key of step j: its pages
@@ -161,9 +163,11 @@ __global__ void __launch_bounds__(Ckl<D, ROWS>::kThreads, 1) ckl_values(PagedChu
         const float2 row = s_row[r];
         const float bid = key < key1 && key <= P + q ? ex2_approx(fmaf(x[r * kCklKeys], row.x, row.y)) : 0.f, before = added;
         added += bid;
-        const __nv_bfloat16 share = __float2bfloat16_rn(bid * rcp_approx(held + p.eps + (p.earlier ? before : added)));
-        *reinterpret_cast<__nv_bfloat16 *>(shares + r * C::kShRow + 2 * lane) = share;
-        sums[r] += __bfloat162float(share);
+        const float share = bid * rcp_approx(held + p.eps + (p.earlier ? before : added));
+        const __nv_bfloat16 hi = __float2bfloat16_rn(share), lo = __float2bfloat16_rn(share - __bfloat162float(hi));
+        *reinterpret_cast<__nv_bfloat16 *>(shares + r * C::kShRow + 2 * lane) = hi;
+        *reinterpret_cast<__nv_bfloat16 *>(shares + (ROWS + r) * C::kShRow + 2 * lane) = lo;
+        sums[r] += __bfloat162float(hi) + __bfloat162float(lo);
         if (++q == n) {
           if (at != nullptr) __stcg(at + ((size_t)h << sh), held + added);
           q = 0;
@@ -173,14 +177,19 @@ __global__ void __launch_bounds__(Ckl<D, ROWS>::kThreads, 1) ckl_values(PagedChu
       __syncwarp();
 #pragma unroll
       for (int ks = 0; ks < kCklKeys / 16; ++ks) {
-        uint32_t a[4];
+        uint32_t a[4], a2[4];
         ldsm_x4(smem_u32(shares) + ar * C::kShRow + (2 * ks + ap) * 16, a);
+        if constexpr (ROWS == 16) ldsm_x4(smem_u32(shares) + (16 + ar) * C::kShRow + (2 * ks + ap) * 16, a2);
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
           uint32_t v[4];
           ldsm_x4_t(smem_u32(now) + piece(16 * ks + ar, 2 * c + ap), v);
           mma16816(acc[2 * c], a, v[0], v[1]);
           mma16816(acc[2 * c + 1], a, v[2], v[3]);
+          if constexpr (ROWS == 16) {
+            mma16816(acc[2 * c], a2, v[0], v[1]);
+            mma16816(acc[2 * c + 1], a2, v[2], v[3]);
+          }
         }
       }
       // (the next step's shares are written after its __syncwarp)
@@ -188,11 +197,15 @@ __global__ void __launch_bounds__(Ckl<D, ROWS>::kThreads, 1) ckl_values(PagedChu
     __syncwarp();   // (all copies have been waited for and read)
     float *mine = reinterpret_cast<float *>(stages);
 #pragma unroll
-    for (int c = 0; c < D / 8; ++c)
-#pragma unroll
-      for (int e = 0; e < ROWS / 4; e += 2)
-        *reinterpret_cast<float2 *>(mine + (lane / 4 + e / 2 * 8) * C::kLd + c * 8 + 2 * (lane % 4)) =
-            make_float2(acc[c][e], acc[c][e + 1]);
+    for (int c = 0; c < D / 8; ++c) {
+      float *to = mine + lane / 4 * C::kLd + c * 8 + 2 * (lane % 4);
+      if constexpr (ROWS == 16) {
+        *reinterpret_cast<float2 *>(to) = make_float2(acc[c][0], acc[c][1]);
+        *reinterpret_cast<float2 *>(to + 8 * C::kLd) = make_float2(acc[c][2], acc[c][3]);
+      } else {
+        *reinterpret_cast<float2 *>(to) = make_float2(acc[c][0] + acc[c][2], acc[c][1] + acc[c][3]);
+      }
+    }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
 #pragma unroll

@@ -7,8 +7,9 @@
 //   keys, values and queries come into shared memory; S = Q K^T by m16n8k16
 //   products, the logits stay in shared memory; every row's (max, sum) goes through
 //   distributed shared memory; one thread a key walks the rows of each head with its
-//   total; the shares, rounded to bf16 once as in paged_chunk_bf16.cu, times V; the
-//   CTAs' numerators and sums are added in the CTAs' order by the CTA that writes them.
+//   total; the shares, each as two bf16 terms (2^-16 of itself; one would double the
+//   output's rounding error, as in a decode step), times V; the CTAs' numerators and sums
+//   are added in the CTAs' order by the CTA that writes them.
 // m16n8k16 and not tcgen05: the products are 1 % of the call.  fp32: all of it on CUDA
 // cores, 4 rows by 4 keys, or columns, a thread.
 #include "da_chunk.cuh"
@@ -166,10 +167,13 @@ struct Cks {
   static constexpr int kPieces = D / 8;
   static constexpr int kLd = kCksKeys + 4;              // floats of a row of logits
   static constexpr uint32_t kOffV = kCksKeys * D * 2, kOffQ = 2 * kOffV, kOffP = kOffQ + kCksRows * D * 2;
-  static constexpr int kSmemBytes = kOffP + kCksRows * kLd * 4;
+  static constexpr uint32_t kShBytes = kCksRows * kCksKeys * 2;   // shares: their first terms over K, their second
+  static constexpr uint32_t kOffSh2 = 2 * kShBytes <= kOffV ? kShBytes : kOffP + kCksRows * kLd * 4;   // behind them, or last
+  static constexpr int kSmemBytes = kOffP + kCksRows * kLd * 4 + (kOffSh2 > kOffP ? kShBytes : 0);
   static constexpr int kSplit = 128 / D;                // warps that share a 16-column tile of out: by keys
   static constexpr int kStage = D + 4;                  // floats of a row of numerators
-  static_assert(kCksRows * kCksKeys * 2 <= kOffV, "shares over K");
+  static_assert(kShBytes <= kOffV, "shares over K");
+  static_assert(kSmemBytes <= 231424, "shared memory");
   static_assert(kSplit * kCksRows * kStage <= kCksRows * kLd, "numerators over the logits");
 };
 
@@ -178,7 +182,7 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk(PagedChunk p, int G,
   using C = Cks<D>;
   constexpr int PP = C::kPieces;
   extern __shared__ __align__(128) uint8_t cks_smem[];
-  const uint32_t sK = smem_u32(cks_smem), sV = sK + C::kOffV, sQ = sK + C::kOffQ, sSh = sK;   // shares: over K
+  const uint32_t sK = smem_u32(cks_smem), sV = sK + C::kOffV, sQ = sK + C::kOffQ, sSh = sK, sSh2 = sK + C::kOffSh2;
   float *sP = reinterpret_cast<float *>(cks_smem + C::kOffP);
   __shared__ float2 s_ml[kCksRows];                     // this CTA's (max, sum) of the rows
   __shared__ float s_nl[kCksRows], s_sum[kCksRows];
@@ -285,9 +289,11 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk(PagedChunk p, int G,
   __syncthreads();
   // shares and totals: a thread a key
   if (tid < fill) {
-    __nv_bfloat16 *sh = reinterpret_cast<__nv_bfloat16 *>(cks_smem);
+    __nv_bfloat16 *sh = reinterpret_cast<__nv_bfloat16 *>(cks_smem), *sh2 = sh + C::kOffSh2 / 2;
     auto put = [&](int r, float v) {
-      sh[cks_off(r, tid >> 3, kCksKeys / 8) / 2 + (tid & 7)] = __float2bfloat16_rn(v);
+      const uint32_t i = cks_off(r, tid >> 3, kCksKeys / 8) / 2 + (tid & 7);
+      sh[i] = __float2bfloat16_rn(v);
+      sh2[i] = __float2bfloat16_rn(v - __bfloat162float(sh[i]));
     };
 #pragma unroll
     for (int h = 0; h < HELD; ++h) {
@@ -307,14 +313,15 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk(PagedChunk p, int G,
     for (int r = rows; r < blocks * 16; ++r) put(r, 0.f);
   }
   __syncthreads();
-  // the sums of the rounded shares; numerators over the logits
+  // the sums of the shares' terms; numerators over the logits
   for (int r = warp; r < rows; r += kCksWarps) {
     float sum = 0.f;
     for (int i = lane; i < fill / 8; i += 32) {
-      const uint4 v = *reinterpret_cast<const uint4 *>(cks_smem + cks_off(r, i, kCksKeys / 8));
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      const uint32_t at = cks_off(r, i, kCksKeys / 8);
+      const uint4 v = *reinterpret_cast<const uint4 *>(cks_smem + at), v2 = *reinterpret_cast<const uint4 *>(cks_smem + C::kOffSh2 + at);
+      const uint32_t w[8] = {v2.x, v2.y, v2.z, v2.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum += __uint_as_float(w[e] << 16) + __uint_as_float(w[e] & 0xffff0000u);
+      for (int e = 0; e < 8; ++e) sum += __uint_as_float(w[e] << 16) + __uint_as_float(w[e] & 0xffff0000u);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -336,10 +343,14 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk(PagedChunk p, int G,
 #pragma unroll
       for (int rb = 0; rb < 4; ++rb) {
         if (rb >= blocks) break;
-        uint32_t sa[4];
-        ldsm_x4(sSh + cks_off(rb * 16 + ar, (i >> 3) + ap, kCksKeys / 8), sa);
+        uint32_t sa[4], sa2[4];
+        const uint32_t off = cks_off(rb * 16 + ar, (i >> 3) + ap, kCksKeys / 8);
+        ldsm_x4(sSh + off, sa);
+        ldsm_x4(sSh2 + off, sa2);
         mma16816(acc[rb][0], sa, vb[0], vb[1]);
         mma16816(acc[rb][1], sa, vb[2], vb[3]);
+        mma16816(acc[rb][0], sa2, vb[0], vb[1]);
+        mma16816(acc[rb][1], sa2, vb[2], vb[3]);
       }
     }
 #pragma unroll
