@@ -460,7 +460,11 @@ int dilution_attn_paged_decode_ex(const void *q, const dilution_attn_paged_cache
  * once by the caller, or NULL for the workspace's first 256 bytes.  The workspace is
  * overwritten from byte 256 on: calls that may overlap on the GPU need workspaces
  * of their own.  One that was sized for some N, max_new and max_len serves every call
- * of this cache within them.  Repeated calls give equal bits.  Errors as for
+ * of this cache within them.  It holds about 4 (d + 7) bytes for each query head of the new
+ * tokens, of up to 8192 of a sequence, and as much for each row of the longest sequence's (up to
+ * 8192) for 152 CTAs (DA_F32: 304, with few rows 456), and the logits, up to 2 GB, of up
+ * to d / 8 new tokens times query heads a key head (DA_BF16).  A prompt of any length from
+ * 8192 tokens on at 12 query heads, d = 128: 0.73 GB and the logits, DA_F32 1.39 GB.  Repeated calls give equal bits.  Errors as for
  * dilution_attn_paged_decode_ex.
  * DA_BF16: products, exponentials and reciprocals as in dilution_attn_paged_decode.  The
  * shares enter the value product as two bf16 terms (2^-16 relative), as there, where a

@@ -365,7 +365,7 @@ int dilution_attn_paged_chunk(const void *q, const dilution_attn_paged_cache *ca
   p.out = out;
   p.cu = cu_tokens;
   p.N = N;
-  p.max_new = max_new;
+  p.max_new = p.all_new = max_new;
   p.max_len = max_len;
   p.hs = head_scale(tau, tau_bh, c.d);
   p.eps = eps;

@@ -41,14 +41,15 @@ __device__ __forceinline__ long long plan_scan(long long v, long long *warp_sum,
   return base + inc - v;
 }
 
-// One sequence, checked: its new tokens, or 0.
+// One sequence, checked: its new tokens of this round, or 0; its length up to them.
 __device__ __forceinline__ ChunkSeq plan_seq(const PagedChunk &p, int s) {
   const int len = __ldcg(p.c.seq_lens + s), a = __ldcg(p.cu + s), b = __ldcg(p.cu + s + 1), n = b - a;
-  if (len < 0 || len > p.max_len || a < 0 || b < a || b > p.N || n > p.max_new || n > len) {
+  if (len < 0 || len > p.max_len || a < 0 || b < a || b > p.N || n > p.all_new || n > len) {
     atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
     return ChunkSeq{0, 0, 0, a};
   }
-  return ChunkSeq{n > 0 ? len : 0, n, 0, a};
+  const int now = max(0, min(n - p.first, p.max_new));
+  return ChunkSeq{now > 0 ? len - n + p.first + now : 0, now, 0, a + p.first};
 }
 __device__ __forceinline__ long long plan_units(const PagedChunk &p, const ChunkPlan &w, const ChunkSeq &q) {
   if (q.n == 0) return 0;
@@ -309,6 +310,7 @@ size_t chunk_few_room(int S, int Hq, int Hkv, int d, long long N, int max_new, i
 
 // Enough for all calls within these bounds, those that keep their logits among them.
 size_t chunk_workspace(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len, int dtype) {
+  if (max_new > kChunkRound) max_new = kChunkRound;
   if (dtype == DA_F32) {   // up to 16 rows a key head have more CTAs
     const int few = 16 / (Hq / Hkv) / 8 * 8;
     const size_t all = chunk_plan_f32(S, Hq, Hkv, d, N, max_new, 16).total,
@@ -326,7 +328,14 @@ size_t chunk_workspace(int S, int Hq, int Hkv, int d, long long N, int max_new, 
 int launch_paged_chunk(const PagedChunk &p, cudaStream_t stream) {
   const int c = chunk_small_cluster(p.c.S, p.c.Hq, p.c.Hkv, p.max_new, p.max_len, p.c.dtype);
   if (c > 0) return launch_chunk_small(p, c, stream);
-  return p.c.dtype == DA_F32 ? launch_chunk_f32(p, stream) : launch_chunk_bf16(p, stream);
+  PagedChunk r = p;
+  int st = DA_OK;
+  do {
+    r.max_new = p.max_new - r.first < kChunkRound ? p.max_new - r.first : kChunkRound;
+    st = p.c.dtype == DA_F32 ? launch_chunk_f32(r, stream) : launch_chunk_bf16(r, stream);
+    r.first += kChunkRound;
+  } while (st == DA_OK && r.first < p.max_new);
+  return st;
 }
 
 }  // namespace da
