@@ -69,6 +69,7 @@ struct CkxTile {
   int tok0;            // query 0 among all
   int rows;            // 0: no more
   int tile, end, t0;   // key tiles; number of the first among the CTA's
+  bool odd;            // a row's sum is NaN: it must not reach the rows before it, nor totals that it does not see
   __device__ __forceinline__ int query(int c) const { return n8 ? c % n8 : i0 + c; }
   __device__ __forceinline__ bool two_terms() const { return n8 != 0 && rows <= 64; }   // of a share
 };
@@ -134,6 +135,7 @@ struct CkxWalk {
                                           int stride) const {
     CkxTile x;
     x.rows = 0;
+    x.odd = false;
     if (!k.any()) return x;
     const int r0 = b * k.g.step;
     x.s = k.s;
@@ -354,13 +356,13 @@ __global__ void __launch_bounds__(CkxKeys<D>::kThreads, 2)
         a[10] = fmaxf(v[30], v[31]);
         const float top =
             fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmax3(a[6], a[7], fmax3(a[8], a[9], a[10])));
-        if (top == -INFINITY) return;
-        const float mn = fmaxf(m, top * c2);
-        const float f = ex2_approx(m - mn);
+        // (no way out where top is -infinity: NaN does not show in it)
+        const float mn = fmaxf(m, top * c2), ms = mn == -INFINITY ? 0.f : mn;
+        const float f = ex2_approx(m - ms);
         m = mn;
         l0 = fmul2(l0, make_float2(f, f));
         l1 = fmul2(l1, make_float2(f, f));
-        const float2 c2v = make_float2(c2, c2), nm = make_float2(-mn, -mn);
+        const float2 c2v = make_float2(c2, c2), nm = make_float2(-ms, -ms);
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
           const float2 x0 = ffma2(make_float2(v[2 * e], v[2 * e + 1]), c2v, nm);
@@ -497,7 +499,7 @@ __device__ __forceinline__ float ckx_den(float total, float eps) {
 // 1 / (d0 d1), with d >= eps >= 1e-18.
 // They go to the key's row of the warpgroup's shares: `to`, the places of its 16-byte
 // pieces 0 .. 3 (of the first 32 rows of 64; of the second 64 bytes on or back).
-template <int CHUNK, bool EARLIER>
+template <int CHUNK>
 __device__ __forceinline__ void ckx_bids(float (&x)[32], float c2, const uint32_t (&nl)[4]) {
   const float2 c2v = make_float2(c2, c2);
 #pragma unroll
@@ -638,9 +640,12 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
         return true;
       };
       for (it.start(p, w, l, cut, lane); ok; ++i) {
-        const CkxTile x = it.tile(p, w, w.acc_a, w.acc_b, acc_stride(D));
+        CkxTile x = it.tile(p, w, w.acc_a, w.acc_b, acc_stride(D));
+        float4 nl = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (x.rows > 0) nl = it.nl(p, w, x, lane);
         ok = warp_wait(&r_free[i % kCkxRing], ((i / kCkxRing) & 1) ^ 1, wc);
         if (!ok) break;
+        x.odd = __any_sync(0xffffffffu, isnan(nl.x + nl.y) || isnan(nl.z + nl.w));   // (no +infinity among them)
         if (lane == 0) {
           ring[i % kCkxRing] = x;
           mbar_arrive(&r_full[i % kCkxRing]);
@@ -650,7 +655,6 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
           break;
         }
         int page = ckx_page(p, sh, x.s, x.len, x.tile, lane);
-        const float4 nl = it.nl(p, w, x, lane);
         // What follows waits for the demand warps of column tile i - 2, and those for the
         // products of what came before; of a sequence's last, partial tile for V itself.
         while (ok && v_due > 0 && (part || nv < before)) ok = bring_v();
@@ -853,7 +857,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
     for (int i = 0;; ++i) {
       if (!warp_wait(&r_full[i % kCkxRing], (i / kCkxRing) & 1, wc)) break;
       const CkxTile &x = ring[i % kCkxRing];
-      const int rows = x.rows, end = x.end, len = x.len, n8 = x.n8;
+      const int rows = x.rows, end = x.end, len = x.len;
       if (rows == 0) break;
       bool ok = true;
       const uint32_t ones = smem_u32(smem + C::kOffOnes);
@@ -890,7 +894,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       int j = x.tile + g;
       float *at = j < end ? total_at(page_of(j), j) : nullptr;
       float total = at != nullptr ? __ldcg(at) : 0.f;
-      if (n8 == 0) {
+      if (x.n8 == 0 && !x.odd) {
         // one head
         const int first = x.P + x.i0;   // place of row 0
         const float c2 = x.c2;
@@ -930,13 +934,13 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
                 if ((unsigned)(32 + e - lo) >= (unsigned)n) b[e] = -INFINITY;
               }
             }
-            ckx_bids<0, EARLIER>(a, c2, nl);
+            ckx_bids<0>(a, c2, nl);
             if (half == 0) {   // the product of the tile before has read the shares
               ok = warp_wait(&sh_free[g], (m & 1) ^ 1, wc);
               if (!ok) break;
             }
             ckx_shares<0, EARLIER>(a, base, added, to);
-            ckx_bids<1, EARLIER>(b, c2, nl);
+            ckx_bids<1>(b, c2, nl);
             ckx_shares<1, EARLIER>(b, base, added, to);
 #pragma unroll
             for (int e = 0; e < 4; ++e) nl[e] += 1024, to[e] += 16384;
@@ -950,8 +954,11 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
           total = next_total;
         }
       } else {
-        // several heads of n8 rows: 8 rows at a time, a head's total from its first rows to its last
-        const int groups = rows / 8, per = n8 / 8, n = x.n, P = x.P, head0 = x.s * p.c.Hq + x.hq0;
+        // several heads of n8 rows: 8 rows at a time, a head's total from its first rows to its last.
+        // (Or one head's, where a row needs the care that this loop takes: a least value for
+        // every pair's denominators costs the other 4 %, bids set to zero after they are formed as much.)
+        const int groups = (rows + 7) / 8, n8 = x.n8 ? x.n8 : 8 * groups, per = n8 / 8, n = x.n8 ? x.n : rows, P = x.P + x.i0,
+                  head0 = x.s * p.c.Hq + x.hq0;
         const bool two = x.two_terms();
         for (; j < end; j += kG, ++m) {
           const int next_page = j + kG < end ? page_of(j + kG) : -1;
@@ -964,7 +971,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
             if (next_at != nullptr) next_total = __ldcg(next_at);
           }
           const int key = j * kCkxEdge + key_l;
-          const int lo = key < len ? max(key - P, 0) : n;   // queries lo .. n - 1 see the key
+          const int lo = key < len ? min(max(key - P, 0), n) : n;   // queries lo .. n - 1 see the key
           float *head_at = at;
           float head_next = 0.f, added = 0.f, c2 = 0.f;
           int q = 0;   // query of the group's first row
@@ -1002,7 +1009,8 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 dd = fadd2(make_float2(d[2 * e + 1], d[2 * e]), b2);
+              float2 dd = fadd2(make_float2(d[2 * e + 1], d[2 * e]), b2);
+              if (!EARLIER) dd.x = fminf(dd.x, 2e18f);   // a NaN of the later row alone (else: both are below)
               const float r = rcp_approx(dd.x * dd.y);
               const float2 s2 = fmul2(fmul2(make_float2(bid[2 * e], bid[2 * e + 1]), dd), make_float2(r, r));
               pk[e] = pack_bf16x2(s2.x, s2.y);

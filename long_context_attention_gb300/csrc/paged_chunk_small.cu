@@ -303,7 +303,8 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk(PagedChunk p, int G,
 #pragma unroll 4
       for (int q = 0; q < n; ++q) {
         const int r = h * n8 + q;
-        const float bid = ex2_approx(sP[r * C::kLd + tid] + s_nl[r]), before = added;
+        const float x = sP[r * C::kLd + tid];
+        const float bid = x == -INFINITY ? 0.f : ex2_approx(x + s_nl[r]), before = added;   // (none from a row that does not see the key, whatever its sum is)
         added += bid;
         put(r, bid * rcp_approx(base + (p.earlier ? before : added)));
       }
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk_f32(PagedChunk p, in
 #pragma unroll 4
     for (int q = 0; q < k.n; ++q) {
       float *x = sP + (h * k.n8 + q) * C::kLdP + key_l;
-      const float bid = key_l < k.fill ? ex2_approx(*x + s_nl[h * k.n8 + q]) : 0.f, before = added;
+      const float bid = key_l < k.fill && *x != -INFINITY ? ex2_approx(*x + s_nl[h * k.n8 + q]) : 0.f, before = added;
       added += bid;
       float r;
       asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(held[j] + (p.earlier ? before : added) + p.eps));

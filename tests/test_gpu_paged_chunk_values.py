@@ -1,0 +1,81 @@
+"""Chunks over the paged cache where something is not finite.
+
+A chunk of n tokens is n decode steps: what a query does not see cannot reach its output, whatever it holds.  What it
+sees does: a NaN in a query or key gives NaN to the query's output, to the totals of the keys that it sees, and through
+them to later outputs.  Finite outputs and totals are held to the tolerances of tests/test_gpu_paged_chunk.py.
+"""
+import numpy as np
+import pytest
+import torch
+
+from long_context_attention_gb300 import binding as b
+from tests._parity import host64
+from tests._paged import LONG
+from tests.test_gpu_paged_chunk import make, oracle
+
+pytestmark = pytest.mark.gpu
+
+# the kernels for short calls and for few rows; several heads a tile; one head a tile, its last one partial
+SIZES = [([300, 90], [4, 2]), ([300, 90], [20, 5]), ([700, 90], [130, 5]), ([130, 260], [130, 140])]
+
+
+def tolerance(cu, info, d, bf16, ro):
+    n = int(cu[-1])
+    news = np.diff(cu.cpu().numpy())
+    g = (2 * d + 8) * 2.0 ** -24 * info["spread"][:n]
+    base = (2 * (4 * g + np.repeat(news, news)[:, None] * 2.0 ** -24 + 2.0 ** -19) * info["vmax"][:n])[..., None]
+    return base + ((2.0 ** -8 * np.abs(ro) + 2.0 ** -8 * (1 + 2.0 ** -7) * info["dev"][:n]) if bf16 else 2.0 ** -24 * np.abs(ro))
+
+
+def run_odd(cache, q, cu, max_new, max_len, spoil):
+    """The call after `spoil`, by both kinds of kernels, against the oracle: the same outputs and totals are not finite,
+    the others right (by the tolerances of the call before `spoil`, whose finite values it shares)."""
+    with np.errstate(all="ignore"):
+        clean = oracle(cache, q, cu)
+        spoil(cache, q)
+        ro, rD, info = oracle(cache, q, cu)
+    start, d, bf16 = cache.demand_pages.clone(), q.shape[-1], q.dtype == torch.bfloat16
+    assert not np.isfinite(ro).all() and np.isfinite(ro).any()
+    for most in sorted({max_len, max(max_len, LONG)}):
+        cache.demand_pages.copy_(start)
+        ws = b.dilution_attn_paged_chunk_workspace(cache, q.shape[0], max_new, most)
+        ws[256:] = 0xC7
+        got = host64(b.dilution_attn_paged_chunk(q, cache, cu, max_new, most, workspace=ws))
+        assert b.dilution_attn_get_error(ws) == b.DA_OK
+        fine = np.isfinite(ro)
+        assert np.array_equal(got[~fine], ro[~fine], equal_nan=True)
+        assert np.isfinite(got[fine]).all()
+        assert (np.abs(got - ro)[fine] <= tolerance(cu, clean[2], d, bf16, ro)[fine]).all()
+        D, fine = host64(cache.demand_pages), np.isfinite(rD)
+        assert np.array_equal(D[~fine], rD[~fine], equal_nan=True)
+        assert np.abs(D - rD)[fine].max() <= 1e-4 * max(1.0, np.abs(rD[fine]).max())
+
+
+def put(pages, cache, s, place, head, cols, value):
+    page = cache.page_size
+    pages[cache.page_table[s, place // page].long(), head, place % page, cols] = value
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("which", ["key", "query"])
+@pytest.mark.parametrize("odd", [0, 1])
+@pytest.mark.parametrize("d,Hq,Hkv,page", [(64, 4, 2, 16), (128, 3, 3, 128)])
+@pytest.mark.parametrize("lens,news", SIZES)
+def test_keys_and_queries_that_come_later(lens, news, d, Hq, Hkv, page, odd, which, dtype):
+    """A NaN in a new key or in a query: rows before it, and totals of keys that only later rows see, stay finite."""
+    cache, q, cu = make(lens, news, Hq, Hkv, d, page, dtype, seed=sum(news) + d + odd)
+    j = news[0] // 4 * 2 + odd
+
+    def spoil(cache, q):
+        if which == "key":
+            put(cache.k_pages, cache, 0, lens[0] - news[0] + j, 0, slice(3, 4), np.nan)
+        else:
+            q[j, 0, 5] = float("nan")
+    run_odd(cache, q, cu, max(news), max(lens), spoil)
+
+
+@pytest.mark.parametrize("P,n", [(256, 129), (240, 17)])
+def test_a_key_of_its_own_block(P, n):
+    """A NaN in the last key, the only one of its 32 that the last row sees."""
+    cache, q, cu = make([P + n], [n], 2, 2, 64, 64, "bf16", seed=n)
+    run_odd(cache, q, cu, n, P + n, lambda c, q: put(c.k_pages, c, 0, P + n - 1, 0, slice(0, 1), np.nan))
