@@ -455,6 +455,9 @@ int dilution_attn_paged_decode_ex(const void *q, const dilution_attn_paged_cache
  * or pass N record DA_ERR_INVALID; such a sequence's rows of out are not written and
  * its demand stays.  A page id outside the pool records it too, and the sequence's
  * results are unspecified.
+ * What is not finite in a new token's value reaches the outputs of the queries that see
+ * the token, and no others; a NaN in a query or key its outputs, the totals of the keys
+ * that its query sees, and through them the sequence's later queries (of that head).
  * tau_bh: nullable device [S*Hq], index s*Hq + h.  tau, eps, flags as for
  * dilution_attn_paged_decode.  status: DEVICE, 256 bytes, 256-byte aligned, zeroed
  * once by the caller, or NULL for the workspace's first 256 bytes.  The workspace is

@@ -25,6 +25,11 @@
 // Rounds.  Every CTA has places for the rows of a sequence's new tokens (b), so that
 // long parts go by rounds of up to kChunkRound of them: a chunk is what two halves of
 // it are, one after the other.
+//
+// Values that are not finite.  A query's share of a key that it does not see is 0, and 0
+// times infinity or NaN would be NaN.  So such elements of new tokens' values are cleared
+// where they enter the products, and added to the outputs of the rows that see them; a
+// flag a sequence (chunk_join) says whether there are any.
 #pragma once
 
 #include "da_paged.h"
@@ -91,7 +96,7 @@ struct ChunkPlan {
   ChunkCost cost;
   long long rows;        // rows of all heads, at most
   int cta_rows;          // rows of a CTA's places
-  size_t seq_off, cum_off, ml_a, ml_b, nl, acc_a, acc_b, total;
+  size_t seq_off, cum_off, odd_off, ml_a, ml_b, nl, acc_a, acc_b, total;
   size_t logits;         // q . k of (token, query head) and key, where they are kept
   int logits_ld;         // their keys (0: not kept)
 };
@@ -122,7 +127,8 @@ inline ChunkPlan chunk_plan(int S, int Hq, int Hkv, int d, long long N, int max_
   auto next = [](size_t off, long long bytes) { return (size_t)round_up((int64_t)off + bytes, 256); };
   w.seq_off = kStatusBytes;
   w.cum_off = next(w.seq_off, ((long long)S + 1) * (long long)sizeof(ChunkSeq));   // (the last: how many rows a head)
-  w.ml_a = next(w.cum_off, ((long long)S + 1) * 8);
+  w.odd_off = next(w.cum_off, ((long long)S + 1) * 8);
+  w.ml_a = next(w.odd_off, (long long)S * 4);
   w.ml_b = next(w.ml_a, w.rows * 8);
   w.nl = next(w.ml_b, b_keys * 8);
   w.acc_a = next(w.nl, w.rows * 4);
@@ -207,6 +213,42 @@ __device__ __forceinline__ ChunkLine chunk_line(const PagedChunk &p, const Chunk
 __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkLine &l, int s) {
   const int4 v = __ldcg(reinterpret_cast<const int4 *>(l.seq + s));
   return ChunkSeq{v.x, v.y, v.z, v.w};
+}
+
+// Whether a new token of the sequence has a value that is not finite.
+__device__ __forceinline__ int *chunk_odd(const PagedChunk &p, const ChunkPlan &w) { return reinterpret_cast<int *>(p.ws + w.odd_off); }
+__device__ __forceinline__ bool chunk_not_finite(uint32_t x) { return (x & 0x7f800000u) == 0x7f800000u; }   // bits of a float
+// Of 16 bytes of values, bf16 or fp32: zeros for what is not finite; whether there was any.
+__device__ __forceinline__ bool chunk_clear(uint4 &v, bool half) {
+  bool any = false;
+  uint32_t *x[4] = {&v.x, &v.y, &v.z, &v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (chunk_not_finite(*x[i])) any = true, *x[i] &= half ? 0xffffu : 0u;
+    if (half && chunk_not_finite(*x[i] << 16)) any = true, *x[i] &= 0xffff0000u;
+  }
+  return any;
+}
+// What is not finite of columns c .. c + 3 of the values of tokens t0 .. t1, onto a.
+template <int D, typename E>
+__device__ void chunk_see(const PagedChunk &p, int sh, int s, int hkv, int t0, int t1, int c, float4 &a) {
+  for (int t = t0; t <= t1; ++t) {
+    const int page = __ldcg(p.c.page_table + (size_t)s * p.c.max_pages + (t >> sh));
+    if ((unsigned)page >= (unsigned)p.c.num_pages) continue;
+    const E *at = static_cast<const E *>(p.c.v_pages) +
+                  ((((size_t)page * p.c.Hkv + hkv) << sh) + (t & ((1 << sh) - 1))) * D + c;
+    uint4 x;
+    if constexpr (sizeof(E) == 4) {
+      x = __ldcg(reinterpret_cast<const uint4 *>(at));
+    } else {
+      const uint2 y = __ldcg(reinterpret_cast<const uint2 *>(at));
+      x = make_uint4(y.x << 16, y.x & 0xffff0000u, y.y << 16, y.y & 0xffff0000u);
+    }
+    if (chunk_not_finite(x.x)) a.x += __uint_as_float(x.x);
+    if (chunk_not_finite(x.y)) a.y += __uint_as_float(x.y);
+    if (chunk_not_finite(x.z)) a.z += __uint_as_float(x.z);
+    if (chunk_not_finite(x.w)) a.w += __uint_as_float(x.w);
+  }
 }
 
 // The last sequence with cum <= u (one with units, for u on the line).  A warp's

@@ -70,6 +70,7 @@ struct CkxTile {
   int rows;            // 0: no more
   int tile, end, t0;   // key tiles; number of the first among the CTA's
   bool odd;            // a row's sum is NaN: it must not reach the rows before it, nor totals that it does not see
+  bool clear;          // new tokens have values that are not finite
   __device__ __forceinline__ int query(int c) const { return n8 ? c % n8 : i0 + c; }
   __device__ __forceinline__ bool two_terms() const { return n8 != 0 && rows <= 64; }   // of a share
 };
@@ -135,7 +136,7 @@ struct CkxWalk {
                                           int stride) const {
     CkxTile x;
     x.rows = 0;
-    x.odd = false;
+    x.odd = x.clear = false;
     if (!k.any()) return x;
     const int r0 = b * k.g.step;
     x.s = k.s;
@@ -626,7 +627,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       bool ok = true;
       int v_len[C::kLag] = {}, v_tile[C::kLag] = {}, v_hkv[C::kLag] = {}, v_page[C::kLag] = {};   // V still to be brought
       int v_due = 0;
-      bool part = false;   // the column tile before held a sequence's last keys, not a whole tile of them
+      bool part = false;   // in the column tile before, demand warps wait for V: see tile_ready
       int before = 0;      // its first key tile's number
       auto bring_v = [&]() {
         const int st = nv % C::kStages;
@@ -642,7 +643,10 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       for (it.start(p, w, l, cut, lane); ok; ++i) {
         CkxTile x = it.tile(p, w, w.acc_a, w.acc_b, acc_stride(D));
         float4 nl = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (x.rows > 0) nl = it.nl(p, w, x, lane);
+        if (x.rows > 0) {
+          nl = it.nl(p, w, x, lane);
+          x.clear = __ldcg(chunk_odd(p, w) + x.s) != 0;
+        }
         ok = warp_wait(&r_free[i % kCkxRing], ((i / kCkxRing) & 1) ^ 1, wc);
         if (!ok) break;
         x.odd = __any_sync(0xffffffffu, isnan(nl.x + nl.y) || isnan(nl.z + nl.w));   // (no +infinity among them)
@@ -656,10 +660,10 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
         }
         int page = ckx_page(p, sh, x.s, x.len, x.tile, lane);
         // What follows waits for the demand warps of column tile i - 2, and those for the
-        // products of what came before; of a sequence's last, partial tile for V itself.
+        // products of what came before; of some tiles for V itself.
         while (ok && v_due > 0 && (part || nv < before)) ok = bring_v();
         if (!ok) break;
-        part = x.end * kCkxEdge > x.len;
+        part = x.end * kCkxEdge > (x.clear ? x.P + x.i0 : x.len);
         before = x.t0;
         const int qs = i % C::kQs;
         // every role is done with column tile i - 2, whose -lse2 this one's replace
@@ -859,6 +863,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
       const CkxTile &x = ring[i % kCkxRing];
       const int rows = x.rows, end = x.end, len = x.len;
       if (rows == 0) break;
+      const int whole = x.clear ? x.P + x.i0 : len;   // keys whose values need no care: see tile_ready
       bool ok = true;
       const uint32_t ones = smem_u32(smem + C::kOffOnes);
       // the page of this thread's key in tile j, for the totals (-1: none), and its place
@@ -875,18 +880,24 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
         return nullptr;
       };
       // The tile's S, and in a sequence's last tile zeros in the rows of V past its end,
-      // which may hold anything: 0 times that is not 0.
+      // which may hold anything: 0 times that is not 0.  Of keys that not every row sees too
+      // (where a flag says so), or that two terms of a share would make inf - inf of.
       auto tile_ready = [&](int j) {
         if (!warp_wait(&s_full[g], m & 1, wc)) return false;
         tc_fence_after();
-        if ((j + 1) * kCkxEdge > len) {
+        if ((j + 1) * kCkxEdge > whole) {
           const int t = x.t0 + (j - x.tile), st = t % C::kStages;
           if (!warp_wait(&v_full[t % C::kFull], (t / C::kFull) & 1, wc)) return false;
-          if (j * kCkxEdge + key_l >= len) {
-#pragma unroll
-            for (int e = 0; e < D / 8; ++e)
-              *reinterpret_cast<uint4 *>(sV + st * C::kTB + (e >> 3) * kCkxHalf + key_l * 128 + ((e & 7) << 4)) =
-                  make_uint4(0u, 0u, 0u, 0u);
+          const int key = j * kCkxEdge + key_l;
+          uint8_t *row = sV + st * C::kTB + key_l * 128;
+          if (key >= whole) {
+#pragma unroll 1
+            for (int e = 0; e < D / 8; ++e) {
+              uint4 *v = reinterpret_cast<uint4 *>(row + (e >> 3) * kCkxHalf + ((e & 7) << 4));
+              uint4 y = *v;
+              chunk_clear(y, true);
+              *v = key < len ? y : make_uint4(0u, 0u, 0u, 0u);
+            }
           }
         }
         return true;

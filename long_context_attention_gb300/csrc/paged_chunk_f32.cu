@@ -117,6 +117,16 @@ struct CkfPages {
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
 };
+// The thread's own copies of a tile of V, once landed: of the sequence's new tokens only
+// what is finite.
+template <int D>
+__device__ __forceinline__ void ckf_clear(const ChunkWalk &k, int tile, float *sV) {
+  for (int j = threadIdx.x / (D / 4); j < kCkfEdge; j += CkfPages<D>::STEP) {
+    uint4 *v = reinterpret_cast<uint4 *>(sV + j * Ckf<D>::kLd + threadIdx.x % (D / 4) * 4);
+    uint4 x = *v;
+    if (tile * kCkfEdge + j >= k.g.P && chunk_clear(x, false)) *v = x;
+  }
+}
 template <int N>
 __device__ __forceinline__ void ckf_landed() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
@@ -336,6 +346,7 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
   if (k.tile + 1 < end) pages.find(p, w, k, k.tile + 1);
   ckf_queries<D, PLACES>(p, k, t, sQ);
   const CkfRows<MAX> rows(p, w, k, t, false);
+  const bool odd = __ldcg(chunk_odd(p, w) + k.s) != 0;
   float num[NR][4 * NV], sum[NR];
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
@@ -403,6 +414,7 @@ __device__ __forceinline__ void ckf_values_tile(const PagedChunk &p, const Chunk
       ckf_landed<1>();   // V (the next K is the newer group)
     else
       ckf_landed<0>();
+    if (odd && (tile + 1) * kCkfEdge > k.g.P) ckf_clear<D>(k, tile, sV);
     __syncthreads();
     if (work) {
 #pragma unroll 4

@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(Ckl<D, ROWS>::kThreads, 1) ckl_values(PagedChu
       s_logits[tid] = reinterpret_cast<uint64_t>(reinterpret_cast<const float *>(p.ws + w.logits) +
                                                  ((size_t)(k.q.tok0 + q) * p.c.Hq + hq0 + h) * (size_t)w.logits_ld);
     }
+    const bool odd = __ldcg(chunk_odd(p, w) + k.s) != 0;
     for (int e = lane; e < C::kShRows * C::kShRow / 4; e += 32) reinterpret_cast<uint32_t *>(shares)[e] = 0u;   // rows from R on stay 0
     __syncthreads();
     const int32_t *vtab = p.c.page_table + (size_t)k.s * p.c.max_pages, *dtab = p.c.demand_table + (size_t)k.s * p.c.max_pages;
@@ -143,7 +144,16 @@ __global__ void __launch_bounds__(Ckl<D, ROWS>::kThreads, 1) ckl_values(PagedChu
     find(warp + C::kWarps);
     for (int j = warp; j < steps; j += C::kWarps) {
       const int key = key0 + j * kCklKeys + lane;
+      uint8_t *now = stages + st * C::kStage;
       asm volatile("cp.async.wait_all;" ::: "memory");
+      if (odd && key0 + (j + 1) * kCklKeys > P) {   // the lane's own copies: no new token's values but finite ones
+#pragma unroll 1
+        for (int e = lane; e < kCklKeys * PP; e += 32) {
+          uint4 *v = reinterpret_cast<uint4 *>(now + piece(e / PP, e % PP));
+          uint4 x = *v;
+          if (key0 + j * kCklKeys + e / PP >= P && chunk_clear(x, true)) *v = x;
+        }
+      }
       __syncwarp();   // the step's copies are there, and the step before has been read
       if (j + C::kWarps < steps) copy(j + C::kWarps, st ^ 1);
       float *at = (unsigned)page < (unsigned)p.c.num_demand_pages
@@ -151,7 +161,6 @@ __global__ void __launch_bounds__(Ckl<D, ROWS>::kThreads, 1) ckl_values(PagedChu
                       : nullptr;
       page = dpage;
       find(j + 2 * C::kWarps);
-      const uint8_t *now = stages + st * C::kStage;
       st ^= 1;
       const float *x = reinterpret_cast<const float *>(now + C::kOffX) + lane, *t = reinterpret_cast<const float *>(now + C::kOffT) + lane;
       float held = 0.f, added = 0.f;   // the rows' bids, summed apart from the total: it would take their last bits

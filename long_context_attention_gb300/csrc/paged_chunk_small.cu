@@ -134,11 +134,21 @@ __device__ __forceinline__ void cks_stats(const float *sP, int ld, const CksPart
   }
 }
 
+// After a cluster barrier: whether a CTA of the cluster has cleared a value (last warp).
+__device__ __forceinline__ void cks_any(const int *s_odd, int *s_any, int csize) {
+  const int lane = threadIdx.x - (kCksThreads - 32);
+  if (lane < 0) return;
+  int odd = 0;
+  if (lane < csize) asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(odd) : "r"(cks_peer(s_odd, (uint32_t)lane)) : "memory");
+  odd = __any_sync(0xffffffffu, odd != 0);
+  if (lane == 0) *s_any = odd;
+}
+
 // After a cluster barrier: out, the CTAs' numerators (`parts` blocks of `rows_max` rows
 // of `stage` floats each) and sums added in order; a CTA writes its share of the pieces.
 template <int D, typename E>
 __device__ __forceinline__ void cks_out(const PagedChunk &p, const CksPart &k, int G, const float *num, int parts, int rows_max, int stage,
-                                        const float *s_sum, int csize) {
+                                        const float *s_sum, int csize, int page_shift, bool odd) {
   for (int e = (int)cks_rank() * kCksThreads + threadIdx.x; e < k.rows * (D / 4); e += csize * kCksThreads) {
     const int r = e / (D / 4), c = e % (D / 4), h = r / k.n8, q = r % k.n8;
     if (q >= k.n) continue;
@@ -153,6 +163,7 @@ __device__ __forceinline__ void cks_out(const PagedChunk &p, const CksPart &k, i
       asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(cks_peer(s_sum + r, (uint32_t)i)) : "memory");
       sum += x;
     }
+    if (odd) chunk_see<D, E>(p, page_shift, k.s, k.hkv, k.P, k.P + q, 4 * c, a);
     const size_t to = ((size_t)(k.a + q) * p.c.Hq + k.hkv * G + h) * D + 4 * c;
     if constexpr (sizeof(E) == 4)
       *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + to) = make_float4(a.x / sum, a.y / sum, a.z / sum, a.w / sum);
@@ -186,6 +197,7 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk(PagedChunk p, int G,
   float *sP = reinterpret_cast<float *>(cks_smem + C::kOffP);
   __shared__ float2 s_ml[kCksRows];                     // this CTA's (max, sum) of the rows
   __shared__ float s_nl[kCksRows], s_sum[kCksRows];
+  __shared__ int s_odd, s_any;                          // values that are not finite: see da_chunk.cuh
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int ps = 1 << page_shift;
   pdl_wait();
@@ -240,7 +252,14 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk(PagedChunk p, int G,
 #pragma unroll
   for (int h = 0; h < HELD; ++h) held[h] = h < G && at != nullptr ? __ldcg(at + ((size_t)h << page_shift)) : 0.f;
   cp_async_wait_all();
-  __syncthreads();
+  bool odd = false;   // of the thread's own copies
+  for (int r = tid / PP; r < cnt; r += kCksThreads / PP) {
+    if (key0 + r < k.P) continue;
+    uint4 *v = reinterpret_cast<uint4 *>(cks_smem + C::kOffV + cks_off(r, tid % PP, PP)), x = *v;
+    if (chunk_clear(x, true)) *v = x, odd = true;
+  }
+  odd = __syncthreads_or(odd);
+  if (tid == 0) s_odd = odd;
   // logits: a warp takes 32 keys
   if (warp * 32 < fill) {
     float acc[4][4][4];
@@ -286,6 +305,7 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk(PagedChunk p, int G,
   cks_stats(sP, C::kLd, k, s_ml);
   cks_sync();
   cks_join(s_ml, s_nl, rows, csize);
+  cks_any(&s_odd, &s_any, csize);
   __syncthreads();
   // shares and totals: a thread a key
   if (tid < fill) {
@@ -366,7 +386,7 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk(PagedChunk p, int G,
     }
   }
   cks_sync();
-  cks_out<D, __nv_bfloat16>(p, k, G, sP, C::kSplit, kCksRows, C::kStage, s_sum, csize);
+  cks_out<D, __nv_bfloat16>(p, k, G, sP, C::kSplit, kCksRows, C::kStage, s_sum, csize, page_shift, s_any != 0);
   cks_sync();   // no CTA leaves while a peer may read it
 }
 
@@ -388,6 +408,7 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk_f32(PagedChunk p, in
   float *sNum = sK;                                     // numerators: over K
   __shared__ float2 s_ml[kCksRowsF32];
   __shared__ float s_nl[kCksRowsF32], s_sum[kCksRowsF32];
+  __shared__ int s_odd, s_any;                          // as above
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, ps = 1 << page_shift;
   pdl_wait();
   pdl_launch_dependents();
@@ -425,7 +446,14 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk_f32(PagedChunk p, in
   for (int j = 0; j < HELD; ++j)
     held[j] = 2 * j + half < G && at != nullptr ? __ldcg(at + ((size_t)(2 * j + half) << page_shift)) : 0.f;
   cp_async_wait_all();
-  __syncthreads();
+  bool odd = false;   // of the thread's own copies
+  for (int r = tid / PP; r < k.cnt; r += kCksThreads / PP) {
+    if (k.key0 + r < k.P) continue;
+    uint4 *v = reinterpret_cast<uint4 *>(sV + r * C::kLd + tid % PP * 4), x = *v;
+    if (chunk_clear(x, false)) *v = x, odd = true;
+  }
+  odd = __syncthreads_or(odd);
+  if (tid == 0) s_odd = odd;
   const bool work = 4 * warp < k.rows;                  // rows 4 warp ..; keys lane + 32 j
   if (work) {
     float2 acc[4][4];
@@ -463,6 +491,7 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk_f32(PagedChunk p, in
   cks_stats(sP, C::kLdP, k, s_ml);
   cks_sync();
   cks_join(s_ml, s_nl, k.rows, csize);
+  cks_any(&s_odd, &s_any, csize);
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < HELD; ++j) {
@@ -522,7 +551,7 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk_f32(PagedChunk p, in
     }
   }
   cks_sync();
-  cks_out<D, float>(p, k, G, sNum, 1, kCksRowsF32, C::kLd, s_sum, csize);
+  cks_out<D, float>(p, k, G, sNum, 1, kCksRowsF32, C::kLd, s_sum, csize, page_shift, s_any != 0);
   cks_sync();   // no CTA leaves while a peer may read it
 }
 

@@ -1,8 +1,9 @@
 """Chunks over the paged cache where something is not finite.
 
 A chunk of n tokens is n decode steps: what a query does not see cannot reach its output, whatever it holds.  What it
-sees does: a NaN in a query or key gives NaN to the query's output, to the totals of the keys that it sees, and through
-them to later outputs.  Finite outputs and totals are held to the tolerances of tests/test_gpu_paged_chunk.py.
+sees does: an infinite value gives an infinite output, NaN and infinities of both signs NaN; a NaN in a query or key
+gives NaN to the query's output, to the totals of the keys that it sees, and through them to later outputs.  Finite
+outputs and totals are held to the tolerances of tests/test_gpu_paged_chunk.py.
 """
 import numpy as np
 import pytest
@@ -45,15 +46,60 @@ def run_odd(cache, q, cu, max_new, max_len, spoil):
         fine = np.isfinite(ro)
         assert np.array_equal(got[~fine], ro[~fine], equal_nan=True)
         assert np.isfinite(got[fine]).all()
-        assert (np.abs(got - ro)[fine] <= tolerance(cu, clean[2], d, bf16, ro)[fine]).all()
+        assert (np.abs(got[fine] - ro[fine]) <= tolerance(cu, clean[2], d, bf16, ro)[fine]).all()
         D, fine = host64(cache.demand_pages), np.isfinite(rD)
         assert np.array_equal(D[~fine], rD[~fine], equal_nan=True)
-        assert np.abs(D - rD)[fine].max() <= 1e-4 * max(1.0, np.abs(rD[fine]).max())
+        assert np.abs(D[fine] - rD[fine]).max() <= 1e-4 * max(1.0, np.abs(rD[fine]).max())
 
 
 def put(pages, cache, s, place, head, cols, value):
     page = cache.page_size
     pages[cache.page_table[s, place // page].long(), head, place % page, cols] = value
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d,Hq,Hkv,page", [(64, 4, 2, 16), (128, 3, 3, 128), (64, 2, 2, 64)])
+@pytest.mark.parametrize("lens,news", SIZES)
+def test_values_that_a_query_does_not_see(lens, news, d, Hq, Hkv, page, dtype):
+    """Infinite and NaN values of later new tokens: earlier rows do not know of them."""
+    cache, q, cu = make(lens, news, Hq, Hkv, d, page, dtype, seed=sum(news) + d)
+
+    def spoil(cache, q):
+        P, n = lens[0] - news[0], news[0]
+        j = n // 2
+        for cols, value in ((slice(0, 8), np.inf), (slice(8, 11), -np.inf), (slice(20, 23), np.nan), (slice(d - 1, d), np.inf)):
+            put(cache.v_pages, cache, 0, P + j, 0, cols, value)
+        put(cache.v_pages, cache, 0, P + j + 1, 0, slice(0, 3), -np.inf)       # and inf - inf
+        put(cache.v_pages, cache, 0, P + n - 1, Hkv - 1, slice(30, 64), np.nan)   # the last row alone sees it
+        put(cache.v_pages, cache, 1, lens[1] - 1, 0, slice(5, 6), np.inf)
+    run_odd(cache, q, cu, max(news), max(lens), spoil)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,news", SIZES + [([300, 2700, 90], [6, 4, 5])])
+def test_the_next_call_knows_nothing_of_it(lens, news, dtype):
+    """One captured call on one workspace: values that are not finite, then finite ones again."""
+    cache, q, cu = make(lens, news, 3, 3, 64, 32, dtype, seed=31)
+    start, values = cache.demand_pages.clone(), cache.v_pages.clone()
+    for max_len in (max(lens), LONG + 200):
+        ref = b.dilution_attn_paged_chunk(q, cache, cu, max(news), max_len)
+        total = cache.demand_pages.clone()
+        ws = b.dilution_attn_paged_chunk_workspace(cache, q.shape[0], max(news), max_len)
+        out, g = torch.zeros_like(q), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            b.dilution_attn_paged_chunk(q, cache, cu, max(news), max_len, out, workspace=ws)
+        for spoilt in (True, False, True):
+            cache.demand_pages.copy_(start)
+            if spoilt:
+                put(cache.v_pages, cache, 1, lens[1] - 1, 0, slice(0, 64), np.nan)
+            g.replay()
+            row = int(cu[2]) - 1
+            same = (out == ref).all(-1)
+            same[row, 0] ^= spoilt       # that row's head 0 alone is NaN, and only then
+            assert same.all() and torch.equal(cache.demand_pages, total)
+            assert torch.isnan(out[row, 0]).all() == spoilt
+            cache.v_pages.copy_(values)
+        cache.demand_pages.copy_(start)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
