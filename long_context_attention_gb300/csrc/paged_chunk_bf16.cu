@@ -486,12 +486,18 @@ __device__ __forceinline__ void ckx_put(uint32_t at, uint32_t a, uint32_t b, uin
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// The denominators' first part: 1e18 at most, so that the product of two is finite and an
-// infinite total leaves its key no share to speak of; NaN stays.
-__device__ __forceinline__ float ckx_den(float total, float eps) {
-  const float d = total + eps;
-  return d > 1e18f ? 1e18f : d;
-}
+// The denominators' first part, up to 1e18, so that the product of two is finite; above that
+// a bid (at most 1) does not change it, and 1e18 / it is a factor of the shares instead (0
+// where it is infinite).  NaN stays.
+constexpr float kCkxLarge = 1e18f;
+struct CkxDen {
+  float base, scale;
+  __device__ __forceinline__ explicit CkxDen(float den) {
+    const bool large = den > kCkxLarge;
+    base = large ? kCkxLarge : den;
+    scale = large ? rcp_approx(den * (1.f / kCkxLarge)) : 1.f;
+  }
+};
 
 // 32 rows of one key (its logits; -infinity where a row does not see it): bids, then
 // shares as bf16 pairs.  `added`: what the column tile's rows have added to the key's total so
@@ -910,6 +916,8 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
         const int first = x.P + x.i0;   // place of row 0
         const float c2 = x.c2;
         for (; j < end; j += kG, ++m) {
+          const float den = total + p.eps;
+          if (__any_sync(0xffffffffu, den > kCkxLarge)) break;
           const int next_page = j + kG < end ? page_of(j + kG) : -1;
           float *next_at = nullptr;
           float next_total = 0.f;
@@ -920,7 +928,6 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
             if (next_at != nullptr) next_total = __ldcg(next_at);
           }
           const bool mask = (j + 1) * kCkxEdge - 1 > first || rows < kCkxEdge;
-          const float den = ckx_den(total, p.eps);
           const float2 base = make_float2(den, den);
           float added = 0.f;
           uint32_t nl[4], to[4];
@@ -964,10 +971,12 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
           at = next_at;
           total = next_total;
         }
-      } else {
+      }
+      if (ok && j < end) {
         // several heads of n8 rows: 8 rows at a time, a head's total from its first rows to its last.
-        // (Or one head's, where a row needs the care that this loop takes: a least value for
-        // every pair's denominators costs the other 4 %, bids set to zero after they are formed as much.)
+        // (Or one head's, where a row's sum or a key's total needs the care that this loop takes: in
+        // the other a least value for every pair's denominators costs 4 %, bids set to zero after
+        // they are formed as much, and their scale 4 % too.)
         const int groups = (rows + 7) / 8, n8 = x.n8 ? x.n8 : 8 * groups, per = n8 / 8, n = x.n8 ? x.n : rows, P = x.P + x.i0,
                   head0 = x.s * p.c.Hq + x.hq0;
         const bool two = x.two_terms();
@@ -986,6 +995,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
           float *head_at = at;
           float head_next = 0.f, added = 0.f, c2 = 0.f;
           int q = 0;   // query of the group's first row
+          CkxDen den(total + p.eps);
           float v[8];
           tmem_ld8(ts, v);
           for (int u = 0, h = 0; u < groups; ++u) {
@@ -1010,8 +1020,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
             else
               ckx_release(&s_free[g], lane);
             uint32_t pk[4], pk2[4];
-            const float den = ckx_den(total, p.eps);
-            const float2 b2 = make_float2(den, den);
+            const float2 b2 = make_float2(den.base, den.base);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               d[e] = added;
@@ -1022,7 +1031,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
             for (int e = 0; e < 4; ++e) {
               float2 dd = fadd2(make_float2(d[2 * e + 1], d[2 * e]), b2);
               if (!EARLIER) dd.x = fminf(dd.x, 2e18f);   // a NaN of the later row alone (else: both are below)
-              const float r = rcp_approx(dd.x * dd.y);
+              const float r = rcp_approx(dd.x * dd.y) * den.scale;
               const float2 s2 = fmul2(fmul2(make_float2(bid[2 * e], bid[2 * e + 1]), dd), make_float2(r, r));
               pk[e] = pack_bf16x2(s2.x, s2.y);
               pk2[e] = pack_bf16x2(s2.x - __uint_as_float(pk[e] << 16), s2.y - __uint_as_float(pk[e] & 0xffff0000u));
@@ -1042,6 +1051,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
                 head_at += ps;
               }
               total = head_next;
+              den = CkxDen(total + p.eps);
               added = 0.f;
             }
           }

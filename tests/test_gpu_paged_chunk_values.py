@@ -1,4 +1,4 @@
-"""Chunks over the paged cache where something is not finite.
+"""Chunks over the paged cache where something is not finite, or a total is very large.
 
 A chunk of n tokens is n decode steps: what a query does not see cannot reach its output, whatever it holds.  What it
 sees does: an infinite value gives an infinite output, NaN and infinities of both signs NaN; a NaN in a query or key
@@ -11,8 +11,8 @@ import torch
 
 from long_context_attention_gb300 import binding as b
 from tests._parity import host64
-from tests._paged import LONG
-from tests.test_gpu_paged_chunk import make, oracle
+from tests._paged import DEV, LONG
+from tests.test_gpu_paged_chunk import make, oracle, run
 
 pytestmark = pytest.mark.gpu
 
@@ -125,3 +125,39 @@ def test_a_key_of_its_own_block(P, n):
     """A NaN in the last key, the only one of its 32 that the last row sees."""
     cache, q, cu = make([P + n], [n], 2, 2, 64, 64, "bf16", seed=n)
     run_odd(cache, q, cu, n, P + n, lambda c, q: put(c.k_pages, c, 0, P + n - 1, 0, slice(0, 1), np.nan))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("flags", [0, 1])
+@pytest.mark.parametrize("lens,news", SIZES)
+def test_very_large_totals(lens, news, flags, dtype):
+    """Finite totals of up to 1e30 divide as any other: all of a head's, some of another's."""
+    cache, q, cu = make(lens, news, 4, 2, 64, 32, dtype, seed=7, fresh=False)
+    g = torch.Generator().manual_seed(8)
+    size = torch.randint(18, 31, cache.demand_pages.shape, generator=g).float()
+    big = (10.0 ** size * (1 + torch.rand(size.shape, generator=g))).to(DEV)
+    some = (torch.rand(size.shape, generator=g) < 0.3).to(DEV)
+    some[:, 0] = True
+    cache.demand_pages.copy_(torch.where(some, big, cache.demand_pages))
+    run(cache, q, cu, max(news), max(lens), flags=flags)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,news", SIZES)
+def test_all_totals_infinite(lens, news, dtype):
+    """No key has a share: NaN, as a decode step's 0 / 0, of that head alone."""
+    cache, q, cu = make(lens, news, 4, 2, 64, 32, dtype, seed=9)
+
+    def spoil(cache, q):
+        t = torch.arange(lens[0], device=DEV)
+        cache.demand_pages[cache.demand_table[0, t // 32].long(), 2, t % 32] = float("inf")
+    run_odd(cache, q, cu, max(news), max(lens), spoil)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("flags", [0, 1])
+@pytest.mark.parametrize("lens,news", SIZES)
+def test_a_very_large_eps(lens, news, flags, dtype):
+    """eps of 1e25: the shares are the bids', and the totals grow by them all the same."""
+    cache, q, cu = make(lens, news, 4, 2, 64, 32, dtype, seed=10)
+    run(cache, q, cu, max(news), max(lens), flags=flags, eps=1e25)
