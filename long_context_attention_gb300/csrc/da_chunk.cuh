@@ -99,6 +99,7 @@ struct ChunkPlan {
   size_t seq_off, cum_off, odd_off, ml_a, ml_b, nl, acc_a, acc_b, total;
   size_t logits;         // q . k of (token, query head) and key, where they are kept
   int logits_ld;         // their keys (0: not kept)
+  int logits_seq;        // tokens that each sequence has of them (0: as many as are new, one behind the other)
 };
 constexpr int kChunkLogits = 128;   // their keys are a multiple of this, a key tile of bf16
 
@@ -320,6 +321,12 @@ struct ChunkWalk {
   }
   __device__ __forceinline__ int hkv(const ChunkPlan &w) const { return g.wide ? seg / w.G : seg; }
 };
+
+// The kept logits of a sequence's query.
+__device__ __forceinline__ float *chunk_logits(const PagedChunk &p, const ChunkPlan &w, int s, int tok0, int query, int hq) {
+  const size_t token = w.logits_seq > 0 ? (size_t)s * w.logits_seq + query : (size_t)tok0 + query;
+  return reinterpret_cast<float *>(p.ws + w.logits) + (token * p.c.Hq + hq) * (size_t)w.logits_ld;
+}
 
 // The place of the piece's row r (of the segment) among `stride` floats a row.
 __device__ __forceinline__ float *chunk_place(const PagedChunk &p, size_t a, size_t b, long long row0, int cta_rows, int tile,

@@ -55,6 +55,7 @@ ChunkPlan chunk_plan_bf16(int S, int Hq, int Hkv, int d, long long N, int max_ne
   if (chunk_few(S, Hq, Hkv, d, N, max_new, max_len)) {   // behind what every call needs
     w.logits = w.total;
     w.logits_ld = (int)round_up(max_len, kChunkLogits);
+    w.logits_seq = N > (long long)S * max_new ? max_new : 0;   // (padded: no room for so many tokens)
   }
   return w;
 }
@@ -331,8 +332,7 @@ __global__ void __launch_bounds__(CkxKeys<D>::kThreads, 2)
         c2 = fmaxf(head_c2(p.hs, x.s * p.c.Hq + x.hq0 + (x.n8 ? c / x.n8 : 0), g == 0 ? p.status : nullptr), 1e-30f);
       float *kept = nullptr;
       if (KEEP && valid)
-        kept = reinterpret_cast<float *>(p.ws + w.logits) +
-               ((size_t)(x.tok0 + q) * p.c.Hq + x.hq0 + (x.n8 ? c / x.n8 : 0)) * (size_t)w.logits_ld + first * kCkxEdge;
+        kept = chunk_logits(p, w, x.s, x.tok0, q, x.hq0 + (x.n8 ? c / x.n8 : 0)) + first * kCkxEdge;
       __syncwarp();
       if (lane == 0) mbar_arrive(&r_free[i % kCkxRing]);
       if (rows == 0) break;

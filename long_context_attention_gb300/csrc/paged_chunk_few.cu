@@ -40,15 +40,16 @@ struct Ckl {
 
 // Whether a call's logits are kept: a key head's group has at most d / 8 rows, whose
 // logits, written and read, are half of the bytes of K, and they take at most 2 GB of
-// workspace (and no sequence's share of the tokens is padding).  Times in us of both second passes' calls (sequences x query / key heads x
+// workspace.  Times in us of both second passes' calls (sequences x query / key heads x
 // keys, new tokens; kept / not):
 //   d = 64, 8 x 12/12 x 131072: 1 583 / 838, 4 620 / 818, 8 699 / 834, 16 1167 / 844;
 //     8 x 12/4 x 32768: 1 113 / 139, 2 116 / 140, 5 (15 rows) 140 / 138;
 //     64 x 12/12 x 4096: 4 215 / 277, 16 337 / 281; 1 x 12/12 x 16384: 4 62 / 67;
 //   d = 128, 8 x 16/4 x 131072: 4 (16 rows) 547 / 614; 4 x 32/2 x 65536: 1 (16 rows) 155 / 265.
 bool chunk_few(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len) {
-  return (long long)(Hq / Hkv) * max_new * 8 <= d && N <= (long long)S * max_new &&
-         N * Hq * round_up(max_len, kChunkLogits) * 4 <= kChunkLogitBytes;
+  const long long tokens = N < (long long)S * max_new ? N : (long long)S * max_new;   // (more are padding)
+  return max_new > 0 && (long long)(Hq / Hkv) * max_new * 8 <= d &&
+         tokens * Hq * round_up(max_len, kChunkLogits) * 4 <= kChunkLogitBytes;
 }
 // Their room in a workspace that serves all calls within these bounds: of those with
 // the most tokens and rows that keep them.
@@ -92,8 +93,7 @@ __global__ void __launch_bounds__(Ckl<D, ROWS>::kThreads, 1) ckl_values(PagedChu
       const int h = tid / n, q = tid % n;
       s_row[tid] = make_float2(fmaxf(head_c2(p.hs, k.s * p.c.Hq + hq0 + h, nullptr), 1e-30f),
                                __ldcg(reinterpret_cast<const float *>(p.ws + w.nl) + row0 + h * n8 + q));
-      s_logits[tid] = reinterpret_cast<uint64_t>(reinterpret_cast<const float *>(p.ws + w.logits) +
-                                                 ((size_t)(k.q.tok0 + q) * p.c.Hq + hq0 + h) * (size_t)w.logits_ld);
+      s_logits[tid] = reinterpret_cast<uint64_t>(chunk_logits(p, w, k.s, k.q.tok0, q, hq0 + h));
     }
     const bool odd = __ldcg(chunk_odd(p, w) + k.s) != 0;
     for (int e = lane; e < C::kShRows * C::kShRow / 4; e += 32) reinterpret_cast<uint32_t *>(shares)[e] = 0u;   // rows from R on stay 0
