@@ -110,9 +110,7 @@ struct CkfPages {
       if (!ok && key < k.g.len) atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
       const float *from = static_cast<const float *>(pages);
       if (ok) from += ((((size_t)page[i] * p.c.Hkv + hkv) << sh) + (key & (ps - 1))) * D + 4 * x;
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to + j * Ckf<D>::kLd + 4 * x)),
-                   "l"(reinterpret_cast<uint64_t>(from)), "r"(ok ? 16 : 0)
-                   : "memory");
+      cp_async16_fill(smem_u32(to + j * Ckf<D>::kLd + 4 * x), from, ok);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }

@@ -61,12 +61,6 @@ size_t chunk_few_room(int S, int Hq, int Hkv, int d, long long N, int max_new, i
   return (size_t)(bytes < kChunkLogitBytes ? bytes : kChunkLogitBytes);
 }
 
-__device__ __forceinline__ void ckl_copy(uint32_t dst, const void *src, bool have) {   // zeros where !have
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
-               "r"(have ? 16 : 0)
-               : "memory");
-}
-
 template <int D, int ROWS>
 __global__ void __launch_bounds__(Ckl<D, ROWS>::kThreads, 1) ckl_values(PagedChunk p, ChunkPlan w) {
   using C = Ckl<D, ROWS>;
@@ -123,14 +117,14 @@ __global__ void __launch_bounds__(Ckl<D, ROWS>::kThreads, 1) ckl_values(PagedChu
       for (int u = 0; u < PP; ++u) {
         const int e = lane + 32 * u, r = e / PP, i = e % PP;
         const uint64_t from = __shfl_sync(0xffffffffu, v, r);
-        ckl_copy(to + piece(r, i), reinterpret_cast<const void *>(from ? from + 16 * i : reinterpret_cast<uint64_t>(p.c.v_pages)), from != 0);
+        cp_async16_fill(to + piece(r, i), reinterpret_cast<const void *>(from ? from + 16 * i : reinterpret_cast<uint64_t>(p.c.v_pages)), from != 0);
       }
       for (int r = lane / 8; r < R; r += 4)   // keys 4 (lane % 8) ..
-        ckl_copy(to + C::kOffX + (r * 8 + lane % 8) * 16, reinterpret_cast<const void *>(s_logits[r] + 4 * first + lane % 8 * 16), true);
+        cp_async16_fill(to + C::kOffX + (r * 8 + lane % 8) * 16, reinterpret_cast<const void *>(s_logits[r] + 4 * first + lane % 8 * 16), true);
       // a page holds all keys of four
       const uint64_t four = __shfl_sync(0xffffffffu, t, lane % 8 * 4);
       for (int h = lane / 8; h < G; h += 4)
-        ckl_copy(to + C::kOffT + (h * 8 + lane % 8) * 16,
+        cp_async16_fill(to + C::kOffT + (h * 8 + lane % 8) * 16,
                  reinterpret_cast<const void *>(four ? four + ((uint64_t)h << sh) * 4 : reinterpret_cast<uint64_t>(p.c.demand_pages)), four != 0);
     };
     float acc[D / 8][4], sums[ROWS];

@@ -42,37 +42,6 @@ int chunk_small_cluster(int S, int Hq, int Hkv, int max_new, int max_len, int dt
   return c;
 }
 
-__device__ __forceinline__ uint32_t cks_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cks_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cks_peer(const void *local, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ float2 cks_peer2(const float2 *local, uint32_t rank) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cks_peer(local, rank)) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 cks_peer4(const float *local, uint32_t rank) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(cks_peer(local, rank))
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ void cks_copy(uint32_t dst, const void *src, bool have) {   // zeros where !have
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
-               "r"(have ? 16 : 0)
-               : "memory");
-}
 // 16-byte piece i of row r of `pieces` pieces, swizzled by the row.
 __device__ __forceinline__ uint32_t cks_off(int r, int i, int pieces) { return (uint32_t)((r * pieces + (i ^ (r & 7))) << 4); }
 
@@ -81,7 +50,7 @@ struct CksPart {
   int s, hkv, a, n, n8, rows, P, key0, cnt, fill;   // first token; cnt keys from key0 on, fill with those up to 16
   bool any;
   __device__ __forceinline__ CksPart(const PagedChunk &p, int G, int csize) {
-    const int pair = blockIdx.x / csize, rank = (int)cks_rank();
+    const int pair = blockIdx.x / csize, rank = (int)cluster_rank();
     s = pair / p.c.Hkv;
     hkv = pair % p.c.Hkv;
     const int len = __ldcg(p.c.seq_lens + s), b = __ldcg(p.cu + s + 1);
@@ -110,7 +79,7 @@ __device__ __forceinline__ void cks_join(const float2 *s_ml, float *s_nl, int ro
   if ((int)threadIdx.x >= rows) return;
   float m = -INFINITY, sum = 0.f;
   for (int c = 0; c < csize; ++c) {
-    const float2 ml = cks_peer2(s_ml + threadIdx.x, (uint32_t)c);
+    const float2 ml = ld_peer(s_ml + threadIdx.x, (uint32_t)c);
     const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
     sum = sum * ex2_approx(m - ms) + ml.y * ex2_approx(ml.x - ms);
     m = mn;
@@ -135,12 +104,10 @@ __device__ __forceinline__ void cks_stats(const float *sP, int ld, const CksPart
 }
 
 // After a cluster barrier: whether a CTA of the cluster has cleared a value (last warp).
-__device__ __forceinline__ void cks_any(const int *s_odd, int *s_any, int csize) {
+__device__ __forceinline__ void cks_any(const uint32_t *s_odd, uint32_t *s_any, int csize) {
   const int lane = threadIdx.x - (kCksThreads - 32);
   if (lane < 0) return;
-  int odd = 0;
-  if (lane < csize) asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(odd) : "r"(cks_peer(s_odd, (uint32_t)lane)) : "memory");
-  odd = __any_sync(0xffffffffu, odd != 0);
+  const uint32_t odd = __any_sync(0xffffffffu, lane < csize && ld_peer(s_odd, (uint32_t)lane) != 0);
   if (lane == 0) *s_any = odd;
 }
 
@@ -149,19 +116,17 @@ __device__ __forceinline__ void cks_any(const int *s_odd, int *s_any, int csize)
 template <int D, typename E>
 __device__ __forceinline__ void cks_out(const PagedChunk &p, const CksPart &k, int G, const float *num, int parts, int rows_max, int stage,
                                         const float *s_sum, int csize, int page_shift, bool odd) {
-  for (int e = (int)cks_rank() * kCksThreads + threadIdx.x; e < k.rows * (D / 4); e += csize * kCksThreads) {
+  for (int e = (int)cluster_rank() * kCksThreads + threadIdx.x; e < k.rows * (D / 4); e += csize * kCksThreads) {
     const int r = e / (D / 4), c = e % (D / 4), h = r / k.n8, q = r % k.n8;
     if (q >= k.n) continue;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     float sum = 0.f;
     for (int i = 0; i < csize; ++i) {
       for (int part = 0; part < parts; ++part) {
-        const float4 v = cks_peer4(num + (part * rows_max + r) * stage + 4 * c, (uint32_t)i);
+        const float4 v = ld_peer4(num + (part * rows_max + r) * stage + 4 * c, (uint32_t)i);
         a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
       }
-      float x;
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(cks_peer(s_sum + r, (uint32_t)i)) : "memory");
-      sum += x;
+      sum += ld_peer(s_sum + r, (uint32_t)i);
     }
     if (odd) chunk_see<D, E>(p, page_shift, k.s, k.hkv, k.P, k.P + q, 4 * c, a);
     const size_t to = ((size_t)(k.a + q) * p.c.Hq + k.hkv * G + h) * D + 4 * c;
@@ -197,7 +162,7 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk(PagedChunk p, int G,
   float *sP = reinterpret_cast<float *>(cks_smem + C::kOffP);
   __shared__ float2 s_ml[kCksRows];                     // this CTA's (max, sum) of the rows
   __shared__ float s_nl[kCksRows], s_sum[kCksRows];
-  __shared__ int s_odd, s_any;                          // values that are not finite: see da_chunk.cuh
+  __shared__ uint32_t s_odd, s_any;                          // values that are not finite: see da_chunk.cuh
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int ps = 1 << page_shift;
   pdl_wait();
@@ -210,7 +175,7 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk(PagedChunk p, int G,
   for (int e = tid; e < blocks * 16 * PP; e += kCksThreads) {
     const int r = e / PP, i = e % PP, h = r / n8, q = r % n8;
     const bool have = r < rows && q < n;
-    cks_copy(sQ + cks_off(r, i, PP),
+    cp_async16_fill(sQ + cks_off(r, i, PP),
              static_cast<const __nv_bfloat16 *>(p.q) + (have ? ((size_t)(a + q) * p.c.Hq + hkv * G + h) * D + 8 * i : 0), have);
   }
   {
@@ -231,8 +196,8 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk(PagedChunk p, int G,
         const bool ok = (unsigned)page[j] < (unsigned)p.c.num_pages;
         if (!ok && r < cnt) atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
         const size_t at = ok ? ((((size_t)page[j] * p.c.Hkv + hkv) << page_shift) + ((key0 + r) & (ps - 1))) * D + 8 * i : 0;
-        cks_copy(sK + cks_off(r, i, PP), static_cast<const __nv_bfloat16 *>(p.c.k_pages) + at, ok);
-        cks_copy(sV + cks_off(r, i, PP), static_cast<const __nv_bfloat16 *>(p.c.v_pages) + at, ok);
+        cp_async16_fill(sK + cks_off(r, i, PP), static_cast<const __nv_bfloat16 *>(p.c.k_pages) + at, ok);
+        cp_async16_fill(sV + cks_off(r, i, PP), static_cast<const __nv_bfloat16 *>(p.c.v_pages) + at, ok);
       }
     }
   }
@@ -303,7 +268,7 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk(PagedChunk p, int G,
   __syncthreads();
   // (max, sum) of every row over the CTA's keys, then over the cluster's
   cks_stats(sP, C::kLd, k, s_ml);
-  cks_sync();
+  cluster_sync();
   cks_join(s_ml, s_nl, rows, csize);
   cks_any(&s_odd, &s_any, csize);
   __syncthreads();
@@ -385,9 +350,9 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk(PagedChunk p, int G,
                                       2 * (lane % 4)) = make_float2(acc[rb][j][e], acc[rb][j][e + 1]);
     }
   }
-  cks_sync();
+  cluster_sync();
   cks_out<D, __nv_bfloat16>(p, k, G, sP, C::kSplit, kCksRows, C::kStage, s_sum, csize, page_shift, s_any != 0);
-  cks_sync();   // no CTA leaves while a peer may read it
+  cluster_sync();   // no CTA leaves while a peer may read it
 }
 
 // ------------------------------------------------------------------------- fp32
@@ -408,7 +373,7 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk_f32(PagedChunk p, in
   float *sNum = sK;                                     // numerators: over K
   __shared__ float2 s_ml[kCksRowsF32];
   __shared__ float s_nl[kCksRowsF32], s_sum[kCksRowsF32];
-  __shared__ int s_odd, s_any;                          // as above
+  __shared__ uint32_t s_odd, s_any;                          // as above
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, ps = 1 << page_shift;
   pdl_wait();
   pdl_launch_dependents();
@@ -418,7 +383,7 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk_f32(PagedChunk p, in
     const int r = e / PP, i = e % PP;
     const bool have = k.last(r) >= 0;
     const size_t at = have ? ((size_t)(k.a + r % k.n8) * p.c.Hq + k.hkv * G + r / k.n8) * D + 4 * i : 0;
-    cks_copy(smem_u32(sQ + r * C::kLd + 4 * i), static_cast<const float *>(p.q) + at, have);
+    cp_async16_fill(smem_u32(sQ + r * C::kLd + 4 * i), static_cast<const float *>(p.q) + at, have);
   }
   const int32_t *table = p.c.page_table + (size_t)k.s * p.c.max_pages;
   for (int e = tid; e < k.fill * PP; e += kCksThreads) {
@@ -427,8 +392,8 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk_f32(PagedChunk p, in
     const bool ok = (unsigned)page < (unsigned)p.c.num_pages;
     if (!ok && r < k.cnt) atomicCAS(p.status, DA_OK, DA_ERR_INVALID);
     const size_t at = ok ? ((((size_t)page * p.c.Hkv + k.hkv) << page_shift) + ((k.key0 + r) & (ps - 1))) * D + 4 * i : 0;
-    cks_copy(smem_u32(sK + r * C::kLd + 4 * i), static_cast<const float *>(p.c.k_pages) + at, ok);
-    cks_copy(smem_u32(sV + r * C::kLd + 4 * i), static_cast<const float *>(p.c.v_pages) + at, ok);
+    cp_async16_fill(smem_u32(sK + r * C::kLd + 4 * i), static_cast<const float *>(p.c.k_pages) + at, ok);
+    cp_async16_fill(smem_u32(sV + r * C::kLd + 4 * i), static_cast<const float *>(p.c.v_pages) + at, ok);
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
   // the totals: a thread a key and every other head
@@ -489,7 +454,7 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk_f32(PagedChunk p, in
   }
   __syncthreads();
   cks_stats(sP, C::kLdP, k, s_ml);
-  cks_sync();
+  cluster_sync();
   cks_join(s_ml, s_nl, k.rows, csize);
   cks_any(&s_odd, &s_any, csize);
   __syncthreads();
@@ -550,9 +515,9 @@ __global__ void __launch_bounds__(kCksThreads, 1) cks_chunk_f32(PagedChunk p, in
       if (lane == 0) s_sum[row] = sum[r];
     }
   }
-  cks_sync();
+  cluster_sync();
   cks_out<D, float>(p, k, G, sNum, 1, kCksRowsF32, C::kLd, s_sum, csize, page_shift, s_any != 0);
-  cks_sync();   // no CTA leaves while a peer may read it
+  cluster_sync();   // no CTA leaves while a peer may read it
 }
 
 template <typename Kernel>

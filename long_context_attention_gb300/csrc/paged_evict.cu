@@ -55,29 +55,6 @@ EvictWorkspace evict_workspace(int S, int Hkv, int max_keep, int max_len) {
   return w;
 }
 
-__device__ __forceinline__ uint32_t ev_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void ev_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t ev_peer(const void *local, uint32_t rank) {   // a word of a peer's shared memory
-  uint32_t a, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-
-__device__ __forceinline__ uint4 ev_peer4(const void *local, uint32_t rank) {   // four words, 16-byte aligned
-  uint32_t a;
-  uint4 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-
 // Scores as integers of the same order; NaN as +infinity, -0 as 0.
 __device__ __forceinline__ uint32_t ev_key(float f) {
   const uint32_t u = __float_as_uint(f);
@@ -91,7 +68,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(EvictArgs a, EvictWo
   __shared__ __align__(16) uint32_t s_hist[kCopies + 1][kBins];   // the first pass's (the third's in its first copy); the second's
   __shared__ uint32_t s_above[kSelWarps], s_equal[kSelWarps], s_count[2], s_pick[2];
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const uint32_t rank = ev_rank(), C = (uint32_t)w.cluster;
+  const uint32_t rank = cluster_rank(), C = (uint32_t)w.cluster;
   pdl_wait();
   pdl_launch_dependents();
   const int item = blockIdx.x / w.cluster, s = item / a.c.Hkv, h = item % a.c.Hkv, G = a.c.Hq / a.c.Hkv;
@@ -173,7 +150,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(EvictArgs a, EvictWo
         for (int k = 1; k < kCopies; ++k) hist[i] += hist[k * kBins + i];
     }
     if (C > 1)
-      ev_sync();
+      cluster_sync();
     else
       __syncthreads();
     // thread i: 4 bins from the top.  (A CTA reads its peers' counts 16 bytes at a time: word
@@ -184,7 +161,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(EvictArgs a, EvictWo
       if (C > 1) {
 #pragma unroll 8
         for (uint32_t r = 0; r < C; ++r) {
-          const uint4 x = ev_peer4(hist + bin0, r);
+          const uint4 x = ld_peer4(hist + bin0, r);
           c[0] += x.w, c[1] += x.z, c[2] += x.y, c[3] += x.x;
         }
       } else {
@@ -246,11 +223,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(EvictArgs a, EvictWo
     s_count[0] = x, s_count[1] = y;
   }
   if (C > 1)
-    ev_sync();
+    cluster_sync();
   else
     __syncthreads();
   uint32_t na = s_above[warp], ne = s_equal[warp];
-  for (uint32_t r = 0; r < rank; ++r) na += ev_peer(&s_count[0], r), ne += ev_peer(&s_count[1], r);
+  for (uint32_t r = 0; r < rank; ++r) na += ld_peer(&s_count[0], r), ne += ld_peer(&s_count[1], r);
   for (int i = r0; i < r1; i += 32) {
     const bool in = i + lane < r1;
     const uint32_t key = in ? keys[i + lane] : 0u;
@@ -261,7 +238,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(EvictArgs a, EvictWo
     na += __popc(ba);
     ne += __popc(be);
   }
-  if (C > 1) ev_sync();   // no CTA leaves while a peer may read it
+  if (C > 1) cluster_sync();   // no CTA leaves while a peer may read it
 }
 
 // ------------------------------------------------------------------------- the rows

@@ -41,27 +41,6 @@ int small_cluster(int S, int Hq, int Hkv, int d, int max_len) {
   return c;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float ld_peer(const float *local, uint32_t rank) {   // the same place in a peer's shared memory
-  uint32_t a;
-  float v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ void cp_async16_fill(uint32_t dst, const void *src, bool have) {   // zeros where !have
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
-               "r"(have ? 16 : 0)
-               : "memory");
-}
-
 // Row r (d elements), 16-byte piece i of a chunk: pieces swizzled by the row.
 template <int D>
 __device__ __forceinline__ uint32_t small_off(int r, int i) {
