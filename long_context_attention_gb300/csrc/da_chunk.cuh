@@ -29,7 +29,7 @@
 // Values that are not finite.  A query's share of a key that it does not see is 0, and 0
 // times infinity or NaN would be NaN.  So such elements of new tokens' values are cleared
 // where they enter the products, and added to the outputs of the rows that see them; a
-// flag a sequence (chunk_join) says whether there are any.
+// flag a sequence and a bit a token and key head (chunk_join) say whether there are any.
 #pragma once
 
 #include "da_paged.h"
@@ -96,7 +96,7 @@ struct ChunkPlan {
   ChunkCost cost;
   long long rows;        // rows of all heads, at most
   int cta_rows;          // rows of a CTA's places
-  size_t seq_off, cum_off, odd_off, ml_a, ml_b, nl, acc_a, acc_b, total;
+  size_t seq_off, cum_off, odd_off, map_off, ml_a, ml_b, nl, acc_a, acc_b, total;
   size_t logits;         // q . k of (token, query head) and key, where they are kept
   int logits_ld;         // their keys (0: not kept)
   int logits_seq;        // tokens that each sequence has of them (0: as many as are new, one behind the other)
@@ -129,7 +129,8 @@ inline ChunkPlan chunk_plan(int S, int Hq, int Hkv, int d, long long N, int max_
   w.seq_off = kStatusBytes;
   w.cum_off = next(w.seq_off, ((long long)S + 1) * (long long)sizeof(ChunkSeq));   // (the last: how many rows a head)
   w.odd_off = next(w.cum_off, ((long long)S + 1) * 8);
-  w.ml_a = next(w.odd_off, (long long)S * 4);
+  w.map_off = next(w.odd_off, (long long)S * 4);
+  w.ml_a = next(w.map_off, w.rows / 8 / w.G);
   w.ml_b = next(w.ml_a, w.rows * 8);
   w.nl = next(w.ml_b, b_keys * 8);
   w.acc_a = next(w.nl, w.rows * 4);
@@ -218,6 +219,10 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkLine &l, int s) {
 
 // Whether a new token of the sequence has a value that is not finite.
 __device__ __forceinline__ int *chunk_odd(const PagedChunk &p, const ChunkPlan &w) { return reinterpret_cast<int *>(p.ws + w.odd_off); }
+// Of which eight of them (from row0 + 8 i of the rows of a head) and key head.
+__device__ __forceinline__ uint8_t *chunk_odd_map(const PagedChunk &p, const ChunkPlan &w, int row, int hkv) {
+  return p.ws + w.map_off + (size_t)(row / 8) * p.c.Hkv + hkv;
+}
 __device__ __forceinline__ bool chunk_not_finite(uint32_t x) { return (x & 0x7f800000u) == 0x7f800000u; }   // bits of a float
 // Of 16 bytes of values, bf16 or fp32: zeros for what is not finite; whether there was any.
 __device__ __forceinline__ bool chunk_clear(uint4 &v, bool half) {
@@ -230,26 +235,24 @@ __device__ __forceinline__ bool chunk_clear(uint4 &v, bool half) {
   }
   return any;
 }
-// What is not finite of columns c .. c + 3 of the values of tokens t0 .. t1, onto a.
+// What is not finite of columns c .. c + 3 of token t's values, onto a.
 template <int D, typename E>
-__device__ void chunk_see(const PagedChunk &p, int sh, int s, int hkv, int t0, int t1, int c, float4 &a) {
-  for (int t = t0; t <= t1; ++t) {
-    const int page = __ldcg(p.c.page_table + (size_t)s * p.c.max_pages + (t >> sh));
-    if ((unsigned)page >= (unsigned)p.c.num_pages) continue;
-    const E *at = static_cast<const E *>(p.c.v_pages) +
-                  ((((size_t)page * p.c.Hkv + hkv) << sh) + (t & ((1 << sh) - 1))) * D + c;
-    uint4 x;
-    if constexpr (sizeof(E) == 4) {
-      x = __ldcg(reinterpret_cast<const uint4 *>(at));
-    } else {
-      const uint2 y = __ldcg(reinterpret_cast<const uint2 *>(at));
-      x = make_uint4(y.x << 16, y.x & 0xffff0000u, y.y << 16, y.y & 0xffff0000u);
-    }
-    if (chunk_not_finite(x.x)) a.x += __uint_as_float(x.x);
-    if (chunk_not_finite(x.y)) a.y += __uint_as_float(x.y);
-    if (chunk_not_finite(x.z)) a.z += __uint_as_float(x.z);
-    if (chunk_not_finite(x.w)) a.w += __uint_as_float(x.w);
+__device__ __forceinline__ void chunk_see(const PagedChunk &p, int sh, int s, int hkv, int t, int c, float4 &a) {
+  const int page = __ldcg(p.c.page_table + (size_t)s * p.c.max_pages + (t >> sh));
+  if ((unsigned)page >= (unsigned)p.c.num_pages) return;
+  const E *at = static_cast<const E *>(p.c.v_pages) +
+                ((((size_t)page * p.c.Hkv + hkv) << sh) + (t & ((1 << sh) - 1))) * D + c;
+  uint4 x;
+  if constexpr (sizeof(E) == 4) {
+    x = __ldcg(reinterpret_cast<const uint4 *>(at));
+  } else {
+    const uint2 y = __ldcg(reinterpret_cast<const uint2 *>(at));
+    x = make_uint4(y.x << 16, y.x & 0xffff0000u, y.y << 16, y.y & 0xffff0000u);
   }
+  if (chunk_not_finite(x.x)) a.x += __uint_as_float(x.x);
+  if (chunk_not_finite(x.y)) a.y += __uint_as_float(x.y);
+  if (chunk_not_finite(x.z)) a.z += __uint_as_float(x.z);
+  if (chunk_not_finite(x.w)) a.w += __uint_as_float(x.w);
 }
 
 // The last sequence with cum <= u (one with units, for u on the line).  A warp's

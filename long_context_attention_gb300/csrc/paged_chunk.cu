@@ -175,22 +175,22 @@ __device__ __forceinline__ void row_groups(const PagedChunk &p, const ChunkPlan 
   }
 }
 
-// Whether a value of eight new tokens (of which n are) of a key head is not finite.
-__device__ __forceinline__ bool values_odd(const PagedChunk &p, int sh, int s, int hkv, int t, int n, int lane) {
+// Which of eight tokens (n of them are) of a key head have a value that is not finite: a bit each.
+__device__ __forceinline__ unsigned values_odd(const PagedChunk &p, int sh, int s, int hkv, int t, int n, int lane) {
   const bool half = p.c.dtype == DA_BF16;
   const int pieces = p.c.d * (half ? 2 : 4) / 16;   // of 16 bytes: 8, 16 or 32
   int page = -1;
   if (lane < n) page = __ldcg(p.c.page_table + (size_t)s * p.c.max_pages + ((t + lane) >> sh));
-  bool odd = false;
+  unsigned odd = 0;
 #pragma unroll 4
   for (int e = lane; e < 8 * pieces; e += 32) {
     const int r = e / pieces, pg = __shfl_sync(0xffffffffu, page, r);
     if ((unsigned)pg >= (unsigned)p.c.num_pages) continue;
     uint4 v = __ldcg(reinterpret_cast<const uint4 *>(p.c.v_pages) +
                      ((((size_t)pg * p.c.Hkv + hkv) << sh) + ((t + r) & ((1 << sh) - 1))) * pieces + e % pieces);
-    odd |= chunk_clear(v, half);
+    odd |= (unsigned)chunk_clear(v, half) << r;
   }
-  return __any_sync(0xffffffffu, odd);
+  return __reduce_or_sync(0xffffffffu, odd);
 }
 
 // -lse2 of every row, from (max, sum) of its pieces: a lane takes a row's every
@@ -207,9 +207,11 @@ __global__ void __launch_bounds__(32 * kRowWarps, kJoinCtas) chunk_join(PagedChu
   const int blocks = gridDim.x / 2;
   if ((int)blockIdx.x >= blocks) {
     row_groups(p, w, l, rows, run, blockIdx.x - blocks, blocks, lane, [&](const ChunkRows &x, long long, bool) {
-      if (x.hq % w.G == 0 &&
-          values_odd(p, w.page_shift, x.s, x.hq / w.G, x.g.P + x.i, min(x.q.n - x.i, 8), lane) && lane == 0)
-        chunk_odd(p, w)[x.s] = 1;
+      if (x.hq % w.G != 0) return;
+      const unsigned odd = values_odd(p, w.page_shift, x.s, x.hq / w.G, x.g.P + x.i, min(x.q.n - x.i, 8), lane);
+      if (lane > 0) return;
+      *chunk_odd_map(p, w, x.q.row0 + x.i, x.hq / w.G) = (uint8_t)odd;
+      if (odd != 0) chunk_odd(p, w)[x.s] = 1;
     });
     return;
   }
@@ -287,12 +289,22 @@ __global__ void __launch_bounds__(32 * kRowWarps, kCombineCtas) chunk_combine(Pa
         for (int e = 0; e < PER; ++e) a[e].x += v[e].x, a[e].y += v[e].y, a[e].z += v[e].z, a[e].w += v[e].w;
       }
     }
-    if (!valid) return;
-    if (odd) {
+    if (odd) {   // what the rows see that is not finite, 32 times eight tokens at a time
+      for (int i0 = 0; i0 <= x.i; i0 += 8 * 32) {
+        const unsigned mine = i0 + 8 * lane <= x.i ? __ldcg(chunk_odd_map(p, w, x.q.row0 + i0 + 8 * lane, x.hq / w.G)) : 0u;
+        for (unsigned have = __ballot_sync(0xffffffffu, mine != 0); have; have &= have - 1) {
+          const int from = __ffs(have) - 1;
+          for (unsigned bits = __shfl_sync(0xffffffffu, mine, from); bits; bits &= bits - 1) {
+            const int i = i0 + 8 * from + __ffs(bits) - 1;
+            if (valid && i <= x.i + r)
 #pragma unroll
-      for (int e = 0; e < PER; ++e)
-        chunk_see<D, E>(p, w.page_shift, x.s, x.hq / w.G, x.g.P, x.g.P + x.i + r, lane / 8 * 4 + 16 * e, a[e]);
+              for (int e = 0; e < PER; ++e)
+                chunk_see<D, E>(p, w.page_shift, x.s, x.hq / w.G, x.g.P + i, lane / 8 * 4 + 16 * e, a[e]);
+          }
+        }
+      }
     }
+    if (!valid) return;
     // a normal reciprocal: one division does for the row
     const bool plain = sum >= 0x1p-100f && sum <= 0x1p100f;
     const float inv = plain ? 1.f / sum : 0.f;

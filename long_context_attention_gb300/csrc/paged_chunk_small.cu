@@ -128,7 +128,8 @@ __device__ __forceinline__ void cks_out(const PagedChunk &p, const CksPart &k, i
       }
       sum += ld_peer(s_sum + r, (uint32_t)i);
     }
-    if (odd) chunk_see<D, E>(p, page_shift, k.s, k.hkv, k.P, k.P + q, 4 * c, a);
+    if (odd)
+      for (int t = k.P; t <= k.P + q; ++t) chunk_see<D, E>(p, page_shift, k.s, k.hkv, t, 4 * c, a);
     const size_t to = ((size_t)(k.a + q) * p.c.Hq + k.hkv * G + h) * D + 4 * c;
     if constexpr (sizeof(E) == 4)
       *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + to) = make_float4(a.x / sum, a.y / sum, a.z / sum, a.w / sum);

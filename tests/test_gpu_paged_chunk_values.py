@@ -161,3 +161,23 @@ def test_a_very_large_eps(lens, news, flags, dtype):
     """eps of 1e25: the shares are the bids', and the totals grow by them all the same."""
     cache, q, cu = make(lens, news, 4, 2, 64, 32, dtype, seed=10)
     run(cache, q, cu, max(news), max(lens), flags=flags, eps=1e25)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,places", [(3000, [0, 7, 8, 255, 256, 2049, 2999]), (8500, [100, 8191, 8192, 8300]), (2900, list(range(2900)))])
+def test_long_parts(T, places, dtype):
+    """Infinite values here and there, across the rounds of a long part, or of every token: each row has those of the tokens
+    up to its own, and the bits of the clean call elsewhere."""
+    d = 64
+    cache, q, cu = make([T, 70], [T, 3], 2, 1, d, 64, dtype, seed=T, fresh=False)
+    start = cache.demand_pages.clone()
+    ref = b.dilution_attn_paged_chunk(q, cache, cu, T, T)
+    total = cache.demand_pages.clone()
+    cache.demand_pages.copy_(start)
+    for i, t in enumerate(places):
+        put(cache.v_pages, cache, 0, t, 0, slice(i % d, i % d + 1), np.inf if i % 2 else -np.inf)
+    out = b.dilution_attn_paged_chunk(q, cache, cu, T, T)
+    want = ref.clone()
+    for i, t in enumerate(places[:d]):
+        want[t:T, :, i % d] = np.inf if i % 2 else -np.inf
+    assert torch.equal(out, want) and torch.equal(cache.demand_pages, total)
