@@ -356,16 +356,21 @@ struct ChunkRows {
   int seen;              // key tiles that their column tile sees
   long long base, row0;  // the segment's place on the line; its first row
 };
-__device__ __forceinline__ bool chunk_rows(const PagedChunk &p, const ChunkPlan &w, const ChunkLine &l, long long row, int lane,
-                                           ChunkRows &x) {
-  int lo = 0, n = p.c.S;   // the last sequence whose first row is at or before this one (see chunk_find)
+// The last sequence whose first row, of `heads` heads, is at or before this one (see chunk_find).
+__device__ __forceinline__ int chunk_seq_of(const ChunkLine &l, int S, int heads, long long row, int lane) {
+  int lo = 0, n = S;
   while (n > 1) {
     const int step = (n + 31) / 32, at = lo + lane * step;
-    const bool le = lane * step < n && (long long)__ldcg(&l.seq[at].row0) * p.c.Hq <= row;
+    const bool le = lane * step < n && (long long)__ldcg(&l.seq[at].row0) * heads <= row;
     const int k = __popc(__ballot_sync(0xffffffffu, le)) - 1;
     lo += k * step;
     n = min(step, n - k * step);
   }
+  return lo;
+}
+__device__ __forceinline__ bool chunk_rows(const PagedChunk &p, const ChunkPlan &w, const ChunkLine &l, long long row, int lane,
+                                           ChunkRows &x) {
+  const int lo = chunk_seq_of(l, p.c.S, p.c.Hq, row, lane);
   x.s = lo;
   x.q = chunk_seq(l, lo);
   if (x.q.n == 0) return false;   // (of the sequences that begin there the last one: behind the last row)

@@ -158,8 +158,8 @@ constexpr int kJoinCtas = 4, kCombineCtas = 2;   // blocks an SM (three of the s
 // A warp's rows: `run` times eight in succession, found once for each column tile.
 template <typename F>
 __device__ __forceinline__ void row_groups(const PagedChunk &p, const ChunkPlan &w, const ChunkLine &l, long long rows, int run,
-                                           int block, int blocks, int lane, F &&f) {
-  for (long long r0 = 8ll * run * (block * kRowWarps + threadIdx.x / 32); r0 < rows; r0 += 8ll * run * blocks * kRowWarps) {
+                                           int blocks, int lane, F &&f) {
+  for (long long r0 = 8ll * run * (blockIdx.x * kRowWarps + threadIdx.x / 32); r0 < rows; r0 += 8ll * run * blocks * kRowWarps) {
     ChunkRows x;
     bool known = false, fresh = false;
     for (long long row = r0; row < r0 + 8 * run && row < rows; row += 8) {
@@ -194,9 +194,10 @@ __device__ __forceinline__ unsigned values_odd(const PagedChunk &p, int sh, int 
 }
 
 // -lse2 of every row, from (max, sum) of its pieces: a lane takes a row's every
-// fourth piece.  Blocks of their own, the second half, look through the new tokens' values
-// meanwhile (mixed batch of 48: 10 us less than the same warps before their rows).
-__global__ void __launch_bounds__(32 * kRowWarps, kJoinCtas) chunk_join(PagedChunk p, ChunkPlan w, int run) {
+// fourth piece.  Blocks from `blocks` on look through the new tokens' values meanwhile, eight
+// tokens of a key head a warp (mixed batch of 48: 10 us less than the same warps before their
+// rows).
+__global__ void __launch_bounds__(32 * kRowWarps, kJoinCtas) chunk_join(PagedChunk p, ChunkPlan w, int run, int blocks) {
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x % 32, r = lane % 8, part = lane / 8;
@@ -204,20 +205,26 @@ __global__ void __launch_bounds__(32 * kRowWarps, kJoinCtas) chunk_join(PagedChu
   const long long rows = (long long)__ldcg(&l.seq[p.c.S].row0) * p.c.Hq;
   const ChunkCut cut = chunk_cut(__ldcg(l.cum + p.c.S), w.ctas_keys);
   float *nl = reinterpret_cast<float *>(p.ws + w.nl);
-  const int blocks = gridDim.x / 2;
   if ((int)blockIdx.x >= blocks) {
-    row_groups(p, w, l, rows, run, blockIdx.x - blocks, blocks, lane, [&](const ChunkRows &x, long long, bool) {
-      if (x.hq % w.G != 0) return;
-      const unsigned odd = values_odd(p, w.page_shift, x.s, x.hq / w.G, x.g.P + x.i, min(x.q.n - x.i, 8), lane);
-      if (lane > 0) return;
-      *chunk_odd_map(p, w, x.q.row0 + x.i, x.hq / w.G) = (uint8_t)odd;
-      if (odd != 0) chunk_odd(p, w)[x.s] = 1;
-    });
+    const long long of_keys = rows / w.G, step = 8ll * kRowWarps * (gridDim.x - blocks);
+    for (long long row = 8ll * ((blockIdx.x - blocks) * kRowWarps + threadIdx.x / 32); row < of_keys; row += step) {
+      const int s = chunk_seq_of(l, p.c.S, p.c.Hkv, row, lane);
+      const ChunkSeq q = chunk_seq(l, s);
+      if (q.n == 0) continue;   // (behind the last row)
+      const int n8 = (q.n + 7) & ~7;
+      const long long at = row - (long long)q.row0 * p.c.Hkv;
+      const int hkv = (int)chunk_div(at, n8), i = (int)(at - (long long)hkv * n8);
+      if (hkv >= p.c.Hkv) continue;
+      const unsigned odd = values_odd(p, w.page_shift, s, hkv, q.len - q.n + i, min(q.n - i, 8), lane);
+      if (lane > 0) continue;
+      *chunk_odd_map(p, w, q.row0 + i, hkv) = (uint8_t)odd;
+      if (odd != 0) chunk_odd(p, w)[s] = 1;
+    }
     return;
   }
   ChunkPieces pc;
   int tile0 = -1;   // of the first 32 CTAs
-  row_groups(p, w, l, rows, run, blockIdx.x, blocks, lane, [&](const ChunkRows &x, long long row, bool fresh) {
+  row_groups(p, w, l, rows, run, blocks, lane, [&](const ChunkRows &x, long long row, bool fresh) {
     if (fresh) {
       pc.find(x, cut);
       tile0 = pc.tile(x, cut, pc.first + lane);
@@ -263,7 +270,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, kCombineCtas) chunk_combine(Pa
   ChunkPieces pc;
   int tile0 = -1;   // of the first 32 CTAs
   bool odd = false;
-  row_groups(p, w, l, rows, run, blockIdx.x, gridDim.x, lane, [&](const ChunkRows &x, long long, bool fresh) {
+  row_groups(p, w, l, rows, run, gridDim.x, lane, [&](const ChunkRows &x, long long, bool fresh) {
     if (fresh) {
       pc.find(x, cut);
       tile0 = pc.tile(x, cut, pc.first + lane);
@@ -341,7 +348,8 @@ cudaError_t launch_chunk_plan(const PagedChunk &p, const ChunkPlan &w, cudaStrea
   return launch_after(chunk_plan_kernel, 1, p.c.S <= 32 * kPlanFew ? 32 : kPlanThreads, 0, stream, p, w);
 }
 cudaError_t launch_chunk_join(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream) {
-  return launch_after(chunk_join, 2 * row_blocks(w.rows, kJoinCtas), 32 * kRowWarps, 0, stream, p, w, row_run(w.rows, kJoinCtas));
+  const int blocks = row_blocks(w.rows, kJoinCtas), of_keys = row_blocks(w.rows / w.G, kJoinCtas);
+  return launch_after(chunk_join, blocks + of_keys, 32 * kRowWarps, 0, stream, p, w, row_run(w.rows, kJoinCtas), blocks);
 }
 template <typename E>
 static cudaError_t launch_combine_t(const PagedChunk &p, const ChunkPlan &w, cudaStream_t stream) {
