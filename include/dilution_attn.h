@@ -470,12 +470,11 @@ int dilution_attn_paged_decode_ex(const void *q, const dilution_attn_paged_cache
  * 8192 tokens on at 12 query heads, d = 128: 0.73 GB and the logits, DA_F32 1.39 GB.  Repeated calls give equal bits.  Errors as for
  * dilution_attn_paged_decode_ex.
  * DA_BF16: products, exponentials and reciprocals as in dilution_attn_paged_decode.  The
- * shares enter the value product as two bf16 terms (2^-16 relative), as there, where a
- * key head's rows, the new tokens rounded up to 8 for each of its query heads, are up to 64
- * (drafted and single tokens: also beside long parts), and where no sequence of the call
- * has more than d / 8 (max_new times query heads a key head) and the logits take up to
- * 2 GB; in larger parts they are rounded to bf16 once, as in dilution_attn_fwd, which
- * moves out by at most 2^-8 of the values' mean distance from it. */
+ * shares enter the value product as two bf16 terms (2^-16 relative), as there, for
+ * sequences with up to 4 new tokens, also beside long parts, and for those with up to 64
+ * rows a key head (the new tokens rounded up to 8, for each of its query heads); in larger
+ * parts they are rounded to bf16 once, as in dilution_attn_fwd, which moves out by at
+ * most 2^-8 of the values' mean distance from it. */
 size_t dilution_attn_paged_chunk_workspace_size(int S, int Hq, int Hkv, int d, int N, int max_new, int max_len, int dtype);
 
 int dilution_attn_paged_chunk(const void *q, const dilution_attn_paged_cache *cache, const int32_t *cu_tokens, int N,

@@ -101,6 +101,7 @@ struct ChunkPlan {
   int logits_ld;         // their keys (0: not kept)
   int logits_seq;        // tokens that each sequence has of them (0: as many as are new, one behind the other)
 };
+constexpr int kChunkFold = 4;       // up to so many new tokens leave room for second terms in their eight rows
 constexpr int kChunkLogits = 128;   // their keys are a multiple of this, a key tile of bf16
 
 // New tokens of a sequence in a round.  (One prompt of 131072 tokens, 12 / 4 heads, d = 128:

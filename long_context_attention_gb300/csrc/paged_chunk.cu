@@ -278,6 +278,9 @@ __global__ void __launch_bounds__(32 * kRowWarps, kCombineCtas) chunk_combine(Pa
     }
     const int r = lane % 8;                     // the lane's row
     const bool valid = x.i + r < x.q.n;
+    // the second terms' sums of row r in row r + 4: see paged_chunk_bf16.cu
+    const bool fold = sizeof(E) == 2 && w.logits_ld == 0 && x.q.n <= kChunkFold;
+    const bool have_row = fold ? r % kChunkFold < x.q.n : valid;
     float4 a[PER];
     float sum = 0.f;
 #pragma unroll
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(32 * kRowWarps, kCombineCtas) chunk_combine(Pa
       for (unsigned have = __ballot_sync(0xffffffffu, tile >= 0); have; have &= have - 1) {
         const int from = __ffs(have) - 1, t = __shfl_sync(0xffffffffu, tile, from);
         const float *at = chunk_place(p, w.acc_a, w.acc_b, x.row0, w.cta_rows, t, c + from, x.r, acc_stride(D));
-        if (!valid) continue;
+        if (!have_row) continue;
         float4 v[PER];
 #pragma unroll
         for (int e = 0; e < PER; ++e) v[e] = __ldcg(reinterpret_cast<const float4 *>(at + chunk_acc(D, r, lane / 8 + 4 * e)));
@@ -295,6 +298,16 @@ __global__ void __launch_bounds__(32 * kRowWarps, kCombineCtas) chunk_combine(Pa
 #pragma unroll
         for (int e = 0; e < PER; ++e) a[e].x += v[e].x, a[e].y += v[e].y, a[e].z += v[e].z, a[e].w += v[e].w;
       }
+    }
+    if (fold) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) {
+        a[e].x += __shfl_xor_sync(0xffffffffu, a[e].x, kChunkFold);
+        a[e].y += __shfl_xor_sync(0xffffffffu, a[e].y, kChunkFold);
+        a[e].z += __shfl_xor_sync(0xffffffffu, a[e].z, kChunkFold);
+        a[e].w += __shfl_xor_sync(0xffffffffu, a[e].w, kChunkFold);
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, kChunkFold);
     }
     if (odd) {   // what the rows see that is not finite, 32 times eight tokens at a time
       for (int i0 = 0; i0 <= x.i; i0 += 8 * 32) {

@@ -18,10 +18,11 @@
 // comes back to the thread that left it.  The shares, rounded to bf16 once (the
 // product's operands have one type; 2^-8 of each share, and numerator and sum hold
 // the same ones), go to shared memory as the MN-major A operand of
-// D[row, :] += share^T [V | 1].  Of several heads' rows, up to 64 in all (drafted and
-// single tokens beside parts of prompts), what the rounding left is a second term in the
-// places of the other 64, and a second product: those shares keep 2^-16, as in a decode
-// step (mixed batch of 48: 353 -> 359 us).  Unlike the prompt's sweep, the rows stay and the keys
+// D[row, :] += share^T [V | 1].  Shares of drafted and single tokens keep 2^-16, as in a
+// decode step: what the rounding left is a second term, of up to 4 tokens in the rows that
+// round them up to 8 (chunk_combine adds them), else, where several heads have up to 64 rows in
+// all, in the places of the other 64, for a second product (mixed batch of 48: 353 -> 359
+// us).  Unlike the prompt's sweep, the rows stay and the keys
 // stream: D stays in TMEM over a piece's key tiles and leaves once, as a partial
 // result of fixed place, so that equal calls give equal bits.
 //
@@ -73,7 +74,9 @@ struct CkxTile {
   bool odd;            // a row's sum is NaN: it must not reach the rows before it, nor totals that it does not see
   bool clear;          // new tokens have values that are not finite
   __device__ __forceinline__ int query(int c) const { return n8 ? c % n8 : i0 + c; }
-  __device__ __forceinline__ bool two_terms() const { return n8 != 0 && rows <= 64; }   // of a share
+  // a second term of the shares: in the rows from 4 on of each head's eight, in those from 64 on
+  __device__ __forceinline__ bool folded() const { return n8 != 0 && n <= kChunkFold; }
+  __device__ __forceinline__ bool two_terms() const { return n8 != 0 && n > kChunkFold && rows <= 64; }
 };
 constexpr int kCkxRing = 4;
 
@@ -979,7 +982,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
         // they are formed as much, and their scale 4 % too.)
         const int groups = (rows + 7) / 8, n8 = x.n8 ? x.n8 : 8 * groups, per = n8 / 8, n = x.n8 ? x.n : rows, P = x.P + x.i0,
                   head0 = x.s * p.c.Hq + x.hq0;
-        const bool two = x.two_terms();
+        const bool two = x.two_terms(), fold = x.folded();
         for (; j < end; j += kG, ++m) {
           const int next_page = j + kG < end ? page_of(j + kG) : -1;
           float *next_at = nullptr;
@@ -1036,6 +1039,7 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
               pk[e] = pack_bf16x2(s2.x, s2.y);
               pk2[e] = pack_bf16x2(s2.x - __uint_as_float(pk[e] << 16), s2.y - __uint_as_float(pk[e] & 0xffff0000u));
             }
+            if (fold) pk[2] = pk2[0], pk[3] = pk2[1];
             if (u == 0) {   // the product of the tile before has read the shares
               ok = warp_wait(&sh_free[g], (m & 1) ^ 1, wc);
               if (!ok) break;

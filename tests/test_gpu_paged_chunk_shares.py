@@ -73,6 +73,19 @@ def test_mixed_batch(d, Hq, Hkv, page, flags):
     assert np.abs(host64(out) - ref[0]).max() < 0.05     # the part's too
 
 
+@pytest.mark.parametrize("flags", [0, 1])
+@pytest.mark.parametrize("d,Hq,Hkv,page", [(64, 12, 1, 16), (64, 16, 1, 64), (128, 20, 1, 32), (128, 34, 2, 128), (64, 3, 3, 32)])
+@pytest.mark.parametrize("part", [0, 130])
+def test_many_heads_on_a_key_head(d, Hq, Hkv, page, part, flags):
+    """Up to four new tokens, however many query heads share their keys: alone, and beside a part of a prompt."""
+    lens, news = [9, 150, 20, 2600, 33, 200], [1, 3, 4, 2, 1, part]
+    cache, q, cu = make(lens, news, Hq, Hkv, d, page, "bf16", seed=d + Hq)
+    ref = oracle(cache, q, cu, earlier=bool(flags))
+    out = b.dilution_attn_paged_chunk(q, cache, cu, max(news), 2600, flags=flags)
+    check_two_terms(out, cu, ref, slice(0, 11))
+    assert np.abs(host64(out) - ref[0]).max() < 0.05
+
+
 def test_a_single_token_is_as_exact_as_a_decode_step():
     """The same token by a chunk, alone and beside a prompt, and by a decode step: errors of one size."""
     lens, news = [33, 12, 60], [1, 1, 1]
