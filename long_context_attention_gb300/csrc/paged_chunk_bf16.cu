@@ -1034,8 +1034,9 @@ __global__ void __launch_bounds__(CkxVal<D>::kThreads, 1) __maxnreg__(CkxVal<D>:
             for (int e = 0; e < 4; ++e) {
               float2 dd = fadd2(make_float2(d[2 * e + 1], d[2 * e]), b2);
               if (!EARLIER) dd.x = fminf(dd.x, 2e18f);   // a NaN of the later row alone (else: both are below)
-              const float r = rcp_approx(dd.x * dd.y) * den.scale;
-              const float2 s2 = fmul2(fmul2(make_float2(bid[2 * e], bid[2 * e + 1]), dd), make_float2(r, r));
+              const float r = rcp_approx(dd.x * dd.y);
+              const float2 one = fmul2(fmul2(make_float2(bid[2 * e], bid[2 * e + 1]), dd), make_float2(r, r));
+              const float2 s2 = fmul2(one, make_float2(den.scale, den.scale));   // (after r: both in one would underflow)
               pk[e] = pack_bf16x2(s2.x, s2.y);
               pk2[e] = pack_bf16x2(s2.x - __uint_as_float(pk[e] << 16), s2.y - __uint_as_float(pk[e] & 0xffff0000u));
             }

@@ -137,7 +137,8 @@ def test_very_large_totals(lens, news, flags, dtype):
     size = torch.randint(18, 31, cache.demand_pages.shape, generator=g).float()
     big = (10.0 ** size * (1 + torch.rand(size.shape, generator=g))).to(DEV)
     some = (torch.rand(size.shape, generator=g) < 0.3).to(DEV)
-    some[:, 0] = True
+    some[:, 0] = some[:, 3] = True
+    big[:, 3] = (1e27 * (1 + 1e3 * torch.rand(big[:, 3].shape, generator=g))).to(DEV)     # of that head's none is below 1e27
     cache.demand_pages.copy_(torch.where(some, big, cache.demand_pages))
     run(cache, q, cu, max(news), max(lens), flags=flags)
 
