@@ -463,11 +463,13 @@ int dilution_attn_paged_decode_ex(const void *q, const dilution_attn_paged_cache
  * once by the caller, or NULL for the workspace's first 256 bytes.  The workspace is
  * overwritten from byte 256 on: calls that may overlap on the GPU need workspaces
  * of their own.  One that was sized for some N, max_new and max_len serves every call
- * of this cache within them.  It holds about 4 (d + 7) bytes for each query head of the new
- * tokens, of up to 8192 of a sequence, and as much for each row of the longest sequence's (up to
- * 8192) for 152 CTAs (DA_F32: 304, with few rows 456), and the logits, up to 2 GB, of up
- * to d / 8 new tokens times query heads a key head (DA_BF16).  A prompt of any length from
- * 8192 tokens on at 12 query heads, d = 128: 0.73 GB and the logits, DA_F32 1.39 GB.  Repeated calls give equal bits.  Errors as for
+ * of this cache within them.  It holds about 4 (d + 7) bytes for each query head of the
+ * new tokens, and as much for each row of the longest sequence's in each of 152 CTAs
+ * (DA_F32: 304, with few rows 456), in both of up to 8192 tokens of a sequence (longer
+ * parts go by rounds of those); and, in DA_BF16, the logits of up to d / 8 new tokens times
+ * query heads a key head, up to 2 GB.  One prompt of any length from 8192 tokens on, 12
+ * query heads, d = 128: 0.73 GB beside those logits, DA_F32 1.39 GB.  Pages that sequences
+ * share are read for each of them.  Repeated calls give equal bits.  Errors as for
  * dilution_attn_paged_decode_ex.
  * DA_BF16: products, exponentials and reciprocals as in dilution_attn_paged_decode.  The
  * shares enter the value product as two bf16 terms (2^-16 relative), as there, for
@@ -490,7 +492,10 @@ int dilution_attn_paged_chunk(const void *q, const dilution_attn_paged_cache *ca
  * 0 .. m - 1 (keys, values and totals move together, bit for bit), so that after
  * an eviction one row holds different tokens in different key heads: keys carry
  * their rotation, and later tokens need their positions passed to
- * dilution_attn_paged_append.
+ * dilution_attn_paged_append.  In place every row behind the first that goes moves, so
+ * that one token costs about what many do (64 sequences of 4097 tokens, 4 key heads,
+ * d = 128: 112 us for one token of each; a decode step reads all of them in about 80):
+ * a serving loop lets sequences grow by some tokens between evictions.
  *   dst_page_table, dst_demand_table: both NULL: in place (pages that sequences share
  *       then hold only tokens that every key head of theirs keeps, as below).  Otherwise DEVICE
  *       [S][dst_max_pages] tables of the same pools, dst_max_pages * page_size at

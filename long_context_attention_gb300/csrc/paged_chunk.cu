@@ -346,8 +346,8 @@ __global__ void __launch_bounds__(32 * kRowWarps, kCombineCtas) chunk_combine(Pa
 }
 
 // Eight rows a warp where there are few, and where there are many up to 32 (16 prompts of
-// d = 128, 325,000 rows: combine 122, 112, 110, 124 us at 8, 16, 32 and 64, join 59, 43, 39,
-// 48: a few rows find their segment again and again, many leave some warps far behind).
+// d = 128, 325,000 rows: combine 122, 112, 110, 124 us at 8, 16, 32 and 64, join, without the
+// blocks for values, 59, 43, 39, 48: a few rows find their segment again and again, many leave some warps far behind).
 static int row_run(long long rows, int ctas) {
   const long long fill = 8ll * kRowWarps * 152 * ctas, run = (rows + fill - 1) / fill;
   return (int)(run < 1 ? 1 : run > 4 ? 4 : run);

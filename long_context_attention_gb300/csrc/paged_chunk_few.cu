@@ -11,7 +11,7 @@
 // values, logits and totals are copied asynchronously a step ahead; a lane has a key for
 // bids, shares and totals; m16n8k16 forms share^T V (tcgen05's 128 rows would be mostly
 // padding).  The warps' sums meet at a piece's end, in their order.
-// 8 x 12 x 131072, 4 tokens, d = 64: 300 us, 6.4 TB/s of values, logits and totals;
+// 8 x 12 x 131072, 4 tokens, d = 64: 307 us, 6.2 TB/s of values, logits and totals;
 // the first pass 288, 6.3 TB/s of keys and logits.
 #include "da_chunk.cuh"
 #include "da_paged_plan.cuh"
@@ -42,10 +42,11 @@ struct Ckl {
 // logits, written and read, are half of the bytes of K, and they take at most 2 GB of
 // workspace.  Times in us of both second passes' calls (sequences x query / key heads x
 // keys, new tokens; kept / not):
-//   d = 64, 8 x 12/12 x 131072: 1 583 / 838, 4 620 / 818, 8 699 / 834, 16 1167 / 844;
-//     8 x 12/4 x 32768: 1 113 / 139, 2 116 / 140, 5 (15 rows) 140 / 138;
-//     64 x 12/12 x 4096: 4 215 / 277, 16 337 / 281; 1 x 12/12 x 16384: 4 62 / 67;
-//   d = 128, 8 x 16/4 x 131072: 4 (16 rows) 547 / 614; 4 x 32/2 x 65536: 1 (16 rows) 155 / 265.
+//   d = 64, 8 x 12/12 x 131072: 1 565 / 853, 4 612 / 857, 8 703 / 861; past the bound 16 1167 / 844;
+//     8 x 12/4 x 32768: 1 93 / 129, 2 98 / 128; past the bound 5 (15 rows) 140 / 138;
+//     64 x 12/12 x 4096: 4 199 / 275; past the bound 16 337 / 281; 1 x 12/12 x 16384: 4 42 / 50;
+//   d = 128, 8 x 16/4 x 131072: 4 (16 rows) 575 / 648; 4 x 32/2 x 65536: 1 (16 rows) 143 / 251.
+// (Past the bound: before shares had second terms.)
 bool chunk_few(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len) {
   const long long tokens = N < (long long)S * max_new ? N : (long long)S * max_new;   // (more are padding)
   return max_new > 0 && (long long)(Hq / Hkv) * max_new * 8 <= d &&

@@ -25,10 +25,10 @@ constexpr int kCksKeysF32 = 128, kCksRowsF32 = 32;
 // CTAs per (sequence, key head), 0 where the call is not short enough: one wave of
 // CTAs (one on each SM), two where there are up to 32 rows, four in fp32.  Device time
 // of this kernel and of the five others in us (sequences x key heads x rows x keys):
-//   bf16, d = 64: 1 x 12 x 8 x 500 8.3 / 30.9, 1 x 12 x 64 x 2048 22.3 / 42.1, 8 x 4 x 8 x
-//   2048 (256 CTAs) 27.3 / 38.6, 38 x 8 x 32 x 256 (304) 27.1 / 38.8; past the bound
-//   8 x 4 x 64 x 2048 (256) 64.9 / 43.9, at d = 128 73.2 / 50.4;
-//   fp32: 1 x 12 x 8 x 500 9.3 / 35.5, 38 x 8 x 32 x 128 (304) 19.3 / 51.0, d = 128 41.0 / 84.8.
+//   bf16, d = 64: 1 x 12 x 8 x 500 9.4 / 26.6, 1 x 12 x 64 x 2048 25.0 / 39.8, 8 x 4 x 8 x
+//   2048 (256 CTAs) 29.6 / 33.8, 38 x 8 x 32 x 256 (304) 30.3 / 42.5; past the bound
+//   8 x 4 x 64 x 2048 (256) 69.3 / 42.9, at d = 128 80.5 / 47.9;
+//   fp32: 1 x 12 x 8 x 500 10.0 / 30.3, 38 x 8 x 32 x 128 (304) 20.9 / 51.7, d = 128 43.7 / 82.3.
 int chunk_small_cluster(int S, int Hq, int Hkv, int max_new, int max_len, int dtype) {
   const int64_t pairs = (int64_t)S * Hkv;
   const int keys = dtype == DA_BF16 ? kCksKeys : kCksKeysF32, rows = dtype == DA_BF16 ? kCksRows : kCksRowsF32;
