@@ -466,7 +466,7 @@ int dilution_attn_paged_decode_ex(const void *q, const dilution_attn_paged_cache
  * of this cache within them.  It holds about 4 (d + 7) bytes for each query head of the
  * new tokens, and as much for each row of the longest sequence's in each of 152 CTAs
  * (DA_F32: 304, with few rows 456), in both of up to 8192 tokens of a sequence (longer
- * parts go by rounds of those); and, in DA_BF16, the logits of up to d / 8 new tokens times
+ * parts go by slices of those); and, in DA_BF16, the logits of up to d / 8 new tokens times
  * query heads a key head, up to 2 GB.  One prompt of any length from 8192 tokens on, 12
  * query heads, d = 128: 0.73 GB beside those logits, DA_F32 1.39 GB.  Pages that sequences
  * share are read for each of them.  Repeated calls give equal bits.  Errors as for

@@ -22,8 +22,8 @@
 // own places (a), those of the piece a CTA continues in the CTA's places (b).
 // They are joined in the line's order: equal calls give equal bits.
 //
-// Rounds.  Every CTA has places for the rows of a sequence's new tokens (b), so that
-// long parts go by rounds of up to kChunkRound of them: a chunk is what two halves of
+// Slices.  Every CTA has places for the rows of a sequence's new tokens (b), so that
+// long parts go by slices of up to kChunkSlice of them: a chunk is what two halves of
 // it are, one after the other.
 //
 // Values that are not finite.  A query's share of a key that it does not see is 0, and 0
@@ -44,7 +44,7 @@ struct PagedChunk {
   void *out;
   const int32_t *cu;   // [S + 1]
   int N, max_new, max_len;
-  int first;           // of each sequence's new tokens the first of this round, which has up to max_new
+  int first;           // of each sequence's new tokens the first of this slice, which has up to max_new
   int all_new;         // new tokens of a sequence, at most
   HeadScale hs;
   float eps;
@@ -104,11 +104,11 @@ struct ChunkPlan {
 constexpr int kChunkFold = 4;       // up to so many new tokens leave room for second terms in their eight rows
 constexpr int kChunkLogits = 128;   // their keys are a multiple of this, a key tile of bf16
 
-// New tokens of a sequence in a round.  (One prompt of 131072 tokens, 12 / 4 heads, d = 128:
-// a workspace of 0.73 GB, in fp32 1.39; all at once 11.7 and 22.2, for 84.5 ms where the rounds
+// New tokens of a sequence in a slice.  (One prompt of 131072 tokens, 12 / 4 heads, d = 128:
+// a workspace of 0.73 GB, in fp32 1.39; all at once 11.7 and 22.2, for 84.5 ms where the slices
 // take 87.9.  32768 tokens 6.8 and 7.2 ms, in fp32 142 and 140; 12 heads of d = 64, 131072
 // tokens 69.6 and 69.9.)
-constexpr int kChunkRound = 8192;
+constexpr int kChunkSlice = 8192;
 
 inline ChunkPlan chunk_plan(int S, int Hq, int Hkv, int d, long long N, int max_new, int page_size, int edge, int ctas_keys,
                             int ctas_values, ChunkCost cost) {
@@ -119,7 +119,7 @@ inline ChunkPlan chunk_plan(int S, int Hq, int Hkv, int d, long long N, int max_
   w.ctas_keys = ctas_keys;
   w.ctas_values = ctas_values;
   w.cost = cost;
-  if (N > (long long)S * max_new) N = (long long)S * max_new;   // (more are padding, or another round's)
+  if (N > (long long)S * max_new) N = (long long)S * max_new;   // (more are padding, or another slice's)
   const long long busy = N < S ? N : S;   // sequences with new tokens
   w.rows = (N + 7 * busy) * Hq;
   const int narrow = (int)round_up(max_new < edge / 2 ? max_new : edge / 2, 8) * w.G;

@@ -42,7 +42,7 @@ __device__ __forceinline__ long long plan_scan(long long v, long long *warp_sum,
   return base + inc - v;
 }
 
-// One sequence, checked: its new tokens of this round, or 0; its length up to them.
+// One sequence, checked: its new tokens of this slice, or 0; its length up to them.
 __device__ __forceinline__ ChunkSeq plan_seq(const PagedChunk &p, int s) {
   const int len = __ldcg(p.c.seq_lens + s), a = __ldcg(p.cu + s), b = __ldcg(p.cu + s + 1), n = b - a;
   if (len < 0 || len > p.max_len || a < 0 || b < a || b > p.N || n > p.all_new || n > len) {
@@ -380,7 +380,7 @@ size_t chunk_few_room(int S, int Hq, int Hkv, int d, long long N, int max_new, i
 
 // Enough for all calls within these bounds, those that keep their logits among them.
 size_t chunk_workspace(int S, int Hq, int Hkv, int d, long long N, int max_new, int max_len, int dtype) {
-  if (max_new > kChunkRound) max_new = kChunkRound;
+  if (max_new > kChunkSlice) max_new = kChunkSlice;
   if (dtype == DA_F32) {   // up to 16 rows a key head have more CTAs
     const int few = 16 / (Hq / Hkv) / 8 * 8;
     const size_t all = chunk_plan_f32(S, Hq, Hkv, d, N, max_new, 16).total,
@@ -401,9 +401,9 @@ int launch_paged_chunk(const PagedChunk &p, cudaStream_t stream) {
   PagedChunk r = p;
   int st = DA_OK;
   do {
-    r.max_new = p.max_new - r.first < kChunkRound ? p.max_new - r.first : kChunkRound;
+    r.max_new = p.max_new - r.first < kChunkSlice ? p.max_new - r.first : kChunkSlice;
     st = p.c.dtype == DA_F32 ? launch_chunk_f32(r, stream) : launch_chunk_bf16(r, stream);
-    r.first += kChunkRound;
+    r.first += kChunkSlice;
   } while (st == DA_OK && r.first < p.max_new);
   return st;
 }

@@ -167,7 +167,7 @@ def test_a_very_large_eps(lens, news, flags, dtype):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T,places", [(3000, [0, 7, 8, 255, 256, 2049, 2999]), (8500, [100, 8191, 8192, 8300]), (2900, list(range(2900)))])
 def test_long_parts(T, places, dtype):
-    """Infinite values here and there, across the rounds of a long part, or of every token: each row has those of the tokens
+    """Infinite values here and there, across the slices of a long part, or of every token: each row has those of the tokens
     up to its own, and the bits of the clean call elsewhere."""
     d = 64
     cache, q, cu = make([T, 70], [T, 3], 2, 1, d, 64, dtype, seed=T, fresh=False)
